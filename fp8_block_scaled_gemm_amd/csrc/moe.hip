@@ -1,0 +1,821 @@
+// Expert routing and the expert row layout for gfx950: from the router's logits to the rows that the
+// grouped GEMMs read (contiguous and masked forms) and back to the tokens, with the gradients.
+//
+//   route       logits (T, E) -> the K experts of each token and their weights
+//   layout      experts of the tokens -> a row for each (token, place), m_indices, counts
+//   dispatch    token rows -> expert rows, copied or quantized (FP8 per 128 columns, int8 per row)
+//   combine     expert rows -> weighted sum per token
+//
+// Every result is deterministic: ranks follow the order of (token, place), sums a fixed order.
+#include "rows.hpp"
+
+namespace dg {
+
+// ---------------------------------------------------------------------------
+// Routing.
+// ---------------------------------------------------------------------------
+constexpr int kRouteWaves = 4;          // tokens per workgroup, one wave each
+constexpr int kRouteMaxExperts = 1024;  // 16 per lane
+constexpr int kRouteMaxTopK = 64;       // one lane per chosen expert
+
+struct RouteParams {
+  const void* logits;
+  int64_t ld;
+  const float* bias;
+  int tokens, experts, top_k;
+  int groups, group_size, topk_groups, group_top;
+  uint32_t group_magic;   // ceil(2^20 / group_size): e * magic >> 20 = e / group_size for e < 1024
+  int lanes_per_group;    // 64 / (groups rounded up to a power of two)
+  int softmax, renorm;
+  float scale;
+  int32_t* ids;
+  float* weights;
+};
+
+// LDS written by some lanes of a wave and read by others: nothing moves across (no instruction).
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Unsigned key of a choice value that orders like the value (-0 as +0); 0 stands for "not available".
+__device__ __forceinline__ uint32_t choice_key(float v) {
+  const uint32_t u = __float_as_uint(v + 0.0f);
+  return (u >> 31) ? ~u : (u | 0x80000000u);
+}
+
+__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+
+// One wave per token; lane l holds experts l, l + 64, ... (coalesced reads; the lowest index of a tie
+// is the lowest register, then the lowest lane).
+template <class T, int C>
+__global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteParams p) {
+  __shared__ float s_value[kRouteWaves][64 * C];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t token = (int64_t)blockIdx.x * kRouteWaves + wave;
+  if (token >= p.tokens) return;   // wave-uniform; no workgroup barrier below
+  const T* row = static_cast<const T*>(p.logits) + token * p.ld;
+
+  float x[C], value[C];
+  bool nan = false;
+  float top = -__builtin_inff();
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int e = 64 * c + lane;
+    x[c] = e < p.experts ? widen(row[e]) : -__builtin_inff();
+    if (x[c] != x[c]) {   // a NaN logit: not chosen, and every weight of the token is NaN
+      nan = true;
+      x[c] = -__builtin_inff();
+    }
+    top = fmaxf(top, x[c]);
+  }
+  // the softmax's maximum and sum, where a probability itself is needed
+  const bool by_logit = p.softmax && p.bias == nullptr && !(p.groups > 1 && p.group_top > 1);
+  float total = 1.0f;
+  if (p.softmax && (!by_logit || !p.renorm)) {
+    for (int sh = 1; sh < 64; sh *= 2) top = fmaxf(top, __shfl_xor(top, sh));
+    float sum = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) sum += x[c] == -__builtin_inff() ? 0.0f : expf(x[c] - top);
+    total = wave_sum(sum);
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int e = 64 * c + lane;
+    const bool off = x[c] == -__builtin_inff();
+    float v = by_logit ? x[c] : p.softmax ? expf(x[c] - top) / total : sigmoid(x[c]);
+    if (p.bias != nullptr && e < p.experts) v += p.bias[e];
+    if (!off && v != v && !by_logit) nan = true;
+    value[c] = off || v != v ? -__builtin_inff() : v;
+  }
+
+  if (p.groups > 1) {
+    // lanes_per_group lanes find the two best values of each group, then every group counts the
+    // groups ahead of it (higher value, or equal and lower index)
+    float* s_val = s_value[wave];
+#pragma unroll
+    for (int c = 0; c < C; ++c) s_val[64 * c + lane] = value[c];
+    wave_lds_fence();
+    const int lpg = p.lanes_per_group;
+    const int mine = lane / lpg, sub = lane - mine * lpg;
+    float t1 = -__builtin_inff(), t2 = -__builtin_inff();
+    if (mine < p.groups) {
+      for (int i = sub; i < p.group_size; i += lpg) {
+        const float v = s_val[mine * p.group_size + i];
+        t2 = fmaxf(t2, fminf(t1, v));
+        t1 = fmaxf(t1, v);
+      }
+    }
+    for (int sh = 1; sh < lpg; sh *= 2) {
+      const float o1 = __shfl_xor(t1, sh), o2 = __shfl_xor(t2, sh);
+      t2 = fmaxf(fminf(t1, o1), fmaxf(t2, o2));
+      t1 = fmaxf(t1, o1);
+    }
+    const float sum = p.group_top > 1 && t2 != -__builtin_inff() ? t1 + t2 : t1;
+    const uint32_t key = t1 == -__builtin_inff() || mine >= p.groups ? 0u : choice_key(sum);
+    int ahead = 0;
+    for (int g = 0; g < p.groups; ++g) {
+      const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)key, g * lpg);
+      ahead += other > key || (other == key && g < mine);
+    }
+    const uint64_t kept = __ballot(ahead < p.topk_groups);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const uint32_t g = ((uint32_t)(64 * c + lane) * p.group_magic) >> 20;
+      if (!((kept >> ((g * lpg) & 63)) & 1)) value[c] = -__builtin_inff();
+    }
+  }
+
+  uint32_t key[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) key[c] = value[c] == -__builtin_inff() ? 0u : choice_key(value[c]);
+
+  // K rounds of the wave's maximum; lane j keeps the j-th choice
+  int id = -1;
+  for (int j = 0; j < p.top_k; ++j) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int c = 1; c < C; ++c) best = umax(best, key[c]);
+    best = wave_max_u32(best);
+    if (best == 0u) break;   // wave-uniform: no available expert is left
+    int pick = 0;
+    bool open = true;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const uint64_t has = __ballot(open && key[c] == best);
+      if (has != 0) {   // wave-uniform: the first register that holds the value
+        const int owner = __builtin_ctzll(has);
+        pick = 64 * c + owner;
+        if (lane == owner) key[c] = 0u;
+        open = false;
+      }
+    }
+    if (lane == j) id = pick;
+  }
+
+  float s = 0.0f;
+  if (p.softmax) {
+    const float xk = id >= 0 ? widen(row[id]) : -__builtin_inff();
+    if (p.renorm) {
+      // over the chosen alone: relative to their own maximum, so none of their sums underflows
+      float m = xk;
+      for (int sh = 1; sh < 64; sh *= 2) m = fmaxf(m, __shfl_xor(m, sh));
+      s = id >= 0 ? expf(xk - m) : 0.0f;
+    } else {
+      s = id >= 0 ? expf(xk - top) / total : 0.0f;
+    }
+  } else if (id >= 0) {
+    s = sigmoid(widen(row[id]));
+  }
+  float w = s;
+  if (p.renorm) {
+    const float sum = wave_sum(s);
+    w = sum == 0.0f ? 0.0f : s / sum;
+  }
+  w *= p.scale;
+  if (__ballot(nan) != 0) w = id >= 0 ? __builtin_nanf("") : 0.0f;
+  if (lane < p.top_k) {
+    p.ids[token * p.top_k + lane] = id;
+    p.weights[token * p.top_k + lane] = w;
+  }
+}
+
+struct RouteGradParams {
+  const float* dweights;
+  const void* logits;
+  int64_t ld;
+  const int32_t* ids;
+  int tokens, experts, top_k;
+  int softmax, renorm;
+  float scale;
+  void* dlogits;
+  int64_t ld_out;
+};
+
+// One wave per token.  The experts' choice is held fixed; only the softmax without renormalisation
+// needs the whole row of logits, every other form the K chosen ones.
+template <class T, int C>
+__global__ __launch_bounds__(64 * kRouteWaves) void route_grad_kernel(RouteGradParams p) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t token = (int64_t)blockIdx.x * kRouteWaves + wave;
+  if (token >= p.tokens) return;
+  const T* row = static_cast<const T*>(p.logits) + token * p.ld;
+  T* out = static_cast<T*>(p.dlogits) + token * p.ld_out;
+
+  int id = lane < p.top_k ? p.ids[token * p.top_k + lane] : -1;
+  if (id >= p.experts) id = -1;
+  const float g = id >= 0 ? p.dweights[token * p.top_k + lane] : 0.0f;
+  const float xk = id >= 0 ? widen(row[id]) : -__builtin_inff();
+
+  float d = 0.0f;   // dL/dx of this lane's chosen expert
+  float x[C], top = -__builtin_inff(), total = 1.0f, dot = 0.0f;
+  const bool full = p.softmax && !p.renorm;
+  if (full) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int e = 64 * c + lane;
+      x[c] = e < p.experts ? widen(row[e]) : -__builtin_inff();
+      top = fmaxf(top, x[c]);
+    }
+    for (int sh = 1; sh < 64; sh *= 2) top = fmaxf(top, __shfl_xor(top, sh));
+    float sum = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      x[c] = x[c] == -__builtin_inff() ? 0.0f : expf(x[c] - top);
+      sum += x[c];
+    }
+    total = wave_sum(sum);
+    if (total == 0.0f) total = 1.0f;   // a row without an available expert
+    const float pk = id >= 0 ? expf(xk - top) / total : 0.0f;
+    const float u = p.scale * g;
+    dot = wave_sum(pk * u);
+    d = pk * (u - dot);
+  } else {
+    float m = 0.0f;
+    if (p.softmax) {
+      m = xk;
+      for (int sh = 1; sh < 64; sh *= 2) m = fmaxf(m, __shfl_xor(m, sh));
+    }
+    const float s = id < 0 ? 0.0f : p.softmax ? expf(xk - m) : sigmoid(xk);
+    if (p.renorm) {
+      const float sum = wave_sum(s);
+      const float r = sum == 0.0f ? 0.0f : s / sum;
+      const float u = p.scale * r * (g - wave_sum(r * g));   // scale r (g - sum r g) = s dL/ds
+      d = p.softmax ? u : u * (1.0f - s);
+    } else {
+      d = p.scale * g * s * (1.0f - s);
+    }
+  }
+  float v[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) v[c] = full ? -(x[c] / total) * dot : 0.0f;
+  for (int j = 0; j < p.top_k; ++j) {
+    const int e = __builtin_amdgcn_readlane(id, j);
+    const float de = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(d), j));
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (e == 64 * c + lane) v[c] = de;
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+    if (64 * c + lane < p.experts) out[64 * c + lane] = narrow<T>(v[c]);
+}
+
+
+template <class T>
+static const void* route_fn(int experts) {
+  void (*fn)(RouteParams) = experts <= 64    ? route_kernel<T, 1>
+                            : experts <= 128 ? route_kernel<T, 2>
+                            : experts <= 256 ? route_kernel<T, 4>
+                            : experts <= 512 ? route_kernel<T, 8>
+                                             : route_kernel<T, 16>;
+  return reinterpret_cast<const void*>(fn);
+}
+template <class T>
+static const void* route_grad_fn(int experts) {
+  void (*fn)(RouteGradParams) = experts <= 64    ? route_grad_kernel<T, 1>
+                                : experts <= 128 ? route_grad_kernel<T, 2>
+                                : experts <= 256 ? route_grad_kernel<T, 4>
+                                : experts <= 512 ? route_grad_kernel<T, 8>
+                                                 : route_grad_kernel<T, 16>;
+  return reinterpret_cast<const void*>(fn);
+}
+
+static int launched(const void* fn, dim3 grid, dim3 block, void** args, hipStream_t stream, const char* what) {
+  if ((uint64_t)grid.x * block.x > 0xffffffffull || grid.y > 65535u)
+    return set_error(kUnsupported, "%s: shape too large for the launch grid", what);
+  const hipError_t e = hipLaunchKernel(fn, grid, block, args, 0, stream);
+  return e == hipSuccess ? kOk : set_error(kHip, "%s launch: %s", what, hipGetErrorString(e));
+}
+
+int launch_route(const void* logits, int dtype, int64_t ld, const float* bias, int64_t tokens, int experts, int top_k,
+                 int groups, int topk_groups, int group_top, bool softmax, bool renorm, float scale, int32_t* ids,
+                 float* weights, hipStream_t stream) {
+  RouteParams p{};
+  p.logits = logits; p.ld = ld; p.bias = bias;
+  p.tokens = (int)tokens; p.experts = experts; p.top_k = top_k;
+  p.groups = groups; p.group_size = experts / groups; p.topk_groups = topk_groups; p.group_top = group_top;
+  p.group_magic = ((1u << 20) + (uint32_t)p.group_size - 1) / (uint32_t)p.group_size;
+  int pow2 = 1;
+  while (pow2 < groups) pow2 *= 2;
+  p.lanes_per_group = 64 / pow2;
+  p.softmax = softmax; p.renorm = renorm; p.scale = scale;
+  p.ids = ids; p.weights = weights;
+  const void* fn = dtype == kF32 ? route_fn<float>(experts) : dtype == kBf16 ? route_fn<Bf16>(experts)
+                                                                            : route_fn<_Float16>(experts);
+  void* args[] = {&p};
+  return launched(fn, dim3((unsigned)((tokens + kRouteWaves - 1) / kRouteWaves)), dim3(64 * kRouteWaves), args, stream,
+                  "moe_route");
+}
+
+int launch_route_grad(const float* dweights, const void* logits, int dtype, int64_t ld, const int32_t* ids,
+                      int64_t tokens, int experts, int top_k, bool softmax, bool renorm, float scale, void* dlogits,
+                      int64_t ld_out, hipStream_t stream) {
+  RouteGradParams p{};
+  p.dweights = dweights; p.logits = logits; p.ld = ld; p.ids = ids;
+  p.tokens = (int)tokens; p.experts = experts; p.top_k = top_k;
+  p.softmax = softmax; p.renorm = renorm; p.scale = scale;
+  p.dlogits = dlogits; p.ld_out = ld_out;
+  const void* fn = dtype == kF32 ? route_grad_fn<float>(experts) : dtype == kBf16 ? route_grad_fn<Bf16>(experts)
+                                                                                 : route_grad_fn<_Float16>(experts);
+  void* args[] = {&p};
+  return launched(fn, dim3((unsigned)((tokens + kRouteWaves - 1) / kRouteWaves)), dim3(64 * kRouteWaves), args, stream,
+                  "moe_route_grad");
+}
+
+// ---------------------------------------------------------------------------
+// Layout: a stable counting sort of the (token, place) entries by expert.
+// ---------------------------------------------------------------------------
+constexpr int kLayThreads = 512;
+constexpr int kLayWaves = kLayThreads / 64;
+constexpr int kLayMaxExperts = 1024;
+constexpr int kLayChunk = 4096;   // entries per workgroup
+
+struct LayoutParams {
+  const int32_t* ids;
+  int n;                 // entries: tokens * top_k
+  int experts;
+  int rows_per_expert;   // 0: the contiguous layout
+  int align;             // row alignment of the contiguous layout
+  int rows_total;
+  int blocks;
+  int32_t* rows;
+  int32_t* sources;
+  int32_t* m_indices;
+  int32_t* counts;
+  int32_t* hist;         // (blocks, experts), when there is more than one workgroup
+};
+
+__device__ __forceinline__ int entry_expert(const LayoutParams& p, int i, int end) {
+  const int e = i < end ? p.ids[i] : -1;
+  return e >= 0 && e < p.experts ? e : -1;
+}
+
+// Each wave of a workgroup owns a run of its entries; s_hist[w][e] counts them by expert.
+__device__ __forceinline__ void count_entries(const LayoutParams& p, int begin, int end, int per_wave, int* s_hist) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int i = threadIdx.x; i < kLayWaves * p.experts; i += kLayThreads) s_hist[i] = 0;
+  __syncthreads();
+  const int w0 = begin + wave * per_wave;
+  const int w1 = w0 + per_wave < end ? w0 + per_wave : end;
+  for (int i = w0 + lane; i < w1; i += 64) {
+    const int e = entry_expert(p, i, w1);
+    if (e >= 0) atomicAdd(&s_hist[wave * p.experts + e], 1);   // integers: the sum has no order
+  }
+  __syncthreads();
+}
+
+__global__ __launch_bounds__(kLayThreads) void layout_count_kernel(LayoutParams p) {
+  extern __shared__ int s_hist[];
+  const int begin = blockIdx.x * kLayChunk;
+  const int end = begin + kLayChunk < p.n ? begin + kLayChunk : p.n;
+  count_entries(p, begin, end, kLayChunk / kLayWaves, s_hist);
+  for (int e = threadIdx.x; e < p.experts; e += kLayThreads) {
+    int sum = 0;
+    for (int w = 0; w < kLayWaves; ++w) sum += s_hist[w * p.experts + e];
+    p.hist[(int64_t)blockIdx.x * p.experts + e] = sum;
+  }
+}
+
+__global__ __launch_bounds__(kLayThreads) void layout_place_kernel(LayoutParams p) {
+  extern __shared__ int smem[];
+  int* s_hist = smem;                                  // (waves, experts): counts, then next ranks
+  int* s_start = smem + kLayWaves * p.experts;         // (experts + 1): first row of each expert
+  int* s_count = s_start + p.experts + 1;              // (experts): entries of each expert, all workgroups
+  __shared__ int s_scan[kLayWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int begin = blockIdx.x * kLayChunk;
+  const int end = begin + kLayChunk < p.n ? begin + kLayChunk : p.n;
+  const int per_wave = kLayChunk / kLayWaves;
+  count_entries(p, begin, end, per_wave, s_hist);
+
+  // ranks: entries of the expert in earlier workgroups, then in this workgroup's earlier waves
+  for (int e = tid; e < p.experts; e += kLayThreads) {
+    int before = 0, all = 0;
+    for (int b = 0; b < p.blocks && p.blocks > 1; ++b) {
+      const int c = p.hist[(int64_t)b * p.experts + e];
+      if (b < (int)blockIdx.x) before += c;
+      all += c;
+    }
+    int here = 0;
+    for (int w = 0; w < kLayWaves; ++w) {
+      const int c = s_hist[w * p.experts + e];
+      s_hist[w * p.experts + e] = before + here;
+      here += c;
+    }
+    if (p.blocks == 1) all = here;
+    s_count[e] = all;
+    if (blockIdx.x == 0) p.counts[e] = all;
+  }
+  __syncthreads();
+  // first rows: an exclusive scan of the aligned counts (each thread two experts), or a fixed pitch
+  if (p.rows_per_expert) {
+    for (int e = tid; e <= p.experts; e += kLayThreads) s_start[e] = e * p.rows_per_expert;
+  } else {
+    const int e0 = 2 * tid;
+    const int c0 = e0 < p.experts ? (s_count[e0] + p.align - 1) / p.align * p.align : 0;
+    const int c1 = e0 + 1 < p.experts ? (s_count[e0 + 1] + p.align - 1) / p.align * p.align : 0;
+    int run = c0 + c1;
+    for (int sh = 1; sh < 64; sh *= 2) {
+      const int o = __shfl_up(run, sh);
+      if (lane >= sh) run += o;
+    }
+    if (lane == 63) s_scan[wave] = run;
+    __syncthreads();
+    int base = 0;
+    for (int w = 0; w < wave; ++w) base += s_scan[w];
+    const int excl = base + run - c0 - c1;
+    if (e0 <= p.experts) s_start[e0] = excl;
+    if (e0 + 1 <= p.experts) s_start[e0 + 1] = excl + c0;
+    if (tid == kLayThreads - 1) s_start[p.experts] = base + run;   // also where no thread's pair reaches it
+  }
+  __syncthreads();
+
+  // place the entries, 64 at a time in their order: a lane's rank is the wave's next rank of its
+  // expert plus the earlier lanes with the same expert
+  const int w0 = begin + wave * per_wave;
+  const int w1 = w0 + per_wave < end ? w0 + per_wave : end;
+  for (int i0 = w0; i0 < w1; i0 += 64) {
+    const int i = i0 + lane;
+    const int e = entry_expert(p, i, w1);
+    uint64_t same = __ballot(e >= 0);
+    for (int bit = 1; bit < p.experts; bit *= 2) {
+      const uint64_t set = __ballot((e & bit) != 0 && e >= 0);
+      same &= (e & bit) ? set : ~set;
+    }
+    const int earlier = __popcll(same & ((1ull << lane) - 1));
+    const int next = s_hist[wave * p.experts + (e >= 0 ? e : 0)];
+    wave_lds_fence();
+    if (e >= 0 && earlier == 0) s_hist[wave * p.experts + e] = next + __popcll(same);
+    wave_lds_fence();
+    if (e >= 0) {
+      const int rank = next + earlier;
+      const bool fits = p.rows_per_expert == 0 || rank < p.rows_per_expert;
+      const int row = s_start[e] + rank;
+      p.rows[i] = fits ? row : -1;
+      if (fits) p.sources[row] = i;
+    } else if (i < w1) {
+      p.rows[i] = -1;
+    }
+  }
+
+  // every row's expert, and -1 for the rows that no entry fills
+  const int used = s_start[p.experts];
+  for (int r = blockIdx.x * kLayThreads + tid; r < p.rows_total; r += gridDim.x * kLayThreads) {
+    int lo = 0, hi = p.experts;   // s_start[lo] <= r < s_start[hi]
+    if (r < used) {
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_start[mid] <= r) lo = mid;
+        else hi = mid;
+      }
+    }
+    if (p.m_indices != nullptr) p.m_indices[r] = r < used ? lo : -1;
+    if (r >= used || r - s_start[lo] >= s_count[lo]) p.sources[r] = -1;
+  }
+}
+
+static int layout_blocks(int64_t n) { return n <= kLayChunk ? 1 : (int)((n + kLayChunk - 1) / kLayChunk); }
+
+size_t moe_layout_workspace_size(int64_t n, int64_t experts) {
+  const int b = layout_blocks(n);
+  return b > 1 ? (size_t)b * (size_t)experts * 4 : 0;
+}
+
+int launch_moe_layout(const int32_t* ids, int64_t n, int experts, int64_t rows_per_expert, int align,
+                      int64_t rows_total, int32_t* rows, int32_t* sources, int32_t* m_indices, int32_t* counts,
+                      void* ws, hipStream_t stream) {
+  LayoutParams p{};
+  p.ids = ids; p.n = (int)n; p.experts = experts;
+  p.rows_per_expert = (int)rows_per_expert; p.align = align; p.rows_total = (int)rows_total;
+  p.blocks = layout_blocks(n);
+  p.rows = rows; p.sources = sources; p.m_indices = m_indices; p.counts = counts;
+  p.hist = static_cast<int32_t*>(ws);
+  const size_t lds = (size_t)kLayWaves * experts * 4;
+  if (p.blocks > 1) {
+    hipLaunchKernelGGL(layout_count_kernel, dim3(p.blocks), dim3(kLayThreads), lds, stream, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return set_error(kHip, "moe_layout launch: %s", hipGetErrorString(e));
+  }
+  hipLaunchKernelGGL(layout_place_kernel, dim3(p.blocks), dim3(kLayThreads), lds + (2 * (size_t)experts + 1) * 4, stream,
+                     p);
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? kOk : set_error(kHip, "moe_layout launch: %s", hipGetErrorString(e));
+}
+
+// ---------------------------------------------------------------------------
+// Dispatch: each token's row is read (and quantized) once and written to its K expert rows.
+// ---------------------------------------------------------------------------
+enum Form : int { kCopy = 0, kFp8 = 1, kInt8 = 2 };
+constexpr int kRowThreads = 256;
+constexpr int kPadRows = 64;   // rows per padding workgroup
+
+struct DispatchParams {
+  const void* x;
+  const int32_t* rows;
+  const int32_t* sources;
+  const int32_t* m_indices;   // contiguous layout: padding rows are zeroed; NULL: masked layout
+  int tokens, top_k, hidden;
+  int rows_total, rows_per_expert;
+  void* q;
+  float* s;
+  int64_t ld_s;
+};
+
+// Row of a (token, place) entry, or -1: entries without a row, and anything a caller's array holds
+// that is not a row of the layout.
+__device__ __forceinline__ int row_at(const int32_t* rows, int k, int rows_total) {
+  const int r = rows[k];
+  return (uint32_t)r < (uint32_t)rows_total ? r : -1;
+}
+
+// Where row's scales of K group kb lie (FP8: K-group-major per matrix, as the GEMMs read them).
+__device__ __forceinline__ int64_t fp8_scale_at(const DispatchParams& p, int row, int kb, int kbc) {
+  if (p.rows_per_expert == 0) return (int64_t)kb * p.ld_s + row;
+  const int g = row / p.rows_per_expert;
+  return ((int64_t)g * kbc + kb) * p.ld_s + (row - g * p.rows_per_expert);
+}
+
+// Zero the padding rows among [row0, row0 + kPadRows): rows of an expert that no entry fills.
+template <class T, int FORM>
+__device__ __forceinline__ void zero_padding(const DispatchParams& p, int row0) {
+  const int lane = threadIdx.x & 63;
+  const int r = row0 + lane;
+  uint64_t pad = __ballot(r < p.rows_total && p.sources[r < p.rows_total ? r : 0] < 0 &&
+                          p.m_indices[r < p.rows_total ? r : 0] >= 0);
+  const int kbc = (p.hidden + kGroup - 1) / kGroup;
+  constexpr int kSize = FORM == kCopy ? (int)sizeof(T) : 1;
+  const int pieces = p.hidden * kSize / 16;
+  while (pad != 0) {   // the same mask in every wave
+    const int row = row0 + __builtin_ctzll(pad);
+    pad &= pad - 1;
+    u32x4_t* dst = reinterpret_cast<u32x4_t*>(static_cast<uint8_t*>(p.q) + (int64_t)row * p.hidden * kSize);
+    for (int i = threadIdx.x; i < pieces; i += kRowThreads) dst[i] = u32x4_t{0u, 0u, 0u, 0u};
+    if constexpr (FORM == kInt8) {
+      if (threadIdx.x == 0) p.s[row] = 1.0f;
+    } else if constexpr (FORM == kFp8) {
+      for (int kb = threadIdx.x; kb < kbc; kb += kRowThreads) p.s[fp8_scale_at(p, row, kb, kbc)] = 1.0f;
+    }
+  }
+}
+
+template <class T, int FORM>
+__global__ __launch_bounds__(kRowThreads) void dispatch_kernel(DispatchParams p) {
+  __shared__ uint32_t s_max[kRowThreads / 64];
+  const int tid = threadIdx.x;
+  if ((int)blockIdx.x >= p.tokens) {
+    zero_padding<T, FORM>(p, ((int)blockIdx.x - p.tokens) * kPadRows);
+    return;
+  }
+  const int token = blockIdx.x;
+  const T* src = static_cast<const T*>(p.x) + (int64_t)token * p.hidden;
+  const int32_t* rows = p.rows + (int64_t)token * p.top_k;
+
+  if constexpr (FORM == kCopy) {
+    T* out = static_cast<T*>(p.q);
+    for (int i = 8 * tid; i < p.hidden; i += 8 * kRowThreads) {
+      const Raw8<T> v = load8(src + i);
+      for (int k = 0; k < p.top_k; ++k) {
+        const int row = row_at(rows, k, p.rows_total);
+        if (row >= 0) store8(out + (int64_t)row * p.hidden + i, v);
+      }
+    }
+  } else if constexpr (FORM == kInt8) {
+    uint8_t* out = static_cast<uint8_t*>(p.q);
+    uint32_t amax = 0;
+    for (int i = 16 * tid; i < p.hidden; i += 16 * kRowThreads) {
+      float v[16];
+      widen8(load8(src + i), v);
+      widen8(load8(src + i + 8), v + 8);
+#pragma unroll
+      for (int u = 0; u < 16; ++u) amax = umax(amax, abs_bits(v[u]));
+    }
+    amax = wave_max_u32(amax);
+    if ((tid & 63) == 0) s_max[tid >> 6] = amax;
+    __syncthreads();
+    amax = umax(umax(s_max[0], s_max[1]), umax(s_max[2], s_max[3]));
+    const float s = int8_scale(amax);
+    for (int i = 16 * tid; i < p.hidden; i += 16 * kRowThreads) {
+      float v[16];
+      widen8(load8(src + i), v);
+      widen8(load8(src + i + 8), v + 8);
+      const u32x4_t codes = {pack4_int8(v, s), pack4_int8(v + 4, s), pack4_int8(v + 8, s), pack4_int8(v + 12, s)};
+      for (int k = 0; k < p.top_k; ++k) {
+        const int row = row_at(rows, k, p.rows_total);
+        if (row >= 0) *reinterpret_cast<u32x4_t*>(out + (int64_t)row * p.hidden + i) = codes;
+      }
+    }
+    if (tid < p.top_k) {
+      const int row = row_at(rows, tid, p.rows_total);
+      if (row >= 0) p.s[row] = s;
+    }
+  } else {
+    // 8 lanes hold one 128-wide group, 16 elements each (hidden % 16 == 0: a lane's are all present
+    // or all absent; absent ones count as zeros)
+    uint8_t* out = static_cast<uint8_t*>(p.q);
+    const int kbc = (p.hidden + kGroup - 1) / kGroup;
+    const int padded = kbc * kGroup;
+    for (int i = 16 * tid; i < padded; i += 16 * kRowThreads) {
+      const bool there = i < p.hidden;
+      float v[16];
+      widen8(load8(src + (there ? i : 0)), v);
+      widen8(load8(src + (there ? i + 8 : 0)), v + 8);
+      uint32_t amax = 0;
+#pragma unroll
+      for (int u = 0; u < 16; ++u) amax = umax(amax, abs_bits(v[u]));
+      amax = max8_u32(there ? amax : 0u);
+      const float s = amax == 0u ? 1.0f : __uint_as_float(amax) / kE4M3Max;
+      u32x4_t codes;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        codes[u] = pack4_e4m3(clamp448(v[4 * u] / s), clamp448(v[4 * u + 1] / s), clamp448(v[4 * u + 2] / s),
+                              clamp448(v[4 * u + 3] / s));
+      for (int k = 0; k < p.top_k; ++k) {
+        const int row = row_at(rows, k, p.rows_total);
+        if (row < 0) continue;
+        if (there) *reinterpret_cast<u32x4_t*>(out + (int64_t)row * p.hidden + i) = codes;
+        if ((tid & 7) == 0) p.s[fp8_scale_at(p, row, i / kGroup, kbc)] = s;
+      }
+    }
+  }
+}
+
+template <int FORM>
+static int launch_dispatch_form(DispatchParams p, int dtype, hipStream_t stream) {
+  const int64_t pad = p.m_indices != nullptr ? (p.rows_total + kPadRows - 1) / kPadRows : 0;
+  void (*fn)(DispatchParams) = dtype == kF32    ? dispatch_kernel<float, FORM>
+                               : dtype == kBf16 ? dispatch_kernel<Bf16, FORM>
+                                                : dispatch_kernel<_Float16, FORM>;
+  if (p.tokens + pad == 0) return kOk;
+  void* args[] = {&p};
+  return launched(reinterpret_cast<const void*>(fn), dim3((unsigned)(p.tokens + pad)), dim3(kRowThreads), args, stream,
+                  "moe_dispatch");
+}
+
+int launch_moe_dispatch(int form, const void* x, int dtype, const int32_t* rows, const int32_t* sources,
+                        const int32_t* m_indices, int64_t tokens, int top_k, int64_t hidden, int64_t rows_total,
+                        int64_t rows_per_expert, void* q, float* s, int64_t ld_s, hipStream_t stream) {
+  DispatchParams p{};
+  p.x = x; p.rows = rows; p.sources = sources; p.m_indices = m_indices;
+  p.tokens = (int)tokens; p.top_k = top_k; p.hidden = (int)hidden;
+  p.rows_total = (int)rows_total; p.rows_per_expert = (int)rows_per_expert;
+  p.q = q; p.s = s; p.ld_s = ld_s;
+  switch (form) {
+    case kFp8: return launch_dispatch_form<kFp8>(p, dtype, stream);
+    case kInt8: return launch_dispatch_form<kInt8>(p, dtype, stream);
+    default: return launch_dispatch_form<kCopy>(p, dtype, stream);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Combine: y[t] = sum over k of w[t, k] * rows[row(t, k)], in fp32, in the order of k.
+// ---------------------------------------------------------------------------
+constexpr int kCombThreads = 128;
+constexpr int kCombBatch = 8;   // expert rows whose loads are in flight together
+
+struct CombineParams {
+  const void* out;
+  const int32_t* rows;
+  const float* weights;   // NULL: 1
+  int tokens, top_k, hidden;
+  int rows_total;
+  void* y;
+};
+
+template <class T>
+__global__ __launch_bounds__(kCombThreads) void combine_kernel(CombineParams p) {
+  const int token = blockIdx.x;
+  const int i = 8 * (blockIdx.y * kCombThreads + threadIdx.x);
+  if (i >= p.hidden) return;
+  const int32_t* rows = p.rows + (int64_t)token * p.top_k;
+  const float* w = p.weights != nullptr ? p.weights + (int64_t)token * p.top_k : nullptr;
+  const T* src = static_cast<const T*>(p.out) + i;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int k0 = 0; k0 < p.top_k; k0 += kCombBatch) {
+    Raw8<T> v[kCombBatch];
+    int row[kCombBatch];
+#pragma unroll
+    for (int u = 0; u < kCombBatch; ++u) {
+      row[u] = k0 + u < p.top_k ? row_at(rows, k0 + u, p.rows_total) : -1;
+      if (row[u] >= 0) v[u] = load8(src + (int64_t)row[u] * p.hidden);
+    }
+#pragma unroll
+    for (int u = 0; u < kCombBatch; ++u) {
+      if (row[u] >= 0) {
+        float f[8];
+        widen8(v[u], f);
+        const float wk = w != nullptr ? w[k0 + u] : 1.0f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) acc[c] = __builtin_fmaf(wk, f[c], acc[c]);
+      }
+    }
+  }
+  store8(static_cast<T*>(p.y) + (int64_t)token * p.hidden + i, narrow8<T>(acc));
+}
+
+int launch_moe_combine(const void* out, int dtype, const int32_t* rows, const float* weights, int64_t tokens, int top_k,
+                       int64_t hidden, int64_t rows_total, void* y, hipStream_t stream) {
+  CombineParams p{};
+  p.rows_total = (int)rows_total;
+  p.out = out; p.rows = rows; p.weights = weights;
+  p.tokens = (int)tokens; p.top_k = top_k; p.hidden = (int)hidden; p.y = y;
+  void (*fn)(CombineParams) = dtype == kF32 ? combine_kernel<float> : dtype == kBf16 ? combine_kernel<Bf16>
+                                                                                     : combine_kernel<_Float16>;
+  void* args[] = {&p};
+  return launched(reinterpret_cast<const void*>(fn),
+                  dim3((unsigned)tokens, (unsigned)((hidden + 8 * kCombThreads - 1) / (8 * kCombThreads))),
+                  dim3(kCombThreads), args, stream, "moe_combine");
+}
+
+// Gradient of the weighted combine: dout[row(t, k)] = w[t, k] dy[t] (padding rows 0) and
+// dw[t, k] = <dy[t], out[row(t, k)]>, one workgroup per token.
+struct CombineGradParams {
+  DispatchParams pad;    // q = dout; for the padding rows
+  const void* dy;
+  const void* out;
+  const float* weights;
+  void* dout;
+  float* dweights;
+};
+
+template <class T>
+__global__ __launch_bounds__(kRowThreads) void combine_grad_kernel(CombineGradParams p) {
+  __shared__ float s_sum[kRowThreads / 64][kCombBatch];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  if ((int)blockIdx.x >= p.pad.tokens) {
+    zero_padding<T, kCopy>(p.pad, ((int)blockIdx.x - p.pad.tokens) * kPadRows);
+    return;
+  }
+  const int token = blockIdx.x, top_k = p.pad.top_k, hidden = p.pad.hidden;
+  const int32_t* rows = p.pad.rows + (int64_t)token * top_k;
+  const float* w = p.weights + (int64_t)token * top_k;
+  const T* dy = static_cast<const T*>(p.dy) + (int64_t)token * hidden;
+  const T* out = static_cast<const T*>(p.out);
+  T* dout = static_cast<T*>(p.dout);
+  for (int k0 = 0; k0 < top_k; k0 += kCombBatch) {
+    float sum[kCombBatch];
+    int row[kCombBatch];
+#pragma unroll
+    for (int u = 0; u < kCombBatch; ++u) {
+      sum[u] = 0.f;
+      row[u] = k0 + u < top_k ? row_at(rows, k0 + u, p.pad.rows_total) : -1;
+    }
+    for (int i = 8 * tid; i < hidden; i += 8 * kRowThreads) {
+      float g[8];
+      widen8(load8(dy + i), g);
+      Raw8<T> v[kCombBatch];
+#pragma unroll
+      for (int u = 0; u < kCombBatch; ++u)
+        if (row[u] >= 0) v[u] = load8(out + (int64_t)row[u] * hidden + i);
+#pragma unroll
+      for (int u = 0; u < kCombBatch; ++u) {
+        if (row[u] >= 0) {
+          float f[8], d[8];
+          widen8(v[u], f);
+          const float wk = w[k0 + u];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            sum[u] = __builtin_fmaf(g[c], f[c], sum[u]);
+            d[c] = wk * g[c];
+          }
+          store8(dout + (int64_t)row[u] * hidden + i, narrow8<T>(d));
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kCombBatch; ++u) {
+      const float s = wave_sum(sum[u]);
+      if (lane == 0) s_sum[wave][u] = s;
+    }
+    __syncthreads();
+    if (tid < kCombBatch && k0 + tid < top_k) {
+      float s = 0.f;
+      for (int v = 0; v < kRowThreads / 64; ++v) s += s_sum[v][tid];
+      p.dweights[(int64_t)token * top_k + k0 + tid] = s;   // 0 where the entry has no row
+    }
+    __syncthreads();
+  }
+}
+
+int launch_moe_combine_grad(const void* dy, const void* out, int dtype, const int32_t* rows, const int32_t* sources,
+                            const int32_t* m_indices, const float* weights, int64_t tokens, int top_k, int64_t hidden,
+                            int64_t rows_total, void* dout, float* dweights, hipStream_t stream) {
+  CombineGradParams p{};
+  p.pad.rows = rows; p.pad.sources = sources; p.pad.m_indices = m_indices;
+  p.pad.tokens = (int)tokens; p.pad.top_k = top_k; p.pad.hidden = (int)hidden;
+  p.pad.rows_total = (int)rows_total; p.pad.q = dout;
+  p.dy = dy; p.out = out; p.weights = weights; p.dout = dout; p.dweights = dweights;
+  const int64_t pad = m_indices != nullptr ? (rows_total + kPadRows - 1) / kPadRows : 0;
+  if (tokens + pad == 0) return kOk;
+  void (*fn)(CombineGradParams) = dtype == kF32    ? combine_grad_kernel<float>
+                                  : dtype == kBf16 ? combine_grad_kernel<Bf16>
+                                                   : combine_grad_kernel<_Float16>;
+  void* args[] = {&p};
+  return launched(reinterpret_cast<const void*>(fn), dim3((unsigned)(tokens + pad)), dim3(kRowThreads), args, stream,
+                  "moe_combine_grad");
+}
+
+}  // namespace dg

@@ -1,0 +1,150 @@
+// Element types of the row operators (expert routing, expert row layout, 8-bit integer quantizer):
+// fp32, bf16 and fp16 rows, read and written in 8-element pieces and computed in fp32.
+#pragma once
+
+#include "common.hpp"
+
+namespace dg {
+
+typedef unsigned u32x2_t __attribute__((ext_vector_type(2)));
+typedef unsigned u32x4_t __attribute__((ext_vector_type(4)));
+
+// Values of enum dg_dtype (include/dg.h).
+enum Dtype : int { kF32 = 0, kBf16 = 1, kF16 = 2 };
+
+struct Bf16 { uint16_t bits; };
+
+__device__ __forceinline__ float widen(float v) { return v; }
+__device__ __forceinline__ float widen(Bf16 v) { return __uint_as_float((uint32_t)v.bits << 16); }
+__device__ __forceinline__ float widen(_Float16 v) { return (float)v; }
+
+// Round to nearest even to the row's type.
+template <class T>
+__device__ __forceinline__ T narrow(float v);
+template <>
+__device__ __forceinline__ float narrow<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ Bf16 narrow<Bf16>(float v) { return Bf16{(uint16_t)pack2_bf16_rne(v, 0.f)}; }
+template <>
+__device__ __forceinline__ _Float16 narrow<_Float16>(float v) { return (_Float16)v; }
+
+__device__ __forceinline__ uint32_t pack2_f16(float lo, float hi) {
+  typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, f16x2_t{(_Float16)lo, (_Float16)hi});
+}
+
+// Eight consecutive elements as loaded: 16 bytes (32 for fp32), 16-byte aligned.
+template <class T>
+struct Raw8 { u32x4_t w; };
+template <>
+struct Raw8<float> { u32x4_t w, w2; };
+
+template <class T>
+__device__ __forceinline__ Raw8<T> load8(const T* p) {
+  Raw8<T> r;
+  r.w = reinterpret_cast<const u32x4_t*>(p)[0];
+  if constexpr (sizeof(T) == 4) r.w2 = reinterpret_cast<const u32x4_t*>(p)[1];
+  return r;
+}
+
+__device__ __forceinline__ void widen8(const Raw8<float>& r, float* v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = __uint_as_float(r.w[i]);
+    v[4 + i] = __uint_as_float(r.w2[i]);
+  }
+}
+__device__ __forceinline__ void widen8(const Raw8<Bf16>& r, float* v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(r.w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(r.w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void widen8(const Raw8<_Float16>& r, float* v) {
+  typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = r.w[i];   // a copy: the compiler casts element 0 for every element of a vector lvalue
+    const f16x2_t h = __builtin_bit_cast(f16x2_t, w);
+    v[2 * i] = (float)h.x;
+    v[2 * i + 1] = (float)h.y;
+  }
+}
+
+template <class T>
+__device__ __forceinline__ Raw8<T> narrow8(const float* v) {
+  Raw8<T> r;
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r.w[i] = __float_as_uint(v[i]);
+      r.w2[i] = __float_as_uint(v[4 + i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (std::is_same_v<T, Bf16>) r.w[i] = pack2_bf16_rne(v[2 * i], v[2 * i + 1]);
+      else r.w[i] = pack2_f16(v[2 * i], v[2 * i + 1]);
+    }
+  }
+  return r;
+}
+
+template <class T>
+__device__ __forceinline__ void store8(T* p, const Raw8<T>& r) {
+  reinterpret_cast<u32x4_t*>(p)[0] = r.w;
+  if constexpr (sizeof(T) == 4) reinterpret_cast<u32x4_t*>(p)[1] = r.w2;
+}
+
+// One lane's DPP partner under a compile-time control.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, CTRL, 0xf, 0xf, false);
+}
+constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppHalfMirror = 0x141, kDppMirror = 0x140;
+
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// Maximum over each 8-lane group, on every lane of it.
+__device__ __forceinline__ uint32_t max8_u32(uint32_t v) {
+  v = umax(v, dpp_u32<kDppXor1>(v));
+  v = umax(v, dpp_u32<kDppXor2>(v));
+  return umax(v, dpp_u32<kDppHalfMirror>(v));
+}
+// Maximum over the wave, as a wave-uniform (scalar) value.
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+  v = max8_u32(v);
+  v = umax(v, dpp_u32<kDppMirror>(v));
+  const uint32_t a = umax((uint32_t)__builtin_amdgcn_readlane((int)v, 0), (uint32_t)__builtin_amdgcn_readlane((int)v, 16));
+  const uint32_t b = umax((uint32_t)__builtin_amdgcn_readlane((int)v, 32), (uint32_t)__builtin_amdgcn_readlane((int)v, 48));
+  return umax(a, b);
+}
+// Sum over the wave in a fixed order, on every lane.
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int sh = 1; sh < 64; sh *= 2) v += __shfl_xor(v, sh);
+  return v;
+}
+
+// |x| as its bit pattern: as unsigned integers these order like the magnitudes, with a NaN above
+// infinity, so a maximum over them keeps a NaN.
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+constexpr float kInt8Max = 127.0f;
+
+// Scale of a row whose largest magnitude has these bits: amax / 127 (IEEE division), 1 for an
+// all-zero row, NaN or infinite where the row holds such a value.
+__device__ __forceinline__ float int8_scale(uint32_t amax_bits) {
+  return amax_bits == 0u ? 1.0f : __uint_as_float(amax_bits) / kInt8Max;
+}
+// Four codes rne(v / s) (IEEE division; |v| <= amax keeps them in [-127, 127]), packed little-endian.
+// A quotient that is not a number gives code 0; the row's scale carries the NaN on.
+__device__ __forceinline__ uint32_t pack4_int8(const float* v, float s) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w |= ((uint32_t)(int)__builtin_rintf(v[i] / s) & 0xffu) << (8 * i);
+  return w;
+}
+
+}  // namespace dg

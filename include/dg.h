@@ -308,6 +308,166 @@ int dg_gemm_fp8_k_grouped_row_scaled(const uint8_t* a, const float* sa, int64_t 
                                      size_t workspace_bytes, dg_stream_t stream);
 
 /*
+ * Element types of the entry points below that take more than one.
+ */
+enum dg_dtype { DG_DTYPE_F32 = 0, DG_DTYPE_BF16 = 1, DG_DTYPE_F16 = 2 };
+
+/*
+ * Expert routing and the expert row layout: what lies between a router's logits and the grouped
+ * GEMMs of the MoE forms above, and between their results and the tokens.  Arrays of indices,
+ * weights, scales and logits need their elements' alignment only; row data (x, q, out, y, ...) the
+ * 16-byte alignment of every other pointer.  Deterministic: the same inputs give the same bits.
+ */
+
+/*
+ * Choice of top_k experts for each token from its logits x (tokens, experts).
+ *   scores   s_i = softmax(x)_i or 1 / (1 + exp(-x_i));  a logit of -inf switches its expert off;
+ *   choice   c_i = s_i + bias_i (bias: fp32 (experts,), NULL for none; it decides the choice only,
+ *            the balance correction of DeepSeek-V3 style routers).  For softmax scores without bias
+ *            and with group_top = 1 the logits themselves are compared (the same order);
+ *   groups   num_groups groups of experts / num_groups consecutive experts; a group's value is the sum
+ *            of its group_top (1 or 2) best choice values, the topk_groups best groups stay;
+ *   ids      int32 (tokens, top_k): the best choices of those groups, best first; ties go to the lower
+ *            expert (group); -1 where fewer than top_k experts are available;
+ *   weights  fp32 (tokens, top_k): scale * s, or with renormalize scale * s / (sum of the chosen s);
+ *            0 for id -1, and 0 where that sum is 0.
+ * All in fp32.  A NaN logit is never chosen and makes the weights of its token's choices NaN.
+ * logits : `dtype`, rows ld elements apart (ld >= experts), read only.
+ * Errors: DG_ERR_INVALID_ARG for null pointers, misaligned elements, sizes outside 1 <= experts <= 1024,
+ * 1 <= top_k <= min(64, experts), 1 <= topk_groups <= num_groups <= 64, experts % num_groups != 0,
+ * group_top not 1 or 2, an unknown score or dtype.  tokens = 0 is a no-op.
+ */
+enum dg_moe_score { DG_MOE_SOFTMAX = 0, DG_MOE_SIGMOID = 1 };
+int dg_moe_route(const void* logits, int dtype, int64_t ld, const float* bias, int64_t tokens, int64_t experts,
+                 int64_t top_k, int64_t num_groups, int64_t topk_groups, int group_top, int score, int renormalize,
+                 float scale, int32_t* ids, float* weights, dg_stream_t stream);
+
+/*
+ * Gradient of the weights of dg_moe_route with respect to the logits, the choice (ids) held fixed:
+ * dlogits (tokens, experts), rows ld_out apart, written whole (0 for experts that do not matter), in
+ * the logits' type, from dweights fp32 (tokens, top_k).  Entries of ids outside [0, experts) count as
+ * not chosen.  Same errors as dg_moe_route.
+ */
+int dg_moe_route_grad(const float* dweights, const void* logits, int dtype, int64_t ld, const int32_t* ids,
+                      int64_t tokens, int64_t experts, int64_t top_k, int score, int renormalize, float scale,
+                      void* dlogits, int64_t ld_out, dg_stream_t stream);
+
+/* Rows that the contiguous layout of any choice of experts fits in (a multiple of 128). */
+int64_t dg_moe_layout_rows(int64_t tokens, int64_t top_k, int64_t experts);
+
+/* Workspace bytes of dg_moe_layout (no initial content needed; 0: none). */
+size_t dg_moe_layout_workspace_size(int64_t tokens, int64_t top_k, int64_t experts);
+
+/*
+ * Places the (token, k) entries of ids (int32 (tokens, top_k)) into the experts' rows, each expert's in
+ * the order of token * top_k + k; ids outside [0, experts) get no row.
+ *   rows_per_expert = 0: the contiguous layout of dg_gemm_*_grouped_contiguous: each expert's rows start
+ *     at a multiple of 128.  m_indices int32 (rows_total,): the rows' expert, padding rows included, -1
+ *     past the last expert's.  rows_total: a multiple of 128, at least dg_moe_layout_rows(...).
+ *   rows_per_expert > 0: the masked layout of dg_gemm_*_grouped_masked: expert e's rows start at
+ *     e * rows_per_expert; entries past its rows are dropped.  m_indices is NULL and rows_total =
+ *     experts * rows_per_expert.  counts serve as masked_m.
+ *   rows int32 (tokens, top_k): each entry's row, -1 for none.  sources int32 (rows_total,): each row's
+ *     entry (token * top_k + k), -1 for none.  counts int32 (experts,): each expert's entries, dropped ones
+ *     included.
+ * workspace : at least dg_moe_layout_workspace_size bytes; calls that share it must be ordered.
+ * Errors: DG_ERR_INVALID_ARG as above, for experts outside [1, 1024] and top_k outside [1, 64];
+ * DG_ERR_WORKSPACE; DG_ERR_UNSUPPORTED for 2^31 entries or rows.
+ */
+int dg_moe_layout(const int32_t* ids, int64_t tokens, int64_t top_k, int64_t experts, int64_t rows_per_expert,
+                  int64_t rows_total, int32_t* rows, int32_t* sources, int32_t* m_indices, int32_t* counts,
+                  void* workspace, size_t workspace_bytes, dg_stream_t stream);
+
+/*
+ * Copies each token's row of x (tokens, hidden) to the rows of its entries in a layout (its rows,
+ * sources, m_indices, rows_total, rows_per_expert).  In the contiguous layout the padding rows of every
+ * expert are written as zeros (their scales as 1); rows of no expert, and the masked layout's rows past
+ * an expert's count, stay untouched.
+ *   dg_moe_dispatch       out: (rows_total, hidden) in x's type;
+ *   dg_moe_dispatch_fp8   q: E4M3 bytes, sa: the activation scales of dg_quantize_per_token_group for the
+ *                         same matrices (contiguous: sa[kb * ld_sa + row]; masked: per expert), bit for bit;
+ *   dg_moe_dispatch_int8  q, s: as dg_quantize_int8_per_token gives them, s fp32 (rows_total,).
+ * The gradient with respect to x is dg_moe_combine of the rows' gradients without weights.
+ * Errors: DG_ERR_INVALID_ARG as above, hidden not a positive multiple of 16, ld_sa too small or not a
+ * multiple of 4.
+ */
+int dg_moe_dispatch(const void* x, int dtype, const int32_t* rows, const int32_t* sources, const int32_t* m_indices,
+                    int64_t tokens, int64_t top_k, int64_t hidden, int64_t rows_total, int64_t rows_per_expert,
+                    void* out, dg_stream_t stream);
+int dg_moe_dispatch_fp8(const void* x, int dtype, const int32_t* rows, const int32_t* sources, const int32_t* m_indices,
+                        int64_t tokens, int64_t top_k, int64_t hidden, int64_t rows_total, int64_t rows_per_expert,
+                        uint8_t* q, float* sa, int64_t ld_sa, dg_stream_t stream);
+int dg_moe_dispatch_int8(const void* x, int dtype, const int32_t* rows, const int32_t* sources,
+                         const int32_t* m_indices, int64_t tokens, int64_t top_k, int64_t hidden, int64_t rows_total,
+                         int64_t rows_per_expert, int8_t* q, float* s, dg_stream_t stream);
+
+/*
+ * y[t] = sum over k of weights[t, k] * out[rows[t, k]] (entries without a row add nothing; weights NULL:
+ * all 1), in fp32 in the order of k, rounded once.  out (rows_total, hidden), y (tokens, hidden) in `dtype`.
+ */
+int dg_moe_combine(const void* out, int dtype, const int32_t* rows, const float* weights, int64_t tokens, int64_t top_k,
+                   int64_t hidden, int64_t rows_total, void* y, dg_stream_t stream);
+
+/*
+ * Gradients of the weighted combine: dout[rows[t, k]] = weights[t, k] * dy[t] (padding rows of the
+ * contiguous layout 0, other rows untouched) and dweights[t, k] = <dy[t], out[rows[t, k]]> in fp32 (0 for
+ * entries without a row).
+ */
+int dg_moe_combine_grad(const void* dy, const void* out, int dtype, const int32_t* rows, const int32_t* sources,
+                        const int32_t* m_indices, const float* weights, int64_t tokens, int64_t top_k, int64_t hidden,
+                        int64_t rows_total, void* dout, float* dweights, dg_stream_t stream);
+
+/*
+ * 8-bit integer GEMMs: D = (A * B^T) * sa[row] * sb[col] with one fp32 scale per token (row of A) and
+ * one per output channel (row of B).  The sum over K is exact in int32; scales and the one rounding to
+ * the output's type (out_dtype, a dg_dtype) follow it.  K is a multiple of 16 as everywhere, and at most
+ * 131056 (what int32 holds of products of any codes); DG_ERR_UNSUPPORTED above.
+ */
+
+/*
+ * Per-row quantizer: s = amax / 127 over the row (1 when amax = 0), q = rne(x / s), both IEEE fp32
+ * divisions.  x (rows, k) in `dtype` - activations (a scale per token) or weights (a scale per output
+ * channel); q int8 (rows, k); s fp32 (rows,).  Bit-exact.  A row with a NaN or an infinity gets a NaN or
+ * infinite scale (its product is NaN).
+ */
+int dg_quantize_int8_per_token(const void* x, int dtype, int64_t rows, int64_t k, int8_t* q, float* s,
+                               dg_stream_t stream);
+
+/*
+ * Normal form: a (m, k), sa (m,), b (n, k), sb (n,), d (m, n).
+ * workspace : optional, as dg_gemm_fp8_nt's (counter prefix zero before the first use, left zero); NULL
+ *   or smaller than dg_gemm_int8_workspace_size(m, n, k, 1): no K split.  The result is the same bits.
+ */
+int dg_gemm_int8_nt(const int8_t* a, const float* sa, const int8_t* b, const float* sb, void* d, int out_dtype,
+                    int64_t m, int64_t n, int64_t k, void* workspace, size_t workspace_bytes, dg_stream_t stream);
+
+/*
+ * Normal form on unquantized activations x (m, k) in `dtype`: dg_quantize_int8_per_token followed by
+ * dg_gemm_int8_nt, the same bits, in one call.
+ * workspace : required, dg_gemm_int8_nt_act_quant_workspace_size(m, n, k) bytes, counter prefix as above.
+ */
+int dg_gemm_int8_nt_act_quant(const void* x, int dtype, const int8_t* b, const float* sb, void* d, int out_dtype,
+                              int64_t m, int64_t n, int64_t k, void* workspace, size_t workspace_bytes,
+                              dg_stream_t stream);
+size_t dg_gemm_int8_nt_act_quant_workspace_size(int64_t m, int64_t n, int64_t k);
+
+/* Contiguous-grouped form (layout and skipping as dg_gemm_fp8_grouped_contiguous): a (m_total, k),
+ * sa (m_total,), b (num_groups, n, k), sb (num_groups, n), d (m_total, n). */
+int dg_gemm_int8_grouped_contiguous(const int8_t* a, const float* sa, const int8_t* b, const float* sb,
+                                    const int32_t* m_indices, int64_t num_groups, void* d, int out_dtype,
+                                    int64_t m_total, int64_t n, int64_t k, dg_stream_t stream);
+
+/* Masked-grouped form (as dg_gemm_fp8_grouped_masked): a (num_groups, m_max, k), sa (num_groups, m_max),
+ * b (num_groups, n, k), sb (num_groups, n), d (num_groups, m_max, n); rows at or past masked_m[g] are
+ * never written. */
+int dg_gemm_int8_grouped_masked(const int8_t* a, const float* sa, const int8_t* b, const float* sb, void* d,
+                                int out_dtype, const int32_t* masked_m, int64_t num_groups, int64_t m_max, int64_t n,
+                                int64_t k, void* workspace, size_t workspace_bytes, dg_stream_t stream);
+
+/* Workspace bytes that let dg_gemm_int8_nt / dg_gemm_int8_grouped_masked split K (0: never split). */
+size_t dg_gemm_int8_workspace_size(int64_t m, int64_t n, int64_t k, int64_t num_groups);
+
+/*
  * Utilities (CSDN article, "utilities": cap on the compute units used,
  * contiguous-layout alignment, aligned column-major scale tensor).
  */

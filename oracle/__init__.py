@@ -23,10 +23,13 @@ news/blog pages; each function cites the page title and section it follows):
 * ``train`` - the backward GEMMs of a linear layer (the pages say the library serves V3/R1
   training; the layouts are readings): per-channel token groups, transposed block scales and
   the GEMM whose two operands both carry per-row group scales.
+* ``moe``   - expert routing (with its gradient), the expert row layout, dispatch and combine (with
+  theirs), in 64 bits.
+* ``int8``  - the per-row 8-bit integer quantizer and the three forms of its GEMM.
 
 Every function here is pinned by ``tests/test_oracle_*.py`` against facts that
 do not come from this package (the format definition, torch's independent
 float8_e4m3fn codec, exact rational arithmetic, closed forms, invariants).
 """
 
-from . import bf16, e4m3, quant, gemm, train  # noqa: F401
+from . import bf16, e4m3, quant, gemm, int8, moe, train  # noqa: F401
