@@ -173,16 +173,461 @@ __global__ __launch_bounds__(C::kThreads) void gemm_int8_kernel(I8Params p) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// Few rows (m <= 128): the weights are streamed once from memory and nothing else matters much.
+// A workgroup takes 16 R weight rows and 16 J activation rows; its W waves (and S workgroups of one
+// tile) split K between them.  Both operands go from memory straight into MFMA registers: a lane reads
+// 16 bytes of one row, so an instruction covers 16 rows x 64 bytes, and U steps of 64 K bytes are in
+// flight while the U before them are multiplied.  Rows past the edges take out-of-range addresses and
+// cost no traffic.  The waves' int32 partials are added in LDS with integer atomics, whose order does
+// not matter; the S partials of a tile go through the workspace to the workgroup that arrives last.
+// ---------------------------------------------------------------------------
+struct I8FewParams {
+  const int8_t* a;        // codes, or (with X) the unquantized activations
+  const float* sa;
+  const int8_t* b;
+  const float* sb;
+  void* d;
+  const int32_t* masked_m;
+  int m, n, k;
+  int strips, mtiles;     // tiles of a group: ceil(n / 16R) x ceil(m / 16J)
+  int splits;
+  int steps, steps_per_wave;
+  int out_dtype;
+  int* ws;
+  unsigned* counters;
+};
+
+// The in-kernel quantizer's limits: rows, and the K that its threads hold in registers.
+constexpr int kFewFusedRows = 2;
+constexpr int kFewFusedK = 16384;
+
+struct FewTile { int g, split, id, m0, n0, m_valid; };
+
+// Block -> (group, tile, split).  The m-tiles of one strip and split are 8 blocks apart, so that they
+// run on one XCD, whose L2 then serves the strip's weights to the second; m_valid = 0 past the last.
+template <int BN, int BM>
+__device__ __forceinline__ FewTile few_tile(const I8FewParams& p) {
+  FewTile t;
+  const int units = p.strips * p.splits;
+  const int per_group = ((units + 7) & ~7) * p.mtiles;
+  t.g = blockIdx.x / per_group;
+  const int rest = blockIdx.x - t.g * per_group;
+  const int run = rest / (8 * p.mtiles), in_run = rest - run * (8 * p.mtiles);
+  const int mtile = in_run >> 3;
+  const int unit = 8 * run + (in_run & 7);
+  const int strip = unit / p.splits;
+  t.split = unit - strip * p.splits;
+  t.id = (t.g * p.strips + strip) * p.mtiles + mtile;
+  t.m0 = mtile * BM;
+  t.n0 = strip * BN;
+  t.m_valid = p.m;
+  if (p.masked_m != nullptr) {
+    const int mv = p.masked_m[t.g];
+    t.m_valid = mv < 0 ? 0 : mv > p.m ? p.m : mv;
+  }
+  if (unit >= units) t.m_valid = 0;
+  return t;
+}
+
+// The workgroup's BM x BN sums in s_sum (rows of BN + 4, complete for its K range): added over the
+// tile's splits by the workgroup that arrives last, then scaled, rounded and stored.
+template <int BN, int BM, int NT, class RowScale>
+__device__ __forceinline__ void few_finish(const I8FewParams& p, const FewTile& t, int* s_sum, int* s_last,
+                                           RowScale row_scale) {
+  constexpr int kPitch = BN + 4;
+  constexpr int kChunks = BM * BN / 4;   // pieces of 4 columns
+  const int tid = threadIdx.x;
+  auto piece = [&](int c) { return reinterpret_cast<v4i*>(&s_sum[(c / (BN / 4)) * kPitch + 4 * (c % (BN / 4))]); };
+  if (p.splits > 1) {
+    // partials leave and return by device-scope accesses (no cache holds another XCD's bytes)
+    const __amdgpu_buffer_rsrc_t rs_ws =
+        make_rsrc(p.ws + (int64_t)t.id * p.splits * (BM * BN), (int64_t)p.splits * BM * BN * 4);
+    for (int c = tid; c < kChunks; c += NT)
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, *piece(c)), rs_ws, (t.split * kChunks + c) * 16, 0,
+                                             kCpolSc1);
+    __builtin_amdgcn_s_waitcnt(0);   // this thread's partials have arrived
+    __syncthreads();
+    if (tid == 0) {
+      const unsigned prev = __hip_atomic_fetch_add(p.counters + t.id, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      *s_last = prev == (unsigned)(p.splits - 1);
+      if (*s_last) __hip_atomic_store(p.counters + t.id, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    if (!*s_last) return;
+  }
+  const float* sb = p.sb + (int64_t)t.g * p.n;
+  const __amdgpu_buffer_rsrc_t rs_ws =
+      make_rsrc(p.ws + (int64_t)t.id * p.splits * (BM * BN), p.splits > 1 ? (int64_t)p.splits * BM * BN * 4 : 0);
+  for (int c = tid; c < kChunks; c += NT) {
+    const int row = t.m0 + c / (BN / 4), col = t.n0 + 4 * (c % (BN / 4));
+    const int count = p.n - col;
+    if (row >= t.m_valid || count <= 0) continue;
+    v4i sum = *piece(c);
+    for (int o = 0; o < p.splits; ++o)
+      if (o != t.split)
+        sum += __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rs_ws, (o * kChunks + c) * 16, 0, kCpolSc1));
+    const float sr = row_scale(row);
+    float v[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] = (float)sum[r] * (sr * (r < count ? sb[col + r] : 0.f));
+    store_out4(p.d, p.out_dtype, ((int64_t)t.g * p.m + row) * p.n + col, v, count < 4 ? count : 4, (p.n & 3) == 0);
+  }
+}
+
+template <int R, int U, int W, class X>
+__global__ __launch_bounds__(64 * W) void gemm_int8_direct_kernel(I8FewParams p) {
+  constexpr int NT = 64 * W;
+  constexpr int BN = 16 * R, BM = 16;
+  constexpr int kPitch = BN + 4;
+  constexpr int kHold = 2;   // 8-element pieces of a row per thread: k <= 16 NT
+  __shared__ __attribute__((aligned(16))) int s_sum[BM * kPitch];
+  __shared__ uint32_t s_max[kFewFusedRows * W];
+  __shared__ int s_last;
+  extern __shared__ __attribute__((aligned(16))) uint8_t s_codes[];   // (m, k) codes
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l16 = lane & 15, g4 = lane >> 4;
+  const FewTile t = few_tile<BN, BM>(p);
+  if (t.m0 >= t.m_valid) return;   // uniform, and so for every split of the tile
+
+  const __amdgpu_buffer_rsrc_t rs_b = make_rsrc(p.b + (int64_t)t.n0 * p.k, (int64_t)(p.n - t.n0) * p.k);
+  const uint32_t row_off = (uint32_t)l16 * (uint32_t)p.k + 16u * g4;
+  const int s0 = (t.split * W + wave) * p.steps_per_wave;
+  const int s1 = s0 + p.steps_per_wave < p.steps ? s0 + p.steps_per_wave : p.steps;
+
+  struct Set { v4i b[U][R]; };
+  // U steps of 64 K bytes; chunks past K and steps past s1 take an out-of-range offset and read zeros
+  auto load = [&](Set& v, int s) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k0 = 64 * (s + u);
+      const uint32_t out = s + u < s1 && k0 + 16 * g4 < p.k ? 0u : 0xFFFFFFF0u;
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        v.b[u][i] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(
+                                                rs_b, (row_off + (uint32_t)(16 * i) * (uint32_t)p.k) | out, k0, 0));
+    }
+  };
+  v4i acc[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) acc[i] = v4i{0, 0, 0, 0};
+  auto multiply = [&](const Set& v, int s) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = 64 * (s + u) + 16 * g4;
+      const v4i act = l16 < p.m && s + u < s1 && at < p.k ? *reinterpret_cast<const v4i*>(s_codes + l16 * p.k + at)
+                                                          : v4i{0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < R; ++i) acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(v.b[u][i], act, acc[i], 0, 0, 0);
+    }
+  };
+
+  // every workgroup quantizes the few rows for itself while its first weights are on the way
+  const X* x = reinterpret_cast<const X*>(p.a);
+  Raw8<X> held[kFewFusedRows][kHold];
+#pragma unroll
+  for (int r = 0; r < kFewFusedRows; ++r)
+#pragma unroll
+    for (int h = 0; h < kHold; ++h)
+      if (r < p.m && 8 * (tid + NT * h) < p.k) held[r][h] = load8(x + (int64_t)r * p.k + 8 * (tid + NT * h));
+  Set even, odd;
+  load(even, s0);
+  for (int i = tid; i < BM * kPitch; i += NT) s_sum[i] = 0;
+#pragma unroll
+  for (int r = 0; r < kFewFusedRows; ++r) {
+    if (r >= p.m) break;   // uniform
+    uint32_t amax = 0;
+#pragma unroll
+    for (int h = 0; h < kHold; ++h) {
+      if (8 * (tid + NT * h) < p.k) {
+        float v[8];
+        widen8(held[r][h], v);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) amax = umax(amax, abs_bits(v[c]));
+      }
+    }
+    amax = wave_max_u32(amax);
+    if (lane == 0) s_max[r * W + wave] = amax;
+  }
+  __syncthreads();
+  float scale[kFewFusedRows];
+#pragma unroll
+  for (int r = 0; r < kFewFusedRows; ++r) {
+    if (r >= p.m) break;   // uniform
+    uint32_t amax = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) amax = umax(amax, s_max[r * W + w]);
+    scale[r] = int8_scale(amax);
+#pragma unroll
+    for (int h = 0; h < kHold; ++h) {
+      if (8 * (tid + NT * h) < p.k) {
+        float v[8];
+        widen8(held[r][h], v);
+        *reinterpret_cast<u32x2_t*>(s_codes + r * p.k + 8 * (tid + NT * h)) =
+            u32x2_t{pack4_int8(v, scale[r]), pack4_int8(v + 4, scale[r])};
+      }
+    }
+  }
+  __syncthreads();
+  for (int s = s0; s < s1; s += 2 * U) {
+    load(odd, s + U);
+    multiply(even, s);
+    if (s + U >= s1) break;
+    load(even, s + 2 * U);
+    multiply(odd, s + U);
+  }
+
+  // the waves' partials: integer atomics, whose order does not matter
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (l16 < p.m) atomicAdd(&s_sum[l16 * kPitch + 16 * i + 4 * g4 + r], acc[i][r]);
+  __syncthreads();
+  few_finish<BN, BM, NT>(p, t, s_sum, &s_last, [&](int row) {
+    float sr = scale[0];
+#pragma unroll
+    for (int r = 1; r < kFewFusedRows; ++r) sr = row == r ? scale[r] : sr;
+    return sr;
+  });
+}
+
+// 17 to 128 rows: as above, but the activations pass through LDS.  Read by every wave straight from
+// memory they cost as many vector-memory requests as the weights (16 rows x 64 bytes an instruction),
+// and that request rate, not the bytes, bounds the kernel (64 x 7168 x 16384: 45 us, 31 us with the
+// activation reads masked off).  Here 2 times 16 weight rows each belong to 4 waves that share
+// their K chunk of 512 bytes, and the workgroup brings the chunk's 16 J activation rows in once, a whole
+// line per 8 lanes, through registers into one of two LDS buffers: one barrier per chunk, the next
+// chunk's weights and activations in flight across it.
+constexpr int kStNS = 2, kStKS = 4;
+
+template <int R, int J, int CHUNK>
+__global__ __launch_bounds__(64 * kStNS * kStKS) void gemm_int8_staged_kernel(I8FewParams p) {
+  constexpr int NS = kStNS, KS = kStKS, NT = 64 * NS * KS;
+  constexpr int BN = 16 * R * NS, BM = 16 * J;
+  constexpr int kPitch = CHUNK + 16;   // 16 rows of one 16-byte column fall in different banks
+  constexpr int U = CHUNK / 64 / KS;              // steps of 64 K bytes per wave and chunk
+  constexpr int kPieces = BM * CHUNK / 16 / NT;   // 16-byte pieces per thread and chunk
+  constexpr int kBuf = BM * kPitch;
+  constexpr int kSumPitch = BN + 4;
+  static_assert(kPieces * NT * 16 == BM * CHUNK && U * KS * 64 == CHUNK, "a chunk splits evenly");
+  constexpr int kLds = 2 * kBuf > BM * kSumPitch * 4 ? 2 * kBuf : BM * kSumPitch * 4;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[kLds];
+  __shared__ int s_last;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int ns = wave % NS, kh = wave / NS;
+  const int l16 = lane & 15, g4 = lane >> 4;
+  const FewTile t = few_tile<BN, BM>(p);
+  if (t.m0 >= t.m_valid) return;   // uniform, and so for every split of the tile
+
+  const __amdgpu_buffer_rsrc_t rs_b = make_rsrc(p.b + ((int64_t)t.g * p.n + t.n0) * p.k, (int64_t)(p.n - t.n0) * p.k);
+  const __amdgpu_buffer_rsrc_t rs_a = make_rsrc(p.a + ((int64_t)t.g * p.m + t.m0) * p.k, (int64_t)(t.m_valid - t.m0) * p.k);
+  // steps_per_wave counts chunks here: the workgroup's chunks [c0, c1)
+  const int c0 = t.split * p.steps_per_wave;
+  const int c1 = c0 + p.steps_per_wave < p.steps ? c0 + p.steps_per_wave : p.steps;
+
+  // this thread's activation pieces: row piece / 32, 16-byte column piece % 32 of the chunk
+  u32x4 act[kPieces];
+  auto load_act = [&](int c) {
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      const int piece = tid + NT * u, row = piece / (CHUNK / 16), col = 16 * (piece % (CHUNK / 16));
+      const uint32_t out = c < c1 && c * CHUNK + col < p.k ? 0u : 0xFFFFFFF0u;   // past K: zeros
+      act[u] = __builtin_amdgcn_raw_buffer_load_b128(rs_a, ((uint32_t)row * (uint32_t)p.k + (uint32_t)col) | out,
+                                                     c * CHUNK, 0);
+    }
+  };
+  auto store_act = [&](int c) {
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      const int piece = tid + NT * u, row = piece / (CHUNK / 16), col = 16 * (piece % (CHUNK / 16));
+      *reinterpret_cast<u32x4*>(smem + (c & 1) * kBuf + row * kPitch + col) = act[u];
+    }
+  };
+  struct Set { v4i b[U][R]; };
+  const uint32_t row_off = (uint32_t)(16 * R * ns + l16) * (uint32_t)p.k + 16u * g4;
+  auto load_b = [&](Set& v, int c) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k0 = c * CHUNK + 64 * (kh * U + u);
+      const uint32_t out = c < c1 && k0 + 16 * g4 < p.k ? 0u : 0xFFFFFFF0u;
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        v.b[u][i] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(
+                                                rs_b, (row_off + (uint32_t)(16 * i) * (uint32_t)p.k) | out, k0, 0));
+    }
+  };
+  v4i acc[R][J];
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int j = 0; j < J; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+  auto multiply = [&](const Set& v, int c) {
+    const uint8_t* base = smem + (c & 1) * kBuf + l16 * kPitch + 64 * kh * U + 16 * g4;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      v4i fa[J];
+#pragma unroll
+      for (int j = 0; j < J; ++j) fa[j] = *reinterpret_cast<const v4i*>(base + 16 * j * kPitch + 64 * u);
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int j = 0; j < J; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(v.b[u][i], fa[j], acc[i][j], 0, 0, 0);
+    }
+  };
+
+  // one chunk of weights and activations ahead (two or three ahead measured the same or slower);
+  // chunks past c1 read nothing
+  Set even, odd;
+  load_act(c0);
+  load_b(even, c0);
+  for (int c = c0; c < c1; c += 2) {
+    store_act(c);
+    load_act(c + 1);
+    load_b(odd, c + 1);
+    __syncthreads();   // chunk c is in its buffer; every wave is done with chunk c - 1's
+    multiply(even, c);
+    if (c + 1 >= c1) break;   // uniform
+    store_act(c + 1);
+    load_act(c + 2);
+    load_b(even, c + 2);
+    __syncthreads();
+    multiply(odd, c + 1);
+  }
+
+  __syncthreads();   // the buffers become the sums
+  int* s_sum = reinterpret_cast<int*>(smem);
+#pragma unroll
+  for (int h = 0; h < KS; ++h) {
+    if (kh == h) {
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          v4i* at = reinterpret_cast<v4i*>(&s_sum[(16 * j + l16) * kSumPitch + 16 * (R * ns + i) + 4 * g4]);
+          *at = h == 0 ? acc[i][j] : *at + acc[i][j];
+        }
+    }
+    __syncthreads();
+  }
+  few_finish<BN, BM, NT>(p, t, s_sum, &s_last, [&](int row) { return p.sa[(int64_t)t.g * p.m + row]; });
+}
+
+// ---------------------------------------------------------------------------
+// Host side.
+// ---------------------------------------------------------------------------
 using I8Tile = I8Cfg<128, 128, 64, 64>;
+
+struct FewPlan {
+  bool direct;
+  int r, j, waves, unit;   // unit: K bytes of a step (direct) or chunk (staged)
+  int bn, bm;
+  int strips, mtiles, splits, steps, steps_per_wave;
+  int64_t tiles;
+  size_t ws_bytes;
+};
+
+// Few-row plan.  `direct`: the kernel that quantizes its rows itself.  What the choices measured:
+//  * direct, waves a workgroup (they share K): 1 x 24576 x 1536 takes 10.3 us with 4, 13.9 with 8, 16.3
+//    with 16; 1 x 4096 x 7168 9.0 with 8, 9.9 with 16; K past 8192 needs 16 to hold the row.
+//  * direct, 32 weight rows a workgroup where that still gives ~3/4 of a workgroup per CU: 1 x 7168 x 2048
+//    5.2 us against 5.7 with 16.
+//  * staged, 128-row tiles: chunks of 256 (two workgroups' buffers fit a CU): 128 x 24576 x 1536 23.0 us,
+//    two 64-row tiles 26.4; 32 weight rows a wave once K is long enough to pay for splitting it:
+//    128 x 7168 x 16384 45.7 us against 52.9 with 16.
+static FewPlan few_plan(bool direct, int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus, bool allow_split) {
+  FewPlan f{};
+  f.direct = direct;
+  if (direct) {
+    f.j = 1;
+    f.r = n >= (int64_t)24 * num_cus ? 2 : 1;
+    f.waves = k <= 4096 ? 4 : k <= 8192 ? 8 : 16;
+    f.unit = 64;
+  } else {
+    f.j = m <= 16 ? 1 : m <= 32 ? 2 : m <= 64 ? 4 : 8;
+    f.r = f.j == 8 && k >= 8192 && n >= (int64_t)24 * num_cus ? 2 : 1;
+    f.waves = kStNS * kStKS;
+    f.unit = f.j == 8 ? 256 : 512;
+  }
+  f.bn = 16 * f.r * (direct ? 1 : kStNS);
+  f.bm = 16 * f.j;
+  f.strips = (int)((n + f.bn - 1) / f.bn);
+  f.mtiles = (int)((m + f.bm - 1) / f.bm);
+  f.tiles = (int64_t)f.strips * f.mtiles * groups;
+  const int sharing = direct ? f.waves : 1;   // units of K go to waves (direct) or to workgroups (staged)
+  f.steps = (int)((k + f.unit - 1) / f.unit);
+  // split K until there is about one workgroup per CU, each keeping a few units (64 x 4096 x 7168:
+  // unsplit 128 workgroups 20 us, split in two 13.1, in four 15.5)
+  int64_t want = (2 * (int64_t)num_cus / f.tiles + 1) / 2;
+  const int64_t most = f.steps / (direct ? 4 * sharing : 2);
+  if (want > most) want = most;
+  if (want > kMaxSplits) want = kMaxSplits;
+  if (!allow_split || want < 1 || f.tiles > kMaxCounterTiles) want = 1;
+  f.steps_per_wave = (int)((f.steps + want * sharing - 1) / (want * sharing));
+  f.splits = (int)((f.steps + (int64_t)f.steps_per_wave * sharing - 1) / ((int64_t)f.steps_per_wave * sharing));   // none empty
+  f.ws_bytes = f.splits > 1 ? kCounterBytes + (size_t)f.tiles * f.splits * f.bn * f.bm * 4 : 0;
+  return f;
+}
+
+static const void* staged_fn(const FewPlan& f) {
+  void (*fn)(I8FewParams) = f.j == 1   ? gemm_int8_staged_kernel<1, 1, 512>
+                            : f.j == 2 ? gemm_int8_staged_kernel<1, 2, 512>
+                            : f.j == 4 ? gemm_int8_staged_kernel<1, 4, 512>
+                            : f.r == 1 ? gemm_int8_staged_kernel<1, 8, 256>
+                                       : gemm_int8_staged_kernel<2, 8, 256>;
+  return reinterpret_cast<const void*>(fn);
+}
+
+template <class X>
+static const void* direct_fn_of(const FewPlan& f) {
+  void (*fn)(I8FewParams);
+  if (f.r == 1)
+    fn = f.waves == 4 ? gemm_int8_direct_kernel<1, 8, 4, X> : f.waves == 8 ? gemm_int8_direct_kernel<1, 8, 8, X>
+                                                                           : gemm_int8_direct_kernel<1, 8, 16, X>;
+  else
+    fn = f.waves == 4 ? gemm_int8_direct_kernel<2, 4, 4, X> : f.waves == 8 ? gemm_int8_direct_kernel<2, 4, 8, X>
+                                                                           : gemm_int8_direct_kernel<2, 4, 16, X>;
+  return reinterpret_cast<const void*>(fn);
+}
+static const void* direct_fn(const FewPlan& f, int dtype) {
+  return dtype == kF32 ? direct_fn_of<float>(f) : dtype == kBf16 ? direct_fn_of<Bf16>(f) : direct_fn_of<_Float16>(f);
+}
+
+// Rows that run on the few-row kernel.
+constexpr int64_t kFewRows = 128;
+
+static int launch_few(const FewPlan& f, const void* fn, I8FewParams p, size_t lds, int64_t groups, void* counters,
+                      void* partials, hipStream_t stream) {
+  p.strips = f.strips; p.mtiles = f.mtiles; p.splits = f.splits;
+  p.steps = f.steps; p.steps_per_wave = f.steps_per_wave;
+  p.counters = static_cast<unsigned*>(counters);
+  p.ws = static_cast<int*>(partials);
+  const int64_t blocks = groups * ((((int64_t)f.strips * f.splits + 7) & ~(int64_t)7) * f.mtiles);
+  if (blocks * 64 * f.waves > 0xffffffffLL) return set_error(kUnsupported, "int8 gemm: too many output tiles");
+  void* args[] = {&p};
+  const hipError_t e = hipLaunchKernel(fn, dim3((unsigned)blocks), dim3(64 * f.waves), args, lds, stream);
+  return e == hipSuccess ? kOk : set_error(kHip, "int8 gemm launch: %s", hipGetErrorString(e));
+}
 
 int launch_quant_int8(const void* x, int dtype, int64_t rows, int64_t k, int8_t* q, float* s, hipStream_t stream);
 
-size_t int8_workspace_size(int64_t, int64_t, int64_t, int64_t, int) { return 0; }
+size_t int8_workspace_size(int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus) {
+  return m <= kFewRows ? few_plan(false, m, n, k, groups, num_cus, true).ws_bytes : 0;
+}
 
 int launch_gemm_int8(int layout, const int8_t* a, const float* sa, const int8_t* b, const float* sb, void* d,
                      int out_dtype, const int32_t* m_indices, const int32_t* masked_m, int64_t groups, int64_t m,
                      int64_t n, int64_t k, void* ws, size_t ws_bytes, hipStream_t stream, int num_cus) {
-  (void)ws; (void)ws_bytes; (void)num_cus;
+  if (layout != kContiguous && m <= kFewRows) {
+    FewPlan f = few_plan(false, m, n, k, groups, num_cus, ws != nullptr);
+    if (ws_bytes < f.ws_bytes) f = few_plan(false, m, n, k, groups, num_cus, false);
+    I8FewParams p{};
+    p.a = a; p.sa = sa; p.b = b; p.sb = sb; p.d = d; p.masked_m = masked_m;
+    p.m = (int)m; p.n = (int)n; p.k = (int)k; p.out_dtype = out_dtype;
+    return launch_few(f, staged_fn(f), p, 0, groups, ws, static_cast<uint8_t*>(ws) + kCounterBytes, stream);
+  }
   I8Params p{};
   p.a = a; p.sa = sa; p.b = b; p.sb = sb; p.d = d;
   p.m_indices = m_indices; p.masked_m = masked_m;
@@ -202,22 +647,46 @@ int launch_gemm_int8(int layout, const int8_t* a, const float* sa, const int8_t*
   return e == hipSuccess ? kOk : set_error(kHip, "int8 gemm launch: %s", hipGetErrorString(e));
 }
 
-// In-call quantization: the counter prefix, the codes, the scales (256-byte pieces).
+// In-call quantization.  Up to kFewFusedRows rows whose codes fit in LDS are quantized by the product's
+// own workgroups; more rows by a launch of the quantizer into the workspace: the counter prefix, the
+// codes, the scales (256-byte pieces), then the K split's partials.
 static size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+static bool few_fused(int64_t m, int64_t k) { return m <= kFewFusedRows && k <= kFewFusedK; }
 
 size_t int8_act_quant_workspace_size(int64_t m, int64_t n, int64_t k, int num_cus) {
-  (void)n; (void)num_cus;
-  return kCounterBytes + align256((size_t)(m * k)) + align256((size_t)m * 4);
+  if (few_fused(m, k)) {
+    const size_t split = few_plan(true, m, n, k, 1, num_cus, true).ws_bytes;
+    return split > 0 ? split : kCounterBytes;
+  }
+  const size_t split = int8_workspace_size(m, n, k, 1, num_cus);
+  return kCounterBytes + align256((size_t)(m * k)) + align256((size_t)m * 4) + (split > 0 ? split - kCounterBytes : 0);
 }
 
 int launch_gemm_int8_act_quant(const void* x, int dtype, const int8_t* b, const float* sb, void* d, int out_dtype,
                                int64_t m, int64_t n, int64_t k, void* ws, size_t ws_bytes, hipStream_t stream,
                                int num_cus) {
-  (void)ws_bytes;
-  int8_t* q = reinterpret_cast<int8_t*>(static_cast<uint8_t*>(ws) + kCounterBytes);
-  float* s = reinterpret_cast<float*>(q + align256((size_t)(m * k)));
+  (void)ws_bytes;   // checked by the caller against int8_act_quant_workspace_size
+  if (few_fused(m, k)) {
+    const FewPlan f = few_plan(true, m, n, k, 1, num_cus, true);
+    I8FewParams p{};
+    p.a = static_cast<const int8_t*>(x); p.b = b; p.sb = sb; p.d = d;
+    p.m = (int)m; p.n = (int)n; p.k = (int)k; p.out_dtype = out_dtype;
+    return launch_few(f, direct_fn(f, dtype), p, (size_t)(m * k), 1, ws, static_cast<uint8_t*>(ws) + kCounterBytes, stream);
+  }
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  int8_t* q = reinterpret_cast<int8_t*>(w + kCounterBytes);
+  float* s = reinterpret_cast<float*>(w + kCounterBytes + align256((size_t)(m * k)));
   const int r = launch_quant_int8(x, dtype, m, k, q, s, stream);
   if (r != kOk) return r;
+  if (m <= kFewRows) {
+    // the split's partials follow the scales; its counters are the workspace's own prefix
+    const FewPlan f = few_plan(false, m, n, k, 1, num_cus, true);
+    I8FewParams p{};
+    p.a = q; p.sa = s; p.b = b; p.sb = sb; p.d = d;
+    p.m = (int)m; p.n = (int)n; p.k = (int)k; p.out_dtype = out_dtype;
+    return launch_few(f, staged_fn(f), p, 0, 1, ws, w + kCounterBytes + align256((size_t)(m * k)) + align256((size_t)m * 4),
+                      stream);
+  }
   return launch_gemm_int8(kDense, q, s, b, sb, d, out_dtype, nullptr, nullptr, 1, m, n, k, nullptr, 0, stream, num_cus);
 }
 

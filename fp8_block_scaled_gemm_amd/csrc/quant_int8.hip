@@ -7,57 +7,74 @@
 
 namespace dg {
 
-constexpr int kQ8Threads = 256;
+// One workgroup of NT threads per row.  Each thread holds up to kQ8Hold pieces of 8 elements in
+// registers, so that a row of up to 8 * NT * kQ8Hold elements is read once; the rest of a longer row is
+// read again (from the caches) for its codes.
+constexpr int kQ8Hold = 2;
 
-// One workgroup per row: the row is read once for its maximum and again (from the caches) for its codes.
-template <class T>
-__global__ __launch_bounds__(kQ8Threads) void quant_int8_kernel(const T* __restrict__ x, int k, uint8_t* __restrict__ q,
-                                                                float* __restrict__ s_out) {
-  __shared__ uint32_t s_max[kQ8Threads / 64];
+template <class T, int NT>
+__global__ __launch_bounds__(NT) void quant_int8_kernel(const T* __restrict__ x, int k, uint8_t* __restrict__ q,
+                                                        float* __restrict__ s_out) {
+  constexpr int W = NT / 64;
+  __shared__ uint32_t s_max[W];
   const int tid = threadIdx.x;
   const int64_t row = blockIdx.x;
   const T* src = x + row * k;
   uint8_t* dst = q + row * k;
-  uint32_t amax = 0;
-  for (int i = 16 * tid; i < k; i += 16 * kQ8Threads) {
-    float v[16];
-    widen8(load8(src + i), v);
-    widen8(load8(src + i + 8), v + 8);
+  Raw8<T> held[kQ8Hold];
 #pragma unroll
-    for (int u = 0; u < 16; ++u) amax = umax(amax, abs_bits(v[u]));
-  }
+  for (int h = 0; h < kQ8Hold; ++h)
+    if (8 * (tid + NT * h) < k) held[h] = load8(src + 8 * (tid + NT * h));
+  uint32_t amax = 0;
+  auto largest = [&](const Raw8<T>& r) {
+    float v[8];
+    widen8(r, v);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) amax = umax(amax, abs_bits(v[c]));
+  };
+#pragma unroll
+  for (int h = 0; h < kQ8Hold; ++h)
+    if (8 * (tid + NT * h) < k) largest(held[h]);
+  for (int i = 8 * (tid + NT * kQ8Hold); i < k; i += 8 * NT) largest(load8(src + i));
   amax = wave_max_u32(amax);
-  if ((tid & 63) == 0) s_max[tid >> 6] = amax;
-  __syncthreads();
-  amax = umax(umax(s_max[0], s_max[1]), umax(s_max[2], s_max[3]));
-  const float s = int8_scale(amax);
-  for (int i = 16 * tid; i < k; i += 16 * kQ8Threads) {
-    float v[16];
-    widen8(load8(src + i), v);
-    widen8(load8(src + i + 8), v + 8);
-    *reinterpret_cast<u32x4_t*>(dst + i) =
-        u32x4_t{pack4_int8(v, s), pack4_int8(v + 4, s), pack4_int8(v + 8, s), pack4_int8(v + 12, s)};
+  if constexpr (W > 1) {
+    if ((tid & 63) == 0) s_max[tid >> 6] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < W; ++w) amax = umax(amax, s_max[w]);
   }
+  const float s = int8_scale(amax);
+  auto encode = [&](const Raw8<T>& r, int i) {
+    float v[8];
+    widen8(r, v);
+    *reinterpret_cast<u32x2_t*>(dst + i) = u32x2_t{pack4_int8(v, s), pack4_int8(v + 4, s)};
+  };
+#pragma unroll
+  for (int h = 0; h < kQ8Hold; ++h)
+    if (8 * (tid + NT * h) < k) encode(held[h], 8 * (tid + NT * h));
+  for (int i = 8 * (tid + NT * kQ8Hold); i < k; i += 8 * NT) encode(load8(src + i), i);
   if (tid == 0) s_out[row] = s;
 }
 
+template <class T>
+static const void* quant_int8_fn(int nt) {
+  void (*fn)(const T*, int, uint8_t*, float*) = nt == 64    ? quant_int8_kernel<T, 64>
+                                                : nt == 256 ? quant_int8_kernel<T, 256>
+                                                            : quant_int8_kernel<T, 1024>;
+  return reinterpret_cast<const void*>(fn);
+}
+
 int launch_quant_int8(const void* x, int dtype, int64_t rows, int64_t k, int8_t* q, float* s, hipStream_t stream) {
-  if (rows * kQ8Threads > 0xffffffffLL || k > 0x7fffffffLL)
+  // threads for one or two pieces each
+  const int nt = k <= 1024 ? 64 : k <= 4096 ? 256 : 1024;
+  if (rows * nt > 0xffffffffLL || k > 0x7fffffffLL)
     return set_error(kUnsupported, "quantize_int8_per_token: shape too large for the launch grid");
+  const void* fn = dtype == kF32 ? quant_int8_fn<float>(nt) : dtype == kBf16 ? quant_int8_fn<Bf16>(nt)
+                                                                            : quant_int8_fn<_Float16>(nt);
+  int ki = (int)k;
   uint8_t* codes = reinterpret_cast<uint8_t*>(q);
-  const dim3 grid((unsigned)rows), block(kQ8Threads);
-  switch (dtype) {
-    case kF32:
-      hipLaunchKernelGGL(quant_int8_kernel<float>, grid, block, 0, stream, static_cast<const float*>(x), (int)k, codes, s);
-      break;
-    case kBf16:
-      hipLaunchKernelGGL(quant_int8_kernel<Bf16>, grid, block, 0, stream, static_cast<const Bf16*>(x), (int)k, codes, s);
-      break;
-    default:
-      hipLaunchKernelGGL(quant_int8_kernel<_Float16>, grid, block, 0, stream, static_cast<const _Float16*>(x), (int)k,
-                         codes, s);
-  }
-  const hipError_t e = hipGetLastError();
+  void* args[] = {&x, &ki, &codes, &s};
+  const hipError_t e = hipLaunchKernel(fn, dim3((unsigned)rows), dim3(nt), args, 0, stream);
   return e == hipSuccess ? kOk : set_error(kHip, "quantize_int8_per_token launch: %s", hipGetErrorString(e));
 }
 
