@@ -21,6 +21,15 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 
 constexpr int kI8Block = 128;   // K bytes of one LDS stage
 
+// Every lane copies 16 (4) bytes from rsrc + voff + soff into lds + lane * 16 (4); out-of-range offsets
+// read zeros.
+__device__ __forceinline__ void lds_dma16(__amdgpu_buffer_rsrc_t rsrc, void* lds, uint32_t voff, int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)lds, 16, voff, soff, 0, 0);
+}
+__device__ __forceinline__ void lds_dma4(__amdgpu_buffer_rsrc_t rsrc, void* lds, uint32_t voff, int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)lds, 4, voff, soff, 0, 0);
+}
+
 __device__ __forceinline__ int swz8(int r) { return (r & 7) ^ ((r >> 3) & 1); }
 
 struct I8Params {
@@ -31,21 +40,31 @@ struct I8Params {
   void* d;
   const int32_t* m_indices;
   const int32_t* masked_m;
-  int m, n, k;
+  int* ws;               // K-split partials
+  unsigned* counters;    // arrival counters, one per split tile
+  int m, n, k;           // rows per group, columns, K
   int groups;
+  int kb_total;          // ceil(k / 128)
   int tiles_m, tiles_n;
+  int splits;            // K splits of the split tiles (1: none)
+  int kb_per_split;
+  int tail_start;        // tiles [0, tail_start) are whole work items; each later tile is `splits` items
   int out_dtype;
 };
 
+// A workgroup tile of BN weight rows x BM activation rows in 8 waves of WN x WM.
 template <int BN_, int BM_, int WN_, int WM_>
 struct I8Cfg {
   static constexpr int BN = BN_, BM = BM_, WN = WN_, WM = WM_;
-  static constexpr int kWaves = (BN / WN) * (BM / WM);
+  static constexpr int kWavesN = BN / WN;
+  static constexpr int kWaves = kWavesN * (BM / WM);
   static constexpr int kThreads = 64 * kWaves;
   static constexpr int kFragN = WN / 16, kFragM = WM / 16;
-  static constexpr int kDma = (BN + BM) / 8;            // DMA instructions of a stage (8 rows each)
-  static constexpr int kDmaPerWave = kDma / kWaves;
-  static_assert(kDma % kWaves == 0 && (BN / 8) % kWaves == 0, "DMA instructions must split evenly over waves");
+  static constexpr int kStage = (BN + BM) * kI8Block;       // one LDS slot
+  static constexpr int kBandsB = BN / 8 / kWaves;           // DMA instructions (8 rows each) per wave: weights,
+  static constexpr int kDmaPerWave = (BN + BM) / 8 / kWaves;   // and in all
+  static constexpr int kScaleBytes = (BN + BM) * 4;
+  static_assert(kWaves == 8 && BN % 64 == 0 && BM % 64 == 0 && kFragN >= 3, "eight waves, at least three fragment rows");
 };
 
 // Four fp32 results of consecutive columns, rounded to the output's type.
@@ -73,102 +92,328 @@ __device__ __forceinline__ void store_out4(void* d, int dtype, int64_t at, const
   }
 }
 
+// ---------------------------------------------------------------------------
+// Tiles: a persistent grid over (group, m-block, n-block, K split), one workgroup per CU, two LDS slots.
+//
+// K block tk is multiplied from slot tk & 1.  A wave reads its weight fragments two fragment rows ahead
+// of their MFMAs and its activation fragments one block ahead, each as soon as the last row's MFMA has
+// consumed its predecessor, so every LDS read has two rows of MFMAs to return, across block boundaries
+// too.  Two rows before a block's end every wave has read all it reads of the block's slot and waits for
+// its own DMAs of the next block; one barrier makes both hold for all.  Then block tk + 2's DMAs go into
+// the freed slot, spread over the MFMAs of the last two rows, and have one block's compute to land.
+// The block body has no branch: past the last block the DMAs take out-of-range offsets and write zeros
+// that nothing reads.
+// ---------------------------------------------------------------------------
+template <int V>
+using IC = std::integral_constant<int, V>;
+
 template <class C, int LAYOUT>
 __global__ __launch_bounds__(C::kThreads) void gemm_int8_kernel(I8Params p) {
-  constexpr int kStage = (C::BN + C::BM) * kI8Block;
-  __shared__ __attribute__((aligned(1024))) uint8_t st[2][kStage];
+  constexpr int NT = C::kThreads, kFN = C::kFragN, kFM = C::kFragM;
+  constexpr int kBarRow = kFN - 2;
+  __shared__ __attribute__((aligned(1024))) uint8_t st0[C::kStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t st1[C::kStage];
+  __shared__ __attribute__((aligned(16))) float s_scale[C::BN + C::BM];   // the tile's column, then row scales
+  __shared__ int s_prefix[LAYOUT == kMasked ? 1025 : 1];
+  __shared__ int s_scan[LAYOUT == kMasked ? 256 : 1];
+  __shared__ int s_flag;
+
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g4 = lane >> 4;
-  const int wn0 = (wave % (C::BN / C::WN)) * C::WN;
-  const int wm0 = (wave / (C::BN / C::WN)) * C::WM;
+  const int wn0 = (wave % C::kWavesN) * C::WN;
+  const int wm0 = (wave / C::kWavesN) * C::WM;
 
-  int rest = blockIdx.x;
-  const int per_group = p.tiles_m * p.tiles_n;
-  const int g = rest / per_group;
-  rest -= g * per_group;
-  const int m0 = (rest % p.tiles_m) * C::BM;
-  const int n0 = (rest / p.tiles_m) * C::BN;
-  int expert = g, m_valid = p.m;
+  int total_items;
   if constexpr (LAYOUT == kMasked) {
-    const int mv = p.masked_m[g];
-    m_valid = mv < 0 ? 0 : mv > p.m ? p.m : mv;
-    if (m0 >= m_valid) return;
+    masked_item_prefix(p.masked_m, p.groups, p.m, C::BM, p.tiles_n, s_prefix, s_scan);
+    total_items = s_prefix[p.groups];
+  } else {
+    const int tiles = p.tiles_m * p.tiles_n;
+    total_items = p.tail_start + (tiles - p.tail_start) * p.splits;
   }
-  if constexpr (LAYOUT == kContiguous) {
-    expert = p.m_indices[m0];
-    if (expert < 0 || expert >= p.groups) return;
-  }
-  const int8_t* a = p.a + (LAYOUT == kMasked ? (int64_t)g * p.m * p.k : 0) + (int64_t)m0 * p.k;
-  const int8_t* b = p.b + ((int64_t)expert * p.n + n0) * p.k;
-  // rows past the edge read zeros (the hardware range check)
-  const __amdgpu_buffer_rsrc_t rs_a = make_rsrc(a, (int64_t)(m_valid - m0) * p.k);
-  const __amdgpu_buffer_rsrc_t rs_b = make_rsrc(b, (int64_t)(p.n - n0) * p.k);
+  // workgroup b runs on XCD b % 8: each XCD takes a contiguous range of items in every round
+  const int grid = gridDim.x;
+  int wg = blockIdx.x;
+  if ((grid & 7) == 0) wg = (blockIdx.x & 7) * (grid >> 3) + (blockIdx.x >> 3);
 
-  const int dma_row = 8 * wave + (lane >> 3);
-  const int dma_chunk = ((lane & 7) ^ swz8(dma_row)) << 4;
-  auto issue = [&](int kb, int slot) {
-    const bool out = kb * kI8Block + dma_chunk >= p.k;   // chunks past K take an out-of-range offset: zeros
-#pragma unroll
-    for (int u = 0; u < C::kDmaPerWave; ++u) {
-      constexpr int kB = C::BN / 8 / C::kWaves;
-      const bool is_b = u < kB;
-      const int row = dma_row + 8 * C::kWaves * (is_b ? u : u - kB);
-      const uint32_t off = out ? 0xFFFFFFF0u : (uint32_t)row * (uint32_t)p.k + (uint32_t)dma_chunk;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(is_b ? rs_b : rs_a,
-                                               (lds_void*)(st[slot] + (wave + C::kWaves * u) * 8 * kI8Block), 16, off,
-                                               kb * kI8Block, 0, 0);
+  // contiguous layout: a tile whose 128-row blocks name two experts runs once for each
+  constexpr bool kTwoPass = LAYOUT == kContiguous && C::BM > kGroup;
+  int step = grid, next_pass = 0;
+  for (int item = wg, pass = 0; item < total_items; item += step, pass = next_pass) {
+    step = grid;
+    next_pass = 0;
+    const bool split_item = LAYOUT != kMasked && item >= p.tail_start && p.splits > 1;
+    const int sidx = split_item ? (item - p.tail_start) / p.splits : 0;
+    const int split = split_item ? (item - p.tail_start) - sidx * p.splits : 0;
+    int rest = split_item ? p.tail_start + sidx : item;
+    int g = 0, mb, nbt, m_lo = 0, m_valid = p.m;
+    if constexpr (LAYOUT == kMasked) {
+      g = masked_group_of(s_prefix, p.groups, rest);
+      rest -= s_prefix[g];
+      const int mblocks = (s_prefix[g + 1] - s_prefix[g]) / p.tiles_n;
+      mb = rest % mblocks;
+      nbt = rest / mblocks;
+      const int mv = p.masked_m[g];
+      m_valid = mv < 0 ? 0 : mv > p.m ? p.m : mv;
+    } else {
+      // runs of 8 m-tiles x all n-tiles, m fastest: the items of one XCD's round share their panels in its L2
+      constexpr int kRun = 8;
+      const int run = rest / (kRun * p.tiles_n);
+      const int first_m = run * kRun;
+      const int run_m = p.tiles_m - first_m < kRun ? p.tiles_m - first_m : kRun;
+      const int in_run = rest - run * (kRun * p.tiles_n);
+      mb = first_m + in_run % run_m;
+      nbt = in_run / run_m;
     }
-  };
-
-  v4i acc[C::kFragN][C::kFragM];
-#pragma unroll
-  for (int i = 0; i < C::kFragN; ++i)
-#pragma unroll
-    for (int j = 0; j < C::kFragM; ++j) acc[i][j] = v4i{0, 0, 0, 0};
-
-  const int kbc = (p.k + kI8Block - 1) / kI8Block;
-  issue(0, 0);
-  for (int kb = 0; kb < kbc; ++kb) {
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();   // block kb landed for every wave; every wave is done with the other slot
-    if (kb + 1 < kbc) issue(kb + 1, (kb + 1) & 1);
-    const uint8_t* sb = st[kb & 1];
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      v4i fb[C::kFragM];
-#pragma unroll
-      for (int j = 0; j < C::kFragM; ++j) {
-        const int r = wm0 + 16 * j + l16;
-        fb[j] = *reinterpret_cast<const v4i*>(sb + (C::BN + r) * kI8Block + (((4 * s + g4) ^ swz8(r)) << 4));
+    const int m0 = mb * C::BM, n0 = nbt * C::BN;
+    int expert = g;
+    if constexpr (LAYOUT == kContiguous) {
+      expert = p.m_indices[m0];
+      if constexpr (kTwoPass) {
+        static_assert(C::BM == 2 * kGroup, "a contiguous tile spans one or two 128-row expert blocks");
+        const int e1 = m0 + kGroup < p.m ? p.m_indices[m0 + kGroup] : expert;
+        if (e1 != expert) {   // uniform
+          if (pass == 0) {
+            step = 0;   // the same item again, as pass 1
+            next_pass = 1;
+            m_valid = m0 + kGroup;
+          } else {
+            expert = e1;
+            m_lo = m0 + kGroup;
+          }
+        }
       }
+      if (expert < 0 || expert >= p.groups) continue;   // uniform: an unmapped block
+    }
+    const int kb_begin = split * p.kb_per_split;
+    int kb_end = split_item ? kb_begin + p.kb_per_split : p.kb_total;
+    if (kb_end > p.kb_total) kb_end = p.kb_total;
+    const int nk = kb_end - kb_begin;
+
+    const int64_t row_base = LAYOUT == kMasked ? (int64_t)g * p.m : 0;
+    // rows past the edge read zeros (the hardware range check)
+    const __amdgpu_buffer_rsrc_t rs_a = make_rsrc(p.a + (row_base + m0) * p.k, (int64_t)(m_valid - m0) * p.k);
+    const __amdgpu_buffer_rsrc_t rs_b =
+        make_rsrc(p.b + ((int64_t)expert * p.n + n0) * p.k, (int64_t)(p.n - n0) * p.k);
+    const __amdgpu_buffer_rsrc_t rs_sa = make_rsrc(p.sa + row_base + m0, (int64_t)(m_valid - m0) * 4);
+    const __amdgpu_buffer_rsrc_t rs_sb = make_rsrc(p.sb + (int64_t)expert * p.n + n0, (int64_t)(p.n - n0) * 4);
+
+    // DMA instruction d of a wave fills 8 tile rows, weights first; lane i writes row i / 8, slot i % 8,
+    // so it loads the logical chunk (i % 8) ^ f(row) (f has period 16 rows: the same for every d)
+    const int dma_row = 8 * wave + (lane >> 3);
+    const int dma_chunk = ((lane & 7) ^ swz8(dma_row)) << 4;
+    const uint32_t dma_off = (uint32_t)dma_row * (uint32_t)p.k + (uint32_t)dma_chunk;
+    const uint32_t band_step = (uint32_t)(8 * C::kWaves) * (uint32_t)p.k;
+    uint8_t* const slot0 = st1;   // blocks 0, 2, ...: the buffer that the epilogue's strips do not use
+    uint8_t* const slot1 = st0;
+    struct DmaCtx { uint8_t* sbase; int koff; uint32_t off, out; };
+    auto dma_ctx = [&](int tk, auto slot_c, bool valid) {
+      DmaCtx c;
+      c.sbase = decltype(slot_c)::value == 0 ? slot0 : slot1;
+      c.koff = (kb_begin + tk) * kI8Block;
+      c.off = dma_off;
+      asm volatile("" : "+v"(c.off));   // the bands' offsets are one add each, not registers of their own
+      // bitwise, no branch: chunks past K and blocks past the last take an out-of-range offset
+      c.out = 0u - ((uint32_t)(!valid) | (uint32_t)(c.koff + dma_chunk >= p.k));
+      return c;
+    };
+    auto dma_one = [&](const DmaCtx& c, int d) {
+      const bool is_b = d < C::kBandsB;
+      const uint32_t off = c.off + (uint32_t)(is_b ? d : d - C::kBandsB) * band_step;
+      lds_dma16(is_b ? rs_b : rs_a, c.sbase + (wave + C::kWaves * d) * 8 * kI8Block, off | (c.out & 0xFFFFFFF0u), c.koff);
+    };
+    auto issue = [&](int tk, auto slot_c, bool valid) {
+      const DmaCtx c = dma_ctx(tk, slot_c, valid);
 #pragma unroll
-      for (int i = 0; i < C::kFragN; ++i) {
-        const int r = wn0 + 16 * i + l16;
-        const v4i fa = *reinterpret_cast<const v4i*>(sb + r * kI8Block + (((4 * s + g4) ^ swz8(r)) << 4));
+      for (int d = 0; d < C::kDmaPerWave; ++d) dma_one(c, d);
+    };
+
+    v4i acc[kFN][kFM];
 #pragma unroll
-        for (int j = 0; j < C::kFragM; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fa, fb[j], acc[i][j], 0, 0, 0);
+    for (int i = 0; i < kFN; ++i)
+#pragma unroll
+      for (int j = 0; j < kFM; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+
+    // a fragment: 16 rows x 128 K bytes, as two steps of 64 (logical chunks g4 and 4 + g4 of a lane's row;
+    // the second's slot differs in bit 2 only: address ^ 64)
+    struct Frag { v4i s[2]; };
+    const int lane_off = l16 * kI8Block + ((g4 ^ swz8(l16)) << 4);
+    auto read_frag = [&](const uint8_t* sbase, int row) {
+      const int off = row * kI8Block + lane_off;
+      Frag f;
+      f.s[0] = *reinterpret_cast<const v4i*>(sbase + off);
+      f.s[1] = *reinterpret_cast<const v4i*>(sbase + (off ^ 64));
+      return f;
+    };
+    // fragment rows [R0, R1) of the block in slot cur.  Row i's weights come from fa[i % 3]; at its start
+    // row i + 2's are requested (rows kFN and kFN + 1 are the next block's rows 0 and 1, from slot nxt).
+    // In the last row each activation fragment half is replaced by the next block's once used.
+    auto rows = [&](auto r0_c, auto r1_c, const uint8_t* cur, const uint8_t* nxt, Frag* fa, Frag* fb, const DmaCtx* dc) {
+      constexpr int R0 = decltype(r0_c)::value, R1 = decltype(r1_c)::value;
+      constexpr int T = (R1 - R0) * kFM * 2;   // MFMAs; with dc, the stage's DMAs are spread over them
+#pragma unroll
+      for (int i = R0; i < R1; ++i) {
+        __builtin_amdgcn_sched_barrier(0);
+        fa[(i + 2) % 3] = i + 2 < kFN ? read_frag(cur, wn0 + 16 * (i + 2)) : read_frag(nxt, wn0 + 16 * (i + 2 - kFN));
+#pragma unroll
+        for (int q = 0; q < 2 * kFM; ++q) {
+          const int s = q / kFM, j = q % kFM;
+          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fa[i % 3].s[s], fb[j].s[s], acc[i][j], 0, 0, 0);
+          if (i == kFN - 1) {
+            const int off = (C::BN + wm0 + 16 * j) * kI8Block + lane_off;
+            fb[j].s[s] = *reinterpret_cast<const v4i*>(nxt + (s == 0 ? off : off ^ 64));
+          }
+          if (dc != nullptr) {
+            const int t = (i - R0) * 2 * kFM + q;
+            const int d0 = t * C::kDmaPerWave / T, d1 = (t + 1) * C::kDmaPerWave / T;
+            for (int d = d0; d < d1; ++d) dma_one(*dc, d);
+          }
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (R1 == kBarRow) {   // no MFMA of these rows moves below the barrier
+#pragma unroll
+        for (int i = R0; i < R1; ++i)
+#pragma unroll
+          for (int j = 0; j < kFM; ++j) asm volatile("" : "+v"(acc[i][j]));
+      }
+    };
+    // the barrier of block tk (slot CUR) and its last two rows; on return fa[0], fa[1] and fb hold the
+    // next block's first fragments
+    auto bar_tail = [&](int tk, auto cur_c, auto nxt_c, Frag* fa, Frag* fb) {
+      const uint8_t* cur = decltype(cur_c)::value == 0 ? slot0 : slot1;
+      const uint8_t* nxt = decltype(nxt_c)::value == 0 ? slot0 : slot1;
+      __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0), lgkmcnt(0): reads of CUR done, DMAs of tk + 1 landed
+      __syncthreads();
+      const DmaCtx dc = dma_ctx(tk + 2, cur_c, tk + 2 < nk);
+      rows(IC<kBarRow>{}, IC<kFN>{}, cur, nxt, fa, fb, &dc);
+      const Frag f0 = fa[kFN % 3], f1 = fa[(kFN + 1) % 3];
+      fa[0] = f0;
+      fa[1] = f1;
+    };
+
+    // Block 0's DMAs go out before the first wait: every wave is past its last read of slot 0, and their
+    // latency overlaps the draining of the previous tile's stores.
+    issue(0, IC<0>{}, true);
+    __builtin_amdgcn_s_waitcnt(0x0070);
+    __syncthreads();   // block 0 landed for every wave; every wave is done with the strips and scales
+    issue(1, IC<1>{}, nk > 1);
+    {   // the tile's scales: 64 a wave (lanes past the edge read zeros)
+      const bool col = wave < C::BN / 64;
+      const int at = col ? 64 * wave : 64 * wave - C::BN;
+      if (64 * wave < C::BN + C::BM)   // wave-uniform
+        lds_dma4(col ? rs_sb : rs_sa, s_scale + 64 * wave, (uint32_t)(at + lane) * 4u, 0);
+    }
+    {
+      Frag fa[3], fb[kFM];
+#pragma unroll
+      for (int j = 0; j < kFM; ++j) fb[j] = read_frag(slot0, C::BN + wm0 + 16 * j);
+      fa[0] = read_frag(slot0, wn0);
+      fa[1] = read_frag(slot0, wn0 + 16);
+      rows(IC<0>{}, IC<kBarRow>{}, slot0, slot1, fa, fb, nullptr);
+      int tk = 0;
+      for (; tk + 2 < nk; tk += 2) {
+        bar_tail(tk, IC<0>{}, IC<1>{}, fa, fb);
+        rows(IC<0>{}, IC<kBarRow>{}, slot1, slot0, fa, fb, nullptr);
+        bar_tail(tk + 1, IC<1>{}, IC<0>{}, fa, fb);
+        rows(IC<0>{}, IC<kBarRow>{}, slot0, slot1, fa, fb, nullptr);
+      }
+      bar_tail(tk, IC<0>{}, IC<1>{}, fa, fb);
+      if (tk + 1 < nk) {
+        rows(IC<0>{}, IC<kBarRow>{}, slot1, slot0, fa, fb, nullptr);
+        bar_tail(tk + 1, IC<1>{}, IC<0>{}, fa, fb);
+      }
+      __builtin_amdgcn_s_waitcnt(0x0070);   // the zero-filling DMAs past the last block
+    }
+
+    // ---- K split: the workgroup that arrives last adds the other partials -------------------------
+    if (split_item) {
+      constexpr int kFrags = kFN * kFM;
+      constexpr int kSplitBytes = kFrags * NT * 16;   // [fragment][thread] pieces of 16 bytes
+      const __amdgpu_buffer_rsrc_t rs_ws =
+          make_rsrc(p.ws + (int64_t)sidx * p.splits * (kSplitBytes / 4), (int64_t)p.splits * kSplitBytes);
+#pragma unroll
+      for (int f = 0; f < kFrags; ++f)
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[f / kFM][f % kFM]), rs_ws,
+                                               split * kSplitBytes + tid * 16 + f * NT * 16, 0, kCpolSc1);
+      __builtin_amdgcn_s_waitcnt(0);   // this thread's partials have arrived
+      __syncthreads();
+      if (tid == 0) {
+        const unsigned prev = __hip_atomic_fetch_add(p.counters + sidx, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        s_flag = prev == (unsigned)(p.splits - 1);
+        if (s_flag) __hip_atomic_store(p.counters + sidx, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+      __syncthreads();
+      if (!s_flag) continue;
+      for (int o = 0; o < p.splits; ++o) {   // integers: any order
+        if (o == split) continue;
+        constexpr int kBatch = 16;   // loads in flight together
+#pragma unroll
+        for (int f0 = 0; f0 < kFrags; f0 += kBatch) {
+          v4i v[kBatch];
+#pragma unroll
+          for (int f = 0; f < kBatch; ++f)
+            v[f] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(
+                                               rs_ws, o * kSplitBytes + tid * 16 + (f0 + f) * NT * 16, 0, kCpolSc1));
+#pragma unroll
+          for (int f = 0; f < kBatch; ++f) acc[(f0 + f) / kFM][(f0 + f) % kFM] += v[f];
+        }
       }
     }
-  }
 
-  const float* sa = p.sa + (LAYOUT == kMasked ? (int64_t)g * p.m : 0);
-  const float* sbp = p.sb + (int64_t)expert * p.n;
-  const int64_t row_base = LAYOUT == kMasked ? (int64_t)g * p.m : 0;
+    // ---- epilogue: scale, round, store --------------------------------------------------------------
+    __syncthreads();   // every wave is done with the slots; the scales have landed
+    auto scaled = [&](int i, int j, float* v) {
+      const float sr = s_scale[C::BN + wm0 + 16 * j + l16];
+      const v4f sc = *reinterpret_cast<const v4f*>(&s_scale[wn0 + 16 * i + 4 * g4]);
 #pragma unroll
-  for (int j = 0; j < C::kFragM; ++j) {
-    const int row = m0 + wm0 + 16 * j + l16;
-    if (row >= m_valid) continue;
-    const float sr = sa[row];
+      for (int r = 0; r < 4; ++r) v[r] = (float)acc[i][j][r] * (sr * sc[r]);
+    };
+    if ((p.n & 7) == 0 && p.out_dtype != kF32) {
+      // through LDS: each wave turns 16 output rows of its tile into whole 16-byte row pieces (a
+      // fragment's own stores would touch 16 rows of 32 bytes each)
+      constexpr int kPitch = C::WN * 2 + 16;
+      constexpr int kPiecesRow = C::WN / 8, kPiecesLane = 16 * kPiecesRow / 64;
+      static_assert(C::kWaves * 16 * kPitch <= C::kStage, "the strips fit in one slot");
+      uint8_t* strip = st0 + wave * (16 * kPitch);
 #pragma unroll
-    for (int i = 0; i < C::kFragN; ++i) {
-      const int col = n0 + wn0 + 16 * i + 4 * g4;
-      const int count = p.n - col;
-      if (count <= 0) continue;
-      float v[4];
+      for (int j = 0; j < kFM; ++j) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] = (float)acc[i][j][r] * (sr * (r < count ? sbp[col + r] : 0.f));
-      store_out4(p.d, p.out_dtype, (row_base + row) * p.n + col, v, count < 4 ? count : 4, (p.n & 3) == 0);
+        for (int i = 0; i < kFN; ++i) {
+          float v[4];
+          scaled(i, j, v);
+          u32x2_t h;
+          if (p.out_dtype == kBf16) h = u32x2_t{pack2_bf16_rne(v[0], v[1]), pack2_bf16_rne(v[2], v[3])};
+          else h = u32x2_t{pack2_f16(v[0], v[1]), pack2_f16(v[2], v[3])};
+          *reinterpret_cast<u32x2_t*>(strip + l16 * kPitch + (16 * i + 4 * g4) * 2) = h;
+        }
+        // the wave reads back what its own lanes wrote (its LDS operations complete in order)
+#pragma unroll
+        for (int u = 0; u < kPiecesLane; ++u) {
+          const int c = lane + 64 * u;
+          const int row = c / kPiecesRow, cc = c % kPiecesRow;
+          const u32x4 val = *reinterpret_cast<const u32x4*>(strip + row * kPitch + cc * 16);
+          const int mrow = m0 + wm0 + 16 * j + row, ncol = n0 + wn0 + 8 * cc;
+          if ((!kTwoPass || mrow >= m_lo) && mrow < m_valid && ncol < p.n)
+            *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.d) + (row_base + mrow) * p.n + ncol) = val;
+        }
+      }
+      continue;
+    }
+#pragma unroll
+    for (int j = 0; j < kFM; ++j) {
+      const int mrow = m0 + wm0 + 16 * j + l16;
+      if ((kTwoPass && mrow < m_lo) || mrow >= m_valid) continue;
+#pragma unroll
+      for (int i = 0; i < kFN; ++i) {
+        const int col = n0 + wn0 + 16 * i + 4 * g4;
+        const int count = p.n - col;
+        if (count <= 0) continue;
+        float v[4];
+        scaled(i, j, v);
+        store_out4(p.d, p.out_dtype, (row_base + mrow) * p.n + col, v, count < 4 ? count : 4, (p.n & 3) == 0);
+      }
     }
   }
 }
@@ -518,7 +763,8 @@ __global__ __launch_bounds__(64 * kStNS * kStKS) void gemm_int8_staged_kernel(I8
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
-using I8Tile = I8Cfg<128, 128, 64, 64>;
+using I8Square = I8Cfg<256, 256, 128, 64>;
+using I8Rows128 = I8Cfg<256, 128, 64, 64>;
 
 struct FewPlan {
   bool direct;
@@ -611,6 +857,52 @@ static int launch_few(const FewPlan& f, const void* fn, I8FewParams p, size_t ld
   return e == hipSuccess ? kOk : set_error(kHip, "int8 gemm launch: %s", hipGetErrorString(e));
 }
 
+struct TilePlan {
+  bool square;
+  int tiles_m, tiles_n, splits, kb_per_split, tail_start;
+  int64_t items;
+  size_t ws_bytes;
+};
+
+// Rounds of a persistent grid of num_cus workgroups; a partial last round costs a fixed part as well.
+static double tile_rounds(int64_t tiles, int num_cus) {
+  const int64_t rest = tiles % num_cus;
+  return (double)(tiles / num_cus) + (rest ? 0.3 + 0.7 * (double)rest / num_cus : 0.0);
+}
+
+static TilePlan tile_plan(int layout, int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus, size_t ws_bytes) {
+  TilePlan t{};
+  const int64_t per = layout == kMasked ? groups : 1;
+  auto tiles = [&](int bn, int bm) { return ((m + bm - 1) / bm) * ((n + bn - 1) / bn) * per; };
+  int64_t square = tiles(I8Square::BN, I8Square::BM);
+  if (layout == kContiguous) {   // a tile that spans two experts runs twice
+    const int64_t mt = (m + I8Square::BM - 1) / I8Square::BM;
+    const int64_t edges = groups - 1 < mt ? groups - 1 : mt;
+    square += edges * ((n + I8Square::BN - 1) / I8Square::BN);
+  }
+  t.square = 1.85 * tile_rounds(square, num_cus) < tile_rounds(tiles(I8Rows128::BN, I8Rows128::BM), num_cus);
+  const int bm = t.square ? I8Square::BM : I8Rows128::BM, bn = 256;
+  t.tiles_m = (int)((m + bm - 1) / bm);
+  t.tiles_n = (int)((n + bn - 1) / bn);
+  t.splits = 1;
+  t.kb_per_split = (int)((k + kI8Block - 1) / kI8Block);
+  t.items = (int64_t)t.tiles_m * t.tiles_n * per;
+  t.tail_start = (int)(t.items < 0x7fffffffLL ? t.items : 0x7fffffff);
+  (void)ws_bytes;
+  return t;
+}
+
+static const void* tile_fn(int layout, bool square) {
+  void (*fn)(I8Params);
+  if (square)
+    fn = layout == kMasked ? gemm_int8_kernel<I8Square, kMasked>
+         : layout == kContiguous ? gemm_int8_kernel<I8Square, kContiguous> : gemm_int8_kernel<I8Square, kDense>;
+  else
+    fn = layout == kMasked ? gemm_int8_kernel<I8Rows128, kMasked>
+         : layout == kContiguous ? gemm_int8_kernel<I8Rows128, kContiguous> : gemm_int8_kernel<I8Rows128, kDense>;
+  return reinterpret_cast<const void*>(fn);
+}
+
 int launch_quant_int8(const void* x, int dtype, int64_t rows, int64_t k, int8_t* q, float* s, hipStream_t stream);
 
 size_t int8_workspace_size(int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus) {
@@ -628,21 +920,24 @@ int launch_gemm_int8(int layout, const int8_t* a, const float* sa, const int8_t*
     p.m = (int)m; p.n = (int)n; p.k = (int)k; p.out_dtype = out_dtype;
     return launch_few(f, staged_fn(f), p, 0, groups, ws, static_cast<uint8_t*>(ws) + kCounterBytes, stream);
   }
+  const TilePlan t = tile_plan(layout, m, n, k, groups, num_cus, ws != nullptr ? ws_bytes : 0);
   I8Params p{};
   p.a = a; p.sa = sa; p.b = b; p.sb = sb; p.d = d;
   p.m_indices = m_indices; p.masked_m = masked_m;
   p.m = (int)m; p.n = (int)n; p.k = (int)k;
   p.groups = (int)groups;
-  p.tiles_m = (int)((m + I8Tile::BM - 1) / I8Tile::BM);
-  p.tiles_n = (int)((n + I8Tile::BN - 1) / I8Tile::BN);
+  p.kb_total = (int)((k + kI8Block - 1) / kI8Block);
+  p.tiles_m = t.tiles_m; p.tiles_n = t.tiles_n;
+  p.splits = t.splits; p.kb_per_split = t.kb_per_split; p.tail_start = t.tail_start;
   p.out_dtype = out_dtype;
-  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n * (layout == kMasked ? groups : 1);
-  if (tiles * I8Tile::kThreads > 0xffffffffLL) return set_error(kUnsupported, "int8 gemm: too many output tiles");
-  void (*fn)(I8Params) = layout == kMasked ? gemm_int8_kernel<I8Tile, kMasked>
-                         : layout == kContiguous ? gemm_int8_kernel<I8Tile, kContiguous>
-                                                 : gemm_int8_kernel<I8Tile, kDense>;
+  if (t.splits > 1) {
+    p.counters = static_cast<unsigned*>(ws);
+    p.ws = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + kCounterBytes);
+  }
+  if (t.items > 0x7fffffffLL) return set_error(kUnsupported, "int8 gemm: too many output tiles");
+  const int64_t blocks = t.items < num_cus ? t.items : num_cus;   // one workgroup per CU (the LDS slots)
   void* args[] = {&p};
-  const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(fn), dim3((unsigned)tiles), dim3(I8Tile::kThreads),
+  const hipError_t e = hipLaunchKernel(tile_fn(layout, t.square), dim3((unsigned)(blocks < 1 ? 1 : blocks)), dim3(512),
                                        args, 0, stream);
   return e == hipSuccess ? kOk : set_error(kHip, "int8 gemm launch: %s", hipGetErrorString(e));
 }
