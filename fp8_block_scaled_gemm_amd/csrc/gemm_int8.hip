@@ -46,16 +46,15 @@ struct I8Params {
   int groups;
   int kb_total;          // ceil(k / 128)
   int tiles_m, tiles_n;
-  int splits;            // K splits of the split tiles (1: none)
+  int splits;            // K splits of every tile (1: none)
   int kb_per_split;
-  int tail_start;        // tiles [0, tail_start) are whole work items; each later tile is `splits` items
   int out_dtype;
 };
 
-// A workgroup tile of BN weight rows x BM activation rows in 8 waves of WN x WM.
-template <int BN_, int BM_, int WN_, int WM_>
+// A workgroup tile of BN weight rows x BM activation rows in 8 waves of WN x WM, OCC workgroups per CU.
+template <int BN_, int BM_, int WN_, int WM_, int OCC_>
 struct I8Cfg {
-  static constexpr int BN = BN_, BM = BM_, WN = WN_, WM = WM_;
+  static constexpr int BN = BN_, BM = BM_, WN = WN_, WM = WM_, OCC = OCC_;
   static constexpr int kWavesN = BN / WN;
   static constexpr int kWaves = kWavesN * (BM / WM);
   static constexpr int kThreads = 64 * kWaves;
@@ -108,7 +107,7 @@ template <int V>
 using IC = std::integral_constant<int, V>;
 
 template <class C, int LAYOUT>
-__global__ __launch_bounds__(C::kThreads) void gemm_int8_kernel(I8Params p) {
+__global__ __launch_bounds__(C::kThreads, 2 * C::OCC) void gemm_int8_kernel(I8Params p) {
   constexpr int NT = C::kThreads, kFN = C::kFragN, kFM = C::kFragM;
   constexpr int kBarRow = kFN - 2;
   __shared__ __attribute__((aligned(1024))) uint8_t st0[C::kStage];
@@ -129,8 +128,7 @@ __global__ __launch_bounds__(C::kThreads) void gemm_int8_kernel(I8Params p) {
     masked_item_prefix(p.masked_m, p.groups, p.m, C::BM, p.tiles_n, s_prefix, s_scan);
     total_items = s_prefix[p.groups];
   } else {
-    const int tiles = p.tiles_m * p.tiles_n;
-    total_items = p.tail_start + (tiles - p.tail_start) * p.splits;
+    total_items = p.tiles_m * p.tiles_n * p.splits;
   }
   // workgroup b runs on XCD b % 8: each XCD takes a contiguous range of items in every round
   const int grid = gridDim.x;
@@ -143,10 +141,9 @@ __global__ __launch_bounds__(C::kThreads) void gemm_int8_kernel(I8Params p) {
   for (int item = wg, pass = 0; item < total_items; item += step, pass = next_pass) {
     step = grid;
     next_pass = 0;
-    const bool split_item = LAYOUT != kMasked && item >= p.tail_start && p.splits > 1;
-    const int sidx = split_item ? (item - p.tail_start) / p.splits : 0;
-    const int split = split_item ? (item - p.tail_start) - sidx * p.splits : 0;
-    int rest = split_item ? p.tail_start + sidx : item;
+    const int tile_id = LAYOUT == kDense ? item / p.splits : item;   // only the normal form splits K
+    const int split = LAYOUT == kDense ? item - tile_id * p.splits : 0;
+    int rest = tile_id;
     int g = 0, mb, nbt, m_lo = 0, m_valid = p.m;
     if constexpr (LAYOUT == kMasked) {
       g = masked_group_of(s_prefix, p.groups, rest);
@@ -187,9 +184,7 @@ __global__ __launch_bounds__(C::kThreads) void gemm_int8_kernel(I8Params p) {
       if (expert < 0 || expert >= p.groups) continue;   // uniform: an unmapped block
     }
     const int kb_begin = split * p.kb_per_split;
-    int kb_end = split_item ? kb_begin + p.kb_per_split : p.kb_total;
-    if (kb_end > p.kb_total) kb_end = p.kb_total;
-    const int nk = kb_end - kb_begin;
+    const int nk = p.kb_total - kb_begin < p.kb_per_split ? p.kb_total - kb_begin : p.kb_per_split;
 
     const int64_t row_base = LAYOUT == kMasked ? (int64_t)g * p.m : 0;
     // rows past the edge read zeros (the hardware range check)
@@ -328,11 +323,11 @@ __global__ __launch_bounds__(C::kThreads) void gemm_int8_kernel(I8Params p) {
     }
 
     // ---- K split: the workgroup that arrives last adds the other partials -------------------------
-    if (split_item) {
+    if (LAYOUT == kDense && p.splits > 1) {
       constexpr int kFrags = kFN * kFM;
       constexpr int kSplitBytes = kFrags * NT * 16;   // [fragment][thread] pieces of 16 bytes
       const __amdgpu_buffer_rsrc_t rs_ws =
-          make_rsrc(p.ws + (int64_t)sidx * p.splits * (kSplitBytes / 4), (int64_t)p.splits * kSplitBytes);
+          make_rsrc(p.ws + (int64_t)tile_id * p.splits * (kSplitBytes / 4), (int64_t)p.splits * kSplitBytes);
 #pragma unroll
       for (int f = 0; f < kFrags; ++f)
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[f / kFM][f % kFM]), rs_ws,
@@ -340,15 +335,15 @@ __global__ __launch_bounds__(C::kThreads) void gemm_int8_kernel(I8Params p) {
       __builtin_amdgcn_s_waitcnt(0);   // this thread's partials have arrived
       __syncthreads();
       if (tid == 0) {
-        const unsigned prev = __hip_atomic_fetch_add(p.counters + sidx, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        const unsigned prev = __hip_atomic_fetch_add(p.counters + tile_id, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         s_flag = prev == (unsigned)(p.splits - 1);
-        if (s_flag) __hip_atomic_store(p.counters + sidx, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (s_flag) __hip_atomic_store(p.counters + tile_id, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
       __syncthreads();
       if (!s_flag) continue;
       for (int o = 0; o < p.splits; ++o) {   // integers: any order
         if (o == split) continue;
-        constexpr int kBatch = 16;   // loads in flight together
+        constexpr int kBatch = kFrags < 16 ? kFrags : 16;   // loads in flight together
 #pragma unroll
         for (int f0 = 0; f0 < kFrags; f0 += kBatch) {
           v4i v[kBatch];
@@ -370,13 +365,15 @@ __global__ __launch_bounds__(C::kThreads) void gemm_int8_kernel(I8Params p) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) v[r] = (float)acc[i][j][r] * (sr * sc[r]);
     };
-    if ((p.n & 7) == 0 && p.out_dtype != kF32) {
-      // through LDS: each wave turns 16 output rows of its tile into whole 16-byte row pieces (a
-      // fragment's own stores would touch 16 rows of 32 bytes each)
+    if (p.out_dtype != kF32) {
+      // through LDS: each wave turns 16 output rows of its tile into whole row pieces (a fragment's own
+      // stores would touch 16 rows of 32 bytes each): of 16 bytes where the rows are 16-byte aligned,
+      // else of one element a lane, 64 consecutive ones an instruction
       constexpr int kPitch = C::WN * 2 + 16;
       constexpr int kPiecesRow = C::WN / 8, kPiecesLane = 16 * kPiecesRow / 64;
       static_assert(C::kWaves * 16 * kPitch <= C::kStage, "the strips fit in one slot");
       uint8_t* strip = st0 + wave * (16 * kPitch);
+      const bool aligned = (p.n & 7) == 0;
 #pragma unroll
       for (int j = 0; j < kFM; ++j) {
 #pragma unroll
@@ -389,14 +386,24 @@ __global__ __launch_bounds__(C::kThreads) void gemm_int8_kernel(I8Params p) {
           *reinterpret_cast<u32x2_t*>(strip + l16 * kPitch + (16 * i + 4 * g4) * 2) = h;
         }
         // the wave reads back what its own lanes wrote (its LDS operations complete in order)
+        uint16_t* out = static_cast<uint16_t*>(p.d);
+        if (aligned) {
 #pragma unroll
-        for (int u = 0; u < kPiecesLane; ++u) {
-          const int c = lane + 64 * u;
-          const int row = c / kPiecesRow, cc = c % kPiecesRow;
-          const u32x4 val = *reinterpret_cast<const u32x4*>(strip + row * kPitch + cc * 16);
-          const int mrow = m0 + wm0 + 16 * j + row, ncol = n0 + wn0 + 8 * cc;
-          if ((!kTwoPass || mrow >= m_lo) && mrow < m_valid && ncol < p.n)
-            *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.d) + (row_base + mrow) * p.n + ncol) = val;
+          for (int u = 0; u < kPiecesLane; ++u) {
+            const int c = lane + 64 * u;
+            const int row = c / kPiecesRow, cc = c % kPiecesRow;
+            const u32x4 val = *reinterpret_cast<const u32x4*>(strip + row * kPitch + cc * 16);
+            const int mrow = m0 + wm0 + 16 * j + row, ncol = n0 + wn0 + 8 * cc;
+            if ((!kTwoPass || mrow >= m_lo) && mrow < m_valid && ncol < p.n)
+              *reinterpret_cast<u32x4*>(out + (row_base + mrow) * p.n + ncol) = val;
+          }
+        } else {
+          for (int u = 0; u < 16 * C::WN / 64; ++u) {
+            const int row = 64 * u / C::WN, cc = 64 * u % C::WN + lane;
+            const uint16_t val = *reinterpret_cast<const uint16_t*>(strip + row * kPitch + cc * 2);
+            const int mrow = m0 + wm0 + 16 * j + row, ncol = n0 + wn0 + cc;
+            if ((!kTwoPass || mrow >= m_lo) && mrow < m_valid && ncol < p.n) out[(row_base + mrow) * p.n + ncol] = val;
+          }
         }
       }
       continue;
@@ -763,8 +770,9 @@ __global__ __launch_bounds__(64 * kStNS * kStKS) void gemm_int8_staged_kernel(I8
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
-using I8Square = I8Cfg<256, 256, 128, 64>;
-using I8Rows128 = I8Cfg<256, 128, 64, 64>;
+using I8Square = I8Cfg<256, 256, 128, 64, 1>;
+using I8Small = I8Cfg<128, 128, 64, 32, 2>;
+enum I8Tile : int { kSquare = 0, kSmall, kTiles };
 
 struct FewPlan {
   bool direct;
@@ -841,9 +849,6 @@ static const void* direct_fn(const FewPlan& f, int dtype) {
   return dtype == kF32 ? direct_fn_of<float>(f) : dtype == kBf16 ? direct_fn_of<Bf16>(f) : direct_fn_of<_Float16>(f);
 }
 
-// Rows that run on the few-row kernel.
-constexpr int64_t kFewRows = 128;
-
 static int launch_few(const FewPlan& f, const void* fn, I8FewParams p, size_t lds, int64_t groups, void* counters,
                       void* partials, hipStream_t stream) {
   p.strips = f.strips; p.mtiles = f.mtiles; p.splits = f.splits;
@@ -857,70 +862,129 @@ static int launch_few(const FewPlan& f, const void* fn, I8FewParams p, size_t ld
   return e == hipSuccess ? kOk : set_error(kHip, "int8 gemm launch: %s", hipGetErrorString(e));
 }
 
-struct TilePlan {
-  bool square;
-  int tiles_m, tiles_n, splits, kb_per_split, tail_start;
-  int64_t items;
-  size_t ws_bytes;
-};
+// Time estimates (microseconds, MI355X, 256 CUs), fitted to timings of every choice on shapes of 192 to
+// 4096 rows.  A workgroup's K block takes longer the more of them run (they share caches and power); a
+// tile costs a fixed part as well (first loads, stores); a K split sends its partials out and back.
+struct TileModel { int bn, bm, occ; double fixed, alone, busy; };
+constexpr TileModel kTileModel[kTiles] = {
+    {I8Square::BN, I8Square::BM, I8Square::OCC, 7.0, 0.9, 1.6},
+    {I8Small::BN, I8Small::BM, I8Small::OCC, 3.5, 0.5, 1.15}};
 
-// Rounds of a persistent grid of num_cus workgroups; a partial last round costs a fixed part as well.
-static double tile_rounds(int64_t tiles, int num_cus) {
-  const int64_t rest = tiles % num_cus;
-  return (double)(tiles / num_cus) + (rest ? 0.3 + 0.7 * (double)rest / num_cus : 0.0);
+static double split_time(double partial_bytes) { return 3.0 + 0.22e-6 * partial_bytes; }
+
+// Few-row tiles of 128 rows: 0.8 us a chunk of 256 alone, 0.7 us per workgroup of a CU once there are more.
+static double few_time(const FewPlan& f, int num_cus) {
+  const double c = (double)f.tiles * f.splits / num_cus;
+  const double t = 3.5 + f.steps_per_wave * (c > 8.0 / 7.0 ? 0.7 * c : 0.8) * f.r;
+  return t + (f.splits > 1 ? split_time((double)f.tiles * f.splits * f.bn * f.bm * 4) : 0.0);
 }
 
-static TilePlan tile_plan(int layout, int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus, size_t ws_bytes) {
+struct TilePlan {
+  int tile;
+  int tiles_m, tiles_n, splits, kb_per_split;
+  int64_t items;
+  size_t ws_bytes;
+  double us;
+};
+
+static TilePlan tile_choice(int tile, int splits, int layout, int64_t m, int64_t n, int64_t k, int64_t groups,
+                            int num_cus) {
+  const TileModel& c = kTileModel[tile];
+  const int kb_total = (int)((k + kI8Block - 1) / kI8Block);
   TilePlan t{};
-  const int64_t per = layout == kMasked ? groups : 1;
-  auto tiles = [&](int bn, int bm) { return ((m + bm - 1) / bm) * ((n + bn - 1) / bn) * per; };
-  int64_t square = tiles(I8Square::BN, I8Square::BM);
-  if (layout == kContiguous) {   // a tile that spans two experts runs twice
-    const int64_t mt = (m + I8Square::BM - 1) / I8Square::BM;
-    const int64_t edges = groups - 1 < mt ? groups - 1 : mt;
-    square += edges * ((n + I8Square::BN - 1) / I8Square::BN);
+  t.tile = tile;
+  t.tiles_m = (int)((m + c.bm - 1) / c.bm);
+  t.tiles_n = (int)((n + c.bn - 1) / c.bn);
+  t.kb_per_split = (kb_total + splits - 1) / splits;
+  t.splits = (kb_total + t.kb_per_split - 1) / t.kb_per_split;   // no empty split
+  double tiles = (double)t.tiles_m * t.tiles_n;
+  if (layout == kMasked) tiles = (double)groups * ((m / 2 + c.bm - 1) / c.bm) * t.tiles_n;   // half the rows in use
+  if (layout == kContiguous && c.bm > kGroup) {   // a tile that spans two experts runs twice
+    const int64_t edges = groups - 1 < t.tiles_m ? groups - 1 : t.tiles_m;
+    tiles += (double)edges * t.tiles_n;
   }
-  t.square = 1.85 * tile_rounds(square, num_cus) < tile_rounds(tiles(I8Rows128::BN, I8Rows128::BM), num_cus);
-  const int bm = t.square ? I8Square::BM : I8Rows128::BM, bn = 256;
-  t.tiles_m = (int)((m + bm - 1) / bm);
-  t.tiles_n = (int)((n + bn - 1) / bn);
-  t.splits = 1;
-  t.kb_per_split = (int)((k + kI8Block - 1) / kI8Block);
-  t.items = (int64_t)t.tiles_m * t.tiles_n * per;
-  t.tail_start = (int)(t.items < 0x7fffffffLL ? t.items : 0x7fffffff);
-  (void)ws_bytes;
+  t.items = (int64_t)t.tiles_m * t.tiles_n * t.splits * (layout == kMasked ? groups : 1);
+  const double items = tiles * t.splits, slots = (double)c.occ * num_cus;
+  const double full = (double)(int64_t)(items / slots), rest = items - full * slots;
+  t.us = full * (c.fixed + t.kb_per_split * c.busy);
+  if (rest > 0) t.us += c.fixed + t.kb_per_split * (c.alone + (c.busy - c.alone) * rest / slots);
+  if (t.splits > 1) {
+    const double partials = items * (double)(c.bm * c.bn) * 4;
+    t.us += split_time(partials);
+    t.ws_bytes = kCounterBytes + (size_t)partials;
+  }
   return t;
 }
 
-static const void* tile_fn(int layout, bool square) {
-  void (*fn)(I8Params);
-  if (square)
-    fn = layout == kMasked ? gemm_int8_kernel<I8Square, kMasked>
-         : layout == kContiguous ? gemm_int8_kernel<I8Square, kContiguous> : gemm_int8_kernel<I8Square, kDense>;
-  else
-    fn = layout == kMasked ? gemm_int8_kernel<I8Rows128, kMasked>
-         : layout == kContiguous ? gemm_int8_kernel<I8Rows128, kContiguous> : gemm_int8_kernel<I8Rows128, kDense>;
+// The fastest of the tiles and, for the normal form with a workspace, of the K splits that keep at least 4
+// K blocks and give each CU about one workgroup (with two, 256 x 4096 x 7168 on 128x128 tiles takes
+// 29.6 us, with one 22.6).
+static TilePlan tile_plan(int layout, int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus, bool allow_split) {
+  TilePlan best{};
+  for (int tile = 0; tile < kTiles; ++tile) {
+    for (int splits = 1; splits <= kMaxSplits; ++splits) {
+      const TilePlan t = tile_choice(tile, splits, layout, m, n, k, groups, num_cus);
+      if (splits > 1) {
+        if (layout != kDense || !allow_split || t.kb_per_split < 4 || 8 * t.items > 9 * (int64_t)num_cus ||
+            t.items / t.splits > kMaxCounterTiles)
+          break;
+        if (t.splits != splits) continue;   // the same as a smaller request
+      }
+      if (best.items == 0 || t.us < best.us) best = t;
+    }
+  }
+  return best;
+}
+
+template <int LAYOUT>
+static const void* tile_fn_of(int tile) {
+  void (*fn)(I8Params) = tile == kSquare ? gemm_int8_kernel<I8Square, LAYOUT> : gemm_int8_kernel<I8Small, LAYOUT>;
   return reinterpret_cast<const void*>(fn);
+}
+static const void* tile_fn(int layout, int tile) {
+  return layout == kMasked ? tile_fn_of<kMasked>(tile) : layout == kContiguous ? tile_fn_of<kContiguous>(tile)
+                                                                              : tile_fn_of<kDense>(tile);
+}
+
+// Rows that always run on the few-row kernel, and the most rows that may (more never measured faster).
+constexpr int64_t kFewRows = 128, kFewRowsMost = 1024;
+
+struct I8Plan {
+  bool few;
+  FewPlan f;
+  TilePlan t;
+  size_t ws_bytes() const { return few ? f.ws_bytes : t.ws_bytes; }
+};
+
+static I8Plan int8_plan(int layout, int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus, bool allow_split) {
+  I8Plan p{};
+  if (layout != kContiguous && m <= (layout == kMasked ? kFewRows : kFewRowsMost))
+    p.f = few_plan(false, m, n, k, groups, num_cus, allow_split);
+  p.few = layout != kContiguous && m <= kFewRows;
+  if (p.few) return p;
+  p.t = tile_plan(layout, m, n, k, groups, num_cus, allow_split);
+  p.few = layout == kDense && m <= kFewRowsMost && few_time(p.f, num_cus) < p.t.us;
+  return p;
 }
 
 int launch_quant_int8(const void* x, int dtype, int64_t rows, int64_t k, int8_t* q, float* s, hipStream_t stream);
 
 size_t int8_workspace_size(int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus) {
-  return m <= kFewRows ? few_plan(false, m, n, k, groups, num_cus, true).ws_bytes : 0;
+  return int8_plan(groups > 1 ? kMasked : kDense, m, n, k, groups, num_cus, true).ws_bytes();
 }
 
-int launch_gemm_int8(int layout, const int8_t* a, const float* sa, const int8_t* b, const float* sb, void* d,
-                     int out_dtype, const int32_t* m_indices, const int32_t* masked_m, int64_t groups, int64_t m,
-                     int64_t n, int64_t k, void* ws, size_t ws_bytes, hipStream_t stream, int num_cus) {
-  if (layout != kContiguous && m <= kFewRows) {
-    FewPlan f = few_plan(false, m, n, k, groups, num_cus, ws != nullptr);
-    if (ws_bytes < f.ws_bytes) f = few_plan(false, m, n, k, groups, num_cus, false);
+// `counters` and `partials`: the K split's workspace, or null for none.
+static int launch_planned(int layout, const int8_t* a, const float* sa, const int8_t* b, const float* sb, void* d,
+                          int out_dtype, const int32_t* m_indices, const int32_t* masked_m, int64_t groups, int64_t m,
+                          int64_t n, int64_t k, const I8Plan& plan, void* counters, void* partials, hipStream_t stream,
+                          int num_cus) {
+  if (plan.few) {
     I8FewParams p{};
     p.a = a; p.sa = sa; p.b = b; p.sb = sb; p.d = d; p.masked_m = masked_m;
     p.m = (int)m; p.n = (int)n; p.k = (int)k; p.out_dtype = out_dtype;
-    return launch_few(f, staged_fn(f), p, 0, groups, ws, static_cast<uint8_t*>(ws) + kCounterBytes, stream);
+    return launch_few(plan.f, staged_fn(plan.f), p, 0, groups, counters, partials, stream);
   }
-  const TilePlan t = tile_plan(layout, m, n, k, groups, num_cus, ws != nullptr ? ws_bytes : 0);
+  const TilePlan& t = plan.t;
   I8Params p{};
   p.a = a; p.sa = sa; p.b = b; p.sb = sb; p.d = d;
   p.m_indices = m_indices; p.masked_m = masked_m;
@@ -928,18 +992,25 @@ int launch_gemm_int8(int layout, const int8_t* a, const float* sa, const int8_t*
   p.groups = (int)groups;
   p.kb_total = (int)((k + kI8Block - 1) / kI8Block);
   p.tiles_m = t.tiles_m; p.tiles_n = t.tiles_n;
-  p.splits = t.splits; p.kb_per_split = t.kb_per_split; p.tail_start = t.tail_start;
+  p.splits = t.splits; p.kb_per_split = t.kb_per_split;
   p.out_dtype = out_dtype;
-  if (t.splits > 1) {
-    p.counters = static_cast<unsigned*>(ws);
-    p.ws = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + kCounterBytes);
-  }
+  p.counters = static_cast<unsigned*>(counters);
+  p.ws = static_cast<int*>(partials);
   if (t.items > 0x7fffffffLL) return set_error(kUnsupported, "int8 gemm: too many output tiles");
-  const int64_t blocks = t.items < num_cus ? t.items : num_cus;   // one workgroup per CU (the LDS slots)
+  const int64_t slots = (int64_t)num_cus * kTileModel[t.tile].occ;
   void* args[] = {&p};
-  const hipError_t e = hipLaunchKernel(tile_fn(layout, t.square), dim3((unsigned)(blocks < 1 ? 1 : blocks)), dim3(512),
-                                       args, 0, stream);
+  const hipError_t e = hipLaunchKernel(tile_fn(layout, t.tile), dim3((unsigned)(t.items < slots ? t.items : slots)),
+                                       dim3(I8Square::kThreads), args, 0, stream);
   return e == hipSuccess ? kOk : set_error(kHip, "int8 gemm launch: %s", hipGetErrorString(e));
+}
+
+int launch_gemm_int8(int layout, const int8_t* a, const float* sa, const int8_t* b, const float* sb, void* d,
+                     int out_dtype, const int32_t* m_indices, const int32_t* masked_m, int64_t groups, int64_t m,
+                     int64_t n, int64_t k, void* ws, size_t ws_bytes, hipStream_t stream, int num_cus) {
+  I8Plan plan = int8_plan(layout, m, n, k, groups, num_cus, ws != nullptr);
+  if (ws_bytes < plan.ws_bytes()) plan = int8_plan(layout, m, n, k, groups, num_cus, false);
+  return launch_planned(layout, a, sa, b, sb, d, out_dtype, m_indices, masked_m, groups, m, n, k, plan, ws,
+                        static_cast<uint8_t*>(ws) + kCounterBytes, stream, num_cus);
 }
 
 // In-call quantization.  Up to kFewFusedRows rows whose codes fit in LDS are quantized by the product's
@@ -969,20 +1040,15 @@ int launch_gemm_int8_act_quant(const void* x, int dtype, const int8_t* b, const 
     return launch_few(f, direct_fn(f, dtype), p, (size_t)(m * k), 1, ws, static_cast<uint8_t*>(ws) + kCounterBytes, stream);
   }
   uint8_t* w = static_cast<uint8_t*>(ws);
-  int8_t* q = reinterpret_cast<int8_t*>(w + kCounterBytes);
-  float* s = reinterpret_cast<float*>(w + kCounterBytes + align256((size_t)(m * k)));
+  uint8_t* codes = w + kCounterBytes;
+  uint8_t* scales = codes + align256((size_t)(m * k));
+  uint8_t* partials = scales + align256((size_t)m * 4);
+  int8_t* q = reinterpret_cast<int8_t*>(codes);
+  float* s = reinterpret_cast<float*>(scales);
   const int r = launch_quant_int8(x, dtype, m, k, q, s, stream);
   if (r != kOk) return r;
-  if (m <= kFewRows) {
-    // the split's partials follow the scales; its counters are the workspace's own prefix
-    const FewPlan f = few_plan(false, m, n, k, 1, num_cus, true);
-    I8FewParams p{};
-    p.a = q; p.sa = s; p.b = b; p.sb = sb; p.d = d;
-    p.m = (int)m; p.n = (int)n; p.k = (int)k; p.out_dtype = out_dtype;
-    return launch_few(f, staged_fn(f), p, 0, 1, ws, w + kCounterBytes + align256((size_t)(m * k)) + align256((size_t)m * 4),
-                      stream);
-  }
-  return launch_gemm_int8(kDense, q, s, b, sb, d, out_dtype, nullptr, nullptr, 1, m, n, k, nullptr, 0, stream, num_cus);
+  return launch_planned(kDense, q, s, b, sb, d, out_dtype, nullptr, nullptr, 1, m, n, k,
+                        int8_plan(kDense, m, n, k, 1, num_cus, true), w, partials, stream, num_cus);
 }
 
 }  // namespace dg
