@@ -300,7 +300,20 @@ __global__ __launch_bounds__(C::kThreads, 2 * C::OCC) void gemm_int8_kernel(I8Pa
       if (64 * wave < C::BN + C::BM)   // wave-uniform
         lds_dma4(col ? rs_sb : rs_sa, s_scale + 64 * wave, (uint32_t)(at + lane) * 4u, 0);
     }
-    {
+    // A wave whose rows or columns all lie outside the tile's part of the problem (edges, a masked
+    // group's count, one half of a two-expert tile) only moves data: its SIMD partner has the matrix
+    // core to itself, and a tile of half the rows takes little more than half the time.
+    const bool active = m0 + wm0 < m_valid && m0 + wm0 + C::WM > m_lo && n0 + wn0 < p.n;   // wave-uniform
+    if (!active) {
+      for (int tk = 0; tk < nk; ++tk) {   // the same barriers and DMAs as below
+        __builtin_amdgcn_s_waitcnt(0x0070);
+        __syncthreads();
+        if (tk + 2 < nk) {
+          if (tk & 1) issue(tk + 2, IC<1>{}, true);
+          else issue(tk + 2, IC<0>{}, true);
+        }
+      }
+    } else {
       Frag fa[3], fb[kFM];
 #pragma unroll
       for (int j = 0; j < kFM; ++j) fb[j] = read_frag(slot0, C::BN + wm0 + 16 * j);
@@ -870,13 +883,15 @@ constexpr TileModel kTileModel[kTiles] = {
     {I8Square::BN, I8Square::BM, I8Square::OCC, 7.0, 0.9, 1.6},
     {I8Small::BN, I8Small::BM, I8Small::OCC, 3.5, 0.5, 1.15}};
 
-static double split_time(double partial_bytes) { return 3.0 + 0.22e-6 * partial_bytes; }
+static double split_time(int splits, double partial_bytes) { return 3.0 + 0.5 * splits + 0.22e-6 * partial_bytes; }
 
-// Few-row tiles of 128 rows: 0.8 us a chunk of 256 alone, 0.7 us per workgroup of a CU once there are more.
+// Few-row tiles: the time of a chunk (512 bytes of K, 256 on 128-row tiles) with one workgroup a CU, and
+// per workgroup of the fullest CU.
 static double few_time(const FewPlan& f, int num_cus) {
-  const double c = (double)f.tiles * f.splits / num_cus;
-  const double t = 3.5 + f.steps_per_wave * (c > 8.0 / 7.0 ? 0.7 * c : 0.8) * f.r;
-  return t + (f.splits > 1 ? split_time((double)f.tiles * f.splits * f.bn * f.bm * 4) : 0.0);
+  const double c = (double)((f.tiles * f.splits + num_cus - 1) / num_cus);
+  const double one = f.j == 8 ? 0.8 * f.r : 0.95, more = f.j == 8 ? 0.7 * f.r : f.j == 4 ? 1.0 : 0.87;
+  const double t = 3.5 + f.steps_per_wave * (c * more > one ? c * more : one);
+  return t + (f.splits > 1 ? split_time(f.splits, (double)f.tiles * f.splits * f.bn * f.bm * 4) : 0.0);
 }
 
 struct TilePlan {
@@ -898,7 +913,8 @@ static TilePlan tile_choice(int tile, int splits, int layout, int64_t m, int64_t
   t.kb_per_split = (kb_total + splits - 1) / splits;
   t.splits = (kb_total + t.kb_per_split - 1) / t.kb_per_split;   // no empty split
   double tiles = (double)t.tiles_m * t.tiles_n;
-  if (layout == kMasked) tiles = (double)groups * ((m / 2 + c.bm - 1) / c.bm) * t.tiles_n;   // half the rows in use
+  // masked: the counts are on the device; any of 0 .. m rows alike use (m-blocks + 1) / 2 blocks on average
+  if (layout == kMasked) tiles = (double)groups * 0.5 * (t.tiles_m + 1) * t.tiles_n;
   if (layout == kContiguous && c.bm > kGroup) {   // a tile that spans two experts runs twice
     const int64_t edges = groups - 1 < t.tiles_m ? groups - 1 : t.tiles_m;
     tiles += (double)edges * t.tiles_n;
@@ -908,24 +924,29 @@ static TilePlan tile_choice(int tile, int splits, int layout, int64_t m, int64_t
   const double full = (double)(int64_t)(items / slots), rest = items - full * slots;
   t.us = full * (c.fixed + t.kb_per_split * c.busy);
   if (rest > 0) t.us += c.fixed + t.kb_per_split * (c.alone + (c.busy - c.alone) * rest / slots);
+  // the weights come from memory at 5 TB/s at best, and at 17 GB/s for each workgroup
+  const double rate = items * 0.017e6 < 5.0e6 ? items * 0.017e6 : 5.0e6;
+  const double weights = c.fixed + (double)n * k * (layout == kDense ? 1 : groups) / rate;
+  if (t.us < weights) t.us = weights;
   if (t.splits > 1) {
     const double partials = items * (double)(c.bm * c.bn) * 4;
-    t.us += split_time(partials);
+    t.us += split_time(t.splits, partials);
     t.ws_bytes = kCounterBytes + (size_t)partials;
   }
   return t;
 }
 
 // The fastest of the tiles and, for the normal form with a workspace, of the K splits that keep at least 4
-// K blocks and give each CU about one workgroup (with two, 256 x 4096 x 7168 on 128x128 tiles takes
-// 29.6 us, with one 22.6).
+// K blocks and give each CU about one workgroup (256 x 4096 x 7168 on 128x128 tiles: split in four 22.6 us,
+// in eight, two workgroups a CU, 29.6), or two with at most three splits (64 x 24576 x 7168: 56.4 us whole,
+// 45.5 in two).
 static TilePlan tile_plan(int layout, int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus, bool allow_split) {
   TilePlan best{};
   for (int tile = 0; tile < kTiles; ++tile) {
     for (int splits = 1; splits <= kMaxSplits; ++splits) {
       const TilePlan t = tile_choice(tile, splits, layout, m, n, k, groups, num_cus);
       if (splits > 1) {
-        if (layout != kDense || !allow_split || t.kb_per_split < 4 || 8 * t.items > 9 * (int64_t)num_cus ||
+        if (layout != kDense || !allow_split || t.kb_per_split < 4 || (splits <= 3 ? t.items > (int64_t)kTileModel[tile].occ * num_cus : 8 * t.items > 9 * (int64_t)num_cus) ||
             t.items / t.splits > kMaxCounterTiles)
           break;
         if (t.splits != splits) continue;   // the same as a smaller request
@@ -946,8 +967,8 @@ static const void* tile_fn(int layout, int tile) {
                                                                               : tile_fn_of<kDense>(tile);
 }
 
-// Rows that always run on the few-row kernel, and the most rows that may (more never measured faster).
-constexpr int64_t kFewRows = 128, kFewRowsMost = 1024;
+// The most rows that may run on the few-row kernel (more never measured faster).
+constexpr int64_t kFewRowsMost = 1024;
 
 struct I8Plan {
   bool few;
@@ -958,12 +979,10 @@ struct I8Plan {
 
 static I8Plan int8_plan(int layout, int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus, bool allow_split) {
   I8Plan p{};
-  if (layout != kContiguous && m <= (layout == kMasked ? kFewRows : kFewRowsMost))
-    p.f = few_plan(false, m, n, k, groups, num_cus, allow_split);
-  p.few = layout != kContiguous && m <= kFewRows;
-  if (p.few) return p;
+  p.few = layout != kContiguous && m <= kFewRowsMost;
+  if (p.few) p.f = few_plan(false, m, n, k, groups, num_cus, allow_split);
   p.t = tile_plan(layout, m, n, k, groups, num_cus, allow_split);
-  p.few = layout == kDense && m <= kFewRowsMost && few_time(p.f, num_cus) < p.t.us;
+  p.few = p.few && few_time(p.f, num_cus) < p.t.us;
   return p;
 }
 
