@@ -154,12 +154,23 @@ def _check(fn, status):
         raise DGError(fn, status)
 
 
+# torch's own query of the current stream's handle (0.1 us; building a Stream object for it takes 2 us,
+# a sixth of a small call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_handle(device):
+    if _raw_stream is None or device.index is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return _raw_stream(device.index)
+
+
 def _stream(t):
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+    return _stream_handle(t.device)
 
 
 def _ptr(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else None
+    return t.data_ptr() if t is not None else None
 
 
 def _bytes(t):
@@ -231,14 +242,13 @@ def default_workspace(device, nbytes):
     there would be zero-filled only when the graph runs): pass one created before the capture."""
     if nbytes == 0:
         return None
-    dev = torch.device(device)
+    dev = device if isinstance(device, torch.device) else torch.device(device)
     if dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())
-    stream = torch.cuda.current_stream(dev)
     if torch.cuda.is_current_stream_capturing():
         raise ValueError("no default workspace during graph capture: pass workspace= (a zero-filled uint8 "
                          "tensor of dg_gemm_workspace_size(...) bytes created before the capture)")
-    key = (dev.index, stream.cuda_stream)
+    key = (dev.index, _stream_handle(dev))
     ws = _ws_cache.get(key)
     if ws is None or ws.numel() < nbytes:
         if ws is not None:
@@ -515,11 +525,15 @@ def dg_moe_route(logits, top_k, bias=None, num_groups=1, topk_groups=1, group_to
     _require(score in _SCORES, "score must be 'softmax' or 'sigmoid'")
     if ids is None:
         ids = torch.empty((t, top_k), dtype=torch.int32, device=logits.device)
+    else:
+        _dev(ids)
+        _require(ids.dtype == torch.int32 and tuple(ids.shape) == (t, top_k), "ids must be int32 (tokens, top_k)")
     if weights is None:
         weights = torch.empty((t, top_k), dtype=torch.float32, device=logits.device)
-    _dev(ids, weights)
-    _require(ids.dtype == torch.int32 and tuple(ids.shape) == (t, top_k), "ids must be int32 (tokens, top_k)")
-    _require(weights.dtype == torch.float32 and tuple(weights.shape) == (t, top_k), "weights must be float32 (tokens, top_k)")
+    else:
+        _dev(weights)
+        _require(weights.dtype == torch.float32 and tuple(weights.shape) == (t, top_k),
+                 "weights must be float32 (tokens, top_k)")
     if bias is not None:
         _dev(bias)
         _require(bias.dtype == torch.float32 and tuple(bias.shape) == (e,), "bias must be float32 (experts,)")
@@ -587,13 +601,17 @@ def dg_moe_layout(ids, num_experts, rows_per_expert=0, rows_total=None, workspac
     # one allocation for the index arrays
     n, contiguous = t * k, not rows_per_expert
     _require(n >= 0 and rows_total >= 0 and num_experts >= 1, "sizes must not be negative")
-    buf = torch.empty(n + rows_total * (2 if contiguous else 1) + num_experts, dtype=torch.int32, device=dev)
-    parts = buf.split((n, rows_total, num_experts, rows_total if contiguous else 0))
-    rows, sources, counts = parts[0].view(t, k), parts[1], parts[2]
-    m_indices = parts[3] if contiguous else None
-    need = L.dg_moe_layout_workspace_size(t, k, num_experts)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if contiguous:
+        buf = torch.empty(n + 2 * rows_total + num_experts, dtype=torch.int32, device=dev)
+        rows, sources, counts, m_indices = buf.split((n, rows_total, num_experts, rows_total))
+    else:
+        buf = torch.empty(n + rows_total + num_experts, dtype=torch.int32, device=dev)
+        (rows, sources, counts), m_indices = buf.split((n, rows_total, num_experts)), None
+    rows = rows.view(t, k)
+    if workspace is None:
+        need = L.dg_moe_layout_workspace_size(t, k, num_experts)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check("dg_moe_layout",
            L.dg_moe_layout(_ptr(ids), t, k, num_experts, rows_per_expert, rows_total, _ptr(rows), _ptr(sources),
