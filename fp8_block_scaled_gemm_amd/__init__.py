@@ -92,7 +92,8 @@ _SIGNATURES = {
     "dg_moe_dispatch": (ctypes.c_int, [_vp, _c_int, _vp, _vp, _vp, _c_int64, _c_int64, _c_int64, _c_int64, _c_int64, _vp,
                                        _vp]),
     "dg_moe_dispatch_fp8": (ctypes.c_int, [_vp, _c_int, _vp, _vp, _vp, _c_int64, _c_int64, _c_int64, _c_int64, _c_int64,
-                                           _vp, _vp, _c_int64, _vp]),
+                                           _vp, _vp, _c_int64, _vp, ctypes.c_size_t, _vp]),
+    "dg_moe_dispatch_fp8_workspace_size": (ctypes.c_size_t, [_c_int64, _c_int64, _c_int64]),
     "dg_moe_dispatch_int8": (ctypes.c_int, [_vp, _c_int, _vp, _vp, _vp, _c_int64, _c_int64, _c_int64, _c_int64, _c_int64,
                                             _vp, _vp, _vp]),
     "dg_moe_combine": (ctypes.c_int, [_vp, _c_int, _vp, _vp, _c_int64, _c_int64, _c_int64, _c_int64, _vp, _vp]),
@@ -637,7 +638,11 @@ def dg_moe_dispatch(x, layout, out=None):
     return out
 
 
-def dg_moe_dispatch_fp8(x, layout, q=None, sa=None):
+def dg_moe_dispatch_fp8_workspace_size(tokens, top_k, hidden):
+    return lib().dg_moe_dispatch_fp8_workspace_size(int(tokens), int(top_k), int(hidden))
+
+
+def dg_moe_dispatch_fp8(x, layout, q=None, sa=None, workspace=None):
     """x (T, H) -> (q uint8 rows, sa float32 (ceil(H/128), ld_sa) per matrix): the layout's rows as
     dg_quantize_per_token_group would quantize them, ready for the grouped FP8 GEMMs."""
     h, lead = x.shape[-1], layout.lead()
@@ -649,8 +654,13 @@ def dg_moe_dispatch_fp8(x, layout, q=None, sa=None):
     _dev(x, q, sa)
     _require(q.dtype == torch.uint8 and q.numel() == layout.rows_total * h, "q must be uint8 and hold the layout's rows")
     _require(sa.dtype == torch.float32 and tuple(sa.shape[:-1]) == (*lead[:-1], -(-h // 128)), "sa must be float32, K-group-major")
+    if workspace is None:
+        need = lib().dg_moe_dispatch_fp8_workspace_size(x.shape[0], layout.rows.shape[1], h)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
     _check("dg_moe_dispatch_fp8",
-           lib().dg_moe_dispatch_fp8(*_dispatch_args(x, layout), _ptr(q), _ptr(sa), sa.shape[-1], _stream(x)))
+           lib().dg_moe_dispatch_fp8(*_dispatch_args(x, layout), _ptr(q), _ptr(sa), sa.shape[-1], *_ws(workspace),
+                                     _stream(x)))
     return q, sa
 
 

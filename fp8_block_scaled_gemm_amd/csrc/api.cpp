@@ -54,7 +54,8 @@ int launch_moe_layout(const int32_t* ids, int64_t n, int experts, int64_t rows_p
                       void* ws, hipStream_t stream);
 int launch_moe_dispatch(int form, const void* x, int dtype, const int32_t* rows, const int32_t* sources,
                         const int32_t* m_indices, int64_t tokens, int top_k, int64_t hidden, int64_t rows_total,
-                        int64_t rows_per_expert, void* q, float* s, int64_t ld_s, hipStream_t stream);
+                        int64_t rows_per_expert, void* q, float* s, int64_t ld_s, float* s_tmp, hipStream_t stream);
+size_t moe_dispatch_fp8_workspace_size(int64_t tokens, int64_t top_k, int64_t hidden);
 int launch_moe_combine(const void* out, int dtype, const int32_t* rows, const float* weights, int64_t tokens, int top_k,
                        int64_t hidden, int64_t rows_total, void* y, hipStream_t stream);
 int launch_moe_combine_grad(const void* dy, const void* out, int dtype, const int32_t* rows, const int32_t* sources,
@@ -502,7 +503,7 @@ static int check_rows(const char* what, int dtype, const int32_t* rows, const in
 
 static int moe_dispatch(const char* what, int form, const void* x, int dtype, const int32_t* rows, const int32_t* sources,
                         const int32_t* m_indices, int64_t tokens, int64_t top_k, int64_t hidden, int64_t rows_total,
-                        int64_t rows_per_expert, void* q, float* s, int64_t ld_s, dg_stream_t stream) {
+                        int64_t rows_per_expert, void* q, float* s, int64_t ld_s, float* s_tmp, dg_stream_t stream) {
   const int c = check_rows(what, dtype, rows, sources, m_indices, tokens, top_k, hidden, rows_total);
   if (c != DG_OK) return c;
   DG_REQUIRE(rows_per_expert >= 0 && (rows_per_expert == 0) == (m_indices != nullptr || rows_total == 0),
@@ -512,31 +513,43 @@ static int moe_dispatch(const char* what, int form, const void* x, int dtype, co
   DG_REQUIRE(q && (tokens == 0 || x) && (form == 0 || s), "%s: null pointer", what);
   DG_REQUIRE(aligned16(x) && aligned16(q) && aligned_to(s, 4), "%s: row data must be 16-byte aligned", what);
   return launch_moe_dispatch(form, x, dtype, rows, sources, m_indices, tokens, (int)top_k, hidden, rows_total,
-                             rows_per_expert, q, s, ld_s, static_cast<hipStream_t>(stream));
+                             rows_per_expert, q, s, ld_s, s_tmp, static_cast<hipStream_t>(stream));
 }
 
 int dg_moe_dispatch(const void* x, int dtype, const int32_t* rows, const int32_t* sources, const int32_t* m_indices,
                     int64_t tokens, int64_t top_k, int64_t hidden, int64_t rows_total, int64_t rows_per_expert,
                     void* out, dg_stream_t stream) {
   return moe_dispatch("moe_dispatch", 0, x, dtype, rows, sources, m_indices, tokens, top_k, hidden, rows_total,
-                      rows_per_expert, out, nullptr, 0, stream);
+                      rows_per_expert, out, nullptr, 0, nullptr, stream);
+}
+
+size_t dg_moe_dispatch_fp8_workspace_size(int64_t tokens, int64_t top_k, int64_t hidden) {
+  if (tokens <= 0 || tokens > kInt31 / 2 || top_k <= 0 || top_k > kMaxTopK || hidden <= 0 || hidden % kKAlign ||
+      hidden > kInt31 / 64)
+    return 0;
+  return moe_dispatch_fp8_workspace_size(tokens, top_k, hidden);
 }
 
 int dg_moe_dispatch_fp8(const void* x, int dtype, const int32_t* rows, const int32_t* sources, const int32_t* m_indices,
                         int64_t tokens, int64_t top_k, int64_t hidden, int64_t rows_total, int64_t rows_per_expert,
-                        uint8_t* q, float* sa, int64_t ld_sa, dg_stream_t stream) {
+                        uint8_t* q, float* sa, int64_t ld_sa, void* workspace, size_t workspace_bytes,
+                        dg_stream_t stream) {
   const int64_t need = rows_per_expert > 0 ? rows_per_expert : rows_total;
   DG_REQUIRE(ld_sa >= need && ld_sa % 4 == 0, "moe_dispatch_fp8: need ld_sa >= %lld and ld_sa %% 4 == 0 (ld_sa=%lld)",
              (long long)need, (long long)ld_sa);
+  DG_REQUIRE(aligned_to(workspace, 4), "moe_dispatch_fp8: misaligned workspace");
+  // without a workspace (or with too small a one) the scales go straight to their places
+  const size_t tmp = dg_moe_dispatch_fp8_workspace_size(tokens, top_k, hidden);
+  const bool moved = tmp > 0 && workspace != nullptr && workspace_bytes >= tmp && sources != nullptr;
   return moe_dispatch("moe_dispatch_fp8", 1, x, dtype, rows, sources, m_indices, tokens, top_k, hidden, rows_total,
-                      rows_per_expert, q, sa, ld_sa, stream);
+                      rows_per_expert, q, sa, ld_sa, moved ? static_cast<float*>(workspace) : nullptr, stream);
 }
 
 int dg_moe_dispatch_int8(const void* x, int dtype, const int32_t* rows, const int32_t* sources,
                          const int32_t* m_indices, int64_t tokens, int64_t top_k, int64_t hidden, int64_t rows_total,
                          int64_t rows_per_expert, int8_t* q, float* s, dg_stream_t stream) {
   return moe_dispatch("moe_dispatch_int8", 2, x, dtype, rows, sources, m_indices, tokens, top_k, hidden, rows_total,
-                      rows_per_expert, q, s, 0, stream);
+                      rows_per_expert, q, s, 0, nullptr, stream);
 }
 
 int dg_moe_combine(const void* out, int dtype, const int32_t* rows, const float* weights, int64_t tokens, int64_t top_k,

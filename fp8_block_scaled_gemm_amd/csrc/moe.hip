@@ -328,11 +328,19 @@ int launch_route_grad(const float* dweights, const void* logits, int dtype, int6
 
 // ---------------------------------------------------------------------------
 // Layout: a stable counting sort of the (token, place) entries by expert.
+//
+// Nothing here is more than a few KB; what counts is the latency of the steps.  A wave takes 64 entries at
+// a time: one ballot per bit of the expert index tells every lane which lanes have its expert, so the
+// expert's first lane adds their number to the wave's own counter in LDS without an atomic, and a lane's
+// rank is the counter's old value plus the earlier lanes of its expert - in the entries' order.
+// Up to kLayOnce entries are counted by every workgroup for itself, in one launch; more are counted by a
+// launch of their own, a chunk a workgroup, whose histograms every workgroup of the second then adds up
+// (2048 entries into 256 experts: 8.8 us in one launch, 9.5 in two; 4096: 13.8 and 9.4).
 // ---------------------------------------------------------------------------
 constexpr int kLayThreads = 512;
 constexpr int kLayWaves = kLayThreads / 64;
-constexpr int kLayMaxExperts = 1024;
-constexpr int kLayChunk = 4096;   // entries per workgroup
+constexpr int kLayChunk = 1024;   // entries per workgroup where there is more than one
+constexpr int kLayOnce = 2048;
 
 struct LayoutParams {
   const int32_t* ids;
@@ -341,38 +349,52 @@ struct LayoutParams {
   int rows_per_expert;   // 0: the contiguous layout
   int align;             // row alignment of the contiguous layout
   int rows_total;
-  int blocks;
+  int chunk, blocks;     // entries per chunk, chunks
   int32_t* rows;
   int32_t* sources;
   int32_t* m_indices;
   int32_t* counts;
-  int32_t* hist;         // (blocks, experts), when there is more than one workgroup
+  int32_t* hist;         // (chunks, experts), with more than one chunk
 };
 
-__device__ __forceinline__ int entry_expert(const LayoutParams& p, int i, int end) {
-  const int e = i < end ? p.ids[i] : -1;
-  return e >= 0 && e < p.experts ? e : -1;
-}
-
-// Each wave of a workgroup owns a run of its entries; s_hist[w][e] counts them by expert.
-__device__ __forceinline__ void count_entries(const LayoutParams& p, int begin, int end, int per_wave, int* s_hist) {
+// Entries [begin, end) in order, split over the waves; f(entry, expert or -1, rank of the entry among the
+// wave's earlier entries of its expert + the counter's start).  s_next: the wave's own (experts) counters.
+template <class F>
+__device__ __forceinline__ void for_entries(const LayoutParams& p, int begin, int end, int* s_next, F f) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int i = threadIdx.x; i < kLayWaves * p.experts; i += kLayThreads) s_hist[i] = 0;
-  __syncthreads();
+  const int per_wave = ((end - begin + kLayWaves - 1) / kLayWaves + 63) & ~63;
   const int w0 = begin + wave * per_wave;
   const int w1 = w0 + per_wave < end ? w0 + per_wave : end;
-  for (int i = w0 + lane; i < w1; i += 64) {
-    const int e = entry_expert(p, i, w1);
-    if (e >= 0) atomicAdd(&s_hist[wave * p.experts + e], 1);   // integers: the sum has no order
+  for (int i0 = w0; i0 < w1; i0 += 64) {
+    const int i = i0 + lane;
+    int e = i < w1 ? p.ids[i] : -1;
+    if ((uint32_t)e >= (uint32_t)p.experts) e = -1;
+    uint64_t same = __ballot(e >= 0);
+    for (int bit = 1; bit < p.experts; bit *= 2) {
+      const uint64_t set = __ballot((e & bit) != 0);   // (a lane without an expert is masked out of `same`)
+      same &= (e & bit) ? set : ~set;
+    }
+    const int earlier = __popcll(same & ((1ull << lane) - 1));
+    const int next = s_next[e >= 0 ? e : 0];
+    wave_lds_fence();
+    if (e >= 0 && earlier == 0) s_next[e] = next + __popcll(same);
+    wave_lds_fence();
+    if (i < w1) f(i, e, next + earlier);
   }
+}
+
+// s_hist[wave][expert]: the entries [begin, end) of each wave, by expert.
+__device__ __forceinline__ void count_entries(const LayoutParams& p, int begin, int end, int* s_hist) {
+  for (int i = threadIdx.x; i < kLayWaves * p.experts; i += kLayThreads) s_hist[i] = 0;
+  __syncthreads();
+  for_entries(p, begin, end, s_hist + (threadIdx.x >> 6) * p.experts, [](int, int, int) {});
   __syncthreads();
 }
 
 __global__ __launch_bounds__(kLayThreads) void layout_count_kernel(LayoutParams p) {
   extern __shared__ int s_hist[];
-  const int begin = blockIdx.x * kLayChunk;
-  const int end = begin + kLayChunk < p.n ? begin + kLayChunk : p.n;
-  count_entries(p, begin, end, kLayChunk / kLayWaves, s_hist);
+  const int begin = blockIdx.x * p.chunk;
+  count_entries(p, begin, begin + p.chunk < p.n ? begin + p.chunk : p.n, s_hist);
   for (int e = threadIdx.x; e < p.experts; e += kLayThreads) {
     int sum = 0;
     for (int w = 0; w < kLayWaves; ++w) sum += s_hist[w * p.experts + e];
@@ -382,25 +404,32 @@ __global__ __launch_bounds__(kLayThreads) void layout_count_kernel(LayoutParams 
 
 __global__ __launch_bounds__(kLayThreads) void layout_place_kernel(LayoutParams p) {
   extern __shared__ int smem[];
-  int* s_hist = smem;                                  // (waves, experts): counts, then next ranks
-  int* s_start = smem + kLayWaves * p.experts;         // (experts + 1): first row of each expert
-  int* s_count = s_start + p.experts + 1;              // (experts): entries of each expert, all workgroups
+  int* s_hist = smem;                             // (waves, experts): counts, then next ranks
+  int* s_start = smem + kLayWaves * p.experts;    // (experts + 1): first row of each expert
+  int* s_count = s_start + p.experts + 1;         // (experts): entries of each expert
   __shared__ int s_scan[kLayWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int begin = blockIdx.x * kLayChunk;
-  const int end = begin + kLayChunk < p.n ? begin + kLayChunk : p.n;
-  const int per_wave = kLayChunk / kLayWaves;
-  count_entries(p, begin, end, per_wave, s_hist);
+  const int block = blockIdx.x;
+  // this workgroup's chunk (with one chunk every workgroup counts it and the first one places it)
+  const int chunk = p.blocks == 1 ? 0 : block;
+  int begin = chunk * p.chunk, end = begin + p.chunk;
+  if (begin > p.n) begin = p.n;
+  if (end > p.n) end = p.n;
+  count_entries(p, begin, end, s_hist);
 
-  // ranks: entries of the expert in earlier workgroups, then in this workgroup's earlier waves
+  // ranks: entries of the expert in earlier chunks, then in this chunk's earlier waves
   for (int e = tid; e < p.experts; e += kLayThreads) {
     int before = 0, all = 0;
-    for (int b = 0; b < p.blocks && p.blocks > 1; ++b) {
-      const int c = p.hist[(int64_t)b * p.experts + e];
-      if (b < (int)blockIdx.x) before += c;
-      all += c;
+    if (p.blocks > 1) {
+#pragma unroll 16
+      for (int b = 0; b < p.blocks; ++b) {
+        const int c = p.hist[(int64_t)b * p.experts + e];
+        before += b < chunk ? c : 0;
+        all += c;
+      }
     }
     int here = 0;
+#pragma unroll
     for (int w = 0; w < kLayWaves; ++w) {
       const int c = s_hist[w * p.experts + e];
       s_hist[w * p.experts + e] = before + here;
@@ -408,7 +437,7 @@ __global__ __launch_bounds__(kLayThreads) void layout_place_kernel(LayoutParams 
     }
     if (p.blocks == 1) all = here;
     s_count[e] = all;
-    if (blockIdx.x == 0) p.counts[e] = all;
+    if (block == 0) p.counts[e] = all;
   }
   __syncthreads();
   // first rows: an exclusive scan of the aligned counts (each thread two experts), or a fixed pitch
@@ -434,37 +463,17 @@ __global__ __launch_bounds__(kLayThreads) void layout_place_kernel(LayoutParams 
   }
   __syncthreads();
 
-  // place the entries, 64 at a time in their order: a lane's rank is the wave's next rank of its
-  // expert plus the earlier lanes with the same expert
-  const int w0 = begin + wave * per_wave;
-  const int w1 = w0 + per_wave < end ? w0 + per_wave : end;
-  for (int i0 = w0; i0 < w1; i0 += 64) {
-    const int i = i0 + lane;
-    const int e = entry_expert(p, i, w1);
-    uint64_t same = __ballot(e >= 0);
-    for (int bit = 1; bit < p.experts; bit *= 2) {
-      const uint64_t set = __ballot((e & bit) != 0 && e >= 0);
-      same &= (e & bit) ? set : ~set;
-    }
-    const int earlier = __popcll(same & ((1ull << lane) - 1));
-    const int next = s_hist[wave * p.experts + (e >= 0 ? e : 0)];
-    wave_lds_fence();
-    if (e >= 0 && earlier == 0) s_hist[wave * p.experts + e] = next + __popcll(same);
-    wave_lds_fence();
-    if (e >= 0) {
-      const int rank = next + earlier;
-      const bool fits = p.rows_per_expert == 0 || rank < p.rows_per_expert;
-      const int row = s_start[e] + rank;
-      p.rows[i] = fits ? row : -1;
+  if (p.blocks > 1 || block == 0)
+    for_entries(p, begin, end, s_hist + wave * p.experts, [&](int i, int e, int rank) {
+      const bool fits = e >= 0 && (p.rows_per_expert == 0 || rank < p.rows_per_expert);
+      const int row = fits ? s_start[e] + rank : -1;
+      p.rows[i] = row;
       if (fits) p.sources[row] = i;
-    } else if (i < w1) {
-      p.rows[i] = -1;
-    }
-  }
+    });
 
-  // every row's expert, and -1 for the rows that no entry fills
+  // every row's expert, and -1 for the rows that no entry fills (a row or two a thread)
   const int used = s_start[p.experts];
-  for (int r = blockIdx.x * kLayThreads + tid; r < p.rows_total; r += gridDim.x * kLayThreads) {
+  for (int r = block * kLayThreads + tid; r < p.rows_total; r += gridDim.x * kLayThreads) {
     int lo = 0, hi = p.experts;   // s_start[lo] <= r < s_start[hi]
     if (r < used) {
       while (hi - lo > 1) {
@@ -478,7 +487,7 @@ __global__ __launch_bounds__(kLayThreads) void layout_place_kernel(LayoutParams 
   }
 }
 
-static int layout_blocks(int64_t n) { return n <= kLayChunk ? 1 : (int)((n + kLayChunk - 1) / kLayChunk); }
+static int layout_blocks(int64_t n) { return n <= kLayOnce ? 1 : (int)((n + kLayChunk - 1) / kLayChunk); }
 
 size_t moe_layout_workspace_size(int64_t n, int64_t experts) {
   const int b = layout_blocks(n);
@@ -492,6 +501,7 @@ int launch_moe_layout(const int32_t* ids, int64_t n, int experts, int64_t rows_p
   p.ids = ids; p.n = (int)n; p.experts = experts;
   p.rows_per_expert = (int)rows_per_expert; p.align = align; p.rows_total = (int)rows_total;
   p.blocks = layout_blocks(n);
+  p.chunk = p.blocks > 1 ? kLayChunk : kLayOnce;
   p.rows = rows; p.sources = sources; p.m_indices = m_indices; p.counts = counts;
   p.hist = static_cast<int32_t*>(ws);
   const size_t lds = (size_t)kLayWaves * experts * 4;
@@ -500,8 +510,12 @@ int launch_moe_layout(const int32_t* ids, int64_t n, int experts, int64_t rows_p
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return set_error(kHip, "moe_layout launch: %s", hipGetErrorString(e));
   }
-  hipLaunchKernelGGL(layout_place_kernel, dim3(p.blocks), dim3(kLayThreads), lds + (2 * (size_t)experts + 1) * 4, stream,
-                     p);
+  // workgroups: a chunk each, and enough to write the rows' arrays
+  int64_t grid = (rows_total + kLayThreads - 1) / kLayThreads;
+  if (grid > 128) grid = 128;
+  if (grid < p.blocks) grid = p.blocks;
+  hipLaunchKernelGGL(layout_place_kernel, dim3((unsigned)(grid < 1 ? 1 : grid)), dim3(kLayThreads),
+                     lds + (2 * (size_t)experts + 1) * 4, stream, p);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? kOk : set_error(kHip, "moe_layout launch: %s", hipGetErrorString(e));
 }
@@ -511,7 +525,7 @@ int launch_moe_layout(const int32_t* ids, int64_t n, int experts, int64_t rows_p
 // ---------------------------------------------------------------------------
 enum Form : int { kCopy = 0, kFp8 = 1, kInt8 = 2 };
 constexpr int kRowThreads = 256;
-constexpr int kPadRows = 64;   // rows per padding workgroup
+constexpr int kPadRows = 16;   // rows per padding workgroup
 
 struct DispatchParams {
   const void* x;
@@ -523,6 +537,7 @@ struct DispatchParams {
   void* q;
   float* s;
   int64_t ld_s;
+  float* s_tmp;               // FP8: token-major scales (tokens, K groups), or NULL: stored to their places at once
 };
 
 // Row of a (token, place) entry, or -1: entries without a row, and anything a caller's array holds
@@ -544,7 +559,7 @@ template <class T, int FORM>
 __device__ __forceinline__ void zero_padding(const DispatchParams& p, int row0) {
   const int lane = threadIdx.x & 63;
   const int r = row0 + lane;
-  uint64_t pad = __ballot(r < p.rows_total && p.sources[r < p.rows_total ? r : 0] < 0 &&
+  uint64_t pad = __ballot(lane < kPadRows && r < p.rows_total && p.sources[r < p.rows_total ? r : 0] < 0 &&
                           p.m_indices[r < p.rows_total ? r : 0] >= 0);
   const int kbc = (p.hidden + kGroup - 1) / kGroup;
   constexpr int kSize = FORM == kCopy ? (int)sizeof(T) : 1;
@@ -557,26 +572,37 @@ __device__ __forceinline__ void zero_padding(const DispatchParams& p, int row0) 
     if constexpr (FORM == kInt8) {
       if (threadIdx.x == 0) p.s[row] = 1.0f;
     } else if constexpr (FORM == kFp8) {
-      for (int kb = threadIdx.x; kb < kbc; kb += kRowThreads) p.s[fp8_scale_at(p, row, kb, kbc)] = 1.0f;
+      if (p.s_tmp == nullptr)   // (else scale_rows_kernel writes them)
+        for (int kb = threadIdx.x; kb < kbc; kb += kRowThreads) p.s[fp8_scale_at(p, row, kb, kbc)] = 1.0f;
     }
   }
 }
 
-template <class T, int FORM>
+// LT lanes hold a token's row (16 elements each at a time): a wave per token, four tokens a workgroup, for
+// rows of up to 1024 elements (16384 tokens of 256: 29 us with a workgroup each), else the workgroup.
+// FP8 scales lie K-group-major, so a row's are ld_s apart, each in a cache line of its own that 31 other
+// rows share: with many of them the kernel writes them token-major into s_tmp and scale_rows_kernel moves
+// them (4096 tokens x 8 of 7168: 72 us, 84 with the scattered stores).
+template <class T, int FORM, int LT>
 __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(DispatchParams p) {
+  constexpr int kTokens = kRowThreads / LT;
   __shared__ uint32_t s_max[kRowThreads / 64];
   const int tid = threadIdx.x;
-  if ((int)blockIdx.x >= p.tokens) {
-    zero_padding<T, FORM>(p, ((int)blockIdx.x - p.tokens) * kPadRows);
+  const int blocks = (p.tokens + kTokens - 1) / kTokens;
+  if ((int)blockIdx.x >= blocks) {
+    zero_padding<T, FORM>(p, ((int)blockIdx.x - blocks) * kPadRows);
     return;
   }
-  const int token = blockIdx.x;
+  // (wave-uniform: LT is a whole number of waves)
+  const int token = blockIdx.x * kTokens + __builtin_amdgcn_readfirstlane(tid / LT);
+  const int lane = tid % LT;
+  if (token >= p.tokens) return;   // only where a wave holds a token: no barrier below
   const T* src = static_cast<const T*>(p.x) + (int64_t)token * p.hidden;
   const int32_t* rows = p.rows + (int64_t)token * p.top_k;
 
   if constexpr (FORM == kCopy) {
     T* out = static_cast<T*>(p.q);
-    for (int i = 8 * tid; i < p.hidden; i += 8 * kRowThreads) {
+    for (int i = 8 * lane; i < p.hidden; i += 8 * LT) {
       const Raw8<T> v = load8(src + i);
       for (int k = 0; k < p.top_k; ++k) {
         const int row = row_at(rows, k, p.rows_total);
@@ -586,7 +612,7 @@ __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(DispatchParams p)
   } else if constexpr (FORM == kInt8) {
     uint8_t* out = static_cast<uint8_t*>(p.q);
     uint32_t amax = 0;
-    for (int i = 16 * tid; i < p.hidden; i += 16 * kRowThreads) {
+    for (int i = 16 * lane; i < p.hidden; i += 16 * LT) {
       float v[16];
       widen8(load8(src + i), v);
       widen8(load8(src + i + 8), v + 8);
@@ -594,11 +620,13 @@ __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(DispatchParams p)
       for (int u = 0; u < 16; ++u) amax = umax(amax, abs_bits(v[u]));
     }
     amax = wave_max_u32(amax);
-    if ((tid & 63) == 0) s_max[tid >> 6] = amax;
-    __syncthreads();
-    amax = umax(umax(s_max[0], s_max[1]), umax(s_max[2], s_max[3]));
+    if constexpr (LT > 64) {
+      if ((tid & 63) == 0) s_max[tid >> 6] = amax;
+      __syncthreads();
+      amax = umax(umax(s_max[0], s_max[1]), umax(s_max[2], s_max[3]));
+    }
     const float s = int8_scale(amax);
-    for (int i = 16 * tid; i < p.hidden; i += 16 * kRowThreads) {
+    for (int i = 16 * lane; i < p.hidden; i += 16 * LT) {   // (read again, from the caches)
       float v[16];
       widen8(load8(src + i), v);
       widen8(load8(src + i + 8), v + 8);
@@ -608,8 +636,8 @@ __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(DispatchParams p)
         if (row >= 0) *reinterpret_cast<u32x4_t*>(out + (int64_t)row * p.hidden + i) = codes;
       }
     }
-    if (tid < p.top_k) {
-      const int row = row_at(rows, tid, p.rows_total);
+    if (lane < p.top_k) {
+      const int row = row_at(rows, lane, p.rows_total);
       if (row >= 0) p.s[row] = s;
     }
   } else {
@@ -618,7 +646,7 @@ __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(DispatchParams p)
     uint8_t* out = static_cast<uint8_t*>(p.q);
     const int kbc = (p.hidden + kGroup - 1) / kGroup;
     const int padded = kbc * kGroup;
-    for (int i = 16 * tid; i < padded; i += 16 * kRowThreads) {
+    for (int i = 16 * lane; i < padded; i += 16 * LT) {
       const bool there = i < p.hidden;
       float v[16];
       widen8(load8(src + (there ? i : 0)), v);
@@ -633,36 +661,91 @@ __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(DispatchParams p)
       for (int u = 0; u < 4; ++u)
         codes[u] = pack4_e4m3(clamp448(v[4 * u] / s), clamp448(v[4 * u + 1] / s), clamp448(v[4 * u + 2] / s),
                               clamp448(v[4 * u + 3] / s));
+      if (p.s_tmp != nullptr && (lane & 7) == 0) p.s_tmp[(int64_t)token * kbc + i / kGroup] = s;
       for (int k = 0; k < p.top_k; ++k) {
         const int row = row_at(rows, k, p.rows_total);
         if (row < 0) continue;
         if (there) *reinterpret_cast<u32x4_t*>(out + (int64_t)row * p.hidden + i) = codes;
-        if ((tid & 7) == 0) p.s[fp8_scale_at(p, row, i / kGroup, kbc)] = s;
+        if (p.s_tmp == nullptr && (lane & 7) == 0) p.s[fp8_scale_at(p, row, i / kGroup, kbc)] = s;
       }
     }
   }
 }
 
+// FP8 scales of 64 rows x 64 K groups from s_tmp (token-major) to their K-group-major places, through LDS.
+constexpr int kScaleTile = 64;
+
+__global__ __launch_bounds__(256) void scale_rows_kernel(DispatchParams p) {
+  __shared__ float s_tile[kScaleTile][kScaleTile + 1];
+  __shared__ int s_src[kScaleTile];
+  const int kbc = (p.hidden + kGroup - 1) / kGroup;
+  const int row0 = blockIdx.x * kScaleTile, kb0 = blockIdx.y * kScaleTile;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (wave == 0) {
+    const int r = row0 + lane;
+    const int src = r < p.rows_total ? p.sources[r] : -1;
+    const bool pad = r < p.rows_total && src < 0 && p.m_indices != nullptr && p.m_indices[r] >= 0;
+    // the row's token; -2: a padding row (scales 1); -1: not written (an entry past the tokens included)
+    s_src[lane] = pad ? -2 : (uint32_t)src < (uint32_t)p.tokens * (uint32_t)p.top_k ? src / p.top_k : -1;
+  }
+  __syncthreads();
+  float v[kScaleTile / 4];   // every lane loads, all of a wave's rows in flight together
+  const int col = kb0 + lane < kbc ? kb0 + lane : kb0;
+#pragma unroll
+  for (int u = 0; u < kScaleTile / 4; ++u) {
+    const int token = s_src[wave + 4 * u];
+    v[u] = p.s_tmp[(int64_t)(token >= 0 ? token : 0) * kbc + col];
+    v[u] = token >= 0 ? v[u] : 1.0f;
+  }
+#pragma unroll
+  for (int u = 0; u < kScaleTile / 4; ++u) s_tile[lane][wave + 4 * u] = v[u];
+  __syncthreads();
+  const bool write = s_src[lane] != -1;
+  for (int kb = wave; kb < kScaleTile && kb0 + kb < kbc; kb += 4)
+    if (write) p.s[fp8_scale_at(p, row0 + lane, kb0 + kb, kbc)] = s_tile[kb][lane];
+}
+
+// Scales past which the second launch pays (2048 tokens x 8 of 2048, 256 K scales: 12.7 us scattered, 14.0 in
+// two launches; 2048 x 8 of 7168, 0.9 M: 36.6 and 32.4; 4096 x 8 of 7168, 1.8 M: 84 and 72).
+constexpr int64_t kScatterScales = 512 * 1024;
+
+size_t moe_dispatch_fp8_workspace_size(int64_t tokens, int64_t top_k, int64_t hidden) {
+  const int64_t kbc = (hidden + kGroup - 1) / kGroup;
+  return tokens * top_k * kbc > kScatterScales ? (size_t)(tokens * kbc) * 4 : 0;
+}
+
+template <int FORM, int LT>
+static const void* dispatch_fn(int dtype) {
+  void (*fn)(DispatchParams) = dtype == kF32    ? dispatch_kernel<float, FORM, LT>
+                               : dtype == kBf16 ? dispatch_kernel<Bf16, FORM, LT>
+                                                : dispatch_kernel<_Float16, FORM, LT>;
+  return reinterpret_cast<const void*>(fn);
+}
+
 template <int FORM>
 static int launch_dispatch_form(DispatchParams p, int dtype, hipStream_t stream) {
   const int64_t pad = p.m_indices != nullptr ? (p.rows_total + kPadRows - 1) / kPadRows : 0;
-  void (*fn)(DispatchParams) = dtype == kF32    ? dispatch_kernel<float, FORM>
-                               : dtype == kBf16 ? dispatch_kernel<Bf16, FORM>
-                                                : dispatch_kernel<_Float16, FORM>;
-  if (p.tokens + pad == 0) return kOk;
+  const bool narrow_rows = p.hidden <= 1024;
+  const int64_t blocks = narrow_rows ? ((int64_t)p.tokens + 3) / 4 : p.tokens;
+  if (blocks + pad == 0) return kOk;
   void* args[] = {&p};
-  return launched(reinterpret_cast<const void*>(fn), dim3((unsigned)(p.tokens + pad)), dim3(kRowThreads), args, stream,
-                  "moe_dispatch");
+  const int r = launched(narrow_rows ? dispatch_fn<FORM, 64>(dtype) : dispatch_fn<FORM, 256>(dtype),
+                         dim3((unsigned)(blocks + pad)), dim3(kRowThreads), args, stream, "moe_dispatch");
+  if (r != kOk || p.s_tmp == nullptr) return r;
+  const int kbc = (p.hidden + kGroup - 1) / kGroup;
+  return launched(reinterpret_cast<const void*>(scale_rows_kernel),
+                  dim3((unsigned)((p.rows_total + kScaleTile - 1) / kScaleTile), (unsigned)((kbc + kScaleTile - 1) / kScaleTile)),
+                  dim3(256), args, stream, "moe_dispatch_fp8 scales");
 }
 
 int launch_moe_dispatch(int form, const void* x, int dtype, const int32_t* rows, const int32_t* sources,
                         const int32_t* m_indices, int64_t tokens, int top_k, int64_t hidden, int64_t rows_total,
-                        int64_t rows_per_expert, void* q, float* s, int64_t ld_s, hipStream_t stream) {
+                        int64_t rows_per_expert, void* q, float* s, int64_t ld_s, float* s_tmp, hipStream_t stream) {
   DispatchParams p{};
   p.x = x; p.rows = rows; p.sources = sources; p.m_indices = m_indices;
   p.tokens = (int)tokens; p.top_k = top_k; p.hidden = (int)hidden;
   p.rows_total = (int)rows_total; p.rows_per_expert = (int)rows_per_expert;
-  p.q = q; p.s = s; p.ld_s = ld_s;
+  p.q = q; p.s = s; p.ld_s = ld_s; p.s_tmp = s_tmp;
   switch (form) {
     case kFp8: return launch_dispatch_form<kFp8>(p, dtype, stream);
     case kInt8: return launch_dispatch_form<kInt8>(p, dtype, stream);

@@ -387,6 +387,8 @@ int dg_moe_layout(const int32_t* ids, int64_t tokens, int64_t top_k, int64_t exp
  *   dg_moe_dispatch_fp8   q: E4M3 bytes, sa: the activation scales of dg_quantize_per_token_group for the
  *                         same matrices (contiguous: sa[kb * ld_sa + row]; masked: per expert), bit for bit;
  *   dg_moe_dispatch_int8  q, s: as dg_quantize_int8_per_token gives them, s fp32 (rows_total,).
+ * workspace (FP8) : optional, dg_moe_dispatch_fp8_workspace_size bytes of any content (0: none is used);
+ *   without it the same bits, slower where there are many scales.  Calls that share it must be ordered.
  * The gradient with respect to x is dg_moe_combine of the rows' gradients without weights.
  * Errors: DG_ERR_INVALID_ARG as above, hidden not a positive multiple of 16, ld_sa too small or not a
  * multiple of 4.
@@ -396,7 +398,9 @@ int dg_moe_dispatch(const void* x, int dtype, const int32_t* rows, const int32_t
                     void* out, dg_stream_t stream);
 int dg_moe_dispatch_fp8(const void* x, int dtype, const int32_t* rows, const int32_t* sources, const int32_t* m_indices,
                         int64_t tokens, int64_t top_k, int64_t hidden, int64_t rows_total, int64_t rows_per_expert,
-                        uint8_t* q, float* sa, int64_t ld_sa, dg_stream_t stream);
+                        uint8_t* q, float* sa, int64_t ld_sa, void* workspace, size_t workspace_bytes,
+                        dg_stream_t stream);
+size_t dg_moe_dispatch_fp8_workspace_size(int64_t tokens, int64_t top_k, int64_t hidden);
 int dg_moe_dispatch_int8(const void* x, int dtype, const int32_t* rows, const int32_t* sources,
                          const int32_t* m_indices, int64_t tokens, int64_t top_k, int64_t hidden, int64_t rows_total,
                          int64_t rows_per_expert, int8_t* q, float* s, dg_stream_t stream);

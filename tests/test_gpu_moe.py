@@ -287,6 +287,32 @@ def test_dispatch(tokens, top_k, experts, per, hidden, dtype):
     assert np.all(gq[~owned] == 0x55) and np.all(gs[~owned] == 5) and torch.all(sa[..., lead[-1]:] == 5)
 
 
+@pytest.mark.parametrize("tokens,top_k,experts,per,hidden", [(4097, 8, 20, 0, 1040), (700, 6, 9, 0, 8400), (3000, 3, 7, 999, 4112)])
+def test_dispatch_of_many_scales(tokens, top_k, experts, per, hidden):
+    """With its workspace the FP8 form moves the scales in a launch of their own: the same bits as without."""
+    rng = np.random.default_rng(tokens)
+    ids = make_ids(rng, tokens, top_k, experts, 0.5)
+    x = dev(rng.standard_normal((tokens, hidden)), BF16)
+    say("dispatch of many scales", tokens, top_k, experts, per, hidden)
+    lay = dg.dg_moe_layout(dev(ids), experts, rows_per_expert=per)
+    need = dg.dg_moe_dispatch_fp8_workspace_size(tokens, top_k, hidden)
+    assert need > 0
+    lead, kb = lay.lead(), -(-hidden // 128)
+    got = []
+    for ws in (torch.full((need,), 0xFF, dtype=torch.uint8, device=device()), torch.empty(0, dtype=torch.uint8, device=device())):
+        q = torch.full((*lead, hidden), 0x55, dtype=torch.uint8, device=device())
+        sa = torch.full((*lead[:-1], kb, dg.dg_get_scale_ld(lead[-1])), 5.0, device=device())
+        got.append(dg.dg_moe_dispatch_fp8(x, lay, q=q, sa=sa, workspace=ws))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    wq, ws = dg.dg_quantize_per_token_group(x)
+    for t, k in ((0, 0), (tokens - 1, top_k - 1), (tokens // 2, 1)):
+        r = int(lay.rows[t, k])
+        if r >= 0:
+            sa = got[0][1].view(-1, kb, got[0][1].shape[-1])
+            g, at = (r // per, r % per) if per else (0, r)
+            assert torch.equal(sa[g, :, at], ws[:, t]) and torch.equal(got[0][0].view(-1, hidden)[r], wq[t])
+
+
 @pytest.mark.parametrize("tokens,top_k,experts,per,hidden", ROWS)
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_combine_and_gradients(tokens, top_k, experts, per, hidden, dtype):

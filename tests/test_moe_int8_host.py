@@ -73,10 +73,12 @@ def test_dispatch_and_combine_refusals(lib):
         assert disp(**bad) == INVALID, bad
     assert disp(total=0, t=0, x=None, out=None) == OK
 
-    def fp8(ld=1024, s=P, per=0, mi=P, total=1024):
-        return lib.dg_moe_dispatch_fp8(P, 1, P, P, mi, 4, 2, 64, total, per, P, s, ld, None)
+    def fp8(ld=1024, s=P, per=0, mi=P, total=1024, ws=None):
+        return lib.dg_moe_dispatch_fp8(P, 1, P, P, mi, 4, 2, 64, total, per, P, s, ld, ws, 0, None)
 
-    for bad in (dict(ld=1020), dict(ld=1026), dict(s=None), dict(per=32, mi=None, ld=28)):
+    assert dg.dg_moe_dispatch_fp8_workspace_size(4, 2, 64) == 0 and dg.dg_moe_dispatch_fp8_workspace_size(4, 2, 60) == 0
+    assert dg.dg_moe_dispatch_fp8_workspace_size(1 << 16, 8, 7168) == (1 << 16) * 56 * 4
+    for bad in (dict(ws=MIS), dict(ld=1020), dict(ld=1026), dict(s=None), dict(per=32, mi=None, ld=28)):
         assert fp8(**bad) == INVALID, bad
     assert lib.dg_moe_dispatch_int8(P, 1, P, P, P, 4, 2, 64, 1024, 0, P, None, None) == INVALID
 
