@@ -26,7 +26,7 @@ struct RouteParams {
   int groups, group_size, topk_groups, group_top;
   uint32_t group_magic;   // ceil(2^20 / group_size): e * magic >> 20 = e / group_size for e < 1024
   int lanes_per_group;    // 64 / (groups rounded up to a power of two)
-  int softmax, renorm;
+  int renorm;
   float scale;
   int32_t* ids;
   float* weights;
@@ -47,10 +47,13 @@ __device__ __forceinline__ uint32_t choice_key(float v) {
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
-// One wave per token; lane l holds experts l, l + 64, ... (coalesced reads; the lowest index of a tie
-// is the lowest register, then the lowest lane).
-template <class T, int C>
+// One wave per token; lane l holds experts l, l + 64, ... (coalesced reads).  What bounds it is the vector
+// unit: ~400 instructions a token for 256 experts, 8 groups and 8 choices, against 1 KB read.  So each lane
+// sorts its C experts once by (choice, lower index first), and a round of the top-k takes the maximum of
+// the lanes' heads, and pops one lane.
+template <class T, int C, bool SOFTMAX>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteParams p) {
+  constexpr float kOff = -__builtin_inff();
   __shared__ float s_value[kRouteWaves][64 * C];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -58,37 +61,48 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteParams p) 
   if (token >= p.tokens) return;   // wave-uniform; no workgroup barrier below
   const T* row = static_cast<const T*>(p.logits) + token * p.ld;
 
-  float x[C], value[C];
+  // every lane loads (an absent expert from the last one), so the loads are in flight together
+  float x[C], bias[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) x[c] = widen(row[64 * c + lane < p.experts ? 64 * c + lane : p.experts - 1]);
+#pragma unroll
+  for (int c = 0; c < C; ++c) bias[c] = 0.0f;
+  if (p.bias != nullptr) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) bias[c] = p.bias[64 * c + lane < p.experts ? 64 * c + lane : p.experts - 1];
+  }
+  // a NaN logit: not chosen, and every weight of the token is NaN
   bool nan = false;
-  float top = -__builtin_inff();
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int e = 64 * c + lane;
-    x[c] = e < p.experts ? widen(row[e]) : -__builtin_inff();
-    if (x[c] != x[c]) {   // a NaN logit: not chosen, and every weight of the token is NaN
-      nan = true;
-      x[c] = -__builtin_inff();
-    }
-    top = fmaxf(top, x[c]);
+    if (64 * c + lane >= p.experts) x[c] = kOff;
+    nan |= x[c] != x[c];
+    x[c] = x[c] != x[c] ? kOff : x[c];
   }
   // the softmax's maximum and sum, where a probability itself is needed
-  const bool by_logit = p.softmax && p.bias == nullptr && !(p.groups > 1 && p.group_top > 1);
-  float total = 1.0f;
-  if (p.softmax && (!by_logit || !p.renorm)) {
+  const bool by_logit = SOFTMAX && p.bias == nullptr && !(p.groups > 1 && p.group_top > 1);
+  float top = kOff, total = 1.0f;
+  if (SOFTMAX && (!by_logit || !p.renorm)) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) top = fmaxf(top, x[c]);
     for (int sh = 1; sh < 64; sh *= 2) top = fmaxf(top, __shfl_xor(top, sh));
     float sum = 0.0f;
 #pragma unroll
-    for (int c = 0; c < C; ++c) sum += x[c] == -__builtin_inff() ? 0.0f : expf(x[c] - top);
+    for (int c = 0; c < C; ++c) sum += x[c] == kOff ? 0.0f : expf(x[c] - top);
     total = wave_sum(sum);
   }
+  float value[C];
+  if (by_logit) {
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int e = 64 * c + lane;
-    const bool off = x[c] == -__builtin_inff();
-    float v = by_logit ? x[c] : p.softmax ? expf(x[c] - top) / total : sigmoid(x[c]);
-    if (p.bias != nullptr && e < p.experts) v += p.bias[e];
-    if (!off && v != v && !by_logit) nan = true;
-    value[c] = off || v != v ? -__builtin_inff() : v;
+    for (int c = 0; c < C; ++c) value[c] = x[c];
+  } else {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const float v = (SOFTMAX ? expf(x[c] - top) / total : sigmoid(x[c])) + bias[c];
+      const bool off = x[c] == kOff;
+      nan |= !off && v != v;
+      value[c] = off || v != v ? kOff : v;
+    }
   }
 
   if (p.groups > 1) {
@@ -100,11 +114,11 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteParams p) 
     wave_lds_fence();
     const int lpg = p.lanes_per_group;
     const int mine = lane / lpg, sub = lane - mine * lpg;
-    float t1 = -__builtin_inff(), t2 = -__builtin_inff();
+    float t1 = kOff, t2 = kOff;
     if (mine < p.groups) {
       for (int i = sub; i < p.group_size; i += lpg) {
         const float v = s_val[mine * p.group_size + i];
-        t2 = fmaxf(t2, fminf(t1, v));
+        t2 = __builtin_amdgcn_fmed3f(t1, t2, v);   // t2 <= t1: the second best of the three
         t1 = fmaxf(t1, v);
       }
     }
@@ -113,61 +127,81 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteParams p) 
       t2 = fmaxf(fminf(t1, o1), fmaxf(t2, o2));
       t1 = fmaxf(t1, o1);
     }
-    const float sum = p.group_top > 1 && t2 != -__builtin_inff() ? t1 + t2 : t1;
-    const uint32_t key = t1 == -__builtin_inff() || mine >= p.groups ? 0u : choice_key(sum);
+    const float sum = p.group_top > 1 && t2 != kOff ? t1 + t2 : t1;
+    const uint32_t key = t1 == kOff || mine >= p.groups ? 0u : choice_key(sum);
+    // lane (group, sub) compares its group with groups sub, sub + lpg, ...; the group's lanes' votes add up
     int ahead = 0;
-    for (int g = 0; g < p.groups; ++g) {
-      const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)key, g * lpg);
-      ahead += other > key || (other == key && g < mine);
+    const uint64_t own = ((lpg < 64 ? 1ull << lpg : 0ull) - 1) << (mine * lpg);
+    for (int g0 = 0; g0 < p.groups; g0 += lpg) {
+      const int g = g0 + sub;
+      const uint32_t other = __shfl(key, (g * lpg) & 63);
+      ahead += __popcll(__ballot(g < p.groups && (other > key || (other == key && g < mine))) & own);
     }
     const uint64_t kept = __ballot(ahead < p.topk_groups);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const uint32_t g = ((uint32_t)(64 * c + lane) * p.group_magic) >> 20;
-      if (!((kept >> ((g * lpg) & 63)) & 1)) value[c] = -__builtin_inff();
+      if (!((kept >> ((g * lpg) & 63)) & 1)) value[c] = kOff;
     }
   }
 
-  uint32_t key[C];
+  // (key, ~expert) pairs, the lane's best first: a sorting network of neighbour exchanges
+  uint32_t key[C], inv[C];
 #pragma unroll
-  for (int c = 0; c < C; ++c) key[c] = value[c] == -__builtin_inff() ? 0u : choice_key(value[c]);
+  for (int c = 0; c < C; ++c) {
+    key[c] = value[c] == kOff ? 0u : choice_key(value[c]);
+    inv[c] = ~(uint32_t)(64 * c + lane);
+  }
+#pragma unroll
+  for (int i = 1; i < C; ++i) {
+#pragma unroll
+    for (int j = i; j > 0; --j) {
+      // (of equal keys the earlier one has the lower index already: insertion keeps their order)
+      // (copies: a conditional of array elements would select the element's address)
+      const uint32_t ka = key[j - 1], kb = key[j], ia = inv[j - 1], ib = inv[j];
+      const bool swap = kb > ka;
+      key[j - 1] = swap ? kb : ka;
+      key[j] = swap ? ka : kb;
+      inv[j - 1] = swap ? ib : ia;
+      inv[j] = swap ? ia : ib;
+    }
+  }
 
-  // K rounds of the wave's maximum; lane j keeps the j-th choice
+  // top_k rounds over the lanes' heads; lane j keeps the j-th choice
   int id = -1;
   for (int j = 0; j < p.top_k; ++j) {
-    uint32_t best = key[0];
-#pragma unroll
-    for (int c = 1; c < C; ++c) best = umax(best, key[c]);
-    best = wave_max_u32(best);
+    const uint32_t best = wave_max_u32(key[0]);
     if (best == 0u) break;   // wave-uniform: no available expert is left
-    int pick = 0;
-    bool open = true;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const uint64_t has = __ballot(open && key[c] == best);
-      if (has != 0) {   // wave-uniform: the first register that holds the value
-        const int owner = __builtin_ctzll(has);
-        pick = 64 * c + owner;
-        if (lane == owner) key[c] = 0u;
-        open = false;
-      }
+    uint64_t has = __ballot(key[0] == best);
+    if (has & (has - 1)) {   // wave-uniform: a tie goes to the lowest index
+      const uint32_t low = wave_max_u32(key[0] == best ? inv[0] : 0u);
+      has = __ballot(key[0] == best && inv[0] == low);
     }
-    if (lane == j) id = pick;
+    const int owner = __builtin_ctzll(has);
+    const int pick = ~__builtin_amdgcn_readlane((int)inv[0], owner);
+    const bool pop = lane == owner;
+#pragma unroll
+    for (int c = 0; c + 1 < C; ++c) {
+      const uint32_t ka = key[c], kb = key[c + 1], ia = inv[c], ib = inv[c + 1];
+      key[c] = pop ? kb : ka;
+      inv[c] = pop ? ib : ia;
+    }
+    const uint32_t last = key[C - 1];
+    key[C - 1] = pop ? 0u : last;
+    id = lane == j ? pick : id;
   }
 
-  float s = 0.0f;
-  if (p.softmax) {
-    const float xk = id >= 0 ? widen(row[id]) : -__builtin_inff();
-    if (p.renorm) {
-      // over the chosen alone: relative to their own maximum, so none of their sums underflows
-      float m = xk;
-      for (int sh = 1; sh < 64; sh *= 2) m = fmaxf(m, __shfl_xor(m, sh));
-      s = id >= 0 ? expf(xk - m) : 0.0f;
-    } else {
-      s = id >= 0 ? expf(xk - top) / total : 0.0f;
-    }
-  } else if (id >= 0) {
-    s = sigmoid(widen(row[id]));
+  const float xk = id >= 0 ? widen(row[id]) : kOff;
+  float s;
+  if (!SOFTMAX) {
+    s = id >= 0 ? sigmoid(xk) : 0.0f;
+  } else if (p.renorm) {
+    // over the chosen alone: relative to their own maximum, so that their sum does not underflow
+    float m = xk;
+    for (int sh = 1; sh < 64; sh *= 2) m = fmaxf(m, __shfl_xor(m, sh));
+    s = id >= 0 ? expf(xk - m) : 0.0f;
+  } else {
+    s = id >= 0 ? expf(xk - top) / total : 0.0f;
   }
   float w = s;
   if (p.renorm) {
@@ -265,14 +299,18 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_grad_kernel(RouteGradP
 }
 
 
-template <class T>
+template <class T, bool SOFTMAX>
 static const void* route_fn(int experts) {
-  void (*fn)(RouteParams) = experts <= 64    ? route_kernel<T, 1>
-                            : experts <= 128 ? route_kernel<T, 2>
-                            : experts <= 256 ? route_kernel<T, 4>
-                            : experts <= 512 ? route_kernel<T, 8>
-                                             : route_kernel<T, 16>;
+  void (*fn)(RouteParams) = experts <= 64    ? route_kernel<T, 1, SOFTMAX>
+                            : experts <= 128 ? route_kernel<T, 2, SOFTMAX>
+                            : experts <= 256 ? route_kernel<T, 4, SOFTMAX>
+                            : experts <= 512 ? route_kernel<T, 8, SOFTMAX>
+                                             : route_kernel<T, 16, SOFTMAX>;
   return reinterpret_cast<const void*>(fn);
+}
+template <class T>
+static const void* route_fn(int experts, bool softmax) {
+  return softmax ? route_fn<T, true>(experts) : route_fn<T, false>(experts);
 }
 template <class T>
 static const void* route_grad_fn(int experts) {
@@ -302,10 +340,10 @@ int launch_route(const void* logits, int dtype, int64_t ld, const float* bias, i
   int pow2 = 1;
   while (pow2 < groups) pow2 *= 2;
   p.lanes_per_group = 64 / pow2;
-  p.softmax = softmax; p.renorm = renorm; p.scale = scale;
+  p.renorm = renorm; p.scale = scale;
   p.ids = ids; p.weights = weights;
-  const void* fn = dtype == kF32 ? route_fn<float>(experts) : dtype == kBf16 ? route_fn<Bf16>(experts)
-                                                                            : route_fn<_Float16>(experts);
+  const void* fn = dtype == kF32 ? route_fn<float>(experts, softmax) : dtype == kBf16 ? route_fn<Bf16>(experts, softmax)
+                                                                                     : route_fn<_Float16>(experts, softmax);
   void* args[] = {&p};
   return launched(fn, dim3((unsigned)((tokens + kRouteWaves - 1) / kRouteWaves)), dim3(64 * kRouteWaves), args, stream,
                   "moe_route");

@@ -97,10 +97,11 @@ __device__ __forceinline__ void store8(T* p, const Raw8<T>& r) {
   if constexpr (sizeof(T) == 4) reinterpret_cast<u32x4_t*>(p)[1] = r.w2;
 }
 
-// One lane's DPP partner under a compile-time control.
-template <int CTRL>
+// One lane's DPP partner under a compile-time control; lanes without one (ROWS: the rows that get one)
+// read 0, which lets the compiler fold the move into an unsigned maximum.
+template <int CTRL, int ROWS = 0xf>
 __device__ __forceinline__ uint32_t dpp_u32(uint32_t x) {
-  return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, CTRL, 0xf, 0xf, false);
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xf, false);
 }
 constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppHalfMirror = 0x141, kDppMirror = 0x140;
 
@@ -112,13 +113,14 @@ __device__ __forceinline__ uint32_t max8_u32(uint32_t v) {
   v = umax(v, dpp_u32<kDppXor2>(v));
   return umax(v, dpp_u32<kDppHalfMirror>(v));
 }
-// Maximum over the wave, as a wave-uniform (scalar) value.
+// Maximum over the wave, as a wave-uniform (scalar) value: within rows of 16 lanes, then each row's last
+// lane to the next row, then lane 31 to the upper half; lane 63 ends with all of it.
 __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
   v = max8_u32(v);
   v = umax(v, dpp_u32<kDppMirror>(v));
-  const uint32_t a = umax((uint32_t)__builtin_amdgcn_readlane((int)v, 0), (uint32_t)__builtin_amdgcn_readlane((int)v, 16));
-  const uint32_t b = umax((uint32_t)__builtin_amdgcn_readlane((int)v, 32), (uint32_t)__builtin_amdgcn_readlane((int)v, 48));
-  return umax(a, b);
+  v = umax(v, dpp_u32<0x142, 0xa>(v));   // row_bcast:15
+  v = umax(v, dpp_u32<0x143, 0xc>(v));   // row_bcast:31
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 // Sum over the wave in a fixed order, on every lane.
 __device__ __forceinline__ float wave_sum(float v) {

@@ -287,7 +287,9 @@ def test_dispatch(tokens, top_k, experts, per, hidden, dtype):
     assert np.all(gq[~owned] == 0x55) and np.all(gs[~owned] == 5) and torch.all(sa[..., lead[-1]:] == 5)
 
 
-@pytest.mark.parametrize("tokens,top_k,experts,per,hidden", [(4097, 8, 20, 0, 1040), (700, 6, 9, 0, 8400), (3000, 3, 7, 999, 4112)])
+@pytest.mark.parametrize("tokens,top_k,experts,per,hidden", [(4097, 8, 20, 0, 1040), (700, 6, 9, 0, 8400), (3000, 3, 7, 999, 4112),
+                                                              (8200, 8, 20, 0, 1040), (1500, 7, 9, 0, 8400),
+                                                              (6000, 3, 7, 1999, 4112)])
 def test_dispatch_of_many_scales(tokens, top_k, experts, per, hidden):
     """With its workspace the FP8 form moves the scales in a launch of their own: the same bits as without."""
     rng = np.random.default_rng(tokens)
@@ -296,7 +298,7 @@ def test_dispatch_of_many_scales(tokens, top_k, experts, per, hidden):
     say("dispatch of many scales", tokens, top_k, experts, per, hidden)
     lay = dg.dg_moe_layout(dev(ids), experts, rows_per_expert=per)
     need = dg.dg_moe_dispatch_fp8_workspace_size(tokens, top_k, hidden)
-    assert need > 0
+    assert need > 0 or tokens * top_k * -(-hidden // 128) < 1 << 19
     lead, kb = lay.lead(), -(-hidden // 128)
     got = []
     for ws in (torch.full((need,), 0xFF, dtype=torch.uint8, device=device()), torch.empty(0, dtype=torch.uint8, device=device())):
