@@ -66,28 +66,28 @@ struct I8Cfg {
   static_assert(kWaves == 8 && BN % 64 == 0 && BM % 64 == 0 && kFragN >= 3, "eight waves, at least three fragment rows");
 };
 
-// Four fp32 results of consecutive columns, rounded to the output's type.
-__device__ __forceinline__ void store_out4(void* d, int dtype, int64_t at, const float* v, int count, bool vec) {
+// The first `count` (at most 4) of four fp32 results of consecutive columns, rounded to the output's type;
+// four are stored together, whatever the row's alignment.
+__device__ __forceinline__ void store_out4(void* d, int dtype, int64_t at, const float* v, int count) {
+  typedef v4f F32x4 __attribute__((aligned(4)));
+  typedef u32x2_t Half4 __attribute__((aligned(2)));
   if (dtype == kF32) {
     float* o = static_cast<float*>(d) + at;
-    if (vec) *reinterpret_cast<v4f*>(o) = v4f{v[0], v[1], v[2], v[3]};
+    if (count >= 4) *reinterpret_cast<F32x4*>(o) = v4f{v[0], v[1], v[2], v[3]};
     else
       for (int i = 0; i < count; ++i) o[i] = v[i];
     return;
   }
-  uint32_t lo, hi;
-  if (dtype == kBf16) {
-    lo = pack2_bf16_rne(v[0], v[1]);
-    hi = pack2_bf16_rne(v[2], v[3]);
-  } else {
-    lo = pack2_f16(v[0], v[1]);
-    hi = pack2_f16(v[2], v[3]);
-  }
+  const u32x2_t h = dtype == kBf16 ? u32x2_t{pack2_bf16_rne(v[0], v[1]), pack2_bf16_rne(v[2], v[3])}
+                                   : u32x2_t{pack2_f16(v[0], v[1]), pack2_f16(v[2], v[3])};
   uint16_t* o = static_cast<uint16_t*>(d) + at;
-  if (vec) *reinterpret_cast<u32x2_t*>(o) = u32x2_t{lo, hi};
-  else {
-    const uint16_t h[4] = {(uint16_t)lo, (uint16_t)(lo >> 16), (uint16_t)hi, (uint16_t)(hi >> 16)};
-    for (int i = 0; i < count; ++i) o[i] = h[i];
+  if (count >= 4) {
+    *reinterpret_cast<Half4*>(o) = h;
+  } else {
+    const uint32_t w0 = h.x, w1 = h.y;
+    if (count > 0) o[0] = (uint16_t)w0;
+    if (count > 1) o[1] = (uint16_t)(w0 >> 16);
+    if (count > 2) o[2] = (uint16_t)w1;
   }
 }
 
@@ -372,69 +372,63 @@ __global__ __launch_bounds__(C::kThreads, 2 * C::OCC) void gemm_int8_kernel(I8Pa
 
     // ---- epilogue: scale, round, store --------------------------------------------------------------
     __syncthreads();   // every wave is done with the slots; the scales have landed
+    // an opaque copy of the lane: the epilogue's addresses are formed here, not kept in registers (256 a
+    // wave, most of them sums) across the main loop
+    int el = lane;
+    asm volatile("" : "+v"(el));
+    const int e16 = el & 15, e4 = el >> 4;
     auto scaled = [&](int i, int j, float* v) {
-      const float sr = s_scale[C::BN + wm0 + 16 * j + l16];
-      const v4f sc = *reinterpret_cast<const v4f*>(&s_scale[wn0 + 16 * i + 4 * g4]);
+      const float sr = s_scale[C::BN + wm0 + 16 * j + e16];
+      const v4f sc = *reinterpret_cast<const v4f*>(&s_scale[wn0 + 16 * i + 4 * e4]);
 #pragma unroll
       for (int r = 0; r < 4; ++r) v[r] = (float)acc[i][j][r] * (sr * sc[r]);
     };
-    if (p.out_dtype != kF32) {
-      // through LDS: each wave turns 16 output rows of its tile into whole row pieces (a fragment's own
-      // stores would touch 16 rows of 32 bytes each): of 16 bytes where the rows are 16-byte aligned,
-      // else of one element a lane, 64 consecutive ones an instruction
-      constexpr int kPitch = C::WN * 2 + 16;
-      constexpr int kPiecesRow = C::WN / 8, kPiecesLane = 16 * kPiecesRow / 64;
-      static_assert(C::kWaves * 16 * kPitch <= C::kStage, "the strips fit in one slot");
+    // Through LDS: each wave turns 16 output rows of its tile (fp32: of half its columns at a time) into
+    // row pieces of 16 bytes (a fragment's own stores would touch 16 rows of 32 or 64 bytes each).
+    auto store_rows = [&](auto size_c) {
+      constexpr int kSize = decltype(size_c)::value;   // bytes of an element
+      constexpr int kParts = kSize / 2, kCols = C::WN / kParts;
+      constexpr int kPitch = kCols * kSize + 16;
+      constexpr int kPiecesRow = kCols * kSize / 16, kPiecesLane = 16 * kPiecesRow / 64;
+      static_assert(C::kWaves * 16 * kPitch <= C::kStage && kFN % kParts == 0, "the strips fit in one slot");
       uint8_t* strip = st0 + wave * (16 * kPitch);
-      const bool aligned = (p.n & 7) == 0;
 #pragma unroll
-      for (int j = 0; j < kFM; ++j) {
+      for (int part = 0; part < kParts; ++part) {
 #pragma unroll
-        for (int i = 0; i < kFN; ++i) {
-          float v[4];
-          scaled(i, j, v);
-          u32x2_t h;
-          if (p.out_dtype == kBf16) h = u32x2_t{pack2_bf16_rne(v[0], v[1]), pack2_bf16_rne(v[2], v[3])};
-          else h = u32x2_t{pack2_f16(v[0], v[1]), pack2_f16(v[2], v[3])};
-          *reinterpret_cast<u32x2_t*>(strip + l16 * kPitch + (16 * i + 4 * g4) * 2) = h;
-        }
-        // the wave reads back what its own lanes wrote (its LDS operations complete in order)
-        uint16_t* out = static_cast<uint16_t*>(p.d);
-        if (aligned) {
+        for (int j = 0; j < kFM; ++j) {
+#pragma unroll
+          for (int i0 = 0; i0 < kFN / kParts; ++i0) {
+            float v[4];
+            scaled(part * (kFN / kParts) + i0, j, v);
+            uint8_t* at = strip + e16 * kPitch + (16 * i0 + 4 * e4) * kSize;
+            if constexpr (kSize == 4) *reinterpret_cast<v4f*>(at) = v4f{v[0], v[1], v[2], v[3]};
+            else if (p.out_dtype == kBf16)
+              *reinterpret_cast<u32x2_t*>(at) = u32x2_t{pack2_bf16_rne(v[0], v[1]), pack2_bf16_rne(v[2], v[3])};
+            else *reinterpret_cast<u32x2_t*>(at) = u32x2_t{pack2_f16(v[0], v[1]), pack2_f16(v[2], v[3])};
+          }
+          // the wave reads back what its own lanes wrote (its LDS operations complete in order)
+          uint8_t* out = static_cast<uint8_t*>(p.d);
+          const int row0 = m0 + wm0 + 16 * j, col0 = n0 + wn0 + part * kCols;
+          using E = std::conditional_t<kSize == 4, uint32_t, uint16_t>;
+          typedef u32x4 Piece __attribute__((aligned(2)));   // rows need no alignment past their elements'
+          constexpr int kElems = 16 / kSize;
 #pragma unroll
           for (int u = 0; u < kPiecesLane; ++u) {
-            const int c = lane + 64 * u;
+            const int c = el + 64 * u;
             const int row = c / kPiecesRow, cc = c % kPiecesRow;
-            const u32x4 val = *reinterpret_cast<const u32x4*>(strip + row * kPitch + cc * 16);
-            const int mrow = m0 + wm0 + 16 * j + row, ncol = n0 + wn0 + 8 * cc;
-            if ((!kTwoPass || mrow >= m_lo) && mrow < m_valid && ncol < p.n)
-              *reinterpret_cast<u32x4*>(out + (row_base + mrow) * p.n + ncol) = val;
-          }
-        } else {
-          for (int u = 0; u < 16 * C::WN / 64; ++u) {
-            const int row = 64 * u / C::WN, cc = 64 * u % C::WN + lane;
-            const uint16_t val = *reinterpret_cast<const uint16_t*>(strip + row * kPitch + cc * 2);
-            const int mrow = m0 + wm0 + 16 * j + row, ncol = n0 + wn0 + cc;
-            if ((!kTwoPass || mrow >= m_lo) && mrow < m_valid && ncol < p.n) out[(row_base + mrow) * p.n + ncol] = val;
+            const uint8_t* from = strip + row * kPitch + cc * 16;
+            const int mrow = row0 + row, ncol = col0 + cc * kElems;
+            if ((kTwoPass && mrow < m_lo) || mrow >= m_valid || ncol >= p.n) continue;
+            E* to = reinterpret_cast<E*>(out) + (row_base + mrow) * p.n + ncol;
+            if (ncol + kElems <= p.n) *reinterpret_cast<Piece*>(to) = *reinterpret_cast<const u32x4*>(from);
+            else   // the N edge inside a piece
+              for (int e = 0; e < p.n - ncol; ++e) to[e] = reinterpret_cast<const E*>(from)[e];
           }
         }
       }
-      continue;
-    }
-#pragma unroll
-    for (int j = 0; j < kFM; ++j) {
-      const int mrow = m0 + wm0 + 16 * j + l16;
-      if ((kTwoPass && mrow < m_lo) || mrow >= m_valid) continue;
-#pragma unroll
-      for (int i = 0; i < kFN; ++i) {
-        const int col = n0 + wn0 + 16 * i + 4 * g4;
-        const int count = p.n - col;
-        if (count <= 0) continue;
-        float v[4];
-        scaled(i, j, v);
-        store_out4(p.d, p.out_dtype, (row_base + mrow) * p.n + col, v, count < 4 ? count : 4, (p.n & 3) == 0);
-      }
-    }
+    };
+    if (p.out_dtype == kF32) store_rows(IC<4>{});
+    else store_rows(IC<2>{});
   }
 }
 
@@ -536,7 +530,7 @@ __device__ __forceinline__ void few_finish(const I8FewParams& p, const FewTile& 
     float v[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) v[r] = (float)sum[r] * (sr * (r < count ? sb[col + r] : 0.f));
-    store_out4(p.d, p.out_dtype, ((int64_t)t.g * p.m + row) * p.n + col, v, count < 4 ? count : 4, (p.n & 3) == 0);
+    store_out4(p.d, p.out_dtype, ((int64_t)t.g * p.m + row) * p.n + col, v, count);
   }
 }
 
