@@ -494,7 +494,8 @@ static int check_rows(const char* what, int dtype, const int32_t* rows, const in
              "%s: need tokens >= 0, 1 <= top_k <= 64, hidden > 0, hidden %% 16 == 0, rows_total >= 0 "
              "(tokens=%lld top_k=%lld hidden=%lld)", what, (long long)tokens, (long long)top_k, (long long)hidden);
   // tokens and rows each index a grid dimension with the padding's workgroups
-  DG_REQUIRE(tokens <= kInt31 / 2 && rows_total <= kInt31 && hidden <= kInt31 / 64, "%s: dimension too large", what);
+  DG_REQUIRE(tokens <= kInt31 / 2 && tokens * top_k <= kInt31 && rows_total <= kInt31 && hidden <= kInt31 / 64,
+             "%s: dimension too large", what);
   DG_REQUIRE(m_indices == nullptr || sources != nullptr, "%s: m_indices without sources", what);
   DG_REQUIRE(tokens == 0 || rows != nullptr, "%s: null pointer", what);
   DG_REQUIRE(aligned_to(rows, 4) && aligned_to(sources, 4) && aligned_to(m_indices, 4), "%s: misaligned pointer", what);

@@ -377,8 +377,9 @@ int launch_route_grad(const float* dweights, const void* logits, int dtype, int6
 // ---------------------------------------------------------------------------
 constexpr int kLayThreads = 512;
 constexpr int kLayWaves = kLayThreads / 64;
-constexpr int kLayChunk = 1024;   // entries per workgroup where there is more than one
 constexpr int kLayOnce = 2048;
+constexpr int kLayChunk = 1024;      // least entries per workgroup where there is more than one
+constexpr int kLayMostChunks = 256;  // every workgroup reads all their histograms
 
 struct LayoutParams {
   const int32_t* ids;
@@ -401,11 +402,12 @@ template <class F>
 __device__ __forceinline__ void for_entries(const LayoutParams& p, int begin, int end, int* s_next, F f) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int per_wave = ((end - begin + kLayWaves - 1) / kLayWaves + 63) & ~63;
-  const int w0 = begin + wave * per_wave;
-  const int w1 = w0 + per_wave < end ? w0 + per_wave : end;
-  for (int i0 = w0; i0 < w1; i0 += 64) {
+  // (differences, not sums: an index near 2^31 must not wrap)
+  const int w0 = end - begin > wave * per_wave ? begin + wave * per_wave : end;
+  const int w1 = end - w0 > per_wave ? w0 + per_wave : end;
+  for (int i0 = w0; i0 < w1; i0 = w1 - i0 > 64 ? i0 + 64 : w1) {
     const int i = i0 + lane;
-    int e = i < w1 ? p.ids[i] : -1;
+    int e = w1 - i0 > lane ? p.ids[i] : -1;
     if ((uint32_t)e >= (uint32_t)p.experts) e = -1;
     uint64_t same = __ballot(e >= 0);
     for (int bit = 1; bit < p.experts; bit *= 2) {
@@ -417,7 +419,7 @@ __device__ __forceinline__ void for_entries(const LayoutParams& p, int begin, in
     wave_lds_fence();
     if (e >= 0 && earlier == 0) s_next[e] = next + __popcll(same);
     wave_lds_fence();
-    if (i < w1) f(i, e, next + earlier);
+    if (w1 - i0 > lane) f(i, e, next + earlier);
   }
 }
 
@@ -432,7 +434,7 @@ __device__ __forceinline__ void count_entries(const LayoutParams& p, int begin, 
 __global__ __launch_bounds__(kLayThreads) void layout_count_kernel(LayoutParams p) {
   extern __shared__ int s_hist[];
   const int begin = blockIdx.x * p.chunk;
-  count_entries(p, begin, begin + p.chunk < p.n ? begin + p.chunk : p.n, s_hist);
+  count_entries(p, begin, p.n - begin < p.chunk ? p.n : begin + p.chunk, s_hist);
   for (int e = threadIdx.x; e < p.experts; e += kLayThreads) {
     int sum = 0;
     for (int w = 0; w < kLayWaves; ++w) sum += s_hist[w * p.experts + e];
@@ -450,9 +452,8 @@ __global__ __launch_bounds__(kLayThreads) void layout_place_kernel(LayoutParams 
   const int block = blockIdx.x;
   // this workgroup's chunk (with one chunk every workgroup counts it and the first one places it)
   const int chunk = p.blocks == 1 ? 0 : block;
-  int begin = chunk * p.chunk, end = begin + p.chunk;
-  if (begin > p.n) begin = p.n;
-  if (end > p.n) end = p.n;
+  const int begin = chunk < p.blocks ? chunk * p.chunk : p.n;
+  const int end = p.n - begin < p.chunk ? p.n : begin + p.chunk;
   count_entries(p, begin, end, s_hist);
 
   // ranks: entries of the expert in earlier chunks, then in this chunk's earlier waves
@@ -525,7 +526,12 @@ __global__ __launch_bounds__(kLayThreads) void layout_place_kernel(LayoutParams 
   }
 }
 
-static int layout_blocks(int64_t n) { return n <= kLayOnce ? 1 : (int)((n + kLayChunk - 1) / kLayChunk); }
+static int64_t layout_chunk(int64_t n) {
+  if (n <= kLayOnce) return kLayOnce;
+  const int64_t even = (n + kLayMostChunks - 1) / kLayMostChunks;
+  return even <= kLayChunk ? kLayChunk : (even + kLayThreads - 1) / kLayThreads * kLayThreads;
+}
+static int layout_blocks(int64_t n) { return n <= kLayOnce ? 1 : (int)((n + layout_chunk(n) - 1) / layout_chunk(n)); }
 
 size_t moe_layout_workspace_size(int64_t n, int64_t experts) {
   const int b = layout_blocks(n);
@@ -539,7 +545,7 @@ int launch_moe_layout(const int32_t* ids, int64_t n, int experts, int64_t rows_p
   p.ids = ids; p.n = (int)n; p.experts = experts;
   p.rows_per_expert = (int)rows_per_expert; p.align = align; p.rows_total = (int)rows_total;
   p.blocks = layout_blocks(n);
-  p.chunk = p.blocks > 1 ? kLayChunk : kLayOnce;
+  p.chunk = (int)layout_chunk(n);
   p.rows = rows; p.sources = sources; p.m_indices = m_indices; p.counts = counts;
   p.hist = static_cast<int32_t*>(ws);
   const size_t lds = (size_t)kLayWaves * experts * 4;
@@ -724,7 +730,7 @@ __global__ __launch_bounds__(256) void scale_rows_kernel(DispatchParams p) {
     const int src = r < p.rows_total ? p.sources[r] : -1;
     const bool pad = r < p.rows_total && src < 0 && p.m_indices != nullptr && p.m_indices[r] >= 0;
     // the row's token; -2: a padding row (scales 1); -1: not written (an entry past the tokens included)
-    s_src[lane] = pad ? -2 : (uint32_t)src < (uint32_t)p.tokens * (uint32_t)p.top_k ? src / p.top_k : -1;
+    s_src[lane] = pad ? -2 : src >= 0 && src < (int64_t)p.tokens * p.top_k ? src / p.top_k : -1;
   }
   __syncthreads();
   float v[kScaleTile / 4];   // every lane loads, all of a wave's rows in flight together

@@ -190,7 +190,7 @@ def make_ids(rng, tokens, top_k, experts, skew=0.0, dropped=0.1):
 LAYOUTS = [  # tokens, top_k, experts, rows_per_expert, skew
     (0, 2, 8, 0, 0.0), (1, 1, 1, 0, 0.0), (1, 8, 256, 0, 0.0), (3, 2, 5, 4, 0.0), (128, 1, 1, 0, 0.0), (129, 1, 1, 0, 0.0),
     (4095, 1, 7, 0, 1.0), (4097, 1, 3, 0, 0.0), (1024, 4, 64, 0, 1.1), (1025, 4, 64, 96, 1.1), (2731, 3, 1024, 0, 0.5),
-    (5000, 6, 1000, 8, 0.0), (700, 64, 129, 0, 0.3), (0, 1, 3, 5, 0.0)]
+    (5000, 6, 1000, 8, 0.0), (700, 64, 129, 0, 0.3), (0, 1, 3, 5, 0.0), (45000, 6, 37, 0, 0.8), (70001, 5, 300, 0, 0.2)]
 
 
 @pytest.mark.parametrize("tokens,top_k,experts,per,skew", LAYOUTS)
