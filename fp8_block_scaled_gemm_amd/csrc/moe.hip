@@ -512,7 +512,8 @@ __global__ __launch_bounds__(kLayThreads) void layout_place_kernel(LayoutParams 
 
   // every row's expert, and -1 for the rows that no entry fills (a row or two a thread)
   const int used = s_start[p.experts];
-  for (int r = block * kLayThreads + tid; r < p.rows_total; r += gridDim.x * kLayThreads) {
+  for (uint32_t at = block * kLayThreads + tid; at < (uint32_t)p.rows_total; at += gridDim.x * kLayThreads) {
+    const int r = (int)at;
     int lo = 0, hi = p.experts;   // s_start[lo] <= r < s_start[hi]
     if (r < used) {
       while (hi - lo > 1) {
