@@ -122,11 +122,15 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
   v = umax(v, dpp_u32<0x143, 0xc>(v));   // row_bcast:31
   return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
-// Sum over the wave in a fixed order, on every lane.
+// Sum over the wave in a fixed order (the steps of wave_max_u32), as a wave-uniform value.
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int sh = 1; sh < 64; sh *= 2) v += __shfl_xor(v, sh);
-  return v;
+  v += __uint_as_float(dpp_u32<kDppXor1>(__float_as_uint(v)));
+  v += __uint_as_float(dpp_u32<kDppXor2>(__float_as_uint(v)));
+  v += __uint_as_float(dpp_u32<kDppHalfMirror>(__float_as_uint(v)));
+  v += __uint_as_float(dpp_u32<kDppMirror>(__float_as_uint(v)));
+  v += __uint_as_float(dpp_u32<0x142, 0xa>(__float_as_uint(v)));
+  v += __uint_as_float(dpp_u32<0x143, 0xc>(__float_as_uint(v)));
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
 }
 
 // |x| as its bit pattern: as unsigned integers these order like the magnitudes, with a NaN above
