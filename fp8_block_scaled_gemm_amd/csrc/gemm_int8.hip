@@ -102,6 +102,13 @@ __device__ __forceinline__ void store_out4(void* d, int dtype, int64_t at, const
 // the freed slot, spread over the MFMAs of the last two rows, and have one block's compute to land.
 // The block body has no branch: past the last block the DMAs take out-of-range offsets and write zeros
 // that nothing reads.
+//
+// Bound by the matrix cores: 16384 x 7168 x 16384 runs at 2.70e15 operations/s (1424 us), 4096 x 4096 x 7168
+// at 2.45e15 (98 us, one round of 256 tiles: its first loads and its stores are not hidden).  The rate
+// depends on the operands' bits (zeros 3.2e15, random codes 2.7e15): power holds the clock, not the
+// instruction stream.  32x32x32 products in the place of
+// 16x16x64 ones ran at 2.53e15; a 256x128 tile was slower for the grouped forms; the smaller tile serves
+// launches that the square one leaves short of work (256 x 4096 x 7168: 21.6 us, split in four).
 // ---------------------------------------------------------------------------
 template <int V>
 using IC = std::integral_constant<int, V>;
@@ -433,13 +440,16 @@ __global__ __launch_bounds__(C::kThreads, 2 * C::OCC) void gemm_int8_kernel(I8Pa
 }
 
 // ---------------------------------------------------------------------------
-// Few rows (m <= 128): the weights are streamed once from memory and nothing else matters much.
-// A workgroup takes 16 R weight rows and 16 J activation rows; its W waves (and S workgroups of one
-// tile) split K between them.  Both operands go from memory straight into MFMA registers: a lane reads
-// 16 bytes of one row, so an instruction covers 16 rows x 64 bytes, and U steps of 64 K bytes are in
-// flight while the U before them are multiplied.  Rows past the edges take out-of-range addresses and
-// cost no traffic.  The waves' int32 partials are added in LDS with integer atomics, whose order does
-// not matter; the S partials of a tile go through the workspace to the workgroup that arrives last.
+// Few rows: the weights are streamed once from memory, and that is what bounds the kernel.  Two kernels, both
+// of them on tiles of 16 weight rows per wave and step, multiplied straight from the registers that memory
+// filled: a lane reads 16 bytes of one row, so an instruction covers 16 rows x 64 bytes of K.  The waves of
+// a workgroup (and S workgroups of one tile) split K; rows past the edges take out-of-range addresses and
+// cost no traffic.  The waves' int32 partials are added in LDS with integer atomics, whose order does not
+// matter; the S partials of a tile go through the workspace to the workgroup that arrives last.
+//  * direct: one or two unquantized rows, which every workgroup quantizes for itself while its first weights
+//    are on the way (1 x 4096 x 7168: 9.0 us, 3.3 TB/s of weights; 1 x 24576 x 1536: 10.3 us, 3.7 TB/s).
+//  * staged: the activations pass through LDS (64 x 4096 x 7168: 13.1 us; 64 x 7168 x 16384: 36.6 us,
+//    3.2 TB/s of weights).
 // ---------------------------------------------------------------------------
 struct I8FewParams {
   const int8_t* a;        // codes, or (with X) the unquantized activations
@@ -652,13 +662,12 @@ __global__ __launch_bounds__(64 * W) void gemm_int8_direct_kernel(I8FewParams p)
   });
 }
 
-// 17 to 128 rows: as above, but the activations pass through LDS.  Read by every wave straight from
-// memory they cost as many vector-memory requests as the weights (16 rows x 64 bytes an instruction),
-// and that request rate, not the bytes, bounds the kernel (64 x 7168 x 16384: 45 us, 31 us with the
-// activation reads masked off).  Here 2 times 16 weight rows each belong to 4 waves that share
-// their K chunk of 512 bytes, and the workgroup brings the chunk's 16 J activation rows in once, a whole
-// line per 8 lanes, through registers into one of two LDS buffers: one barrier per chunk, the next
-// chunk's weights and activations in flight across it.
+// The activations pass through LDS.  Read by every wave straight from memory they cost as many
+// vector-memory requests as the weights (16 rows x 64 bytes an instruction), and that request rate, not the
+// bytes, then bounds the kernel (64 x 7168 x 16384: 45 us so, 36.6 here).  Here 2 times 16 R weight rows
+// each belong to 4 waves that share their K chunk of 512 bytes (256 on 128-row tiles), and the workgroup
+// brings the chunk's 16 J activation rows in once, a whole line per 8 lanes, through registers into one of
+// two LDS buffers: one barrier per chunk, the next chunk's weights and activations in flight across it.
 constexpr int kStNS = 2, kStKS = 4;
 
 template <int R, int J, int CHUNK>
@@ -869,8 +878,8 @@ static int launch_few(const FewPlan& f, const void* fn, I8FewParams p, size_t ld
   return e == hipSuccess ? kOk : set_error(kHip, "int8 gemm launch: %s", hipGetErrorString(e));
 }
 
-// Time estimates (microseconds, MI355X, 256 CUs), fitted to timings of every choice on shapes of 192 to
-// 4096 rows.  A workgroup's K block takes longer the more of them run (they share caches and power); a
+// Time estimates (microseconds, MI355X, 256 CUs), fitted to timings of every choice on shapes of 1 to 4096
+// rows.  A workgroup's K block takes longer the more of them run (they share caches and power); a
 // tile costs a fixed part as well (first loads, stores); a K split sends its partials out and back.
 struct TileModel { int bn, bm, occ; double fixed, alone, busy; };
 constexpr TileModel kTileModel[kTiles] = {
@@ -940,8 +949,9 @@ static TilePlan tile_plan(int layout, int64_t m, int64_t n, int64_t k, int64_t g
     for (int splits = 1; splits <= kMaxSplits; ++splits) {
       const TilePlan t = tile_choice(tile, splits, layout, m, n, k, groups, num_cus);
       if (splits > 1) {
-        if (layout != kDense || !allow_split || t.kb_per_split < 4 || (splits <= 3 ? t.items > (int64_t)kTileModel[tile].occ * num_cus : 8 * t.items > 9 * (int64_t)num_cus) ||
-            t.items / t.splits > kMaxCounterTiles)
+        const bool crowded = splits <= 3 ? t.items > (int64_t)kTileModel[tile].occ * num_cus
+                                         : 8 * t.items > 9 * (int64_t)num_cus;
+        if (layout != kDense || !allow_split || t.kb_per_split < 4 || crowded || t.items / t.splits > kMaxCounterTiles)
           break;
         if (t.splits != splits) continue;   // the same as a smaller request
       }
@@ -1026,9 +1036,9 @@ int launch_gemm_int8(int layout, const int8_t* a, const float* sa, const int8_t*
                         static_cast<uint8_t*>(ws) + kCounterBytes, stream, num_cus);
 }
 
-// In-call quantization.  Up to kFewFusedRows rows whose codes fit in LDS are quantized by the product's
-// own workgroups; more rows by a launch of the quantizer into the workspace: the counter prefix, the
-// codes, the scales (256-byte pieces), then the K split's partials.
+// In-call quantization.  Up to kFewFusedRows rows of at most kFewFusedK elements are quantized by the
+// product's own workgroups; more rows by a launch of the quantizer into the workspace: the counter prefix,
+// the codes, the scales (256-byte pieces), then the K split's partials.
 static size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 static bool few_fused(int64_t m, int64_t k) { return m <= kFewFusedRows && k <= kFewFusedK; }
 

@@ -48,7 +48,8 @@ __device__ __forceinline__ uint32_t choice_key(float v) {
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
 // One wave per token; lane l holds experts l, l + 64, ... (coalesced reads).  What bounds it is the vector
-// unit: ~400 instructions a token for 256 experts, 8 groups and 8 choices, against 1 KB read.  So each lane
+// unit: ~690 instructions a token for 256 experts, 8 groups and 8 choices, against 1 KB read (16384 tokens:
+// 18.6 us; plain softmax 11.0; one token 4.2, a launch and two memory latencies).  So each lane
 // sorts its C experts once by (choice, lower index first), and a round of the top-k takes the maximum of
 // the lanes' heads, and pops one lane.
 template <class T, int C, bool SOFTMAX>
@@ -228,7 +229,11 @@ struct RouteGradParams {
 };
 
 // One wave per token.  The experts' choice is held fixed; only the softmax without renormalisation
-// needs the whole row of logits, every other form the K chosen ones.
+// needs the whole row of logits, every other form the K chosen ones:
+//   s = sigmoid(x) or exp(x - max), r = s / sum s, w = scale r:  dx = scale r (g - sum r g) [(1 - s) for sigmoid]
+//   w = scale s:  dx = scale g s (1 - s) for sigmoid; for softmax over the row, dx_e = p_e (u_e - sum p u), u = scale g.
+// Every element of the row is written (zeros where nothing was chosen), which bounds it: 16384 x 256 fp32
+// 8.8 us, 2.0 TB/s in these sizes' few microseconds; the full softmax 12.4.
 template <class T, int C>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_grad_kernel(RouteGradParams p) {
   const int lane = threadIdx.x & 63;

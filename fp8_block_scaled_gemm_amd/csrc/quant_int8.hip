@@ -9,7 +9,8 @@ namespace dg {
 
 // One workgroup of NT threads per row.  Each thread holds HOLD pieces of 8 elements in registers, so that a
 // row of up to 8 * NT * HOLD elements is read once; the rest of a longer row is read again (from the
-// caches) for its codes.
+// caches) for its codes.  Bound by memory: 16384 x 16384 bf16 139 us, 5.8 TB/s (some of the
+// row blocks come from the last-level cache).
 template <class T, int NT, int HOLD>
 __global__ __launch_bounds__(NT) void quant_int8_kernel(const T* __restrict__ x, int k, uint8_t* __restrict__ q,
                                                         float* __restrict__ s_out) {
