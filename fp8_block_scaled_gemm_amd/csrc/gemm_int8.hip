@@ -440,16 +440,22 @@ __global__ __launch_bounds__(C::kThreads, 2 * C::OCC) void gemm_int8_kernel(I8Pa
 }
 
 // ---------------------------------------------------------------------------
-// Few rows: the weights are streamed once from memory, and that is what bounds the kernel.  Two kernels, both
-// of them on tiles of 16 weight rows per wave and step, multiplied straight from the registers that memory
-// filled: a lane reads 16 bytes of one row, so an instruction covers 16 rows x 64 bytes of K.  The waves of
-// a workgroup (and S workgroups of one tile) split K; rows past the edges take out-of-range addresses and
-// cost no traffic.  The waves' int32 partials are added in LDS with integer atomics, whose order does not
-// matter; the S partials of a tile go through the workspace to the workgroup that arrives last.
+// Few rows: the weights are streamed once from memory, and that is what bounds the kernels.  Two of them, both
+// multiplying straight from the registers that memory filled; the waves of a workgroup (and S workgroups of
+// one tile) split K.  Rows past the edges take out-of-range addresses and cost no traffic.  The waves' int32
+// partials are added in LDS, the S partials of a tile go through the workspace to the workgroup that arrives
+// last; integers, so no order changes the result.
 //  * direct: one or two unquantized rows, which every workgroup quantizes for itself while its first weights
-//    are on the way (1 x 4096 x 7168: 9.0 us, 3.3 TB/s of weights; 1 x 24576 x 1536: 10.3 us, 3.7 TB/s).
-//  * staged: the activations pass through LDS (64 x 4096 x 7168: 13.1 us; 64 x 7168 x 16384: 36.6 us,
-//    3.2 TB/s of weights).
+//    are on the way (1 x 4096 x 7168: 8.2 us, 3.6 TB/s of weights; 1 x 24576 x 7168: 31.4 us, 5.6 TB/s).
+//  * staged: the activations pass through LDS (16 x 24576 x 7168: 29.0 us, 6.1 TB/s of weights; 64 rows 40.3,
+//    4.4 TB/s; 64 x 4096 x 7168: 13.0 us).
+//
+// A load of weights takes whole lines of 8 rows, lane (l16, g4) the 16 bytes 16 g4 + 64 (l16 / 8) of row
+// l16 % 8; two such loads (rows 0-7, rows 8-15) become two products' operands by exchanging half rows of
+// lanes, one move across lanes (row_ror:8) per register.  Half lines of 16 rows, which need no exchange, stream
+// at 4.0 TB/s where whole ones reach 5.9 (7168 x 16384, nothing but the loads).  Up to 32 rows the loads are
+// nontemporal, as a model's weights come from memory (16 x 7168 x 16384: 23.3 us, 25.4 without; where the
+// last-level cache holds them 21.7 and 20.4; more rows only lose by it, 128 x 4096 x 7168 18.0 and 20.2).
 // ---------------------------------------------------------------------------
 struct I8FewParams {
   const int8_t* a;        // codes, or (with X) the unquantized activations
@@ -461,7 +467,7 @@ struct I8FewParams {
   int m, n, k;
   int strips, mtiles;     // tiles of a group: ceil(n / 16R) x ceil(m / 16J)
   int splits;
-  int steps, steps_per_wave;
+  int all_chunks, chunks;   // of K, and of one split
   int out_dtype;
   int* ws;
   unsigned* counters;
@@ -499,6 +505,18 @@ __device__ __forceinline__ FewTile few_tile(const I8FewParams& p) {
   return t;
 }
 
+// The two loads' halves exchanged: w[h] holds K bytes 64 h + 16 g4 .. + 15 of the line, of row l16.
+constexpr int kNontemporal = 2;
+
+__device__ __forceinline__ void exchange_halves(const v4i (&x)[2], v4i (&w)[2]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int x0 = x[0][c], x1 = x[1][c];
+    w[0][c] = __builtin_amdgcn_update_dpp(x0, x1, 0x128, 0xf, 0xc, false);   // lanes 8-15 of each row: x1 of 8 before
+    w[1][c] = __builtin_amdgcn_update_dpp(x1, x0, 0x128, 0xf, 0x3, false);   // lanes 0-7: x0 of 8 after
+  }
+}
+
 // The workgroup's BM x BN sums in s_sum (rows of BN + 4, complete for its K range): added over the
 // tile's splits by the workgroup that arrives last, then scaled, rounded and stored.
 template <int BN, int BM, int NT, class RowScale>
@@ -526,20 +544,43 @@ __device__ __forceinline__ void few_finish(const I8FewParams& p, const FewTile& 
     if (!*s_last) return;
   }
   const float* sb = p.sb + (int64_t)t.g * p.n;
-  const __amdgpu_buffer_rsrc_t rs_ws =
-      make_rsrc(p.ws + (int64_t)t.id * p.splits * (BM * BN), p.splits > 1 ? (int64_t)p.splits * BM * BN * 4 : 0);
-  for (int c = tid; c < kChunks; c += NT) {
+  constexpr int kMine = (kChunks + NT - 1) / NT;   // pieces of this thread
+  v4i sum[kMine];
+#pragma unroll
+  for (int u = 0; u < kMine; ++u)
+    if (tid + NT * u < kChunks) sum[u] = *piece(tid + NT * u);
+  if (p.splits > 1) {
+    // the other splits' partials, eight loads together: one by one each costs a trip to memory
+    constexpr int kTogether = kMine >= 8 ? 1 : 8 / kMine;
+    const __amdgpu_buffer_rsrc_t rs_ws =
+        make_rsrc(p.ws + (int64_t)t.id * p.splits * (BM * BN), (int64_t)p.splits * BM * BN * 4);
+    for (int o0 = 0; o0 < p.splits; o0 += kTogether) {
+      v4i v[kTogether][kMine];
+#pragma unroll
+      for (int o = 0; o < kTogether; ++o)
+#pragma unroll
+        for (int u = 0; u < kMine; ++u) {
+          const int c = tid + NT * u;
+          const uint32_t out = o0 + o < p.splits && o0 + o != t.split && c < kChunks ? 0u : 0xFFFFFFF0u;   // zeros
+          v[o][u] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(
+                                                rs_ws, (uint32_t)(((o0 + o) * kChunks + c) * 16) | out, 0, kCpolSc1));
+        }
+#pragma unroll
+      for (int o = 0; o < kTogether; ++o)
+#pragma unroll
+        for (int u = 0; u < kMine; ++u) sum[u] += v[o][u];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kMine; ++u) {
+    const int c = tid + NT * u;
     const int row = t.m0 + c / (BN / 4), col = t.n0 + 4 * (c % (BN / 4));
     const int count = p.n - col;
-    if (row >= t.m_valid || count <= 0) continue;
-    v4i sum = *piece(c);
-    for (int o = 0; o < p.splits; ++o)
-      if (o != t.split)
-        sum += __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rs_ws, (o * kChunks + c) * 16, 0, kCpolSc1));
+    if (c >= kChunks || row >= t.m_valid || count <= 0) continue;
     const float sr = row_scale(row);
     float v[4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) v[r] = (float)sum[r] * (sr * (r < count ? sb[col + r] : 0.f));
+    for (int r = 0; r < 4; ++r) v[r] = (float)sum[u][r] * (sr * (r < count ? sb[col + r] : 0.f));
     store_out4(p.d, p.out_dtype, ((int64_t)t.g * p.m + row) * p.n + col, v, count);
   }
 }
@@ -561,34 +602,49 @@ __global__ __launch_bounds__(64 * W) void gemm_int8_direct_kernel(I8FewParams p)
   if (t.m0 >= t.m_valid) return;   // uniform, and so for every split of the tile
 
   const __amdgpu_buffer_rsrc_t rs_b = make_rsrc(p.b + (int64_t)t.n0 * p.k, (int64_t)(p.n - t.n0) * p.k);
-  const uint32_t row_off = (uint32_t)l16 * (uint32_t)p.k + 16u * g4;
-  const int s0 = (t.split * W + wave) * p.steps_per_wave;
-  const int s1 = s0 + p.steps_per_wave < p.steps ? s0 + p.steps_per_wave : p.steps;
+  const int line = 16 * g4 + 64 * (l16 >> 3);
+  const uint32_t row_off = (uint32_t)(l16 & 7) * (uint32_t)p.k + (uint32_t)line;
+  // the workgroup's `count` chunks from c0 on, a line of each for every wave
+  const int c0 = t.split * p.chunks;
+  const int count = c0 + p.chunks < p.all_chunks ? p.chunks : p.all_chunks - c0;
+  auto byte_of = [&](int i) { return (c0 + i) * (128 * W) + 128 * wave; };
 
-  struct Set { v4i b[U][R]; };
-  // U steps of 64 K bytes; chunks past K and steps past s1 take an out-of-range offset and read zeros
-  auto load = [&](Set& v, int s) {
+  struct Set { v4i b[U][R][2]; };
+  // U lines; pieces past K and past the workgroup's range take an out-of-range offset and read zeros
+  auto load = [&](Set& v, int i) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int k0 = 64 * (s + u);
-      const uint32_t out = s + u < s1 && k0 + 16 * g4 < p.k ? 0u : 0xFFFFFFF0u;
+      const int at = byte_of(i + u);
+      const uint32_t out = i + u < count && at + line < p.k ? 0u : 0xFFFFFFF0u;
 #pragma unroll
-      for (int i = 0; i < R; ++i)
-        v.b[u][i] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(
-                                                rs_b, (row_off + (uint32_t)(16 * i) * (uint32_t)p.k) | out, k0, 0));
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          v.b[u][r][h] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(
+                                                     rs_b, (row_off + (uint32_t)(16 * r + 8 * h) * (uint32_t)p.k) | out,
+                                                     at, kNontemporal));
     }
   };
   v4i acc[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) acc[i] = v4i{0, 0, 0, 0};
-  auto multiply = [&](const Set& v, int s) {
+  auto multiply = [&](const Set& v, int i) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int at = 64 * (s + u) + 16 * g4;
-      const v4i act = l16 < p.m && s + u < s1 && at < p.k ? *reinterpret_cast<const v4i*>(s_codes + l16 * p.k + at)
-                                                          : v4i{0, 0, 0, 0};
+      v4i act[2];
 #pragma unroll
-      for (int i = 0; i < R; ++i) acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(v.b[u][i], act, acc[i], 0, 0, 0);
+      for (int h = 0; h < 2; ++h) {
+        const int at = byte_of(i + u) + 64 * h + 16 * g4;
+        act[h] = l16 < p.m && i + u < count && at < p.k ? *reinterpret_cast<const v4i*>(s_codes + l16 * p.k + at)
+                                                        : v4i{0, 0, 0, 0};
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        v4i w[2];
+        exchange_halves(v.b[u][r], w);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) acc[r] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[h], act[h], acc[r], 0, 0, 0);
+      }
     }
   };
 
@@ -601,7 +657,7 @@ __global__ __launch_bounds__(64 * W) void gemm_int8_direct_kernel(I8FewParams p)
     for (int h = 0; h < kHold; ++h)
       if (r < p.m && 8 * (tid + NT * h) < p.k) held[r][h] = load8(x + (int64_t)r * p.k + 8 * (tid + NT * h));
   Set even, odd;
-  load(even, s0);
+  load(even, 0);
   for (int i = tid; i < BM * kPitch; i += NT) s_sum[i] = 0;
 #pragma unroll
   for (int r = 0; r < kFewFusedRows; ++r) {
@@ -639,12 +695,12 @@ __global__ __launch_bounds__(64 * W) void gemm_int8_direct_kernel(I8FewParams p)
     }
   }
   __syncthreads();
-  for (int s = s0; s < s1; s += 2 * U) {
-    load(odd, s + U);
-    multiply(even, s);
-    if (s + U >= s1) break;
-    load(even, s + 2 * U);
-    multiply(odd, s + U);
+  for (int i = 0; i < count; i += 2 * U) {
+    load(odd, i + U);
+    multiply(even, i);
+    if (i + U >= count) break;   // uniform
+    load(even, i + 2 * U);
+    multiply(odd, i + U);
   }
 
   // the waves' partials: integer atomics, whose order does not matter
@@ -662,25 +718,29 @@ __global__ __launch_bounds__(64 * W) void gemm_int8_direct_kernel(I8FewParams p)
   });
 }
 
-// The activations pass through LDS.  Read by every wave straight from memory they cost as many
-// vector-memory requests as the weights (16 rows x 64 bytes an instruction), and that request rate, not the
-// bytes, then bounds the kernel (64 x 7168 x 16384: 45 us so, 36.6 here).  Here 2 times 16 R weight rows
-// each belong to 4 waves that share their K chunk of 512 bytes (256 on 128-row tiles), and the workgroup
-// brings the chunk's 16 J activation rows in once, a whole line per 8 lanes, through registers into one of
-// two LDS buffers: one barrier per chunk, the next chunk's weights and activations in flight across it.
-constexpr int kStNS = 2, kStKS = 4;
+// NS x KS = 8 waves on 16 R NS weight rows and 16 J activation rows: wave (ns, kh) multiplies line kh of each
+// chunk of KS lines with its R fragment rows.
+//
+// Each strip starts its K range elsewhere: rows a power of two apart meet in the same channels otherwise
+// (16 x 7168 x 16384: 28.3 us, 23.5 so; other lengths are the same either way).
+//
+// Activations: through registers into one of two LDS buffers, one barrier a chunk, D - 1 chunks ahead.  They
+// come from L2, but a CU's loads return in order, behind the weights' trips to memory: with R NS small the
+// kernel waits for them (64 x 24576 x 7168: strips of 32 rows 51 us, 96 rows 38.7).
+constexpr int kStWaves = 8;
 
-template <int R, int J, int CHUNK>
-__global__ __launch_bounds__(64 * kStNS * kStKS) void gemm_int8_staged_kernel(I8FewParams p) {
-  constexpr int NS = kStNS, KS = kStKS, NT = 64 * NS * KS;
+template <int NS, int R, int J, int D, int W = kStWaves>
+__global__ __launch_bounds__(64 * W) void gemm_int8_staged_kernel(I8FewParams p) {
+  constexpr int KS = W / NS, NT = 64 * W;
   constexpr int BN = 16 * R * NS, BM = 16 * J;
-  constexpr int kPitch = CHUNK + 16;   // 16 rows of one 16-byte column fall in different banks
-  constexpr int U = CHUNK / 64 / KS;              // steps of 64 K bytes per wave and chunk
-  constexpr int kPieces = BM * CHUNK / 16 / NT;   // 16-byte pieces per thread and chunk
+  constexpr int kChunk = 128 * KS;
+  constexpr int kPitch = kChunk + 16;   // 16 rows of one 16-byte column fall in different banks
+  constexpr int kRowPieces = kChunk / 16;
+  constexpr int kPieces = (BM * kRowPieces + NT - 1) / NT;   // 16-byte pieces per thread and chunk
   constexpr int kBuf = BM * kPitch;
   constexpr int kSumPitch = BN + 4;
-  static_assert(kPieces * NT * 16 == BM * CHUNK && U * KS * 64 == CHUNK, "a chunk splits evenly");
   constexpr int kLds = 2 * kBuf > BM * kSumPitch * 4 ? 2 * kBuf : BM * kSumPitch * 4;
+  constexpr int kPolicy = J <= 2 ? kNontemporal : 0;
   __shared__ __attribute__((aligned(16))) uint8_t smem[kLds];
   __shared__ int s_last;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -692,77 +752,72 @@ __global__ __launch_bounds__(64 * kStNS * kStKS) void gemm_int8_staged_kernel(I8
 
   const __amdgpu_buffer_rsrc_t rs_b = make_rsrc(p.b + ((int64_t)t.g * p.n + t.n0) * p.k, (int64_t)(p.n - t.n0) * p.k);
   const __amdgpu_buffer_rsrc_t rs_a = make_rsrc(p.a + ((int64_t)t.g * p.m + t.m0) * p.k, (int64_t)(t.m_valid - t.m0) * p.k);
-  // steps_per_wave counts chunks here: the workgroup's chunks [c0, c1)
-  const int c0 = t.split * p.steps_per_wave;
-  const int c1 = c0 + p.steps_per_wave < p.steps ? c0 + p.steps_per_wave : p.steps;
+  // the workgroup's `count` chunks from c0 on, the strip's own one first
+  const int c0 = t.split * p.chunks;
+  const int count = c0 + p.chunks < p.all_chunks ? p.chunks : p.all_chunks - c0;
+  const int first = (t.n0 / BN) % count;
 
-  // this thread's activation pieces: row piece / 32, 16-byte column piece % 32 of the chunk
-  u32x4 act[kPieces];
-  auto load_act = [&](int c) {
+  struct Set { u32x4 act[kPieces]; v4i b[R][2]; };
+  const int line = 128 * kh + 16 * g4 + 64 * (l16 >> 3);
+  const uint32_t row_off = (uint32_t)(16 * R * ns + (l16 & 7)) * (uint32_t)p.k + (uint32_t)line;
+  auto load = [&](Set& v, int i) {   // the i-th chunk; past the last, and past K, zeros
+    const int at = (c0 + (i + first < count ? i + first : i + first - count)) * kChunk;
+    const uint32_t out_b = i < count && at + line < p.k ? 0u : 0xFFFFFFF0u;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        v.b[r][u] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(
+                                                rs_b, (row_off + (uint32_t)(16 * r + 8 * u) * (uint32_t)p.k) | out_b, at,
+                                                kPolicy));
 #pragma unroll
     for (int u = 0; u < kPieces; ++u) {
-      const int piece = tid + NT * u, row = piece / (CHUNK / 16), col = 16 * (piece % (CHUNK / 16));
-      const uint32_t out = c < c1 && c * CHUNK + col < p.k ? 0u : 0xFFFFFFF0u;   // past K: zeros
-      act[u] = __builtin_amdgcn_raw_buffer_load_b128(rs_a, ((uint32_t)row * (uint32_t)p.k + (uint32_t)col) | out,
-                                                     c * CHUNK, 0);
+      const int piece = tid + NT * u, row = piece / kRowPieces, col = 16 * (piece % kRowPieces);
+      const uint32_t out = i < count && at + col < p.k && row < BM ? 0u : 0xFFFFFFF0u;
+      v.act[u] = __builtin_amdgcn_raw_buffer_load_b128(rs_a, ((uint32_t)row * (uint32_t)p.k + (uint32_t)col) | out, at, 0);
     }
   };
-  auto store_act = [&](int c) {
+  auto store_act = [&](const Set& v, int parity) {
 #pragma unroll
     for (int u = 0; u < kPieces; ++u) {
-      const int piece = tid + NT * u, row = piece / (CHUNK / 16), col = 16 * (piece % (CHUNK / 16));
-      *reinterpret_cast<u32x4*>(smem + (c & 1) * kBuf + row * kPitch + col) = act[u];
-    }
-  };
-  struct Set { v4i b[U][R]; };
-  const uint32_t row_off = (uint32_t)(16 * R * ns + l16) * (uint32_t)p.k + 16u * g4;
-  auto load_b = [&](Set& v, int c) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k0 = c * CHUNK + 64 * (kh * U + u);
-      const uint32_t out = c < c1 && k0 + 16 * g4 < p.k ? 0u : 0xFFFFFFF0u;
-#pragma unroll
-      for (int i = 0; i < R; ++i)
-        v.b[u][i] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(
-                                                rs_b, (row_off + (uint32_t)(16 * i) * (uint32_t)p.k) | out, k0, 0));
+      const int piece = tid + NT * u, row = piece / kRowPieces, col = 16 * (piece % kRowPieces);
+      if (BM * kRowPieces >= NT || row < BM)
+        *reinterpret_cast<u32x4*>(smem + parity * kBuf + row * kPitch + col) = v.act[u];
     }
   };
   v4i acc[R][J];
 #pragma unroll
-  for (int i = 0; i < R; ++i)
+  for (int r = 0; r < R; ++r)
 #pragma unroll
-    for (int j = 0; j < J; ++j) acc[i][j] = v4i{0, 0, 0, 0};
-  auto multiply = [&](const Set& v, int c) {
-    const uint8_t* base = smem + (c & 1) * kBuf + l16 * kPitch + 64 * kh * U + 16 * g4;
+    for (int j = 0; j < J; ++j) acc[r][j] = v4i{0, 0, 0, 0};
+  auto multiply = [&](const Set& v, int parity) {
+    const uint8_t* base = smem + parity * kBuf + l16 * kPitch + 128 * kh + 16 * g4;
+    v4i w[R][2];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      v4i fa[J];
+    for (int r = 0; r < R; ++r) exchange_halves(v.b[r], w[r]);
 #pragma unroll
-      for (int j = 0; j < J; ++j) fa[j] = *reinterpret_cast<const v4i*>(base + 16 * j * kPitch + 64 * u);
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int i = 0; i < R; ++i)
+      for (int j = 0; j < J; ++j) {
+        const v4i fa = *reinterpret_cast<const v4i*>(base + 16 * j * kPitch + 64 * u);
 #pragma unroll
-        for (int j = 0; j < J; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(v.b[u][i], fa[j], acc[i][j], 0, 0, 0);
-    }
+        for (int r = 0; r < R; ++r) acc[r][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[r][u], fa, acc[r][j], 0, 0, 0);
+      }
   };
 
-  // one chunk of weights and activations ahead (two or three ahead measured the same or slower);
-  // chunks past c1 read nothing
-  Set even, odd;
-  load_act(c0);
-  load_b(even, c0);
-  for (int c = c0; c < c1; c += 2) {
-    store_act(c);
-    load_act(c + 1);
-    load_b(odd, c + 1);
-    __syncthreads();   // chunk c is in its buffer; every wave is done with chunk c - 1's
-    multiply(even, c);
-    if (c + 1 >= c1) break;   // uniform
-    store_act(c + 1);
-    load_act(c + 2);
-    load_b(even, c + 2);
-    __syncthreads();
-    multiply(odd, c + 1);
+  Set set[D];
+#pragma unroll
+  for (int d = 0; d < D - 1; ++d) load(set[d], d);
+  constexpr int kUnroll = D % 2 ? 2 * D : D;   // both the set and the buffer of a step are fixed
+  for (int i0 = 0; i0 < count; i0 += kUnroll) {
+#pragma unroll
+    for (int d = 0; d < kUnroll; ++d) {
+      if (i0 + d >= count) break;   // uniform
+      store_act(set[d % D], d & 1);
+      load(set[(d + D - 1) % D], i0 + d + D - 1);
+      __syncthreads();   // this chunk is in its buffer; every wave is done with the one before
+      multiply(set[d % D], d & 1);
+    }
   }
 
   __syncthreads();   // the buffers become the sums
@@ -773,9 +828,9 @@ __global__ __launch_bounds__(64 * kStNS * kStKS) void gemm_int8_staged_kernel(I8
 #pragma unroll
       for (int j = 0; j < J; ++j)
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-          v4i* at = reinterpret_cast<v4i*>(&s_sum[(16 * j + l16) * kSumPitch + 16 * (R * ns + i) + 4 * g4]);
-          *at = h == 0 ? acc[i][j] : *at + acc[i][j];
+        for (int r = 0; r < R; ++r) {
+          v4i* at = reinterpret_cast<v4i*>(&s_sum[(16 * j + l16) * kSumPitch + 16 * (R * ns + r) + 4 * g4]);
+          *at = h == 0 ? acc[r][j] : *at + acc[r][j];
         }
     }
     __syncthreads();
@@ -791,74 +846,113 @@ using I8Small = I8Cfg<128, 128, 64, 32, 2>;
 enum I8Tile : int { kSquare = 0, kSmall, kTiles };
 
 struct FewPlan {
-  bool direct;
-  int r, j, waves, unit;   // unit: K bytes of a step (direct) or chunk (staged)
+  int ns, r, j, waves, unit;   // unit: K bytes of a chunk, one or more lines for each wave
   int bn, bm;
-  int strips, mtiles, splits, steps, steps_per_wave;
+  int strips, mtiles, splits;
+  int all_chunks, chunks;   // of K, and of one split
   int64_t tiles;
   size_t ws_bytes;
 };
 
-// Few-row plan.  `direct`: the kernel that quantizes its rows itself.  What the choices measured:
-//  * direct, waves a workgroup (they share K): 1 x 24576 x 1536 takes 10.3 us with 4, 13.9 with 8, 16.3
-//    with 16; 1 x 4096 x 7168 9.0 with 8, 9.9 with 16; K past 8192 needs 16 to hold the row.
-//  * direct, 32 weight rows a workgroup where that still gives ~3/4 of a workgroup per CU: 1 x 7168 x 2048
-//    5.2 us against 5.7 with 16.
-//  * staged, 128-row tiles: chunks of 256 (two workgroups' buffers fit a CU): 128 x 24576 x 1536 23.0 us,
-//    two 64-row tiles 26.4; 32 weight rows a wave once K is long enough to pay for splitting it:
-//    128 x 7168 x 16384 45.7 us against 52.9 with 16.
-static FewPlan few_plan(bool direct, int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus, bool allow_split) {
+// The tiles and the split of K into at most `want` parts, none empty.
+static void few_grid(FewPlan* f, int64_t m, int64_t n, int64_t k, int64_t groups, int64_t want) {
+  f->bn = 16 * f->r * f->ns;
+  f->bm = 16 * f->j;
+  f->strips = (int)((n + f->bn - 1) / f->bn);
+  f->mtiles = (int)((m + f->bm - 1) / f->bm);
+  f->tiles = (int64_t)f->strips * f->mtiles * groups;
+  f->all_chunks = (int)((k + f->unit - 1) / f->unit);
+  f->chunks = (int)((f->all_chunks + want - 1) / want);
+  f->splits = (f->all_chunks + f->chunks - 1) / f->chunks;
+  f->ws_bytes = f->splits > 1 ? kCounterBytes + (size_t)f->tiles * f->splits * f->bn * f->bm * 4 : 0;
+}
+
+// The kernel that quantizes its rows itself.  What the choices measured: waves a workgroup (they share K):
+// 1 x 24576 x 1536 takes 9.7 us with 4, 12.2 with 8, 17.1 with 16; 1 x 4096 x 7168 8.5 with 8, 9.3 with 16;
+// the row has to fit the threads' registers, 1024 elements a wave.  32 weight rows a workgroup where that still
+// gives ~3/4 of a workgroup per CU: 1 x 24576 x 7168 30.6 us, 36.2 with 16; 1 x 4096 x 7168 10.6 and 8.5.  K is not
+// split over workgroups: each would quantize the row again (1 x 2112 x 7168 7.8 us whole, 10.8 in two).
+static FewPlan direct_plan(int64_t m, int64_t n, int64_t k, int num_cus) {
   FewPlan f{};
-  f.direct = direct;
-  if (direct) {
-    f.j = 1;
-    f.r = n >= (int64_t)24 * num_cus ? 2 : 1;
-    f.waves = k <= 4096 ? 4 : k <= 8192 ? 8 : 16;
-    f.unit = 64;
-  } else {
-    f.j = m <= 16 ? 1 : m <= 32 ? 2 : m <= 64 ? 4 : 8;
-    f.r = f.j == 8 && k >= 8192 && n >= (int64_t)24 * num_cus ? 2 : 1;
-    f.waves = kStNS * kStKS;
-    f.unit = f.j == 8 ? 256 : 512;
-  }
-  f.bn = 16 * f.r * (direct ? 1 : kStNS);
-  f.bm = 16 * f.j;
-  f.strips = (int)((n + f.bn - 1) / f.bn);
-  f.mtiles = (int)((m + f.bm - 1) / f.bm);
-  f.tiles = (int64_t)f.strips * f.mtiles * groups;
-  const int sharing = direct ? f.waves : 1;   // units of K go to waves (direct) or to workgroups (staged)
-  f.steps = (int)((k + f.unit - 1) / f.unit);
-  // split K until there is about one workgroup per CU, each keeping a few units (64 x 4096 x 7168:
-  // unsplit 128 workgroups 20 us, split in two 13.1, in four 15.5)
-  int64_t want = (2 * (int64_t)num_cus / f.tiles + 1) / 2;
-  const int64_t most = f.steps / (direct ? 4 * sharing : 2);
-  if (want > most) want = most;
-  if (want > kMaxSplits) want = kMaxSplits;
-  if (!allow_split || want < 1 || f.tiles > kMaxCounterTiles) want = 1;
-  f.steps_per_wave = (int)((f.steps + want * sharing - 1) / (want * sharing));
-  f.splits = (int)((f.steps + (int64_t)f.steps_per_wave * sharing - 1) / ((int64_t)f.steps_per_wave * sharing));   // none empty
-  f.ws_bytes = f.splits > 1 ? kCounterBytes + (size_t)f.tiles * f.splits * f.bn * f.bm * 4 : 0;
+  f.ns = 1;
+  f.j = 1;
+  f.r = n >= (int64_t)24 * num_cus ? 2 : 1;
+  f.waves = k <= 4096 ? 4 : k <= 8192 ? 8 : 16;
+  f.unit = 128 * f.waves;
+  few_grid(&f, m, n, k, 1, 1);
   return f;
 }
 
-static const void* staged_fn(const FewPlan& f) {
-  void (*fn)(I8FewParams) = f.j == 1   ? gemm_int8_staged_kernel<1, 1, 512>
-                            : f.j == 2 ? gemm_int8_staged_kernel<1, 2, 512>
-                            : f.j == 4 ? gemm_int8_staged_kernel<1, 4, 512>
-                            : f.r == 1 ? gemm_int8_staged_kernel<1, 8, 256>
-                                       : gemm_int8_staged_kernel<2, 8, 256>;
+// Joining K splits: the partials' way to the workspace and back, and three trips to memory in turn.
+static double few_split_time(const FewPlan& f) {
+  return f.splits > 1 ? 1.5 + 0.2 * f.splits + 0.15e-6 * (double)f.tiles * f.splits * f.bn * f.bm * 4 : 0.0;
+}
+
+// Time estimate (microseconds, MI355X): a fixed part, and per K byte what the fullest CU's workgroups load and
+// multiply, fitted to 16, 32 and 64 rows by 4096 x 7168 ... 24576 x 7168 over every tile and split below.
+static double few_time(const FewPlan& f, int64_t n, int64_t k, int64_t groups, int num_cus) {
+  const double c = (double)((f.tiles * f.splits + num_cus - 1) / num_cus);
+  const double per_byte = f.bn * (0.0322 + 0.000183 * f.bm) + 0.0098 * f.bm;
+  const double loads = c * 1e-3 * f.chunks * f.unit * per_byte, memory = (double)groups * n * k / 5.9e6;
+  return 4.0 + (loads > memory ? loads : memory) + few_split_time(f);
+}
+
+// Strips of 32 to 128 weight rows: wide ones read the activations less often, narrow ones need less of a K
+// split to fill the chip (its join costs 2-4 us).  64 rows, fastest split: 24576 x 7168 51.1 us with 32, 45
+// with 64, 38.7 with 96, 40.7 with 128; 4096 x 7168 14.2, 13.5, 16.4, 17.6; 7168 x 2048 8.3, 10.2, 12.5, 12.6.
+// D: 3 pays where a wave keeps one fragment row and a workgroup has the chunks (16 x 4096 x 7168 10.8 -> 10.2 us;
+// 64 x 7168 x 2048, four chunks, 8.3 -> 9.1).
+static FewPlan staged_plan(int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus, bool allow_split) {
+  static constexpr struct { int ns, r; } kStrips[] = {{2, 1}, {4, 1}, {2, 3}, {4, 2}};
+  FewPlan best{};
+  double best_us = 0.0;
+  for (const auto& strip : kStrips) {
+    FewPlan f{};
+    f.j = m <= 16 ? 1 : m <= 32 ? 2 : m <= 64 ? 4 : 8;
+    if (f.j == 8 && strip.r == 3) continue;   // (never measured faster)
+    f.ns = strip.ns; f.r = strip.r;
+    // up to 16 rows and long K: one strip of two fragment rows, K over all eight waves (16 x 7168 x 16384
+    // 25.3 -> 23.1 us; 16 x 4096 x 7168 10.2 -> 10.5)
+    if (f.j == 1 && f.ns * f.r == 2 && k > 8192) f.ns = 1, f.r = 2;
+    f.waves = f.j == 8 && f.ns == 2 ? kStWaves / 2 : kStWaves;   // (two workgroups' buffers fit a CU)
+    f.unit = 128 * (f.waves / f.ns);
+    for (int want = 1; want <= kMaxSplits; ++want) {
+      few_grid(&f, m, n, k, groups, want);
+      if (want > 1 && (!allow_split || f.tiles > kMaxCounterTiles || f.chunks < 2)) break;
+      const double us = few_time(f, n, k, groups, num_cus);
+      if (best_us == 0.0 || us <= best_us) best = f, best_us = us;   // (of equals, bound by memory, the widest)
+    }
+  }
+  return best;
+}
+
+template <int J>
+static const void* staged_fn_of(const FewPlan& f) {
+  const bool deep = f.chunks >= 7;
+  void (*fn)(I8FewParams);
+  if (f.ns == 4)
+    fn = f.r == 2 ? gemm_int8_staged_kernel<4, 2, J, 2> : deep ? gemm_int8_staged_kernel<4, 1, J, J < 8 ? 3 : 2>
+                                                              : gemm_int8_staged_kernel<4, 1, J, 2>;
+  else if constexpr (J == 8)
+    fn = gemm_int8_staged_kernel<2, 1, 8, 2, kStWaves / 2>;
+  else
+    fn = f.ns == 1 ? gemm_int8_staged_kernel<1, 2, 1, 2> : f.r == 3 ? gemm_int8_staged_kernel<2, 3, J, 2>
+         : deep ? gemm_int8_staged_kernel<2, 1, J, 3> : gemm_int8_staged_kernel<2, 1, J, 2>;
   return reinterpret_cast<const void*>(fn);
+}
+static const void* staged_fn(const FewPlan& f) {
+  return f.j == 1 ? staged_fn_of<1>(f) : f.j == 2 ? staged_fn_of<2>(f) : f.j == 4 ? staged_fn_of<4>(f) : staged_fn_of<8>(f);
 }
 
 template <class X>
 static const void* direct_fn_of(const FewPlan& f) {
   void (*fn)(I8FewParams);
   if (f.r == 1)
-    fn = f.waves == 4 ? gemm_int8_direct_kernel<1, 8, 4, X> : f.waves == 8 ? gemm_int8_direct_kernel<1, 8, 8, X>
-                                                                           : gemm_int8_direct_kernel<1, 8, 16, X>;
+    fn = f.waves == 4 ? gemm_int8_direct_kernel<1, 4, 4, X> : f.waves == 8 ? gemm_int8_direct_kernel<1, 4, 8, X>
+                                                                           : gemm_int8_direct_kernel<1, 4, 16, X>;
   else
-    fn = f.waves == 4 ? gemm_int8_direct_kernel<2, 4, 4, X> : f.waves == 8 ? gemm_int8_direct_kernel<2, 4, 8, X>
-                                                                           : gemm_int8_direct_kernel<2, 4, 16, X>;
+    fn = f.waves == 4 ? gemm_int8_direct_kernel<2, 2, 4, X> : f.waves == 8 ? gemm_int8_direct_kernel<2, 2, 8, X>
+                                                                           : gemm_int8_direct_kernel<2, 2, 16, X>;
   return reinterpret_cast<const void*>(fn);
 }
 static const void* direct_fn(const FewPlan& f, int dtype) {
@@ -868,7 +962,7 @@ static const void* direct_fn(const FewPlan& f, int dtype) {
 static int launch_few(const FewPlan& f, const void* fn, I8FewParams p, size_t lds, int64_t groups, void* counters,
                       void* partials, hipStream_t stream) {
   p.strips = f.strips; p.mtiles = f.mtiles; p.splits = f.splits;
-  p.steps = f.steps; p.steps_per_wave = f.steps_per_wave;
+  p.all_chunks = f.all_chunks; p.chunks = f.chunks;
   p.counters = static_cast<unsigned*>(counters);
   p.ws = static_cast<int*>(partials);
   const int64_t blocks = groups * ((((int64_t)f.strips * f.splits + 7) & ~(int64_t)7) * f.mtiles);
@@ -887,15 +981,6 @@ constexpr TileModel kTileModel[kTiles] = {
     {I8Small::BN, I8Small::BM, I8Small::OCC, 3.5, 0.5, 1.15}};
 
 static double split_time(int splits, double partial_bytes) { return 3.0 + 0.5 * splits + 0.22e-6 * partial_bytes; }
-
-// Few-row tiles: the time of a chunk (512 bytes of K, 256 on 128-row tiles) with one workgroup a CU, and
-// per workgroup of the fullest CU.
-static double few_time(const FewPlan& f, int num_cus) {
-  const double c = (double)((f.tiles * f.splits + num_cus - 1) / num_cus);
-  const double one = f.j == 8 ? 0.8 * f.r : 0.95, more = f.j == 8 ? 0.7 * f.r : f.j == 4 ? 1.0 : 0.87;
-  const double t = 3.5 + f.steps_per_wave * (c * more > one ? c * more : one);
-  return t + (f.splits > 1 ? split_time(f.splits, (double)f.tiles * f.splits * f.bn * f.bm * 4) : 0.0);
-}
 
 struct TilePlan {
   int tile;
@@ -927,8 +1012,8 @@ static TilePlan tile_choice(int tile, int splits, int layout, int64_t m, int64_t
   const double full = (double)(int64_t)(items / slots), rest = items - full * slots;
   t.us = full * (c.fixed + t.kb_per_split * c.busy);
   if (rest > 0) t.us += c.fixed + t.kb_per_split * (c.alone + (c.busy - c.alone) * rest / slots);
-  // the weights come from memory at 5 TB/s at best, and at 17 GB/s for each workgroup
-  const double rate = items * 0.017e6 < 5.0e6 ? items * 0.017e6 : 5.0e6;
+  // the weights come from memory at 5.6 TB/s at best, and at 17 GB/s for each workgroup
+  const double rate = items * 0.017e6 < 5.6e6 ? items * 0.017e6 : 5.6e6;
   const double weights = c.fixed + (double)n * k * (layout == kDense ? 1 : groups) / rate;
   if (t.us < weights) t.us = weights;
   if (t.splits > 1) {
@@ -984,9 +1069,9 @@ struct I8Plan {
 static I8Plan int8_plan(int layout, int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus, bool allow_split) {
   I8Plan p{};
   p.few = layout != kContiguous && m <= kFewRowsMost;
-  if (p.few) p.f = few_plan(false, m, n, k, groups, num_cus, allow_split);
+  if (p.few) p.f = staged_plan(m, n, k, groups, num_cus, allow_split);
   p.t = tile_plan(layout, m, n, k, groups, num_cus, allow_split);
-  p.few = p.few && few_time(p.f, num_cus) < p.t.us;
+  p.few = p.few && few_time(p.f, n, k, groups, num_cus) < p.t.us;
   return p;
 }
 
@@ -1043,10 +1128,7 @@ static size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 static bool few_fused(int64_t m, int64_t k) { return m <= kFewFusedRows && k <= kFewFusedK; }
 
 size_t int8_act_quant_workspace_size(int64_t m, int64_t n, int64_t k, int num_cus) {
-  if (few_fused(m, k)) {
-    const size_t split = few_plan(true, m, n, k, 1, num_cus, true).ws_bytes;
-    return split > 0 ? split : kCounterBytes;
-  }
+  if (few_fused(m, k)) return kCounterBytes;   // (not used)
   const size_t split = int8_workspace_size(m, n, k, 1, num_cus);
   return kCounterBytes + align256((size_t)(m * k)) + align256((size_t)m * 4) + (split > 0 ? split - kCounterBytes : 0);
 }
@@ -1056,11 +1138,11 @@ int launch_gemm_int8_act_quant(const void* x, int dtype, const int8_t* b, const 
                                int num_cus) {
   (void)ws_bytes;   // checked by the caller against int8_act_quant_workspace_size
   if (few_fused(m, k)) {
-    const FewPlan f = few_plan(true, m, n, k, 1, num_cus, true);
+    const FewPlan f = direct_plan(m, n, k, num_cus);
     I8FewParams p{};
     p.a = static_cast<const int8_t*>(x); p.b = b; p.sb = sb; p.d = d;
     p.m = (int)m; p.n = (int)n; p.k = (int)k; p.out_dtype = out_dtype;
-    return launch_few(f, direct_fn(f, dtype), p, (size_t)(m * k), 1, ws, static_cast<uint8_t*>(ws) + kCounterBytes, stream);
+    return launch_few(f, direct_fn(f, dtype), p, (size_t)(m * k), 1, nullptr, nullptr, stream);
   }
   uint8_t* w = static_cast<uint8_t*>(ws);
   uint8_t* codes = w + kCounterBytes;

@@ -190,6 +190,27 @@ def test_under_a_cu_cap():
         dg.dg_set_num_cus(cus)
 
 
+@pytest.mark.parametrize("m", [3, 16, 20, 32, 50, 64, 100, 128])
+@pytest.mark.parametrize("n,k", [(1029, 2064), (390, 8336)])
+def test_few_rows_on_every_strip_width(m, n, k):
+    """The plans for fewer compute units take wider strips of the weights and other splits of K."""
+    rng = np.random.default_rng(m + n)
+    (a, sa), (b, sb) = codes(rng, m, k), codes(rng, n, k)
+    want = oracle.int8.gemm_nt(a, sa, b, sb)
+    args = [dev(v) for v in (a, sa, b, sb)]
+    cus = dg.dg_get_num_cus()
+    try:
+        for cap in (1, 2, 4, 8, 11, 16, 32, cus):
+            say("int8 gemm of few rows, strips under a CU cap", m, n, k, cap)
+            dg.dg_set_num_cus(cap)
+            for use in (True, False):
+                d = torch.full((m, n), float("nan"), device=device())
+                dg.dg_gemm_int8_nt(*args, d=d, use_workspace=use)
+                check(d, want)
+    finally:
+        dg.dg_set_num_cus(cus)
+
+
 def test_results_past_32_bit_offsets():
     m, n, k = 40000, 32768, 16
     say("int8 gemm, results past 32-bit offsets", m, n, k)
