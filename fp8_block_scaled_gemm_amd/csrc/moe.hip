@@ -802,11 +802,15 @@ int launch_moe_dispatch(int form, const void* x, int dtype, const int32_t* rows,
 // ---------------------------------------------------------------------------
 // Combine: y[t] = sum over k of w[t, k] * rows[row(t, k)], in fp32, in the order of k.
 //
-// It reads K rows for one written: bound by memory reads.  4096 tokens x 8 rows of 7168 bf16: 110 us,
-// 4.8 TB/s; 16384 x 2 of 1024: 20.2 us, 5.0 TB/s (a large copy reaches 5.1).
+// It reads K rows for one written: bound by memory reads.  4096 tokens x 8 rows of 7168 bf16: 96 us, 5.5 TB/s;
+// 16384 x 2 of 1024: 20.2 us, 5.0 TB/s (a large copy reaches 5.1, a large read 6 to 7).
 // ---------------------------------------------------------------------------
 constexpr int kCombThreads = 128;
 constexpr int kCombBatch = 8;   // expert rows whose loads are in flight together
+
+// Rows that the last-level cache cannot hold are read with nontemporal loads (4096 tokens x 8 of 7168 bf16, 470 MB:
+// combine 109.5 us, 95.8 with them; 2048 x 8 of 7168, 235 MB: 40.6 and 48.3 when the rows are there).
+constexpr int64_t kCacheBytes = 256 << 20;
 
 struct CombineParams {
   const void* out;
@@ -820,7 +824,7 @@ struct CombineParams {
 // B rows' loads are in flight together.  They are unconditional (a branch around a load makes it wait for
 // the ones before it: 4093 tokens x 6 of 2048, 33.3 us, 29.9 without): a place without a row reads the
 // token's first one again, or the output's row.
-template <class T, int B>
+template <class T, int B, bool NT>
 __global__ __launch_bounds__(kCombThreads) void combine_kernel(CombineParams p) {
   const int token = blockIdx.x;
   const int i = 8 * (blockIdx.y * kCombThreads + threadIdx.x);
@@ -837,7 +841,7 @@ __global__ __launch_bounds__(kCombThreads) void combine_kernel(CombineParams p) 
     for (int u = 0; u < B; ++u) row[u] = k0 + u < p.top_k ? row_at(rows, k0 + u, p.rows_total) : -1;
     const T* spare = row[0] >= 0 ? out + (int64_t)row[0] * p.hidden : y;
 #pragma unroll
-    for (int u = 0; u < B; ++u) v[u] = load8((row[u] >= 0 ? out + (int64_t)row[u] * p.hidden : spare) + i);
+    for (int u = 0; u < B; ++u) v[u] = load8<NT>((row[u] >= 0 ? out + (int64_t)row[u] * p.hidden : spare) + i);
 #pragma unroll
     for (int u = 0; u < B; ++u) {
       if (row[u] >= 0) {
@@ -852,12 +856,16 @@ __global__ __launch_bounds__(kCombThreads) void combine_kernel(CombineParams p) 
   store8(y + i, narrow8<T>(acc));
 }
 
-template <int B>
+template <int B, bool NT>
 static const void* combine_fn(int dtype) {
-  void (*fn)(CombineParams) = dtype == kF32    ? combine_kernel<float, B>
-                              : dtype == kBf16 ? combine_kernel<Bf16, B>
-                                               : combine_kernel<_Float16, B>;
+  void (*fn)(CombineParams) = dtype == kF32    ? combine_kernel<float, B, NT>
+                              : dtype == kBf16 ? combine_kernel<Bf16, B, NT>
+                                               : combine_kernel<_Float16, B, NT>;
   return reinterpret_cast<const void*>(fn);
+}
+template <bool NT>
+static const void* combine_fn(int dtype, int top_k) {
+  return top_k <= 2 ? combine_fn<2, NT>(dtype) : top_k <= 4 ? combine_fn<4, NT>(dtype) : combine_fn<kCombBatch, NT>(dtype);
 }
 
 int launch_moe_combine(const void* out, int dtype, const int32_t* rows, const float* weights, int64_t tokens, int top_k,
@@ -866,8 +874,9 @@ int launch_moe_combine(const void* out, int dtype, const int32_t* rows, const fl
   p.rows_total = (int)rows_total;
   p.out = out; p.rows = rows; p.weights = weights;
   p.tokens = (int)tokens; p.top_k = top_k; p.hidden = (int)hidden; p.y = y;
+  const bool nontemporal = tokens * top_k * hidden * (dtype == kF32 ? 4 : 2) > kCacheBytes;
   void* args[] = {&p};
-  return launched(top_k <= 2 ? combine_fn<2>(dtype) : top_k <= 4 ? combine_fn<4>(dtype) : combine_fn<kCombBatch>(dtype),
+  return launched(nontemporal ? combine_fn<true>(dtype, top_k) : combine_fn<false>(dtype, top_k),
                   dim3((unsigned)tokens, (unsigned)((hidden + 8 * kCombThreads - 1) / (8 * kCombThreads))),
                   dim3(kCombThreads), args, stream, "moe_combine");
 }
@@ -875,7 +884,7 @@ int launch_moe_combine(const void* out, int dtype, const int32_t* rows, const fl
 // Gradient of the weighted combine: dout[row(t, k)] = w[t, k] dy[t] (padding rows 0) and
 // dw[t, k] = <dy[t], out[row(t, k)]>; a token a wave or a workgroup, as in dispatch (16384 tokens x 2 of 1024
 // bf16: 58.9 us with a workgroup each, 35.2 with a wave).  Bound by memory, half of it writes: that call moves
-// 4.8 TB/s, 4096 x 8 of 7168 (217 us) 4.6 without counting the padding rows' zeros.
+// 4.8 TB/s, 4096 x 8 of 7168 (218 us) 4.6 without counting the padding rows' zeros.
 struct CombineGradParams {
   DispatchParams pad;    // q = dout; for the padding rows
   const void* dy;
@@ -885,7 +894,7 @@ struct CombineGradParams {
   float* dweights;
 };
 
-template <class T, int LT>
+template <class T, int LT, bool NT>
 __global__ __launch_bounds__(kRowThreads) void combine_grad_kernel(CombineGradParams p) {
   constexpr int kTokens = kRowThreads / LT;
   __shared__ float s_sum[kRowThreads / 64][64];
@@ -921,7 +930,7 @@ __global__ __launch_bounds__(kRowThreads) void combine_grad_kernel(CombineGradPa
       Raw8<T> v[kCombBatch];
 #pragma unroll
       for (int u = 0; u < kCombBatch; ++u)
-        if (row[u] >= 0) v[u] = load8(out + (int64_t)row[u] * hidden + i);
+        if (row[u] >= 0) v[u] = load8<NT>(out + (int64_t)row[u] * hidden + i);
       widen8(dg, g);
 #pragma unroll
       for (int u = 0; u < kCombBatch; ++u) {
@@ -951,12 +960,16 @@ __global__ __launch_bounds__(kRowThreads) void combine_grad_kernel(CombineGradPa
   if (lane < top_k) p.dweights[(int64_t)token * top_k + lane] = mine;   // (top_k <= 64: lane is wave_lane)
 }
 
-template <int LT>
+template <int LT, bool NT>
 static const void* combine_grad_fn(int dtype) {
-  void (*fn)(CombineGradParams) = dtype == kF32    ? combine_grad_kernel<float, LT>
-                                  : dtype == kBf16 ? combine_grad_kernel<Bf16, LT>
-                                                   : combine_grad_kernel<_Float16, LT>;
+  void (*fn)(CombineGradParams) = dtype == kF32    ? combine_grad_kernel<float, LT, NT>
+                                  : dtype == kBf16 ? combine_grad_kernel<Bf16, LT, NT>
+                                                   : combine_grad_kernel<_Float16, LT, NT>;
   return reinterpret_cast<const void*>(fn);
+}
+template <int LT>
+static const void* combine_grad_fn(int dtype, bool nontemporal) {
+  return nontemporal ? combine_grad_fn<LT, true>(dtype) : combine_grad_fn<LT, false>(dtype);
 }
 
 int launch_moe_combine_grad(const void* dy, const void* out, int dtype, const int32_t* rows, const int32_t* sources,
@@ -967,12 +980,13 @@ int launch_moe_combine_grad(const void* dy, const void* out, int dtype, const in
   p.pad.tokens = (int)tokens; p.pad.top_k = top_k; p.pad.hidden = (int)hidden;
   p.pad.rows_total = (int)rows_total; p.pad.q = dout;
   p.dy = dy; p.out = out; p.weights = weights; p.dout = dout; p.dweights = dweights;
+  const bool nontemporal = 2 * tokens * top_k * hidden * (dtype == kF32 ? 4 : 2) > kCacheBytes;   // rows and their gradients
   const int64_t pad = m_indices != nullptr ? (rows_total + kPadRows - 1) / kPadRows : 0;
   const bool narrow_rows = hidden <= kNarrowRow;
   const int64_t blocks = narrow_rows ? (tokens + 3) / 4 : tokens;
   if (blocks + pad == 0) return kOk;
   void* args[] = {&p};
-  return launched(narrow_rows ? combine_grad_fn<64>(dtype) : combine_grad_fn<256>(dtype), dim3((unsigned)(blocks + pad)),
+  return launched(narrow_rows ? combine_grad_fn<64>(dtype, nontemporal) : combine_grad_fn<256>(dtype, nontemporal), dim3((unsigned)(blocks + pad)),
                   dim3(kRowThreads), args, stream, "moe_combine_grad");
 }
 

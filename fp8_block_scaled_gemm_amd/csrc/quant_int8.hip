@@ -9,8 +9,8 @@ namespace dg {
 
 // One workgroup of NT threads per row.  Each thread holds HOLD pieces of 8 elements in registers, so that a
 // row of up to 8 * NT * HOLD elements is read once; the rest of a longer row is read again (from the
-// caches) for its codes.  Bound by memory: 16384 x 16384 bf16 139 us, 5.8 TB/s (some of the
-// row blocks come from the last-level cache).
+// caches) for its codes.  Bound by memory: 32768 x 7168 bf16 142 us, 5.0 TB/s;
+// 65536 x 2048 fp32 115 us, 5.9 TB/s (nontemporal loads of rows past the last-level cache: 2% of that, either way).
 template <class T, int NT, int HOLD>
 __global__ __launch_bounds__(NT) void quant_int8_kernel(const T* __restrict__ x, int k, uint8_t* __restrict__ q,
                                                         float* __restrict__ s_out) {

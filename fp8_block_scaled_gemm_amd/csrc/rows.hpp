@@ -39,11 +39,17 @@ struct Raw8 { u32x4_t w; };
 template <>
 struct Raw8<float> { u32x4_t w, w2; };
 
-template <class T>
+template <bool NONTEMPORAL = false, class T>
 __device__ __forceinline__ Raw8<T> load8(const T* p) {
+  const u32x4_t* w = reinterpret_cast<const u32x4_t*>(p);
   Raw8<T> r;
-  r.w = reinterpret_cast<const u32x4_t*>(p)[0];
-  if constexpr (sizeof(T) == 4) r.w2 = reinterpret_cast<const u32x4_t*>(p)[1];
+  if constexpr (NONTEMPORAL) {
+    r.w = __builtin_nontemporal_load(w);
+    if constexpr (sizeof(T) == 4) r.w2 = __builtin_nontemporal_load(w + 1);
+  } else {
+    r.w = w[0];
+    if constexpr (sizeof(T) == 4) r.w2 = w[1];
+  }
   return r;
 }
 
