@@ -883,16 +883,17 @@ static FewPlan direct_plan(int64_t m, int64_t n, int64_t k, int num_cus) {
   return f;
 }
 
-// Joining K splits: the partials' way to the workspace and back, and three trips to memory in turn.
+// Joining K splits: three trips to memory in turn, and a tile's partials through one workgroup at 70 B/ns.
 static double few_split_time(const FewPlan& f) {
-  return f.splits > 1 ? 1.5 + 0.2 * f.splits + 0.15e-6 * (double)f.tiles * f.splits * f.bn * f.bm * 4 : 0.0;
+  return f.splits > 1 ? 1.5 + 0.2 * f.splits + f.splits * (double)(f.bn * f.bm * 4) / 70e3 : 0.0;
 }
 
 // Time estimate (microseconds, MI355X): a fixed part, and per K byte what the fullest CU's workgroups load and
 // multiply, fitted to 16, 32 and 64 rows by 4096 x 7168 ... 24576 x 7168 over every tile and split below.
 static double few_time(const FewPlan& f, int64_t n, int64_t k, int64_t groups, int num_cus) {
   const double c = (double)((f.tiles * f.splits + num_cus - 1) / num_cus);
-  const double per_byte = f.bn * (0.0322 + 0.000183 * f.bm) + 0.0098 * f.bm;
+  const double wide = f.j == 8 ? 1.15 : 1.0;   // (16 KB of sums a wave, one workgroup's buffers a CU)
+  const double per_byte = wide * (f.bn * (0.0322 + 0.000183 * f.bm) + 0.0098 * f.bm);
   const double loads = c * 1e-3 * f.chunks * f.unit * per_byte, memory = (double)groups * n * k / 5.9e6;
   return 4.0 + (loads > memory ? loads : memory) + few_split_time(f);
 }
@@ -980,7 +981,7 @@ constexpr TileModel kTileModel[kTiles] = {
     {I8Square::BN, I8Square::BM, I8Square::OCC, 7.0, 0.9, 1.6},
     {I8Small::BN, I8Small::BM, I8Small::OCC, 3.5, 0.5, 1.15}};
 
-static double split_time(int splits, double partial_bytes) { return 3.0 + 0.5 * splits + 0.22e-6 * partial_bytes; }
+static double split_time(int splits, double partial_bytes) { return 1.5 + 1.1 * splits + 0.07e-6 * partial_bytes; }
 
 struct TilePlan {
   int tile;
@@ -1034,8 +1035,7 @@ static TilePlan tile_plan(int layout, int64_t m, int64_t n, int64_t k, int64_t g
     for (int splits = 1; splits <= kMaxSplits; ++splits) {
       const TilePlan t = tile_choice(tile, splits, layout, m, n, k, groups, num_cus);
       if (splits > 1) {
-        const bool crowded = splits <= 3 ? t.items > (int64_t)kTileModel[tile].occ * num_cus
-                                         : 8 * t.items > 9 * (int64_t)num_cus;
+        const bool crowded = t.items > (int64_t)(splits <= 3 ? kTileModel[tile].occ : 1) * num_cus;
         if (layout != kDense || !allow_split || t.kb_per_split < 4 || crowded || t.items / t.splits > kMaxCounterTiles)
           break;
         if (t.splits != splits) continue;   // the same as a smaller request
