@@ -4,7 +4,9 @@
  * The method: FP8 (E4M3) matrix multiplication with DeepSeek-V3 style
  * fine-grained scaling and two-level (promoted) FP32 accumulation, in three
  * forms - a normal GEMM, a contiguous-grouped MoE GEMM and a masked-grouped
- * MoE GEMM.  Sources (DeepGEMM news/blog pages):
+ * MoE GEMM.  Beside them (end of this file): expert routing, the expert row
+ * layout with dispatch and combine, and the three forms in 8-bit integers.
+ * Sources (DeepGEMM news/blog pages):
  *   - 机器之心 DeepGEMM report, opening section: fine-grained scaling as in
  *     DeepSeek-V3; normal and MoE grouped GEMMs; two-level accumulation on
  *     the general-purpose cores because FP8 tensor-core accumulation is
