@@ -657,13 +657,24 @@ __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(DispatchParams p)
     }
   } else if constexpr (FORM == kInt8) {
     uint8_t* out = static_cast<uint8_t*>(p.q);
+    // a lane's first 16 elements stay in registers; those of longer rows are read again, from the caches
+    Raw8<T> held[2];
     uint32_t amax = 0;
-    for (int i = 16 * lane; i < p.hidden; i += 16 * LT) {
+    auto largest = [&](const Raw8<T> (&r)[2]) {
       float v[16];
-      widen8(load8(src + i), v);
-      widen8(load8(src + i + 8), v + 8);
+      widen8(r[0], v);
+      widen8(r[1], v + 8);
 #pragma unroll
       for (int u = 0; u < 16; ++u) amax = umax(amax, abs_bits(v[u]));
+    };
+    if (16 * lane < p.hidden) {
+      held[0] = load8(src + 16 * lane);
+      held[1] = load8(src + 16 * lane + 8);
+      largest(held);
+    }
+    for (int i = 16 * (lane + LT); i < p.hidden; i += 16 * LT) {
+      const Raw8<T> r[2] = {load8(src + i), load8(src + i + 8)};
+      largest(r);
     }
     amax = wave_max_u32(amax);
     if constexpr (LT > 64) {
@@ -672,15 +683,20 @@ __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(DispatchParams p)
       amax = umax(umax(s_max[0], s_max[1]), umax(s_max[2], s_max[3]));
     }
     const float s = int8_scale(amax);
-    for (int i = 16 * lane; i < p.hidden; i += 16 * LT) {   // (read again, from the caches)
+    auto encode = [&](const Raw8<T> (&r)[2], int i) {
       float v[16];
-      widen8(load8(src + i), v);
-      widen8(load8(src + i + 8), v + 8);
+      widen8(r[0], v);
+      widen8(r[1], v + 8);
       const u32x4_t codes = {pack4_int8(v, s), pack4_int8(v + 4, s), pack4_int8(v + 8, s), pack4_int8(v + 12, s)};
       for (int k = 0; k < p.top_k; ++k) {
         const int row = row_at(rows, k, p.rows_total);
         if (row >= 0) *reinterpret_cast<u32x4_t*>(out + (int64_t)row * p.hidden + i) = codes;
       }
+    };
+    if (16 * lane < p.hidden) encode(held, 16 * lane);
+    for (int i = 16 * (lane + LT); i < p.hidden; i += 16 * LT) {
+      const Raw8<T> r[2] = {load8(src + i), load8(src + i + 8)};
+      encode(r, i);
     }
     if (lane < p.top_k) {
       const int row = row_at(rows, lane, p.rows_total);
