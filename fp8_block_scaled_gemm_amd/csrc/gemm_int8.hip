@@ -895,7 +895,7 @@ static double few_time(const FewPlan& f, int layout, int64_t n, int64_t k, int64
   const double wide = f.j == 8 ? 1.1 : 1.0;   // (fitted to 128 rows: more sums and pieces in each thread's registers)
   const double per_byte = wide * (f.bn * (0.0322 + 0.000183 * f.bm) + 0.0098 * f.bm);
   const double loads = c * 1e-3 * f.chunks * f.unit * per_byte, memory = (double)groups * n * k / 5.9e6;
-  const double shared = layout == kDense ? 0.17 * (double)n * k / 5.6e6 : 0.0;   // (where memory hides behind the loads, not all does)
+  const double shared = layout == kDense ? 0.17 * (double)n * k / 5.6e6 : 0.0;   // what of memory nothing hides
   return 4.8 + shared + (loads > memory ? loads : memory) + few_split_time(f);
 }
 
