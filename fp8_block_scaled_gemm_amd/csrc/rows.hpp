@@ -150,12 +150,25 @@ constexpr float kInt8Max = 127.0f;
 __device__ __forceinline__ float int8_scale(uint32_t amax_bits) {
   return amax_bits == 0u ? 1.0f : __uint_as_float(amax_bits) / kInt8Max;
 }
-// Four codes rne(v / s) (IEEE division; |v| <= amax keeps them in [-127, 127]), packed little-endian.
-// A quotient that is not a number gives code 0; the row's scale carries the NaN on.
+// Four codes rne(v / s) (IEEE division), saturated to [-127, 127], packed little-endian; s is the same in every
+// lane of the wave.  |v| <= amax keeps a quotient there by itself unless amax / 127 is subnormal: rounded to a
+// few bits it lets quotients reach 190, rounded to 0 it makes them infinite.  A quotient that is not a number
+// gives code 0; where the row holds one or an infinity, its scale carries it on.  Only scales outside the
+// normal numbers take the instructions for all that (for every row: 65536 x 1024 bf16 35.7 -> 39.5 us).
 __device__ __forceinline__ uint32_t pack4_int8(const float* v, float s) {
+  const uint32_t bits = (uint32_t)__builtin_amdgcn_readfirstlane((int)__float_as_uint(s));
   uint32_t w = 0;
+  if (bits - 0x00800000u < 0x7f000000u) {   // 2^-126 <= s < infinity
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w |= ((uint32_t)(int)__builtin_rintf(v[i] / s) & 0xffu) << (8 * i);
+    for (int i = 0; i < 4; ++i) w |= ((uint32_t)(int)__builtin_rintf(v[i] / s) & 0xffu) << (8 * i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float q = v[i] / s;
+      const float c = fminf(fmaxf(__builtin_rintf(q), -kInt8Max), kInt8Max);
+      w |= ((uint32_t)(int)(q == q ? c : 0.0f) & 0xffu) << (8 * i);
+    }
+  }
   return w;
 }
 

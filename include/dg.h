@@ -431,10 +431,11 @@ int dg_moe_combine_grad(const void* dy, const void* out, int dtype, const int32_
  */
 
 /*
- * Per-row quantizer: s = amax / 127 over the row (1 when amax = 0), q = rne(x / s), both IEEE fp32
- * divisions.  x (rows, k) in `dtype` - activations (a scale per token) or weights (a scale per output
- * channel); q int8 (rows, k); s fp32 (rows,).  Bit-exact.  A row with a NaN or an infinity gets a NaN or
- * infinite scale (its product is NaN).
+ * Per-row quantizer: s = amax / 127 over the row (1 when amax = 0), q = rne(x / s) saturated to
+ * [-127, 127], both IEEE fp32 divisions.  x (rows, k) in `dtype` - activations (a scale per token) or weights
+ * (a scale per output channel); q int8 (rows, k); s fp32 (rows,).  Bit-exact, also where amax / 127 is
+ * subnormal (fp32 rows of amax below 1.5e-36; it is 0 for amax of 63 * 2^-149 and less).  A row with a NaN or
+ * an infinity gets a NaN or infinite scale (its product is NaN).
  */
 int dg_quantize_int8_per_token(const void* x, int dtype, int64_t rows, int64_t k, int8_t* q, float* s,
                                dg_stream_t stream);

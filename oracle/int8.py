@@ -1,6 +1,8 @@
 """Plain NumPy 8-bit integer product: per-row quantizer and the three forms of the GEMM.
 
-s = fl32(amax / 127) over a row (1 when amax = 0), q = nearest even integer of fl32(x / s);
+s = fl32(amax / 127) over a row (1 when amax = 0), q = nearest even integer of fl32(x / s), saturated to
+[-127, 127] (a subnormal s is rounded so far that quotients pass them, or become infinite), 0 where x / s is
+not a number;
 D = (A * B^T) * sa[row] * sb[col], the integer sum exact, the scales in 64 bits.
 """
 
@@ -12,7 +14,9 @@ def quantize(x):
     x = np.asarray(x, dtype=np.float32)
     amax = np.abs(x).max(axis=-1)
     s = np.where(amax == 0, np.float32(1), amax / np.float32(127)).astype(np.float32)
-    return np.rint(x / s[..., None]).astype(np.int8), s
+    with np.errstate(divide="ignore", invalid="ignore"):
+        q = np.rint(x / s[..., None])
+    return np.where(np.isnan(q), np.float32(0), np.clip(q, -127, 127)).astype(np.int8), s
 
 
 def gemm_nt(a, sa, b, sb):
