@@ -713,11 +713,12 @@ __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(DispatchParams p)
       float v[16];
       widen8(load8(src + (there ? i : 0)), v);
       widen8(load8(src + (there ? i + 8 : 0)), v + 8);
-      uint32_t amax = 0;
+      // the quantizer's maximum: a NaN takes no part unless the group holds nothing else
+      float amax = fabsf(v[0]);
 #pragma unroll
-      for (int u = 0; u < 16; ++u) amax = umax(amax, abs_bits(v[u]));
-      amax = max8_u32(there ? amax : 0u);
-      const float s = amax == 0u ? 1.0f : __uint_as_float(amax) / kE4M3Max;
+      for (int u = 1; u < 16; ++u) amax = fmaxf(amax, fabsf(v[u]));
+      amax = max8(there ? amax : 0.0f);
+      const float s = amax == 0.0f ? 1.0f : amax / kE4M3Max;
       u32x4_t codes;
 #pragma unroll
       for (int u = 0; u < 4; ++u)

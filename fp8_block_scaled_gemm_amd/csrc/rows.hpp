@@ -119,6 +119,11 @@ __device__ __forceinline__ uint32_t max8_u32(uint32_t v) {
   v = umax(v, dpp_u32<kDppXor2>(v));
   return umax(v, dpp_u32<kDppHalfMirror>(v));
 }
+__device__ __forceinline__ float max8(float v) {
+  v = fmaxf(v, __uint_as_float(dpp_u32<kDppXor1>(__float_as_uint(v))));
+  v = fmaxf(v, __uint_as_float(dpp_u32<kDppXor2>(__float_as_uint(v))));
+  return fmaxf(v, __uint_as_float(dpp_u32<kDppHalfMirror>(__float_as_uint(v))));
+}
 // Maximum over the wave, as a wave-uniform (scalar) value: within rows of 16 lanes, then each row's last
 // lane to the next row, then lane 31 to the upper half; lane 63 ends with all of it.
 __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {

@@ -387,7 +387,8 @@ int dg_moe_layout(const int32_t* ids, int64_t tokens, int64_t top_k, int64_t exp
  * an expert's count, stay untouched.
  *   dg_moe_dispatch       out: (rows_total, hidden) in x's type;
  *   dg_moe_dispatch_fp8   q: E4M3 bytes, sa: the activation scales of dg_quantize_per_token_group for the
- *                         same matrices (contiguous: sa[kb * ld_sa + row]; masked: per expert), bit for bit;
+ *                         same matrices (contiguous: sa[kb * ld_sa + row]; masked: per expert), bit for bit
+ *                         (a NaN does not take part in its group's amax unless the group holds only NaNs);
  *   dg_moe_dispatch_int8  q, s: as dg_quantize_int8_per_token gives them, s fp32 (rows_total,).
  * workspace (FP8) : optional, dg_moe_dispatch_fp8_workspace_size bytes of any content (0: none is used);
  *   without it the same bits, slower where there are many scales.  Calls that share it must be ordered.

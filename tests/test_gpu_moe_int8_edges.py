@@ -77,3 +77,41 @@ def test_codes_of_the_smallest_rows_saturate(k):
     for r in range(0, t, 2):
         got = dg.dg_gemm_int8_nt_act_quant(dev(x[r:r + 2]), b, sb, out_dtype=F32)
         assert torch.equal(got, dg.dg_gemm_int8_nt(q[r:r + 2], s[r:r + 2], b, sb, out_dtype=F32)), r
+
+
+# ---- dispatch of values that are not finite -------------------------------------------------------
+
+@pytest.mark.parametrize("tokens,top_k,hidden", [(20, 2, 400), (20, 2, 2064), (1300, 3, 2064 * 16)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_fp8_dispatch_of_values_that_are_not_finite_is_the_quantizer(tokens, top_k, hidden, dtype):
+    """NaNs and infinities in a group, alone and together, in whole groups and in the partial last one."""
+    rng = np.random.default_rng(hidden)
+    x = rng.standard_normal((tokens, hidden)).astype(np.float32)
+    nan, inf, last = np.nan, np.inf, hidden // 128 * 128
+    x[0, 5] = nan
+    x[1, [3, 77]] = nan, -nan
+    x[2, 128:256] = nan                  # a group of NaNs alone
+    x[3, last:] = nan                    # and the partial one
+    x[4, 17], x[5, 200] = inf, -inf
+    x[6, [1, 2, 300]] = nan, inf, nan
+    x[7, 128:256] = 0
+    x[7, 130] = nan                      # zeros and a NaN
+    x[8, 0], x[8, hidden - 1] = nan, nan
+    x[9, 384] = nan
+    x[9, 385] = 3e38
+    say("FP8 dispatch, not finite", tokens, top_k, hidden, dtype)
+    d = dev(x).to(dtype)
+    q, sa = dg.dg_quantize_per_token_group(d)
+    ids = dev(np.argsort(rng.random((tokens, 5)), axis=1)[:, :top_k].astype(np.int32))
+    for per in (0, 1 << 10):
+        lay = dg.dg_moe_layout(ids, 5, rows_per_expert=per)
+        gq, gs = dg.dg_moe_dispatch_fp8(d, lay)
+        gq, gs = gq.view(-1, hidden), gs.view(-1, gs.shape[-2], gs.shape[-1])
+        rows = lay.rows.long()
+        token = torch.arange(tokens, device=device())[:, None].expand_as(rows)[rows >= 0]
+        rows = rows[rows >= 0]
+        assert torch.equal(gq[rows], q[token])
+        got = gs[rows // per, :, rows % per] if per else gs[0][:, rows].t()
+        want = sa[:, token].t()
+        assert torch.equal(torch.isnan(got), torch.isnan(want))
+        assert torch.equal(torch.nan_to_num(got, nan=-1.0), torch.nan_to_num(want, nan=-1.0))
