@@ -115,3 +115,75 @@ def test_fp8_dispatch_of_values_that_are_not_finite_is_the_quantizer(tokens, top
         want = sa[:, token].t()
         assert torch.equal(torch.isnan(got), torch.isnan(want))
         assert torch.equal(torch.nan_to_num(got, nan=-1.0), torch.nan_to_num(want, nan=-1.0))
+
+
+# ---- scales far from one --------------------------------------------------------------------------
+
+FAR = [1.0, 1e-34, 1e-6, 1e30, 1e-30, 1e10, 1e-10, 3e38, 1.2e-38, 0.0, 7 * 2.0 ** -149, 2.0 ** -133, 1e-20, 1e20, 1e-24]
+
+
+def far_scales(rng, *shape):
+    """Every pair of FAR meets where rows and columns count len(FAR) or more; some of them negative."""
+    s = np.resize(np.array(FAR, dtype=np.float32), shape) * rng.choice([1, 1, -1], shape).astype(np.float32)
+    return s.astype(np.float32)
+
+
+def check_far(d, want):
+    """As check, where a result past the type's range is the infinity of its sign."""
+    got, top = host(d), float(torch.finfo(d.dtype).max)
+    inside = np.abs(want) <= top * (1 - 2.0 ** -10)
+    assert np.all(np.abs(got - want)[inside] <= (REL[d.dtype] * np.abs(want) + ABS[d.dtype])[inside])
+    past = np.abs(want) >= top * (1 + 2.0 ** -7)
+    assert np.array_equal(got[past], np.copysign(np.inf, want[past]))
+
+
+@pytest.mark.parametrize("m,n,k", [(15, 64, 272), (33, 129, 2064), (128, 96, 400), (200, 130, 528), (513, 1030, 272)])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_scales_far_from_one(m, n, k, dtype):
+    """(sum * sa) * sb has a value where sa * sb does not: its product underflows, or overflows beside a small
+    sum.  Rows of zero sums are 0 whatever the scales."""
+    rng = np.random.default_rng(m + n)
+    a, b = rng.integers(-128, 128, (m, k)).astype(np.int8), rng.integers(-128, 128, (n, k)).astype(np.int8)
+    a[5] = 0
+    a[6], b[7, 3] = 0, 1
+    a[6, 3] = 1                          # sums of one code
+    a[7] = a[6]
+    sa, sb = far_scales(rng, m), far_scales(rng, n)
+    sb = np.roll(sb, 4)
+    sa[5], sa[7] = 3e38, 1e-38
+    say("int8 scales far from one", m, n, k, dtype)
+    args = [dev(v) for v in (a, sa, b, sb)]
+    d = dg.dg_gemm_int8_nt(*args, out_dtype=dtype)
+    check_far(d, oracle.int8.gemm_nt(a, sa, b, sb))
+    assert torch.all(d[5] == 0)
+    assert torch.equal(d, dg.dg_gemm_int8_nt(*args, out_dtype=dtype, use_workspace=False))
+    # the grouped forms
+    mi = np.repeat(np.array([1, 0, -1, 1], dtype=np.int32), 128)
+    ga, gsa = rng.integers(-128, 128, (512, k)).astype(np.int8), far_scales(rng, 512)
+    gb, gsb = rng.integers(-128, 128, (2, n, k)).astype(np.int8), np.roll(far_scales(rng, 2, n), 4, axis=1)
+    d = torch.zeros((512, n), dtype=dtype, device=device())
+    dg.dg_gemm_int8_grouped_contiguous(*(dev(v) for v in (ga, gsa, gb, gsb, mi)), d=d)
+    check_far(d, np.nan_to_num(oracle.int8.gemm_grouped_contiguous(ga, gsa, gb, gsb, mi)))
+    for m_max in (64, 256):
+        ga, gsa = ga.reshape(-1)[:2 * m_max * k].reshape(2, m_max, k), gsa[:2 * m_max].reshape(2, m_max)
+        mm = np.array([m_max, 17], dtype=np.int32)
+        d = torch.zeros((2, m_max, n), dtype=dtype, device=device())
+        dg.dg_gemm_int8_grouped_masked(*(dev(v) for v in (ga, gsa, gb, gsb, mm)), d=d)
+        check_far(d, np.nan_to_num(oracle.int8.gemm_grouped_masked(ga, gsa, gb, gsb, mm)))
+        ga, gsa = rng.integers(-128, 128, (512, k)).astype(np.int8), far_scales(rng, 512)
+
+
+@pytest.mark.parametrize("rows", [1, 2, 5])
+def test_scales_far_from_one_with_in_call_quantization(rows):
+    rng = np.random.default_rng(rows)
+    n, k = 300, 1040
+    b, sb = rng.integers(-128, 128, (n, k)).astype(np.int8), np.roll(far_scales(rng, n), 4)
+    for size in (1e-36, 1e-30, 1.0, 1e30, 3e37):
+        x = (rng.standard_normal((rows, k)) * size).astype(np.float32)
+        say("int8 scales far from one, in-call quantization", rows, size)
+        a, sa = oracle.int8.quantize(x)
+        want = oracle.int8.gemm_nt(a, sa, b, sb)
+        for dtype in DTYPES:
+            d = dg.dg_gemm_int8_nt_act_quant(dev(x), dev(b), dev(sb), out_dtype=dtype)
+            check_far(d, want)
+            assert torch.equal(d, dg.dg_gemm_int8_nt(dev(a), dev(sa), dev(b), dev(sb), out_dtype=dtype))
