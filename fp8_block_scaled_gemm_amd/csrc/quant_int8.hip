@@ -34,7 +34,9 @@ __global__ __launch_bounds__(NT) void quant_int8_kernel(const T* __restrict__ x,
 #pragma unroll
   for (int h = 0; h < HOLD; ++h)
     if (8 * (tid + NT * h) < k) largest(held[h]);
-  for (int i = 8 * (tid + NT * HOLD); i < k; i += 8 * NT) largest(load8(src + i));
+  // (unsigned: past the last piece of a row of almost 2^31 elements the index must not wrap)
+  const uint32_t len = (uint32_t)k;
+  for (uint32_t i = 8 * (tid + NT * HOLD); i < len; i += 8 * NT) largest(load8(src + i));
   amax = wave_max_u32(amax);
   if constexpr (W > 1) {
     if ((tid & 63) == 0) s_max[tid >> 6] = amax;
@@ -43,7 +45,7 @@ __global__ __launch_bounds__(NT) void quant_int8_kernel(const T* __restrict__ x,
     for (int w = 0; w < W; ++w) amax = umax(amax, s_max[w]);
   }
   const float s = int8_scale(amax);
-  auto encode = [&](const Raw8<T>& r, int i) {
+  auto encode = [&](const Raw8<T>& r, uint32_t i) {
     float v[8];
     widen8(r, v);
     *reinterpret_cast<u32x2_t*>(dst + i) = u32x2_t{pack4_int8(v, s), pack4_int8(v + 4, s)};
@@ -51,7 +53,7 @@ __global__ __launch_bounds__(NT) void quant_int8_kernel(const T* __restrict__ x,
 #pragma unroll
   for (int h = 0; h < HOLD; ++h)
     if (8 * (tid + NT * h) < k) encode(held[h], 8 * (tid + NT * h));
-  for (int i = 8 * (tid + NT * HOLD); i < k; i += 8 * NT) encode(load8(src + i), i);
+  for (uint32_t i = 8 * (tid + NT * HOLD); i < len; i += 8 * NT) encode(load8(src + i), i);
   if (tid == 0) s_out[row] = s;
 }
 
@@ -67,7 +69,7 @@ int launch_quant_int8(const void* x, int dtype, int64_t rows, int64_t k, int8_t*
   // threads for one to four pieces each (bf16: 16384 x 16384 139 us with 512 threads, 158 with 256, 193 with
   // 1024 that read the row twice; 65536 x 1024 35 us with 64, 51 with 256)
   const int nt = k <= 1024 ? 64 : k <= 4096 ? 256 : 512;
-  if (rows * nt > 0xffffffffLL || k > 0x7fffffffLL)
+  if (rows > 0xffffffffLL / nt || k > 0x7fffffffLL)
     return set_error(kUnsupported, "quantize_int8_per_token: shape too large for the launch grid");
   const void* fn = dtype == kF32 ? quant_int8_fn<float>(nt) : dtype == kBf16 ? quant_int8_fn<Bf16>(nt)
                                                                             : quant_int8_fn<_Float16>(nt);

@@ -79,6 +79,19 @@ def test_codes_of_the_smallest_rows_saturate(k):
         assert torch.equal(got, dg.dg_gemm_int8_nt(q[r:r + 2], s[r:r + 2], b, sb, out_dtype=F32)), r
 
 
+def test_the_longest_rows():
+    """A row of 2^31 - 16 elements: its last pieces lie where a 32-bit index is about to wrap."""
+    k, d = 2 ** 31 - 16, device()
+    say("int8 quantizer, longest row", k)
+    x = torch.zeros((1, k), dtype=BF16, device=d)
+    at = torch.tensor([0, 5, 16383, 16384, 2 ** 30 + 3, k - 4100, k - 4096, k - 9, k - 1], device=d)
+    x[0, at] = torch.tensor([1.0, -3.0, 10.0, 127.0, -127.0, 0.4, 63.0, -2.0, 64.5], device=d).to(BF16)
+    q, s = dg.dg_quantize_int8_per_token(x)
+    assert s.item() == 1.0
+    assert q[0, at].tolist() == [1, -3, 10, 127, -127, 0, 63, -2, 64]
+    assert int(q.count_nonzero()) == 8
+
+
 # ---- dispatch of values that are not finite -------------------------------------------------------
 
 @pytest.mark.parametrize("tokens,top_k,hidden", [(20, 2, 400), (20, 2, 2064), (1300, 3, 2064 * 16)])
