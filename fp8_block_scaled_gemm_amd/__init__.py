@@ -109,6 +109,7 @@ _SIGNATURES = {
                                                        _c_int64, _vp]),
     "dg_gemm_int8_grouped_masked": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _c_int, _vp, _c_int64, _c_int64, _c_int64,
                                                    _c_int64, _vp, ctypes.c_size_t, _vp]),
+    "dg_gemm_int8_config_name": (ctypes.c_char_p, [ctypes.c_int, _c_int64, _c_int64, _c_int64, _c_int64]),
     "dg_gemm_int8_workspace_size": (ctypes.c_size_t, [_c_int64, _c_int64, _c_int64, _c_int64]),
     "dg_get_num_cus": (ctypes.c_int, []),
     "dg_set_num_cus": (ctypes.c_int, [ctypes.c_int]),
@@ -731,6 +732,11 @@ def dg_moe_combine_grad(dy, out, layout, weights, dout=None, dweights=None):
 
 def dg_gemm_int8_workspace_size(m, n, k, num_groups=1):
     return lib().dg_gemm_int8_workspace_size(int(m), int(n), int(k), int(num_groups))
+
+
+def dg_gemm_int8_config_name(layout, m, n, k, num_groups=1):
+    """Tile or strip and K split that the int8 GEMM picks (layout 0 normal, 1 contiguous, 2 masked)."""
+    return lib().dg_gemm_int8_config_name(int(layout), int(m), int(n), int(k), int(num_groups)).decode()
 
 
 def dg_gemm_int8_nt_act_quant_workspace_size(m, n, k):

@@ -68,6 +68,8 @@ int launch_gemm_int8(int layout, const int8_t* a, const float* sa, const int8_t*
 int launch_gemm_int8_act_quant(const void* x, int dtype, const int8_t* b, const float* sb, void* d, int out_dtype,
                                int64_t m, int64_t n, int64_t k, void* ws, size_t ws_bytes, hipStream_t stream,
                                int num_cus);
+void gemm_int8_config_name(int layout, int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus, char* buf,
+                           size_t len);
 size_t int8_workspace_size(int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus);
 size_t int8_act_quant_workspace_size(int64_t m, int64_t n, int64_t k, int num_cus);
 
@@ -694,6 +696,18 @@ const char* dg_gemm_config_name(int layout, int64_t m, int64_t n, int64_t k, int
   const int cus = effective_cus();
   if (cus < 0) return buf;
   gemm_config_name(layout, m, n, k, num_groups, cus, buf, sizeof(buf));
+  return buf;
+}
+
+const char* dg_gemm_int8_config_name(int layout, int64_t m, int64_t n, int64_t k, int64_t num_groups) {
+  static thread_local char buf[96];
+  buf[0] = 0;
+  if (layout < 0 || layout > 2 || m <= 0 || m > kInt31 - 1024 || n <= 0 || n > kInt31 - 1024 || k <= 0 || k % kKAlign ||
+      k > kInt8MaxK || num_groups <= 0 || num_groups > kInt31 || (layout == 2 && num_groups > 1024))
+    return buf;
+  const int cus = effective_cus();
+  if (cus < 0) return buf;
+  gemm_int8_config_name(layout, m, n, k, num_groups, cus, buf, sizeof(buf));
   return buf;
 }
 

@@ -11,6 +11,10 @@
 //  * Operand tiles of 128 K bytes go from global memory into LDS by DMA (buffer_load ... lds); row r's
 //    16-byte chunk c lies at slot c ^ f(r), f(r) = (r & 7) ^ ((r >> 3) & 1), so a DMA writes whole lines
 //    and a fragment read (16 rows, one chunk) touches 16 distinct bank groups.
+#include <cstdio>
+#include <cstdlib>
+#include <cstring>
+
 #include "gemm_common.hpp"
 #include "rows.hpp"
 
@@ -897,6 +901,25 @@ struct FewPlan {
   size_t ws_bytes;
 };
 
+// DG_PLAN: a measurement override of the plan (read at every call, like DG_DEBUG), comma-separated:
+// "tile=256x256" or "tile=128x128", or "strip=32", 64, 96 or 128 (weight rows of a strip; forms and sizes that
+// may run on the few-row kernel), and "splits=S" where the call may split K.  Anything else is ignored; the
+// workspace queries see the same plan.
+struct I8Override { int bn = 0, bm = 0, strip = 0, splits = 0; };
+static I8Override plan_override() {
+  I8Override o;
+  const char* e = std::getenv("DG_PLAN");
+  for (const char* q = e; q != nullptr && *q;) {
+    if (std::sscanf(q, "tile=%dx%d", &o.bn, &o.bm) == 2 || std::sscanf(q, "strip=%d", &o.strip) == 1 ||
+        std::sscanf(q, "splits=%d", &o.splits) == 1) {}
+    q = std::strchr(q, ',');
+    if (q != nullptr) ++q;
+  }
+  if (o.splits < 0) o.splits = 0;
+  if (o.splits > kMaxSplits) o.splits = kMaxSplits;
+  return o;
+}
+
 // The tiles and the split of K into at most `want` parts, none empty.
 static void few_grid(FewPlan* f, int64_t m, int64_t n, int64_t k, int64_t groups, int64_t want) {
   f->bn = 16 * f->r * f->ns;
@@ -947,7 +970,8 @@ static double few_time(const FewPlan& f, int layout, int64_t n, int64_t k, int64
 // with 64, 38.7 with 96, 40.7 with 128; 4096 x 7168 14.2, 13.5, 16.4, 17.6; 7168 x 2048 8.3, 10.2, 12.5, 12.6.
 // D: 3 pays where a wave keeps one fragment row and a workgroup has the chunks (16 x 4096 x 7168 10.8 -> 10.2 us;
 // 64 x 7168 x 2048, four chunks, 8.3 -> 9.1).
-static FewPlan staged_plan(int layout, int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus, bool allow_split) {
+static FewPlan staged_plan(int layout, int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus, bool allow_split,
+                           const I8Override& o) {
   static constexpr struct { int ns, r; } kStrips[] = {{2, 1}, {4, 1}, {2, 3}, {4, 2}};
   FewPlan best{};
   double best_us = 0.0;
@@ -956,13 +980,19 @@ static FewPlan staged_plan(int layout, int64_t m, int64_t n, int64_t k, int64_t 
     f.j = m <= 16 ? 1 : m <= 32 ? 2 : m <= 64 ? 4 : 8;
     if (f.j == 8 && strip.r == 3) continue;   // (not built: 128 rows of its chunks fill the LDS)
     f.ns = strip.ns; f.r = strip.r;
+    if (o.strip != 0 && o.strip != 16 * f.r * f.ns) continue;
     // up to 16 rows and long K: one strip of two fragment rows, K over all eight waves (16 x 7168 x 16384
     // 25.3 -> 23.1 us; 16 x 4096 x 7168 10.2 -> 10.5)
     if (f.j == 1 && f.ns * f.r == 2 && k > 8192) f.ns = 1, f.r = 2;
     f.waves = f.j == 8 && f.ns == 2 ? kStWaves / 2 : kStWaves;   // (two workgroups' buffers fit a CU)
     f.unit = 128 * (f.waves / f.ns);
-    for (int want = 1; want <= kMaxSplits; ++want) {
-      few_grid(&f, m, n, k, groups, want);
+    bool forced = false;
+    if (o.splits != 0 && allow_split) {
+      few_grid(&f, m, n, k, groups, o.splits);
+      forced = f.tiles <= kMaxCounterTiles;
+    }
+    for (int want = 1; want <= (forced ? 1 : kMaxSplits); ++want) {
+      if (!forced) few_grid(&f, m, n, k, groups, want);
       if (want > 1 && (!allow_split || f.tiles > kMaxCounterTiles || f.chunks < 2)) break;
       const double us = few_time(f, layout, n, k, groups, num_cus);
       if (best_us == 0.0 || us <= best_us) best = f, best_us = us;   // (of equals, bound by memory, the widest)
@@ -1004,13 +1034,17 @@ static const void* direct_fn(const FewPlan& f, int dtype) {
   return dtype == kF32 ? direct_fn_of<float>(f) : dtype == kBf16 ? direct_fn_of<Bf16>(f) : direct_fn_of<_Float16>(f);
 }
 
+static int64_t few_blocks(const FewPlan& f, int64_t groups) {
+  return groups * ((((int64_t)f.strips * f.splits + 7) & ~(int64_t)7) * f.mtiles);
+}
+
 static int launch_few(const FewPlan& f, const void* fn, I8FewParams p, size_t lds, int64_t groups, void* counters,
                       void* partials, hipStream_t stream) {
   p.strips = f.strips; p.mtiles = f.mtiles; p.splits = f.splits;
   p.all_chunks = f.all_chunks; p.chunks = f.chunks;
   p.counters = static_cast<unsigned*>(counters);
   p.ws = static_cast<int*>(partials);
-  const int64_t blocks = groups * ((((int64_t)f.strips * f.splits + 7) & ~(int64_t)7) * f.mtiles);
+  const int64_t blocks = few_blocks(f, groups);
   if (blocks * 64 * f.waves > 0xffffffffLL) return set_error(kUnsupported, "int8 gemm: too many output tiles");
   void* args[] = {&p};
   const hipError_t e = hipLaunchKernel(fn, dim3((unsigned)blocks), dim3(64 * f.waves), args, lds, stream);
@@ -1076,15 +1110,24 @@ static TilePlan tile_choice(int tile, int splits, int layout, int64_t m, int64_t
 // K blocks and give each CU about one workgroup (256 x 4096 x 7168 on 128x128 tiles: split in four 22.6 us,
 // in eight, two workgroups a CU, 29.6), or two with at most three splits (64 x 24576 x 7168: 56.4 us whole,
 // 45.5 in two).
-static TilePlan tile_plan(int layout, int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus, bool allow_split) {
+static TilePlan tile_plan(int layout, int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus, bool allow_split,
+                          const I8Override& o) {
   TilePlan best{};
+  const bool may_split = layout == kDense && allow_split;
   for (int tile = 0; tile < kTiles; ++tile) {
+    if (o.bn != 0 && (o.bn != kTileModel[tile].bn || o.bm != kTileModel[tile].bm)) continue;
+    if (o.splits != 0 && may_split) {
+      const TilePlan t = tile_choice(tile, o.splits, layout, m, n, k, groups, num_cus);
+      if (t.items / t.splits <= kMaxCounterTiles) {
+        if (best.items == 0 || t.us < best.us) best = t;
+        continue;
+      }
+    }
     for (int splits = 1; splits <= kMaxSplits; ++splits) {
       const TilePlan t = tile_choice(tile, splits, layout, m, n, k, groups, num_cus);
       if (splits > 1) {
         const bool crowded = t.items > (int64_t)(splits <= 3 ? kTileModel[tile].occ : 1) * num_cus;
-        if (layout != kDense || !allow_split || t.kb_per_split < 4 || crowded || t.items / t.splits > kMaxCounterTiles)
-          break;
+        if (!may_split || t.kb_per_split < 4 || crowded || t.items / t.splits > kMaxCounterTiles) break;
         if (t.splits != splits) continue;   // the same as a smaller request
       }
       if (best.items == 0 || t.us < best.us) best = t;
@@ -1114,12 +1157,39 @@ struct I8Plan {
 };
 
 static I8Plan int8_plan(int layout, int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus, bool allow_split) {
+  I8Override o = plan_override();
+  bool known = false;
+  for (const TileModel& t : kTileModel) known |= o.bn == t.bn && o.bm == t.bm;
+  if (!known) o.bn = o.bm = 0;
+  const bool may_few = layout != kContiguous && m <= kFewRowsMost;
+  const bool strip = o.strip == 32 || o.strip == 64 || (o.strip == 96 && m <= 64) || o.strip == 128;
+  if (!strip || !may_few || o.bn != 0) o.strip = 0;
   I8Plan p{};
-  p.few = layout != kContiguous && m <= kFewRowsMost;
-  if (p.few) p.f = staged_plan(layout, m, n, k, groups, num_cus, allow_split);
-  p.t = tile_plan(layout, m, n, k, groups, num_cus, allow_split);
-  p.few = p.few && few_time(p.f, layout, n, k, groups, num_cus) < p.t.us;
+  if (may_few) p.f = staged_plan(layout, m, n, k, groups, num_cus, allow_split, o);
+  p.t = tile_plan(layout, m, n, k, groups, num_cus, allow_split, o);
+  p.few = may_few && o.bn == 0 && (o.strip != 0 || few_time(p.f, layout, n, k, groups, num_cus) < p.t.us);
   return p;
+}
+
+// "BNxBM/Wwaves/splitS", the few-row kernel's after "strip".
+static void plan_name(const I8Plan& p, char* buf, size_t len) {
+  const TileModel& t = kTileModel[p.t.tile];
+  if (p.few) snprintf(buf, len, "strip%dx%d/%dwaves/split%d", p.f.bn, p.f.bm, p.f.waves, p.f.splits);
+  else snprintf(buf, len, "%dx%d/%dwaves/split%d", t.bn, t.bm, I8Square::kWaves, p.t.splits);
+}
+
+void gemm_int8_config_name(int layout, int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus, char* buf,
+                           size_t len) {
+  plan_name(int8_plan(layout, m, n, k, layout == kDense ? 1 : groups, num_cus, layout != kContiguous), buf, len);
+}
+
+// DG_DEBUG: one line per launch with the plan.
+static void log_plan(int layout, const char* name, int64_t m, int64_t n, int64_t k, int64_t groups, int64_t workgroups,
+                     size_t need, size_t ws_bytes) {
+  static const char* const kNames[] = {"normal", "contiguous", "masked"};
+  std::fprintf(stderr, "[dg] int8 gemm %s m=%lld n=%lld k=%lld groups=%lld: %s workgroups=%lld workspace=%zu/%zu bytes\n",
+               kNames[layout], (long long)m, (long long)n, (long long)k, (long long)groups, name, (long long)workgroups,
+               need, ws_bytes);
 }
 
 int launch_quant_int8(const void* x, int dtype, int64_t rows, int64_t k, int8_t* q, float* s, hipStream_t stream);
@@ -1128,11 +1198,18 @@ size_t int8_workspace_size(int64_t m, int64_t n, int64_t k, int64_t groups, int 
   return int8_plan(groups > 1 ? kMasked : kDense, m, n, k, groups, num_cus, true).ws_bytes();
 }
 
-// `counters` and `partials`: the K split's workspace, or null for none.
+// `counters` and `partials`: the K split's workspace, or null for none; ws_bytes: what the caller gave, for the log.
 static int launch_planned(int layout, const int8_t* a, const float* sa, const int8_t* b, const float* sb, void* d,
                           int out_dtype, const int32_t* m_indices, const int32_t* masked_m, int64_t groups, int64_t m,
-                          int64_t n, int64_t k, const I8Plan& plan, void* counters, void* partials, hipStream_t stream,
-                          int num_cus) {
+                          int64_t n, int64_t k, const I8Plan& plan, void* counters, void* partials, size_t ws_bytes,
+                          hipStream_t stream, int num_cus) {
+  const int64_t slots = (int64_t)num_cus * kTileModel[plan.t.tile].occ;
+  const int64_t workgroups = plan.few ? few_blocks(plan.f, groups) : plan.t.items < slots ? plan.t.items : slots;
+  if (debug_enabled()) {
+    char name[64];
+    plan_name(plan, name, sizeof(name));
+    log_plan(layout, name, m, n, k, groups, workgroups, plan.ws_bytes(), ws_bytes);
+  }
   if (plan.few) {
     I8FewParams p{};
     p.a = a; p.sa = sa; p.b = b; p.sb = sb; p.d = d; p.masked_m = masked_m;
@@ -1152,10 +1229,9 @@ static int launch_planned(int layout, const int8_t* a, const float* sa, const in
   p.counters = static_cast<unsigned*>(counters);
   p.ws = static_cast<int*>(partials);
   if (t.items > 0x7fffffffLL) return set_error(kUnsupported, "int8 gemm: too many output tiles");
-  const int64_t slots = (int64_t)num_cus * kTileModel[t.tile].occ;
   void* args[] = {&p};
-  const hipError_t e = hipLaunchKernel(tile_fn(layout, t.tile), dim3((unsigned)(t.items < slots ? t.items : slots)),
-                                       dim3(I8Square::kThreads), args, 0, stream);
+  const hipError_t e = hipLaunchKernel(tile_fn(layout, t.tile), dim3((unsigned)workgroups), dim3(I8Square::kThreads), args,
+                                       0, stream);
   return e == hipSuccess ? kOk : set_error(kHip, "int8 gemm launch: %s", hipGetErrorString(e));
 }
 
@@ -1165,7 +1241,7 @@ int launch_gemm_int8(int layout, const int8_t* a, const float* sa, const int8_t*
   I8Plan plan = int8_plan(layout, m, n, k, groups, num_cus, ws != nullptr);
   if (ws_bytes < plan.ws_bytes()) plan = int8_plan(layout, m, n, k, groups, num_cus, false);
   return launch_planned(layout, a, sa, b, sb, d, out_dtype, m_indices, masked_m, groups, m, n, k, plan, ws,
-                        static_cast<uint8_t*>(ws) + kCounterBytes, stream, num_cus);
+                        static_cast<uint8_t*>(ws) + kCounterBytes, ws_bytes, stream, num_cus);
 }
 
 // In-call quantization.  Up to kFewFusedRows rows of at most kFewFusedK elements are quantized by the
@@ -1183,9 +1259,14 @@ size_t int8_act_quant_workspace_size(int64_t m, int64_t n, int64_t k, int num_cu
 int launch_gemm_int8_act_quant(const void* x, int dtype, const int8_t* b, const float* sb, void* d, int out_dtype,
                                int64_t m, int64_t n, int64_t k, void* ws, size_t ws_bytes, hipStream_t stream,
                                int num_cus) {
-  (void)ws_bytes;   // checked by the caller against int8_act_quant_workspace_size
+  // (ws_bytes: checked by the caller against int8_act_quant_workspace_size)
   if (few_fused(m, k)) {
     const FewPlan f = direct_plan(m, n, k, num_cus);
+    if (debug_enabled()) {
+      char name[64];
+      snprintf(name, sizeof(name), "direct%dx%d/%dwaves/split1", f.bn, f.bm, f.waves);
+      log_plan(kDense, name, m, n, k, 1, few_blocks(f, 1), 0, ws_bytes);
+    }
     I8FewParams p{};
     p.a = static_cast<const int8_t*>(x); p.b = b; p.sb = sb; p.d = d;
     p.m = (int)m; p.n = (int)n; p.k = (int)k; p.out_dtype = out_dtype;
@@ -1200,7 +1281,7 @@ int launch_gemm_int8_act_quant(const void* x, int dtype, const int8_t* b, const 
   const int r = launch_quant_int8(x, dtype, m, k, q, s, stream);
   if (r != kOk) return r;
   return launch_planned(kDense, q, s, b, sb, d, out_dtype, nullptr, nullptr, 1, m, n, k,
-                        int8_plan(kDense, m, n, k, 1, num_cus, true), w, partials, stream, num_cus);
+                        int8_plan(kDense, m, n, k, 1, num_cus, true), w, partials, ws_bytes, stream, num_cus);
 }
 
 }  // namespace dg

@@ -509,6 +509,11 @@ size_t dg_gemm_workspace_size(int64_t m, int64_t n, int64_t k, int64_t num_group
  * per group), 3 row-scaled normal.  For profiling and reports; returns "" for invalid arguments. */
 const char* dg_gemm_config_name(int layout, int64_t m, int64_t n, int64_t k, int64_t num_groups);
 
+/* The same for the 8-bit integer GEMMs (layout 0, 1 or 2): "BNxBM/Wwaves/splitS" for tiles,
+ * "stripBNxBM/Wwaves/splitS" for the kernel that streams strips of the weights past few rows.  One or two rows
+ * that dg_gemm_int8_nt_act_quant quantizes itself run on a kernel without a choice of plans. */
+const char* dg_gemm_int8_config_name(int layout, int64_t m, int64_t n, int64_t k, int64_t num_groups);
+
 /*
  * Debug facility (the analogue of the pages' debug switch among the environment variables,
  * CSDN article, "environment variables").  With DG_DEBUG set to a value other than "" or "0"
@@ -529,7 +534,10 @@ const char* dg_gemm_config_name(int layout, int64_t m, int64_t n, int64_t k, int
  * m <= 128 rows; 256x128, 256x192 or 256x256 above; 256x128 or 256x256 for the contiguous form,
  * 256x128 for the row-scaled one); splits
  * (1..16) split every tile's K range where the call may split K.  Anything else is ignored.
- * dg_gemm_config_name and dg_gemm_workspace_size report the overridden plan; results stay within
+ * The 8-bit integer GEMMs take "tile=256x256" or "tile=128x128", or "strip=32", 64, 96 or 128 (rows of the
+ * weights; the normal and masked forms of at most 1024 rows, 96 of at most 64), and "splits=S" likewise; their
+ * results stay the same bits.
+ * dg_gemm_config_name and dg_gemm_workspace_size (dg_gemm_int8_...) report the overridden plan; results stay within
  * the GEMM tolerance (a different K split changes the fp32 summation order).  For measuring the
  * alternatives the planner weighs, not for production use.
  */

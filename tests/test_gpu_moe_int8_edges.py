@@ -5,6 +5,8 @@ Quantizers are compared byte for byte; a GEMM's tolerance is that of its arithme
 exact; its conversion and two products with the scales round in fp32, 3 * 2^-24, then the output's type:
 2^-8 relative for bf16, 2^-11 for fp16 and 2^-25 absolute near zero, fp32 2^-149)."""
 
+import os
+
 import numpy as np
 import pytest
 import torch
@@ -200,3 +202,57 @@ def test_scales_far_from_one_with_in_call_quantization(rows):
             d = dg.dg_gemm_int8_nt_act_quant(dev(x), dev(b), dev(sb), out_dtype=dtype)
             check_far(d, want)
             assert torch.equal(d, dg.dg_gemm_int8_nt(dev(a), dev(sa), dev(b), dev(sb), out_dtype=dtype))
+
+
+# ---- plans ----------------------------------------------------------------------------------------
+
+class env:
+    """Environment variables for the duration of a block (the library reads them per call); None: not set."""
+
+    def __init__(self, **kv):
+        self.kv = kv
+
+    def _set(self, kv):
+        for k, v in kv.items():
+            if v is None:
+                os.environ.pop(k, None)
+            else:
+                os.environ[k] = v
+
+    def __enter__(self):
+        self.old = {k: os.environ.get(k) for k in self.kv}
+        self._set(self.kv)
+
+    def __exit__(self, *exc):
+        self._set(self.old)
+
+
+def test_debug_log_of_int8_plans(capfd):
+    """DG_DEBUG logs the plan of every form, the one that DG_PLAN asks for, and nothing without it."""
+    rng = np.random.default_rng(1)
+    say("int8 plan log")
+    (a, sa), (b, sb) = codes(rng, 256, 512), codes(rng, 2, 300, 512)
+    a, sa, b, sb = (dev(v) for v in (a, sa, b, sb))
+    mi = torch.zeros(256, dtype=torch.int32, device=device())
+    mm = torch.full((2,), 100, dtype=torch.int32, device=device())
+
+    def run():
+        dg.dg_gemm_int8_nt(a, sa, b[0], sb[0])
+        dg.dg_gemm_int8_grouped_contiguous(a, sa, b, sb, mi)
+        dg.dg_gemm_int8_grouped_masked(a.view(2, 128, 512), sa.view(2, 128), b, sb, mm)
+        dg.dg_gemm_int8_nt_act_quant(a[:2].float(), b[0], sb[0])
+        torch.cuda.synchronize()
+        return capfd.readouterr().err
+
+    with env(DG_DEBUG=None, DG_PLAN=None):
+        capfd.readouterr()
+        assert "int8 gemm" not in run()
+    for plan in (None, "tile=256x256", "tile=128x128", "strip=64"):
+        with env(DG_DEBUG="1", DG_PLAN=plan):
+            err = run()
+            for form, m, groups, layout in (("normal", 256, 1, 0), ("contiguous", 256, 2, 1), ("masked", 128, 2, 2)):
+                name = dg.dg_gemm_int8_config_name(layout, m, 300, 512, groups)
+                assert f"[dg] int8 gemm {form} m={m} n=300 k=512 groups={groups}: {name} " in err, (plan, err)
+                if plan is not None and (plan != "strip=64" or layout != 1):
+                    assert plan.split("=")[1] in name, (plan, name)
+        assert "[dg] int8 gemm normal m=2 n=300 k=512 groups=1: direct16x16/4waves/split1 " in err, err
