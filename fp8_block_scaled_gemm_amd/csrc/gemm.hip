@@ -1460,6 +1460,18 @@ int launch_gemm_no_alloc(const uint8_t* a, const float* sa, int64_t ld_sa, const
                      stream, num_cus);
 }
 
+// The same check as a launch of its own, a workgroup per 128-row block, for the int8 form.
+__global__ __launch_bounds__(kGroup) void check_contiguous_kernel(const int32_t* m_indices, int m, int groups) {
+  check_contiguous_block<kGroup, kGroup>(m_indices, m, groups, blockIdx.x * kGroup);
+}
+
+int launch_check_contiguous(const int32_t* m_indices, int64_t m, int64_t groups, hipStream_t stream) {
+  hipLaunchKernelGGL(check_contiguous_kernel, dim3((unsigned)(m / kGroup)), dim3(kGroup), 0, stream, m_indices, (int)m,
+                     (int)groups);
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? kOk : set_error(kHip, "contiguous layout check launch: %s", hipGetErrorString(e));
+}
+
 // The device diagnostics words of the current device, after every queued kernel on it has
 // finished; optionally cleared.
 int read_diag(unsigned out[4], bool clear) {

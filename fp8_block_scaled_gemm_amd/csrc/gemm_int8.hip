@@ -1193,6 +1193,7 @@ static void log_plan(int layout, const char* name, int64_t m, int64_t n, int64_t
 }
 
 int launch_quant_int8(const void* x, int dtype, int64_t rows, int64_t k, int8_t* q, float* s, hipStream_t stream);
+int launch_check_contiguous(const int32_t* m_indices, int64_t m, int64_t groups, hipStream_t stream);
 
 size_t int8_workspace_size(int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus) {
   return int8_plan(groups > 1 ? kMasked : kDense, m, n, k, groups, num_cus, true).ws_bytes();
@@ -1209,6 +1210,10 @@ static int launch_planned(int layout, const int8_t* a, const float* sa, const in
     char name[64];
     plan_name(plan, name, sizeof(name));
     log_plan(layout, name, m, n, k, groups, workgroups, plan.ws_bytes(), ws_bytes);
+    if (layout == kContiguous) {   // (the kernel itself carries no check)
+      const int r = launch_check_contiguous(m_indices, m, groups, stream);
+      if (r != kOk) return r;
+    }
   }
   if (plan.few) {
     I8FewParams p{};

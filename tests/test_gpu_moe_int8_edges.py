@@ -256,3 +256,33 @@ def test_debug_log_of_int8_plans(capfd):
                 if plan is not None and (plan != "strip=64" or layout != 1):
                     assert plan.split("=")[1] in name, (plan, name)
         assert "[dg] int8 gemm normal m=2 n=300 k=512 groups=1: direct16x16/4waves/split1 " in err, err
+
+
+def test_debug_check_of_the_int8_contiguous_layout():
+    """DG_DEBUG: a 128-row block of two experts and an expert out of range are reported; the rest is silent."""
+    rng = np.random.default_rng(2)
+    (a, sa), (b, sb) = codes(rng, 512, 272), codes(rng, 3, 130, 272)
+    args = [dev(v) for v in (a, sa, b, sb)]
+    valid = np.repeat(np.array([0, 1, -1, 2], np.int32), 128)
+    mixed, far = valid.copy(), valid.copy()
+    mixed[128 + 72] = 2
+    far[384:] = 7
+    say("int8 contiguous layout check")
+    dg.dg_get_debug_status(clear=True)
+
+    def status(m_indices):
+        d = torch.full((512, 130), float("nan"), device=device())
+        dg.dg_gemm_int8_grouped_contiguous(*args, dev(m_indices), d=d)
+        return d, dg.dg_get_debug_status(clear=True)
+
+    with env(DG_DEBUG="0"):
+        assert status(mixed)[1] == (0, -1)
+    with env(DG_DEBUG="1"):
+        d, st = status(valid)
+        assert st == (0, -1)
+        check(d, oracle.int8.gemm_grouped_contiguous(a, sa, b, sb, valid))
+        assert status(mixed)[1] == (dg.DG_DIAG_MIXED_BLOCK, 1)
+        d, st = status(far)
+        assert st == (dg.DG_DIAG_EXPERT_RANGE, 3)
+        check(d, oracle.int8.gemm_grouped_contiguous(a, sa, b, sb, far))
+    assert dg.dg_get_debug_status(clear=False) == (0, -1)
