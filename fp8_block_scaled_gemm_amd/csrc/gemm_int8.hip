@@ -1195,8 +1195,16 @@ static void log_plan(int layout, const char* name, int64_t m, int64_t n, int64_t
 int launch_quant_int8(const void* x, int dtype, int64_t rows, int64_t k, int8_t* q, float* s, hipStream_t stream);
 int launch_check_contiguous(const int32_t* m_indices, int64_t m, int64_t groups, hipStream_t stream);
 
+// One group may be the normal form or a masked buffer, whose plans differ: what either of them takes (only the
+// few-row kernel splits the masked one, so more rows need no second plan).
 size_t int8_workspace_size(int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus) {
-  return int8_plan(groups > 1 ? kMasked : kDense, m, n, k, groups, num_cus, true).ws_bytes();
+  size_t need = 0;
+  if (groups == 1) need = int8_plan(kDense, m, n, k, 1, num_cus, true).ws_bytes();
+  if (groups > 1 || m <= kFewRowsMost) {
+    const size_t masked = int8_plan(kMasked, m, n, k, groups, num_cus, true).ws_bytes();
+    if (masked > need) need = masked;
+  }
+  return need;
 }
 
 // `counters` and `partials`: the K split's workspace, or null for none; ws_bytes: what the caller gave, for the log.
@@ -1257,7 +1265,7 @@ static bool few_fused(int64_t m, int64_t k) { return m <= kFewFusedRows && k <= 
 
 size_t int8_act_quant_workspace_size(int64_t m, int64_t n, int64_t k, int num_cus) {
   if (few_fused(m, k)) return kCounterBytes;   // (not used)
-  const size_t split = int8_workspace_size(m, n, k, 1, num_cus);
+  const size_t split = int8_plan(kDense, m, n, k, 1, num_cus, true).ws_bytes();
   return kCounterBytes + align256((size_t)(m * k)) + align256((size_t)m * 4) + (split > 0 ? split - kCounterBytes : 0);
 }
 

@@ -92,6 +92,16 @@ def test_int8_plans_on_256_cus():
     assert dg.lib().dg_gemm_int8_config_name(0, 1, 1, 131072, 1) == b""
 
 
+def test_workspace_of_one_group_serves_the_masked_form():
+    """The size asked for one group lets the masked form split K as well as the normal one."""
+    nks = [(4096, 7168), (2112, 7168), (512, 4096), (7168, 2048)]
+    cases = [[layout, m, n, k, 1] for layout in (0, 2) for m in (16, 64, 100, 300, 512, 1000) for n, k in nks]
+    got = plans(cases)
+    assert any(v[0].endswith("/split4") for c, v in got.items() if c[0] == 2)
+    for case, (name, ws, _) in got.items():
+        assert ws >= split_bytes(case, name), (case, name, ws)
+
+
 def test_int8_plan_invariants():
     nks = [(1, 16), (128, 128), (512, 7168), (2112, 7168), (7168, 2048), (24576, 1536), (300, 16400), (2113, 131056)]
     cases = [[0, m, n, k, 1] for m in (1, 2, 17, 33, 64, 65, 128, 129, 300, 1000, 1025, 8192) for n, k in nks]
