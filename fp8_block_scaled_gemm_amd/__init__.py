@@ -798,7 +798,7 @@ def dg_gemm_int8_nt(a, sa, b, sb, d=None, out_dtype=torch.bfloat16, workspace=No
 def dg_gemm_int8_nt_act_quant(x, b, sb, d=None, out_dtype=torch.bfloat16, workspace=None):
     """D (M, N) from unquantized x (M, K) float32 / bfloat16 / float16: dg_quantize_int8_per_token(x) and
     dg_gemm_int8_nt in one call, the same bits.  The workspace is required (by default one per device
-    and stream)."""
+    and stream) for more than two rows or 16384 elements a row."""
     _require(x.dim() == 2 and b.dim() == 2 and b.dtype == torch.int8 and x.shape[1] == b.shape[1], "x (M, K), b int8 (N, K)")
     _require(sb.dtype == torch.float32 and sb.shape == b.shape[:1], "sb must be float32, one per row of b")
     m, k = x.shape

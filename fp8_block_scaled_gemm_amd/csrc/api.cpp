@@ -641,7 +641,7 @@ int dg_gemm_int8_nt_act_quant(const void* x, int dtype, const int8_t* b, const f
   const int cus = effective_cus();
   if (cus < 0) return cus;
   const size_t need = int8_act_quant_workspace_size(m, n, k, cus);
-  if (workspace == nullptr || workspace_bytes < need)
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need))
     return set_error(kWorkspace, "int8 gemm with activation quantization: workspace of %zu bytes, %zu needed",
                      workspace ? workspace_bytes : (size_t)0, need);
   return launch_gemm_int8_act_quant(x, dtype, b, sb, d, out_dtype, m, n, k, workspace, workspace_bytes,

@@ -1264,7 +1264,7 @@ static size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 static bool few_fused(int64_t m, int64_t k) { return m <= kFewFusedRows && k <= kFewFusedK; }
 
 size_t int8_act_quant_workspace_size(int64_t m, int64_t n, int64_t k, int num_cus) {
-  if (few_fused(m, k)) return kCounterBytes;   // (not used)
+  if (few_fused(m, k)) return 0;
   const size_t split = int8_plan(kDense, m, n, k, 1, num_cus, true).ws_bytes();
   return kCounterBytes + align256((size_t)(m * k)) + align256((size_t)m * 4) + (split > 0 ? split - kCounterBytes : 0);
 }

@@ -452,7 +452,8 @@ int dg_gemm_int8_nt(const int8_t* a, const float* sa, const int8_t* b, const flo
 /*
  * Normal form on unquantized activations x (m, k) in `dtype`: dg_quantize_int8_per_token followed by
  * dg_gemm_int8_nt, the same bits, in one call.
- * workspace : required, dg_gemm_int8_nt_act_quant_workspace_size(m, n, k) bytes, counter prefix as above.
+ * workspace : required, dg_gemm_int8_nt_act_quant_workspace_size(m, n, k) bytes, counter prefix as above (0 for
+ *   one or two rows of at most 16384 elements, which need none: NULL).
  */
 int dg_gemm_int8_nt_act_quant(const void* x, int dtype, const int8_t* b, const float* sb, void* d, int out_dtype,
                               int64_t m, int64_t n, int64_t k, void* workspace, size_t workspace_bytes,

@@ -286,3 +286,26 @@ def test_debug_check_of_the_int8_contiguous_layout():
         assert st == (dg.DG_DIAG_EXPERT_RANGE, 3)
         check(d, oracle.int8.gemm_grouped_contiguous(a, sa, b, sb, far))
     assert dg.dg_get_debug_status(clear=False) == (0, -1)
+
+
+def test_one_or_two_rows_in_a_graph_without_a_workspace():
+    d = device()
+    say("int8 gemm of one and two rows, captured without a workspace")
+    gen = torch.Generator(device=d).manual_seed(3)
+    b, sb = dg.dg_quantize_int8_per_token(torch.randn((700, 2064), generator=gen, device=d))
+    xs = [torch.randn((m, 2064), generator=gen, device=d).to(BF16) for m in (1, 2)]
+    outs = [torch.empty((m, 700), dtype=BF16, device=d) for m in (1, 2)]
+    step = lambda outs: [dg.dg_gemm_int8_nt_act_quant(x, b, sb, d=o) for x, o in zip(xs, outs)]
+    step(outs)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(outs)
+    for _ in range(3):
+        for x in xs:
+            x.copy_(torch.randn(x.shape, generator=gen, device=d))
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, o in zip(xs, outs):
+            q, s = dg.dg_quantize_int8_per_token(x)
+            assert torch.equal(o, dg.dg_gemm_int8_nt(q, s, b, sb))

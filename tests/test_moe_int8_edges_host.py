@@ -13,7 +13,7 @@ import numpy as np
 import fp8_block_scaled_gemm_amd as dg
 import oracle
 
-UNSUPPORTED = -2
+UNSUPPORTED, WORKSPACE = -2, -3
 
 
 def test_plain_codes_of_the_smallest_rows_saturate():
@@ -100,6 +100,32 @@ def test_workspace_of_one_group_serves_the_masked_form():
     assert any(v[0].endswith("/split4") for c, v in got.items() if c[0] == 2)
     for case, (name, ws, _) in got.items():
         assert ws >= split_bytes(case, name), (case, name, ws)
+
+
+def test_one_or_two_rows_need_no_workspace():
+    cases = [[0, m, n, k, 1] for m in (1, 2, 3) for n in (1, 8, 24576) for k in (16, 7168, 16384, 16400)]
+    for (_, m, n, k, _), (_, _, ws_quant) in plans(cases).items():
+        assert (ws_quant == 0) == (m <= 2 and k <= 16384), (m, n, k, ws_quant)
+    # and the call asks for none: it gets as far as the device, which is not there
+    for m, status in ((3, WORKSPACE), (2, None), (1, None)):
+        got = _act_quant_without_device(m)
+        assert got != WORKSPACE if status is None else got == status, (m, got)
+
+
+def _act_quant_without_device(m):
+    """Status of the call without a workspace, in a process that sees no device."""
+    code = f"""
+import ctypes, sys
+sys.path.insert(0, {ROOT!r})
+import fp8_block_scaled_gemm_amd as dg
+p = ctypes.c_void_p(0x1000)
+dg.dg_set_num_cus(256)
+print(dg.lib().dg_gemm_int8_nt_act_quant(p, 1, p, p, p, 1, {m}, 64, 128, None, 0, None))
+"""
+    env = dict(os.environ, HIP_VISIBLE_DEVICES="-1", ROCR_VISIBLE_DEVICES="-1")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120, env=env)
+    assert r.returncode == 0, r.stderr[-2000:]
+    return int(r.stdout.strip().splitlines()[-1])
 
 
 def test_int8_plan_invariants():
