@@ -95,7 +95,7 @@ constexpr int kMaxDevices = 64;
 static std::atomic<int> g_dev_cus[kMaxDevices];
 
 // CUs of the current device (cached per device), or a negative status.
-static int device_cus() {
+int device_cu_count() {
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess || dev < 0) return set_error(kHip, "hipGetDevice failed");
   if (dev < kMaxDevices) {
@@ -114,7 +114,7 @@ static int device_cus() {
 // workspace sizes) also answer on a host without a GPU; launches still fail there.
 static int effective_cus() {
   const int cap = g_cu_cap.load(std::memory_order_relaxed);
-  const int cus = device_cus();
+  const int cus = device_cu_count();
   if (cus < 0) return cap > 0 ? cap : cus;
   return (cap > 0 && cap < cus) ? cap : cus;
 }

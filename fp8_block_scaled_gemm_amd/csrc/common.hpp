@@ -21,6 +21,9 @@ enum Status : int { kOk = 0, kInvalidArg = -1, kUnsupported = -2, kWorkspace = -
 // Records a thread-local error message (implemented in api.cpp).
 int set_error(int status, const char* fmt, ...);
 
+// CUs of the current device whatever cap is set, or a negative status (implemented in api.cpp).
+int device_cu_count();
+
 // DG_DEBUG set in the environment (read at every call): device-side layout checks and a log of
 // each GEMM's plan on stderr (implemented in api.cpp).
 bool debug_enabled();

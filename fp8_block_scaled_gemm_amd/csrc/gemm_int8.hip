@@ -504,6 +504,7 @@ struct I8FewParams {
   int m, n, k;
   int strips, mtiles;     // tiles of a group: ceil(n / 16R) x ceil(m / 16J)
   int splits;
+  int block0;             // the launch's first (tile, split) pair: under a CU cap a call is several launches
   int all_chunks, chunks;   // of K, and of one split
   int out_dtype;
   int* ws;
@@ -523,8 +524,9 @@ __device__ __forceinline__ FewTile few_tile(const I8FewParams& p) {
   FewTile t;
   const int units = p.strips * p.splits;
   const int per_group = ((units + 7) & ~7) * p.mtiles;
-  t.g = blockIdx.x / per_group;
-  const int rest = blockIdx.x - t.g * per_group;
+  const int block = p.block0 + blockIdx.x;
+  t.g = block / per_group;
+  const int rest = block - t.g * per_group;
   const int run = rest / (8 * p.mtiles), in_run = rest - run * (8 * p.mtiles);
   const int mtile = in_run >> 3;
   const int unit = 8 * run + (in_run & 7);
@@ -1038,17 +1040,39 @@ static int64_t few_blocks(const FewPlan& f, int64_t groups) {
   return groups * ((((int64_t)f.strips * f.splits + 7) & ~(int64_t)7) * f.mtiles);
 }
 
-static int launch_few(const FewPlan& f, const void* fn, I8FewParams p, size_t lds, int64_t groups, void* counters,
-                      void* partials, hipStream_t stream) {
+// Every (tile, split) pair is a workgroup.  dg_set_num_cus keeps a call to fewer CUs than the device has by
+// launching no more of them at once than those hold, one launch after the other: the pairs do not wait for each
+// other, whichever of them arrives last joins a tile's splits.  (A loop over pairs in the kernel would do it in
+// one launch, but takes 10 to 40 registers more of the uncapped call, and a wave per SIMD with them.)
+static int64_t few_workgroups(const FewPlan& f, const void* fn, size_t lds, int64_t groups, int num_cus) {
+  const int64_t blocks = few_blocks(f, groups);
+  if (num_cus >= device_cu_count()) return blocks;
+  int occ = 0;
+  if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&occ, fn, 64 * f.waves, lds) != hipSuccess || occ < 1) {
+    (void)hipGetLastError();
+    occ = 1;
+  }
+  int64_t most = (int64_t)num_cus * occ;
+  if (most > 8) most = most / 8 * 8;   // (few_tile's runs of 8 stay on their XCDs)
+  return blocks < most ? blocks : most;
+}
+
+static int launch_few(const FewPlan& f, const void* fn, I8FewParams p, size_t lds, int64_t groups, int64_t workgroups,
+                      void* counters, void* partials, hipStream_t stream) {
   p.strips = f.strips; p.mtiles = f.mtiles; p.splits = f.splits;
   p.all_chunks = f.all_chunks; p.chunks = f.chunks;
   p.counters = static_cast<unsigned*>(counters);
   p.ws = static_cast<int*>(partials);
   const int64_t blocks = few_blocks(f, groups);
   if (blocks * 64 * f.waves > 0xffffffffLL) return set_error(kUnsupported, "int8 gemm: too many output tiles");
-  void* args[] = {&p};
-  const hipError_t e = hipLaunchKernel(fn, dim3((unsigned)blocks), dim3(64 * f.waves), args, lds, stream);
-  return e == hipSuccess ? kOk : set_error(kHip, "int8 gemm launch: %s", hipGetErrorString(e));
+  for (int64_t at = 0; at < blocks; at += workgroups) {
+    p.block0 = (int)at;
+    void* args[] = {&p};
+    const hipError_t e = hipLaunchKernel(fn, dim3((unsigned)(blocks - at < workgroups ? blocks - at : workgroups)),
+                                         dim3(64 * f.waves), args, lds, stream);
+    if (e != hipSuccess) return set_error(kHip, "int8 gemm launch: %s", hipGetErrorString(e));
+  }
+  return kOk;
 }
 
 // Time estimates (microseconds, MI355X, 256 CUs).  A workgroup's K block takes longer the more of them run (they
@@ -1213,7 +1237,10 @@ static int launch_planned(int layout, const int8_t* a, const float* sa, const in
                           int64_t n, int64_t k, const I8Plan& plan, void* counters, void* partials, size_t ws_bytes,
                           hipStream_t stream, int num_cus) {
   const int64_t slots = (int64_t)num_cus * kTileModel[plan.t.tile].occ;
-  const int64_t workgroups = plan.few ? few_blocks(plan.f, groups) : plan.t.items < slots ? plan.t.items : slots;
+  const void* fn = plan.few ? staged_fn(plan.f) : tile_fn(layout, plan.t.tile);
+  const int64_t workgroups = plan.few               ? few_workgroups(plan.f, fn, 0, groups, num_cus)
+                             : plan.t.items < slots ? plan.t.items
+                                                    : slots;
   if (debug_enabled()) {
     char name[64];
     plan_name(plan, name, sizeof(name));
@@ -1227,7 +1254,7 @@ static int launch_planned(int layout, const int8_t* a, const float* sa, const in
     I8FewParams p{};
     p.a = a; p.sa = sa; p.b = b; p.sb = sb; p.d = d; p.masked_m = masked_m;
     p.m = (int)m; p.n = (int)n; p.k = (int)k; p.out_dtype = out_dtype;
-    return launch_few(plan.f, staged_fn(plan.f), p, 0, groups, counters, partials, stream);
+    return launch_few(plan.f, fn, p, 0, groups, workgroups, counters, partials, stream);
   }
   const TilePlan& t = plan.t;
   I8Params p{};
@@ -1243,8 +1270,7 @@ static int launch_planned(int layout, const int8_t* a, const float* sa, const in
   p.ws = static_cast<int*>(partials);
   if (t.items > 0x7fffffffLL) return set_error(kUnsupported, "int8 gemm: too many output tiles");
   void* args[] = {&p};
-  const hipError_t e = hipLaunchKernel(tile_fn(layout, t.tile), dim3((unsigned)workgroups), dim3(I8Square::kThreads), args,
-                                       0, stream);
+  const hipError_t e = hipLaunchKernel(fn, dim3((unsigned)workgroups), dim3(I8Square::kThreads), args, 0, stream);
   return e == hipSuccess ? kOk : set_error(kHip, "int8 gemm launch: %s", hipGetErrorString(e));
 }
 
@@ -1275,15 +1301,18 @@ int launch_gemm_int8_act_quant(const void* x, int dtype, const int8_t* b, const 
   // (ws_bytes: checked by the caller against int8_act_quant_workspace_size)
   if (few_fused(m, k)) {
     const FewPlan f = direct_plan(m, n, k, num_cus);
+    const void* fn = direct_fn(f, dtype);
+    const size_t lds = (size_t)(m * k);
+    const int64_t workgroups = few_workgroups(f, fn, lds, 1, num_cus);
     if (debug_enabled()) {
       char name[64];
       snprintf(name, sizeof(name), "direct%dx%d/%dwaves/split1", f.bn, f.bm, f.waves);
-      log_plan(kDense, name, m, n, k, 1, few_blocks(f, 1), 0, ws_bytes);
+      log_plan(kDense, name, m, n, k, 1, workgroups, 0, ws_bytes);
     }
     I8FewParams p{};
     p.a = static_cast<const int8_t*>(x); p.b = b; p.sb = sb; p.d = d;
     p.m = (int)m; p.n = (int)n; p.k = (int)k; p.out_dtype = out_dtype;
-    return launch_few(f, direct_fn(f, dtype), p, (size_t)(m * k), 1, nullptr, nullptr, stream);
+    return launch_few(f, fn, p, lds, 1, workgroups, nullptr, nullptr, stream);
   }
   uint8_t* w = static_cast<uint8_t*>(ws);
   uint8_t* codes = w + kCounterBytes;

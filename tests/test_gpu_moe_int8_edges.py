@@ -309,3 +309,42 @@ def test_one_or_two_rows_in_a_graph_without_a_workspace():
         for x, o in zip(xs, outs):
             q, s = dg.dg_quantize_int8_per_token(x)
             assert torch.equal(o, dg.dg_gemm_int8_nt(q, s, b, sb))
+
+
+def test_few_rows_keep_to_the_cu_cap(capfd):
+    """Under dg_set_num_cus no launch of the few-row kernels has more workgroups than the capped CUs hold (32 waves
+    a CU), and the results stay the same bits."""
+    rng = np.random.default_rng(4)
+    shapes = [(1, 6200, 1040), (2, 3000, 7168), (16, 4096, 2064), (64, 4096, 4112), (100, 2050, 1040)]
+    ops = [[dev(v) for pair in (codes(rng, m, k), codes(rng, n, k)) for v in pair] for m, n, k in shapes]
+    masked = [dev(v) for pair in (codes(rng, 6, 40, 528), codes(rng, 6, 700, 528)) for v in pair]
+    mm = dev(np.array([40, 0, 3, 17, 39, 33], np.int32))
+    xs = [dev(rng.standard_normal((m, k)).astype(np.float32)) for m, _, k in shapes]
+
+    def run():
+        out = [dg.dg_gemm_int8_nt(*o, out_dtype=F32) for o in ops]
+        out += [dg.dg_gemm_int8_nt_act_quant(x, o[2], o[3], out_dtype=F32) for x, o in zip(xs, ops)]
+        d = torch.zeros((6, 40, 700), device=device())
+        return out + [dg.dg_gemm_int8_grouped_masked(*masked, mm, d=d)]
+
+    say("few-row int8 kernels under a CU cap")
+    want = run()
+    cus = dg.dg_get_num_cus()
+    try:
+        for cap in (1, 3, 8, 20, 100):
+            dg.dg_set_num_cus(cap)
+            with env(DG_DEBUG="1", DG_PLAN="strip=32"):
+                capfd.readouterr()
+                got = run()
+                err = capfd.readouterr().err
+            lines = [line for line in err.splitlines() if "int8 gemm" in line]
+            assert len(lines) == len(want), err
+            for line in lines:
+                plan, workgroups = line.split(": ")[1].split()[0], int(line.split("workgroups=")[1].split()[0])
+                waves = int(plan.split("/")[1][:-len("waves")])
+                assert plan.startswith(("strip", "direct")), line
+                assert workgroups <= cap * (32 // waves), line
+            for a, b in zip(got, want):
+                assert torch.equal(a, b), cap
+    finally:
+        dg.dg_set_num_cus(cus)
