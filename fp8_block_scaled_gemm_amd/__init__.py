@@ -600,15 +600,20 @@ def dg_moe_layout(ids, num_experts, rows_per_expert=0, rows_total=None, workspac
     dev, L = ids.device, lib()
     if rows_total is None:
         rows_total = num_experts * rows_per_expert if rows_per_expert else L.dg_moe_layout_rows(t, k, num_experts)
-    # one allocation for the index arrays
+    # one allocation for the index arrays, each at a multiple of 16 bytes (as every pointer of the GEMMs)
     n, contiguous = t * k, not rows_per_expert
     _require(n >= 0 and rows_total >= 0 and num_experts >= 1, "sizes must not be negative")
+    e4, r4 = num_experts + -num_experts % 4, rows_total + -rows_total % 4
     if contiguous:
-        buf = torch.empty(n + 2 * rows_total + num_experts, dtype=torch.int32, device=dev)
-        rows, sources, counts, m_indices = buf.split((n, rows_total, num_experts, rows_total))
+        buf = torch.empty(2 * r4 + e4 + n, dtype=torch.int32, device=dev)
+        sources, m_indices, counts, rows = buf.split((r4, r4, e4, n))
     else:
-        buf = torch.empty(n + rows_total + num_experts, dtype=torch.int32, device=dev)
-        (rows, sources, counts), m_indices = buf.split((n, rows_total, num_experts)), None
+        buf = torch.empty(r4 + e4 + n, dtype=torch.int32, device=dev)
+        (sources, counts, rows), m_indices = buf.split((r4, e4, n)), None
+    if e4 != num_experts:
+        counts = counts[:num_experts]
+    if r4 != rows_total:   # (the masked layout's; the other's rows are a multiple of 128, or refused)
+        sources = sources[:rows_total]
     rows = rows.view(t, k)
     if workspace is None:
         need = L.dg_moe_layout_workspace_size(t, k, num_experts)

@@ -132,6 +132,23 @@ def test_fp8_dispatch_of_values_that_are_not_finite_is_the_quantizer(tokens, top
         assert torch.equal(torch.nan_to_num(got, nan=-1.0), torch.nan_to_num(want, nan=-1.0))
 
 
+# ---- layout ---------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("tokens,top_k,experts,per", [(1, 1, 1, 0), (3, 3, 5, 0), (7, 1, 6, 0), (5, 3, 7, 3), (1, 1, 1, 1), (9, 5, 3, 33)])
+def test_index_arrays_are_aligned(tokens, top_k, experts, per):
+    """Every array of a layout starts at a multiple of 16 bytes, as the pointers that the GEMMs take."""
+    say("alignment of a layout's arrays", tokens, top_k, experts, per)
+    ids = np.random.default_rng(tokens).integers(0, experts, (tokens, top_k)).astype(np.int32)
+    lay = dg.dg_moe_layout(dev(ids), experts, rows_per_expert=per)
+    for name in ("rows", "sources", "counts") + (() if per else ("m_indices",)):
+        assert getattr(lay, name).data_ptr() % 16 == 0, name
+    rows, sources, m_indices, counts = oracle.moe.layout(ids, experts, per)
+    assert np.array_equal(lay.rows.cpu().numpy(), rows) and np.array_equal(lay.counts.cpu().numpy(), counts)
+    assert np.array_equal(lay.sources.cpu().numpy()[:len(sources)], sources)
+    if not per:
+        assert np.array_equal(lay.m_indices.cpu().numpy()[:len(m_indices)], m_indices)
+
+
 # ---- scales far from one --------------------------------------------------------------------------
 
 FAR = [1.0, 1e-34, 1e-6, 1e30, 1e-30, 1e10, 1e-10, 3e38, 1.2e-38, 0.0, 7 * 2.0 ** -149, 2.0 ** -133, 1e-20, 1e20, 1e-24]
