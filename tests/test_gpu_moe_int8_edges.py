@@ -365,3 +365,195 @@ def test_few_rows_keep_to_the_cu_cap(capfd):
                 assert torch.equal(a, b), cap
     finally:
         dg.dg_set_num_cus(cus)
+
+
+# ---- every kernel that a plan can name ------------------------------------------------------------
+
+TILES = ["tile=256x256", "tile=128x128"]
+# rows, columns, K: 1, 2, 3, 5, 8 and 9 blocks of 128 with a partial last one, edges on every side of a tile
+TILE_SHAPES = [(1, 1, 16), (255, 257, 128), (300, 515, 256), (129, 250, 272), (256, 512, 640), (513, 300, 1024), (600, 259, 1040)]
+
+
+@pytest.mark.parametrize("m,n,k", TILE_SHAPES)
+@pytest.mark.parametrize("tile", TILES)
+def test_tiles_and_their_splits(tile, m, n, k):
+    rng = np.random.default_rng(m + n + k)
+    (a, sa), (b, sb) = codes(rng, m, k), codes(rng, n, k)
+    sa[::7] = far_scales(rng, m)[::7]     # some waves meet scales far from one, some do not
+    want = oracle.int8.gemm_nt(a, sa, b, sb)
+    args = [dev(v) for v in (a, sa, b, sb)]
+    for dtype in DTYPES:
+        first = None
+        for splits in (1, 2, 3, 16):
+            with env(DG_PLAN=f"{tile},splits={splits}"):
+                kb = -(-k // 128)
+                name = f"{tile[5:]}/8waves/split{-(-kb // -(-kb // splits))}"
+                assert dg.dg_gemm_int8_config_name(0, m, n, k) == name
+                say("int8 tiles", name, m, n, k, dtype)
+                ws = torch.zeros(max(dg.dg_gemm_int8_workspace_size(m, n, k), 16), dtype=torch.uint8, device=device())
+                for _ in range(2):        # the counters are left zero
+                    d = torch.full((m, n), float("nan"), dtype=dtype, device=device())
+                    dg.dg_gemm_int8_nt(*args, d=d, workspace=ws)
+                    assert int(ws[:64 << 10].count_nonzero()) == 0
+                    if first is None:
+                        check_far(d, want)
+                        first = d
+                    assert torch.equal(d, first), (name, dtype)
+
+
+# experts of the 128-row blocks of a call: both halves of a 256-row tile of one expert, of two, one or both
+# unused, out of range, and a last tile of one block
+TWO_EXPERTS = [[0, 1], [1, 1], [-1, 1], [1, -1], [-1, -1, 2], [0, 0, 1], [2, 0, 0, 7, -1, 1, 1], [0, 1, 2, 0, 1, 2, 2, 2],
+               [-4, 2 ** 30, 0, 1, 1, 2, -1, 0, 0]]
+
+
+@pytest.mark.parametrize("blocks", TWO_EXPERTS)
+@pytest.mark.parametrize("tile", TILES)
+def test_contiguous_tiles_of_two_experts(tile, blocks):
+    rng = np.random.default_rng(len(blocks))
+    m = 128 * len(blocks)
+    mi = np.repeat(np.array(blocks, dtype=np.int32), 128)
+    for n, k in ((257, 16), (300, 256), (512, 400), (130, 1040)):
+        (a, sa), (b, sb) = codes(rng, m, k), codes(rng, 3, n, k)
+        want = oracle.int8.gemm_grouped_contiguous(a, sa, b, sb, mi)
+        args = [dev(v) for v in (a, sa, b, sb, mi)]
+        with env(DG_PLAN=tile):
+            assert dg.dg_gemm_int8_config_name(1, m, n, k, 3) == tile[5:] + "/8waves/split1"
+            for dtype in DTYPES:
+                say("int8 contiguous tiles", tile, blocks, n, k, dtype)
+                d = torch.full((m, n), float("nan"), dtype=dtype, device=device())
+                dg.dg_gemm_int8_grouped_contiguous(*args, d=d)
+                check(d, want)
+
+
+MASKED_COUNTS = [(300, [0, 1, 127, 128, 129, 255, 256, 257, 300, -3, 999]), (256, [256, 0, 255]), (60, [60, 0, 7, 33])]
+
+
+@pytest.mark.parametrize("plan,m_max,counts", [(plan, m, c) for plan in TILES + ["strip=32", "strip=64", "strip=96", "strip=128"]
+                                               for m, c in MASKED_COUNTS if plan != "strip=96" or m <= 64])
+def test_masked_on_every_plan(plan, m_max, counts):
+    rng = np.random.default_rng(m_max)
+    g, mm = len(counts), np.array(counts, dtype=np.int32)
+    for n, k in ((257, 128), (300, 1040), (64, 2064)):
+        (a, sa), (b, sb) = codes(rng, g, m_max, k), codes(rng, g, n, k)
+        want = oracle.int8.gemm_grouped_masked(a, sa, b, sb, mm)
+        args = [dev(v) for v in (a, sa, b, sb, mm)]
+        for dtype in DTYPES:
+            for splits in (1, 3):
+                with env(DG_PLAN=f"{plan},splits={splits}"):
+                    name = dg.dg_gemm_int8_config_name(2, m_max, n, k, g)
+                    assert plan[5:] in name if plan in TILES else name.startswith("strip" + plan[6:] + "x"), name
+                    say("int8 masked on", name, m_max, n, k, dtype)
+                    d = torch.full((g, m_max, n), float("nan"), dtype=dtype, device=device())
+                    dg.dg_gemm_int8_grouped_masked(*args, d=d)
+                    check(d, want)
+
+
+@pytest.mark.parametrize("strip,m", [(strip, m) for strip in (32, 64, 96, 128) for m in (1, 3, 16, 17, 32, 33, 64, 65, 128, 200)
+                                     if strip != 96 or m <= 64])
+def test_strips_and_their_splits(strip, m):
+    rng = np.random.default_rng(m)
+    for n, k in ((1, 16), (130, 400), (257, 2064), (100, 9232)):
+        (a, sa), (b, sb) = codes(rng, m, k), codes(rng, n, k)
+        want = oracle.int8.gemm_nt(a, sa, b, sb)
+        args = [dev(v) for v in (a, sa, b, sb)]
+        for splits, dtype in ((1, F32), (2, BF16), (5, F16), (16, F32)):
+            with env(DG_PLAN=f"strip={strip},splits={splits}"):
+                name = dg.dg_gemm_int8_config_name(0, m, n, k)
+                assert name.startswith(f"strip{strip}x"), name
+                say("int8 strips", name, m, n, k, dtype)
+                d = torch.full((m, n), float("nan"), dtype=dtype, device=device())
+                dg.dg_gemm_int8_nt(*args, d=d)
+                check(d, want)
+
+
+@pytest.mark.parametrize("m,n,k,name", [(1, 6200, 1040, "direct32x16/4waves"), (2, 6150, 7168, "direct32x16/8waves"),
+                                        (1, 300, 16384, "direct16x16/16waves"), (2, 6150, 16384, "direct32x16/16waves"),
+                                        (2, 129, 4096, "direct16x16/4waves"), (1, 515, 8192, "direct16x16/8waves"),
+                                        (1, 6144, 4112, "direct32x16/8waves")])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_rows_quantized_by_the_product_itself(m, n, k, name, dtype, capfd):
+    rng = np.random.default_rng(n + k)
+    x = dev(rng.standard_normal((m, k)).astype(np.float32) * 3).to(dtype)
+    b, sb = (dev(v) for v in codes(rng, n, k))
+    say("int8 gemm that quantizes its rows", name, m, n, k, dtype)
+    a, sa = oracle.int8.quantize(x.float().cpu().numpy())
+    want = oracle.int8.gemm_nt(a, sa, b.cpu().numpy(), sb.cpu().numpy())
+    for out in DTYPES:
+        capfd.readouterr()
+        with env(DG_DEBUG="1"):
+            d = dg.dg_gemm_int8_nt_act_quant(x, b, sb, out_dtype=out)
+        if dg.dg_get_num_cus() == 256:
+            assert f": {name}/split1 " in capfd.readouterr().err
+        check(d, want)
+
+
+# ---- rows that the last-level cache cannot hold ----------------------------------------------------
+
+@pytest.mark.parametrize("tokens,top_k,hidden,dtype", [(70000, 2, 1024, BF16), (35000, 4, 1024, BF16), (17000, 4, 2064, BF16),
+                                                       (9000, 8, 2064, F16), (35100, 1, 2064, F32)])
+def test_combine_and_gradients_past_the_cache(tokens, top_k, hidden, dtype):
+    """More than 256 MiB of rows: the nontemporal forms of combine and of its gradient.  Tolerances: a chain of
+    top_k fused multiply-adds and one rounding; a sum of `hidden` products in lanes."""
+    d = device()
+    say("combine past the cache", tokens, top_k, hidden, dtype)
+    gen = torch.Generator(device=d).manual_seed(tokens)
+    ids = torch.argsort(torch.rand((tokens, 8), generator=gen, device=d), dim=1)[:, :top_k].int().contiguous()
+    ids[5] = -1
+    ids[11, 0] = -1
+    lay = dg.dg_moe_layout(ids, 8)
+    out = torch.randn((lay.rows_total, hidden), generator=gen, device=d).to(dtype)
+    assert tokens * top_k * hidden * out.element_size() > 256 << 20
+    w = torch.rand((tokens, top_k), generator=gen, device=d)
+    dy = torch.randn((tokens, hidden), generator=gen, device=d).to(dtype)
+    y = dg.dg_moe_combine(out, lay, weights=w)
+    y1 = dg.dg_moe_combine(out, lay)
+    dout, dw = dg.dg_moe_combine_grad(dy, out, lay, w, dout=torch.full_like(out, 9.0))
+    rel = {F32: 2.0 ** -24, BF16: 2.0 ** -8, F16: 2.0 ** -11}[dtype]
+    chain = 2 * (top_k + 1) * 2.0 ** -24
+    for t0 in range(0, tokens, 8192):
+        t = slice(t0, min(t0 + 8192, tokens))
+        rows = lay.rows[t].long()
+        there = (rows >= 0).double().unsqueeze(-1)
+        picked = out[rows.clamp_min(0)].double() * there
+        for got, weight in ((y[t], w[t].double().unsqueeze(-1)), (y1[t], torch.ones_like(there))):
+            want, size = (picked * weight).sum(1), (picked * weight).abs().sum(1)
+            assert bool(((got.double() - want).abs() <= rel * want.abs() + ABS[dtype] + chain * size).all())
+        products = picked * dy[t].double().unsqueeze(1)
+        near = (hidden / 64 + 16) * 2.0 ** -24 * products.abs().sum(2) + 1e-37
+        assert bool(((dw[t].double() - products.sum(2)).abs() <= near).all())
+        want = dy[t].double().unsqueeze(1) * w[t].double().unsqueeze(-1) * there
+        got = dout[rows.clamp_min(0)].double() * there
+        assert bool(((got - want).abs() <= (rel + 2.0 ** -23) * want.abs() + ABS[dtype]).all())
+    free = lay.sources < 0
+    assert bool((dout[free & (lay.m_indices >= 0)] == 0).all()) and bool((dout[lay.m_indices < 0] == 9).all())
+
+
+# ---- routing under masks of the type's lowest value ------------------------------------------------
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_under_masks_of_the_lowest_value(score, dtype):
+    """A mask that writes the type's lowest value leaves its expert available, last, and with no weight beside
+    any other; a row of nothing else is shared evenly (softmax) or has no score left (sigmoid)."""
+    rng = np.random.default_rng(8)
+    low = torch.finfo(dtype).min
+    x = dev(rng.standard_normal((40, 96)) * 2).to(dtype)
+    x = torch.where(dev(rng.random((40, 96)) < 0.5), torch.full_like(x, low), x)
+    x[3] = low
+    x[4, 2:] = low
+    x[5, 1:] = -np.inf
+    x[5, 0] = low
+    x[6, ::2], x[6, 1::2] = torch.finfo(dtype).max, low
+    say("route under masks of the lowest value", score, dtype)
+    for renorm in (True, False):
+        ids, w = dg.dg_moe_route(x, 6, score=score, renormalize=renorm)
+        want, _ = oracle.moe.route(host(x), 6, score=score, renormalize=renorm)
+        if score == "softmax":            # compared by the logits, exactly
+            assert np.array_equal(ids.cpu().numpy(), want)
+        want = oracle.moe.weights_of(host(x), ids.cpu().numpy(), score, renorm, 1.0)
+        np.testing.assert_allclose(host(w), want, rtol=80 * 2.0 ** -24, atol=1e-37)
+        dx = dg.dg_moe_route_grad(torch.ones_like(w), x, ids, score=score, renormalize=renorm)
+        want = oracle.moe.route_grad(np.ones(w.shape), host(x), ids.cpu().numpy(), score, renorm, 1.0)
+        assert torch.isfinite(dx).all()
+        assert np.all(np.abs(host(dx) - want) <= REL[dtype] * np.abs(want) + ABS[dtype] + 4 * 80 * 2.0 ** -24)
