@@ -124,9 +124,9 @@ __device__ __forceinline__ void store_out4(void* d, int dtype, int64_t at, const
 // The block body has no branch: past the last block the DMAs take out-of-range offsets and write zeros
 // that nothing reads.
 //
-// Bound by the matrix cores: 16384 x 7168 x 16384 runs at 2.70e15 operations/s (1424 us), 4096 x 4096 x 7168
-// at 2.45e15 (98 us, one round of 256 tiles: its first loads and its stores are not hidden).  The rate
-// depends on the operands' bits (zeros 3.2e15, random codes 2.7e15): power holds the clock, not the
+// Bound by the matrix cores: 16384 x 7168 x 16384 runs at 2.65e15 operations/s (1450 us, 1424 to 1482 over several
+// boxes), 4096 x 4096 x 7168 at 2.45e15 (98 us, one round of 256 tiles: its first loads and its stores are not
+// hidden).  The rate depends on the operands' bits (zeros 3.2e15, random codes 2.65e15): power holds the clock, not the
 // instruction stream.  32x32x32 products in the place of
 // 16x16x64 ones ran at 2.53e15; a 256x128 tile was slower for the grouped forms; the smaller tile serves
 // launches that the square one leaves short of work (256 x 4096 x 7168: 21.6 us, split in four).
@@ -483,7 +483,7 @@ __global__ __launch_bounds__(C::kThreads, 2 * C::OCC) void gemm_int8_kernel(I8Pa
 // partials are added in LDS, the S partials of a tile go through the workspace to the workgroup that arrives
 // last; integers, so no order changes the result.
 //  * direct: one or two unquantized rows, which every workgroup quantizes for itself while its first weights
-//    are on the way (1 x 4096 x 7168: 8.2 us, 3.6 TB/s of weights; 1 x 24576 x 7168: 31.4 us, 5.6 TB/s).
+//    are on the way (1 x 4096 x 7168: 8.6 us, 3.4 TB/s of weights; 1 x 24576 x 7168: 30.3 us, 5.8 TB/s).
 //  * staged: the activations pass through LDS (16 x 24576 x 7168: 29.0 us, 6.1 TB/s of weights; 64 rows 40.3,
 //    4.4 TB/s; 64 x 4096 x 7168: 13.0 us).
 //
@@ -1078,8 +1078,9 @@ static int launch_few(const FewPlan& f, const void* fn, I8FewParams p, size_t ld
 // Time estimates (microseconds, MI355X, 256 CUs).  A workgroup's K block takes longer the more of them run (they
 // share caches and power); a tile costs a fixed part as well (first loads, stores); a K split sends its partials
 // out and back.  Fitted, with few_time's fixed part, to timings of every choice on 154 shapes of 72 to 1024
-// rows, 512 to 24576 columns and K from 512 to 16384: the plan takes 0.5% longer than the fastest choice on
-// average, 13% at worst.
+// rows, 512 to 24576 columns and K from 512 to 16384: the plan takes 1.0% longer than the fastest choice on
+// average, 19% at worst (777 x 2112 x 7168: 34.7 us in three parts, 29.1 in four).  The grouped forms use the same
+// constants without a fit of their own.
 struct TileModel { int bn, bm, occ; double fixed, alone, busy; };
 constexpr TileModel kTileModel[kTiles] = {
     {I8Square::BN, I8Square::BM, I8Square::OCC, 7.0, 0.9, 1.6},
@@ -1108,7 +1109,10 @@ static TilePlan tile_choice(int tile, int splits, int layout, int64_t m, int64_t
   double tiles = (double)t.tiles_m * t.tiles_n;
   // masked: the counts are on the device; any of 0 .. m rows alike use (m-blocks + 1) / 2 blocks on average
   if (layout == kMasked) tiles = (double)groups * 0.5 * (t.tiles_m + 1) * t.tiles_n;
-  if (layout == kContiguous && c.bm > kGroup) {   // a tile that spans two experts runs twice
+  // A tile that spans two experts runs twice, one pass after the other in its workgroup.  Counted as another tile it
+  // costs too much where the tiles fill one round: 4096 x 4096 x 7168, four experts of whole tiles, takes 98 us on
+  // 256x256 tiles and 123 on the 128x128 ones that are chosen (every edge inside a tile: 126 and 127).
+  if (layout == kContiguous && c.bm > kGroup) {
     const int64_t edges = groups - 1 < t.tiles_m ? groups - 1 : t.tiles_m;
     tiles += (double)edges * t.tiles_n;
   }

@@ -233,7 +233,7 @@ struct RouteGradParams {
 //   s = sigmoid(x) or exp(x - max), r = s / sum s, w = scale r:  dx = scale r (g - sum r g) [(1 - s) for sigmoid]
 //   w = scale s:  dx = scale g s (1 - s) for sigmoid; for softmax over the row, dx_e = p_e (u_e - sum p u), u = scale g.
 // Every element of the row is written (zeros where nothing was chosen), which bounds it: 16384 x 256 fp32
-// 8.8 us, 2.0 TB/s in these sizes' few microseconds; the full softmax 12.4.
+// 9.5 us, 1.8 TB/s in these sizes' few microseconds; the full softmax 12.4.
 template <class T, int C>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_grad_kernel(RouteGradParams p) {
   const int lane = threadIdx.x & 63;
@@ -820,7 +820,8 @@ int launch_moe_dispatch(int form, const void* x, int dtype, const int32_t* rows,
 // Combine: y[t] = sum over k of w[t, k] * rows[row(t, k)], in fp32, in the order of k.
 //
 // It reads K rows for one written: bound by memory reads.  4096 tokens x 8 rows of 7168 bf16: 91 us, 5.8 TB/s;
-// 16384 x 2 of 1024: 20.2 us, 5.0 TB/s (a large copy reaches 5.1, a large read 6 to 7).
+// 16384 x 2 of 1024: 20.2 us, 5.0 TB/s (a large copy reaches 5.1, a large read 6 to 7; calls back to back in a
+// graph, other rows each time).
 // ---------------------------------------------------------------------------
 constexpr int kCombThreads = 128;
 constexpr int kCombBatch = 8;   // expert rows whose loads are in flight together

@@ -9,8 +9,8 @@ namespace dg {
 
 // One workgroup of NT threads per row.  Each thread holds HOLD pieces of 8 elements in registers, so that a
 // row of up to 8 * NT * HOLD elements is read once; the rest of a longer row is read again (from the
-// caches) for its codes.  Bound by memory: 32768 x 7168 bf16 142 us, 5.0 TB/s;
-// 65536 x 2048 fp32 115 us, 5.9 TB/s (nontemporal loads of rows past the last-level cache: 2% of that, either way).
+// caches) for its codes.  Bound by memory: 32768 x 7168 bf16 135 us, 5.2 TB/s; 16384 x 16384 bf16 150 us, 5.4;
+// 65536 x 2048 fp32 113 us, 5.9 TB/s (nontemporal loads of rows past the last-level cache: 2% of that, either way).
 template <class T, int NT, int HOLD>
 __global__ __launch_bounds__(NT) void quant_int8_kernel(const T* __restrict__ x, int k, uint8_t* __restrict__ q,
                                                         float* __restrict__ s_out) {
@@ -66,8 +66,8 @@ static const void* quant_int8_fn(int nt) {
 }
 
 int launch_quant_int8(const void* x, int dtype, int64_t rows, int64_t k, int8_t* q, float* s, hipStream_t stream) {
-  // threads for one to four pieces each (bf16: 16384 x 16384 139 us with 512 threads, 158 with 256, 193 with
-  // 1024 that read the row twice; 65536 x 1024 35 us with 64, 51 with 256)
+  // threads for one to four pieces each (bf16, 16384 x 16384: 512 threads 12% faster than 256 and 28% faster than 1024
+  // that read the row twice; 65536 x 1024: 64 threads 31% faster than 256)
   const int nt = k <= 1024 ? 64 : k <= 4096 ? 256 : 512;
   if (rows > 0xffffffffLL / nt || k > 0x7fffffffLL)
     return set_error(kUnsupported, "quantize_int8_per_token: shape too large for the launch grid");

@@ -159,7 +159,7 @@ __device__ __forceinline__ float int8_scale(uint32_t amax_bits) {
 // lane of the wave.  |v| <= amax keeps a quotient there by itself unless amax / 127 is subnormal: rounded to a
 // few bits it lets quotients reach 190, rounded to 0 it makes them infinite.  A quotient that is not a number
 // gives code 0; where the row holds one or an infinity, its scale carries it on.  Only scales outside the
-// normal numbers take the instructions for all that (for every row: 65536 x 1024 bf16 35.7 -> 39.5 us).
+// normal numbers take the instructions for all that (65536 x 1024 bf16 33.7 us, 39.5 with them for every row).
 __device__ __forceinline__ uint32_t pack4_int8(const float* v, float s) {
   const uint32_t bits = (uint32_t)__builtin_amdgcn_readfirstlane((int)__float_as_uint(s));
   uint32_t w = 0;
