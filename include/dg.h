@@ -427,8 +427,9 @@ int dg_moe_combine_grad(const void* dy, const void* out, int dtype, const int32_
 /*
  * 8-bit integer GEMMs: D = (A * B^T) * sa[row] * sb[col] with one fp32 scale per token (row of A) and
  * one per output channel (row of B).  The sum over K is exact in int32; scales (in an order in which their own
- * product's range is no limit) and the one rounding to the output's type (out_dtype, a dg_dtype) follow it.  K is a multiple of 16 as everywhere, and at most
- * 131056 (what int32 holds of products of any codes); DG_ERR_UNSUPPORTED above.
+ * product's range is no limit) and the one rounding to the output's type (out_dtype, a dg_dtype) follow it.  K is a
+ * multiple of 16 as everywhere, and at most 131056 (what int32 holds of products of any codes);
+ * DG_ERR_UNSUPPORTED above.
  */
 
 /*
