@@ -577,11 +577,22 @@ class MoeLayout:
     """Rows of the (token, k) entries of a batch: rows int32 (T, top_k) (-1: none), sources int32
     (rows_total,) (the inverse), m_indices int32 (rows_total,) for the contiguous grouped GEMMs (None in
     the masked layout), counts int32 (experts,) (masked_m of the masked ones).  rows_per_expert is 0 in
-    the contiguous layout."""
+    the contiguous layout.  Made by dg_moe_layout, or by hand from arrays of those kinds."""
 
     __slots__ = ("rows", "sources", "m_indices", "counts", "rows_total", "rows_per_expert", "num_experts")
 
-    def __init__(self, rows, sources, m_indices, counts, rows_total, rows_per_expert, num_experts):
+    def __init__(self, rows, sources, m_indices, counts, rows_total, rows_per_expert, num_experts, _check=True):
+        if _check:
+            arrays = [rows, sources, counts] + ([] if m_indices is None else [m_indices])
+            _dev(*arrays)
+            _require(all(a.dtype == torch.int32 and a.device == rows.device for a in arrays),
+                     "the arrays of a layout must be int32, on one device")
+            _require(rows_per_expert >= 0 and (m_indices is None) == (rows_per_expert > 0) and
+                     (not rows_per_expert or rows_total == num_experts * rows_per_expert),
+                     "m_indices for the contiguous layout, num_experts * rows_per_expert rows for the masked one")
+            _require(rows.dim() == 2 and sources.numel() == rows_total and counts.numel() == num_experts and
+                     (m_indices is None or m_indices.numel() == rows_total),
+                     "rows (tokens, top_k), sources and m_indices (rows_total,), counts (num_experts,)")
         self.rows, self.sources, self.m_indices, self.counts = rows, sources, m_indices, counts
         self.rows_total, self.rows_per_expert, self.num_experts = rows_total, rows_per_expert, num_experts
 
@@ -619,11 +630,10 @@ def dg_moe_layout(ids, num_experts, rows_per_expert=0, rows_total=None, workspac
         need = L.dg_moe_layout_workspace_size(t, k, num_experts)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check("dg_moe_layout",
            L.dg_moe_layout(_ptr(ids), t, k, num_experts, rows_per_expert, rows_total, _ptr(rows), _ptr(sources),
-                           _ptr(m_indices), _ptr(counts), _ptr(workspace), ws_bytes, _stream(ids)))
-    return MoeLayout(rows, sources, m_indices, counts, rows_total, rows_per_expert, num_experts)
+                           _ptr(m_indices), _ptr(counts), *_ws(workspace), _stream(ids)))
+    return MoeLayout(rows, sources, m_indices, counts, rows_total, rows_per_expert, num_experts, _check=False)
 
 
 def _dispatch_args(x, layout):
@@ -780,7 +790,11 @@ def _int8_out(d, shape, out_dtype, device):
 
 
 def _ws(workspace):
-    return _ptr(workspace), (workspace.numel() * workspace.element_size() if workspace is not None else 0)
+    """(pointer, bytes) of a caller's workspace, or of none."""
+    if workspace is None:
+        return None, 0
+    _dev(workspace)
+    return _ptr(workspace), workspace.numel() * workspace.element_size()
 
 
 def dg_gemm_int8_nt(a, sa, b, sb, d=None, out_dtype=torch.bfloat16, workspace=None, use_workspace=True):

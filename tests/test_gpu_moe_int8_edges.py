@@ -559,3 +559,38 @@ def test_route_under_masks_of_the_lowest_value(score, dtype):
         want = oracle.moe.route_grad(np.ones(w.shape), host(x), ids.cpu().numpy(), score, renorm, 1.0)
         assert torch.isfinite(dx).all()
         assert np.all(np.abs(host(dx) - want) <= REL[dtype] * np.abs(want) + ABS[dtype] + 4 * 80 * 2.0 ** -24)
+
+
+# ---- refusals of the binding ----------------------------------------------------------------------
+
+def test_workspaces_and_layouts_that_the_kernels_cannot_read_are_refused():
+    d = device()
+    say("refused workspaces and layouts")
+    rng = np.random.default_rng(6)
+    (a, sa), (b, sb) = codes(rng, 40, 4112), codes(rng, 300, 4112)
+    a, sa, b, sb = (dev(v) for v in (a, sa, b, sb))
+    mm = torch.full((1,), 40, dtype=torch.int32, device=d)
+    ids = torch.zeros((3000, 2), dtype=torch.int32, device=d)
+    x = torch.ones((3000, 128), device=d)
+    big = torch.zeros(1 << 22, dtype=torch.uint8, device=d)
+    lay = dg.dg_moe_layout(ids, 4)
+    for ws in (torch.zeros(1 << 21, dtype=torch.uint8), big[::2]):    # on the host; with gaps
+        for call in (lambda: dg.dg_gemm_int8_nt(a, sa, b, sb, workspace=ws),
+                     lambda: dg.dg_gemm_int8_nt_act_quant(x, b[:, :128].contiguous(), sb, workspace=ws),
+                     lambda: dg.dg_gemm_int8_grouped_masked(a[None], sa[None], b[None], sb[None], mm, workspace=ws),
+                     lambda: dg.dg_moe_layout(ids, 4, workspace=ws), lambda: dg.dg_moe_dispatch_fp8(x, lay, workspace=ws)):
+            with pytest.raises(ValueError):
+                call()
+    # a layout made by hand: the same arrays are taken, others refused
+    args = (lay.rows, lay.sources, lay.m_indices, lay.counts, lay.rows_total, 0, 4)
+    mine = dg.MoeLayout(*args)
+    assert torch.equal(dg.dg_moe_combine(dg.dg_moe_dispatch(x, mine), mine), 2 * x)
+    for at, bad in ((0, lay.rows.long()), (0, lay.rows.cpu()), (0, lay.rows.view(-1)), (0, lay.rows.t()), (1, lay.sources[1:]),
+                    (1, lay.sources.cpu()), (2, None), (2, lay.m_indices.long()), (3, lay.counts[:3]), (4, lay.rows_total - 1),
+                    (5, 128), (5, -1)):
+        with pytest.raises(ValueError):
+            dg.MoeLayout(*(bad if i == at else v for i, v in enumerate(args)))
+    masked = dg.dg_moe_layout(ids, 4, rows_per_expert=16)
+    dg.MoeLayout(masked.rows, masked.sources, None, masked.counts, 64, 16, 4)
+    with pytest.raises(ValueError):
+        dg.MoeLayout(masked.rows, masked.sources, None, masked.counts, 64, 16, 5)
