@@ -125,7 +125,7 @@ __device__ __forceinline__ void store_out4(void* d, int dtype, int64_t at, const
 // that nothing reads.
 //
 // Bound by the matrix cores: 16384 x 7168 x 16384 runs at 2.65e15 operations/s (1450 us, 1424 to 1482 over several
-// boxes), 4096 x 4096 x 7168 at 2.45e15 (98 us, one round of 256 tiles: its first loads and its stores are not
+// cards), 4096 x 4096 x 7168 at 2.45e15 (98 us, one round of 256 tiles: its first loads and its stores are not
 // hidden).  The rate depends on the operands' bits (zeros 3.2e15, random codes 2.65e15): power holds the clock, not the
 // instruction stream.  32x32x32 products in the place of
 // 16x16x64 ones ran at 2.53e15; a 256x128 tile was slower for the grouped forms; the smaller tile serves
