@@ -28,6 +28,11 @@ Functions carry the C names:
 * 8-bit integer GEMMs (one scale per token, one per output channel): ``dg_quantize_int8_per_token(x)`` ->
   (q int8, s float32); ``dg_gemm_int8_nt``, ``dg_gemm_int8_nt_act_quant``,
   ``dg_gemm_int8_grouped_contiguous``, ``dg_gemm_int8_grouped_masked`` -> d bf16, fp16 or fp32
+* gated activation on two projections side by side: ``dg_gated_act`` / ``_fp8`` / ``_int8`` (pre (..., 2N) ->
+  act(g) * u, quantized or not), ``dg_gated_act_grad`` and ``dg_gated_act_grad_fp8`` (the operands of the backward
+  FP8 products)
+* residual norms: ``dg_residual_norm`` / ``_fp8`` / ``_int8`` (norm, gate, residual sum and the next block's norm in
+  one pass) and ``dg_residual_norm_grad`` (``ResidualNormGrad``)
 * utilities ``dg_get_num_cus``, ``dg_set_num_cus``,
   ``dg_get_m_alignment_for_contiguous_layout``, ``dg_get_scale_ld``,
   ``dg_gemm_workspace_size``.
@@ -36,6 +41,7 @@ Activation scales use the K-group-major layout of the library: ``sa[kb, row]``
 (for the masked form ``sa[g, kb, row]``), row stride ``ld_sa = sa.shape[-1]``.
 """
 
+import collections
 import ctypes
 import os
 import threading
@@ -111,6 +117,22 @@ _SIGNATURES = {
                                                    _c_int64, _vp, ctypes.c_size_t, _vp]),
     "dg_gemm_int8_config_name": (ctypes.c_char_p, [ctypes.c_int, _c_int64, _c_int64, _c_int64, _c_int64]),
     "dg_gemm_int8_workspace_size": (ctypes.c_size_t, [_c_int64, _c_int64, _c_int64, _c_int64]),
+    "dg_gated_act": (ctypes.c_int, [_vp, _c_int, _c_int, _vp, _vp, _c_int64, _c_int64, _c_int64, _vp, _vp]),
+    "dg_gated_act_fp8": (ctypes.c_int, [_vp, _c_int, _c_int, _vp, _vp, _c_int64, _c_int64, _c_int64, _vp, _vp, _c_int64, _vp]),
+    "dg_gated_act_int8": (ctypes.c_int, [_vp, _c_int, _c_int, _vp, _vp, _c_int64, _c_int64, _c_int64, _vp, _vp, _vp]),
+    "dg_gated_act_grad": (ctypes.c_int, [_vp, _vp, _c_int, _c_int, _c_int64, _c_int64, _vp, _vp]),
+    "dg_gated_act_grad_fp8": (ctypes.c_int, [_vp, _vp, _c_int, _c_int, _c_int64, _c_int64, _vp, _vp, _c_int64, _vp, _vp,
+                                             _c_int64, _vp, _vp, _c_int64, _vp]),
+    "dg_residual_norm": (ctypes.c_int, [_vp, _vp, _c_int, _c_int, _vp, _vp, _c_int64, _c_int, _vp, ctypes.c_float,
+                                        ctypes.c_float, _c_int64, _c_int64, _vp, _vp, _vp]),
+    "dg_residual_norm_fp8": (ctypes.c_int, [_vp, _vp, _c_int, _c_int, _vp, _vp, _c_int64, _c_int, _vp, ctypes.c_float,
+                                            ctypes.c_float, _c_int64, _c_int64, _vp, _vp, _vp, _c_int64, _vp]),
+    "dg_residual_norm_int8": (ctypes.c_int, [_vp, _vp, _c_int, _c_int, _vp, _vp, _c_int64, _c_int, _vp, ctypes.c_float,
+                                             ctypes.c_float, _c_int64, _c_int64, _vp, _vp, _vp, _vp]),
+    "dg_residual_norm_grad": (ctypes.c_int, [_vp, _vp, _vp, _vp, _c_int, _c_int, _vp, _vp, _c_int64, _c_int, _vp,
+                                             ctypes.c_float, ctypes.c_float, _c_int64, _c_int64, _vp, _vp, _vp, _vp, _vp,
+                                             _vp, ctypes.c_size_t, _vp]),
+    "dg_residual_norm_grad_workspace_size": (ctypes.c_size_t, [_c_int64, _c_int64]),
     "dg_get_num_cus": (ctypes.c_int, []),
     "dg_set_num_cus": (ctypes.c_int, [ctypes.c_int]),
     "dg_get_m_alignment_for_contiguous_layout": (ctypes.c_int, []),
@@ -863,3 +885,255 @@ def dg_gemm_int8_grouped_masked(a, sa, b, sb, masked_m, d=None, out_dtype=torch.
            lib().dg_gemm_int8_grouped_masked(_ptr(a), _ptr(sa), _ptr(b), _ptr(sb), _ptr(d), _dtype(d, "d"), _ptr(masked_m),
                                              g, m_max, n, k, *_ws(workspace), _stream(a)))
     return d
+
+
+# ---------------------------------------------------------------------------
+# the gated activation
+# ---------------------------------------------------------------------------
+
+_ACTS = {"silu": 0, "gelu": 1}
+
+
+def _act(act):
+    _require(act in _ACTS, "act must be 'silu' or 'gelu' (the tanh form)")
+    return _ACTS[act]
+
+
+def _one_device(*ts):
+    """Contiguous tensors (or None) on one device: that device."""
+    ts = [t for t in ts if t is not None]
+    dev = _dev(*ts)
+    for t in ts:
+        _require(t.device == dev, "tensors must be on one device")
+    return dev
+
+
+def _run(name, dev, *args):
+    """A library call on the current stream of `dev`, which need not be the current device."""
+    fn = getattr(lib(), name)
+    if dev.index == torch.cuda.current_device():
+        status = fn(*args, _stream_handle(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, _stream_handle(dev))
+    if status != 0:
+        raise DGError(name, status)
+
+
+def _like(t, shape, dtype, device, what):
+    """The caller's output if it has this shape and type, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _require(t.dtype == dtype and tuple(t.shape) == tuple(shape), f"{what} must be {dtype} {tuple(shape)}")
+    return t
+
+
+def _scales_like(s, lead, groups, device):
+    """Group-major scales (..., groups, ld) of rows with these leading dimensions: the caller's, or new ones."""
+    shape = (*lead[:-1], groups)
+    if s is None:
+        return torch.empty((*shape, dg_get_scale_ld(lead[-1])), dtype=torch.float32, device=device)
+    _require(s.dtype == torch.float32 and tuple(s.shape[:-1]) == shape and s.shape[-1] >= lead[-1] and s.shape[-1] % 4 == 0,
+             f"scales must be float32 {shape} with a last dimension of at least {lead[-1]}, a multiple of 4")
+    return s
+
+
+def _act_rows(pre, act, m_indices, masked_m):
+    """(lead, n, arguments of the call) of projections pre (rows, 2N) or (G, M_max, 2N)."""
+    _require(pre.dim() in (2, 3) and pre.shape[-1] % 2 == 0 and pre.shape[-1] > 0, "pre must be (rows, 2N) or (G, M_max, 2N)")
+    lead, n = tuple(pre.shape[:-1]), pre.shape[-1] // 2
+    _require((masked_m is None) == (pre.dim() == 2), "masked_m goes with pre (G, M_max, 2N)")
+    _require(m_indices is None or (m_indices.dtype == torch.int32 and pre.dim() == 2 and m_indices.numel() == lead[0]),
+             "m_indices must be int32, one per row of pre (rows, 2N)")
+    _require(masked_m is None or (masked_m.dtype == torch.int32 and masked_m.numel() == lead[0]),
+             "masked_m must be int32, one per group")
+    rows = lead[0] if pre.dim() == 2 else lead[0] * lead[1]
+    return lead, n, (_ptr(pre), _dtype(pre, "pre"), _act(act), _ptr(m_indices), _ptr(masked_m),
+                     lead[1] if pre.dim() == 3 and rows else 0, rows, n)
+
+
+def dg_gated_act(pre, act="silu", h=None, m_indices=None, masked_m=None):
+    """h (rows, N) = act(g) * u from pre (rows, 2N) = (g | u) float32 / bfloat16 / float16, in that type; act 'silu' or
+    'gelu' (tanh form).  With m_indices int32 (rows,) the rows of a negative index stay untouched; pre (G, M_max, 2N)
+    with masked_m int32 (G,): only each group's first masked_m[g] rows."""
+    lead, n, args = _act_rows(pre, act, m_indices, masked_m)
+    h = _like(h, (*lead, n), pre.dtype, pre.device, "h")
+    dev = _one_device(pre, h, m_indices, masked_m)
+    if h.numel():
+        _run("dg_gated_act", dev, *args, _ptr(h))
+    return h
+
+
+def dg_gated_act_fp8(pre, act="silu", q=None, s=None, m_indices=None, masked_m=None):
+    """dg_gated_act's h as dg_quantize_per_token_group would quantize it in fp32: (q uint8 (rows, N), s float32
+    (ceil(N/128), ld)), or (G, M_max, N) and (G, ceil(N/128), ld) with masked_m."""
+    lead, n, args = _act_rows(pre, act, m_indices, masked_m)
+    q = _like(None if q is None else _bytes(q), (*lead, n), torch.uint8, pre.device, "q")
+    s = _scales_like(s, lead, -(-n // 128), pre.device)
+    dev = _one_device(pre, q, s, m_indices, masked_m)
+    if q.numel():
+        _run("dg_gated_act_fp8", dev, *args, _ptr(q), _ptr(s), s.shape[-1])
+    return q, s
+
+
+def dg_gated_act_int8(pre, act="silu", q=None, s=None, m_indices=None, masked_m=None):
+    """dg_gated_act's h as dg_quantize_int8_per_token would quantize it in fp32: (q int8 like h, s float32 per row)."""
+    lead, n, args = _act_rows(pre, act, m_indices, masked_m)
+    q = _like(q, (*lead, n), torch.int8, pre.device, "q")
+    s = _like(s, lead, torch.float32, pre.device, "s")
+    dev = _one_device(pre, q, s, m_indices, masked_m)
+    if q.numel():
+        _run("dg_gated_act_int8", dev, *args, _ptr(q), _ptr(s))
+    return q, s
+
+
+def _act_grad_rows(dh, pre):
+    _require(pre.dim() == 2 and pre.shape[1] % 2 == 0 and pre.shape[1] > 0, "pre must be (rows, 2N)")
+    rows, n = pre.shape[0], pre.shape[1] // 2
+    _require(dh.dtype == pre.dtype and tuple(dh.shape) == (rows, n), "dh must be (rows, N) in pre's type")
+    return rows, n
+
+
+def dg_gated_act_grad(dh, pre, act="silu", dpre=None):
+    """The gradient of pre (rows, 2N) from dh (rows, N) of dg_gated_act, both in one type, in that type."""
+    rows, n = _act_grad_rows(dh, pre)
+    dpre = _like(dpre, pre.shape, pre.dtype, pre.device, "dpre")
+    dev = _one_device(dh, pre, dpre)
+    if rows:
+        _run("dg_gated_act_grad", dev, _ptr(dh), _ptr(pre), _dtype(pre, "pre"), _act(act), rows, n, _ptr(dpre))
+    return dpre
+
+
+def dg_gated_act_grad_fp8(dh, pre, act="silu", rows_wanted=True, columns_wanted=True, h_wanted=True):
+    """What the backward FP8 products read, from dh (rows, N) and pre (rows, 2N) in one pass:
+    (q uint8 (rows, 2N), s float32 (2N/128, ld)) as dg_quantize_per_token_group of dpre, (qt uint8 (2N, rows), st
+    float32 (ceil(rows/128), ld)) as dg_quantize_per_channel_group of dpre, (ht uint8 (N, rows), hst) likewise of h;
+    returned as (q, s, qt, st, ht, hst), None for pairs that are not wanted.  N a multiple of 128, rows of 16."""
+    rows, n = _act_grad_rows(dh, pre)
+    _require(n % 128 == 0 and rows % 16 == 0, "N must be a multiple of 128 and rows one of 16")
+    _require(rows_wanted or columns_wanted or h_wanted, "no output is wanted")
+    dev, blocks, code = _one_device(dh, pre), -(-rows // 128), _act(act)
+    q = s = qt = st = ht = hst = None
+    if rows_wanted:
+        q = torch.empty((rows, 2 * n), dtype=torch.uint8, device=dev)
+        s = torch.empty((2 * n // 128, dg_get_scale_ld(rows)), dtype=torch.float32, device=dev)
+    if columns_wanted:
+        qt = torch.empty((2 * n, rows), dtype=torch.uint8, device=dev)
+        st = torch.empty((blocks, 2 * n), dtype=torch.float32, device=dev)
+    if h_wanted:
+        ht = torch.empty((n, rows), dtype=torch.uint8, device=dev)
+        hst = torch.empty((blocks, n), dtype=torch.float32, device=dev)
+    if rows:
+        _run("dg_gated_act_grad_fp8", dev, _ptr(dh), _ptr(pre), _dtype(pre, "pre"), code, rows, n, _ptr(q), _ptr(s),
+             rows, _ptr(qt), _ptr(st), 2 * n, _ptr(ht), _ptr(hst), n)
+    return q, s, qt, st, ht, hst
+
+
+# ---------------------------------------------------------------------------
+# residual norms
+# ---------------------------------------------------------------------------
+
+ResidualNormGrad = collections.namedtuple("ResidualNormGrad", "dx dresidual dweight dgate dpost_weight")
+
+
+def _norm_args(x, residual, dtype, weight, gate, post_norm, post_weight, scale, eps, what="residual"):
+    _require(residual.dim() == 2, f"{what} must be (rows, hidden)")
+    rows, hidden = residual.shape
+    code = _dtype(dtype, "x")
+    _require(residual.dtype in (dtype, torch.float32), f"{what} must be float32 or in x's type")
+    _require(x is None or (x.dtype == dtype and x.shape == residual.shape), f"x must be like {what}, (rows, hidden)")
+    _require(x is not None or (gate is None and not post_norm), "a gate or a first norm needs x")
+    for w, name in ((weight, "weight"), (post_weight, "post_weight")):
+        _require(w is None or (w.dtype == torch.float32 and tuple(w.shape) == (hidden,)), f"{name} must be float32 (hidden,)")
+    _require(post_weight is None or post_norm, "post_weight goes with post_norm")
+    gate_rows = 0
+    if gate is not None:
+        _require(gate.dtype == dtype and gate.shape[-1] == hidden and gate.dim() in (1, 2),
+                 "gate must be (hidden,) or (gate_rows, hidden) in x's type")
+        gate_rows = gate.shape[0] if gate.dim() == 2 else 1
+        _require(gate_rows > 0 and rows % gate_rows == 0 or rows == gate_rows == 0, "the gate's rows must divide the rows")
+    return rows, hidden, (code, _DTYPES[residual.dtype], _ptr(weight), _ptr(gate) if gate_rows else None, gate_rows,
+                          int(bool(post_norm)), _ptr(post_weight), float(scale), float(eps), rows, hidden)
+
+
+def _norm_sum(x, residual, total):
+    """Where the sum goes: (tensor returned as the sum, the call's pointer)."""
+    if x is None:
+        _require(total is None, "without x the sum is the residual")
+        return residual, None
+    total = _like(total, residual.shape, residual.dtype, residual.device, "sum")
+    return total, _ptr(total)
+
+
+def dg_residual_norm(x, residual, weight=None, gate=None, post_norm=False, post_weight=None, scale=1.0, eps=1e-6, sum=None,
+                     y=None, dtype=None):
+    """(sum, y) (rows, hidden) of one pass between two blocks: z = post_weight * x / rms(x) with post_norm, else x;
+    sum = residual + scale * gate * z (residual float32 or in x's type; `sum` may be residual itself: in place); y =
+    weight * sum / rms(sum) in x's type.  gate (hidden,) or (gate_rows, hidden) in x's type, gate_rows dividing rows: each
+    gate row serves that many consecutive rows.  weights float32, None for ones.  x None: the norm alone (sum is residual),
+    y in `dtype`, by default residual's."""
+    t = x.dtype if x is not None else dtype or residual.dtype
+    rows, hidden, args = _norm_args(x, residual, t, weight, gate, post_norm, post_weight, scale, eps)
+    total, at = _norm_sum(x, residual, sum)
+    y = _like(y, (rows, hidden), t, residual.device, "y")
+    dev = _one_device(x, residual, weight, gate, post_weight, total, y)
+    _run("dg_residual_norm", dev, _ptr(x), _ptr(residual), *args, at, _ptr(y))
+    return total, y
+
+
+def dg_residual_norm_fp8(x, residual, weight=None, gate=None, post_norm=False, post_weight=None, scale=1.0, eps=1e-6,
+                         sum=None, q=None, s=None):
+    """dg_residual_norm with y as dg_quantize_per_token_group would quantize it in fp32: (sum, q uint8 (rows, hidden), s
+    float32 (ceil(hidden/128), ld))."""
+    t = x.dtype if x is not None else residual.dtype
+    rows, hidden, args = _norm_args(x, residual, t, weight, gate, post_norm, post_weight, scale, eps)
+    total, at = _norm_sum(x, residual, sum)
+    q = _like(None if q is None else _bytes(q), (rows, hidden), torch.uint8, residual.device, "q")
+    s = _scales_like(s, (rows,), -(-hidden // 128), residual.device)
+    dev = _one_device(x, residual, weight, gate, post_weight, total, q, s)
+    _run("dg_residual_norm_fp8", dev, _ptr(x), _ptr(residual), *args, at, _ptr(q), _ptr(s), s.shape[-1])
+    return total, q, s
+
+
+def dg_residual_norm_int8(x, residual, weight=None, gate=None, post_norm=False, post_weight=None, scale=1.0, eps=1e-6,
+                          sum=None, q=None, s=None):
+    """dg_residual_norm with y as dg_quantize_int8_per_token would quantize it in fp32: (sum, q int8 (rows, hidden), s
+    float32 (rows,))."""
+    t = x.dtype if x is not None else residual.dtype
+    rows, hidden, args = _norm_args(x, residual, t, weight, gate, post_norm, post_weight, scale, eps)
+    total, at = _norm_sum(x, residual, sum)
+    q = _like(q, (rows, hidden), torch.int8, residual.device, "q")
+    s = _like(s, (rows,), torch.float32, residual.device, "s")
+    dev = _one_device(x, residual, weight, gate, post_weight, total, q, s)
+    _run("dg_residual_norm_int8", dev, _ptr(x), _ptr(residual), *args, at, _ptr(q), _ptr(s))
+    return total, q, s
+
+
+def dg_residual_norm_grad_workspace_size(rows, hidden):
+    return lib().dg_residual_norm_grad_workspace_size(int(rows), int(hidden))
+
+
+def dg_residual_norm_grad(dy, dsum, x, sum, weight=None, gate=None, post_norm=False, post_weight=None, scale=1.0, eps=1e-6,
+                          dx=None, dresidual=None, workspace=None):
+    """Gradients of dg_residual_norm from dy (rows, hidden) in x's type, dsum (what the sum gets from elsewhere, in the
+    residual's type; None for nothing), x (None as there) and the sum that it returned -> ResidualNormGrad(dx, dresidual,
+    dweight float32 (hidden,), dgate like gate, dpost_weight float32 (hidden,)), None where there is nothing to have one.
+    `dresidual` may be dsum itself."""
+    rows, hidden, args = _norm_args(x, sum, dy.dtype, weight, gate, post_norm, post_weight, scale, eps, what="sum")
+    _require(dy.shape == sum.shape, "dy must be (rows, hidden) in x's type")
+    _require(dsum is None or (dsum.dtype == sum.dtype and dsum.shape == sum.shape), "dsum must be like sum")
+    device = sum.device
+    _require(x is not None or dx is None, "dx without x")
+    dx = _like(dx, sum.shape, dy.dtype, device, "dx") if x is not None else None
+    dresidual = _like(dresidual, sum.shape, sum.dtype, device, "dresidual")
+    dweight = torch.empty(hidden, dtype=torch.float32, device=device) if weight is not None else None
+    dgate = torch.empty_like(gate) if gate is not None else None
+    dpost = torch.empty(hidden, dtype=torch.float32, device=device) if post_weight is not None else None
+    if workspace is None and (dweight is not None or dgate is not None or dpost is not None):
+        need = lib().dg_residual_norm_grad_workspace_size(rows, hidden)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    dev = _one_device(dy, dsum, x, sum, weight, gate, post_weight, dx, dresidual, workspace)
+    _run("dg_residual_norm_grad", dev, _ptr(dy), _ptr(dsum), _ptr(x), _ptr(sum), *args, _ptr(dx), _ptr(dresidual),
+         _ptr(dweight), _ptr(dgate), _ptr(dpost), *_ws(workspace))
+    return ResidualNormGrad(dx, dresidual, dweight, dgate, dpost)

@@ -73,6 +73,24 @@ void gemm_int8_config_name(int layout, int64_t m, int64_t n, int64_t k, int64_t 
 size_t int8_workspace_size(int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus);
 size_t int8_act_quant_workspace_size(int64_t m, int64_t n, int64_t k, int num_cus);
 
+int launch_gated_act(int form, const void* pre, int dtype, int act, const int32_t* m_indices, const int32_t* masked_m,
+                     int64_t rows_per_group, int64_t rows, int64_t n, void* h, float* scales, int64_t ld_s,
+                     hipStream_t stream);
+int launch_gated_act_grad(const void* dh, const void* pre, int dtype, int act, int64_t rows, int64_t n, void* dpre,
+                          hipStream_t stream);
+int launch_gated_act_grad_fp8(const void* dh, const void* pre, int dtype, int act, int64_t rows, int64_t n, uint8_t* q,
+                              float* s, int64_t ld_s, uint8_t* qt, float* st, int64_t ld_st, uint8_t* ht, float* hst,
+                              int64_t ld_hst, hipStream_t stream);
+int launch_residual_norm(int out, const void* x, const void* residual, int dtype, int residual_dtype, const float* weight,
+                         const void* gate, int64_t gate_rows, bool post_norm, const float* post_weight, float scale,
+                         float eps, int64_t rows, int64_t hidden, void* sum, void* y, float* scales, int64_t ld_s,
+                         hipStream_t stream);
+size_t residual_norm_grad_workspace_size(int64_t rows, int64_t hidden);
+int launch_residual_norm_grad(const void* dy, const void* dsum, const void* x, const void* sum, int dtype,
+                              int residual_dtype, const float* weight, const void* gate, int64_t gate_rows, bool post_norm,
+                              const float* post_weight, float scale, float eps, int64_t rows, int64_t hidden, void* dx,
+                              void* dresidual, float* dweight, void* dgate, float* dpost, void* ws, hipStream_t stream);
+
 static thread_local char g_msg[512] = "";
 
 int set_error(int status, const char* fmt, ...) {
@@ -677,6 +695,169 @@ int dg_gemm_int8_grouped_masked(const int8_t* a, const float* sa, const int8_t* 
   if (cus < 0) return cus;
   return launch_gemm_int8(2, a, sa, b, sb, d, out_dtype, nullptr, masked_m, num_groups, m_max, n, k, workspace,
                           workspace ? workspace_bytes : 0, static_cast<hipStream_t>(stream), cus);
+}
+
+// ---- gated activation ---------------------------------------------------------------------------
+static int check_act(const char* what, int dtype, int act, int64_t rows, int64_t n) {
+  DG_REQUIRE(known_dtype(dtype), "%s: unknown dtype %d", what, dtype);
+  DG_REQUIRE(act == DG_ACT_SILU || act == DG_ACT_GELU, "%s: unknown activation %d", what, act);
+  DG_REQUIRE(rows >= 0 && n > 0 && n % kKAlign == 0, "%s: need rows >= 0, n > 0, n %% 16 == 0 (rows=%lld n=%lld)", what,
+             (long long)rows, (long long)n);
+  DG_REQUIRE(n <= kInt31 / 64 && rows <= kInt31, "%s: dimension too large", what);
+  return DG_OK;
+}
+
+static int gated_act(const char* what, int form, const void* pre, int dtype, int act, const int32_t* m_indices,
+                     const int32_t* masked_m, int64_t rows_per_group, int64_t rows, int64_t n, void* h, float* s,
+                     int64_t ld_s, dg_stream_t stream) {
+  const int c = check_act(what, dtype, act, rows, n);
+  if (c != DG_OK) return c;
+  DG_REQUIRE(m_indices == nullptr || masked_m == nullptr, "%s: m_indices or masked_m, not both", what);
+  DG_REQUIRE(masked_m != nullptr ? rows_per_group > 0 && rows % rows_per_group == 0 : rows_per_group == 0,
+             "%s: rows_per_group goes with masked_m and divides rows (rows_per_group=%lld rows=%lld)", what,
+             (long long)rows_per_group, (long long)rows);
+  if (form == 1) {
+    const int64_t need = masked_m != nullptr ? rows_per_group : rows;
+    DG_REQUIRE(ld_s >= need && ld_s % 4 == 0, "%s: need ld_s >= %lld and ld_s %% 4 == 0 (ld_s=%lld)", what, (long long)need,
+               (long long)ld_s);
+  }
+  if (rows == 0) return DG_OK;
+  DG_REQUIRE(pre && h && (form == 0 || s), "%s: null pointer", what);
+  DG_REQUIRE(aligned16(pre) && aligned16(h), "%s: row data must be 16-byte aligned", what);
+  DG_REQUIRE(aligned_to(s, 4) && aligned_to(m_indices, 4) && aligned_to(masked_m, 4), "%s: misaligned pointer", what);
+  return launch_gated_act(form, pre, dtype, act, m_indices, masked_m, rows_per_group, rows, n, h, s, ld_s,
+                          static_cast<hipStream_t>(stream));
+}
+
+int dg_gated_act(const void* pre, int dtype, int act, const int32_t* m_indices, const int32_t* masked_m,
+                 int64_t rows_per_group, int64_t rows, int64_t n, void* h, dg_stream_t stream) {
+  return gated_act("gated_act", 0, pre, dtype, act, m_indices, masked_m, rows_per_group, rows, n, h, nullptr, 0, stream);
+}
+
+int dg_gated_act_fp8(const void* pre, int dtype, int act, const int32_t* m_indices, const int32_t* masked_m,
+                     int64_t rows_per_group, int64_t rows, int64_t n, uint8_t* q, float* s, int64_t ld_s,
+                     dg_stream_t stream) {
+  return gated_act("gated_act_fp8", 1, pre, dtype, act, m_indices, masked_m, rows_per_group, rows, n, q, s, ld_s, stream);
+}
+
+int dg_gated_act_int8(const void* pre, int dtype, int act, const int32_t* m_indices, const int32_t* masked_m,
+                      int64_t rows_per_group, int64_t rows, int64_t n, int8_t* q, float* s, dg_stream_t stream) {
+  return gated_act("gated_act_int8", 2, pre, dtype, act, m_indices, masked_m, rows_per_group, rows, n, q, s, 0, stream);
+}
+
+int dg_gated_act_grad(const void* dh, const void* pre, int dtype, int act, int64_t rows, int64_t n, void* dpre,
+                      dg_stream_t stream) {
+  const int c = check_act("gated_act_grad", dtype, act, rows, n);
+  if (c != DG_OK) return c;
+  if (rows == 0) return DG_OK;
+  DG_REQUIRE(dh && pre && dpre, "gated_act_grad: null pointer");
+  DG_REQUIRE(aligned16(dh) && aligned16(pre) && aligned16(dpre), "gated_act_grad: row data must be 16-byte aligned");
+  return launch_gated_act_grad(dh, pre, dtype, act, rows, n, dpre, static_cast<hipStream_t>(stream));
+}
+
+int dg_gated_act_grad_fp8(const void* dh, const void* pre, int dtype, int act, int64_t rows, int64_t n, uint8_t* q,
+                          float* s, int64_t ld_s, uint8_t* qt, float* st, int64_t ld_st, uint8_t* ht, float* hst,
+                          int64_t ld_hst, dg_stream_t stream) {
+  const int c = check_act("gated_act_grad_fp8", dtype, act, rows, n);
+  if (c != DG_OK) return c;
+  DG_REQUIRE(n % kGroup == 0 && rows % kKAlign == 0, "gated_act_grad_fp8: need n %% 128 == 0 and rows %% 16 == 0 (rows=%lld n=%lld)",
+             (long long)rows, (long long)n);
+  if (rows == 0) return DG_OK;
+  DG_REQUIRE(dh && pre && (q || qt || ht), "gated_act_grad_fp8: null pointer");
+  DG_REQUIRE((q == nullptr) == (s == nullptr) && (qt == nullptr) == (st == nullptr) && (ht == nullptr) == (hst == nullptr),
+             "gated_act_grad_fp8: codes and scales are given together");
+  DG_REQUIRE((!q || (ld_s >= rows && ld_s % 4 == 0)) && (!qt || (ld_st >= 2 * n && ld_st % 4 == 0)) &&
+                 (!ht || (ld_hst >= n && ld_hst % 4 == 0)),
+             "gated_act_grad_fp8: need ld_s >= rows, ld_st >= 2n, ld_hst >= n, multiples of 4");
+  DG_REQUIRE(aligned16(dh) && aligned16(pre) && aligned16(q) && aligned16(s) && aligned16(qt) && aligned16(st) &&
+                 aligned16(ht) && aligned16(hst), "gated_act_grad_fp8: pointers must be 16-byte aligned");
+  return launch_gated_act_grad_fp8(dh, pre, dtype, act, rows, n, q, s, ld_s, qt, st, ld_st, ht, hst, ld_hst,
+                                   static_cast<hipStream_t>(stream));
+}
+
+// ---- residual norms -----------------------------------------------------------------------------
+static int check_norm(const char* what, int dtype, int residual_dtype, const void* x, const float* weight, const void* gate,
+                      int64_t gate_rows, int post_norm, const float* post_weight, float eps, int64_t rows, int64_t hidden) {
+  DG_REQUIRE(known_dtype(dtype) && (residual_dtype == dtype || residual_dtype == DG_DTYPE_F32),
+             "%s: unknown dtype %d, or residual_dtype %d neither that nor fp32", what, dtype, residual_dtype);
+  DG_REQUIRE(rows >= 0 && hidden > 0 && hidden % kKAlign == 0, "%s: need rows >= 0, hidden > 0, hidden %% 16 == 0 "
+             "(rows=%lld hidden=%lld)", what, (long long)rows, (long long)hidden);
+  DG_REQUIRE((gate == nullptr) == (gate_rows == 0) && gate_rows >= 0 && (gate_rows == 0 || rows % gate_rows == 0),
+             "%s: gate_rows must divide rows, 0 without a gate (gate_rows=%lld rows=%lld)", what, (long long)gate_rows,
+             (long long)rows);
+  DG_REQUIRE(x != nullptr || rows == 0 || (gate == nullptr && !post_norm), "%s: a gate or a first norm without x", what);
+  DG_REQUIRE(post_norm || post_weight == nullptr, "%s: post_weight without post_norm", what);
+  DG_REQUIRE(eps >= 0.0f && eps <= 3.0e38f, "%s: eps must be finite and not negative", what);
+  DG_REQUIRE(aligned16(x) && aligned16(gate) && aligned16(weight) && aligned16(post_weight),
+             "%s: pointers must be 16-byte aligned", what);
+  return DG_OK;
+}
+
+static int residual_norm(const char* what, int out, const void* x, const void* residual, int dtype, int residual_dtype,
+                         const float* weight, const void* gate, int64_t gate_rows, int post_norm,
+                         const float* post_weight, float scale, float eps, int64_t rows, int64_t hidden, void* sum, void* y,
+                         float* s, int64_t ld_s, dg_stream_t stream) {
+  const int c = check_norm(what, dtype, residual_dtype, x, weight, gate, gate_rows, post_norm, post_weight, eps, rows, hidden);
+  if (c != DG_OK) return c;
+  DG_REQUIRE(out != 1 || (ld_s >= rows && ld_s % 4 == 0), "%s: need ld_s >= rows and ld_s %% 4 == 0 (ld_s=%lld)", what,
+             (long long)ld_s);
+  if (rows == 0) return DG_OK;
+  DG_REQUIRE(residual && y && (out == 0 || s), "%s: null pointer", what);
+  DG_REQUIRE(x != nullptr || sum == nullptr, "%s: without x the sum is the residual: sum must be null", what);
+  DG_REQUIRE(aligned16(residual) && aligned16(sum) && aligned16(y), "%s: row data must be 16-byte aligned", what);
+  DG_REQUIRE(aligned_to(s, 4), "%s: misaligned pointer", what);
+  return launch_residual_norm(out, x, residual, dtype, residual_dtype, weight, gate, gate_rows, post_norm != 0, post_weight,
+                              scale, eps, rows, hidden, sum, y, s, ld_s, static_cast<hipStream_t>(stream));
+}
+
+int dg_residual_norm(const void* x, const void* residual, int dtype, int residual_dtype, const float* weight,
+                     const void* gate, int64_t gate_rows, int post_norm, const float* post_weight, float scale, float eps,
+                     int64_t rows, int64_t hidden, void* sum, void* y, dg_stream_t stream) {
+  return residual_norm("residual_norm", 0, x, residual, dtype, residual_dtype, weight, gate, gate_rows, post_norm,
+                       post_weight, scale, eps, rows, hidden, sum, y, nullptr, 0, stream);
+}
+
+int dg_residual_norm_fp8(const void* x, const void* residual, int dtype, int residual_dtype, const float* weight,
+                         const void* gate, int64_t gate_rows, int post_norm, const float* post_weight, float scale,
+                         float eps, int64_t rows, int64_t hidden, void* sum, uint8_t* q, float* s, int64_t ld_s,
+                         dg_stream_t stream) {
+  return residual_norm("residual_norm_fp8", 1, x, residual, dtype, residual_dtype, weight, gate, gate_rows, post_norm,
+                       post_weight, scale, eps, rows, hidden, sum, q, s, ld_s, stream);
+}
+
+int dg_residual_norm_int8(const void* x, const void* residual, int dtype, int residual_dtype, const float* weight,
+                          const void* gate, int64_t gate_rows, int post_norm, const float* post_weight, float scale,
+                          float eps, int64_t rows, int64_t hidden, void* sum, int8_t* q, float* s, dg_stream_t stream) {
+  return residual_norm("residual_norm_int8", 2, x, residual, dtype, residual_dtype, weight, gate, gate_rows, post_norm,
+                       post_weight, scale, eps, rows, hidden, sum, q, s, 0, stream);
+}
+
+size_t dg_residual_norm_grad_workspace_size(int64_t rows, int64_t hidden) {
+  if (rows <= 0 || hidden <= 0 || hidden % kKAlign || rows > kInt31 || hidden > kInt31) return 0;
+  return residual_norm_grad_workspace_size(rows, hidden);
+}
+
+int dg_residual_norm_grad(const void* dy, const void* dsum, const void* x, const void* sum, int dtype, int residual_dtype,
+                          const float* weight, const void* gate, int64_t gate_rows, int post_norm,
+                          const float* post_weight, float scale, float eps, int64_t rows, int64_t hidden, void* dx,
+                          void* dresidual, float* dweight, void* dgate, float* dpost_weight, void* workspace,
+                          size_t workspace_bytes, dg_stream_t stream) {
+  const char* what = "residual_norm_grad";
+  const int c = check_norm(what, dtype, residual_dtype, x, weight, gate, gate_rows, post_norm, post_weight, eps, rows, hidden);
+  if (c != DG_OK) return c;
+  DG_REQUIRE(rows == 0 || (dy && sum && dresidual && (x == nullptr) == (dx == nullptr)), "%s: null pointer", what);
+  DG_REQUIRE(weight || !dweight, "%s: dweight without a weight", what);
+  DG_REQUIRE(gate || !dgate, "%s: dgate without a gate", what);
+  DG_REQUIRE(post_weight || !dpost_weight, "%s: dpost_weight without a post_weight", what);
+  DG_REQUIRE(aligned16(dy) && aligned16(dsum) && aligned16(sum) && aligned16(dx) && aligned16(dresidual) &&
+                 aligned16(dweight) && aligned16(dgate) && aligned16(dpost_weight) && aligned16(workspace),
+             "%s: pointers must be 16-byte aligned", what);
+  const size_t need = dweight || dgate || dpost_weight ? dg_residual_norm_grad_workspace_size(rows, hidden) : 0;
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need))
+    return set_error(kWorkspace, "%s: workspace of %zu bytes, %zu needed", what, workspace ? workspace_bytes : (size_t)0, need);
+  return launch_residual_norm_grad(dy, dsum, x, sum, dtype, residual_dtype, weight, gate, gate_rows, post_norm != 0,
+                                   post_weight, scale, eps, rows, hidden, dx, dresidual, dweight, dgate, dpost_weight,
+                                   workspace, static_cast<hipStream_t>(stream));
 }
 
 int dg_get_debug_status(uint32_t* flags, int64_t* block, int clear) {

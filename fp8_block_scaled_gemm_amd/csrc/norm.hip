@@ -1,0 +1,607 @@
+// What lies between two blocks of a transformer, one pass over its rows (the arithmetic is fp32 throughout):
+//   z = v * x * rsqrt(mean(x^2) + eps)        the norm after the first block (or z = x without one)
+//   s = r + scale * gate * z                  its gate and residual scale, and the residual stream
+//   y = w * s * rsqrt(mean(s^2) + eps)        the norm before the second block
+// with y in x's type, or quantized for an FP8 or int8 product as the library's quantizers would quantize it.
+// And the backward pass: from dy, ds (the gradient that s gets from later blocks), x and s as it was stored,
+//   du = ds + rho * (dy w - s rho^2 mean(dy w s)),  rho = rsqrt(mean(s^2) + eps)       -> dr = du
+//   dz = scale * gate * du,  dgate = scale * sum(z du),  dw = sum(dy s rho)
+//   dx = sigma * (dz v - x sigma^2 mean(dz v x)),  sigma = rsqrt(mean(x^2) + eps),  dv = sum(dz x sigma)
+// Bound by memory: a row is read once into registers, its sums of squares are reduced there.
+#include "rows.hpp"
+
+namespace dg {
+
+enum NormOut : int { kNormSame = 0, kNormFp8 = 1, kNormInt8 = 2 };
+
+struct NormParams {
+  const void* x;              // null: s = r
+  const void* residual;
+  const float* weight;        // null: ones
+  const float* post_weight;   // null: ones
+  const void* gate;           // null: none
+  void* sum;                  // null: not stored
+  void* y;                    // y, or its codes
+  float* scales;
+  int64_t ld_s;
+  int64_t rows, rows_per_gate;
+  int hidden, post_norm;
+  float scale, eps;
+};
+
+// Sums of N values over the LT lanes of a row, the same on each of them: within waves, then over the waves in order.
+// Two calls in a row need different `red` arrays (no barrier keeps the first one's readers from the second's writers).
+template <int LT, int N>
+__device__ __forceinline__ void row_sums(float* v, float (*red)[N], int tid) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+  if constexpr (LT > 64) {
+    if ((tid & 63) == 0)
+#pragma unroll
+      for (int i = 0; i < N; ++i) red[tid >> 6][i] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float s = red[0][i];
+#pragma unroll
+      for (int w = 1; w < LT / 64; ++w) s += red[w][i];
+      v[i] = s;
+    }
+  }
+}
+
+// 1 / sqrt(mean + eps), both operations IEEE (one per row and lane: they cost nothing beside the row's memory traffic)
+__device__ __forceinline__ float inv_rms(float sum_sq, int hidden, float eps) {
+  return 1.0f / sqrtf(sum_sq / (float)hidden + eps);
+}
+
+constexpr int kNormThreads = 256;   // threads of a workgroup whose rows take one wave each
+
+template <int LT>
+constexpr int norm_threads() { return LT > kNormThreads ? LT : kNormThreads; }
+template <int LT>
+constexpr int norm_rows() { return LT >= kNormThreads ? 1 : kNormThreads / LT; }
+
+// LT lanes a row, V pieces of 8 elements a lane.
+template <class T, class TR, int OUT, int LT, int V>
+__global__ __launch_bounds__(norm_threads<LT>()) void residual_norm_kernel(NormParams p) {
+  constexpr int kWaves = LT / 64;
+  __shared__ float red_x[kWaves][1], red_s[kWaves][1];
+  __shared__ uint32_t red_max[kWaves];
+  const int tid = threadIdx.x % LT;
+  const int64_t row = (int64_t)blockIdx.x * norm_rows<LT>() + threadIdx.x / LT;
+  if (row >= p.rows) return;   // uniform over the row's waves, which share no barrier with another row's
+  const int64_t base = row * p.hidden;
+  const T* x = static_cast<const T*>(p.x);
+  const TR* r = static_cast<const TR*>(p.residual);
+  bool ok[V];
+  int at[V];
+  Raw8<TR> rr[V];
+  Raw8<T> rx[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    at[i] = 8 * (tid + LT * i);
+    ok[i] = at[i] < p.hidden;
+    if (ok[i]) rr[i] = load8(r + base + at[i]);
+    if (ok[i] && x != nullptr) rx[i] = load8(x + base + at[i]);
+  }
+  float s[V][8];
+  if (x != nullptr) {
+    float sigma = 1.0f;
+    if (p.post_norm) {
+      float sq[1] = {0.0f};
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (ok[i]) {
+          float v[8];
+          widen8(rx[i], v);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) sq[0] = __builtin_fmaf(v[c], v[c], sq[0]);
+        }
+      row_sums<LT, 1>(sq, red_x, tid);
+      sigma = inv_rms(sq[0], p.hidden, p.eps);
+    }
+    const T* gate = p.gate != nullptr ? static_cast<const T*>(p.gate) + (row / p.rows_per_gate) * p.hidden : nullptr;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (ok[i]) {
+        float v[8], z[8];
+        widen8(rr[i], v);
+        widen8(rx[i], z);
+        if (p.post_norm) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) z[c] *= sigma;
+          if (p.post_weight != nullptr) {
+            float w[8];
+            widen8(load8(p.post_weight + at[i]), w);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) z[c] *= w[c];
+          }
+        }
+        if (gate != nullptr) {
+          float g[8];
+          widen8(load8(gate + at[i]), g);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) z[c] *= g[c];
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) s[i][c] = __builtin_fmaf(p.scale, z[c], v[c]);
+        if (p.sum != nullptr) store8(static_cast<TR*>(p.sum) + base + at[i], narrow8<TR>(s[i]));
+      }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (ok[i]) widen8(rr[i], s[i]);
+  }
+  float sq[1] = {0.0f};
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (ok[i])
+#pragma unroll
+      for (int c = 0; c < 8; ++c) sq[0] = __builtin_fmaf(s[i][c], s[i][c], sq[0]);
+  row_sums<LT, 1>(sq, red_s, tid);
+  const float rho = inv_rms(sq[0], p.hidden, p.eps);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if (ok[i]) {
+      float w[8];
+      if (p.weight != nullptr) widen8(load8(p.weight + at[i]), w);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) s[i][c] = p.weight != nullptr ? s[i][c] * rho * w[c] : s[i][c] * rho;
+    } else {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) s[i][c] = 0.0f;
+    }
+  }
+  if constexpr (OUT == kNormSame) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (ok[i]) store8(static_cast<T*>(p.y) + base + at[i], narrow8<T>(s[i]));
+  } else if constexpr (OUT == kNormFp8) {
+    uint8_t* q = static_cast<uint8_t*>(p.y) + base;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      // a group of 128 is the pieces of 16 neighbouring lanes; a partial last one holds zeros past the row
+      const float scale = group16_scale(s[i]);
+      if (ok[i]) {
+        *reinterpret_cast<u32x2_t*>(q + at[i]) = pack8_e4m3(s[i], scale);
+        if ((tid & 15) == 0) p.scales[(int64_t)(at[i] / kGroup) * p.ld_s + row] = scale;
+      }
+    }
+  } else {
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) amax = umax(amax, abs_bits(s[i][c]));
+    amax = wave_max_u32(amax);
+    if constexpr (LT > 64) {
+      if ((tid & 63) == 0) red_max[tid >> 6] = amax;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) amax = umax(amax, red_max[w]);
+    }
+    const float scale = int8_scale(amax);
+    uint8_t* q = static_cast<uint8_t*>(p.y) + base;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (ok[i]) *reinterpret_cast<u32x2_t*>(q + at[i]) = u32x2_t{pack4_int8(s[i], scale), pack4_int8(s[i] + 4, scale)};
+    if (tid == 0) p.scales[row] = scale;
+  }
+}
+
+struct NormGradParams {
+  const void* dy;
+  const void* dsum;           // null: zeros
+  const void* x;              // null: s = r
+  const void* sum;
+  const float* weight;
+  const float* post_weight;
+  const void* gate;
+  void* dx;
+  void* dresidual;
+  float* dweight;             // null: not wanted
+  void* dgate;
+  float* dpost;
+  float* part;                // partials: dweight, dpost, and two of dgate, (parts, hidden) each
+  int64_t rows, rows_per_gate;
+  int64_t rows_per_part;
+  int parts;
+  int hidden, post_norm;
+  float scale, eps;
+};
+
+// A workgroup takes p.rows_per_part consecutive rows, its row groups (of LT lanes) every norm_rows-th of them, and holds
+// the columns' sums in registers.  They end in `part` (one row a workgroup), added by norm_grad_sum_kernel in the order
+// of the workgroups: no atomics, the same bits from run to run.  A gate's rows ("segment") may end inside the
+// workgroup's range: a segment that lies in it whole is written at once; a piece of one that does not goes to
+// slot 0 where the range begins inside the segment, or with it, and to slot 1 where the segment begins later.
+template <class T, class TR, int LT, int V>
+__global__ __launch_bounds__(norm_threads<LT>()) void residual_norm_grad_kernel(NormGradParams p) {
+  constexpr int kWaves = LT / 64, kRows = norm_rows<LT>();
+  __shared__ float red_a[kWaves][3], red_b[kWaves][1];
+  __shared__ float cols[kRows > 1 ? kRows : 1][kRows > 1 ? 8 * LT * V : 1];
+  const int tid = threadIdx.x % LT, group = threadIdx.x / LT;
+  const int64_t first = (int64_t)blockIdx.x * p.rows_per_part;
+  const int64_t end = first + p.rows_per_part < p.rows ? first + p.rows_per_part : p.rows;
+  const bool has_x = p.x != nullptr;
+  const bool each_row = p.rows_per_gate == 1;   // a gate for every row: its gradient is no sum
+  const bool gate_sums = p.dgate != nullptr && !each_row;
+  float dw[V][8], dv[V][8], dgs[V][8];
+  int at[V];
+  bool ok[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    at[i] = 8 * (tid + LT * i);
+    ok[i] = at[i] < p.hidden;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) dw[i][c] = dv[i][c] = dgs[i][c] = 0.0f;
+  }
+  // a column sum of the whole workgroup (its row groups added in order), written by the first row group
+  auto flush = [&](float (*v)[8], auto&& put) {
+    if constexpr (kRows > 1) {
+      __syncthreads();   // the previous flush's readers are done
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) cols[group][at[i] + c] = v[i][c];
+      __syncthreads();
+    }
+    if (group == 0) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (ok[i]) {
+          float t[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            t[c] = v[i][c];
+            if constexpr (kRows > 1)
+#pragma unroll
+              for (int g = 1; g < kRows; ++g) t[c] += cols[g][at[i] + c];
+          }
+          put(at[i], t);
+        }
+    }
+  };
+  const int64_t plane = (int64_t)p.parts * p.hidden;
+  for (int64_t piece = first; piece < end;) {
+    // the rows up to the segment's end (every row without sums of gates); uniform over the workgroup
+    int64_t piece_end = end, segment = 0;
+    if (gate_sums) {
+      segment = piece / p.rows_per_gate;
+      const int64_t e = (segment + 1) * p.rows_per_gate;
+      piece_end = e < end ? e : end;
+    }
+    // rows of the piece in steps of kRows: every row group runs every step (they share barriers only in flush)
+    for (int64_t row = piece + group; row < piece_end; row += kRows) {
+      const int64_t base = row * p.hidden;
+      Raw8<TR> ru[V], rds[V];
+      Raw8<T> rdy[V], rx[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (ok[i]) {
+          ru[i] = load8(static_cast<const TR*>(p.sum) + base + at[i]);
+          rdy[i] = load8(static_cast<const T*>(p.dy) + base + at[i]);
+          if (p.dsum != nullptr) rds[i] = load8(static_cast<const TR*>(p.dsum) + base + at[i]);
+          if (has_x) rx[i] = load8(static_cast<const T*>(p.x) + base + at[i]);
+        }
+      float sums[3] = {0.0f, 0.0f, 0.0f};   // s^2, dy w s, x^2
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (ok[i]) {
+          float u[8], dy[8], w[8];
+          widen8(ru[i], u);
+          widen8(rdy[i], dy);
+          if (p.weight != nullptr) widen8(load8(p.weight + at[i]), w);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            sums[0] = __builtin_fmaf(u[c], u[c], sums[0]);
+            sums[1] = __builtin_fmaf(p.weight != nullptr ? dy[c] * w[c] : dy[c], u[c], sums[1]);
+          }
+          if (has_x && p.post_norm) {
+            float x[8];
+            widen8(rx[i], x);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) sums[2] = __builtin_fmaf(x[c], x[c], sums[2]);
+          }
+        }
+      if constexpr (LT > 64) __syncthreads();   // the previous row's readers of red_a are done
+      row_sums<LT, 3>(sums, red_a, tid);
+      const float rho = inv_rms(sums[0], p.hidden, p.eps);
+      const float back = rho * rho * sums[1] / (float)p.hidden;
+      const float sigma = has_x && p.post_norm ? inv_rms(sums[2], p.hidden, p.eps) : 1.0f;
+      const T* gate = p.gate != nullptr ? static_cast<const T*>(p.gate) + (row / p.rows_per_gate) * p.hidden : nullptr;
+      float dz[V][8];   // the gradient of z, times v where there is a norm
+      float inner[1] = {0.0f};
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (ok[i]) {
+          float u[8], dy[8], w[8], du[8];
+          widen8(ru[i], u);
+          widen8(rdy[i], dy);
+          if (p.weight != nullptr) widen8(load8(p.weight + at[i]), w);
+          if (p.dsum != nullptr) {
+            widen8(rds[i], du);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) du[c] = 0.0f;
+          }
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const float t = p.weight != nullptr ? dy[c] * w[c] : dy[c];
+            du[c] += rho * (t - u[c] * back);
+            dw[i][c] = __builtin_fmaf(dy[c], u[c] * rho, dw[i][c]);
+          }
+          store8(static_cast<TR*>(p.dresidual) + base + at[i], narrow8<TR>(du));
+          if (!has_x) continue;
+          float x[8], v[8], g[8];
+          widen8(rx[i], x);
+          const bool weighted = p.post_norm && p.post_weight != nullptr;
+          if (weighted) widen8(load8(p.post_weight + at[i]), v);
+          if (gate != nullptr) {
+            widen8(load8(gate + at[i]), g);
+            if (p.dgate != nullptr) {
+              float dg[8];
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                const float n = x[c] * sigma;
+                dg[c] = p.scale * du[c] * (weighted ? n * v[c] : n);
+              }
+              if (each_row) {
+                store8(static_cast<T*>(p.dgate) + base + at[i], narrow8<T>(dg));
+              } else {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) dgs[i][c] += dg[c];
+              }
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < 8; ++c) dz[i][c] = gate != nullptr ? p.scale * du[c] * g[c] : p.scale * du[c];
+          if (p.post_norm) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              dv[i][c] = __builtin_fmaf(dz[i][c], x[c] * sigma, dv[i][c]);
+              if (weighted) dz[i][c] *= v[c];
+              inner[0] = __builtin_fmaf(dz[i][c], x[c], inner[0]);
+            }
+          } else {
+            store8(static_cast<T*>(p.dx) + base + at[i], narrow8<T>(dz[i]));
+          }
+        }
+      if (has_x && p.post_norm) {
+        row_sums<LT, 1>(inner, red_b, tid);   // (red_b's readers of the previous row are past the barrier above)
+        const float along = sigma * sigma * inner[0] / (float)p.hidden;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (ok[i]) {
+            float x[8], dx[8];
+            widen8(rx[i], x);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) dx[c] = sigma * (dz[i][c] - x[c] * along);
+            store8(static_cast<T*>(p.dx) + base + at[i], narrow8<T>(dx));
+          }
+      }
+    }
+    if (gate_sums) {
+      const int64_t seg_first = segment * p.rows_per_gate;
+      const bool whole = seg_first >= first && seg_first + p.rows_per_gate <= end;
+      float* slot = p.part + (seg_first > first ? 3 : 2) * plane + (int64_t)blockIdx.x * p.hidden;
+      flush(dgs, [&](int c0, const float* t) {
+        if (whole) {
+          store8(static_cast<T*>(p.dgate) + segment * p.hidden + c0, narrow8<T>(t));
+        } else {
+          store8(slot + c0, narrow8<float>(t));
+        }
+      });
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) dgs[i][c] = 0.0f;
+    }
+    piece = piece_end;
+  }
+  float* mine = p.part + (int64_t)blockIdx.x * p.hidden;
+  if (p.dweight != nullptr) flush(dw, [&](int c0, const float* t) { store8(mine + c0, narrow8<float>(t)); });
+  if (p.dpost != nullptr) flush(dv, [&](int c0, const float* t) { store8(mine + plane + c0, narrow8<float>(t)); });
+}
+
+// Column sums of the partials: 64 columns a workgroup (16 lanes of 4), 16 of the partials side by side, added in a fixed
+// order.  blockIdx.y = 0: dweight, 1: dpost, 2 + j: the gate whose rows pass from workgroup j to j + 1.
+template <class T>
+__global__ __launch_bounds__(256) void norm_grad_sum_kernel(NormGradParams p) {
+  __shared__ v4f s_sum[16][16];
+  const int lane = threadIdx.x & 15, along = threadIdx.x >> 4;
+  const int col = blockIdx.x * 64 + 4 * lane;
+  const int64_t plane = (int64_t)p.parts * p.hidden;
+  const float* src = p.part;
+  int begin = 0, end = p.parts;
+  int64_t segment = 0;
+  int head = -1;   // the workgroup in which the gate's rows begin, where that piece is in slot 1
+  if (blockIdx.y == 0) {
+    if (p.dweight == nullptr) return;
+  } else if (blockIdx.y == 1) {
+    if (p.dpost == nullptr) return;
+    src += plane;
+  } else {
+    const int j = blockIdx.y - 2;
+    const int64_t border = (int64_t)(j + 1) * p.rows_per_part;
+    segment = border / p.rows_per_gate;
+    const int64_t first = segment * p.rows_per_gate;
+    // (rows of one gate end at the border, or this gate's were met at an earlier border)
+    if (first == border || first < (int64_t)j * p.rows_per_part) return;
+    begin = j;
+    end = (int)((first + p.rows_per_gate + p.rows_per_part - 1) / p.rows_per_part);
+    if (first > (int64_t)j * p.rows_per_part) head = j;
+    src += 2 * plane;
+  }
+  v4f sum = {0.f, 0.f, 0.f, 0.f};
+  if (col < p.hidden)
+    for (int i = begin + along; i < end; i += 16)
+      sum += *reinterpret_cast<const v4f*>(src + (i == head ? plane : 0) + (int64_t)i * p.hidden + col);
+  s_sum[along][lane] = sum;
+  __syncthreads();
+  if (along != 0 || col >= p.hidden) return;
+#pragma unroll
+  for (int i = 1; i < 16; ++i) sum += s_sum[i][lane];
+  if (blockIdx.y == 0) {
+    *reinterpret_cast<v4f*>(p.dweight + col) = sum;
+  } else if (blockIdx.y == 1) {
+    *reinterpret_cast<v4f*>(p.dpost + col) = sum;
+  } else {
+    T* out = static_cast<T*>(p.dgate) + segment * p.hidden + col;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) out[c] = narrow<T>(sum[c]);
+  }
+}
+
+// ---- host ------------------------------------------------------------------------------------------
+constexpr int kNormMaxHidden = 16384;
+
+template <class T, class TR, int OUT>
+static const void* norm_fn(int lt, int v) {
+  void (*fn)(NormParams) = lt == 64    ? (v == 1 ? residual_norm_kernel<T, TR, OUT, 64, 1> : residual_norm_kernel<T, TR, OUT, 64, 2>)
+                           : lt == 256 ? (v == 1 ? residual_norm_kernel<T, TR, OUT, 256, 1>
+                                                 : residual_norm_kernel<T, TR, OUT, 256, 2>)
+                           : lt == 512 ? residual_norm_kernel<T, TR, OUT, 512, 2>
+                                       : residual_norm_kernel<T, TR, OUT, 1024, 2>;
+  return reinterpret_cast<const void*>(fn);
+}
+
+template <class T, class TR>
+static const void* norm_fn_of(int out, int lt, int v) {
+  return out == kNormSame ? norm_fn<T, TR, kNormSame>(lt, v)
+         : out == kNormFp8 ? norm_fn<T, TR, kNormFp8>(lt, v) : norm_fn<T, TR, kNormInt8>(lt, v);
+}
+
+template <class T, class TR>
+static const void* norm_grad_fn(int lt, int v) {
+  void (*fn)(NormGradParams) = lt == 64    ? (v == 1 ? residual_norm_grad_kernel<T, TR, 64, 1> : residual_norm_grad_kernel<T, TR, 64, 2>)
+                               : lt == 256 ? (v == 1 ? residual_norm_grad_kernel<T, TR, 256, 1>
+                                                     : residual_norm_grad_kernel<T, TR, 256, 2>)
+                               : lt == 512 ? residual_norm_grad_kernel<T, TR, 512, 2>
+                                           : residual_norm_grad_kernel<T, TR, 1024, 2>;
+  return reinterpret_cast<const void*>(fn);
+}
+
+// Lanes a row and pieces a lane.
+static void norm_shape(int64_t hidden, int* lt, int* v) {
+  *lt = hidden <= 1024 ? 64 : hidden <= 4096 ? 256 : hidden <= 8192 ? 512 : 1024;
+  *v = (int)((hidden + 8 * *lt - 1) / (8 * *lt));
+  if (*lt > 256) *v = 2;
+}
+
+static int check_norm_size(int64_t rows, int64_t hidden) {
+  if (hidden > kNormMaxHidden)
+    return set_error(kUnsupported, "residual_norm: hidden = %lld, rows of at most %d are held in registers",
+                     (long long)hidden, kNormMaxHidden);
+  if (rows > 0x7fffffffLL) return set_error(kUnsupported, "residual_norm: 2^31 rows");
+  return kOk;
+}
+
+int launch_residual_norm(int out, const void* x, const void* residual, int dtype, int residual_dtype, const float* weight,
+                         const void* gate, int64_t gate_rows, bool post_norm, const float* post_weight, float scale,
+                         float eps, int64_t rows, int64_t hidden, void* sum, void* y, float* scales, int64_t ld_s,
+                         hipStream_t stream) {
+  const int c = check_norm_size(rows, hidden);
+  if (c != kOk) return c;
+  NormParams p{};
+  p.x = x;
+  p.residual = residual;
+  p.weight = weight;
+  p.post_weight = post_weight;
+  p.gate = gate;
+  p.sum = sum;
+  p.y = y;
+  p.scales = scales;
+  p.ld_s = ld_s;
+  p.rows = rows;
+  p.rows_per_gate = gate_rows > 0 ? rows / gate_rows : 1;
+  p.hidden = (int)hidden;
+  p.post_norm = post_norm;
+  p.scale = scale;
+  p.eps = eps;
+  int lt, v;
+  norm_shape(hidden, &lt, &v);
+  const bool wide = residual_dtype == kF32;
+  const void* fn = dtype == kF32 ? norm_fn_of<float, float>(out, lt, v)
+                   : dtype == kBf16 ? (wide ? norm_fn_of<Bf16, float>(out, lt, v) : norm_fn_of<Bf16, Bf16>(out, lt, v))
+                                    : (wide ? norm_fn_of<_Float16, float>(out, lt, v) : norm_fn_of<_Float16, _Float16>(out, lt, v));
+  const int threads = lt > kNormThreads ? lt : kNormThreads, per_wg = lt >= kNormThreads ? 1 : kNormThreads / lt;
+  void* args[] = {&p};
+  const hipError_t e = hipLaunchKernel(fn, dim3((unsigned)((rows + per_wg - 1) / per_wg)), dim3(threads), args, 0, stream);
+  return e == hipSuccess ? kOk : set_error(kHip, "residual_norm launch: %s", hipGetErrorString(e));
+}
+
+// Workgroups of the backward pass and the rows of each.
+static void norm_grad_parts(int64_t rows, int64_t hidden, int64_t* per_part, int* parts) {
+  int lt, v;
+  norm_shape(hidden, &lt, &v);
+  const int64_t most = lt <= 256 ? 1024 : lt == 512 ? 512 : 256;
+  *per_part = (rows + most - 1) / most;
+  *parts = rows == 0 ? 0 : (int)((rows + *per_part - 1) / *per_part);
+}
+
+size_t residual_norm_grad_workspace_size(int64_t rows, int64_t hidden) {
+  int64_t per_part;
+  int parts;
+  norm_grad_parts(rows, hidden, &per_part, &parts);
+  return (size_t)parts * hidden * 4 * sizeof(float);
+}
+
+int launch_fill_zero_bf16(uint16_t* d, int64_t count, hipStream_t stream);
+
+int launch_residual_norm_grad(const void* dy, const void* dsum, const void* x, const void* sum, int dtype,
+                              int residual_dtype, const float* weight, const void* gate, int64_t gate_rows, bool post_norm,
+                              const float* post_weight, float scale, float eps, int64_t rows, int64_t hidden, void* dx,
+                              void* dresidual, float* dweight, void* dgate, float* dpost, void* ws, hipStream_t stream) {
+  const int c = check_norm_size(rows, hidden);
+  if (c != kOk) return c;
+  if (rows == 0) {   // sums over no rows
+    int r = kOk;
+    if (dweight != nullptr) r = launch_fill_zero_bf16(reinterpret_cast<uint16_t*>(dweight), 2 * hidden, stream);
+    if (r == kOk && dpost != nullptr) r = launch_fill_zero_bf16(reinterpret_cast<uint16_t*>(dpost), 2 * hidden, stream);
+    if (r == kOk && dgate != nullptr)
+      r = launch_fill_zero_bf16(static_cast<uint16_t*>(dgate), gate_rows * hidden * (dtype == kF32 ? 2 : 1), stream);
+    return r;
+  }
+  NormGradParams p{};
+  p.dy = dy;
+  p.dsum = dsum;
+  p.x = x;
+  p.sum = sum;
+  p.weight = weight;
+  p.post_weight = post_weight;
+  p.gate = gate;
+  p.dx = dx;
+  p.dresidual = dresidual;
+  p.dweight = dweight;
+  p.dgate = dgate;
+  p.dpost = dpost;
+  p.part = static_cast<float*>(ws);
+  p.rows = rows;
+  p.rows_per_gate = gate_rows > 0 ? rows / gate_rows : 1;
+  p.hidden = (int)hidden;
+  p.post_norm = post_norm;
+  p.scale = scale;
+  p.eps = eps;
+  norm_grad_parts(rows, hidden, &p.rows_per_part, &p.parts);
+  int lt, v;
+  norm_shape(hidden, &lt, &v);
+  const bool wide = residual_dtype == kF32;
+  const void* fn = dtype == kF32 ? norm_grad_fn<float, float>(lt, v)
+                   : dtype == kBf16 ? (wide ? norm_grad_fn<Bf16, float>(lt, v) : norm_grad_fn<Bf16, Bf16>(lt, v))
+                                    : (wide ? norm_grad_fn<_Float16, float>(lt, v) : norm_grad_fn<_Float16, _Float16>(lt, v));
+  void* args[] = {&p};
+  hipError_t e = hipLaunchKernel(fn, dim3((unsigned)p.parts), dim3(lt > kNormThreads ? lt : kNormThreads), args, 0, stream);
+  if (e != hipSuccess) return set_error(kHip, "residual_norm_grad launch: %s", hipGetErrorString(e));
+  const bool borders = dgate != nullptr && p.rows_per_gate > 1 && p.parts > 1;
+  if (dweight == nullptr && dpost == nullptr && !borders) return kOk;
+  void (*sum_fn)(NormGradParams) = dtype == kF32 ? norm_grad_sum_kernel<float>
+                                   : dtype == kBf16 ? norm_grad_sum_kernel<Bf16> : norm_grad_sum_kernel<_Float16>;
+  e = hipLaunchKernel(reinterpret_cast<const void*>(sum_fn),
+                      dim3((unsigned)((hidden + 63) / 64), borders ? (unsigned)(2 + p.parts - 1) : 2u), dim3(256), args, 0,
+                      stream);
+  return e == hipSuccess ? kOk : set_error(kHip, "residual_norm_grad sums launch: %s", hipGetErrorString(e));
+}
+
+}  // namespace dg

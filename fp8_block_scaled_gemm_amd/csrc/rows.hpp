@@ -148,6 +148,20 @@ __device__ __forceinline__ float wave_sum(float v) {
 // infinity, so a maximum over them keeps a NaN.
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
+// E4M3 scale of a 128-element group held as 8 values by each of 16 neighbouring lanes, by the rule of the per-token-group quantizer: amax / 448, 1 for an all-zero group.
+__device__ __forceinline__ float group16_scale(const float* v) {
+  float amax = fabsf(v[0]);
+#pragma unroll
+  for (int c = 1; c < 8; ++c) amax = fmaxf(amax, fabsf(v[c]));
+  amax = row16_max(amax);
+  return amax == 0.0f ? 1.0f : amax / kE4M3Max;
+}
+// The E4M3 codes of eight values over that scale (IEEE divisions, saturated), packed little-endian.
+__device__ __forceinline__ u32x2_t pack8_e4m3(const float* v, float s) {
+  return u32x2_t{pack4_e4m3(clamp448(v[0] / s), clamp448(v[1] / s), clamp448(v[2] / s), clamp448(v[3] / s)),
+                 pack4_e4m3(clamp448(v[4] / s), clamp448(v[5] / s), clamp448(v[6] / s), clamp448(v[7] / s))};
+}
+
 constexpr float kInt8Max = 127.0f;
 
 // Scale of a row whose largest magnitude has these bits: amax / 127 (IEEE division), 1 for an

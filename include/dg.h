@@ -478,6 +478,102 @@ int dg_gemm_int8_grouped_masked(const int8_t* a, const float* sa, const int8_t* 
 size_t dg_gemm_int8_workspace_size(int64_t m, int64_t n, int64_t k, int64_t num_groups);
 
 /*
+ * The activation of a gated feed-forward block on its two projections, and the backward pass.
+ *   pre (rows, 2n): a row holds g (n) and then u (n);  h = act(g) * u, in fp32, rounded once.
+ *   DG_ACT_SILU: act(g) = g / (1 + exp(-g));  DG_ACT_GELU: the tanh form, 0.5 g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))).
+ * Deterministic.  Row data needs the 16-byte alignment of every other pointer, index and scale arrays their elements'.
+ * Outputs must not overlap inputs.
+ */
+enum dg_act { DG_ACT_SILU = 0, DG_ACT_GELU = 1 };
+
+/*
+ * h from pre (`dtype`; n a positive multiple of 16):
+ *   dg_gated_act       h (rows, n) in pre's type;
+ *   dg_gated_act_fp8   q, s: the codes and scales that dg_quantize_per_token_group gives for h in fp32 (its layout of
+ *                      scales: s[nb * ld_s + row]; per group with masked_m), nothing rounded before;
+ *   dg_gated_act_int8  q, s: as dg_quantize_int8_per_token gives them for h in fp32, s (rows,).
+ * Rows that are not computed are neither read nor written:
+ *   m_indices (rows,) (not NULL): those of a negative index (the contiguous layout's padding behind the last expert);
+ *   masked_m (rows / rows_per_group,) (not NULL): those at or past their group's count (the masked layout).
+ * Errors: DG_ERR_INVALID_ARG for null or misaligned pointers, an unknown dtype or activation, n % 16 != 0, negative sizes, both
+ * masks, masked_m without a rows_per_group that divides rows (or with one and no masked_m), ld_s too small or not a multiple
+ * of 4; DG_ERR_UNSUPPORTED for shapes past the launch grid.  rows = 0 is a no-op.
+ */
+int dg_gated_act(const void* pre, int dtype, int act, const int32_t* m_indices, const int32_t* masked_m,
+                 int64_t rows_per_group, int64_t rows, int64_t n, void* h, dg_stream_t stream);
+int dg_gated_act_fp8(const void* pre, int dtype, int act, const int32_t* m_indices, const int32_t* masked_m,
+                     int64_t rows_per_group, int64_t rows, int64_t n, uint8_t* q, float* s, int64_t ld_s,
+                     dg_stream_t stream);
+int dg_gated_act_int8(const void* pre, int dtype, int act, const int32_t* m_indices, const int32_t* masked_m,
+                      int64_t rows_per_group, int64_t rows, int64_t n, int8_t* q, float* s, dg_stream_t stream);
+
+/*
+ * The gradient of pre: dpre (rows, 2n) = (dh * u * act'(g) | dh * act(g)), dh (rows, n) and pre in `dtype`.
+ *   dg_gated_act_grad      dpre in that type; n a positive multiple of 16.
+ *   dg_gated_act_grad_fp8  dpre and h as the backward FP8 products read them, from one pass over dh and pre; each pair may be
+ *     NULL if it is not wanted (one must not be):
+ *     q (rows, 2n), s[kb * ld_s + row]      as dg_quantize_per_token_group of dpre: the input gradient dpre * W (W^T's codes
+ *                                           from dg_transpose_blocks);
+ *     qt (2n, rows), st[mb * ld_st + col]   as dg_quantize_per_channel_group of dpre: the weight gradient dpre^T * X;
+ *     ht (n, rows), hst[mb * ld_hst + col]  as dg_quantize_per_channel_group of h: the next product's weight gradient.
+ *     n a positive multiple of 128 (the groups of q must not hold columns of both halves), rows a multiple of 16.
+ * Errors: as above, and a code pointer without its scales or the reverse.
+ */
+int dg_gated_act_grad(const void* dh, const void* pre, int dtype, int act, int64_t rows, int64_t n, void* dpre,
+                      dg_stream_t stream);
+int dg_gated_act_grad_fp8(const void* dh, const void* pre, int dtype, int act, int64_t rows, int64_t n, uint8_t* q,
+                          float* s, int64_t ld_s, uint8_t* qt, float* st, int64_t ld_st, uint8_t* ht, float* hst,
+                          int64_t ld_hst, dg_stream_t stream);
+
+/*
+ * What lies between two blocks of a transformer, in one pass over the rows (hidden: a multiple of 16, at most 16384):
+ *   z = post_weight * x / sqrt(mean(x^2) + eps)   the norm after the first block (post_norm != 0; otherwise z = x)
+ *   sum = residual + scale * gate * z             its gate and residual scale, and the residual stream
+ *   y = weight * sum / sqrt(mean(sum^2) + eps)    the norm before the second block, of the sum as it is before rounding
+ * All in fp32, each output rounded once; sums of squares are fp32 (values up to 1e18).
+ *   x         (rows, hidden) in `dtype`, the first block's output; NULL for a norm alone (sum = residual is then not
+ *             written, `sum` and `gate` are NULL and post_norm is 0);
+ *   residual  (rows, hidden) in `residual_dtype`: DG_DTYPE_F32 or `dtype`;
+ *   weight, post_weight  fp32 (hidden,), NULL for ones;
+ *   gate      (gate_rows, hidden) in `dtype`, NULL (gate_rows 0) for none; gate_rows divides rows: gate row i serves the i-th
+ *             rows / gate_rows consecutive rows (1: one gate for all; rows: each row its own);
+ *   sum       (rows, hidden) in residual_dtype, NULL if it is not wanted; it may be `residual` itself (in place);
+ *   y         dg_residual_norm: (rows, hidden) in `dtype`;
+ *             dg_residual_norm_fp8: q, s as dg_quantize_per_token_group gives them for y in fp32;
+ *             dg_residual_norm_int8: q, s as dg_quantize_int8_per_token gives them for y in fp32.
+ * Errors: DG_ERR_INVALID_ARG for null or misaligned pointers, unknown types, a residual_dtype that is neither, hidden % 16 != 0,
+ * gate_rows that does not divide rows, a negative or non-finite eps, ld_s too small or not a multiple of 4;
+ * DG_ERR_UNSUPPORTED for hidden > 16384 or 2^31 rows.  rows = 0 is a no-op.  Deterministic.
+ */
+int dg_residual_norm(const void* x, const void* residual, int dtype, int residual_dtype, const float* weight,
+                     const void* gate, int64_t gate_rows, int post_norm, const float* post_weight, float scale, float eps,
+                     int64_t rows, int64_t hidden, void* sum, void* y, dg_stream_t stream);
+int dg_residual_norm_fp8(const void* x, const void* residual, int dtype, int residual_dtype, const float* weight,
+                         const void* gate, int64_t gate_rows, int post_norm, const float* post_weight, float scale,
+                         float eps, int64_t rows, int64_t hidden, void* sum, uint8_t* q, float* s, int64_t ld_s,
+                         dg_stream_t stream);
+int dg_residual_norm_int8(const void* x, const void* residual, int dtype, int residual_dtype, const float* weight,
+                          const void* gate, int64_t gate_rows, int post_norm, const float* post_weight, float scale,
+                          float eps, int64_t rows, int64_t hidden, void* sum, int8_t* q, float* s, dg_stream_t stream);
+
+/*
+ * Gradients of dg_residual_norm from dy (rows, hidden) in `dtype`, dsum (residual_dtype; what the sum gets from elsewhere; NULL
+ * for none), x (NULL as there) and sum as the forward pass stored it:
+ *   dresidual (residual_dtype; it may be dsum itself) and dx (`dtype`; NULL with x), written;
+ *   dweight, dpost_weight fp32 (hidden,), dgate (gate_rows, hidden) in `dtype`: written where not NULL (sums over the rows,
+ *   in fp32 in a fixed order, rounded once; NULL where there is no weight, norm or gate).
+ * workspace : dg_residual_norm_grad_workspace_size(rows, hidden) bytes of any content; calls that share it must be ordered.
+ *   Not needed (NULL) where dweight, dpost_weight and dgate are NULL.
+ * Errors: as dg_residual_norm; DG_ERR_WORKSPACE.  rows = 0 writes zeros to the three sums.
+ */
+int dg_residual_norm_grad(const void* dy, const void* dsum, const void* x, const void* sum, int dtype, int residual_dtype,
+                          const float* weight, const void* gate, int64_t gate_rows, int post_norm,
+                          const float* post_weight, float scale, float eps, int64_t rows, int64_t hidden, void* dx,
+                          void* dresidual, float* dweight, void* dgate, float* dpost_weight, void* workspace,
+                          size_t workspace_bytes, dg_stream_t stream);
+size_t dg_residual_norm_grad_workspace_size(int64_t rows, int64_t hidden);
+
+/*
  * Utilities (CSDN article, "utilities": cap on the compute units used,
  * contiguous-layout alignment, aligned column-major scale tensor).
  */

@@ -25,6 +25,7 @@ news/blog pages; each function cites the page title and section it follows):
   the GEMM whose two operands both carry per-row group scales.
 * ``moe``   - expert routing (with its gradient), the expert row layout, dispatch and combine (with
   theirs), in 64 bits.
+* ``feed_forward`` - the gated activation and the residual norms with their gradients, in 64 bits.
 * ``int8``  - the per-row 8-bit integer quantizer and the three forms of its GEMM.
 
 Every function here is pinned by ``tests/test_oracle_*.py`` against facts that
@@ -32,4 +33,4 @@ do not come from this package (the format definition, torch's independent
 float8_e4m3fn codec, exact rational arithmetic, closed forms, invariants).
 """
 
-from . import bf16, e4m3, quant, gemm, int8, moe, train  # noqa: F401
+from . import bf16, e4m3, feed_forward, quant, gemm, int8, moe, train  # noqa: F401
