@@ -28,6 +28,8 @@ Functions carry the C names:
 * 8-bit integer GEMMs (one scale per token, one per output channel): ``dg_quantize_int8_per_token(x)`` ->
   (q int8, s float32); ``dg_gemm_int8_nt``, ``dg_gemm_int8_nt_act_quant``,
   ``dg_gemm_int8_grouped_contiguous``, ``dg_gemm_int8_grouped_masked`` -> d bf16, fp16 or fp32
+* gated FP8 GEMMs, both projections of a feed-forward block, the activation and the product in one launch:
+  ``dg_gemm_fp8_gated_nt``, ``dg_gemm_fp8_gated_contiguous``, ``dg_gemm_fp8_gated_masked`` -> h bf16, or (q, s) of h
 * gated activation on two projections side by side: ``dg_gated_act`` / ``_fp8`` / ``_int8`` (pre (..., 2N) ->
   act(g) * u, quantized or not), ``dg_gated_act_grad`` and ``dg_gated_act_grad_fp8`` (the operands of the backward
   FP8 products)
@@ -117,6 +119,14 @@ _SIGNATURES = {
                                                    _c_int64, _vp, ctypes.c_size_t, _vp]),
     "dg_gemm_int8_config_name": (ctypes.c_char_p, [ctypes.c_int, _c_int64, _c_int64, _c_int64, _c_int64]),
     "dg_gemm_int8_workspace_size": (ctypes.c_size_t, [_c_int64, _c_int64, _c_int64, _c_int64]),
+    "dg_gemm_fp8_gated_nt": (ctypes.c_int, [_vp, _vp, _c_int64, _vp, _vp, _c_int, _vp, _vp, _vp, _c_int64, _vp, _c_int64,
+                                            _c_int64, _c_int64, _vp, ctypes.c_size_t, _vp]),
+    "dg_gemm_fp8_gated_contiguous": (ctypes.c_int, [_vp, _vp, _c_int64, _vp, _vp, _vp, _c_int64, _c_int, _vp, _vp, _vp,
+                                                    _c_int64, _vp, _c_int64, _c_int64, _c_int64, _vp]),
+    "dg_gemm_fp8_gated_masked": (ctypes.c_int, [_vp, _vp, _c_int64, _vp, _vp, _vp, _c_int64, _c_int, _vp, _vp, _vp, _c_int64,
+                                                _vp, _c_int64, _c_int64, _c_int64, _vp, ctypes.c_size_t, _vp]),
+    "dg_gemm_fp8_gated_workspace_size": (ctypes.c_size_t, [_c_int64, _c_int64, _c_int64, _c_int64]),
+    "dg_gemm_fp8_gated_config_name": (ctypes.c_char_p, [ctypes.c_int, _c_int64, _c_int64, _c_int64, _c_int64]),
     "dg_gated_act": (ctypes.c_int, [_vp, _c_int, _c_int, _vp, _vp, _c_int64, _c_int64, _c_int64, _vp, _vp]),
     "dg_gated_act_fp8": (ctypes.c_int, [_vp, _c_int, _c_int, _vp, _vp, _c_int64, _c_int64, _c_int64, _vp, _vp, _c_int64, _vp]),
     "dg_gated_act_int8": (ctypes.c_int, [_vp, _c_int, _c_int, _vp, _vp, _c_int64, _c_int64, _c_int64, _vp, _vp, _vp]),
@@ -936,6 +946,106 @@ def _scales_like(s, lead, groups, device):
     _require(s.dtype == torch.float32 and tuple(s.shape[:-1]) == shape and s.shape[-1] >= lead[-1] and s.shape[-1] % 4 == 0,
              f"scales must be float32 {shape} with a last dimension of at least {lead[-1]}, a multiple of 4")
     return s
+
+
+def dg_gemm_fp8_gated_workspace_size(m, n, k, num_groups=1):
+    return lib().dg_gemm_fp8_gated_workspace_size(int(m), int(n), int(k), int(num_groups))
+
+
+def dg_gemm_fp8_gated_config_name(layout, m, n, k, num_groups=1):
+    """Tile and K split of the gated GEMMs (layout 0 normal, 1 contiguous, 2 masked); n is the width of h."""
+    return lib().dg_gemm_fp8_gated_config_name(int(layout), int(m), int(n), int(k), int(num_groups)).decode()
+
+
+def _gated_operands(a, sa, b, sb, groups):
+    """(a, b as bytes, N, K) of activations and the gate and up matrices b ([G,] 2, N, K), or ([G,] 2N, K) for N a multiple
+    of 128, with their scales."""
+    a, b = _bytes(a), _bytes(b)
+    lead = () if groups is None else (groups,)
+    _require(a.dtype == torch.uint8 and b.dtype == torch.uint8 and sa.dtype == torch.float32 and sb.dtype == torch.float32,
+             "a and b must be E4M3 bytes, sa and sb float32")
+    k = a.shape[-1]
+    _require(b.dim() in (2 + len(lead), 3 + len(lead)) and tuple(b.shape[:len(lead)]) == lead and b.shape[-1] == k,
+             "b must be ([G,] 2, N, K)")
+    if b.dim() == 3 + len(lead):
+        _require(b.shape[-3] == 2, "b must be ([G,] 2, N, K)")
+        n = b.shape[-2]
+    else:
+        _require(b.shape[-2] % 256 == 0, "b ([G,] 2N, K) needs N a multiple of 128")
+        n = b.shape[-2] // 2
+    kb = -(-k // 128)
+    _require(sb.numel() == (groups if groups is not None else 1) * 2 * -(-n // 128) * kb, "sb must be ([G,] 2, ceil(N/128), ceil(K/128))")
+    return a, b, n, k, kb
+
+
+def _gated_out(lead, n, out, d, q, s, pre, device):
+    """(d, q, s) as given or allocated, one of d and (q, s) None."""
+    _require(out in ("bf16", "fp8"), "out must be 'bf16' or 'fp8'")
+    _require(pre is None or (pre.dtype == torch.bfloat16 and tuple(pre.shape) == (*lead, 2 * n)), f"pre must be bfloat16 {(*lead, 2 * n)}")
+    if out == "bf16":
+        _require(q is None and s is None, "q and s go with out='fp8'")
+        return _like(d, (*lead, n), torch.bfloat16, device, "d"), None, None
+    _require(d is None, "d goes with out='bf16'")
+    _require(n % 16 == 0, "out='fp8' needs N a multiple of 16")
+    return (None, _like(None if q is None else _bytes(q), (*lead, n), torch.uint8, device, "q"),
+            _scales_like(s, lead, -(-n // 128), device))
+
+
+def dg_gemm_fp8_gated_nt(a, sa, b, sb, act="silu", out="bf16", d=None, q=None, s=None, pre=None, workspace=None,
+                         use_workspace=True):
+    """h (M, N) = act(A * Bg^T) * (A * Bu^T) from a (M, K), sa as dg_gemm_fp8_nt and b (2, N, K) = gate, up with sb (2,
+    ceil(N/128), ceil(K/128)): -> d bfloat16, or with out='fp8' (q uint8, s float32 (ceil(N/128), ld)) as
+    dg_quantize_per_token_group would quantize h in fp32.  pre (bfloat16 (M, 2N)) receives both projections."""
+    _require(a.dim() == 2, "a (M, K)")
+    a, b, n, k, kb = _gated_operands(a, sa, b, sb, None)
+    m = a.shape[0]
+    _require(sa.dim() == 2 and sa.shape[0] == kb and sa.shape[1] >= m, "sa must be (ceil(K/128), ld >= M)")
+    d, q, s = _gated_out((m,), n, out, d, q, s, pre, a.device)
+    dev = _one_device(a, sa, b, sb, d, q, s, pre, workspace)
+    if m == 0:
+        return d if out == "bf16" else (q, s)
+    if workspace is None and use_workspace:
+        workspace = default_workspace(dev, dg_gemm_fp8_gated_workspace_size(m, n, k, 1))
+    _run("dg_gemm_fp8_gated_nt", dev, _ptr(a), _ptr(sa), sa.shape[-1], _ptr(b), _ptr(sb), _act(act), _ptr(d), _ptr(q), _ptr(s),
+         0 if s is None else s.shape[-1], _ptr(pre), m, n, k, *_ws(workspace))
+    return d if out == "bf16" else (q, s)
+
+
+def dg_gemm_fp8_gated_contiguous(a, sa, b, sb, m_indices, act="silu", out="bf16", d=None, q=None, s=None, pre=None):
+    """The contiguous-grouped form: row r of a (M_total, K) uses expert m_indices[r] of b (G, 2, N, K) (or (G, 2N, K), N a
+    multiple of 128); rows of an index outside [0, G) stay untouched."""
+    _require(a.dim() == 2 and b.dim() >= 3, "a (M_total, K), b (G, 2, N, K)")
+    g = b.shape[0]
+    a, b, n, k, kb = _gated_operands(a, sa, b, sb, g)
+    m = a.shape[0]
+    _require(sa.dim() == 2 and sa.shape[0] == kb and sa.shape[1] >= m, "sa must be (ceil(K/128), ld >= M_total)")
+    _require(m_indices.dtype == torch.int32 and m_indices.numel() == m, "m_indices must be int32, one per row")
+    d, q, s = _gated_out((m,), n, out, d, q, s, pre, a.device)
+    dev = _one_device(a, sa, b, sb, m_indices, d, q, s, pre)
+    if m:
+        _run("dg_gemm_fp8_gated_contiguous", dev, _ptr(a), _ptr(sa), sa.shape[-1], _ptr(b), _ptr(sb), _ptr(m_indices), g,
+             _act(act), _ptr(d), _ptr(q), _ptr(s), 0 if s is None else s.shape[-1], _ptr(pre), m, n, k)
+    return d if out == "bf16" else (q, s)
+
+
+def dg_gemm_fp8_gated_masked(a, sa, b, sb, masked_m, act="silu", out="bf16", d=None, q=None, s=None, pre=None, workspace=None,
+                             use_workspace=True):
+    """The masked-grouped form: a (G, M_max, K), sa (G, ceil(K/128), ld), b (G, 2, N, K) (or (G, 2N, K), N a multiple of
+    128); expert g computes its first masked_m[g] rows, the rest stay untouched.  s is (G, ceil(N/128), ld)."""
+    _require(a.dim() == 3, "a (G, M_max, K)")
+    g, m = a.shape[:2]
+    a, b, n, k, kb = _gated_operands(a, sa, b, sb, g)
+    _require(tuple(sa.shape[:-1]) == (g, kb) and sa.shape[-1] >= m, "sa must be (G, ceil(K/128), ld >= M_max)")
+    _require(masked_m.dtype == torch.int32 and masked_m.numel() == g, "masked_m must be int32, one per expert")
+    d, q, s = _gated_out((g, m), n, out, d, q, s, pre, a.device)
+    dev = _one_device(a, sa, b, sb, masked_m, d, q, s, pre, workspace)
+    if g * m == 0:
+        return d if out == "bf16" else (q, s)
+    if workspace is None and use_workspace:
+        workspace = default_workspace(dev, dg_gemm_fp8_gated_workspace_size(m, n, k, g))
+    _run("dg_gemm_fp8_gated_masked", dev, _ptr(a), _ptr(sa), sa.shape[-1], _ptr(b), _ptr(sb), _ptr(masked_m), g, _act(act),
+         _ptr(d), _ptr(q), _ptr(s), 0 if s is None else s.shape[-1], _ptr(pre), m, n, k, *_ws(workspace))
+    return d if out == "bf16" else (q, s)
 
 
 def _act_rows(pre, act, m_indices, masked_m):

@@ -73,6 +73,13 @@ void gemm_int8_config_name(int layout, int64_t m, int64_t n, int64_t k, int64_t 
 size_t int8_workspace_size(int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus);
 size_t int8_act_quant_workspace_size(int64_t m, int64_t n, int64_t k, int num_cus);
 
+int launch_gemm_gated(int layout, const uint8_t* a, const float* sa, int64_t ld_sa, const uint8_t* b, const float* sb,
+                      int act, uint16_t* d, uint8_t* q, float* s, int64_t ld_s, uint16_t* pre, const int32_t* m_indices,
+                      const int32_t* masked_m, int64_t groups, int64_t m, int64_t n, int64_t k, void* ws, size_t ws_bytes,
+                      hipStream_t stream, int num_cus);
+size_t gemm_gated_workspace_size(int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus);
+void gemm_gated_config_name(int layout, int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus, char* buf,
+                            size_t len);
 int launch_gated_act(int form, const void* pre, int dtype, int act, const int32_t* m_indices, const int32_t* masked_m,
                      int64_t rows_per_group, int64_t rows, int64_t n, void* h, float* scales, int64_t ld_s,
                      hipStream_t stream);
@@ -695,6 +702,72 @@ int dg_gemm_int8_grouped_masked(const int8_t* a, const float* sa, const int8_t* 
   if (cus < 0) return cus;
   return launch_gemm_int8(2, a, sa, b, sb, d, out_dtype, nullptr, masked_m, num_groups, m_max, n, k, workspace,
                           workspace ? workspace_bytes : 0, static_cast<hipStream_t>(stream), cus);
+}
+
+// ---- gated GEMMs ----------------------------------------------------------------------------------
+static int gemm_gated(int layout, const uint8_t* a, const float* sa, int64_t ld_sa, const uint8_t* b, const float* sb,
+                      int act, uint16_t* d, uint8_t* q, float* s, int64_t ld_s, uint16_t* pre, const int32_t* m_indices,
+                      const int32_t* masked_m, int64_t groups, int64_t m, int64_t n, int64_t k, void* workspace,
+                      size_t workspace_bytes, dg_stream_t stream) {
+  DG_REQUIRE(groups >= 0 && (layout != 2 || groups <= 1024), "gated gemm: need 0 <= num_groups, at most 1024 masked ones (got %lld)",
+             (long long)groups);
+  DG_REQUIRE(act == DG_ACT_SILU || act == DG_ACT_GELU, "gated gemm: unknown activation %d", act);
+  if (groups == 0) return DG_OK;
+  DG_REQUIRE(layout != 1 || m % kGroup == 0, "contiguous gated gemm: m_total must be a multiple of 128 (got %lld)", (long long)m);
+  DG_REQUIRE((d == nullptr) != (q == nullptr) || m == 0 || n == 0, "gated gemm: one of d and q is given");
+  const int c = check_gemm_common(a, sa, ld_sa, b, sb, d != nullptr ? d : reinterpret_cast<uint16_t*>(q), m, n, k);
+  if (c <= 0) return c;
+  DG_REQUIRE(q == nullptr || (s != nullptr && aligned_to(s, 4) && n % kKAlign == 0 && ld_s >= m && ld_s % 4 == 0),
+             "gated gemm: quantized output needs scales, n %% 16 == 0, ld_s >= m, ld_s %% 4 == 0 (n=%lld ld_s=%lld)",
+             (long long)n, (long long)ld_s);
+  DG_REQUIRE(aligned16(pre) && aligned16(workspace), "gated gemm: pointers must be 16-byte aligned");
+  DG_REQUIRE(layout != 1 || (m_indices != nullptr && aligned_to(m_indices, 4)), "contiguous gated gemm: m_indices is null or misaligned");
+  DG_REQUIRE(layout != 2 || (masked_m != nullptr && aligned_to(masked_m, 4)), "masked gated gemm: masked_m is null or misaligned");
+  const int cus = effective_cus();
+  if (cus < 0) return cus;
+  return launch_gemm_gated(layout, a, sa, ld_sa, b, sb, act, d, q, s, ld_s, pre, m_indices, masked_m, groups, m, n, k,
+                           workspace, workspace ? workspace_bytes : 0, static_cast<hipStream_t>(stream), cus);
+}
+
+int dg_gemm_fp8_gated_nt(const uint8_t* a, const float* sa, int64_t ld_sa, const uint8_t* b, const float* sb, int act,
+                         uint16_t* d, uint8_t* q, float* s, int64_t ld_s, uint16_t* pre, int64_t m, int64_t n, int64_t k,
+                         void* workspace, size_t workspace_bytes, dg_stream_t stream) {
+  return gemm_gated(0, a, sa, ld_sa, b, sb, act, d, q, s, ld_s, pre, nullptr, nullptr, 1, m, n, k, workspace,
+                    workspace_bytes, stream);
+}
+
+int dg_gemm_fp8_gated_contiguous(const uint8_t* a, const float* sa, int64_t ld_sa, const uint8_t* b, const float* sb,
+                                 const int32_t* m_indices, int64_t num_groups, int act, uint16_t* d, uint8_t* q, float* s,
+                                 int64_t ld_s, uint16_t* pre, int64_t m_total, int64_t n, int64_t k, dg_stream_t stream) {
+  return gemm_gated(1, a, sa, ld_sa, b, sb, act, d, q, s, ld_s, pre, m_indices, nullptr, num_groups, m_total, n, k,
+                    nullptr, 0, stream);
+}
+
+int dg_gemm_fp8_gated_masked(const uint8_t* a, const float* sa, int64_t ld_sa, const uint8_t* b, const float* sb,
+                             const int32_t* masked_m, int64_t num_groups, int act, uint16_t* d, uint8_t* q, float* s,
+                             int64_t ld_s, uint16_t* pre, int64_t m_max, int64_t n, int64_t k, void* workspace,
+                             size_t workspace_bytes, dg_stream_t stream) {
+  return gemm_gated(2, a, sa, ld_sa, b, sb, act, d, q, s, ld_s, pre, nullptr, masked_m, num_groups, m_max, n, k, workspace,
+                    workspace_bytes, stream);
+}
+
+size_t dg_gemm_fp8_gated_workspace_size(int64_t m, int64_t n, int64_t k, int64_t num_groups) {
+  if (m <= 0 || n <= 0 || k <= 0 || k % kKAlign || num_groups <= 0 || num_groups > 1024 || m > kInt31 || n > kInt31 || k > kInt31)
+    return 0;
+  const int cus = effective_cus();
+  return cus < 0 ? 0 : gemm_gated_workspace_size(m, n, k, num_groups, cus);
+}
+
+const char* dg_gemm_fp8_gated_config_name(int layout, int64_t m, int64_t n, int64_t k, int64_t num_groups) {
+  static thread_local char buf[96];
+  buf[0] = 0;
+  if (layout < 0 || layout > 2 || m <= 0 || n <= 0 || k <= 0 || k % kKAlign || num_groups <= 0 || m > kInt31 || n > kInt31 ||
+      k > kInt31 || (layout == 2 && num_groups > 1024))
+    return buf;
+  const int cus = effective_cus();
+  if (cus < 0) return buf;
+  gemm_gated_config_name(layout, m, n, k, num_groups, cus, buf, sizeof(buf));
+  return buf;
 }
 
 // ---- gated activation ---------------------------------------------------------------------------

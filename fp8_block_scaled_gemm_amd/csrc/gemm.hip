@@ -50,6 +50,7 @@
 #include <mutex>
 #include <type_traits>
 
+#include "gated.hpp"
 #include "gemm_common.hpp"
 
 namespace dg {
@@ -295,7 +296,119 @@ __device__ __forceinline__ void fused_act_quant_exit(const GemmParams& p) {
 }
 
 
-template <class C, int LAYOUT, bool FQ = false>
+// The epilogue of the gated form.  acc holds the wave's 16x16 fragments: gate columns in fragment rows [0, kFragN / 2), the same
+// columns' up projections in the rest, so that h = act(g) u needs values of one lane only.
+//  * Stores go through the wave's padded strip of LDS (16 rows of a fragment column) as in the plain epilogue, so that
+//    they are runs of whole row pieces; widths that are no multiple of 8 are stored element by element.
+//  * FP8: a tile is 128 columns of h, one scale group a row.  A row's maximum is taken over the lane's values, the
+//    4 lanes 16 apart, and the waves along the columns through LDS.
+template <class C, int LAYOUT>
+__device__ __forceinline__ void gated_epilogue(const GemmParams& p, const TileCoord& t, int m0, int n0, int wave_n, int wm0,
+                                               int wave, int lane, v4f (*acc)[C::kFragM], uint8_t* lds) {
+  constexpr int kHF = C::kFragN / 2, kCols = 16 * kHF;   // fragments and columns of h a wave holds
+  constexpr bool kTwoPass = LAYOUT == kContiguous && C::BM > kGroup;
+  const int l16 = lane & 15, g4 = lane >> 4;
+  const int wc0 = n0 + wave_n * kCols;                   // the wave's first column of h
+  const int64_t row_base = LAYOUT == kMasked ? (int64_t)t.g * p.m : 0;
+  auto stored = [&](int mrow) { return (!kTwoPass || mrow >= t.m_lo) && mrow < t.m_valid; };
+  constexpr int kPitch = kCols * 2 + 16;
+  constexpr int kStripBytes = 16 * kPitch;
+  static_assert(C::kWaves * kStripBytes + 4 * C::kWavesN * C::BM <= (C::BN + C::BM) * kGroup,
+                "the strips and the rows' maxima fit in one ring buffer");
+  uint8_t* strip = lds + wave * kStripBytes;
+  // fragments [f0, f0 + kHF) of fragment column j as bf16 to columns wc0 .. of rows `ld` elements long, `off` elements in
+  auto store_bf16 = [&](uint16_t* out, int64_t ld, int off, int f0, int j) {
+    if ((p.n & 7) == 0) {
+#pragma unroll
+      for (int i = 0; i < kHF; ++i) {
+        uint2 v;
+        v.x = pack2_bf16_rne(acc[f0 + i][j][0], acc[f0 + i][j][1]);
+        v.y = pack2_bf16_rne(acc[f0 + i][j][2], acc[f0 + i][j][3]);
+        *reinterpret_cast<uint2*>(strip + l16 * kPitch + (16 * i + 4 * g4) * 2) = v;
+      }
+      constexpr int kChunksRow = kCols / 8, kChunks = 16 * kChunksRow;
+#pragma unroll
+      for (int u = 0; u < (kChunks + 63) / 64; ++u) {
+        const int c = lane + 64 * u;
+        const int row = c / kChunksRow, cc = c % kChunksRow;
+        const int mrow = m0 + wm0 + 16 * j + row, ncol = wc0 + 8 * cc;
+        if (c < kChunks && stored(mrow) && ncol < p.n)
+          *reinterpret_cast<u32x4*>(out + (row_base + mrow) * ld + off + ncol) =
+              *reinterpret_cast<const u32x4*>(strip + row * kPitch + cc * 16);
+      }
+    } else {
+      const int mrow = m0 + wm0 + 16 * j + l16;
+      if (!stored(mrow)) return;
+      uint16_t* drow = out + (row_base + mrow) * ld + off;
+#pragma unroll
+      for (int i = 0; i < kHF; ++i) {
+        const int ncol = wc0 + 16 * i + 4 * g4;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (ncol + r < p.n) drow[ncol + r] = (uint16_t)pack2_bf16_rne(acc[f0 + i][j][r], 0.0f);
+      }
+    }
+  };
+  __syncthreads();   // every wave is done with the ring (the last K block's operands)
+#pragma unroll
+  for (int j = 0; j < C::kFragM; ++j) {
+    if (p.pre != nullptr) {
+      store_bf16(p.pre, 2 * (int64_t)p.n, 0, 0, j);
+      store_bf16(p.pre, 2 * (int64_t)p.n, p.n, kHF, j);
+    }
+#pragma unroll
+    for (int i = 0; i < kHF; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float g = acc[i][j][r];
+        acc[i][j][r] = (p.act == kSilu ? act_value<kSilu>(g) : act_value<kGelu>(g)) * acc[kHF + i][j][r];
+      }
+    if (p.q == nullptr) store_bf16(p.d, p.n, 0, 0, j);
+  }
+  if (p.q == nullptr) return;
+  static_assert(C::BN == 2 * kGroup, "a tile is one scale group wide");
+  float* s_max = reinterpret_cast<float*>(lds + C::kWaves * kStripBytes);
+  float amax[C::kFragM];
+#pragma unroll
+  for (int j = 0; j < C::kFragM; ++j) {
+    float a = fabsf(acc[0][j][0]);
+#pragma unroll
+    for (int i = 0; i < kHF; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) a = fmaxf(a, fabsf(acc[i][j][r]));
+    a = fmaxf(a, __shfl_xor(a, 16));
+    amax[j] = fmaxf(a, __shfl_xor(a, 32));
+    if (g4 == 0) s_max[wave_n * C::BM + wm0 + 16 * j + l16] = amax[j];
+  }
+  __syncthreads();
+  constexpr int kPitch8 = kCols + 16;
+  const int nb = n0 / kGroup;
+#pragma unroll
+  for (int j = 0; j < C::kFragM; ++j) {
+    float a = amax[j];
+#pragma unroll
+    for (int w = 0; w < C::kWavesN; ++w) a = fmaxf(a, s_max[w * C::BM + wm0 + 16 * j + l16]);
+    const float s = a == 0.0f ? 1.0f : a / kE4M3Max;
+    if (wave_n == 0 && g4 == 0 && stored(m0 + wm0 + 16 * j + l16))
+      p.s[(LAYOUT == kMasked ? (int64_t)t.g * p.s_gstride : 0) + (int64_t)nb * p.ld_s + m0 + wm0 + 16 * j + l16] = s;
+#pragma unroll
+    for (int i = 0; i < kHF; ++i)
+      *reinterpret_cast<uint32_t*>(strip + l16 * kPitch8 + 16 * i + 4 * g4) =
+          pack4_e4m3(clamp448(acc[i][j][0] / s), clamp448(acc[i][j][1] / s), clamp448(acc[i][j][2] / s),
+                     clamp448(acc[i][j][3] / s));
+    constexpr int kChunksRow = kCols / 16, kChunks = 16 * kChunksRow;   // at most one a lane; n % 16 == 0
+    static_assert(kChunks <= 64, "one chunk a lane");
+    const int row = lane / kChunksRow, cc = lane % kChunksRow;
+    const int mrow = m0 + wm0 + 16 * j + row, ncol = wc0 + 16 * cc;
+    if (lane < kChunks && stored(mrow) && ncol < p.n)
+      *reinterpret_cast<u32x4*>(p.q + (row_base + mrow) * p.n + ncol) =
+          *reinterpret_cast<const u32x4*>(strip + row * kPitch8 + cc * 16);
+  }
+}
+
+// GATED: b holds two matrices, gate and up; a tile's B rows are BN / 2 rows of each, and a wave's fragment rows the gate and
+// the up rows of the same columns, each half with its own block scale.
+template <class C, int LAYOUT, bool FQ = false, bool GATED = false>
 __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
   constexpr int NT = C::kThreads;
   constexpr int S = C::STAGES;
@@ -310,6 +423,8 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
   __shared__ int s_flag;
   static_assert(NT >= 256, "the masked-layout prefix needs 256 threads");
   static_assert(!FQ || LAYOUT == kDense, "activation quantization in the launch: dense layout only");
+  static_assert(!GATED || (!FQ && !kRowB), "the gated form has block scales and quantized activations");
+  constexpr int kCols = GATED ? C::BN / 2 : C::BN;   // output columns of a tile
 
   const int tid = threadIdx.x;
   const int lane = tid & 63;
@@ -385,7 +500,7 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
       t.m_valid = p.m;
     }
     const int m0 = t.mb * C::BM;
-    const int n0 = t.nbt * C::BN;
+    const int n0 = t.nbt * kCols;
     int expert = t.g;
     if constexpr (LAYOUT == kContiguous) {
       expert = p.m_indices[m0];
@@ -437,6 +552,9 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
     const uint32_t band_step = (uint32_t)kBandRows * (uint32_t)ld;
     const __amdgpu_buffer_rsrc_t rs_b =
         make_rsrc(b_g + (int64_t)n0 * ld, p.n > n0 ? (int64_t)(p.n - n0 - 1) * ld + p.k : 0);
+    // (gated: the rows of the up matrix, n rows further)
+    const __amdgpu_buffer_rsrc_t rs_bu =
+        GATED ? make_rsrc(b_g + (int64_t)(p.n + n0) * ld, p.n > n0 ? (int64_t)(p.n - n0 - 1) * ld + p.k : 0) : rs_b;
     const __amdgpu_buffer_rsrc_t rs_a =
         make_rsrc(a_g + (int64_t)m0 * ld, t.m_valid > m0 ? (int64_t)(t.m_valid - m0 - 1) * ld + p.k : 0);
     // activation scales: lanes [kSaLanesPerWave*wave, +kSaLanesPerWave) of the BM/4 16-byte chunks
@@ -452,16 +570,29 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
     // chunks of sb[kb][n0 .. n0+BN), clamped to the caller's ld_sb row.
     const int sbr_lane = iw * C::kSbRowLanesPerWave + lane;
     const bool sb_active =
-        issuer && (kRowB ? (lane < C::kSbRowLanesPerWave && sbr_lane < C::BN / 4) : lane < C::kSbCount);
+        issuer && (kRowB ? (lane < C::kSbRowLanesPerWave && sbr_lane < C::BN / 4) : lane < (GATED ? 2 : C::kSbCount));
     int sb_blk = (n0 >> 7) + lane;
     sb_blk = sb_blk < p.nb128 ? sb_blk : p.nb128 - 1;
+    if constexpr (GATED) sb_blk = (n0 >> 7) + (lane & 1) * p.nb128;   // the gate's block and the up matrix's
     int sbr_row = n0 + 4 * sbr_lane;
     sbr_row = sbr_row + 4 <= p.ld_sb ? sbr_row : (int)p.ld_sb - 4;
     const uint32_t sb_src = kRowB ? (uint32_t)sbr_row * 4u : (uint32_t)sb_blk * (uint32_t)p.kb_total * 4u;
     const int sb_idx = ((n0 + wn0) >> 7) - (n0 >> 7);   // this wave's block within the tile
     const __amdgpu_buffer_rsrc_t rs_sa = make_rsrc(sa_g, (int64_t)p.kb_total * p.ld_sa * 4);
     const __amdgpu_buffer_rsrc_t rs_sb =
-        make_rsrc(sb_g, kRowB ? (int64_t)p.kb_total * p.ld_sb * 4 : (int64_t)p.nb128 * p.kb_total * 4);
+        make_rsrc(sb_g, kRowB ? (int64_t)p.kb_total * p.ld_sb * 4 : (int64_t)p.nb128 * p.kb_total * (GATED ? 8 : 4));
+    // tile row of this wave's B fragment i (gated: the first half of them gate rows, the second the same columns' up rows)
+    auto frag_row = [&](int i) {
+      if constexpr (GATED)
+        return (i < C::kFragN / 2 ? 0 : C::BN / 2) + wave_n * (C::WN / 2) + 16 * (i % (C::kFragN / 2));
+      else
+        return wn0 + 16 * i;
+    };
+    // resource and band of operand DMA d of a stage
+    auto dma_rsrc = [&](int d) { return d >= kBandsB ? rs_a : (GATED && d >= kBandsB / 2) ? rs_bu : rs_b; };
+    auto dma_band = [&](int d) { return (uint32_t)(d >= kBandsB ? d - kBandsB : (GATED && d >= kBandsB / 2) ? d - kBandsB / 2 : d); };
+    static_assert(!GATED || (kBandsB % 2 == 0 && C::kFragN % 2 == 0 && (C::BN / 2) % kBandRows == 0),
+                  "gated: each half of the B rows is whole bands");
 
     v4f acc[C::kFragN][C::kFragM];
 #pragma unroll
@@ -488,9 +619,8 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
 #pragma unroll
       for (int u = 0; u < C::kDmaPerWave; ++u) {
         const int q = iw + C::kIssuers * u;
-        const bool is_b = u < kBandsB;
-        const uint32_t voff = base_off + (uint32_t)(is_b ? u : u - kBandsB) * band_step;
-        lds_dma16(is_b ? rs_b : rs_a, sbase + q * (C::kDmaRows * kGroup), chunk_out ? 0xFFFFFFF0u : voff,
+        const uint32_t voff = base_off + dma_band(u) * band_step;
+        lds_dma16(dma_rsrc(u), sbase + q * (C::kDmaRows * kGroup), chunk_out ? 0xFFFFFFF0u : voff,
                   kb * kGroup);
       }
       if (sa_active)
@@ -522,7 +652,7 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
       // chunk's slot differs from the first's in bit 0 only: address ^ 16.
       const int lane_off = lds_off(l16, 2 * g4);   // == lds_off(16x + l16, 2*g4) - 16x*128
       auto read_a = [&](int i) {
-        const int off = (wn0 + 16 * i) * kGroup + lane_off;
+        const int off = frag_row(i) * kGroup + lane_off;
         return make_v8i(*reinterpret_cast<const u32x4*>(sbase + off),
                         *reinterpret_cast<const u32x4*>(sbase + (off ^ 16)));
       };
@@ -536,7 +666,7 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
       const float* sa_l = reinterpret_cast<const float*>(sbase + C::kSaOffset);
       // block scales: scale[j] = fl32(sa * sb) of the lane's row, the wave's weight block; per-row
       // B scales: scale[j] = sa, and the 4 scales of the lane's 4 B rows of fragment i in sbr[i]
-      float scale[C::kFragM];
+      float scale[C::kFragM], scale_up[C::kFragM];
       v4f sbr[kRowB ? C::kFragN : 1];
       if constexpr (kRowB) {
 #pragma unroll
@@ -545,9 +675,14 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
         for (int i = 0; i < C::kFragN; ++i)
           sbr[i] = *reinterpret_cast<const v4f*>(sbase + C::kSbOffset + 4 * (wn0 + 16 * i + 4 * g4));
       } else {
-        const float sbv = sa_l[C::BM + (wave % C::kIssuers) * (C::kSbWaveBytes / 4) + sb_idx];   // an issuer's copy
+        const float sbv = sa_l[C::BM + (wave % C::kIssuers) * (C::kSbWaveBytes / 4) + (GATED ? 0 : sb_idx)];   // an issuer's copy
 #pragma unroll
         for (int j = 0; j < C::kFragM; ++j) scale[j] = sa_l[wm0 + 16 * j + l16] * sbv;   // fl32(sa * sb)
+        if constexpr (GATED) {
+          const float sbu = sa_l[C::BM + (wave % C::kIssuers) * (C::kSbWaveBytes / 4) + 1];
+#pragma unroll
+          for (int j = 0; j < C::kFragM; ++j) scale_up[j] = sa_l[wm0 + 16 * j + l16] * sbu;
+        }
       }
 
       constexpr int Q = C::kFragN * C::kFragM;
@@ -569,7 +704,8 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
           const int i = (q - 1) / C::kFragM, j = (q - 1) % C::kFragM;
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            acc[i][j][r] = __builtin_fmaf(part[(q - 1) & 1][r], kRowB ? scale[j] * sbr[kRowB ? i : 0][r] : scale[j],
+            acc[i][j][r] = __builtin_fmaf(part[(q - 1) & 1][r], kRowB ? scale[j] * sbr[kRowB ? i : 0][r]
+                                                               : GATED && i >= C::kFragN / 2 ? scale_up[j] : scale[j],
                                           acc[i][j][r]);   // kRowB: fl32(sa * sb) per element
         }
         if (q > 0 && q < Q) {
@@ -609,6 +745,8 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
       const uint32_t sa_lane_off = sa_row < (int)p.ld_sa ? (uint32_t)sa_row * 4u : kOut;
       int sb_blk_w = (n0 + wn0) >> 7;
       sb_blk_w = sb_blk_w < p.nb128 ? sb_blk_w : p.nb128 - 1;
+      // (gated: the upper lanes copy the up block's scale, 128 bytes behind the gate block's)
+      if constexpr (GATED) sb_blk_w = (n0 >> 7) + (lane >> 5) * p.nb128;
       const uint32_t sb_wave_off = (uint32_t)sb_blk_w * (uint32_t)p.kb_total * 4u;
       // The DMAs of one stage, issued one at a time (DMA d < kDmaPerWave: operand rows; then the
       // activation scales and the weight-block scale), so that the issue can be spread over MFMAs.
@@ -635,9 +773,8 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
       auto dma_one = [&](const DmaCtx& c, int d) {
         if (d < C::kDmaPerWave) {
           const int q = iw + C::kIssuers * d;
-          const bool is_b = d < kBandsB;
-          const uint32_t voff = c.base_off + (uint32_t)(is_b ? d : d - kBandsB) * band_step;
-          lds_dma16(is_b ? rs_b : rs_a, c.sbase + q * (C::kDmaRows * kGroup), voff | (c.out_mask & kOut),
+          const uint32_t voff = c.base_off + dma_band(d) * band_step;
+          lds_dma16(dma_rsrc(d), c.sbase + q * (C::kDmaRows * kGroup), voff | (c.out_mask & kOut),
                     c.kb * kGroup);
         } else if (d == C::kDmaPerWave) {
           // (readfirstlane: the offset is uniform; keeps the compiler from computing it per lane)
@@ -654,7 +791,7 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
         for (int d = 0; d < kStageDmas; ++d) dma_one(c, d);
       };
       auto read_a = [&](SlotPtr sbase, int i) {
-        const int off = (wn0 + 16 * i) * kGroup + lane_off;
+        const int off = frag_row(i) * kGroup + lane_off;
         return make_v8i(*reinterpret_cast<const u32x4*>(sbase + off),
                         *reinterpret_cast<const u32x4*>(sbase + (off ^ 16)));
       };
@@ -671,6 +808,7 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
 #pragma unroll
         for (int j = 0; j < kFM; ++j) raw[j] = sa_w[16 * j + l16];
         raw[kFM] = *reinterpret_cast<const float*>(sbase + C::kPipeSbOffset + wave * 256);
+        if constexpr (GATED) raw[kFM + 1] = *reinterpret_cast<const float*>(sbase + C::kPipeSbOffset + wave * 256 + 128);
       };
       // Fragment rows [R0, R1) of the block in slot cur; the rows from 0 first form the promotion
       // scales sc[j] = fl32(sa * sb) from the raw ones.  Row i takes its A fragment from a[i % 3]
@@ -686,6 +824,8 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
 #pragma unroll
           for (int j = 0; j < kFM; ++j) sc[j] = raw[j] * raw[kFM];   // fl32(sa * sb)
         }
+        // gated: from the first up row on, the scales of the up block (its row lags one MFMA: formed at its promotion)
+        auto up_scale = [&](int j) { sc[j] = raw[j] * raw[kFM + 1]; };
         constexpr int T = (R1 - R0) * kFM;   // MFMAs of these rows; with dc, the stage's DMAs spread over them
         v4f part[2];
 #pragma unroll
@@ -703,6 +843,8 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
           }
           if (q > R0 * kFM) {
             const int i = (q - 1) / kFM, j = (q - 1) % kFM;
+            if constexpr (GATED)
+              if (i == kFN / 2) up_scale(j);
 #pragma unroll
             for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(part[(q - 1) & 1][r], sc[j], acc[i][j][r]);
           }
@@ -727,7 +869,7 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
       // loop iteration starts here: it waits for every DMA in flight, so what the compiler's wait
       // insertion cannot track across the loop's back edge costs nothing.  On return a[0], a[1]
       // hold the next block's first two A fragments, bop its B fragments, rn its raw scales.
-      auto bar_tail = [&](int tk, auto cur_c, auto nxt_c, v8i* a, v8i* bop, float* sc, float* rn) {
+      auto bar_tail = [&](int tk, auto cur_c, auto nxt_c, v8i* a, v8i* bop, float* sc, float* rn, const float* rc) {
         constexpr int cur_slot = decltype(cur_c)::value;
         constexpr int nxt_slot = decltype(nxt_c)::value;
         const SlotPtr cur = cur_slot == 0 ? slot0 : slot1;
@@ -737,7 +879,7 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
         __syncthreads();                      // ... and every wave's
         const DmaCtx dc = dma_ctx(tk + 2, cur_c, tk + 2 < nk);
         read_scales(nxt, rn);
-        rows(IC<kBarRow>{}, IC<kFN>{}, cur, nxt, a, bop, sc, nullptr, &dc);
+        rows(IC<kBarRow>{}, IC<kFN>{}, cur, nxt, a, bop, sc, rc, &dc);
         const v8i n0a = a[kFN % 3], n1a = a[(kFN + 1) % 3];
         a[0] = n0a;
         a[1] = n1a;
@@ -752,7 +894,7 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
       if (nk > 0) {
       issue_pipe(1, IC<1>{}, nk > 1);
       v8i bop[kFM], a[3];
-      float sc[kFM], r0[kFM + 1], r1[kFM + 1];
+      float sc[kFM], r0[kFM + 2], r1[kFM + 2];
 #pragma unroll
       for (int j = 0; j < kFM; ++j) bop[j] = read_b(slot0, j);
       read_scales(slot0, r0);
@@ -763,15 +905,15 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
       // two blocks per iteration (the slots alternate), while a block tk+2 follows; then the rest
       int tk = 0;
       for (; tk + 2 < nk; tk += 2) {
-        bar_tail(tk, IC<0>{}, IC<1>{}, a, bop, sc, r1);
+        bar_tail(tk, IC<0>{}, IC<1>{}, a, bop, sc, r1, r0);
         rows(IC<0>{}, IC<kBarRow>{}, slot1, slot0, a, bop, sc, r1, nullptr);
-        bar_tail(tk + 1, IC<1>{}, IC<0>{}, a, bop, sc, r0);
+        bar_tail(tk + 1, IC<1>{}, IC<0>{}, a, bop, sc, r0, r1);
         rows(IC<0>{}, IC<kBarRow>{}, slot0, slot1, a, bop, sc, r0, nullptr);
       }
-      bar_tail(tk, IC<0>{}, IC<1>{}, a, bop, sc, r1);
+      bar_tail(tk, IC<0>{}, IC<1>{}, a, bop, sc, r1, r0);
       if (tk + 1 < nk) {
         rows(IC<0>{}, IC<kBarRow>{}, slot1, slot0, a, bop, sc, r1, nullptr);
-        bar_tail(tk + 1, IC<1>{}, IC<0>{}, a, bop, sc, r0);
+        bar_tail(tk + 1, IC<1>{}, IC<0>{}, a, bop, sc, r0, r1);
       }
       wait_vmcnt<0>();   // the zero-filling DMAs past the last K block
       }
@@ -859,6 +1001,10 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
         __hip_atomic_store(p.counters + sidx, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
 
+    if constexpr (GATED) {
+      gated_epilogue<C, LAYOUT>(p, t, m0, n0, wave_n, wm0, wave, lane, acc, st0);
+      continue;
+    }
     // ---- epilogue: fp32 -> bf16 (RNE), row-major store, edge masking ------------
     uint16_t* d_g = p.d + (LAYOUT == kMasked ? (int64_t)t.g * p.d_gstride : 0);
     if ((p.n & 7) == 0) {
@@ -937,9 +1083,9 @@ struct LaunchInfo {
   int lds_bytes;   // the kernel's static LDS: its __shared__ arrays
 };
 
-template <class C, int LAYOUT, bool FQ = false>
+template <class C, int LAYOUT, bool FQ = false, bool GATED = false>
 static LaunchInfo info() {
-  void (*fn)(GemmParams) = gemm_fp8_kernel<C, LAYOUT, FQ>;
+  void (*fn)(GemmParams) = gemm_fp8_kernel<C, LAYOUT, FQ, GATED>;
   constexpr int kStage = stage_bytes<C, LAYOUT>();
   constexpr int kLds = 2 * kStage + (C::STAGES > 2 ? kStage : 16) + (C::STAGES > 3 ? kStage : 16) +
                        4 * (LAYOUT == kMasked ? 1025 + 256 + 1 : 3);
@@ -1023,8 +1169,7 @@ struct Plan {
   size_t ws_bytes;   // needed workspace for this plan (0 when splits == 1)
 };
 
-static void finish_plan(Plan& pl, int64_t m, int64_t n, int64_t k, int64_t groups) {
-  const LaunchInfo li = cfg_info<kDense>(pl.cfg);
+static void finish_plan(Plan& pl, const LaunchInfo& li, int64_t m, int64_t n, int64_t k, int64_t groups) {
   pl.bn = li.bn;
   pl.bm = li.bm;
   pl.tiles_m = (int)((m + li.bm - 1) / li.bm);
@@ -1041,6 +1186,10 @@ static void finish_plan(Plan& pl, int64_t m, int64_t n, int64_t k, int64_t group
   pl.ws_bytes = 0;
   if (pl.splits > 1)
     pl.ws_bytes = kCounterBytes + (size_t)(pl.tiles - pl.tail_start) * pl.splits * (size_t)li.bn * li.bm * 4;
+}
+
+static void finish_plan(Plan& pl, int64_t m, int64_t n, int64_t k, int64_t groups) {
+  finish_plan(pl, cfg_info<kDense>(pl.cfg), m, n, k, groups);
 }
 
 // K splits of the tiles in the partial last round of the persistent grid (1: none).  That round
@@ -1264,9 +1413,8 @@ size_t gemm_workspace_size(int64_t m, int64_t n, int64_t k, int64_t groups, int 
   return dense > rowb ? dense : rowb;
 }
 
-template <int LAYOUT, bool FQ = false>
-static int launch_layout(GemmParams p, const Plan& pl, hipStream_t stream, int num_cus) {
-  const LaunchInfo li = cfg_info<LAYOUT, FQ>(pl.cfg);
+template <int LAYOUT>
+static int launch_info(const LaunchInfo& li, GemmParams p, const Plan& pl, hipStream_t stream, int num_cus) {
   const int occ = occupancy(li);
   const int64_t tiles = (int64_t)pl.tiles_m * pl.tiles_n * (LAYOUT == kContiguous ? 1 : p.num_groups);
   const int64_t items = pl.tail_start + (tiles - pl.tail_start) * pl.splits;
@@ -1277,6 +1425,11 @@ static int launch_layout(GemmParams p, const Plan& pl, hipStream_t stream, int n
   void* args[] = {&p};
   const hipError_t e = hipLaunchKernel(li.fn, dim3((unsigned)grid), dim3(li.threads), args, 0, stream);
   return e == hipSuccess ? kOk : set_error(kHip, "gemm launch: %s", hipGetErrorString(e));
+}
+
+template <int LAYOUT, bool FQ = false>
+static int launch_layout(GemmParams p, const Plan& pl, hipStream_t stream, int num_cus) {
+  return launch_info<LAYOUT>(cfg_info<LAYOUT, FQ>(pl.cfg), p, pl, stream, num_cus);
 }
 
 static GemmParams make_params(int layout, const Plan& pl, const uint8_t* a, const float* sa, int64_t ld_sa,
@@ -1342,6 +1495,126 @@ int launch_gemm(int layout, const uint8_t* a, const float* sa, int64_t ld_sa, co
     case kMasked: return launch_layout<kMasked>(p, pl, stream, num_cus);
     case kDenseRowB: return launch_layout<kDenseRowB>(p, pl, stream, num_cus);
     default: return launch_layout<kDense>(p, pl, stream, num_cus);
+  }
+}
+
+// ---- gated form: both projections of a feed-forward block, the activation and the product ------
+// The large tiles of the plain forms, with 128 gate and 128 up rows for 256 rows of weights; up to 64 rows a 32- or 64-row
+// tile of the two-stage ring whose weight rows are 256 too, so that a tile holds whole scale groups of h.
+enum GatedCfgId : int { kGatedRows128 = 0, kGatedWide, kGatedSquare, kGatedDec32, kGatedDec64 };
+using CfgGatedDec32 = Cfg<256, 32, 64, 32, 2>;
+using CfgGatedDec64 = Cfg<256, 64, 64, 32, 2>;
+
+template <int LAYOUT>
+static LaunchInfo gated_info(int cfg) {
+  switch (cfg) {
+    case kGatedWide:
+      if constexpr (LAYOUT != kContiguous) return info<CfgWide, LAYOUT, false, true>();
+      else return info<CfgRows128, LAYOUT, false, true>();
+    case kGatedSquare: return info<CfgSquare, LAYOUT, false, true>();
+    case kGatedDec32:
+      if constexpr (LAYOUT != kContiguous) return info<CfgGatedDec32, LAYOUT, false, true>();
+      else return info<CfgRows128, LAYOUT, false, true>();
+    case kGatedDec64:
+      if constexpr (LAYOUT != kContiguous) return info<CfgGatedDec64, LAYOUT, false, true>();
+      else return info<CfgRows128, LAYOUT, false, true>();
+    default: return info<CfgRows128, LAYOUT, false, true>();
+  }
+}
+
+static int gated_cfg_of(int cfg) { return cfg == kCfgSquare ? kGatedSquare : cfg == kCfgWide ? kGatedWide : kGatedRows128; }
+
+// n: the width of h.
+static Plan make_gated_plan(int layout, int64_t m, int64_t n, int64_t k, int64_t call_groups, int num_cus, bool allow_split) {
+  const int64_t groups = layout == kMasked ? call_groups : 1;
+  const int64_t weight_rows = (n + kGroup - 1) / kGroup * (2 * kGroup);   // rows of b in whole tiles
+  const int kb_total = (int)((k + kGroup - 1) / kGroup);
+  Plan pl{};
+  pl.splits = 1;
+  pl.kb_per_split = kb_total;
+  int max_split = 1;
+  if (layout == kContiguous) {
+    pl.cfg = gated_cfg_of(choose_contiguous(m, weight_rows, call_groups, num_cus));
+  } else if (m <= 64) {
+    pl.cfg = m <= 32 ? kGatedDec32 : kGatedDec64;
+    max_split = kb_total / 2;
+  } else {
+    pl.cfg = gated_cfg_of(choose_large(m, weight_rows, groups, num_cus, kb_total, false));
+    max_split = kb_total / 4;
+  }
+  const LaunchInfo li = gated_info<kDense>(pl.cfg);
+  // few tiles: split K so that every CU gets work
+  const int64_t tiles = ((m + li.bm - 1) / li.bm) * (weight_rows / li.bn) * groups;
+  if (allow_split && layout != kContiguous && 2 * tiles <= num_cus) {
+    int64_t want = num_cus / tiles;
+    if (want > max_split) want = max_split;
+    if (want > kMaxSplits) want = kMaxSplits;
+    if (want > 1) pl.splits = (int)want;
+  }
+  // DG_PLAN, as for the plain forms
+  if (const char* e = std::getenv("DG_PLAN"); e != nullptr && e[0] != '\0') {
+    int bn = 0, bm = 0, want = 0;
+    for (const char* q = e; *q;) {
+      if (std::sscanf(q, "tile=%dx%d", &bn, &bm) == 2 || std::sscanf(q, "splits=%d", &want) == 1) {}
+      const char* c = std::strchr(q, ',');
+      if (c == nullptr) break;
+      q = c + 1;
+    }
+    static const int kAll[] = {kGatedRows128, kGatedWide, kGatedSquare, kGatedDec32, kGatedDec64};
+    for (const int cfg : kAll) {
+      const LaunchInfo l = gated_info<kDense>(cfg);
+      if (layout == kContiguous && cfg != kGatedRows128 && cfg != kGatedSquare) continue;
+      if (l.bn == bn && l.bm == bm) pl.cfg = cfg;
+    }
+    if (want > 0 && allow_split && layout != kContiguous) pl.splits = want < kMaxSplits ? want : kMaxSplits;
+  }
+  pl.kb_per_split = (kb_total + pl.splits - 1) / pl.splits;
+  pl.splits = (kb_total + pl.kb_per_split - 1) / pl.kb_per_split;   // no empty split
+  finish_plan(pl, gated_info<kDense>(pl.cfg), m, weight_rows, k, groups);
+  return pl;
+}
+
+size_t gemm_gated_workspace_size(int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus) {
+  return make_gated_plan(groups > 1 ? kMasked : kDense, m, n, k, groups, num_cus, true).ws_bytes;
+}
+
+void gemm_gated_config_name(int layout, int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus, char* buf,
+                            size_t len) {
+  const Plan pl = make_gated_plan(layout, m, n, k, layout == kDense ? 1 : groups, num_cus, layout != kContiguous);
+  snprintf(buf, len, "%dx%d/%dwaves/split%d", pl.bn, pl.bm, gated_info<kDense>(pl.cfg).threads / 64, pl.splits);
+}
+
+int launch_gemm_gated(int layout, const uint8_t* a, const float* sa, int64_t ld_sa, const uint8_t* b, const float* sb,
+                      int act, uint16_t* d, uint8_t* q, float* s, int64_t ld_s, uint16_t* pre, const int32_t* m_indices,
+                      const int32_t* masked_m, int64_t groups, int64_t m, int64_t n, int64_t k, void* ws, size_t ws_bytes,
+                      hipStream_t stream, int num_cus) {
+  if (2 * n * k > 0x7fffffffLL || m * k > 0x7fffffffLL)
+    return set_error(kUnsupported, "gated gemm: one group's operand must be < 2^31 bytes (m=%lld n=%lld k=%lld)",
+                     (long long)m, (long long)n, (long long)k);
+  const int64_t plan_groups = layout == kDense ? 1 : groups;
+  Plan pl = make_gated_plan(layout, m, n, k, plan_groups, num_cus, layout != kContiguous && ws != nullptr);
+  if (pl.splits > 1 && ws_bytes < pl.ws_bytes) pl = make_gated_plan(layout, m, n, k, plan_groups, num_cus, false);
+  GemmParams p = make_params(layout, pl, a, sa, ld_sa, b, sb, 0, k, d, m_indices, masked_m, groups, m, n, k);
+  p.b_gstride = 2 * n * k;
+  p.sb_gstride = 2 * (int64_t)p.nb128 * p.kb_total;
+  p.q = q;
+  p.s = s;
+  p.ld_s = ld_s;
+  p.s_gstride = (int64_t)p.nb128 * ld_s;
+  p.pre = pre;
+  p.act = act;
+  if (pl.splits > 1) {
+    p.counters = static_cast<unsigned*>(ws);
+    p.ws = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kCounterBytes);
+  }
+  if (p.debug)
+    std::fprintf(stderr, "[dg] gated gemm %s m=%lld n=%lld k=%lld groups=%lld: %dx%d splits=%d workspace=%zu/%zu bytes\n",
+                 layout == kContiguous ? "contiguous" : layout == kMasked ? "masked" : "normal", (long long)m, (long long)n,
+                 (long long)k, (long long)groups, pl.bn, pl.bm, pl.splits, pl.ws_bytes, ws_bytes);
+  switch (layout) {
+    case kContiguous: return launch_info<kContiguous>(gated_info<kContiguous>(pl.cfg), p, pl, stream, num_cus);
+    case kMasked: return launch_info<kMasked>(gated_info<kMasked>(pl.cfg), p, pl, stream, num_cus);
+    default: return launch_info<kDense>(gated_info<kDense>(pl.cfg), p, pl, stream, num_cus);
   }
 }
 

@@ -45,6 +45,14 @@ struct GemmParams {
   int fq_bf16;
   int fq_max_polls; // bound of the wait for every chunk (polls of the finished-chunk counter)
   int debug;        // DG_DEBUG: run the layout checks and report through the diagnostics words
+  // Gated form: n is the width of h; b holds n gate rows and then n up rows (sb likewise, nb128 block rows each) per group.
+  // h goes to d, or quantized to q / s (then d is null); pre (2n wide: gate, up) is null if it is not kept.
+  uint8_t* q;
+  float* s;
+  uint16_t* pre;
+  int64_t ld_s;
+  int64_t s_gstride;
+  int act;
 };
 
 // Flag bits of the device diagnostics word (sticky until read with clearing).

@@ -487,6 +487,40 @@ size_t dg_gemm_int8_workspace_size(int64_t m, int64_t n, int64_t k, int64_t num_
 enum dg_act { DG_ACT_SILU = 0, DG_ACT_GELU = 1 };
 
 /*
+ * Gated FP8 GEMMs: both projections of a feed-forward block, the activation and the product in one launch.
+ *   g = A * Bg^T, u = A * Bu^T (each with the block scales and promoted sums of dg_gemm_fp8_nt);  h = act(g) * u in fp32.
+ * a, sa   : as dg_gemm_fp8_nt (contiguous, masked: as those forms).
+ * b, sb   : E4M3 (2, n, k) and fp32 (2, ceil(n/128), KB) per group: the gate matrix, then the up matrix, each quantized by
+ *           itself (dg_quantize_per_block of 2 matrices per group; where n % 128 == 0 that is its result for (2n, k)).
+ * output  : exactly one of
+ *           d  bf16 (m, n), h rounded once, or
+ *           q, s: the codes and scales that dg_quantize_per_token_group gives for h in fp32, s[nb * ld_s + row] (masked: per
+ *           group), ready for the next FP8 product; n % 16 == 0, ld_s >= m (m_max), ld_s % 4 == 0.
+ * pre     : bf16 (m, 2n), a row (g | u) rounded once, as dg_gated_act_grad reads it; NULL if it is not wanted.
+ * Rows that the plain forms leave unwritten (m_indices outside [0, num_groups), rows at or past masked_m) are left
+ * unwritten in every output.
+ * workspace : as dg_gemm_fp8_nt's (its first 64 KiB zero before the first use, left zero by every call; calls that share it
+ *   must be ordered); NULL or smaller than dg_gemm_fp8_gated_workspace_size: no K split.
+ * Errors: as the plain forms, an unknown activation, both or neither of d and q, q without s; DG_ERR_UNSUPPORTED where 2 n k or
+ * m k reaches 2^31.  Deterministic.
+ */
+int dg_gemm_fp8_gated_nt(const uint8_t* a, const float* sa, int64_t ld_sa, const uint8_t* b, const float* sb, int act,
+                         uint16_t* d, uint8_t* q, float* s, int64_t ld_s, uint16_t* pre, int64_t m, int64_t n, int64_t k,
+                         void* workspace, size_t workspace_bytes, dg_stream_t stream);
+int dg_gemm_fp8_gated_contiguous(const uint8_t* a, const float* sa, int64_t ld_sa, const uint8_t* b, const float* sb,
+                                 const int32_t* m_indices, int64_t num_groups, int act, uint16_t* d, uint8_t* q, float* s,
+                                 int64_t ld_s, uint16_t* pre, int64_t m_total, int64_t n, int64_t k, dg_stream_t stream);
+int dg_gemm_fp8_gated_masked(const uint8_t* a, const float* sa, int64_t ld_sa, const uint8_t* b, const float* sb,
+                             const int32_t* masked_m, int64_t num_groups, int act, uint16_t* d, uint8_t* q, float* s,
+                             int64_t ld_s, uint16_t* pre, int64_t m_max, int64_t n, int64_t k, void* workspace,
+                             size_t workspace_bytes, dg_stream_t stream);
+
+/* Workspace bytes that let dg_gemm_fp8_gated_nt / _masked split K (0: never split), and the tile and K split of a shape
+ * (layout 0 normal, 1 contiguous, 2 masked), as dg_gemm_workspace_size and dg_gemm_config_name. */
+size_t dg_gemm_fp8_gated_workspace_size(int64_t m, int64_t n, int64_t k, int64_t num_groups);
+const char* dg_gemm_fp8_gated_config_name(int layout, int64_t m, int64_t n, int64_t k, int64_t num_groups);
+
+/*
  * h from pre (`dtype`; n a positive multiple of 16):
  *   dg_gated_act       h (rows, n) in pre's type;
  *   dg_gated_act_fp8   q, s: the codes and scales that dg_quantize_per_token_group gives for h in fp32 (its layout of

@@ -22,6 +22,81 @@ def lib():
 
 # ---- what is refused ------------------------------------------------------------------------------
 
+def test_gated_refusals(lib):
+    base = dict(a=P, sa=P, ld=8, b=P, sb=P)
+    out = dict(act=0, d=P, q=None, s=None, ld_s=0, pre=None, m=8, n=64, k=128)
+
+    def nt(ws=None, nws=0, **kw):
+        v = {**base, **out, **kw}
+        return lib.dg_gemm_fp8_gated_nt(*v.values(), ws, nws, None)
+
+    fp8 = dict(d=None, q=P, s=P, ld_s=8)
+    common = (dict(a=None), dict(sa=None), dict(b=None), dict(sb=None), dict(d=None), dict(q=P), dict(act=2), dict(act=-1),
+              dict(m=-1), dict(n=-1), dict(k=0), dict(k=24), dict(ld=4), dict(ld=10), dict(a=MIS), dict(b=MIS), dict(d=MIS),
+              dict(pre=MIS), {**fp8, "s": None}, {**fp8, "n": 72}, {**fp8, "ld_s": 4}, {**fp8, "ld_s": 9}, {**fp8, "s": MIS},
+              {**fp8, "q": MIS})
+    for bad in common + (dict(ws=MIS),):
+        assert nt(**bad) == INVALID, bad
+    assert nt(m=0, a=None, sa=None, d=None) == OK and nt(n=0) == OK
+    assert lib.dg_set_num_cus(256) == OK     # (without a device, so that the plans can be made)
+    assert nt(n=1 << 23, k=128) == UNSUPPORTED
+    assert nt(m=1 << 21, k=1024, ld=1 << 21) == UNSUPPORTED
+
+    def grouped(name, where=P, g=2, tail=(), **kw):
+        v = {**base, **out, **kw}
+        v = list(v.values())
+        return getattr(lib, name)(*v[:5], where, g, *v[5:], *tail, None)
+
+    for bad in common[:-1] + (dict(where=None), dict(where=MIS), dict(g=-1)):
+        assert grouped("dg_gemm_fp8_gated_masked", tail=(None, 0), **bad) == INVALID, bad
+        assert grouped("dg_gemm_fp8_gated_contiguous", **{"m": 128, "ld": 128, **({"ld_s": 128} if bad.get("q") else {}), **bad}) == INVALID, bad
+    assert grouped("dg_gemm_fp8_gated_masked", tail=(None, 0), g=1025) == INVALID
+    assert grouped("dg_gemm_fp8_gated_contiguous", m=100, ld=100) == INVALID
+    assert grouped("dg_gemm_fp8_gated_contiguous", g=0) == OK and grouped("dg_gemm_fp8_gated_masked", g=0, tail=(None, 0)) == OK
+
+
+def test_gated_plans(lib, monkeypatch):
+    """Names and workspaces of the plans; forced ones; no plan for what is refused."""
+    assert lib.dg_set_num_cus(256) == OK
+    for m, n, k, groups in ((1, 2048, 7168, 1), (64, 128, 4096, 1), (100, 256, 2048, 1), (8192, 8192, 7168, 1), (5, 300, 640, 8)):
+        name = dg.dg_gemm_fp8_gated_config_name(2 if groups > 1 else 0, m, n, k, groups)
+        tile, splits = name.split("/")[0], int(name.rsplit("split", 1)[1])
+        bn, bm = (int(v) for v in tile.split("x"))
+        assert bn == 256 and bm in (32, 64, 128, 192, 256)
+        tiles = -(-n // 128) * -(-m // bm) * groups
+        need = dg.dg_gemm_fp8_gated_workspace_size(m, n, k, groups)
+        assert need == (65536 + tiles * splits * bn * bm * 4 if splits > 1 else 0)
+    monkeypatch.setenv("DG_PLAN", "tile=256x192,splits=5")
+    assert dg.dg_gemm_fp8_gated_config_name(0, 8, 128, 1280) == "256x192/8waves/split5"
+    assert not dg.dg_gemm_fp8_gated_config_name(1, 128, 128, 1280, 2).startswith("256x192")
+    monkeypatch.delenv("DG_PLAN")
+    for bad in ((3, 8, 128, 128, 1), (0, 0, 128, 128, 1), (0, 8, 0, 128, 1), (0, 8, 128, 100, 1), (2, 8, 128, 128, 0), (2, 8, 128, 128, 1025)):
+        assert dg.dg_gemm_fp8_gated_config_name(*bad) == ""
+    assert dg.dg_gemm_fp8_gated_workspace_size(8, 128, 100) == 0 and dg.dg_gemm_fp8_gated_workspace_size(8, 128, 128, 0) == 0
+
+
+def test_gated_binding_refusals():
+    a, sa = torch.zeros((8, 128), dtype=torch.uint8), torch.zeros((1, 8))
+    b, sb = torch.zeros((2, 64, 128), dtype=torch.uint8), torch.zeros((2, 1, 1))
+    mi = torch.zeros(8, dtype=torch.int32)
+    for bad in (lambda: dg.dg_gemm_fp8_gated_nt(a, sa, b, sb),   # not on a device
+                lambda: dg.dg_gemm_fp8_gated_nt(a[0], sa, b, sb), lambda: dg.dg_gemm_fp8_gated_nt(a, sa, b[:, :, :64], sb),
+                lambda: dg.dg_gemm_fp8_gated_nt(a, sa, b.view(128, 128), sb),   # stacked rows need N % 128 == 0
+                lambda: dg.dg_gemm_fp8_gated_nt(a, sa, b, sb[:1]), lambda: dg.dg_gemm_fp8_gated_nt(a, sa[:, :4], b, sb),
+                lambda: dg.dg_gemm_fp8_gated_nt(a.int(), sa, b, sb), lambda: dg.dg_gemm_fp8_gated_nt(a, sa.double(), b, sb),
+                lambda: dg.dg_gemm_fp8_gated_nt(a, sa, b, sb, out="int8"), lambda: dg.dg_gemm_fp8_gated_nt(a, sa, b, sb, q=a),
+                lambda: dg.dg_gemm_fp8_gated_nt(a, sa, b, sb, out="fp8", d=torch.zeros((8, 64), dtype=torch.bfloat16)),
+                lambda: dg.dg_gemm_fp8_gated_nt(a, sa, b[:, :40].contiguous(), sb, out="fp8"),
+                lambda: dg.dg_gemm_fp8_gated_nt(a, sa, b, sb, pre=torch.zeros((8, 64), dtype=torch.bfloat16)),
+                lambda: dg.dg_gemm_fp8_gated_nt(a, sa, b, sb, d=torch.zeros((8, 64))),
+                lambda: dg.dg_gemm_fp8_gated_contiguous(a, sa, b[None], sb[None], mi.long()),
+                lambda: dg.dg_gemm_fp8_gated_contiguous(a, sa, b[None], sb[None], mi[:4]),
+                lambda: dg.dg_gemm_fp8_gated_masked(a, sa, b[None], sb[None], mi[:1]),
+                lambda: dg.dg_gemm_fp8_gated_masked(a[None], sa[None], b[None], sb[None], mi)):
+        with pytest.raises(ValueError):
+            bad()
+
+
 def test_act_refusals(lib):
     def act(pre=P, dt=1, a=0, mi=None, mm=None, per=0, rows=32, n=64, h=P):
         return lib.dg_gated_act(pre, dt, a, mi, mm, per, rows, n, h, None)

@@ -1,0 +1,304 @@
+"""The gated FP8 GEMMs against 64-bit arithmetic and against the plain forms.
+
+Tolerances: a matrix instruction cuts what it adds at 2^-15 or less of the magnitudes of a K block's products (the largest
+error of 16x16x128 products of random codes is 1.7e-5 of them), the promotion adds at most KB * 2^-24 and the scales' product
+2^-24; together below 2^-14 of S = sum |a b| for each projection.  Through h = act(g) u that becomes at most
+1.13 e_g |u| + |act(g)| e_u + 1.13 e_g e_u (the slopes of both activations are below 1.13), and the activation adds
+(10 + 6 |z|) 2^-24 (see the activation's own tests).  bf16 outputs are rounded once (2^-8); E4M3 codes are within half a step
+of h / s: 2^-4 of it, or 2^-10 below the normal codes.
+
+Without a K split the projections are, K block by K block, the operations of the plain forms: the same bits.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import fp8_block_scaled_gemm_amd as dg
+import oracle
+from gpu_util import device, say
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+OF = oracle.feed_forward
+
+
+def operands(rng, lead, n, k, groups=None):
+    """Quantized a (*lead, k) and gate and up weights ([groups,] 2, n, k)."""
+    x = rng.standard_normal((*lead, k)).astype(np.float32)
+    x.reshape(-1, k)[::7] *= 30
+    w = (rng.standard_normal((*(() if groups is None else (groups,)), 2, n, k)) / np.sqrt(k) * 1.5).astype(np.float32)
+    a, sa = dg.dg_quantize_per_token_group(torch.from_numpy(x).to(device()))
+    b, sb = dg.dg_quantize_per_block(torch.from_numpy(w.reshape(-1, n, k)).to(device()))
+    return a, sa, b.view(*w.shape), sb.view(*w.shape[:-2], *sb.shape[-2:])
+
+
+def alone(t):
+    """A copy with an allocation of its own (the plain forms want 16-byte aligned operands)."""
+    return t.clone(memory_format=torch.contiguous_format)
+
+
+def dequantized(a, sa, rows, b, sb):
+    """float64 a (rows, k) and b (2, n, k)."""
+    k, n = a.shape[-1], b.shape[-2]
+    av = a.view(torch.float8_e4m3fn).double().cpu().numpy()
+    s = sa[:, :rows].t().double().cpu().numpy()
+    av = av * np.repeat(s, 128, axis=1)[:, :k]
+    bv = b.view(torch.float8_e4m3fn).double().cpu().numpy()
+    t = sb.double().cpu().numpy()
+    return av, bv * np.repeat(np.repeat(t, 128, axis=1)[:, :n], 128, axis=2)[:, :, :k]
+
+
+def reference(a, sa, rows, b, sb, act):
+    """(g, u, h, tolerances of g, u and h) in 64 bits."""
+    av, bv = dequantized(a, sa, rows, b, sb)
+    g, u = av @ bv[0].T, av @ bv[1].T
+    eg, eu = (2.0 ** -14 * (np.abs(av) @ np.abs(bv[i]).T) for i in (0, 1))
+    f = OF.act_value(g, act)
+    eh = 1.13 * eg * np.abs(u) + np.abs(f) * eu + 1.13 * eg * eu + (10 + 6 * np.abs(OF._arg(g, act)[0])) * 2.0 ** -24 * np.abs(f * u)
+    return g, u, f * u, eg, eu, eh
+
+
+def host(t):
+    return t.detach().double().cpu().numpy()
+
+
+def check_bf16(got, want, tol, what):
+    g = host(got)
+    bad = ~(np.abs(g - want) <= tol + 2.0 ** -8 * (np.abs(want) + tol) + 2.0 ** -126)
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} off"
+
+
+def check_fp8(q, s, h, tol, what):
+    """Codes q (rows, n) and scales s (rows, groups) of h."""
+    rows, n = h.shape
+    v, s = host(q.view(torch.float8_e4m3fn)), host(s)
+    for kb in range(-(-n // 128)):
+        c = slice(128 * kb, min(128 * kb + 128, n))
+        want = np.abs(h[:, c]).max(1) / 448
+        most = tol[:, c].max(1) / 448
+        assert np.all(np.abs(s[:, kb] - want) <= most + 2.0 ** -23 * want), what
+        step = np.maximum(np.abs(h[:, c]) * 2.0 ** -4, s[:, kb:kb + 1] * 2.0 ** -10)
+        assert np.all(np.abs(v[:, c] * s[:, kb:kb + 1] - h[:, c]) <= step * 1.001 + 1.07 * (tol[:, c] + most[:, None] * 448)), what
+        assert np.all(np.abs(v[:, c]).max(1) == 448), what
+
+
+def same_bits(a, b, what=""):
+    assert a.dtype == b.dtype and a.shape == b.shape, what
+    view = {1: torch.uint8, 2: torch.int16, 4: torch.int32}[a.element_size()]
+    assert torch.equal(a.contiguous().view(view), b.contiguous().view(view)), what
+
+
+SHAPES = [(1, 16, 16), (1, 128, 128), (1, 2048, 1024), (3, 144, 272), (17, 64, 256), (33, 400, 640), (64, 256, 4096), (65, 128, 1024),
+          (100, 272, 1552), (130, 384, 512), (257, 1040, 768), (600, 512, 2048)]
+ODD = [(1, 1, 128), (5, 7, 144), (31, 130, 16), (64, 129, 400), (129, 37, 256), (300, 1057, 528)]
+
+
+@pytest.mark.parametrize("m,n,k", SHAPES + ODD)
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_normal(m, n, k, act):
+    rng = np.random.default_rng(m + n + k)
+    say("gated normal", m, n, k, act)
+    a, sa, b, sb = operands(rng, (m,), n, k)
+    g, u, h, eg, eu, eh = reference(a, sa, m, b, sb, act)
+    for use in (True, False):
+        pre = torch.full((m, 2 * n), 9.0, dtype=BF16, device=device())
+        d = dg.dg_gemm_fp8_gated_nt(a, sa, b, sb, act=act, pre=pre, use_workspace=use)
+        check_bf16(d, h, eh, "h")
+        check_bf16(pre[:, :n], g, eg, "gate")
+        check_bf16(pre[:, n:], u, eu, "up")
+        same_bits(d, dg.dg_gemm_fp8_gated_nt(a, sa, b, sb, act=act, use_workspace=use), "without pre")
+        if not use:
+            for i in (0, 1):
+                plain = dg.dg_gemm_fp8_nt(a, sa, alone(b[i]), alone(sb[i]), use_workspace=False)
+                same_bits(pre[:, i * n:(i + 1) * n], plain, f"projection {i} as the plain GEMM")
+        if n % 16 == 0:
+            pre2 = torch.full((m, 2 * n), 9.0, dtype=BF16, device=device())
+            q, s = dg.dg_gemm_fp8_gated_nt(a, sa, b, sb, act=act, out="fp8", pre=pre2, use_workspace=use)
+            check_fp8(q, s[:, :m].t(), h, eh, "fp8")
+            same_bits(pre2, pre, "pre beside fp8")
+            q2, s2 = dg.dg_gemm_fp8_gated_nt(a, sa, b, sb, act=act, out="fp8", use_workspace=use)
+            same_bits(q2, q, "again")
+            same_bits(s2[:, :m], s[:, :m], "again")
+
+
+@pytest.mark.parametrize("tile", ["256x32", "256x64", "256x128", "256x192", "256x256"])
+@pytest.mark.parametrize("splits", [1, 3, 16])
+def test_every_tile_and_split(tile, splits, monkeypatch):
+    """Every tile at sizes on both sides of its edges, each split: values, and a workspace left as it was found."""
+    rng = np.random.default_rng(splits)
+    monkeypatch.setenv("DG_PLAN", f"tile={tile},splits={splits}")
+    for m, n, k in ((1, 144, 2048), (200, 272, 400), (270, 128, 2064)):
+        say("gated tile", tile, splits, m, n, k)
+        name = dg.dg_gemm_fp8_gated_config_name(0, m, n, k)
+        kb = -(-k // 128)
+        per = -(-kb // splits)
+        assert name.startswith(tile + "/") and name.endswith(f"split{-(-kb // per)}"), name
+        a, sa, b, sb = operands(rng, (m,), n, k)
+        h, eh = reference(a, sa, m, b, sb, "silu")[2::3]
+        need = dg.dg_gemm_fp8_gated_workspace_size(m, n, k)
+        ws = torch.zeros(max(need, 16), dtype=torch.uint8, device=device())
+        d = dg.dg_gemm_fp8_gated_nt(a, sa, b, sb, workspace=ws)
+        check_bf16(d, h, eh, "h")
+        q, s = dg.dg_gemm_fp8_gated_nt(a, sa, b, sb, out="fp8", workspace=ws)
+        check_fp8(q, s[:, :m].t(), h, eh, "fp8")
+        assert torch.all(ws[:65536] == 0)
+        same_bits(d, dg.dg_gemm_fp8_gated_nt(a, sa, b, sb, workspace=ws), "again")
+
+
+@pytest.mark.parametrize("m,n,k,groups", [(1, 128, 256, 3), (20, 144, 400, 5), (64, 256, 1024, 2), (70, 272, 528, 4), (256, 384, 768, 6),
+                                          (33, 37, 256, 3), (130, 131, 144, 2)])
+def test_masked(m, n, k, groups):
+    rng = np.random.default_rng(m + n)
+    counts = [0, m, min(m, 3), -2, m + 9, max(m // 2, 1)][:groups]
+    for use in (True, False):
+        say("gated masked", m, n, k, groups, use)
+        a, sa, b, sb = operands(rng, (groups, m), n, k, groups)
+        masked = torch.tensor(counts, dtype=torch.int32, device=device())
+        pre = torch.full((groups, m, 2 * n), 9.0, dtype=BF16, device=device())
+        d = torch.full((groups, m, n), 9.0, dtype=BF16, device=device())
+        dg.dg_gemm_fp8_gated_masked(a, sa, b, sb, masked, act="gelu", d=d, pre=pre, use_workspace=use)
+        fp8 = n % 16 == 0
+        if fp8:
+            q = torch.full((groups, m, n), 0x11, dtype=torch.uint8, device=device())
+            s = torch.full((groups, -(-n // 128), -(-m // 4) * 4 + 4), 9.0, device=device())
+            dg.dg_gemm_fp8_gated_masked(a, sa, b, sb, masked, act="gelu", out="fp8", q=q, s=s, use_workspace=use)
+        for j, c in enumerate(counts):
+            c = min(max(c, 0), m)
+            assert torch.all(d[j, c:] == 9.0) and torch.all(pre[j, c:] == 9.0)
+            if fp8:
+                assert torch.all(q[j, c:] == 0x11) and torch.all(s[j, :, c:] == 9.0)
+            if not c:
+                continue
+            g, u, h, eg, eu, eh = reference(a[j, :c], sa[j], c, b[j], sb[j], "gelu")
+            check_bf16(d[j, :c], h, eh, "h")
+            check_bf16(pre[j, :c, :n], g, eg, "gate")
+            check_bf16(pre[j, :c, n:], u, eu, "up")
+            if fp8:
+                check_fp8(q[j, :c], s[j, :, :c].t(), h, eh, "fp8")
+        if not use:
+            for i in (0, 1):
+                plain = torch.full((groups, m, n), 9.0, dtype=BF16, device=device())
+                dg.dg_gemm_fp8_grouped_masked(a, sa, alone(b[:, i]), alone(sb[:, i]), masked, d=plain, use_workspace=False)
+                same_bits(pre[..., i * n:(i + 1) * n], plain, f"projection {i} as the plain GEMM")
+
+
+@pytest.mark.parametrize("tile", ["", "256x128", "256x256"])
+@pytest.mark.parametrize("experts,n,k", [([0, 0, 1, 2, 2, 2, -1], 128, 256), ([3, 0, -1, 1], 144, 400), ([1], 400, 1024),
+                                         ([-1, 2, 2, 0, 7, 1], 37, 272)])
+def test_contiguous(experts, n, k, tile, monkeypatch):
+    """Blocks of experts that change inside a 256-row tile, and blocks of none (-1, and an index past the last expert)."""
+    if tile:
+        monkeypatch.setenv("DG_PLAN", f"tile={tile}")
+    rng = np.random.default_rng(n + len(experts))
+    m, groups = 128 * len(experts), 4
+    say("gated contiguous", experts, n, k, tile)
+    a, sa, b, sb = operands(rng, (m,), n, k, groups)
+    mi = torch.tensor(np.repeat(experts, 128), dtype=torch.int32, device=device())
+    pre = torch.full((m, 2 * n), 9.0, dtype=BF16, device=device())
+    d = torch.full((m, n), 9.0, dtype=BF16, device=device())
+    dg.dg_gemm_fp8_gated_contiguous(a, sa, b, sb, mi, d=d, pre=pre)
+    fp8 = n % 16 == 0
+    if fp8:
+        q = torch.full((m, n), 0x11, dtype=torch.uint8, device=device())
+        s = torch.full((-(-n // 128), m + 4), 9.0, device=device())
+        dg.dg_gemm_fp8_gated_contiguous(a, sa, b, sb, mi, out="fp8", q=q, s=s)
+        assert torch.all(s[:, m:] == 9.0)
+    for i, e in enumerate(experts):
+        r = slice(128 * i, 128 * i + 128)
+        if not 0 <= e < groups:
+            assert torch.all(d[r] == 9.0) and torch.all(pre[r] == 9.0)
+            if fp8:
+                assert torch.all(q[r] == 0x11) and torch.all(s[:, r] == 9.0)
+            continue
+        h, eh = reference(a[r], sa[:, r], 128, b[e], sb[e], "silu")[2::3]
+        check_bf16(d[r], h, eh, "h")
+        if fp8:
+            check_fp8(q[r], s[:, r].t(), h, eh, "fp8")
+    for i in (0, 1):
+        plain = torch.full((m, n), 9.0, dtype=BF16, device=device())
+        dg.dg_gemm_fp8_grouped_contiguous(a, sa, alone(b[:, i]), alone(sb[:, i]), mi, d=plain)
+        same_bits(pre[:, i * n:(i + 1) * n], plain, f"projection {i} as the plain GEMM")
+
+
+def test_stacked_weights():
+    """b (2N, K) and (G, 2N, K) as one block quantization of both matrices gives them."""
+    rng = np.random.default_rng(2)
+    say("gated stacked weights")
+    a, sa, b, sb = operands(rng, (40,), 256, 384)
+    want = dg.dg_gemm_fp8_gated_nt(a, sa, b, sb)
+    same_bits(dg.dg_gemm_fp8_gated_nt(a, sa, b.view(512, 384), sb.view(4, 3)), want)
+    a, sa, b, sb = operands(rng, (2, 40), 128, 384, 2)
+    counts = torch.tensor([40, 40], dtype=torch.int32, device=device())
+    same_bits(dg.dg_gemm_fp8_gated_masked(a, sa, b.view(2, 256, 384), sb.view(2, 2, 3), counts),
+              dg.dg_gemm_fp8_gated_masked(a, sa, b, sb, counts))
+
+
+def test_of_zeros_and_of_none():
+    say("gated zeros")
+    d = device()
+    a, sa = torch.zeros((20, 256), dtype=torch.uint8, device=d), torch.ones((2, 20), device=d)
+    b, sb = torch.zeros((2, 144, 256), dtype=torch.uint8, device=d), torch.ones((2, 2, 2), device=d)
+    q, s = dg.dg_gemm_fp8_gated_nt(a, sa, b, sb, out="fp8")
+    assert torch.all(q == 0) and torch.all(s[:, :20] == 1)
+    assert dg.dg_gemm_fp8_gated_nt(a[:0], sa, b, sb).shape == (0, 144)
+
+
+def test_values_at_their_limits():
+    """Scales that make h overflow bf16, NaN scales: infinities and NaN where the formula has them, in their rows only."""
+    say("gated limits")
+    rng = np.random.default_rng(4)
+    a, sa, b, sb = operands(rng, (8, ), 128, 256)
+    clean = dg.dg_gemm_fp8_gated_nt(a, sa, b, sb)
+    sa[:, 2] = float("nan")
+    sa[:, 3] = 1e30
+    d = dg.dg_gemm_fp8_gated_nt(a, sa, b, sb)
+    assert torch.isnan(d[2]).all()
+    rest = [0, 1, 4, 5, 6, 7]
+    same_bits(d[rest], clean[rest])
+    # at 1e30 the gate is 0 or passes through; products with the up projection leave bf16's range or are zero
+    assert torch.all(torch.isinf(d[3]) | (d[3] == 0))
+
+
+def test_block_in_a_graph_and_on_streams():
+    """Gated product, product and norm as a block runs them, captured with workspaces of their own, against eager calls;
+    two graphs that share no workspace replayed on two streams."""
+    say("gated block graph")
+    rng = np.random.default_rng(6)
+    d = device()
+    a, sa, b, sb = operands(rng, (24,), 256, 1024)
+    w = dg.dg_quantize_per_block(torch.randn((1024, 256), device=d) / 16)
+    res = torch.randn((24, 1024), device=d, dtype=BF16)
+    sizes = dg.dg_gemm_fp8_gated_workspace_size(24, 256, 1024), dg.dg_gemm_workspace_size(24, 1024, 256)
+    assert sizes[0] > 0
+
+    def step(ws):
+        q, s = dg.dg_gemm_fp8_gated_nt(a, sa, b, sb, out="fp8", workspace=ws[0])
+        y = dg.dg_gemm_fp8_nt(q, s, *w, workspace=ws[1])
+        total, q2, s2 = dg.dg_residual_norm_fp8(y, res, post_norm=True)
+        return [q, y, total, q2, s2[:, :24]]
+
+    def spaces():
+        return [torch.zeros(max(n, 16), dtype=torch.uint8, device=d) for n in sizes]
+
+    step(spaces())
+    graphs = []
+    for _ in range(2):
+        ws, g = spaces(), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = step(ws)
+        graphs.append((g, out, ws))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for n in range(3):
+        res.copy_(torch.randn((24, 1024), device=d))
+        torch.cuda.synchronize()
+        for (g, _, _), st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+        want = step(spaces())
+        torch.cuda.synchronize()
+        for _, out, _ in graphs:
+            for x, y in zip(out, want):
+                same_bits(x, y, f"replay {n}")
