@@ -16,7 +16,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdg.so")
-SOURCES = ["api.cpp", "quant.hip", "gemm.hip", "moe.hip", "quant_int8.hip", "gemm_int8.hip", "gated_act.hip",
+SOURCES = ["api.cpp", "quant.hip", "gemm.hip", "gemm_gated_few.hip", "moe.hip", "quant_int8.hip", "gemm_int8.hip", "gated_act.hip",
            "norm.hip"]
 
 ARCH = "gfx950"

@@ -44,14 +44,15 @@
 //    workgroup and one L2 invalidation per wave, which on this 8-XCD part exceed what
 //    a separate quantizer launch costs in a HIP graph; the two-launch path stays the
 //    faster one.
+#include <cmath>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
 #include <type_traits>
 
-#include "gated.hpp"
 #include "gemm_common.hpp"
+#include "gemm_gated.hpp"
 
 namespace dg {
 
@@ -150,15 +151,6 @@ constexpr int stage_bytes() {
   return C::kSbOffset + (LAYOUT == kDenseRowB ? C::BN * 4 : C::kIssuers * C::kSbWaveBytes);
 }
 
-// LDS slot of 16-byte chunk c of tile row r.  f depends on r mod 16 only, so every fragment
-// of a lane shares one pattern and fragment addresses differ by immediates.
-__device__ __forceinline__ int swz_row(int r) { return (r & 7) ^ ((r >> 3) & 1); }
-__device__ __forceinline__ int lds_off(int r, int c) { return r * kGroup + ((c ^ swz_row(r)) << 4); }
-
-__device__ __forceinline__ v8i make_v8i(u32x4 lo, u32x4 hi) {
-  return v8i{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
-}
-
 // s_waitcnt vmcnt(N) (gfx9 encoding; expcnt and lgkmcnt left at their maxima).
 template <int N>
 __device__ __forceinline__ void wait_vmcnt() {
@@ -179,11 +171,6 @@ __device__ __forceinline__ void wait_groups(int younger) {
   }
   wait_vmcnt<0>();
 }
-
-struct TileCoord {
-  int g, mb, nbt, split;
-  int m_lo, m_valid;   // the tile's output rows are those in [m_lo, m_valid)
-};
 
 // ---- activation quantization inside the GEMM launch (dense layout) ---------------------------
 // The 1 x 128 groups of x, numbered in row-major order (r * KB + kb), are cut into chunks of
@@ -295,116 +282,6 @@ __device__ __forceinline__ void fused_act_quant_exit(const GemmParams& p) {
   }
 }
 
-
-// The epilogue of the gated form.  acc holds the wave's 16x16 fragments: gate columns in fragment rows [0, kFragN / 2), the same
-// columns' up projections in the rest, so that h = act(g) u needs values of one lane only.
-//  * Stores go through the wave's padded strip of LDS (16 rows of a fragment column) as in the plain epilogue, so that
-//    they are runs of whole row pieces; widths that are no multiple of 8 are stored element by element.
-//  * FP8: a tile is 128 columns of h, one scale group a row.  A row's maximum is taken over the lane's values, the
-//    4 lanes 16 apart, and the waves along the columns through LDS.
-template <class C, int LAYOUT>
-__device__ __forceinline__ void gated_epilogue(const GemmParams& p, const TileCoord& t, int m0, int n0, int wave_n, int wm0,
-                                               int wave, int lane, v4f (*acc)[C::kFragM], uint8_t* lds) {
-  constexpr int kHF = C::kFragN / 2, kCols = 16 * kHF;   // fragments and columns of h a wave holds
-  constexpr bool kTwoPass = LAYOUT == kContiguous && C::BM > kGroup;
-  const int l16 = lane & 15, g4 = lane >> 4;
-  const int wc0 = n0 + wave_n * kCols;                   // the wave's first column of h
-  const int64_t row_base = LAYOUT == kMasked ? (int64_t)t.g * p.m : 0;
-  auto stored = [&](int mrow) { return (!kTwoPass || mrow >= t.m_lo) && mrow < t.m_valid; };
-  constexpr int kPitch = kCols * 2 + 16;
-  constexpr int kStripBytes = 16 * kPitch;
-  static_assert(C::kWaves * kStripBytes + 4 * C::kWavesN * C::BM <= (C::BN + C::BM) * kGroup,
-                "the strips and the rows' maxima fit in one ring buffer");
-  uint8_t* strip = lds + wave * kStripBytes;
-  // fragments [f0, f0 + kHF) of fragment column j as bf16 to columns wc0 .. of rows `ld` elements long, `off` elements in
-  auto store_bf16 = [&](uint16_t* out, int64_t ld, int off, int f0, int j) {
-    if ((p.n & 7) == 0) {
-#pragma unroll
-      for (int i = 0; i < kHF; ++i) {
-        uint2 v;
-        v.x = pack2_bf16_rne(acc[f0 + i][j][0], acc[f0 + i][j][1]);
-        v.y = pack2_bf16_rne(acc[f0 + i][j][2], acc[f0 + i][j][3]);
-        *reinterpret_cast<uint2*>(strip + l16 * kPitch + (16 * i + 4 * g4) * 2) = v;
-      }
-      constexpr int kChunksRow = kCols / 8, kChunks = 16 * kChunksRow;
-#pragma unroll
-      for (int u = 0; u < (kChunks + 63) / 64; ++u) {
-        const int c = lane + 64 * u;
-        const int row = c / kChunksRow, cc = c % kChunksRow;
-        const int mrow = m0 + wm0 + 16 * j + row, ncol = wc0 + 8 * cc;
-        if (c < kChunks && stored(mrow) && ncol < p.n)
-          *reinterpret_cast<u32x4*>(out + (row_base + mrow) * ld + off + ncol) =
-              *reinterpret_cast<const u32x4*>(strip + row * kPitch + cc * 16);
-      }
-    } else {
-      const int mrow = m0 + wm0 + 16 * j + l16;
-      if (!stored(mrow)) return;
-      uint16_t* drow = out + (row_base + mrow) * ld + off;
-#pragma unroll
-      for (int i = 0; i < kHF; ++i) {
-        const int ncol = wc0 + 16 * i + 4 * g4;
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (ncol + r < p.n) drow[ncol + r] = (uint16_t)pack2_bf16_rne(acc[f0 + i][j][r], 0.0f);
-      }
-    }
-  };
-  __syncthreads();   // every wave is done with the ring (the last K block's operands)
-#pragma unroll
-  for (int j = 0; j < C::kFragM; ++j) {
-    if (p.pre != nullptr) {
-      store_bf16(p.pre, 2 * (int64_t)p.n, 0, 0, j);
-      store_bf16(p.pre, 2 * (int64_t)p.n, p.n, kHF, j);
-    }
-#pragma unroll
-    for (int i = 0; i < kHF; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float g = acc[i][j][r];
-        acc[i][j][r] = (p.act == kSilu ? act_value<kSilu>(g) : act_value<kGelu>(g)) * acc[kHF + i][j][r];
-      }
-    if (p.q == nullptr) store_bf16(p.d, p.n, 0, 0, j);
-  }
-  if (p.q == nullptr) return;
-  static_assert(C::BN == 2 * kGroup, "a tile is one scale group wide");
-  float* s_max = reinterpret_cast<float*>(lds + C::kWaves * kStripBytes);
-  float amax[C::kFragM];
-#pragma unroll
-  for (int j = 0; j < C::kFragM; ++j) {
-    float a = fabsf(acc[0][j][0]);
-#pragma unroll
-    for (int i = 0; i < kHF; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) a = fmaxf(a, fabsf(acc[i][j][r]));
-    a = fmaxf(a, __shfl_xor(a, 16));
-    amax[j] = fmaxf(a, __shfl_xor(a, 32));
-    if (g4 == 0) s_max[wave_n * C::BM + wm0 + 16 * j + l16] = amax[j];
-  }
-  __syncthreads();
-  constexpr int kPitch8 = kCols + 16;
-  const int nb = n0 / kGroup;
-#pragma unroll
-  for (int j = 0; j < C::kFragM; ++j) {
-    float a = amax[j];
-#pragma unroll
-    for (int w = 0; w < C::kWavesN; ++w) a = fmaxf(a, s_max[w * C::BM + wm0 + 16 * j + l16]);
-    const float s = a == 0.0f ? 1.0f : a / kE4M3Max;
-    if (wave_n == 0 && g4 == 0 && stored(m0 + wm0 + 16 * j + l16))
-      p.s[(LAYOUT == kMasked ? (int64_t)t.g * p.s_gstride : 0) + (int64_t)nb * p.ld_s + m0 + wm0 + 16 * j + l16] = s;
-#pragma unroll
-    for (int i = 0; i < kHF; ++i)
-      *reinterpret_cast<uint32_t*>(strip + l16 * kPitch8 + 16 * i + 4 * g4) =
-          pack4_e4m3(clamp448(acc[i][j][0] / s), clamp448(acc[i][j][1] / s), clamp448(acc[i][j][2] / s),
-                     clamp448(acc[i][j][3] / s));
-    constexpr int kChunksRow = kCols / 16, kChunks = 16 * kChunksRow;   // at most one a lane; n % 16 == 0
-    static_assert(kChunks <= 64, "one chunk a lane");
-    const int row = lane / kChunksRow, cc = lane % kChunksRow;
-    const int mrow = m0 + wm0 + 16 * j + row, ncol = wc0 + 16 * cc;
-    if (lane < kChunks && stored(mrow) && ncol < p.n)
-      *reinterpret_cast<u32x4*>(p.q + (row_base + mrow) * p.n + ncol) =
-          *reinterpret_cast<const u32x4*>(strip + row * kPitch8 + cc * 16);
-  }
-}
 
 // GATED: b holds two matrices, gate and up; a tile's B rows are BN / 2 rows of each, and a wave's fragment rows the gate and
 // the up rows of the same columns, each half with its own block scale.
@@ -1002,7 +879,30 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
     }
 
     if constexpr (GATED) {
-      gated_epilogue<C, LAYOUT>(p, t, m0, n0, wave_n, wm0, wave, lane, acc, st0);
+      // a chunk: one fragment column of every wave, 16 rows of each of the wave rows
+      static_assert(C::kWavesM * 16 * kGatedPitch * 4 <= kStage && C::BN == 2 * kGroup, "a chunk fits in one ring buffer");
+      float* chunk = reinterpret_cast<float*>(st0);
+      gated_epilogue<NT, LAYOUT, kTwoPass>(
+          p, t, n0, C::kFragM, C::kWavesM * 16, chunk,
+          [&](int c) {
+            float* dst = chunk + (wave_m * 16 + l16) * kGatedPitch + wave_n * (C::WN / 2) + 4 * g4;
+            // constant indices, in blocks that the compiler cannot merge: the accumulators stay in registers
+            auto put = [&](auto jc) {
+              asm volatile("; fragment column %0" ::"i"(decltype(jc)::value));
+#pragma unroll
+              for (int i = 0; i < C::kFragN; ++i)
+                *reinterpret_cast<v4f*>(dst + (i < C::kFragN / 2 ? 0 : kGroup) + 16 * (i % (C::kFragN / 2))) =
+                    acc[i][decltype(jc)::value];
+              asm volatile("; fragment column %0 end" ::"i"(decltype(jc)::value));
+            };
+            static_assert(C::kFragM == 4, "four fragment columns");
+            if (c == 0) put(IC<0>{});
+            else if (c == 1) put(IC<1>{});
+            else if (c == 2) put(IC<2>{});
+            else put(IC<3>{});
+          },
+          [&](int c, int r) { return m0 + (r >> 4) * C::WM + 16 * c + (r & 15); });
+      __syncthreads();   // the next tile's first DMAs may not meet readers of the chunk
       continue;
     }
     // ---- epilogue: fp32 -> bf16 (RNE), row-major store, edge masking ------------
@@ -1499,79 +1399,122 @@ int launch_gemm(int layout, const uint8_t* a, const float* sa, int64_t ld_sa, co
 }
 
 // ---- gated form: both projections of a feed-forward block, the activation and the product ------
-// The large tiles of the plain forms, with 128 gate and 128 up rows for 256 rows of weights; up to 64 rows a 32- or 64-row
-// tile of the two-stage ring whose weight rows are 256 too, so that a tile holds whole scale groups of h.
-enum GatedCfgId : int { kGatedRows128 = 0, kGatedWide, kGatedSquare, kGatedDec32, kGatedDec64 };
-using CfgGatedDec32 = Cfg<256, 32, 64, 32, 2>;
-using CfgGatedDec64 = Cfg<256, 64, 64, 32, 2>;
+// The large tiles of the plain forms, with 128 gate and 128 up rows for 256 rows of weights; for few rows the kernel that
+// streams the weights (csrc/gemm_gated_few.hip), with tiles of 16 or 64 rows.
+const void* gated_few_kernel(int layout, int bm);
+int gated_few_lds(int bm);
+int launch_gated_join(int layout, GemmParams p, int bm, hipStream_t stream);
+
+enum GatedCfgId : int { kGatedRows128 = 0, kGatedSquare, kGatedFew16, kGatedFew64 };
+constexpr int kMaxStreamSplits = 32;
 
 template <int LAYOUT>
 static LaunchInfo gated_info(int cfg) {
-  switch (cfg) {
-    case kGatedWide:
-      if constexpr (LAYOUT != kContiguous) return info<CfgWide, LAYOUT, false, true>();
-      else return info<CfgRows128, LAYOUT, false, true>();
-    case kGatedSquare: return info<CfgSquare, LAYOUT, false, true>();
-    case kGatedDec32:
-      if constexpr (LAYOUT != kContiguous) return info<CfgGatedDec32, LAYOUT, false, true>();
-      else return info<CfgRows128, LAYOUT, false, true>();
-    case kGatedDec64:
-      if constexpr (LAYOUT != kContiguous) return info<CfgGatedDec64, LAYOUT, false, true>();
-      else return info<CfgRows128, LAYOUT, false, true>();
-    default: return info<CfgRows128, LAYOUT, false, true>();
+  if (cfg >= kGatedFew16 && LAYOUT != kContiguous) {
+    const int bm = cfg == kGatedFew16 ? 16 : 64;
+    return LaunchInfo{256, bm, 512, 2, gated_few_kernel(LAYOUT, bm), gated_few_lds(bm)};
   }
+  return cfg == kGatedSquare ? info<CfgSquare, LAYOUT, false, true>() : info<CfgRows128, LAYOUT, false, true>();
 }
 
-static int gated_cfg_of(int cfg) { return cfg == kCfgSquare ? kGatedSquare : cfg == kCfgWide ? kGatedWide : kGatedRows128; }
+// Estimated time (us) of a dense gated product by tile and K split, from timings of every choice on MI355X over 15
+// shapes of 1 to 1024 rows, n 256 to 8192, k 1024 to 7168 (cold weights): a start, the K blocks of a workgroup one after
+// the other, in rounds of the CUs, and the weights' bytes at 5 TB/s; and for splits the partials: out and back at 4
+// TB/s with a launch for the streaming kernel, the last workgroup's reading of them for the large tiles and few rows.
+static double gated_estimate(int cfg, int64_t m, int64_t strips, int64_t k, int num_cus, int splits, int kbps, bool in_kernel) {
+  const double bm = cfg == kGatedFew16 ? 16 : cfg == kGatedFew64 ? 64 : cfg == kGatedRows128 ? 128 : 256;
+  const double start = cfg == kGatedFew16 ? 6.0 : cfg == kGatedFew64 ? 5.0 : cfg == kGatedRows128 ? 8.6 : 13.5;
+  const double block = cfg == kGatedFew16 ? 1.07 : cfg == kGatedFew64 ? 1.0 : cfg == kGatedRows128 ? 1.15 : 1.95;
+  const int64_t tiles = (int64_t)((m + bm - 1) / bm) * strips;
+  const int blocks = cfg == kGatedFew16 ? (kbps + 3) / 4 * 4 : kbps;   // (its loop takes four at a time)
+  const double chain = (double)((tiles * splits + num_cus - 1) / num_cus) * blocks * block;
+  const double memory = (double)strips * 2 * kGroup * (double)k / 5.0e6;
+  double t = start + std::sqrt(chain * chain + memory * memory);   // (both near the larger one slow each other)
+  if (splits > 1) {
+    if (cfg >= kGatedFew16 && !in_kernel) t += 4.0 + (double)strips * (double)m * splits * 2048.0 / 4.0e6;
+    else if (cfg >= kGatedFew16) t += 2.5 + (double)splits * (double)m * 1024.0 / 3.0e4;
+    else t += 2.0 + 1.8 * splits * bm / 128;
+  }
+  return t;
+}
+
+// Whether the streaming kernel's split tiles are ended by their last workgroup: 16 rows of at most 16 KB of partials each
+// (1 x 2048 x 7168, 14 splits: 12.8 us, with a second launch 15.5).
+static bool gated_join_in_kernel(int cfg, int64_t m, int splits) { return cfg == kGatedFew16 && m * splits <= 64; }
 
 // n: the width of h.
 static Plan make_gated_plan(int layout, int64_t m, int64_t n, int64_t k, int64_t call_groups, int num_cus, bool allow_split) {
   const int64_t groups = layout == kMasked ? call_groups : 1;
-  const int64_t weight_rows = (n + kGroup - 1) / kGroup * (2 * kGroup);   // rows of b in whole tiles
+  const int64_t strips = (n + kGroup - 1) / kGroup;
+  const int64_t weight_rows = strips * (2 * kGroup);   // rows of b in whole tiles
   const int kb_total = (int)((k + kGroup - 1) / kGroup);
   Plan pl{};
   pl.splits = 1;
-  pl.kb_per_split = kb_total;
-  int max_split = 1;
-  if (layout == kContiguous) {
-    pl.cfg = gated_cfg_of(choose_contiguous(m, weight_rows, call_groups, num_cus));
-  } else if (m <= 64) {
-    pl.cfg = m <= 32 ? kGatedDec32 : kGatedDec64;
-    max_split = kb_total / 2;
-  } else {
-    pl.cfg = gated_cfg_of(choose_large(m, weight_rows, groups, num_cus, kb_total, false));
-    max_split = kb_total / 4;
-  }
-  const LaunchInfo li = gated_info<kDense>(pl.cfg);
-  // few tiles: split K so that every CU gets work
-  const int64_t tiles = ((m + li.bm - 1) / li.bm) * (weight_rows / li.bn) * groups;
-  if (allow_split && layout != kContiguous && 2 * tiles <= num_cus) {
-    int64_t want = num_cus / tiles;
-    if (want > max_split) want = max_split;
-    if (want > kMaxSplits) want = kMaxSplits;
-    if (want > 1) pl.splits = (int)want;
-  }
-  // DG_PLAN, as for the plain forms
+  // DG_PLAN, as for the plain forms; "stream=16" or 64 takes the streaming kernel's tiles
+  int want = 0, forced = -1;
   if (const char* e = std::getenv("DG_PLAN"); e != nullptr && e[0] != '\0') {
-    int bn = 0, bm = 0, want = 0;
+    int bn = 0, bm = 0, stream = 0;
     for (const char* q = e; *q;) {
-      if (std::sscanf(q, "tile=%dx%d", &bn, &bm) == 2 || std::sscanf(q, "splits=%d", &want) == 1) {}
+      if (std::sscanf(q, "tile=%dx%d", &bn, &bm) == 2 || std::sscanf(q, "stream=%d", &stream) == 1 ||
+          std::sscanf(q, "splits=%d", &want) == 1) {}
       const char* c = std::strchr(q, ',');
       if (c == nullptr) break;
       q = c + 1;
     }
-    static const int kAll[] = {kGatedRows128, kGatedWide, kGatedSquare, kGatedDec32, kGatedDec64};
-    for (const int cfg : kAll) {
-      const LaunchInfo l = gated_info<kDense>(cfg);
-      if (layout == kContiguous && cfg != kGatedRows128 && cfg != kGatedSquare) continue;
-      if (l.bn == bn && l.bm == bm) pl.cfg = cfg;
-    }
-    if (want > 0 && allow_split && layout != kContiguous) pl.splits = want < kMaxSplits ? want : kMaxSplits;
+    if (bn == 256 && bm == 128) forced = kGatedRows128;
+    if (bn == 256 && bm == 256) forced = kGatedSquare;
+    if (layout != kContiguous && stream == 16) forced = kGatedFew16;
+    if (layout != kContiguous && stream == 64) forced = kGatedFew64;
   }
+  const auto most = [&](int cfg) { return cfg >= kGatedFew16 ? kMaxStreamSplits : kMaxSplits; };
+  if (layout == kContiguous) {
+    pl.cfg = forced >= 0 ? forced
+             : choose_contiguous(m, weight_rows, call_groups, num_cus) == kCfgSquare ? kGatedSquare : kGatedRows128;
+  } else if (layout == kMasked) {
+    // rows in use are not known here; beyond 64 the 128-row tile, which a group's last rows fill worse than the streaming
+    // kernel's but the weights pass less often (32 x 256 x 2048 x 7168, half in use: 275 us, 256-row tiles 300, 64-row strips 380)
+    pl.cfg = forced >= 0 ? forced : m <= 16 ? kGatedFew16 : m <= 64 ? kGatedFew64 : kGatedRows128;
+    const int64_t bm = gated_info<kDense>(pl.cfg).bm;
+    const int64_t tiles = ((m + bm - 1) / bm) * strips * groups;
+    if (allow_split && 2 * tiles <= num_cus) {   // few tiles: split K so that every CU gets work
+      int64_t s = num_cus / tiles;
+      if (s > kb_total / 4) s = kb_total / 4;
+      pl.splits = (int)(s < 1 ? 1 : s > most(pl.cfg) ? most(pl.cfg) : s);
+    }
+  } else {
+    double best = 1e30;
+    for (const int cfg : {kGatedSquare, kGatedRows128, kGatedFew64, kGatedFew16}) {
+      if (forced >= 0 ? cfg != forced : cfg == kGatedFew16 && m > 64) continue;
+      for (int s = 1; s <= (allow_split ? most(cfg) : 1); ++s) {
+        const int kbps = (kb_total + s - 1) / s;
+        if ((kb_total + kbps - 1) / kbps != s || (s > 1 && kbps < (cfg >= kGatedFew16 ? 2 : 4))) continue;
+        const double t = gated_estimate(cfg, m, strips, k, num_cus, s, kbps, gated_join_in_kernel(cfg, m, s));
+        if (t < best) {
+          best = t;
+          pl.cfg = cfg;
+          pl.splits = s;
+        }
+      }
+    }
+  }
+  if (want > 0 && allow_split && layout != kContiguous) pl.splits = want < most(pl.cfg) ? want : most(pl.cfg);
   pl.kb_per_split = (kb_total + pl.splits - 1) / pl.splits;
   pl.splits = (kb_total + pl.kb_per_split - 1) / pl.kb_per_split;   // no empty split
   finish_plan(pl, gated_info<kDense>(pl.cfg), m, weight_rows, k, groups);
   return pl;
+}
+
+static void gated_plan_name(const Plan& pl, char* buf, size_t len) {
+  snprintf(buf, len, "%s%dx%d/8waves/split%d", pl.cfg >= kGatedFew16 ? "stream" : "", pl.bn, pl.bm, pl.splits);
+}
+
+template <int LAYOUT>
+static int launch_gated(GemmParams p, const Plan& pl, hipStream_t stream, int num_cus) {
+  if (pl.cfg < kGatedFew16 || pl.splits == 1 || gated_join_in_kernel(pl.cfg, p.m, pl.splits))
+    return launch_info<LAYOUT>(gated_info<LAYOUT>(pl.cfg), p, pl, stream, num_cus);
+  p.counters = nullptr;   // the second launch ends the tiles
+  const int r = launch_info<LAYOUT>(gated_info<LAYOUT>(pl.cfg), p, pl, stream, num_cus);
+  return r == kOk ? launch_gated_join(LAYOUT, p, pl.bm, stream) : r;
 }
 
 size_t gemm_gated_workspace_size(int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus) {
@@ -1581,7 +1524,7 @@ size_t gemm_gated_workspace_size(int64_t m, int64_t n, int64_t k, int64_t groups
 void gemm_gated_config_name(int layout, int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus, char* buf,
                             size_t len) {
   const Plan pl = make_gated_plan(layout, m, n, k, layout == kDense ? 1 : groups, num_cus, layout != kContiguous);
-  snprintf(buf, len, "%dx%d/%dwaves/split%d", pl.bn, pl.bm, gated_info<kDense>(pl.cfg).threads / 64, pl.splits);
+  gated_plan_name(pl, buf, len);
 }
 
 int launch_gemm_gated(int layout, const uint8_t* a, const float* sa, int64_t ld_sa, const uint8_t* b, const float* sb,
@@ -1607,14 +1550,17 @@ int launch_gemm_gated(int layout, const uint8_t* a, const float* sa, int64_t ld_
     p.counters = static_cast<unsigned*>(ws);
     p.ws = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kCounterBytes);
   }
-  if (p.debug)
-    std::fprintf(stderr, "[dg] gated gemm %s m=%lld n=%lld k=%lld groups=%lld: %dx%d splits=%d workspace=%zu/%zu bytes\n",
+  if (p.debug) {
+    char name[96];
+    gated_plan_name(pl, name, sizeof(name));
+    std::fprintf(stderr, "[dg] gated gemm %s m=%lld n=%lld k=%lld groups=%lld: %s workspace=%zu/%zu bytes\n",
                  layout == kContiguous ? "contiguous" : layout == kMasked ? "masked" : "normal", (long long)m, (long long)n,
-                 (long long)k, (long long)groups, pl.bn, pl.bm, pl.splits, pl.ws_bytes, ws_bytes);
+                 (long long)k, (long long)groups, name, pl.ws_bytes, ws_bytes);
+  }
   switch (layout) {
-    case kContiguous: return launch_info<kContiguous>(gated_info<kContiguous>(pl.cfg), p, pl, stream, num_cus);
-    case kMasked: return launch_info<kMasked>(gated_info<kMasked>(pl.cfg), p, pl, stream, num_cus);
-    default: return launch_info<kDense>(gated_info<kDense>(pl.cfg), p, pl, stream, num_cus);
+    case kContiguous: return launch_gated<kContiguous>(p, pl, stream, num_cus);
+    case kMasked: return launch_gated<kMasked>(p, pl, stream, num_cus);
+    default: return launch_gated<kDense>(p, pl, stream, num_cus);
   }
 }
 

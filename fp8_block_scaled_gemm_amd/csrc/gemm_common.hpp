@@ -77,6 +77,20 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, in
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, n, kBufferWord3);
 }
 
+struct TileCoord {
+  int g, mb, nbt, split;
+  int m_lo, m_valid;   // the tile's output rows are those in [m_lo, m_valid)
+};
+
+// LDS slot of 16-byte chunk c of tile row r.  f depends on r mod 16 only, so every fragment
+// of a lane shares one pattern and fragment addresses differ by immediates.
+__device__ __forceinline__ int swz_row(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+__device__ __forceinline__ int lds_off(int r, int c) { return r * kGroup + ((c ^ swz_row(r)) << 4); }
+
+__device__ __forceinline__ v8i make_v8i(u32x4 lo, u32x4 hi) {
+  return v8i{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+}
+
 // Masked layout: per-group work-item prefix s_prefix[0..groups] (s_prefix[g] = items before group
 // g), where group g has ceil(clamp(masked_m[g], 0, m) / bm) * per_mblock items.  Threads 0..255 of
 // the workgroup (at least 256 threads) count 4 groups each and scan in LDS; ends with a barrier.

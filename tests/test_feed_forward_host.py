@@ -60,15 +60,18 @@ def test_gated_plans(lib, monkeypatch):
     assert lib.dg_set_num_cus(256) == OK
     for m, n, k, groups in ((1, 2048, 7168, 1), (64, 128, 4096, 1), (100, 256, 2048, 1), (8192, 8192, 7168, 1), (5, 300, 640, 8)):
         name = dg.dg_gemm_fp8_gated_config_name(2 if groups > 1 else 0, m, n, k, groups)
-        tile, splits = name.split("/")[0], int(name.rsplit("split", 1)[1])
+        tile, splits = name.split("/")[0].removeprefix("stream"), int(name.rsplit("split", 1)[1])
         bn, bm = (int(v) for v in tile.split("x"))
-        assert bn == 256 and bm in (32, 64, 128, 192, 256)
+        assert bn == 256 and bm in (16, 64, 128, 256)
         tiles = -(-n // 128) * -(-m // bm) * groups
         need = dg.dg_gemm_fp8_gated_workspace_size(m, n, k, groups)
         assert need == (65536 + tiles * splits * bn * bm * 4 if splits > 1 else 0)
-    monkeypatch.setenv("DG_PLAN", "tile=256x192,splits=5")
-    assert dg.dg_gemm_fp8_gated_config_name(0, 8, 128, 1280) == "256x192/8waves/split5"
-    assert not dg.dg_gemm_fp8_gated_config_name(1, 128, 128, 1280, 2).startswith("256x192")
+    monkeypatch.setenv("DG_PLAN", "tile=256x128,splits=5")
+    assert dg.dg_gemm_fp8_gated_config_name(0, 8, 128, 1280) == "256x128/8waves/split5"
+    assert dg.dg_gemm_fp8_gated_config_name(1, 128, 128, 1280, 2) == "256x128/8waves/split1"
+    monkeypatch.setenv("DG_PLAN", "stream=64")
+    assert dg.dg_gemm_fp8_gated_config_name(0, 1000, 1280, 1280).startswith("stream256x64/8waves/")
+    assert not dg.dg_gemm_fp8_gated_config_name(1, 128, 128, 1280, 2).startswith("stream")
     monkeypatch.delenv("DG_PLAN")
     for bad in ((3, 8, 128, 128, 1), (0, 0, 128, 128, 1), (0, 8, 0, 128, 1), (0, 8, 128, 100, 1), (2, 8, 128, 128, 0), (2, 8, 128, 128, 1025)):
         assert dg.dg_gemm_fp8_gated_config_name(*bad) == ""

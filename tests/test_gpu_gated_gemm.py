@@ -7,7 +7,8 @@ error of 16x16x128 products of random codes is 1.7e-5 of them), the promotion ad
 (10 + 6 |z|) 2^-24 (see the activation's own tests).  bf16 outputs are rounded once (2^-8); E4M3 codes are within half a step
 of h / s: 2^-4 of it, or 2^-10 below the normal codes.
 
-Without a K split the projections are, K block by K block, the operations of the plain forms: the same bits.
+On the large tiles without a K split the projections are, K block by K block, the operations of the plain forms: the same
+bits.  (The kernel for few rows hands the matrix instruction a K block's elements in another order.)
 """
 
 import numpy as np
@@ -109,7 +110,7 @@ def test_normal(m, n, k, act):
         check_bf16(pre[:, :n], g, eg, "gate")
         check_bf16(pre[:, n:], u, eu, "up")
         same_bits(d, dg.dg_gemm_fp8_gated_nt(a, sa, b, sb, act=act, use_workspace=use), "without pre")
-        if not use:
+        if not use and m > 256:
             for i in (0, 1):
                 plain = dg.dg_gemm_fp8_nt(a, sa, alone(b[i]), alone(sb[i]), use_workspace=False)
                 same_bits(pre[:, i * n:(i + 1) * n], plain, f"projection {i} as the plain GEMM")
@@ -123,18 +124,19 @@ def test_normal(m, n, k, act):
             same_bits(s2[:, :m], s[:, :m], "again")
 
 
-@pytest.mark.parametrize("tile", ["256x32", "256x64", "256x128", "256x192", "256x256"])
+@pytest.mark.parametrize("tile", ["stream=16", "stream=64", "tile=256x128", "tile=256x256"])
 @pytest.mark.parametrize("splits", [1, 3, 16])
 def test_every_tile_and_split(tile, splits, monkeypatch):
     """Every tile at sizes on both sides of its edges, each split: values, and a workspace left as it was found."""
     rng = np.random.default_rng(splits)
-    monkeypatch.setenv("DG_PLAN", f"tile={tile},splits={splits}")
+    monkeypatch.setenv("DG_PLAN", f"{tile},splits={splits}")
     for m, n, k in ((1, 144, 2048), (200, 272, 400), (270, 128, 2064)):
         say("gated tile", tile, splits, m, n, k)
         name = dg.dg_gemm_fp8_gated_config_name(0, m, n, k)
         kb = -(-k // 128)
         per = -(-kb // splits)
-        assert name.startswith(tile + "/") and name.endswith(f"split{-(-kb // per)}"), name
+        kind, size = tile.split("=")
+        assert name.startswith((size if kind == "tile" else f"stream256x{size}") + "/") and name.endswith(f"split{-(-kb // per)}"), name
         a, sa, b, sb = operands(rng, (m,), n, k)
         h, eh = reference(a, sa, m, b, sb, "silu")[2::3]
         need = dg.dg_gemm_fp8_gated_workspace_size(m, n, k)
@@ -148,7 +150,7 @@ def test_every_tile_and_split(tile, splits, monkeypatch):
 
 
 @pytest.mark.parametrize("m,n,k,groups", [(1, 128, 256, 3), (20, 144, 400, 5), (64, 256, 1024, 2), (70, 272, 528, 4), (256, 384, 768, 6),
-                                          (33, 37, 256, 3), (130, 131, 144, 2)])
+                                          (33, 37, 256, 3), (130, 131, 144, 2), (300, 400, 384, 3), (270, 67, 256, 2)])
 def test_masked(m, n, k, groups):
     rng = np.random.default_rng(m + n)
     counts = [0, m, min(m, 3), -2, m + 9, max(m // 2, 1)][:groups]
@@ -177,7 +179,7 @@ def test_masked(m, n, k, groups):
             check_bf16(pre[j, :c, n:], u, eu, "up")
             if fp8:
                 check_fp8(q[j, :c], s[j, :, :c].t(), h, eh, "fp8")
-        if not use:
+        if not use and m > 256:
             for i in (0, 1):
                 plain = torch.full((groups, m, n), 9.0, dtype=BF16, device=device())
                 dg.dg_gemm_fp8_grouped_masked(a, sa, alone(b[:, i]), alone(sb[:, i]), masked, d=plain, use_workspace=False)
