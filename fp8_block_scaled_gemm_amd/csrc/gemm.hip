@@ -1423,7 +1423,7 @@ static LaunchInfo gated_info(int cfg) {
 // TB/s with a launch for the streaming kernel, the last workgroup's reading of them for the large tiles and few rows.
 static double gated_estimate(int cfg, int64_t m, int64_t strips, int64_t k, int num_cus, int splits, int kbps, bool in_kernel) {
   const double bm = cfg == kGatedFew16 ? 16 : cfg == kGatedFew64 ? 64 : cfg == kGatedRows128 ? 128 : 256;
-  const double start = cfg == kGatedFew16 ? 6.0 : cfg == kGatedFew64 ? 5.0 : cfg == kGatedRows128 ? 8.6 : 13.5;
+  const double start = cfg == kGatedFew16 ? 4.5 : cfg == kGatedFew64 ? 6.0 : cfg == kGatedRows128 ? 8.6 : 13.5;
   const double block = cfg == kGatedFew16 ? 1.07 : cfg == kGatedFew64 ? 1.0 : cfg == kGatedRows128 ? 1.15 : 1.95;
   const int64_t tiles = (int64_t)((m + bm - 1) / bm) * strips;
   const int blocks = cfg == kGatedFew16 ? (kbps + 3) / 4 * 4 : kbps;   // (its loop takes four at a time)
@@ -1432,7 +1432,7 @@ static double gated_estimate(int cfg, int64_t m, int64_t strips, int64_t k, int 
   double t = start + std::sqrt(chain * chain + memory * memory);   // (both near the larger one slow each other)
   if (splits > 1) {
     if (cfg >= kGatedFew16 && !in_kernel) t += 4.0 + (double)strips * (double)m * splits * 2048.0 / 4.0e6;
-    else if (cfg >= kGatedFew16) t += 2.5 + (double)splits * (double)m * 1024.0 / 3.0e4;
+    else if (cfg >= kGatedFew16) t += 1.5 + (double)splits * (double)m * 1024.0 / 3.0e4;
     else t += 2.0 + 1.8 * splits * bm / 128;
   }
   return t;
