@@ -10,22 +10,21 @@ namespace dg {
 enum Act : int { kSilu = 0, kGelu = 1 };
 
 // exp(-a) for a >= 0: 2^-(hi + lo), hi + lo = a log2(e) to twice fp32's bits (rounding a log2(e) alone would cost
-// 2^-18 of the result at a = 88); within 3 * 2^-24 of its value, 0 below 2^-126.
+// 2^-18 of the result at a = 88); within 3 * 2^-24 of its value, 0 below 2^-126; a NaN stays one.
 __device__ __forceinline__ float exp_neg(float a) {
   constexpr float kLog2e = 1.44269502f, kLog2eLo = 1.92596299e-8f, kLn2 = 0.693147181f;
   const float hi = a * kLog2e;
-  const float lo = __builtin_fmaf(a, kLog2e, -hi) + a * kLog2eLo;
+  const float lo = __builtin_fmaf(a, kLog2eLo, __builtin_fmaf(a, kLog2e, -hi));
   const float e = __builtin_amdgcn_exp2f(-hi);
   return hi > 126.0f ? 0.0f : __builtin_fmaf(-lo * kLn2, e, e);
 }
 
-// sigmoid(z) and 1 - sigmoid(z), both to full relative precision.
+// sigmoid(z) and 1 - sigmoid(z), both to full relative precision (the hardware's reciprocal: within 2 * 2^-24).
 __device__ __forceinline__ void sigmoid2(float z, float& p, float& rest) {
   const float e = exp_neg(fabsf(z));
-  const float r = 1.0f / (1.0f + e);
-  p = z >= 0.0f ? r : e * r;
-  rest = z >= 0.0f ? e * r : r;
-  if (z != z) p = rest = z;
+  const float r = __builtin_amdgcn_rcpf(1.0f + e), er = e * r;
+  p = z >= 0.0f ? r : er;
+  rest = z >= 0.0f ? er : r;
 }
 
 constexpr float kGeluRoot = 1.59576912f;   // 2 sqrt(2 / pi): 0.5 (1 + tanh(y)) = sigmoid(2 y)

@@ -11,8 +11,13 @@ struct RowMask {
   const int32_t* m_indices;
   const int32_t* masked_m;
   int64_t rows_per_group;
-  __device__ __forceinline__ bool skips(int64_t row) const {
-    if (masked_m != nullptr) return row % rows_per_group >= masked_m[row / rows_per_group];
+  // (group, row in it) of a row: of the masked layout, or all one group.  Rows are below 2^31.
+  __device__ __forceinline__ void split(int64_t row, int& group, int& in_group) const {
+    group = masked_m != nullptr ? (int)((uint32_t)row / (uint32_t)rows_per_group) : 0;
+    in_group = (int)row - group * (int)rows_per_group;
+  }
+  __device__ __forceinline__ bool skips(int64_t row, int group, int in_group) const {
+    if (masked_m != nullptr) return in_group >= masked_m[group];
     return m_indices != nullptr && m_indices[row] < 0;
   }
 };
@@ -41,7 +46,9 @@ template <class T, int ACT, bool FP8, int G>
 __global__ __launch_bounds__(kActThreads) void gated_act_kernel(GatedActParams p) {
   const int lane = threadIdx.x & 15;
   const int64_t row = ((int64_t)blockIdx.y + (int64_t)gridDim.y * blockIdx.z) * (kActThreads / 16) + (threadIdx.x >> 4);
-  if (row >= p.rows || p.mask.skips(row)) return;   // uniform over the 16 lanes
+  int group, in_group;
+  p.mask.split(row, group, in_group);
+  if (row >= p.rows || p.mask.skips(row, group, in_group)) return;   // uniform over the 16 lanes
   const int col0 = blockIdx.x * (G * kGroup) + 8 * lane;
   const T* src = static_cast<const T*>(p.pre) + row * 2 * p.n;
   Raw8<T> g[G], u[G];
@@ -65,11 +72,7 @@ __global__ __launch_bounds__(kActThreads) void gated_act_kernel(GatedActParams p
       const float s = group16_scale(h);
       if (col < p.n) {
         *reinterpret_cast<u32x2_t*>(static_cast<uint8_t*>(p.h) + row * p.n + col) = pack8_e4m3(h, s);
-        if (lane == 0) {
-          const int64_t group = p.mask.masked_m != nullptr ? row / p.mask.rows_per_group : 0;
-          const int64_t in_group = p.mask.masked_m != nullptr ? row % p.mask.rows_per_group : row;
-          p.scales[(group * ((p.n + kGroup - 1) / kGroup) + col / kGroup) * p.ld_s + in_group] = s;
-        }
+        if (lane == 0) p.scales[((int64_t)group * ((p.n + kGroup - 1) / kGroup) + col / kGroup) * p.ld_s + in_group] = s;
       }
     } else if (col < p.n) {
       store8(static_cast<T*>(p.h) + row * p.n + col, narrow8<T>(h));
@@ -84,7 +87,9 @@ __global__ __launch_bounds__(kActThreads) void gated_act_int8_kernel(GatedActPar
   __shared__ uint32_t s_max[kActThreads / 64];
   const int tid = threadIdx.x;
   const int64_t row = blockIdx.x;
-  if (p.mask.skips(row)) return;
+  int group, in_group;
+  p.mask.split(row, group, in_group);
+  if (p.mask.skips(row, group, in_group)) return;
   const T* src = static_cast<const T*>(p.pre) + row * 2 * p.n;
   uint8_t* dst = static_cast<uint8_t*>(p.h) + row * p.n;
   float h[HOLD][8];
@@ -192,7 +197,8 @@ constexpr int kTurnPitch = 33;   // dwords of one turned column (128 bytes and o
 template <class T, int ACT>
 __global__ __launch_bounds__(kGradThreads) void gated_act_grad_fp8_kernel(ActGradFp8Params p) {
   __shared__ float s_max[kGradThreads / 64][kGroup];
-  __shared__ float s_scale[kGroup];
+  __shared__ Divisor s_scale[kGroup];
+  __shared__ int s_plain[2];
   __shared__ uint32_t s_turn[kGroup * kTurnPitch];
   const int tid = threadIdx.x, lane = tid & 15, quad = tid >> 4;   // rows 4 quad .. 4 quad + 3 of the tile
   const int col = blockIdx.x * kGroup + 8 * lane;
@@ -264,16 +270,23 @@ __global__ __launch_bounds__(kGradThreads) void gated_act_grad_fp8_kernel(ActGra
 #pragma unroll
       for (int w = 1; w < kGradThreads / 64; ++w) a = fmaxf(a, s_max[w][tid]);
       const float s = a == 0.0f ? 1.0f : a / kE4M3Max;
-      s_scale[tid] = s;
+      s_scale[tid] = divisor(s);
+      const bool plain = __all(scale_in_range(s));
+      if ((tid & 63) == 0) s_plain[tid >> 6] = plain;
       sc[(int64_t)blockIdx.y * ld + col0 + tid] = s;
     }
     __syncthreads();
+    auto turn = [&](auto plain) {
+      constexpr bool P = decltype(plain)::value;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const float s = s_scale[8 * lane + c];
-      s_turn[(8 * lane + c) * kTurnPitch + quad] = pack4_e4m3(clamp448(v[0][c] / s), clamp448(v[1][c] / s),
-                                                              clamp448(v[2][c] / s), clamp448(v[3][c] / s));
-    }
+      for (int c = 0; c < 8; ++c) {
+        const Divisor d = s_scale[8 * lane + c];
+        s_turn[(8 * lane + c) * kTurnPitch + quad] = codes4_e4m3(quotient<P>(v[0][c], d), quotient<P>(v[1][c], d),
+                                                                 quotient<P>(v[2][c], d), quotient<P>(v[3][c], d));
+      }
+    };
+    if (s_plain[0] && s_plain[1]) turn(std::true_type{});
+    else turn(std::false_type{});
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {

@@ -1484,7 +1484,7 @@ static Plan make_gated_plan(int layout, int64_t m, int64_t n, int64_t k, int64_t
   } else {
     double best = 1e30;
     for (const int cfg : {kGatedSquare, kGatedRows128, kGatedFew64, kGatedFew16}) {
-      if (forced >= 0 ? cfg != forced : cfg == kGatedFew16 && m > 64) continue;
+      if (forced >= 0 ? cfg != forced : cfg == kGatedFew16 && m > 16) continue;
       for (int s = 1; s <= (allow_split ? most(cfg) : 1); ++s) {
         const int kbps = (kb_total + s - 1) / s;
         if ((kb_total + kbps - 1) / kbps != s || (s > 1 && kbps < (cfg >= kGatedFew16 ? 2 : 4))) continue;
