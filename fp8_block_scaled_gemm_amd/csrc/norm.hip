@@ -216,7 +216,8 @@ struct NormGradParams {
 // of the workgroups: no atomics, the same bits from run to run.  A gate's rows ("segment") may end inside the
 // workgroup's range: a segment that lies in it whole is written at once; a piece of one that does not goes to
 // slot 0 where the range begins inside the segment, or with it, and to slot 1 where the segment begins later.
-template <class T, class TR, int LT, int V>
+// Absent weights, gates and norms are ones and scales of 1 rather than branches (those took 190 registers where 110 do).
+template <class T, class TR, bool HASX, int LT, int V>
 __global__ __launch_bounds__(norm_threads<LT>()) void residual_norm_grad_kernel(NormGradParams p) {
   constexpr int kWaves = LT / 64, kRows = norm_rows<LT>();
   __shared__ float red_a[kWaves][3], red_b[kWaves][1];
@@ -224,10 +225,10 @@ __global__ __launch_bounds__(norm_threads<LT>()) void residual_norm_grad_kernel(
   const int tid = threadIdx.x % LT, group = threadIdx.x / LT;
   const int64_t first = (int64_t)blockIdx.x * p.rows_per_part;
   const int64_t end = first + p.rows_per_part < p.rows ? first + p.rows_per_part : p.rows;
-  const bool has_x = p.x != nullptr;
   const bool each_row = p.rows_per_gate == 1;   // a gate for every row: its gradient is no sum
   const bool gate_sums = p.dgate != nullptr && !each_row;
-  float dw[V][8], dv[V][8], dgs[V][8];
+  constexpr int VX = HASX ? V : 1;
+  float dw[V][8], dv[VX][8], dgs[VX][8];
   int at[V];
   bool ok[V];
 #pragma unroll
@@ -235,8 +236,57 @@ __global__ __launch_bounds__(norm_threads<LT>()) void residual_norm_grad_kernel(
     at[i] = 8 * (tid + LT * i);
     ok[i] = at[i] < p.hidden;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) dw[i][c] = dv[i][c] = dgs[i][c] = 0.0f;
+    for (int c = 0; c < 8; ++c) {
+      dw[i][c] = 0.0f;
+      if constexpr (HASX) dv[i][c] = dgs[i][c] = 0.0f;
+    }
   }
+  struct Row {
+    Raw8<TR> u[V], ds[V];
+    Raw8<T> dy[V], x[VX];
+  };
+  auto load_row = [&](int64_t row, Row& r) {
+    const int64_t base = row * p.hidden;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (ok[i]) {
+        r.u[i] = load8(static_cast<const TR*>(p.sum) + base + at[i]);
+        r.dy[i] = load8(static_cast<const T*>(p.dy) + base + at[i]);
+        if (p.dsum != nullptr) r.ds[i] = load8(static_cast<const TR*>(p.dsum) + base + at[i]);
+        if constexpr (HASX) r.x[i] = load8(static_cast<const T*>(p.x) + base + at[i]);
+      }
+  };
+  // weights and a piece's gate stay in registers where these suffice (4096 x 7168: 126 us, 133 with loads for every row), and are
+  // loaded piece by piece for rows of more than 8192
+  constexpr bool kHold = V <= 2;
+  constexpr int H = kHold ? V : 1;
+  const bool normed = p.post_norm, weighted = p.post_weight != nullptr;
+  float held_w[H][8], held_v[H][8], held_g[H][8];
+  auto hold = [&](const auto* src, bool there, float (*to)[8]) {
+    if constexpr (kHold) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (there && ok[i]) {
+          widen8(load8(src + at[i]), to[i]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) to[i][c] = 1.0f;
+        }
+    }
+  };
+  auto columns = [&](const auto* src, bool there, const float (*held)[8], int i, float* to) {
+    if constexpr (kHold) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) to[c] = held[i][c];
+    } else if (there) {
+      widen8(load8(src + at[i]), to);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) to[c] = 1.0f;
+    }
+  };
+  hold(p.weight, p.weight != nullptr, held_w);
+  if constexpr (HASX) hold(p.post_weight, weighted, held_v);
   // a column sum of the whole workgroup (its row groups added in order), written by the first row group
   auto flush = [&](float (*v)[8], auto&& put) {
     if constexpr (kRows > 1) {
@@ -272,35 +322,37 @@ __global__ __launch_bounds__(norm_threads<LT>()) void residual_norm_grad_kernel(
       const int64_t e = (segment + 1) * p.rows_per_gate;
       piece_end = e < end ? e : end;
     }
-    // rows of the piece in steps of kRows: every row group runs every step (they share barriers only in flush)
+      // rows of the piece in steps of kRows: every row group runs its own (they share barriers only in flush)
+    const bool gated = p.gate != nullptr;
+    const T* gate = static_cast<const T*>(p.gate);
+    if (HASX && !(gated && each_row)) {
+      if (gated) gate += (gate_sums ? segment : piece / p.rows_per_gate) * p.hidden;
+      hold(gate, gated, held_g);
+    }
+    Row cur;
     for (int64_t row = piece + group; row < piece_end; row += kRows) {
       const int64_t base = row * p.hidden;
-      Raw8<TR> ru[V], rds[V];
-      Raw8<T> rdy[V], rx[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (ok[i]) {
-          ru[i] = load8(static_cast<const TR*>(p.sum) + base + at[i]);
-          rdy[i] = load8(static_cast<const T*>(p.dy) + base + at[i]);
-          if (p.dsum != nullptr) rds[i] = load8(static_cast<const TR*>(p.dsum) + base + at[i]);
-          if (has_x) rx[i] = load8(static_cast<const T*>(p.x) + base + at[i]);
-        }
+      load_row(row, cur);
+      if (HASX && gated && each_row) {
+        gate = static_cast<const T*>(p.gate) + base;
+        hold(gate, true, held_g);
+      }
       float sums[3] = {0.0f, 0.0f, 0.0f};   // s^2, dy w s, x^2
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (ok[i]) {
           float u[8], dy[8], w[8];
-          widen8(ru[i], u);
-          widen8(rdy[i], dy);
-          if (p.weight != nullptr) widen8(load8(p.weight + at[i]), w);
+          widen8(cur.u[i], u);
+          widen8(cur.dy[i], dy);
+          columns(p.weight, p.weight != nullptr, held_w, i, w);
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             sums[0] = __builtin_fmaf(u[c], u[c], sums[0]);
-            sums[1] = __builtin_fmaf(p.weight != nullptr ? dy[c] * w[c] : dy[c], u[c], sums[1]);
+            sums[1] = __builtin_fmaf(dy[c] * w[c], u[c], sums[1]);
           }
-          if (has_x && p.post_norm) {
+          if constexpr (HASX) {
             float x[8];
-            widen8(rx[i], x);
+            widen8(cur.x[i], x);
 #pragma unroll
             for (int c = 0; c < 8; ++c) sums[2] = __builtin_fmaf(x[c], x[c], sums[2]);
           }
@@ -309,80 +361,61 @@ __global__ __launch_bounds__(norm_threads<LT>()) void residual_norm_grad_kernel(
       row_sums<LT, 3>(sums, red_a, tid);
       const float rho = inv_rms(sums[0], p.hidden, p.eps);
       const float back = rho * rho * sums[1] / (float)p.hidden;
-      const float sigma = has_x && p.post_norm ? inv_rms(sums[2], p.hidden, p.eps) : 1.0f;
-      const T* gate = p.gate != nullptr ? static_cast<const T*>(p.gate) + (row / p.rows_per_gate) * p.hidden : nullptr;
-      float dz[V][8];   // the gradient of z, times v where there is a norm
+      const float sigma = normed ? inv_rms(sums[2], p.hidden, p.eps) : 1.0f;
+      float dz[VX][8];   // the gradient of z, times v
       float inner[1] = {0.0f};
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (ok[i]) {
-          float u[8], dy[8], w[8], du[8];
-          widen8(ru[i], u);
-          widen8(rdy[i], dy);
-          if (p.weight != nullptr) widen8(load8(p.weight + at[i]), w);
+          float u[8], dy[8], du[8], w[8];
+          widen8(cur.u[i], u);
+          widen8(cur.dy[i], dy);
+          columns(p.weight, p.weight != nullptr, held_w, i, w);
           if (p.dsum != nullptr) {
-            widen8(rds[i], du);
+            widen8(cur.ds[i], du);
           } else {
 #pragma unroll
             for (int c = 0; c < 8; ++c) du[c] = 0.0f;
           }
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            const float t = p.weight != nullptr ? dy[c] * w[c] : dy[c];
-            du[c] += rho * (t - u[c] * back);
+            du[c] += rho * (dy[c] * w[c] - u[c] * back);
             dw[i][c] = __builtin_fmaf(dy[c], u[c] * rho, dw[i][c]);
           }
           store8(static_cast<TR*>(p.dresidual) + base + at[i], narrow8<TR>(du));
-          if (!has_x) continue;
-          float x[8], v[8], g[8];
-          widen8(rx[i], x);
-          const bool weighted = p.post_norm && p.post_weight != nullptr;
-          if (weighted) widen8(load8(p.post_weight + at[i]), v);
-          if (gate != nullptr) {
-            widen8(load8(gate + at[i]), g);
-            if (p.dgate != nullptr) {
-              float dg[8];
-#pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                const float n = x[c] * sigma;
-                dg[c] = p.scale * du[c] * (weighted ? n * v[c] : n);
-              }
-              if (each_row) {
-                store8(static_cast<T*>(p.dgate) + base + at[i], narrow8<T>(dg));
-              } else {
-#pragma unroll
-                for (int c = 0; c < 8; ++c) dgs[i][c] += dg[c];
-              }
-            }
-          }
-#pragma unroll
-          for (int c = 0; c < 8; ++c) dz[i][c] = gate != nullptr ? p.scale * du[c] * g[c] : p.scale * du[c];
-          if (p.post_norm) {
+          if constexpr (HASX) {
+            float x[8], v[8], g[8], dg[8];
+            widen8(cur.x[i], x);
+            columns(p.post_weight, weighted, held_v, i, v);
+            columns(gate, gated, held_g, i, g);
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
-              dv[i][c] = __builtin_fmaf(dz[i][c], x[c] * sigma, dv[i][c]);
-              if (weighted) dz[i][c] *= v[c];
+              const float n = x[c] * sigma, dz0 = p.scale * du[c];
+              dg[c] = dz0 * (n * v[c]);
+              dgs[i][c] += dg[c];
+              dz[i][c] = dz0 * g[c];
+              dv[i][c] = __builtin_fmaf(dz[i][c], n, dv[i][c]);
+              dz[i][c] *= v[c];
               inner[0] = __builtin_fmaf(dz[i][c], x[c], inner[0]);
             }
-          } else {
-            store8(static_cast<T*>(p.dx) + base + at[i], narrow8<T>(dz[i]));
+            if (each_row && p.dgate != nullptr) store8(static_cast<T*>(p.dgate) + base + at[i], narrow8<T>(dg));
           }
         }
-      if (has_x && p.post_norm) {
-        row_sums<LT, 1>(inner, red_b, tid);   // (red_b's readers of the previous row are past the barrier above)
+      if constexpr (HASX) {
+        if (normed) row_sums<LT, 1>(inner, red_b, tid);   // (red_b's readers of the previous row are past the barrier above)
         const float along = sigma * sigma * inner[0] / (float)p.hidden;
 #pragma unroll
         for (int i = 0; i < V; ++i)
           if (ok[i]) {
             float x[8], dx[8];
-            widen8(rx[i], x);
+            widen8(cur.x[i], x);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) dx[c] = sigma * (dz[i][c] - x[c] * along);
+            for (int c = 0; c < 8; ++c) dx[c] = sigma * (dz[i][c] - (normed ? x[c] * along : 0.0f));
             store8(static_cast<T*>(p.dx) + base + at[i], narrow8<T>(dx));
           }
       }
     }
-    if (gate_sums) {
+    if (HASX && gate_sums) {
       const int64_t seg_first = segment * p.rows_per_gate;
       const bool whole = seg_first >= first && seg_first + p.rows_per_gate <= end;
       float* slot = p.part + (seg_first > first ? 3 : 2) * plane + (int64_t)blockIdx.x * p.hidden;
@@ -402,56 +435,73 @@ __global__ __launch_bounds__(norm_threads<LT>()) void residual_norm_grad_kernel(
   }
   float* mine = p.part + (int64_t)blockIdx.x * p.hidden;
   if (p.dweight != nullptr) flush(dw, [&](int c0, const float* t) { store8(mine + c0, narrow8<float>(t)); });
-  if (p.dpost != nullptr) flush(dv, [&](int c0, const float* t) { store8(mine + plane + c0, narrow8<float>(t)); });
+  if (HASX && p.dpost != nullptr) flush(dv, [&](int c0, const float* t) { store8(mine + plane + c0, narrow8<float>(t)); });
 }
 
-// Column sums of the partials: 64 columns a workgroup (16 lanes of 4), 16 of the partials side by side, added in a fixed
-// order.  blockIdx.y = 0: dweight, 1: dpost, 2 + j: the gate whose rows pass from workgroup j to j + 1.
+// Column sums of the partials: 64 columns a workgroup (16 lanes of 4), 64 of the partials side by side, eight loads of each
+// in flight, all added in a fixed order.  blockIdx.y = 0: dweight, 1: dpost, the rest the gates whose rows lie in more than
+// one workgroup's: 2 + i is gate i where gates have at least a workgroup's rows; where they have fewer, the 64 borders from
+// 64 i on between workgroups j and j + 1, each with the last piece of j and the first of j + 1.
+constexpr int kSumAlong = 64;
+
 template <class T>
-__global__ __launch_bounds__(256) void norm_grad_sum_kernel(NormGradParams p) {
-  __shared__ v4f s_sum[16][16];
+__global__ __launch_bounds__(16 * kSumAlong) void norm_grad_sum_kernel(NormGradParams p) {
+  __shared__ v4f s_sum[kSumAlong][16];
   const int lane = threadIdx.x & 15, along = threadIdx.x >> 4;
   const int col = blockIdx.x * 64 + 4 * lane;
+  const bool there = col < p.hidden;
   const int64_t plane = (int64_t)p.parts * p.hidden;
-  const float* src = p.part;
-  int begin = 0, end = p.parts;
-  int64_t segment = 0;
+  auto at = [&](int which, int part) { return *reinterpret_cast<const v4f*>(p.part + which * plane + (int64_t)part * p.hidden + col); };
+  auto put_gate = [&](int64_t gate, v4f v) {
+    T* out = static_cast<T*>(p.dgate) + gate * p.hidden + col;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) out[c] = narrow<T>(v[c]);
+  };
+  int which = blockIdx.y, begin = 0, end = p.parts;
   int head = -1;   // the workgroup in which the gate's rows begin, where that piece is in slot 1
-  if (blockIdx.y == 0) {
-    if (p.dweight == nullptr) return;
-  } else if (blockIdx.y == 1) {
-    if (p.dpost == nullptr) return;
-    src += plane;
+  if (blockIdx.y < 2) {
+    if (blockIdx.y == 0 ? p.dweight == nullptr : p.dpost == nullptr) return;
+  } else if (p.rows_per_gate < p.rows_per_part) {
+    const int j = (blockIdx.y - 2) * kSumAlong + along;
+    if (j + 1 >= p.parts || !there) return;
+    const int64_t border = (int64_t)(j + 1) * p.rows_per_part, gate = border / p.rows_per_gate;
+    if (gate * p.rows_per_gate != border) put_gate(gate, at(3, j) + at(2, j + 1));
+    return;
   } else {
-    const int j = blockIdx.y - 2;
-    const int64_t border = (int64_t)(j + 1) * p.rows_per_part;
-    segment = border / p.rows_per_gate;
-    const int64_t first = segment * p.rows_per_gate;
-    // (rows of one gate end at the border, or this gate's were met at an earlier border)
-    if (first == border || first < (int64_t)j * p.rows_per_part) return;
-    begin = j;
-    end = (int)((first + p.rows_per_gate + p.rows_per_part - 1) / p.rows_per_part);
-    if (first > (int64_t)j * p.rows_per_part) head = j;
-    src += 2 * plane;
+    const int64_t first = (int64_t)(blockIdx.y - 2) * p.rows_per_gate;
+    begin = (int)(first / p.rows_per_part);
+    end = (int)((first + p.rows_per_gate - 1) / p.rows_per_part) + 1;
+    if (end - begin == 1) return;   // written already
+    if (first > (int64_t)begin * p.rows_per_part) head = begin;
+    which = 2;
   }
   v4f sum = {0.f, 0.f, 0.f, 0.f};
-  if (col < p.hidden)
-    for (int i = begin + along; i < end; i += 16)
-      sum += *reinterpret_cast<const v4f*>(src + (i == head ? plane : 0) + (int64_t)i * p.hidden + col);
+  if (there)
+    for (int i0 = begin + along; i0 < end; i0 += 8 * kSumAlong) {
+      v4f v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int i = i0 + u * kSumAlong < end ? i0 + u * kSumAlong : i0;
+        v[u] = at(i == head ? 3 : which, i);
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (i0 + u * kSumAlong < end) sum += v[u];
+    }
   s_sum[along][lane] = sum;
   __syncthreads();
-  if (along != 0 || col >= p.hidden) return;
+  if (along < 8) {
 #pragma unroll
-  for (int i = 1; i < 16; ++i) sum += s_sum[i][lane];
-  if (blockIdx.y == 0) {
-    *reinterpret_cast<v4f*>(p.dweight + col) = sum;
-  } else if (blockIdx.y == 1) {
-    *reinterpret_cast<v4f*>(p.dpost + col) = sum;
-  } else {
-    T* out = static_cast<T*>(p.dgate) + segment * p.hidden + col;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) out[c] = narrow<T>(sum[c]);
+    for (int i = 8; i < kSumAlong; i += 8) sum += s_sum[along + i][lane];
+    s_sum[along][lane] = sum;   // (no other thread reads these eight before the barrier)
   }
+  __syncthreads();
+  if (along != 0 || !there) return;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) sum += s_sum[i][lane];
+  if (blockIdx.y == 0) *reinterpret_cast<v4f*>(p.dweight + col) = sum;
+  else if (blockIdx.y == 1) *reinterpret_cast<v4f*>(p.dpost + col) = sum;
+  else put_gate(blockIdx.y - 2, sum);
 }
 
 // ---- host ------------------------------------------------------------------------------------------
@@ -473,14 +523,18 @@ static const void* norm_fn_of(int out, int lt, int v) {
          : out == kNormFp8 ? norm_fn<T, TR, kNormFp8>(lt, v) : norm_fn<T, TR, kNormInt8>(lt, v);
 }
 
-template <class T, class TR>
-static const void* norm_grad_fn(int lt, int v) {
-  void (*fn)(NormGradParams) = lt == 64    ? (v == 1 ? residual_norm_grad_kernel<T, TR, 64, 1> : residual_norm_grad_kernel<T, TR, 64, 2>)
-                               : lt == 256 ? (v == 1 ? residual_norm_grad_kernel<T, TR, 256, 1>
-                                                     : residual_norm_grad_kernel<T, TR, 256, 2>)
-                               : lt == 512 ? residual_norm_grad_kernel<T, TR, 512, 2>
-                                           : residual_norm_grad_kernel<T, TR, 1024, 2>;
+template <class T, class TR, bool HASX>
+static const void* norm_grad_fn_of(int lt, int v) {
+  void (*fn)(NormGradParams) =
+      lt == 64 ? (v == 1 ? residual_norm_grad_kernel<T, TR, HASX, 64, 1> : residual_norm_grad_kernel<T, TR, HASX, 64, 2>)
+      : lt == 256 ? (v == 1 ? residual_norm_grad_kernel<T, TR, HASX, 256, 1> : residual_norm_grad_kernel<T, TR, HASX, 256, 2>)
+                  : (v == 2 ? residual_norm_grad_kernel<T, TR, HASX, 512, 2> : residual_norm_grad_kernel<T, TR, HASX, 512, 4>);
   return reinterpret_cast<const void*>(fn);
+}
+
+template <class T, class TR>
+static const void* norm_grad_fn(bool has_x, int lt, int v) {
+  return has_x ? norm_grad_fn_of<T, TR, true>(lt, v) : norm_grad_fn_of<T, TR, false>(lt, v);
 }
 
 // Lanes a row and pieces a lane.
@@ -532,11 +586,20 @@ int launch_residual_norm(int out, const void* x, const void* residual, int dtype
   return e == hipSuccess ? kOk : set_error(kHip, "residual_norm launch: %s", hipGetErrorString(e));
 }
 
-// Workgroups of the backward pass and the rows of each.
+// The backward pass: at most 512 lanes a row, whose registers hold the columns' sums too.
+static void norm_grad_shape(int64_t hidden, int* lt, int* v) {
+  norm_shape(hidden, lt, v);
+  if (*lt == 1024) {
+    *lt = 512;
+    *v = 4;
+  }
+}
+
+// Its workgroups and the rows of each.
 static void norm_grad_parts(int64_t rows, int64_t hidden, int64_t* per_part, int* parts) {
   int lt, v;
-  norm_shape(hidden, &lt, &v);
-  const int64_t most = lt <= 256 ? 1024 : lt == 512 ? 512 : 256;
+  norm_grad_shape(hidden, &lt, &v);
+  const int64_t most = lt <= 256 ? 1024 : v == 2 ? 512 : 256;
   *per_part = (rows + most - 1) / most;
   *parts = rows == 0 ? 0 : (int)((rows + *per_part - 1) / *per_part);
 }
@@ -586,21 +649,22 @@ int launch_residual_norm_grad(const void* dy, const void* dsum, const void* x, c
   p.eps = eps;
   norm_grad_parts(rows, hidden, &p.rows_per_part, &p.parts);
   int lt, v;
-  norm_shape(hidden, &lt, &v);
+  norm_grad_shape(hidden, &lt, &v);
   const bool wide = residual_dtype == kF32;
-  const void* fn = dtype == kF32 ? norm_grad_fn<float, float>(lt, v)
-                   : dtype == kBf16 ? (wide ? norm_grad_fn<Bf16, float>(lt, v) : norm_grad_fn<Bf16, Bf16>(lt, v))
-                                    : (wide ? norm_grad_fn<_Float16, float>(lt, v) : norm_grad_fn<_Float16, _Float16>(lt, v));
+  const void* fn = dtype == kF32 ? norm_grad_fn<float, float>(x != nullptr, lt, v)
+                   : dtype == kBf16 ? (wide ? norm_grad_fn<Bf16, float>(x != nullptr, lt, v) : norm_grad_fn<Bf16, Bf16>(x != nullptr, lt, v))
+                                    : (wide ? norm_grad_fn<_Float16, float>(x != nullptr, lt, v) : norm_grad_fn<_Float16, _Float16>(x != nullptr, lt, v));
   void* args[] = {&p};
   hipError_t e = hipLaunchKernel(fn, dim3((unsigned)p.parts), dim3(lt > kNormThreads ? lt : kNormThreads), args, 0, stream);
   if (e != hipSuccess) return set_error(kHip, "residual_norm_grad launch: %s", hipGetErrorString(e));
-  const bool borders = dgate != nullptr && p.rows_per_gate > 1 && p.parts > 1;
-  if (dweight == nullptr && dpost == nullptr && !borders) return kOk;
+  int64_t gates = 0;   // rows of the sums' grid for gates
+  if (dgate != nullptr && p.rows_per_gate > 1 && p.parts > 1)
+    gates = p.rows_per_gate < p.rows_per_part ? (p.parts - 1 + kSumAlong - 1) / kSumAlong : gate_rows;
+  if (dweight == nullptr && dpost == nullptr && gates == 0) return kOk;
   void (*sum_fn)(NormGradParams) = dtype == kF32 ? norm_grad_sum_kernel<float>
                                    : dtype == kBf16 ? norm_grad_sum_kernel<Bf16> : norm_grad_sum_kernel<_Float16>;
   e = hipLaunchKernel(reinterpret_cast<const void*>(sum_fn),
-                      dim3((unsigned)((hidden + 63) / 64), borders ? (unsigned)(2 + p.parts - 1) : 2u), dim3(256), args, 0,
-                      stream);
+                      dim3((unsigned)((hidden + 63) / 64), (unsigned)(2 + gates)), dim3(16 * kSumAlong), args, 0, stream);
   return e == hipSuccess ? kOk : set_error(kHip, "residual_norm_grad sums launch: %s", hipGetErrorString(e));
 }
 
