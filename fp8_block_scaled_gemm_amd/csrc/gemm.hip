@@ -98,8 +98,9 @@ __device__ __forceinline__ void check_contiguous_block(const int32_t* m_indices,
 template <int BN_, int BM_, int WN_, int WM_, int STAGES_, bool HALF_ISSUE_ = false, bool PIPE_ = false>
 struct Cfg {
   static constexpr int BN = BN_, BM = BM_, WN = WN_, WM = WM_, STAGES = STAGES_;
-  // PIPE: the two-slot main loop that overlaps every K block's operand reads and DMA issue with
-  // the previous block's MFMAs (one barrier per K block, placed two fragment rows before its end)
+  // PIPE: the two-slot (gated form: also three-slot) main loop that overlaps every K block's operand
+  // reads and DMA issue with the previous block's MFMAs (one barrier per K block, placed two
+  // fragment rows before its end)
   static constexpr bool PIPE = PIPE_;
   static constexpr int kWavesN = BN / WN;
   static constexpr int kWavesM = BM / WM;
@@ -134,7 +135,7 @@ struct Cfg {
   static_assert(WN % 16 == 0 && WM % 16 == 0 && 128 % WN == 0, "wave tile must be 16-aligned, WN | 128");
   static_assert(STAGES >= 2 && STAGES <= 4, "2..4 stages");
   static_assert(kVmPerStage * (STAGES - 1) < 64, "vmcnt range");
-  static_assert(!PIPE || (STAGES == 2 && WN / 16 >= 3 && !HALF_ISSUE_), "PIPE: two slots, >= 3 fragment rows, all waves issue");
+  static_assert(!PIPE || (STAGES <= 3 && WN / 16 >= 3 && !HALF_ISSUE_), "PIPE: 2..3 slots, >= 3 fragment rows, all waves issue");
   // every issuing wave issues exactly kVmPerStage instructions per stage (lane 0 of each scale DMA
   // is active), which the vmcnt waits count on
   static_assert(kSaLanesPerWave <= 64 && BM % 4 == 0 && (kIssuers - 1) * kSaLanesPerWave < BM / 4,
@@ -147,7 +148,8 @@ struct Cfg {
 // copies of the tile's block scales, or BN per-row scales for kDenseRowB).
 template <class C, int LAYOUT>
 constexpr int stage_bytes() {
-  if constexpr (C::PIPE) return C::kPipeSbOffset + C::kWaves * 256;
+  // (three slots: four copies of the block scales, each fetched by two waves to the same end)
+  if constexpr (C::PIPE) return C::kPipeSbOffset + (C::STAGES == 3 ? 4 : C::kWaves) * 256;
   return C::kSbOffset + (LAYOUT == kDenseRowB ? C::BN * 4 : C::kIssuers * C::kSbWaveBytes);
 }
 
@@ -615,6 +617,8 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
       // slot 0 (blocks 0, 2, ...) is the buffer the epilogue's strips do not use
       uint8_t* const slot0 = st1;
       uint8_t* const slot1 = st0;
+      static_assert(S == 2 || GATED, "three slots: the gated form");
+      const int sb_copy = S == 3 ? wave & 3 : wave;
       const int lane_off = lds_off(l16, 2 * g4);
       // this wave's activation-scale rows m0 + wm0 + lane (64 of them, the wave's WM first) and the
       // scale of its weight block, as byte offsets within a K block's scale row
@@ -636,7 +640,7 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
       auto dma_ctx = [&](int tk, auto slot_c, bool valid) {
         constexpr int slot = decltype(slot_c)::value;
         DmaCtx c;
-        c.sbase = slot == 0 ? slot0 : slot1;
+        c.sbase = slot == 0 ? slot0 : slot == 1 ? slot1 : st2;
         c.kb = kb_begin + tk;
         c.base_off = dma_off;
         asm volatile("" : "+v"(c.base_off));
@@ -658,7 +662,7 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
           lds_dma4(rs_sa, c.sbase + C::kPipeSaOffset + wave * 256, sa_lane_off | (c.inv_mask & kOut),
                    __builtin_amdgcn_readfirstlane(c.kb * (int)p.ld_sa * 4));
         } else {
-          lds_dma4(rs_sb, c.sbase + C::kPipeSbOffset + wave * 256, sb_wave_off | (c.inv_mask & kOut),
+          lds_dma4(rs_sb, c.sbase + C::kPipeSbOffset + sb_copy * 256, sb_wave_off | (c.inv_mask & kOut),
                    __builtin_amdgcn_readfirstlane(c.kb * 4));
         }
       };
@@ -684,8 +688,9 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
         const float* sa_w = reinterpret_cast<const float*>(sbase + C::kPipeSaOffset + wave * 256);
 #pragma unroll
         for (int j = 0; j < kFM; ++j) raw[j] = sa_w[16 * j + l16];
-        raw[kFM] = *reinterpret_cast<const float*>(sbase + C::kPipeSbOffset + wave * 256);
-        if constexpr (GATED) raw[kFM + 1] = *reinterpret_cast<const float*>(sbase + C::kPipeSbOffset + wave * 256 + 128);
+        raw[kFM] = *reinterpret_cast<const float*>(sbase + C::kPipeSbOffset + sb_copy * 256);
+        if constexpr (GATED)
+          raw[kFM + 1] = *reinterpret_cast<const float*>(sbase + C::kPipeSbOffset + sb_copy * 256 + 128);
       };
       // Fragment rows [R0, R1) of the block in slot cur; the rows from 0 first form the promotion
       // scales sc[j] = fl32(sa * sb) from the raw ones.  Row i takes its A fragment from a[i % 3]
@@ -749,12 +754,18 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
       auto bar_tail = [&](int tk, auto cur_c, auto nxt_c, v8i* a, v8i* bop, float* sc, float* rn, const float* rc) {
         constexpr int cur_slot = decltype(cur_c)::value;
         constexpr int nxt_slot = decltype(nxt_c)::value;
-        const SlotPtr cur = cur_slot == 0 ? slot0 : slot1;
-        const SlotPtr nxt = nxt_slot == 0 ? slot0 : slot1;
+        const SlotPtr cur = cur_slot == 0 ? slot0 : cur_slot == 1 ? slot1 : st2;
+        const SlotPtr nxt = nxt_slot == 0 ? slot0 : nxt_slot == 1 ? slot1 : st2;
         __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): this wave's reads of slot CUR are done
-        wait_vmcnt<0>();                      // its DMAs of block tk+1 have landed
-        __syncthreads();                      // ... and every wave's
-        const DmaCtx dc = dma_ctx(tk + 2, cur_c, tk + 2 < nk);
+        if constexpr (S == 3) {
+          // its DMAs of block tk+1 have landed, those of block tk+2 fly on (__syncthreads would wait for them too)
+          wait_vmcnt<kStageDmas>();
+          asm volatile("s_barrier" ::: "memory");
+        } else {
+          wait_vmcnt<0>();                    // its DMAs of block tk+1 have landed
+          __syncthreads();                    // ... and every wave's
+        }
+        const DmaCtx dc = dma_ctx(tk + S, cur_c, tk + S < nk);
         read_scales(nxt, rn);
         rows(IC<kBarRow>{}, IC<kFN>{}, cur, nxt, a, bop, sc, rc, &dc);
         const v8i n0a = a[kFN % 3], n1a = a[(kFN + 1) % 3];
@@ -770,6 +781,7 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
       __syncthreads();   // block 0 landed for every wave; every wave is done with the strips
       if (nk > 0) {
       issue_pipe(1, IC<1>{}, nk > 1);
+      if constexpr (S == 3) issue_pipe(2, IC<2>{}, nk > 2);
       v8i bop[kFM], a[3];
       float sc[kFM], r0[kFM + 2], r1[kFM + 2];
 #pragma unroll
@@ -779,8 +791,28 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
       a[1] = read_a(slot0, 1);
       // block 0 up to its barrier row
       rows(IC<0>{}, IC<kBarRow>{}, slot0, slot1, a, bop, sc, r0, nullptr);
-      // two blocks per iteration (the slots alternate), while a block tk+2 follows; then the rest
+      // two (three) blocks per iteration (the slots alternate), while a block after them follows; then the rest
       int tk = 0;
+      if constexpr (S == 3) {
+        float r2[kFM + 2];
+        for (; tk + 3 < nk; tk += 3) {
+          bar_tail(tk, IC<0>{}, IC<1>{}, a, bop, sc, r1, r0);
+          rows(IC<0>{}, IC<kBarRow>{}, slot1, st2, a, bop, sc, r1, nullptr);
+          bar_tail(tk + 1, IC<1>{}, IC<2>{}, a, bop, sc, r2, r1);
+          rows(IC<0>{}, IC<kBarRow>{}, st2, slot0, a, bop, sc, r2, nullptr);
+          bar_tail(tk + 2, IC<2>{}, IC<0>{}, a, bop, sc, r0, r2);
+          rows(IC<0>{}, IC<kBarRow>{}, slot0, slot1, a, bop, sc, r0, nullptr);
+        }
+        bar_tail(tk, IC<0>{}, IC<1>{}, a, bop, sc, r1, r0);
+        if (tk + 1 < nk) {
+          rows(IC<0>{}, IC<kBarRow>{}, slot1, st2, a, bop, sc, r1, nullptr);
+          bar_tail(tk + 1, IC<1>{}, IC<2>{}, a, bop, sc, r2, r1);
+          if (tk + 2 < nk) {
+            rows(IC<0>{}, IC<kBarRow>{}, st2, slot0, a, bop, sc, r2, nullptr);
+            bar_tail(tk + 2, IC<2>{}, IC<0>{}, a, bop, sc, r0, r2);
+          }
+        }
+      } else {
       for (; tk + 2 < nk; tk += 2) {
         bar_tail(tk, IC<0>{}, IC<1>{}, a, bop, sc, r1, r0);
         rows(IC<0>{}, IC<kBarRow>{}, slot1, slot0, a, bop, sc, r1, nullptr);
@@ -791,6 +823,7 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
       if (tk + 1 < nk) {
         rows(IC<0>{}, IC<kBarRow>{}, slot1, slot0, a, bop, sc, r1, nullptr);
         bar_tail(tk + 1, IC<1>{}, IC<0>{}, a, bop, sc, r0, r1);
+      }
       }
       wait_vmcnt<0>();   // the zero-filling DMAs past the last K block
       }
@@ -1405,6 +1438,11 @@ const void* gated_few_kernel(int layout, int bm);
 int gated_few_lds(int bm);
 int launch_gated_join(int layout, GemmParams p, int bm, hipStream_t stream);
 
+// The 256x128 tile on three slots (157 KB LDS): weights that only a few row blocks read come from memory, whose latency
+// under load passes the time of this tile's K block (32 groups of 256 rows, half in use, 2048 x 7168: 257 us, with two
+// slots 275; contiguous, 8 groups in 8192 rows: 285, with two slots 350).
+using CfgGatedRows128 = Cfg<256, 128, 64, 64, 3, false, true>;
+
 enum GatedCfgId : int { kGatedRows128 = 0, kGatedSquare, kGatedFew16, kGatedFew64 };
 constexpr int kMaxStreamSplits = 32;
 
@@ -1414,7 +1452,7 @@ static LaunchInfo gated_info(int cfg) {
     const int bm = cfg == kGatedFew16 ? 16 : 64;
     return LaunchInfo{256, bm, 512, 2, gated_few_kernel(LAYOUT, bm), gated_few_lds(bm)};
   }
-  return cfg == kGatedSquare ? info<CfgSquare, LAYOUT, false, true>() : info<CfgRows128, LAYOUT, false, true>();
+  return cfg == kGatedSquare ? info<CfgSquare, LAYOUT, false, true>() : info<CfgGatedRows128, LAYOUT, false, true>();
 }
 
 // Estimated time (us) of a dense gated product by tile and K split, from timings of every choice on MI355X over 15
@@ -1472,7 +1510,7 @@ static Plan make_gated_plan(int layout, int64_t m, int64_t n, int64_t k, int64_t
              : choose_contiguous(m, weight_rows, call_groups, num_cus) == kCfgSquare ? kGatedSquare : kGatedRows128;
   } else if (layout == kMasked) {
     // rows in use are not known here; beyond 64 the 128-row tile, which a group's last rows fill worse than the streaming
-    // kernel's but the weights pass less often (32 x 256 x 2048 x 7168, half in use: 275 us, 256-row tiles 300, 64-row strips 380)
+    // kernel's but the weights pass less often (32 x 256 x 2048 x 7168, half in use: 257 us, 256-row tiles 300, 64-row strips 380)
     pl.cfg = forced >= 0 ? forced : m <= 16 ? kGatedFew16 : m <= 64 ? kGatedFew64 : kGatedRows128;
     const int64_t bm = gated_info<kDense>(pl.cfg).bm;
     const int64_t tiles = ((m + bm - 1) / bm) * strips * groups;
