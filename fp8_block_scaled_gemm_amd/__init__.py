@@ -911,10 +911,16 @@ def _act(act):
 
 def _one_device(*ts):
     """Contiguous tensors (or None) on one device: that device."""
-    ts = [t for t in ts if t is not None]
-    dev = _dev(*ts)
+    dev = None
     for t in ts:
-        _require(t.device == dev, "tensors must be on one device")
+        if t is None:
+            continue
+        if not (t.is_cuda and t.is_contiguous()):
+            raise ValueError("tensors must be contiguous CUDA (HIP) tensors")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError("tensors must be on one device")
     return dev
 
 
@@ -934,7 +940,8 @@ def _like(t, shape, dtype, device, what):
     """The caller's output if it has this shape and type, or a new one."""
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    _require(t.dtype == dtype and tuple(t.shape) == tuple(shape), f"{what} must be {dtype} {tuple(shape)}")
+    if t.dtype != dtype or t.shape != shape:   # (the message's text costs more than the check)
+        raise ValueError(f"{what} must be {dtype} {tuple(shape)}")
     return t
 
 
@@ -943,8 +950,8 @@ def _scales_like(s, lead, groups, device):
     shape = (*lead[:-1], groups)
     if s is None:
         return torch.empty((*shape, dg_get_scale_ld(lead[-1])), dtype=torch.float32, device=device)
-    _require(s.dtype == torch.float32 and tuple(s.shape[:-1]) == shape and s.shape[-1] >= lead[-1] and s.shape[-1] % 4 == 0,
-             f"scales must be float32 {shape} with a last dimension of at least {lead[-1]}, a multiple of 4")
+    if s.dtype != torch.float32 or s.shape[:-1] != shape or s.shape[-1] < lead[-1] or s.shape[-1] % 4 != 0:
+        raise ValueError(f"scales must be float32 {shape} with a last dimension of at least {lead[-1]}, a multiple of 4")
     return s
 
 
@@ -981,7 +988,8 @@ def _gated_operands(a, sa, b, sb, groups):
 def _gated_out(lead, n, out, d, q, s, pre, device):
     """(d, q, s) as given or allocated, one of d and (q, s) None."""
     _require(out in ("bf16", "fp8"), "out must be 'bf16' or 'fp8'")
-    _require(pre is None or (pre.dtype == torch.bfloat16 and tuple(pre.shape) == (*lead, 2 * n)), f"pre must be bfloat16 {(*lead, 2 * n)}")
+    if pre is not None:
+        _like(pre, (*lead, 2 * n), torch.bfloat16, device, "pre")
     if out == "bf16":
         _require(q is None and s is None, "q and s go with out='fp8'")
         return _like(d, (*lead, n), torch.bfloat16, device, "d"), None, None
@@ -1147,14 +1155,19 @@ ResidualNormGrad = collections.namedtuple("ResidualNormGrad", "dx dresidual dwei
 
 
 def _norm_args(x, residual, dtype, weight, gate, post_norm, post_weight, scale, eps, what="residual"):
-    _require(residual.dim() == 2, f"{what} must be (rows, hidden)")
-    rows, hidden = residual.shape
+    shape = residual.shape
+    if len(shape) != 2:
+        raise ValueError(f"{what} must be (rows, hidden)")
+    rows, hidden = shape
     code = _dtype(dtype, "x")
-    _require(residual.dtype in (dtype, torch.float32), f"{what} must be float32 or in x's type")
-    _require(x is None or (x.dtype == dtype and x.shape == residual.shape), f"x must be like {what}, (rows, hidden)")
+    if residual.dtype != dtype and residual.dtype != torch.float32:
+        raise ValueError(f"{what} must be float32 or in x's type")
+    if x is not None and (x.dtype != dtype or x.shape != shape):
+        raise ValueError(f"x must be like {what}, (rows, hidden)")
     _require(x is not None or (gate is None and not post_norm), "a gate or a first norm needs x")
     for w, name in ((weight, "weight"), (post_weight, "post_weight")):
-        _require(w is None or (w.dtype == torch.float32 and tuple(w.shape) == (hidden,)), f"{name} must be float32 (hidden,)")
+        if w is not None and (w.dtype != torch.float32 or w.shape != (hidden,)):
+            raise ValueError(f"{name} must be float32 (hidden,)")
     _require(post_weight is None or post_norm, "post_weight goes with post_norm")
     gate_rows = 0
     if gate is not None:
@@ -1171,8 +1184,11 @@ def _norm_sum(x, residual, total):
     if x is None:
         _require(total is None, "without x the sum is the residual")
         return residual, None
-    total = _like(total, residual.shape, residual.dtype, residual.device, "sum")
-    return total, _ptr(total)
+    if total is None:
+        total = torch.empty_like(residual)
+    else:
+        _like(total, residual.shape, residual.dtype, residual.device, "sum")
+    return total, total.data_ptr()
 
 
 def dg_residual_norm(x, residual, weight=None, gate=None, post_norm=False, post_weight=None, scale=1.0, eps=1e-6, sum=None,
