@@ -1199,6 +1199,7 @@ def dg_residual_norm(x, residual, weight=None, gate=None, post_norm=False, post_
     gate row serves that many consecutive rows.  weights float32, None for ones.  x None: the norm alone (sum is residual),
     y in `dtype`, by default residual's."""
     t = x.dtype if x is not None else dtype or residual.dtype
+    _require(dtype is None or dtype == t, "dtype goes without x: y is in x's type")
     rows, hidden, args = _norm_args(x, residual, t, weight, gate, post_norm, post_weight, scale, eps)
     total, at = _norm_sum(x, residual, sum)
     y = _like(y, (rows, hidden), t, residual.device, "y")

@@ -86,10 +86,10 @@ template <class T, int ACT, int HOLD>
 __global__ __launch_bounds__(kActThreads) void gated_act_int8_kernel(GatedActParams p) {
   __shared__ uint32_t s_max[kActThreads / 64];
   const int tid = threadIdx.x;
-  const int64_t row = blockIdx.x;
+  const int64_t row = blockIdx.x + (int64_t)gridDim.x * blockIdx.y;
   int group, in_group;
   p.mask.split(row, group, in_group);
-  if (p.mask.skips(row, group, in_group)) return;
+  if (row >= p.rows || p.mask.skips(row, group, in_group)) return;
   const T* src = static_cast<const T*>(p.pre) + row * 2 * p.n;
   uint8_t* dst = static_cast<uint8_t*>(p.h) + row * p.n;
   float h[HOLD][8];
@@ -313,9 +313,10 @@ template <class T, int ACT>
 static int launch_act(int form, GatedActParams p, hipStream_t stream) {
   void* args[] = {&p};
   if (form == 2) {
-    if (p.rows > 0x7fffffffLL) return set_error(kUnsupported, "gated_act_int8: 2^31 rows");
+    const int64_t gx = p.rows < kGridRow ? p.rows : kGridRow;
     void (*fn)(GatedActParams) = gated_act_int8_kernel<T, ACT, 4>;
-    return act_launched("gated_act_int8", hipLaunchKernel(reinterpret_cast<const void*>(fn), dim3((unsigned)p.rows),
+    return act_launched("gated_act_int8", hipLaunchKernel(reinterpret_cast<const void*>(fn),
+                                                          dim3((unsigned)gx, (unsigned)((p.rows + gx - 1) / gx)),
                                                           dim3(kActThreads), args, 0, stream));
   }
   const int groups = (p.n + kGroup - 1) / kGroup;

@@ -1556,7 +1556,9 @@ static int launch_gated(GemmParams p, const Plan& pl, hipStream_t stream, int nu
 }
 
 size_t gemm_gated_workspace_size(int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus) {
-  return make_gated_plan(groups > 1 ? kMasked : kDense, m, n, k, groups, num_cus, true).ws_bytes;
+  const size_t masked = make_gated_plan(kMasked, m, n, k, groups, num_cus, true).ws_bytes;
+  const size_t dense = groups == 1 ? make_gated_plan(kDense, m, n, k, 1, num_cus, true).ws_bytes : 0;
+  return masked > dense ? masked : dense;   // (one group may be either form's)
 }
 
 void gemm_gated_config_name(int layout, int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus, char* buf,
@@ -1572,6 +1574,9 @@ int launch_gemm_gated(int layout, const uint8_t* a, const float* sa, int64_t ld_
   if (2 * n * k > 0x7fffffffLL || m * k > 0x7fffffffLL)
     return set_error(kUnsupported, "gated gemm: one group's operand must be < 2^31 bytes (m=%lld n=%lld k=%lld)",
                      (long long)m, (long long)n, (long long)k);
+  if (ld_sa > 0x1fffffffLL / ((k + kGroup - 1) / kGroup))   // offsets into one group's scales are 32 bits
+    return set_error(kUnsupported, "gated gemm: one group's activation scales must be < 2^31 bytes (k=%lld ld_sa=%lld)",
+                     (long long)k, (long long)ld_sa);
   const int64_t plan_groups = layout == kDense ? 1 : groups;
   Plan pl = make_gated_plan(layout, m, n, k, plan_groups, num_cus, layout != kContiguous && ws != nullptr);
   if (pl.splits > 1 && ws_bytes < pl.ws_bytes) pl = make_gated_plan(layout, m, n, k, plan_groups, num_cus, false);

@@ -69,7 +69,7 @@ __global__ __launch_bounds__(norm_threads<LT>()) void residual_norm_kernel(NormP
   __shared__ float red_x[kWaves][1], red_s[kWaves][1];
   __shared__ uint32_t red_max[kWaves];
   const int tid = threadIdx.x % LT;
-  const int64_t row = (int64_t)blockIdx.x * norm_rows<LT>() + threadIdx.x / LT;
+  const int64_t row = (blockIdx.x + (int64_t)gridDim.x * blockIdx.y) * norm_rows<LT>() + threadIdx.x / LT;
   if (row >= p.rows) return;   // uniform over the row's waves, which share no barrier with another row's
   const int64_t base = row * p.hidden;
   const T* x = static_cast<const T*>(p.x);
@@ -322,7 +322,7 @@ __global__ __launch_bounds__(norm_threads<LT>()) void residual_norm_grad_kernel(
       const int64_t e = (segment + 1) * p.rows_per_gate;
       piece_end = e < end ? e : end;
     }
-      // rows of the piece in steps of kRows: every row group runs its own (they share barriers only in flush)
+    // rows of the piece in steps of kRows: every row group runs its own (they share barriers only in flush)
     const bool gated = p.gate != nullptr;
     const T* gate = static_cast<const T*>(p.gate);
     if (HASX && !(gated && each_row)) {
@@ -582,7 +582,8 @@ int launch_residual_norm(int out, const void* x, const void* residual, int dtype
                                     : (wide ? norm_fn_of<_Float16, float>(out, lt, v) : norm_fn_of<_Float16, _Float16>(out, lt, v));
   const int threads = lt > kNormThreads ? lt : kNormThreads, per_wg = lt >= kNormThreads ? 1 : kNormThreads / lt;
   void* args[] = {&p};
-  const hipError_t e = hipLaunchKernel(fn, dim3((unsigned)((rows + per_wg - 1) / per_wg)), dim3(threads), args, 0, stream);
+  const int64_t blocks = (rows + per_wg - 1) / per_wg, gx = blocks < kGridRow ? blocks : kGridRow;
+  const hipError_t e = hipLaunchKernel(fn, dim3((unsigned)gx, (unsigned)((blocks + gx - 1) / gx)), dim3(threads), args, 0, stream);
   return e == hipSuccess ? kOk : set_error(kHip, "residual_norm launch: %s", hipGetErrorString(e));
 }
 

@@ -33,6 +33,9 @@ __device__ __forceinline__ uint32_t pack2_f16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, f16x2_t{(_Float16)lo, (_Float16)hi});
 }
 
+// Workgroups of up to 1024 threads along x (a launch holds fewer than 2^32 threads there); more go along y.
+constexpr int64_t kGridRow = 1 << 21;
+
 // Eight consecutive elements as loaded: 16 bytes (32 for fp32), 16-byte aligned.
 template <class T>
 struct Raw8 { u32x4_t w; };

@@ -78,6 +78,21 @@ def test_gated_plans(lib, monkeypatch):
     assert dg.dg_gemm_fp8_gated_workspace_size(8, 128, 100) == 0 and dg.dg_gemm_fp8_gated_workspace_size(8, 128, 128, 0) == 0
 
 
+def test_gated_sizes_at_their_limits(lib):
+    """Scales whose offsets leave 32 bits are refused; one expert's workspace is that of either form."""
+    assert lib.dg_set_num_cus(256) == OK
+    out = (0, P, None, None, 0, None, 8, 64)
+    assert lib.dg_gemm_fp8_gated_nt(P, P, 1 << 29, P, P, *out, 128, None, 0, None) == UNSUPPORTED
+    assert lib.dg_gemm_fp8_gated_nt(P, P, 1 << 28, P, P, *out, 256, None, 0, None) == UNSUPPORTED
+    for m, n, k in ((8, 128, 4096), (40, 128, 4096), (100, 256, 2048), (256, 256, 7168)):
+        for layout in (0, 2):
+            name = dg.dg_gemm_fp8_gated_config_name(layout, m, n, k, 1)
+            splits = int(name.rsplit("split", 1)[1])
+            bn, bm = (int(v) for v in name.split("/")[0].removeprefix("stream").split("x"))
+            need = 65536 + -(-n // 128) * -(-m // bm) * splits * bn * bm * 4 if splits > 1 else 0
+            assert dg.dg_gemm_fp8_gated_workspace_size(m, n, k, 1) >= need
+
+
 def test_gated_binding_refusals():
     a, sa = torch.zeros((8, 128), dtype=torch.uint8), torch.zeros((1, 8))
     b, sb = torch.zeros((2, 64, 128), dtype=torch.uint8), torch.zeros((2, 1, 1))
@@ -202,7 +217,7 @@ def test_binding_refusals():
             bad()
     x = torch.zeros((6, 32), dtype=torch.bfloat16)
     w = torch.ones(32)
-    for bad in (lambda: dg.dg_residual_norm(x, x.half(), w), lambda: dg.dg_residual_norm(x, x[:5], w),
+    for bad in (lambda: dg.dg_residual_norm(x, x, w, dtype=torch.float16), lambda: dg.dg_residual_norm(x, x.half(), w), lambda: dg.dg_residual_norm(x, x[:5], w),
                 lambda: dg.dg_residual_norm(x, x, w.bfloat16()), lambda: dg.dg_residual_norm(x, x, w[:16]),
                 lambda: dg.dg_residual_norm(x, x, w, gate=torch.zeros((4, 32), dtype=torch.bfloat16)),
                 lambda: dg.dg_residual_norm(x, x, w, gate=w), lambda: dg.dg_residual_norm(x, x, w, post_weight=w),

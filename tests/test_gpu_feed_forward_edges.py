@@ -1,0 +1,194 @@
+"""The feed-forward operators where indexes and loops end: every length of K around the main loops' steps, more rows than a
+launch holds workgroups of along x, offsets past 32 bits, calls at once on two streams.
+
+Tolerances: those of the gated products' tests (64-bit arithmetic); elsewhere the same bits as the call on the rows alone.
+Random codes (test_gated_product_of_many_rows) have products of all sizes, for which 2^-14 of their magnitudes is no bound:
+a matrix instruction adds 8 neighbouring products at a time and keeps of each what reaches 2^-13 of the power of two below
+the largest (measured: beside 2^16 the product 2^3 counts, 2^2 does not, at the seven places next to it and at no
+other; 100 of them beside it lose 7).  So each loses less than min(|p|, 2^-13 max |p|), the largest nothing (8
+bits); the groups' sums and the promotion add less than 2^-19 of the magnitudes (16 sums of 24 bits)."""
+
+import numpy as np
+import pytest
+import torch
+
+import fp8_block_scaled_gemm_amd as dg
+from gpu_util import device, say
+from test_gpu_gated_gemm import OF, check_bf16, check_fp8, dequantized, operands, reference, same_bits
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+
+
+@pytest.mark.parametrize("tile", ["stream=16", "stream=64", "tile=256x128", "tile=256x256"])
+@pytest.mark.parametrize("k", [16, 128, 144, 384, 512, 528, 640, 768, 896, 1024, 1168])
+def test_every_length_of_k(tile, k, monkeypatch):
+    """One to ten K blocks, whole and partial, through rings of two, three, four and six blocks; several tiles a
+    workgroup (few CUs), so that a tile's end meets the next one's start."""
+    say("gated K", tile, k)
+    monkeypatch.setenv("DG_PLAN", f"{tile},splits=1")
+    rng = np.random.default_rng(k)
+    a, sa, b, sb = operands(rng, (300,), 272, k)
+    h, eh = reference(a, sa, 300, b, sb, "silu")[2::3]
+    dg.dg_set_num_cus(8)
+    try:
+        d = dg.dg_gemm_fp8_gated_nt(a, sa, b, sb)
+        q, s = dg.dg_gemm_fp8_gated_nt(a, sa, b, sb, out="fp8")
+    finally:
+        dg.dg_set_num_cus(256)
+    check_bf16(d, h, eh, "h")
+    check_fp8(q, s[:, :300].t(), h, eh, "fp8")
+
+
+@pytest.mark.parametrize("k", [128, 384, 512, 640, 896])
+def test_lengths_of_k_in_groups(k, monkeypatch):
+    """The same for the grouped forms on the 256x128 tile: contiguous, and masked with empty and full experts."""
+    say("gated K in groups", k)
+    monkeypatch.setenv("DG_PLAN", "tile=256x128")
+    rng = np.random.default_rng(k + 1)
+    a, sa, b, sb = operands(rng, (640,), 144, k, groups=3)
+    experts = [2, 0, -1, 0, 1]
+    mi = torch.tensor(experts, dtype=torch.int32, device=device()).repeat_interleave(128)
+    counts = [200, 0, 130]
+    masked = operands(rng, (3 * 256,), 144, k, groups=3)
+    am = masked[0].view(3, 256, k)
+    sm = masked[1][:, :768].view(-1, 3, 256).transpose(0, 1).contiguous()
+    dg.dg_set_num_cus(8)
+    try:
+        d = dg.dg_gemm_fp8_gated_contiguous(a, sa, b, sb, mi, d=torch.full((640, 144), 7.0, dtype=BF16, device=device()))
+        dm = dg.dg_gemm_fp8_gated_masked(am, sm, *masked[2:], torch.tensor(counts, dtype=torch.int32, device=device()),
+                                         d=torch.full((3, 256, 144), 7.0, dtype=BF16, device=device()), use_workspace=False)
+    finally:
+        dg.dg_set_num_cus(256)
+    for i, e in enumerate(experts):
+        rows = slice(128 * i, 128 * i + 128)
+        if e < 0:
+            assert torch.all(d[rows] == 7)
+        else:
+            h, eh = reference(a[rows], sa[:, rows], 128, b[e], sb[e], "silu")[2::3]
+            check_bf16(d[rows], h, eh, f"block {i}")
+    for g, c in enumerate(counts):
+        assert torch.all(dm[g, c:] == 7)
+        if c:
+            h, eh = reference(am[g, :c], sm[g, :, :c], c, masked[2][g], masked[3][g], "silu")[2::3]
+            check_bf16(dm[g, :c], h, eh, f"expert {g}")
+
+
+def wide_reference(a, sa, rows, b, sb):
+    """(h, tolerance) for codes of any sizes, SiLU."""
+    av, bv = dequantized(a, sa, rows, b, sb)
+    g, u, e = av @ bv[0].T, av @ bv[1].T, []
+    for w in bv:
+        p = np.abs(av[:, None, :] * w[None]).reshape(rows, w.shape[0], -1, 8)
+        cut = np.minimum(p, 2.0 ** -13 * p.max(-1, keepdims=True))
+        e.append((cut.sum(-1) - cut.max(-1)).sum(-1) + 2.0 ** -19 * p.sum((-1, -2)))
+    eg, eu = e
+    f = OF.act_value(g, "silu")
+    return f * u, 1.13 * eg * np.abs(u) + np.abs(f) * eu + 1.13 * eg * eu + (10 + 6 * np.abs(g)) * 2.0 ** -24 * np.abs(f * u)
+
+
+def spots(rows):
+    """Runs of rows at both ends and where 32-bit counts of elements and bytes would wrap."""
+    at = sorted({0, 1 << 21, 1 << 22, 1 << 23, 1 << 24, 1 << 25, 1 << 26, rows - 40})
+    return [slice(max(0, a - 24), a + 40) for a in at if a + 40 <= rows]
+
+
+def test_gated_product_of_many_rows():
+    """2^27 rows of 16: 2 GiB of activations, outputs past 2^32 bytes."""
+    m, n, k = (1 << 27) - 100, 32, 16
+    say("gated many rows", m, n, k)
+    d = device()
+    rng = np.random.default_rng(9)
+    _, _, b, sb = operands(rng, (8,), n, k)
+    gen = torch.Generator(device=d).manual_seed(11)
+    a = torch.randint(0, 0x70, (m, k), dtype=torch.uint8, device=d, generator=gen)
+    sa = torch.rand((1, m), device=d, generator=gen)
+    out = dg.dg_gemm_fp8_gated_nt(a, sa, b, sb)
+    for r in spots(m):
+        h, eh = wide_reference(a[r], sa[:, r], r.stop - r.start, b, sb)
+        check_bf16(out[r], h, eh, f"rows {r}")
+    del out
+    q, s = dg.dg_gemm_fp8_gated_nt(a, sa, b, sb, out="fp8")
+    for r in spots(m):
+        h, eh = wide_reference(a[r], sa[:, r], r.stop - r.start, b, sb)
+        check_fp8(q[r], s[:, r].t(), h, eh, f"rows {r}")
+
+
+def test_activation_of_many_rows():
+    rows, n = (1 << 26) + 48, 32
+    say("activation many rows", rows, n)
+    d = device()
+    pre = torch.randn((rows, 2 * n), device=d, dtype=BF16)
+    h, (q, s), (q8, s8) = dg.dg_gated_act(pre), dg.dg_gated_act_fp8(pre), dg.dg_gated_act_int8(pre)
+    for r in spots(rows):
+        same_bits(h[r], dg.dg_gated_act(pre[r].clone()))
+        want, ws = dg.dg_gated_act_fp8(pre[r].clone())
+        same_bits(q[r], want)
+        same_bits(s[:, r], ws[:, :want.shape[0]])
+        want, ws = dg.dg_gated_act_int8(pre[r].clone())
+        same_bits(q8[r].view(torch.uint8), want.view(torch.uint8))
+        same_bits(s8[r], ws)
+    del q, s, q8, s8
+    got = dg.dg_gated_act_grad(h, pre)
+    for r in spots(rows):
+        same_bits(got[r], dg.dg_gated_act_grad(h[r].clone(), pre[r].clone()))
+
+
+def test_norm_of_many_rows():
+    rows, hidden = (1 << 26) + 48, 32
+    say("norm many rows", rows, hidden)
+    d = device()
+    x, res = (torch.randn((rows, hidden), device=d, dtype=BF16) for _ in range(2))
+    total, y = dg.dg_residual_norm(x, res)
+    _, q, s = dg.dg_residual_norm_fp8(x, res)
+    _, q8, s8 = dg.dg_residual_norm_int8(x, res)
+    got = dg.dg_residual_norm_grad(y, res, x, total)
+    for r in spots(rows):
+        xr, rr = x[r].clone(), res[r].clone()
+        same_bits(total[r], dg.dg_residual_norm(xr, rr)[0])
+        same_bits(y[r], dg.dg_residual_norm(xr, rr)[1])
+        want = dg.dg_residual_norm_fp8(xr, rr)
+        same_bits(q[r], want[1])
+        same_bits(s[:, r], want[2][:, :xr.shape[0]])
+        want = dg.dg_residual_norm_int8(xr, rr)
+        same_bits(q8[r].view(torch.uint8), want[1].view(torch.uint8))
+        same_bits(s8[r], want[2])
+        want = dg.dg_residual_norm_grad(y[r].clone(), rr, xr, total[r].clone())
+        same_bits(got.dx[r], want.dx)
+        same_bits(got.dresidual[r], want.dresidual)
+
+
+def test_two_streams_at_once():
+    """K splits of one shape from two streams at once, each with its own default workspace, the calls in flight together."""
+    say("gated two streams")
+    rng = np.random.default_rng(8)
+    cases = [operands(rng, (m,), 256, 4096) for m in (1, 1, 60, 100)]
+    want = [dg.dg_gemm_fp8_gated_nt(*c) for c in cases]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(8):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append([dg.dg_gemm_fp8_gated_nt(*c) for c in (cases if i else cases[::-1])])
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        for outs in got[i]:
+            for x, y in zip(outs, want if i else want[::-1]):
+                same_bits(x, y)
+
+
+def test_one_expert():
+    """The masked form of one expert gets the workspace that its plan asks for."""
+    say("gated one expert")
+    rng = np.random.default_rng(7)
+    a, sa, b, sb = operands(rng, (40,), 128, 4096)
+    need = dg.dg_gemm_fp8_gated_workspace_size(40, 128, 4096, 1)
+    assert not dg.dg_gemm_fp8_gated_config_name(2, 40, 128, 4096, 1).endswith("split1")
+    ws = torch.zeros(need, dtype=torch.uint8, device=device())
+    count = torch.tensor([37], dtype=torch.int32, device=device())
+    d = dg.dg_gemm_fp8_gated_masked(a[None], sa[None], b[None], sb[None], count, workspace=ws)
+    h, eh = reference(a[:37], sa, 37, b, sb, "silu")[2::3]
+    check_bf16(d[0, :37], h, eh, "h")
+    assert torch.all(ws[:65536] == 0)
