@@ -69,10 +69,10 @@ __global__ __launch_bounds__(kActThreads) void gated_act_kernel(GatedActParams p
       if (col >= p.n)
 #pragma unroll
         for (int c = 0; c < 8; ++c) h[c] = 0.0f;
-      const float s = group16_scale(h);
+      const GroupScale s = group16_scale(h);
       if (col < p.n) {
         *reinterpret_cast<u32x2_t*>(static_cast<uint8_t*>(p.h) + row * p.n + col) = pack8_e4m3(h, s);
-        if (lane == 0) p.scales[((int64_t)group * ((p.n + kGroup - 1) / kGroup) + col / kGroup) * p.ld_s + in_group] = s;
+        if (lane == 0) p.scales[((int64_t)group * ((p.n + kGroup - 1) / kGroup) + col / kGroup) * p.ld_s + in_group] = s.d.s;
       }
     } else if (col < p.n) {
       store8(static_cast<T*>(p.h) + row * p.n + col, narrow8<T>(h));
@@ -240,8 +240,8 @@ __global__ __launch_bounds__(kGradThreads) void gated_act_grad_fp8_kernel(ActGra
       v4f scales;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float s = group16_scale(v[i]);
-        scales[i] = s;
+        const GroupScale s = group16_scale(v[i]);
+        scales[i] = s.d.s;
         if (there)
           *reinterpret_cast<u32x2_t*>(p.q + (row + i) * 2 * p.n + half * p.n + col) = pack8_e4m3(v[i], s);
       }
@@ -269,11 +269,10 @@ __global__ __launch_bounds__(kGradThreads) void gated_act_grad_fp8_kernel(ActGra
       float a = s_max[0][tid];
 #pragma unroll
       for (int w = 1; w < kGradThreads / 64; ++w) a = fmaxf(a, s_max[w][tid]);
-      const float s = a == 0.0f ? 1.0f : a / kE4M3Max;
-      s_scale[tid] = divisor(s);
-      const bool plain = __all(scale_in_range(s));
-      if ((tid & 63) == 0) s_plain[tid >> 6] = plain;
-      sc[(int64_t)blockIdx.y * ld + col0 + tid] = s;
+      const GroupScale s = group_scale(a);
+      s_scale[tid] = s.d;
+      if ((tid & 63) == 0) s_plain[tid >> 6] = s.plain;
+      sc[(int64_t)blockIdx.y * ld + col0 + tid] = s.d.s;
     }
     __syncthreads();
     auto turn = [&](auto plain) {

@@ -67,9 +67,9 @@ __device__ __forceinline__ void gated_piece(const GemmParams& p, int64_t out_row
   if (count <= 0)   // columns past n take no part (n % 16 == 0: all eight or none)
 #pragma unroll
     for (int c = 0; c < 8; ++c) h[c] = 0.0f;
-  const float s = group16_scale(h);
+  const GroupScale s = group16_scale(h);
   if (count > 0) *reinterpret_cast<u32x2_t*>(p.q + out_row * p.n + col) = pack8_e4m3(h, s);
-  if (lane16 == 0) *scale_at = s;
+  if (lane16 == 0) *scale_at = s.d.s;
 }
 
 // The rows of a tile of 128 columns of h, a loop of few instructions (written out for every fragment, the epilogue is tens

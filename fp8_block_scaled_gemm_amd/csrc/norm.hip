@@ -162,10 +162,10 @@ __global__ __launch_bounds__(norm_threads<LT>()) void residual_norm_kernel(NormP
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       // a group of 128 is the pieces of 16 neighbouring lanes; a partial last one holds zeros past the row
-      const float scale = group16_scale(s[i]);
+      const GroupScale scale = group16_scale(s[i]);
       if (ok[i]) {
         *reinterpret_cast<u32x2_t*>(q + at[i]) = pack8_e4m3(s[i], scale);
-        if ((tid & 15) == 0) p.scales[(int64_t)(at[i] / kGroup) * p.ld_s + row] = scale;
+        if ((tid & 15) == 0) p.scales[(int64_t)(at[i] / kGroup) * p.ld_s + row] = scale.d.s;
       }
     }
   } else {

@@ -151,14 +151,6 @@ __device__ __forceinline__ float wave_sum(float v) {
 // infinity, so a maximum over them keeps a NaN.
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
-// E4M3 scale of a 128-element group held as 8 values by each of 16 neighbouring lanes, by the rule of the per-token-group quantizer: amax / 448, 1 for an all-zero group.
-__device__ __forceinline__ float group16_scale(const float* v) {
-  float amax = fabsf(v[0]);
-#pragma unroll
-  for (int c = 1; c < 8; ++c) amax = fmaxf(amax, fabsf(v[c]));
-  amax = row16_max(amax);
-  return amax == 0.0f ? 1.0f : amax / kE4M3Max;
-}
 // Quotients by one scale: x r corrected by its exact remainder, r = 1 / s rounded.  They are the IEEE quotients wherever that
 // decides a code: the correction's error is below 2^-24 of a last place, so only a quotient that close to the middle of
 // two fp32 numbers could round otherwise, and a code needs that middle to lie beside a middle of two codes.
@@ -166,8 +158,35 @@ __device__ __forceinline__ float group16_scale(const float* v) {
 // 127).  Scales outside [2^-60, 2^60], where the remainder may not be exact, take the division itself; above that a
 // quotient whose remainder is not exact is below 2^-40, code 0.  Three instructions a value instead of ten.
 struct Divisor { float s, r; };
-__device__ __forceinline__ Divisor divisor(float s) { return Divisor{s, 1.0f / s}; }
 __device__ __forceinline__ bool scale_in_range(float s) { return __float_as_uint(s) - 0x21800000u <= 0x3c000000u; }
+
+// An E4M3 scale by the rule of the per-token-group quantizer, amax / 448, 1 for an all-zero group, and its reciprocal, both
+// with the bits of IEEE divisions: a product by 1 / 448, and the hardware's reciprocal, each corrected by its exact
+// remainder (compared with the divisions for every number from 2^-60 to 2^70 on the device); the divisions themselves
+// where a scale of the wave lies outside [2^-60, 2^60].  Seven instructions instead of twenty.
+struct GroupScale {
+  Divisor d;
+  bool plain;   // every active lane's scale lies in the range: quotient<true> serves
+};
+__device__ __forceinline__ GroupScale group_scale(float amax) {
+  constexpr float kInv = 1.0f / kE4M3Max;
+  const float q = amax * kInv;
+  float s = __builtin_fmaf(__builtin_fmaf(-kE4M3Max, q, amax), kInv, q);
+  s = amax == 0.0f ? 1.0f : s;
+  if (__all(scale_in_range(s))) {
+    const float r = __builtin_amdgcn_rcpf(s);
+    return {{s, __builtin_fmaf(__builtin_fmaf(-s, r, 1.0f), r, r)}, true};
+  }
+  s = amax == 0.0f ? 1.0f : amax / kE4M3Max;
+  return {{s, 1.0f / s}, false};
+}
+// That of a 128-element group held as 8 values by each of 16 neighbouring lanes.
+__device__ __forceinline__ GroupScale group16_scale(const float* v) {
+  float amax = fabsf(v[0]);
+#pragma unroll
+  for (int c = 1; c < 8; ++c) amax = fmaxf(amax, fabsf(v[c]));
+  return group_scale(row16_max(amax));
+}
 template <bool PLAIN>
 __device__ __forceinline__ float quotient(float x, Divisor d) {
   if constexpr (!PLAIN) return x / d.s;
@@ -181,16 +200,14 @@ __device__ __forceinline__ uint32_t codes4_e4m3(float a, float b, float c, float
   const int w = __builtin_amdgcn_cvt_pk_fp8_f32(sat(a), sat(b), 0, false);
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(sat(c), sat(d), w, true);
 }
-// The E4M3 codes of eight values over their group's scale, packed little-endian (every lane of the wave that is active
-// takes part; the result is that of IEEE divisions).
-__device__ __forceinline__ u32x2_t pack8_e4m3(const float* v, float s) {
-  const Divisor d = divisor(s);
+// The E4M3 codes of eight values over their group's scale, packed little-endian: the result of IEEE divisions.
+__device__ __forceinline__ u32x2_t pack8_e4m3(const float* v, const GroupScale& g) {
   auto codes = [&](auto plain) {
     constexpr bool P = decltype(plain)::value;
-    return u32x2_t{codes4_e4m3(quotient<P>(v[0], d), quotient<P>(v[1], d), quotient<P>(v[2], d), quotient<P>(v[3], d)),
-                   codes4_e4m3(quotient<P>(v[4], d), quotient<P>(v[5], d), quotient<P>(v[6], d), quotient<P>(v[7], d))};
+    return u32x2_t{codes4_e4m3(quotient<P>(v[0], g.d), quotient<P>(v[1], g.d), quotient<P>(v[2], g.d), quotient<P>(v[3], g.d)),
+                   codes4_e4m3(quotient<P>(v[4], g.d), quotient<P>(v[5], g.d), quotient<P>(v[6], g.d), quotient<P>(v[7], g.d))};
   };
-  if (__all(scale_in_range(s))) return codes(std::true_type{});
+  if (g.plain) return codes(std::true_type{});
   return codes(std::false_type{});
 }
 
