@@ -192,3 +192,46 @@ def test_one_expert():
     h, eh = reference(a[:37], sa, 37, b, sb, "silu")[2::3]
     check_bf16(d[0, :37], h, eh, "h")
     assert torch.all(ws[:65536] == 0)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("dtype", [torch.float32, BF16])
+@pytest.mark.parametrize("rows,n", [(1024, 2048), (1040, 2048), (1168, 1792)])
+def test_act_grad_fp8_of_many_tiles(rows, n, act, dtype):
+    """Both sides of the number of tiles up to which four workgroups share one: the bits of the fp32 gradient followed by the
+    library's quantizers, with values whose scales lie far from 1 on both sides, and one that is infinite."""
+    say("act grad fp8", rows, n, act, dtype)
+    g = torch.Generator(device=device()).manual_seed(rows + n)
+    pre = (torch.randn((rows, 2 * n), generator=g, device=device()) * 1.5).to(dtype)
+    dh = torch.randn((rows, n), generator=g, device=device()).to(dtype)
+    dh[7] *= 2.0 ** -70
+    dh[:, 300:420] *= 2.0 ** -80
+    dh[200:330, 130] *= 2.0 ** 100
+    dh[900, 1000] = float("inf")
+    wide = dg.dg_gated_act_grad(dh.float(), pre.float(), act=act)
+    h = dg.dg_gated_act(pre.float(), act=act)
+    got = dg.dg_gated_act_grad_fp8(dh, pre, act=act)
+    want = (*dg.dg_quantize_per_token_group(wide), *dg.dg_quantize_per_channel_group(wide),
+            *dg.dg_quantize_per_channel_group(h))
+    for i, (a, b) in enumerate(zip(got, want)):
+        b = b[..., :a.shape[-1]]
+        assert torch.equal(torch.isnan(a.float()), torch.isnan(b.float()))
+        a, b = a.clone(), b.clone()
+        if a.dtype == torch.float32:   # (any NaN is one)
+            a[torch.isnan(a)] = b[torch.isnan(b)] = 0.0
+        same_bits(a, b, f"output {i}")
+
+
+@pytest.mark.parametrize("power", [-140, -120, -100, -59, -52, 0, 40, 66, 70, 100, 118])
+def test_scales_of_every_size(power):
+    """Groups whose scales are subnormal, at the borders of the range that products serve, and next to fp32's largest."""
+    say("scales", power)
+    g = torch.Generator(device=device()).manual_seed(power + 200)
+    x = torch.randn((64, 1024), generator=g, device=device())
+    pre = torch.cat([torch.full((64, 1024), 30.0, device=device()), x * 2.0 ** (power / 2) * 2.0 ** (power / 2)], 1)
+    pre[:, 2000:2040] = 0
+    h = dg.dg_gated_act(pre)
+    q, s = dg.dg_gated_act_fp8(pre)
+    want, ws = dg.dg_quantize_per_token_group(h)
+    same_bits(q, want)
+    same_bits(s[:, :64], ws[:, :64])
