@@ -13,6 +13,9 @@
 // in the order of the splits, end the rows: taken by a second launch, or, of few bytes, by the last workgroup of a tile to
 // arrive (the hand-off of the plain forms).  A CU takes some 30 bytes a nanosecond from memory, so the last workgroup alone
 // is the slower the more there is to add, while a launch costs 3 us whatever it does.
+// Bound by what a CU takes from memory, and for one token by the latencies of one pass: 1 x 2048 x 7168, 14 splits, 11.6 us
+// (29 MB; 5.9 us at the rate of a copy); 777 x 1057 x 1552 in 117 tiles of 64 rows on 256 CUs 18 us; 64 x 2048
+// x 7168 in 8 splits 22 us.  Tiles of 128 and 256 rows were no faster than the large tiles.
 #include <type_traits>
 
 #include "gemm_common.hpp"

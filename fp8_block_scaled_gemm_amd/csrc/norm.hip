@@ -7,7 +7,9 @@
 //   du = ds + rho * (dy w - s rho^2 mean(dy w s)),  rho = rsqrt(mean(s^2) + eps)       -> dr = du
 //   dz = scale * gate * du,  dgate = scale * sum(z du),  dw = sum(dy s rho)
 //   dx = sigma * (dz v - x sigma^2 mean(dz v x)),  sigma = rsqrt(mean(x^2) + eps),  dv = sum(dz x sigma)
-// Bound by memory: a row is read once into registers, its sums of squares are reduced there.
+// Bound by memory: a row is read once into registers, its sums of squares are reduced there, so that every input passes
+// once and every output once (4096 x 7168 bf16 over an fp32 stream, to FP8: 66 us, 332 MB at 5.0 TB/s, what a copy
+// reaches; 8191 x 2048 bf16: 27 us).  One row alone is the latency of two loads and a reduction, 3.3 us.
 #include "rows.hpp"
 
 namespace dg {
@@ -62,7 +64,7 @@ constexpr int norm_threads() { return LT > kNormThreads ? LT : kNormThreads; }
 template <int LT>
 constexpr int norm_rows() { return LT >= kNormThreads ? 1 : kNormThreads / LT; }
 
-// LT lanes a row, V pieces of 8 elements a lane.
+// LT lanes a row, V pieces of 8 elements a lane: at most two, so that enough rows are in flight on a CU.
 template <class T, class TR, int OUT, int LT, int V>
 __global__ __launch_bounds__(norm_threads<LT>()) void residual_norm_kernel(NormParams p) {
   constexpr int kWaves = LT / 64;
@@ -216,6 +218,8 @@ struct NormGradParams {
 // of the workgroups: no atomics, the same bits from run to run.  A gate's rows ("segment") may end inside the
 // workgroup's range: a segment that lies in it whole is written at once; a piece of one that does not goes to
 // slot 0 where the range begins inside the segment, or with it, and to slot 1 where the segment begins later.
+// Bound by memory: 8191 x 2048 bf16 with a gate 41 us (220 MB at 5.3 TB/s), 16064 x 1536 fp16 over an fp32 stream with 64
+// gates 97 us (4.6 TB/s), and 6 and 9 us for the sums of the partials.
 // Absent weights, gates and norms are ones and scales of 1 rather than branches (those took 190 registers where 110 do).
 template <class T, class TR, bool HASX, int LT, int V>
 __global__ __launch_bounds__(norm_threads<LT>()) void residual_norm_grad_kernel(NormGradParams p) {

@@ -5,7 +5,8 @@
  * fine-grained scaling and two-level (promoted) FP32 accumulation, in three
  * forms - a normal GEMM, a contiguous-grouped MoE GEMM and a masked-grouped
  * MoE GEMM.  Beside them (end of this file): expert routing, the expert row
- * layout with dispatch and combine, and the three forms in 8-bit integers.
+ * layout with dispatch and combine, the three forms in 8-bit integers, and the
+ * gated feed-forward product, activation and residual norms.
  * Sources (DeepGEMM news/blog pages):
  *   - 机器之心 DeepGEMM report, opening section: fine-grained scaling as in
  *     DeepSeek-V3; normal and MoE grouped GEMMs; two-level accumulation on
@@ -669,7 +670,9 @@ const char* dg_gemm_int8_config_name(int layout, int64_t m, int64_t n, int64_t k
  * The 8-bit integer GEMMs take "tile=256x256" or "tile=128x128", or "strip=32", 64, 96 or 128 (rows of the
  * weights; the normal and masked forms of at most 1024 rows, 96 of at most 64), and "splits=S" likewise; their
  * results stay the same bits.
- * dg_gemm_config_name and dg_gemm_workspace_size (dg_gemm_int8_...) report the overridden plan; results stay within
+ * The gated FP8 GEMMs take "tile=256x128" or "tile=256x256", or "stream=16" or 64 (rows of the streaming kernel's
+ * tile; not the contiguous form), and "splits=S", to 32 for the streaming kernel.
+ * dg_gemm_config_name and dg_gemm_workspace_size (dg_gemm_int8_..., dg_gemm_fp8_gated_...) report the overridden plan; results stay within
  * the GEMM tolerance (a different K split changes the fp32 summation order).  For measuring the
  * alternatives the planner weighs, not for production use.
  */
