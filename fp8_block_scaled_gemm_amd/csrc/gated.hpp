@@ -9,22 +9,12 @@ namespace dg {
 // Values of enum dg_act (include/dg.h).
 enum Act : int { kSilu = 0, kGelu = 1 };
 
-// exp(-a) for a >= 0: 2^-(hi + lo), hi + lo = a log2(e) to twice fp32's bits (rounding a log2(e) alone would cost
-// 2^-18 of the result at a = 88); within 3 * 2^-24 of its value, 0 below 2^-126; a NaN stays one.
-__device__ __forceinline__ float exp_neg(float a) {
-  constexpr float kLog2e = 1.44269502f, kLog2eLo = 1.92596299e-8f, kLn2 = 0.693147181f;
-  const float hi = a * kLog2e;
-  const float lo = __builtin_fmaf(a, kLog2eLo, __builtin_fmaf(a, kLog2e, -hi));
-  const float e = __builtin_amdgcn_exp2f(-hi);
-  return hi > 126.0f ? 0.0f : __builtin_fmaf(-lo * kLn2, e, e);
-}
-
-// sigmoid(z) and 1 - sigmoid(z), both to full relative precision (the hardware's reciprocal: within 2 * 2^-24).
-__device__ __forceinline__ void sigmoid2(float z, float& p, float& rest) {
-  const float e = exp_neg(fabsf(z));
-  const float r = __builtin_amdgcn_rcpf(1.0f + e), er = e * r;
-  p = z >= 0.0f ? r : er;
-  rest = z >= 0.0f ? er : r;
+// e = exp(-z) and p = sigmoid(z) = 1 / (1 + e), by the hardware's exponential and reciprocal (each within 2 * 2^-24).  The
+// rounded argument -z log2(e) makes that (1.5 |z| + 2) 2^-24 of e, so p lies within (1.5 |z| + 6) 2^-24 of its value where
+// z < 0, and closer above.  p is 0 where it lies below 2^-126, e is then infinite; a NaN stays one.
+__device__ __forceinline__ float sigmoid(float z, float& e) {
+  e = __builtin_amdgcn_exp2f(z * -1.44269502f);
+  return __builtin_amdgcn_rcpf(1.0f + e);
 }
 
 constexpr float kGeluRoot = 1.59576912f;   // 2 sqrt(2 / pi): 0.5 (1 + tanh(y)) = sigmoid(2 y)
@@ -38,18 +28,18 @@ __device__ __forceinline__ float act_arg(float g) {
 // g sigmoid(g), or the tanh form of GELU.
 template <int ACT>
 __device__ __forceinline__ float act_value(float g) {
-  float p, rest;
-  sigmoid2(act_arg<ACT>(g), p, rest);
-  return g * p;
+  float e;
+  return g * sigmoid(act_arg<ACT>(g), e);
 }
 
-// Value and slope: p + g p (1 - p) dz/dg (the second term is 0, not a product with an infinity, where p (1 - p) is).
+// Value and slope: p + g p (1 - p) dz/dg, 1 - p = e p where that is small (the second term is 0, not a product with an
+// infinity, where p (1 - p) is).
 template <int ACT>
 __device__ __forceinline__ void act_both(float g, float& value, float& slope) {
-  float p, rest;
-  sigmoid2(act_arg<ACT>(g), p, rest);
+  float e;
+  const float z = act_arg<ACT>(g), p = sigmoid(z, e);
   value = g * p;
-  const float q = p * rest;
+  const float q = p * (z >= 0.0f ? e * p : 1.0f - p);
   const float dz = ACT == kSilu ? 1.0f : kGeluRoot * __builtin_fmaf(3.0f * kGeluCube * g, g, 1.0f);
   slope = q == 0.0f ? p : __builtin_fmaf(g * q, dz, p);
 }

@@ -42,7 +42,7 @@ __device__ __forceinline__ void gated_values(const float* g, const float* u, flo
 constexpr int kActThreads = 256;
 
 // h in the type of pre, or E4M3 codes with a scale per 128: 16 lanes a group of 128, 16 rows a workgroup, G groups of a
-// row each, whose loads are in flight together (8192 x 2048 bf16 to FP8 17.9 us, 84 MB at 4.7 TB/s; 32 groups of 256 rows
+// row each, whose loads are in flight together (8192 x 2048 bf16 to FP8 15.1 us, 84 MB at 5.6 TB/s; 32 groups of 256 rows
 // with half of them in use 12.3 us, of which a launch of workgroups that find nothing to do is 3 to 4).
 template <class T, int ACT, bool FP8, int G>
 __global__ __launch_bounds__(kActThreads) void gated_act_kernel(GatedActParams p) {
@@ -176,8 +176,8 @@ __global__ __launch_bounds__(kActThreads) void gated_act_grad_kernel(const T* __
 // A row's 128 columns are the pieces of 16 neighbouring lanes, whose maximum is a row scale; a column's 128 rows are the 32
 // threads 16 apart, reduced over the 4 lanes of a wave and then over the 8 waves through LDS.  Codes of columns are
 // turned in LDS, one matrix after the other, so that stores are 128-byte runs.  Every input is read once, every output
-// written once.  8192 x 2048 bf16: 49.6 us where a copy of its 185 MB takes 37; the vector instructions, 80 for each g, u and
-// dh (28 the activation and its slope, 25 the five codes), are busy for most of it.
+// written once.  8192 x 2048 bf16: 48 us where a copy of its 185 MB takes 37; the vector instructions, 75 for each g, u and
+// dh (22 the activation and its slope, 25 the five codes), are busy for most of it.
 struct ActGradFp8Params {
   const void* dh;
   const void* pre;

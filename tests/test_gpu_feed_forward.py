@@ -2,9 +2,9 @@
 
 Tolerances, from the arithmetic (eps = 2^-24, half a step of fp32):
 
-* act(g) u: the exponential is within 3 eps of its value at its argument, 1 + e, the quotient and three products add one
-  each, and an argument z that is rounded itself (GELU: 4 operations) changes the exponential by 4 eps |z|; below
-  (10 + 6 |z|) eps of the value.  A slope is a sum of two such terms and is held to their magnitudes.
+* act(g) u: the exponential of the rounded product z log2(e) is within (2 + 1.5 |z|) eps of its value, 1 + e, the reciprocal
+  and three products add one or two each, and an argument z that is rounded itself (GELU: 4 operations) changes the exponential by
+  4 eps |z|; below (10 + 6 |z|) eps of the value.  A slope is a sum of two such terms and is held to their magnitudes.
 * norms: a lane adds at most 16 squares, then 10 additions join lanes and waves; the square root halves that, five more
   operations follow, and the second norm inherits the first's error: below 80 eps of the magnitudes of the terms that
   are added (|residual| + |scale gate z| for the sum).
