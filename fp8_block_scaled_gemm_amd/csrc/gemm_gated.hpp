@@ -45,7 +45,11 @@ __device__ __forceinline__ void gated_piece(const GemmParams& p, int64_t out_row
   auto store = [&](uint16_t* dst, const float* v) {
     const uint32_t w[4] = {pack2_bf16_rne(v[0], v[1]), pack2_bf16_rne(v[2], v[3]), pack2_bf16_rne(v[4], v[5]),
                            pack2_bf16_rne(v[6], v[7])};
-    store_bf16_run(dst, w, count, lane16);
+    if ((p.n & 7) == 0) {   // every run of eight is 16-byte aligned, and there or not there as a whole
+      if (count > 0) *reinterpret_cast<u32x4*>(dst) = u32x4{w[0], w[1], w[2], w[3]};
+    } else {
+      store_bf16_run(dst, w, count, lane16);
+    }
   };
   if (p.pre != nullptr) {
     uint16_t* dst = p.pre + out_row * 2 * p.n + col;
