@@ -71,7 +71,8 @@ __global__ __launch_bounds__(norm_threads<LT>()) void residual_norm_kernel(NormP
   __shared__ float red_x[kWaves][1], red_s[kWaves][1];
   __shared__ uint32_t red_max[kWaves];
   const int tid = threadIdx.x % LT;
-  const int64_t row = (blockIdx.x + (int64_t)gridDim.x * blockIdx.y) * norm_rows<LT>() + threadIdx.x / LT;
+  const int64_t row = (blockIdx.x + (int64_t)gridDim.x * blockIdx.y) * norm_rows<LT>() +
+                      __builtin_amdgcn_readfirstlane(threadIdx.x / LT);
   if (row >= p.rows) return;   // uniform over the row's waves, which share no barrier with another row's
   const int64_t base = row * p.hidden;
   const T* x = static_cast<const T*>(p.x);
@@ -213,26 +214,33 @@ struct NormGradParams {
   float scale, eps;
 };
 
+// What a norm's backward pass has to do beside the second norm's.
+enum NormGradKind : int { kNormAlone = 0, kNormWithX = 1, kNormGateRows = 2 };   // no x; x; x and a gate for every row
+
 // A workgroup takes p.rows_per_part consecutive rows, its row groups (of LT lanes) every norm_rows-th of them, and holds
 // the columns' sums in registers.  They end in `part` (one row a workgroup), added by norm_grad_sum_kernel in the order
 // of the workgroups: no atomics, the same bits from run to run.  A gate's rows ("segment") may end inside the
 // workgroup's range: a segment that lies in it whole is written at once; a piece of one that does not goes to
 // slot 0 where the range begins inside the segment, or with it, and to slot 1 where the segment begins later.
+// One sum of a piece serves two gradients: with a = sum(scale du x sigma) over its rows, dgate is v a and dv gets gate a
+// (held in LDS from piece to piece).  Absent weights, gates and norms are ones and scales of 1 rather than branches (those
+// took 190 registers where 110 do).
 // Bound by memory: 8191 x 2048 bf16 with a gate 41 us (220 MB at 5.3 TB/s), 16064 x 1536 fp16 over an fp32 stream with 64
 // gates 97 us (4.6 TB/s), and 6 and 9 us for the sums of the partials.
-// Absent weights, gates and norms are ones and scales of 1 rather than branches (those took 190 registers where 110 do).
-template <class T, class TR, bool HASX, int LT, int V>
-__global__ __launch_bounds__(norm_threads<LT>()) void residual_norm_grad_kernel(NormGradParams p) {
+template <class T, class TR, int KIND, int LT, int V>
+__global__ __launch_bounds__(norm_threads<LT>(), V == 1 ? 3 : 2) void residual_norm_grad_kernel(NormGradParams p) {
+  constexpr bool HASX = KIND != kNormAlone, GATES = KIND == kNormGateRows;
   constexpr int kWaves = LT / 64, kRows = norm_rows<LT>();
   __shared__ float red_a[kWaves][3], red_b[kWaves][1];
   __shared__ float cols[kRows > 1 ? kRows : 1][kRows > 1 ? 8 * LT * V : 1];
-  const int tid = threadIdx.x % LT, group = threadIdx.x / LT;
+  __shared__ v4f s_dv[HASX ? kRows : 1][HASX ? 2 * V : 1][HASX ? LT : 1];
+  // (a row group is whole waves: with its number in a scalar register the loop over its rows has no lane leave it alone)
+  const int tid = threadIdx.x % LT, group = __builtin_amdgcn_readfirstlane(threadIdx.x / LT);
   const int64_t first = (int64_t)blockIdx.x * p.rows_per_part;
   const int64_t end = first + p.rows_per_part < p.rows ? first + p.rows_per_part : p.rows;
-  const bool each_row = p.rows_per_gate == 1;   // a gate for every row: its gradient is no sum
-  const bool gate_sums = p.dgate != nullptr && !each_row;
+  const bool gate_sums = !GATES && p.dgate != nullptr;
   constexpr int VX = HASX ? V : 1;
-  float dw[V][8], dv[VX][8], dgs[VX][8];
+  float dw[V][8], sum[VX][8];
   int at[V];
   bool ok[V];
 #pragma unroll
@@ -242,63 +250,82 @@ __global__ __launch_bounds__(norm_threads<LT>()) void residual_norm_grad_kernel(
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
       dw[i][c] = 0.0f;
-      if constexpr (HASX) dv[i][c] = dgs[i][c] = 0.0f;
+      if constexpr (HASX) sum[i][c] = 0.0f;
     }
+    if constexpr (HASX) s_dv[group][2 * i][tid] = s_dv[group][2 * i + 1][tid] = v4f{0.f, 0.f, 0.f, 0.f};
   }
   struct Row {
     Raw8<TR> u[V], ds[V];
-    Raw8<T> dy[V], x[VX];
+    Raw8<T> dy[V], x[VX], g[GATES ? V : 1];
   };
-  auto load_row = [&](int64_t row, Row& r) {
+  Row cur;
+  // (an absent piece loads the row's first one: the loads stand in no branch)
+  auto load_row = [&](int64_t row) {   // all but x
     const int64_t base = row * p.hidden;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (ok[i]) {
-        r.u[i] = load8(static_cast<const TR*>(p.sum) + base + at[i]);
-        r.dy[i] = load8(static_cast<const T*>(p.dy) + base + at[i]);
-        if (p.dsum != nullptr) r.ds[i] = load8(static_cast<const TR*>(p.dsum) + base + at[i]);
-        if constexpr (HASX) r.x[i] = load8(static_cast<const T*>(p.x) + base + at[i]);
-      }
-  };
-  // weights and a piece's gate stay in registers where these suffice (4096 x 7168: 126 us, 133 with loads for every row), and are
-  // loaded piece by piece for rows of more than 8192
-  constexpr bool kHold = V <= 2;
-  constexpr int H = kHold ? V : 1;
-  const bool normed = p.post_norm, weighted = p.post_weight != nullptr;
-  float held_w[H][8], held_v[H][8], held_g[H][8];
-  auto hold = [&](const auto* src, bool there, float (*to)[8]) {
-    if constexpr (kHold) {
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (there && ok[i]) {
-          widen8(load8(src + at[i]), to[i]);
-        } else {
-#pragma unroll
-          for (int c = 0; c < 8; ++c) to[i][c] = 1.0f;
-        }
+    for (int i = 0; i < V; ++i) {
+      const int64_t from = base + (ok[i] ? at[i] : 0);
+      cur.u[i] = load8(static_cast<const TR*>(p.sum) + from);
+      cur.dy[i] = load8(static_cast<const T*>(p.dy) + from);
+      if (p.dsum != nullptr) cur.ds[i] = load8(static_cast<const TR*>(p.dsum) + from);
+      if constexpr (GATES) cur.g[i] = load8(static_cast<const T*>(p.gate) + from);
     }
   };
-  auto columns = [&](const auto* src, bool there, const float (*held)[8], int i, float* to) {
-    if constexpr (kHold) {
+  auto load_x = [&](int64_t row) {
+    if constexpr (HASX)
 #pragma unroll
-      for (int c = 0; c < 8; ++c) to[c] = held[i][c];
-    } else if (there) {
+      for (int i = 0; i < V; ++i) cur.x[i] = load8(static_cast<const T*>(p.x) + row * p.hidden + (ok[i] ? at[i] : 0));
+  };
+  const bool normed = p.post_norm;
+  auto columns = [&](const auto* src, int i, float* to) {   // of a weight or gate, ones where there is none
+    if (src != nullptr && ok[i]) {
       widen8(load8(src + at[i]), to);
     } else {
 #pragma unroll
       for (int c = 0; c < 8; ++c) to[c] = 1.0f;
     }
   };
-  hold(p.weight, p.weight != nullptr, held_w);
-  if constexpr (HASX) hold(p.post_weight, weighted, held_v);
+  // weight, and post_weight times the piece's gate (a gate for every row: post_weight), held where the registers suffice, and
+  // loaded piece by piece for rows of more than 8192
+  constexpr bool kHold = V <= 2;
+  const T* gate = nullptr;   // of the piece
+  auto gated_weight = [&](int i, float* to) {
+    columns(p.post_weight, i, to);
+    if constexpr (KIND == kNormWithX) {
+      float g[8];
+      columns(gate, i, g);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) to[c] *= g[c];
+    }
+  };
+  float held_w[kHold ? V : 1][8], held_v[kHold ? VX : 1][8];
+  auto hold = [&](float (*to)[8], auto&& get) {
+    if constexpr (kHold)
+#pragma unroll
+      for (int i = 0; i < V; ++i) get(i, to[i]);
+  };
+  auto held = [&](const float (*from)[8], int i, float* to, auto&& get) {
+    if constexpr (kHold) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) to[c] = from[i][c];
+    } else {
+      get(i, to);
+    }
+  };
+  auto weight = [&](int i, float* to) { columns(p.weight, i, to); };
+  hold(held_w, weight);
+  if constexpr (GATES) hold(held_v, gated_weight);
   // a column sum of the whole workgroup (its row groups added in order), written by the first row group
-  auto flush = [&](float (*v)[8], auto&& put) {
+  auto flush = [&](auto&& get, auto&& put) {
     if constexpr (kRows > 1) {
       __syncthreads();   // the previous flush's readers are done
 #pragma unroll
-      for (int i = 0; i < V; ++i)
+      for (int i = 0; i < V; ++i) {
+        float t[8];
+        get(i, t);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) cols[group][at[i] + c] = v[i][c];
+        for (int c = 0; c < 8; ++c) cols[group][at[i] + c] = t[c];
+      }
       __syncthreads();
     }
     if (group == 0) {
@@ -306,10 +333,10 @@ __global__ __launch_bounds__(norm_threads<LT>()) void residual_norm_grad_kernel(
       for (int i = 0; i < V; ++i)
         if (ok[i]) {
           float t[8];
+          get(i, t);
+          if constexpr (kRows > 1) {
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            t[c] = v[i][c];
-            if constexpr (kRows > 1)
+            for (int c = 0; c < 8; ++c)
 #pragma unroll
               for (int g = 1; g < kRows; ++g) t[c] += cols[g][at[i] + c];
           }
@@ -321,26 +348,23 @@ __global__ __launch_bounds__(norm_threads<LT>()) void residual_norm_grad_kernel(
   for (int64_t piece = first; piece < end;) {
     // the rows up to the segment's end (every row without sums of gates); uniform over the workgroup
     int64_t piece_end = end, segment = 0;
-    if (gate_sums) {
-      segment = piece / p.rows_per_gate;
-      const int64_t e = (segment + 1) * p.rows_per_gate;
-      piece_end = e < end ? e : end;
+    if constexpr (KIND == kNormWithX) {
+      if (p.gate != nullptr) {
+        segment = piece / p.rows_per_gate;
+        const int64_t e = (segment + 1) * p.rows_per_gate;
+        piece_end = e < end ? e : end;
+        gate = static_cast<const T*>(p.gate) + segment * p.hidden;
+      }
+      hold(held_v, gated_weight);
     }
-    // rows of the piece in steps of kRows: every row group runs its own (they share barriers only in flush)
-    const bool gated = p.gate != nullptr;
-    const T* gate = static_cast<const T*>(p.gate);
-    if (HASX && !(gated && each_row)) {
-      if (gated) gate += (gate_sums ? segment : piece / p.rows_per_gate) * p.hidden;
-      hold(gate, gated, held_g);
+    // rows of the piece in steps of kRows: every row group runs its own (they share barriers only in flush).  The next
+    // row's loads go out as soon as the registers that they fill are free.
+    if (piece + group < piece_end) {
+      load_row(piece + group);
+      load_x(piece + group);
     }
-    Row cur;
     for (int64_t row = piece + group; row < piece_end; row += kRows) {
       const int64_t base = row * p.hidden;
-      load_row(row, cur);
-      if (HASX && gated && each_row) {
-        gate = static_cast<const T*>(p.gate) + base;
-        hold(gate, true, held_g);
-      }
       float sums[3] = {0.0f, 0.0f, 0.0f};   // s^2, dy w s, x^2
 #pragma unroll
       for (int i = 0; i < V; ++i)
@@ -348,7 +372,7 @@ __global__ __launch_bounds__(norm_threads<LT>()) void residual_norm_grad_kernel(
           float u[8], dy[8], w[8];
           widen8(cur.u[i], u);
           widen8(cur.dy[i], dy);
-          columns(p.weight, p.weight != nullptr, held_w, i, w);
+          held(held_w, i, w, weight);
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             sums[0] = __builtin_fmaf(u[c], u[c], sums[0]);
@@ -374,7 +398,7 @@ __global__ __launch_bounds__(norm_threads<LT>()) void residual_norm_grad_kernel(
           float u[8], dy[8], du[8], w[8];
           widen8(cur.u[i], u);
           widen8(cur.dy[i], dy);
-          columns(p.weight, p.weight != nullptr, held_w, i, w);
+          held(held_w, i, w, weight);
           if (p.dsum != nullptr) {
             widen8(cur.ds[i], du);
           } else {
@@ -390,21 +414,25 @@ __global__ __launch_bounds__(norm_threads<LT>()) void residual_norm_grad_kernel(
           if constexpr (HASX) {
             float x[8], v[8], g[8], dg[8];
             widen8(cur.x[i], x);
-            columns(p.post_weight, weighted, held_v, i, v);
-            columns(gate, gated, held_g, i, g);
+            held(held_v, i, v, gated_weight);
+            if constexpr (GATES) widen8(cur.g[i], g);
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
-              const float n = x[c] * sigma, dz0 = p.scale * du[c];
-              dg[c] = dz0 * (n * v[c]);
-              dgs[i][c] += dg[c];
-              dz[i][c] = dz0 * g[c];
-              dv[i][c] = __builtin_fmaf(dz[i][c], n, dv[i][c]);
-              dz[i][c] *= v[c];
+              const float n = x[c] * sigma;
+              float dz0 = p.scale * du[c];
+              if constexpr (GATES) {
+                dg[c] = dz0 * (n * v[c]);
+                dz0 *= g[c];
+              }
+              sum[i][c] = __builtin_fmaf(dz0, n, sum[i][c]);
+              dz[i][c] = dz0 * v[c];
               inner[0] = __builtin_fmaf(dz[i][c], x[c], inner[0]);
             }
-            if (each_row && p.dgate != nullptr) store8(static_cast<T*>(p.dgate) + base + at[i], narrow8<T>(dg));
+            if constexpr (GATES)
+              if (p.dgate != nullptr) store8(static_cast<T*>(p.dgate) + base + at[i], narrow8<T>(dg));
           }
         }
+      if (row + kRows < piece_end) load_row(row + kRows);
       if constexpr (HASX) {
         if (normed) row_sums<LT, 1>(inner, red_b, tid);   // (red_b's readers of the previous row are past the barrier above)
         const float along = sigma * sigma * inner[0] / (float)p.hidden;
@@ -417,29 +445,60 @@ __global__ __launch_bounds__(norm_threads<LT>()) void residual_norm_grad_kernel(
             for (int c = 0; c < 8; ++c) dx[c] = sigma * (dz[i][c] - (normed ? x[c] * along : 0.0f));
             store8(static_cast<T*>(p.dx) + base + at[i], narrow8<T>(dx));
           }
+        if (row + kRows < piece_end) load_x(row + kRows);
       }
     }
-    if (HASX && gate_sums) {
-      const int64_t seg_first = segment * p.rows_per_gate;
-      const bool whole = seg_first >= first && seg_first + p.rows_per_gate <= end;
-      float* slot = p.part + (seg_first > first ? 3 : 2) * plane + (int64_t)blockIdx.x * p.hidden;
-      flush(dgs, [&](int c0, const float* t) {
-        if (whole) {
-          store8(static_cast<T*>(p.dgate) + segment * p.hidden + c0, narrow8<T>(t));
-        } else {
-          store8(slot + c0, narrow8<float>(t));
+    if constexpr (KIND == kNormWithX) {
+      if (gate_sums) {
+        const int64_t seg_first = segment * p.rows_per_gate;
+        const bool whole = seg_first >= first && seg_first + p.rows_per_gate <= end;
+        float* slot = p.part + (seg_first > first ? 3 : 2) * plane + (int64_t)blockIdx.x * p.hidden;
+        flush(
+            [&](int i, float* t) {
+              columns(p.post_weight, i, t);
+#pragma unroll
+              for (int c = 0; c < 8; ++c) t[c] *= sum[i][c];
+            },
+            [&](int c0, const float* t) {
+              if (whole) {
+                store8(static_cast<T*>(p.dgate) + segment * p.hidden + c0, narrow8<T>(t));
+              } else {
+                store8(slot + c0, narrow8<float>(t));
+              }
+            });
+      }
+      if (p.dpost != nullptr) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          float g[8];
+          columns(gate, i, g);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) s_dv[group][2 * i + (c >> 2)][tid][c & 3] += g[c] * sum[i][c];
         }
-      });
+      }
 #pragma unroll
       for (int i = 0; i < V; ++i)
 #pragma unroll
-        for (int c = 0; c < 8; ++c) dgs[i][c] = 0.0f;
+        for (int c = 0; c < 8; ++c) sum[i][c] = 0.0f;
     }
     piece = piece_end;
   }
   float* mine = p.part + (int64_t)blockIdx.x * p.hidden;
-  if (p.dweight != nullptr) flush(dw, [&](int c0, const float* t) { store8(mine + c0, narrow8<float>(t)); });
-  if (HASX && p.dpost != nullptr) flush(dv, [&](int c0, const float* t) { store8(mine + plane + c0, narrow8<float>(t)); });
+  if (p.dweight != nullptr)
+    flush(
+        [&](int i, float* t) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) t[c] = dw[i][c];
+        },
+        [&](int c0, const float* t) { store8(mine + c0, narrow8<float>(t)); });
+  if constexpr (HASX)
+    if (p.dpost != nullptr)
+      flush(
+          [&](int i, float* t) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) t[c] = GATES ? sum[i][c] : s_dv[group][2 * i + (c >> 2)][tid][c & 3];
+          },
+          [&](int c0, const float* t) { store8(mine + plane + c0, narrow8<float>(t)); });
 }
 
 // Column sums of the partials: 64 columns a workgroup (16 lanes of 4), 64 of the partials side by side, eight loads of each
@@ -527,18 +586,19 @@ static const void* norm_fn_of(int out, int lt, int v) {
          : out == kNormFp8 ? norm_fn<T, TR, kNormFp8>(lt, v) : norm_fn<T, TR, kNormInt8>(lt, v);
 }
 
-template <class T, class TR, bool HASX>
+template <class T, class TR, int KIND>
 static const void* norm_grad_fn_of(int lt, int v) {
   void (*fn)(NormGradParams) =
-      lt == 64 ? (v == 1 ? residual_norm_grad_kernel<T, TR, HASX, 64, 1> : residual_norm_grad_kernel<T, TR, HASX, 64, 2>)
-      : lt == 256 ? (v == 1 ? residual_norm_grad_kernel<T, TR, HASX, 256, 1> : residual_norm_grad_kernel<T, TR, HASX, 256, 2>)
-                  : (v == 2 ? residual_norm_grad_kernel<T, TR, HASX, 512, 2> : residual_norm_grad_kernel<T, TR, HASX, 512, 4>);
+      lt == 64 ? (v == 1 ? residual_norm_grad_kernel<T, TR, KIND, 64, 1> : residual_norm_grad_kernel<T, TR, KIND, 64, 2>)
+      : lt == 256 ? (v == 1 ? residual_norm_grad_kernel<T, TR, KIND, 256, 1> : residual_norm_grad_kernel<T, TR, KIND, 256, 2>)
+                  : (v == 2 ? residual_norm_grad_kernel<T, TR, KIND, 512, 2> : residual_norm_grad_kernel<T, TR, KIND, 512, 4>);
   return reinterpret_cast<const void*>(fn);
 }
 
 template <class T, class TR>
-static const void* norm_grad_fn(bool has_x, int lt, int v) {
-  return has_x ? norm_grad_fn_of<T, TR, true>(lt, v) : norm_grad_fn_of<T, TR, false>(lt, v);
+static const void* norm_grad_fn(int kind, int lt, int v) {
+  return kind == kNormAlone   ? norm_grad_fn_of<T, TR, kNormAlone>(lt, v)
+         : kind == kNormWithX ? norm_grad_fn_of<T, TR, kNormWithX>(lt, v) : norm_grad_fn_of<T, TR, kNormGateRows>(lt, v);
 }
 
 // Lanes a row and pieces a lane.
@@ -601,7 +661,7 @@ static void norm_grad_shape(int64_t hidden, int* lt, int* v) {
 }
 
 // Its workgroups and the rows of each: as many as the CUs hold at once (three of 256 threads, two with twice the columns,
-// one of 512; 8191 x 2048 43.9 us, 47.9 with 1024 workgroups; 4096 x 4096 76 us, 89).
+// one of 512; 8191 x 2048 42.9 us with the sums, 47.9 with 1024 workgroups).
 static void norm_grad_parts(int64_t rows, int64_t hidden, int64_t* per_part, int* parts) {
   int lt, v;
   norm_grad_shape(hidden, &lt, &v);
@@ -657,9 +717,10 @@ int launch_residual_norm_grad(const void* dy, const void* dsum, const void* x, c
   int lt, v;
   norm_grad_shape(hidden, &lt, &v);
   const bool wide = residual_dtype == kF32;
-  const void* fn = dtype == kF32 ? norm_grad_fn<float, float>(x != nullptr, lt, v)
-                   : dtype == kBf16 ? (wide ? norm_grad_fn<Bf16, float>(x != nullptr, lt, v) : norm_grad_fn<Bf16, Bf16>(x != nullptr, lt, v))
-                                    : (wide ? norm_grad_fn<_Float16, float>(x != nullptr, lt, v) : norm_grad_fn<_Float16, _Float16>(x != nullptr, lt, v));
+  const int kind = x == nullptr ? kNormAlone : gate != nullptr && p.rows_per_gate == 1 ? kNormGateRows : kNormWithX;
+  const void* fn = dtype == kF32 ? norm_grad_fn<float, float>(kind, lt, v)
+                   : dtype == kBf16 ? (wide ? norm_grad_fn<Bf16, float>(kind, lt, v) : norm_grad_fn<Bf16, Bf16>(kind, lt, v))
+                                    : (wide ? norm_grad_fn<_Float16, float>(kind, lt, v) : norm_grad_fn<_Float16, _Float16>(kind, lt, v));
   void* args[] = {&p};
   hipError_t e = hipLaunchKernel(fn, dim3((unsigned)p.parts), dim3(lt > kNormThreads ? lt : kNormThreads), args, 0, stream);
   if (e != hipSuccess) return set_error(kHip, "residual_norm_grad launch: %s", hipGetErrorString(e));
