@@ -210,6 +210,7 @@ struct NormGradParams {
   int64_t rows, rows_per_gate;
   int64_t rows_per_part;
   int parts;
+  int gates_shared;           // gates that share a workgroup of the sums
   int hidden, post_norm;
   float scale, eps;
 };
@@ -503,8 +504,9 @@ __global__ __launch_bounds__(norm_threads<LT>(), V == 1 ? 3 : 2) void residual_n
 
 // Column sums of the partials: 64 columns a workgroup (16 lanes of 4), 64 of the partials side by side, eight loads of each
 // in flight, all added in a fixed order.  blockIdx.y = 0: dweight, 1: dpost, the rest the gates whose rows lie in more than
-// one workgroup's: 2 + i is gate i where gates have at least a workgroup's rows; where they have fewer, the 64 borders from
-// 64 i on between workgroups j and j + 1, each with the last piece of j and the first of j + 1.
+// one workgroup's: 2 + i is gate i, or the p.gates_shared gates from p.gates_shared i on, where gates have at least a
+// workgroup's rows; where they have fewer, the 64 borders from 64 i on between workgroups j and j + 1, each with the last
+// piece of j and the first of j + 1.
 constexpr int kSumAlong = 64;
 
 template <class T>
@@ -522,6 +524,8 @@ __global__ __launch_bounds__(16 * kSumAlong) void norm_grad_sum_kernel(NormGradP
   };
   int which = blockIdx.y, begin = 0, end = p.parts;
   int head = -1;   // the workgroup in which the gate's rows begin, where that piece is in slot 1
+  int beside = kSumAlong, place = along;   // partials side by side of this sum, and which of them this thread takes
+  int64_t gate_sum = -1;
   if (blockIdx.y < 2) {
     if (blockIdx.y == 0 ? p.dweight == nullptr : p.dpost == nullptr) return;
   } else if (p.rows_per_gate < p.rows_per_part) {
@@ -531,40 +535,52 @@ __global__ __launch_bounds__(16 * kSumAlong) void norm_grad_sum_kernel(NormGradP
     if (gate * p.rows_per_gate != border) put_gate(gate, at(3, j) + at(2, j + 1));
     return;
   } else {
-    const int64_t first = (int64_t)(blockIdx.y - 2) * p.rows_per_gate;
-    begin = (int)(first / p.rows_per_part);
-    end = (int)((first + p.rows_per_gate - 1) / p.rows_per_part) + 1;
-    if (end - begin == 1) return;   // written already
-    if (first > (int64_t)begin * p.rows_per_part) head = begin;
+    beside = kSumAlong / p.gates_shared;
+    place = along % beside;
+    gate_sum = (int64_t)(blockIdx.y - 2) * p.gates_shared + along / beside;
+    const int64_t first = gate_sum * p.rows_per_gate;
+    begin = end = 0;
+    if (first < p.rows) {
+      begin = (int)(first / p.rows_per_part);
+      end = (int)((first + p.rows_per_gate - 1) / p.rows_per_part) + 1;
+      if (end - begin == 1) end = begin;   // written already
+      if (first > (int64_t)begin * p.rows_per_part) head = begin;
+    }
     which = 2;
   }
   v4f sum = {0.f, 0.f, 0.f, 0.f};
   if (there)
-    for (int i0 = begin + along; i0 < end; i0 += 8 * kSumAlong) {
+    for (int i0 = begin + place; i0 < end; i0 += 8 * beside) {
       v4f v[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        const int i = i0 + u * kSumAlong < end ? i0 + u * kSumAlong : i0;
+        const int i = i0 + u * beside < end ? i0 + u * beside : i0;
         v[u] = at(i == head ? 3 : which, i);
       }
 #pragma unroll
       for (int u = 0; u < 8; ++u)
-        if (i0 + u * kSumAlong < end) sum += v[u];
+        if (i0 + u * beside < end) sum += v[u];
     }
   s_sum[along][lane] = sum;
   __syncthreads();
+  if (beside < kSumAlong) {
+    if (place != 0 || !there || begin == end) return;
+    for (int i = 1; i < beside; ++i) sum += s_sum[along + i][lane];
+    put_gate(gate_sum, sum);
+    return;
+  }
   if (along < 8) {
 #pragma unroll
     for (int i = 8; i < kSumAlong; i += 8) sum += s_sum[along + i][lane];
     s_sum[along][lane] = sum;   // (no other thread reads these eight before the barrier)
   }
   __syncthreads();
-  if (along != 0 || !there) return;
+  if (along != 0 || !there || begin == end) return;
 #pragma unroll
   for (int i = 1; i < 8; ++i) sum += s_sum[i][lane];
   if (blockIdx.y == 0) *reinterpret_cast<v4f*>(p.dweight + col) = sum;
   else if (blockIdx.y == 1) *reinterpret_cast<v4f*>(p.dpost + col) = sum;
-  else put_gate(blockIdx.y - 2, sum);
+  else put_gate(gate_sum, sum);
 }
 
 // ---- host ------------------------------------------------------------------------------------------
@@ -725,8 +741,17 @@ int launch_residual_norm_grad(const void* dy, const void* dsum, const void* x, c
   hipError_t e = hipLaunchKernel(fn, dim3((unsigned)p.parts), dim3(lt > kNormThreads ? lt : kNormThreads), args, 0, stream);
   if (e != hipSuccess) return set_error(kHip, "residual_norm_grad launch: %s", hipGetErrorString(e));
   int64_t gates = 0;   // rows of the sums' grid for gates
-  if (dgate != nullptr && p.rows_per_gate > 1 && p.parts > 1)
-    gates = p.rows_per_gate < p.rows_per_part ? (p.parts - 1 + kSumAlong - 1) / kSumAlong : gate_rows;
+  p.gates_shared = 1;
+  if (dgate != nullptr && p.rows_per_gate > 1 && p.parts > 1) {
+    if (p.rows_per_gate < p.rows_per_part) {
+      gates = (p.parts - 1 + kSumAlong - 1) / kSumAlong;
+    } else {
+      // as many threads to a gate as leave each at most two of its partials (64 gates of 251 rows: 103 -> 99.5 us with the sums)
+      const int64_t pieces = p.rows_per_gate / p.rows_per_part + 2;
+      while (p.gates_shared < 16 && 2 * (kSumAlong / (2 * p.gates_shared)) >= pieces) p.gates_shared *= 2;
+      gates = (gate_rows + p.gates_shared - 1) / p.gates_shared;
+    }
+  }
   if (dweight == nullptr && dpost == nullptr && gates == 0) return kOk;
   void (*sum_fn)(NormGradParams) = dtype == kF32 ? norm_grad_sum_kernel<float>
                                    : dtype == kBf16 ? norm_grad_sum_kernel<Bf16> : norm_grad_sum_kernel<_Float16>;

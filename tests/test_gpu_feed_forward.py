@@ -297,7 +297,7 @@ def test_norm_alone(rows, hidden):
 @pytest.mark.parametrize("rows,hidden,gates", [(1, 16, 1), (5, 64, 5), (12, 144, 4), (66, 512, 3), (2500, 64, 1), (2500, 64, 5),
                                                (2499, 128, 833), (2500, 48, 1250), (3000, 32, 3000), (1050, 1024, 7),
                                                (1030, 2064, 2), (64, 4096, 0), (1060, 4112, 1), (600, 8192, 3), (520, 8208, 2),
-                                               (300, 16384, 1)])
+                                               (300, 16384, 1), (1280, 64, 64), (1300, 1040, 20), (1000, 528, 100)])
 @pytest.mark.parametrize("post", [False, True])
 def test_norm_grad(rows, hidden, gates, post):
     rng = np.random.default_rng(rows + hidden + gates)
