@@ -1434,7 +1434,7 @@ int launch_gemm(int layout, const uint8_t* a, const float* sa, int64_t ld_sa, co
 // ---- gated form: both projections of a feed-forward block, the activation and the product ------
 // The large tiles of the plain forms, with 128 gate and 128 up rows for 256 rows of weights; for few rows the kernel that
 // streams the weights (csrc/gemm_gated_few.hip), with tiles of 16 or 64 rows.  A wave of a large tile holds gate and up
-// fragments of the same columns, so the epilogue needs no other workgroup.  8192 x 8192 x 7168: 1690 us, 2.28e15 operations/s,
+// fragments of the same columns, so the epilogue needs no other workgroup.  8192 x 8192 x 7168: 1653 us, 2.33e15 operations/s,
 // the matrix cores busy for half of the cycles and the promotion's FMAs for the other half, as in the plain form.
 const void* gated_few_kernel(int layout, int bm);
 int gated_few_lds(int bm);

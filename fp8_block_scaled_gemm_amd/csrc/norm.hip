@@ -226,8 +226,8 @@ enum NormGradKind : int { kNormAlone = 0, kNormWithX = 1, kNormGateRows = 2 };  
 // One sum of a piece serves two gradients: with a = sum(scale du x sigma) over its rows, dgate is v a and dv gets gate a
 // (held in LDS from piece to piece).  Absent weights, gates and norms are ones and scales of 1 rather than branches (those
 // took 190 registers where 110 do).
-// Bound by memory: 8191 x 2048 bf16 with a gate 41 us (220 MB at 5.3 TB/s), 16064 x 1536 fp16 over an fp32 stream with 64
-// gates 97 us (4.6 TB/s), and 6 and 9 us for the sums of the partials.
+// Bound by memory: 8191 x 2048 bf16 with a gate 40 us (220 MB at 5.5 TB/s), 16064 x 1536 fp16 over an fp32 stream with 64
+// gates 97 us (4.6 TB/s), and 6 us for the sums of the partials.
 template <class T, class TR, int KIND, int LT, int V>
 __global__ __launch_bounds__(norm_threads<LT>(), V == 1 ? 3 : 2) void residual_norm_grad_kernel(NormGradParams p) {
   constexpr bool HASX = KIND != kNormAlone, GATES = KIND == kNormGateRows;
