@@ -964,25 +964,27 @@ def dg_gemm_fp8_gated_config_name(layout, m, n, k, num_groups=1):
     return lib().dg_gemm_fp8_gated_config_name(int(layout), int(m), int(n), int(k), int(num_groups)).decode()
 
 
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
 def _gated_operands(a, sa, b, sb, groups):
-    """(a, b as bytes, N, K) of activations and the gate and up matrices b ([G,] 2, N, K), or ([G,] 2N, K) for N a multiple
+    """(N, K, ceil(K / 128)) of activations and the gate and up matrices b ([G,] 2, N, K), or ([G,] 2N, K) for N a multiple
     of 128, with their scales."""
-    a, b = _bytes(a), _bytes(b)
-    lead = () if groups is None else (groups,)
-    _require(a.dtype == torch.uint8 and b.dtype == torch.uint8 and sa.dtype == torch.float32 and sb.dtype == torch.float32,
-             "a and b must be E4M3 bytes, sa and sb float32")
-    k = a.shape[-1]
-    _require(b.dim() in (2 + len(lead), 3 + len(lead)) and tuple(b.shape[:len(lead)]) == lead and b.shape[-1] == k,
-             "b must be ([G,] 2, N, K)")
-    if b.dim() == 3 + len(lead):
-        _require(b.shape[-3] == 2, "b must be ([G,] 2, N, K)")
-        n = b.shape[-2]
+    if a.dtype not in _CODES or b.dtype not in _CODES or sa.dtype != torch.float32 or sb.dtype != torch.float32:
+        raise ValueError("a and b must be E4M3 bytes, sa and sb float32")
+    k, shape = a.shape[-1], b.shape
+    lead = 0 if groups is None else 1
+    if len(shape) not in (2 + lead, 3 + lead) or shape[-1] != k or (lead and shape[0] != groups):
+        raise ValueError("b must be ([G,] 2, N, K)")
+    if len(shape) == 3 + lead:
+        _require(shape[-3] == 2, "b must be ([G,] 2, N, K)")
+        n = shape[-2]
     else:
-        _require(b.shape[-2] % 256 == 0, "b ([G,] 2N, K) needs N a multiple of 128")
-        n = b.shape[-2] // 2
+        _require(shape[-2] % 256 == 0, "b ([G,] 2N, K) needs N a multiple of 128")
+        n = shape[-2] // 2
     kb = -(-k // 128)
-    _require(sb.numel() == (groups if groups is not None else 1) * 2 * -(-n // 128) * kb, "sb must be ([G,] 2, ceil(N/128), ceil(K/128))")
-    return a, b, n, k, kb
+    _require(sb.numel() == (groups if lead else 1) * 2 * -(-n // 128) * kb, "sb must be ([G,] 2, ceil(N/128), ceil(K/128))")
+    return n, k, kb
 
 
 def _gated_out(lead, n, out, d, q, s, pre, device):
@@ -1005,7 +1007,7 @@ def dg_gemm_fp8_gated_nt(a, sa, b, sb, act="silu", out="bf16", d=None, q=None, s
     ceil(N/128), ceil(K/128)): -> d bfloat16, or with out='fp8' (q uint8, s float32 (ceil(N/128), ld)) as
     dg_quantize_per_token_group would quantize h in fp32.  pre (bfloat16 (M, 2N)) receives both projections."""
     _require(a.dim() == 2, "a (M, K)")
-    a, b, n, k, kb = _gated_operands(a, sa, b, sb, None)
+    n, k, kb = _gated_operands(a, sa, b, sb, None)
     m = a.shape[0]
     _require(sa.dim() == 2 and sa.shape[0] == kb and sa.shape[1] >= m, "sa must be (ceil(K/128), ld >= M)")
     d, q, s = _gated_out((m,), n, out, d, q, s, pre, a.device)
@@ -1024,7 +1026,7 @@ def dg_gemm_fp8_gated_contiguous(a, sa, b, sb, m_indices, act="silu", out="bf16"
     multiple of 128); rows of an index outside [0, G) stay untouched."""
     _require(a.dim() == 2 and b.dim() >= 3, "a (M_total, K), b (G, 2, N, K)")
     g = b.shape[0]
-    a, b, n, k, kb = _gated_operands(a, sa, b, sb, g)
+    n, k, kb = _gated_operands(a, sa, b, sb, g)
     m = a.shape[0]
     _require(sa.dim() == 2 and sa.shape[0] == kb and sa.shape[1] >= m, "sa must be (ceil(K/128), ld >= M_total)")
     _require(m_indices.dtype == torch.int32 and m_indices.numel() == m, "m_indices must be int32, one per row")
@@ -1042,7 +1044,7 @@ def dg_gemm_fp8_gated_masked(a, sa, b, sb, masked_m, act="silu", out="bf16", d=N
     128); expert g computes its first masked_m[g] rows, the rest stay untouched.  s is (G, ceil(N/128), ld)."""
     _require(a.dim() == 3, "a (G, M_max, K)")
     g, m = a.shape[:2]
-    a, b, n, k, kb = _gated_operands(a, sa, b, sb, g)
+    n, k, kb = _gated_operands(a, sa, b, sb, g)
     _require(tuple(sa.shape[:-1]) == (g, kb) and sa.shape[-1] >= m, "sa must be (G, ceil(K/128), ld >= M_max)")
     _require(masked_m.dtype == torch.int32 and masked_m.numel() == g, "masked_m must be int32, one per expert")
     d, q, s = _gated_out((g, m), n, out, d, q, s, pre, a.device)
