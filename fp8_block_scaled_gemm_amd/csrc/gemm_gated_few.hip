@@ -108,10 +108,11 @@ __global__ __launch_bounds__(C::kThreads) void gemm_gated_few_kernel(GemmParams 
     const float* sb_g = p.sb + (int64_t)t.g * p.sb_gstride + (int64_t)t.nbt * p.kb_total + kb0;
     const float* sb_u = sb_g + (int64_t)p.nb128 * p.kb_total;
 
-    // A lane's 32 bytes of a K block, of weights and activations alike: 16 of each half (a row's four lanes read 64 bytes
-    // in one piece).  Loads past the last K block, or past k, take an out-of-range offset.
+    // A lane's 32 bytes of a K block, of weights and activations alike, as in the large tiles: the matrix instruction adds
+    // the same products together, whatever the tile (16 bytes of each half, 64 of a row in one piece, were no faster).
+    // Loads past the last K block, or past k, take an out-of-range offset.
     auto offset = [&](int tk, int half, uint32_t row_off) {
-      return tk < nk && (kb0 + tk) * kGroup + 64 * half + 16 * g4 < p.k ? row_off + 64u * half + 16u * g4 : kOut;
+      return tk < nk && (kb0 + tk) * kGroup + 16 * half + 32 * g4 < p.k ? row_off + 16u * half + 32u * g4 : kOut;
     };
     auto load16 = [&](__amdgpu_buffer_rsrc_t rs, int tk, int half, uint32_t row_off) {
       return __builtin_amdgcn_raw_buffer_load_b128(rs, offset(tk, half, row_off), (kb0 + tk) * kGroup, 0);
@@ -199,12 +200,12 @@ __global__ __launch_bounds__(C::kThreads) void gemm_gated_few_kernel(GemmParams 
         }
         *reinterpret_cast<float*>(base + C::kScaleOffset + 4 * tid) = sr[stage];
       };
-      const int lane_off = lds_off(l16, g4);   // the second half's chunk differs in bit 2: address ^ 64
+      const int lane_off = lds_off(l16, 2 * g4);   // the second half's chunk differs in bit 0: address ^ 16
       auto compute = [&](int slot, const v8i* r, float sbg, float sbu) {
         const uint8_t* base = lds + slot * C::kSlot;
         auto read = [&](int j) {
           const int off = 16 * j * kGroup + lane_off;
-          return make_v8i(*reinterpret_cast<const u32x4*>(base + off), *reinterpret_cast<const u32x4*>(base + (off ^ 64)));
+          return make_v8i(*reinterpret_cast<const u32x4*>(base + off), *reinterpret_cast<const u32x4*>(base + (off ^ 16)));
         };
         // four fragments read at a time
 #pragma unroll
