@@ -1457,22 +1457,24 @@ static LaunchInfo gated_info(int cfg) {
   return cfg == kGatedSquare ? info<CfgSquare, LAYOUT, false, true>() : info<CfgGatedRows128, LAYOUT, false, true>();
 }
 
-// Estimated time (us) of a dense gated product by tile and K split, from timings of every choice on MI355X over 15
-// shapes of 1 to 1024 rows, n 256 to 8192, k 1024 to 7168 (cold weights): a start, the K blocks of a workgroup one after
-// the other, in rounds of the CUs, and the weights' bytes at 5 TB/s; and for splits the partials: out and back at 4
-// TB/s with a launch for the streaming kernel, the last workgroup's reading of them for the large tiles and few rows.
-static double gated_estimate(int cfg, int64_t m, int64_t strips, int64_t k, int num_cus, int splits, int kbps, bool in_kernel) {
+// Estimated time (us) of a dense or masked gated product by tile and K split: `rows` rows in `row_blocks` tiles on each of
+// `strips` strips of weights.  From timings of every choice on MI355X over 15 dense shapes of 1 to 1024 rows, n 256 to 8192,
+// k 1024 to 7168 (cold weights), and 30 masked ones: a start, the K blocks of a workgroup one after the other, in rounds of
+// the CUs, and the weights' bytes at 5 TB/s (4.4 on 16-row tiles); and for splits the partials: out and back at 4 TB/s with a
+// launch for the streaming kernel, the last workgroup's reading of them for the large tiles and few rows.
+static double gated_estimate(int cfg, double row_blocks, double rows, int64_t strips, int64_t k, int num_cus, int splits, int kbps,
+                             bool in_kernel) {
   const double bm = cfg == kGatedFew16 ? 16 : cfg == kGatedFew64 ? 64 : cfg == kGatedRows128 ? 128 : 256;
   const double start = cfg == kGatedFew16 ? 4.5 : cfg == kGatedFew64 ? 6.0 : cfg == kGatedRows128 ? 8.6 : 13.5;
   const double block = cfg == kGatedFew16 ? 1.07 : cfg == kGatedFew64 ? 1.0 : cfg == kGatedRows128 ? 1.15 : 1.95;
-  const int64_t tiles = (int64_t)((m + bm - 1) / bm) * strips;
+  const int64_t tiles = (int64_t)std::ceil(row_blocks * (double)strips);
   const int blocks = cfg == kGatedFew16 ? (kbps + 3) / 4 * 4 : kbps;   // (its loop takes four at a time)
   const double chain = (double)((tiles * splits + num_cus - 1) / num_cus) * blocks * block;
-  const double memory = (double)strips * 2 * kGroup * (double)k / 5.0e6;
+  const double memory = (double)strips * 2 * kGroup * (double)k / (cfg == kGatedFew16 ? 4.4e6 : 5.0e6);
   double t = start + std::sqrt(chain * chain + memory * memory);   // (both near the larger one slow each other)
   if (splits > 1) {
-    if (cfg >= kGatedFew16 && !in_kernel) t += 4.0 + (double)strips * (double)m * splits * 2048.0 / 4.0e6;
-    else if (cfg >= kGatedFew16) t += 1.5 + (double)splits * (double)m * 1024.0 / 3.0e4;
+    if (cfg >= kGatedFew16 && !in_kernel) t += 4.0 + (double)strips * rows * splits * 2048.0 / 4.0e6;
+    else if (cfg >= kGatedFew16) t += 1.5 + (double)splits * rows * 1024.0 / 3.0e4;
     else t += 2.0 + 1.8 * splits * bm / 128;
   }
   return t;
@@ -1510,25 +1512,23 @@ static Plan make_gated_plan(int layout, int64_t m, int64_t n, int64_t k, int64_t
   if (layout == kContiguous) {
     pl.cfg = forced >= 0 ? forced
              : choose_contiguous(m, weight_rows, call_groups, num_cus) == kCfgSquare ? kGatedSquare : kGatedRows128;
-  } else if (layout == kMasked) {
-    // rows in use are not known here; beyond 64 the 128-row tile, which a group's last rows fill worse than the streaming
-    // kernel's but the weights pass less often (32 x 256 x 2048 x 7168, half in use: 257 us, 256-row tiles 300, 64-row strips 380)
-    pl.cfg = forced >= 0 ? forced : m <= 16 ? kGatedFew16 : m <= 64 ? kGatedFew64 : kGatedRows128;
-    const int64_t bm = gated_info<kDense>(pl.cfg).bm;
-    const int64_t tiles = ((m + bm - 1) / bm) * strips * groups;
-    if (allow_split && 2 * tiles <= num_cus) {   // few tiles: split K so that every CU gets work
-      int64_t s = num_cus / tiles;
-      if (s > kb_total / 4) s = kb_total / 4;
-      pl.splits = (int)(s < 1 ? 1 : s > most(pl.cfg) ? most(pl.cfg) : s);
-    }
   } else {
+    // The rows that a group of the masked form has are not known here: between none and m, as likely one as the other (32 x 256
+    // x 2048 x 7168, half in use: 250 us on the 128-row tile, 300 on 256 rows, 380 on 64; 8 x 128 x 512 x 4096: 23, 32 on
+    // 128 rows; 32 x 16 x 2048 x 7168: 153 on 64 rows, 179 on 16).
+    const bool masked = layout == kMasked;
     double best = 1e30;
     for (const int cfg : {kGatedSquare, kGatedRows128, kGatedFew64, kGatedFew16}) {
       if (forced >= 0 ? cfg != forced : cfg == kGatedFew16 && m > 16) continue;
+      const int64_t bm = gated_info<kDense>(cfg).bm, most_blocks = (m + bm - 1) / bm;
+      const double row_blocks =
+          masked ? (double)most_blocks - (double)bm * (double)(most_blocks * (most_blocks - 1)) / (2.0 * (double)m) : (double)most_blocks;
       for (int s = 1; s <= (allow_split ? most(cfg) : 1); ++s) {
         const int kbps = (kb_total + s - 1) / s;
         if ((kb_total + kbps - 1) / kbps != s || (s > 1 && kbps < (cfg >= kGatedFew16 ? 2 : 4))) continue;
-        const double t = gated_estimate(cfg, m, strips, k, num_cus, s, kbps, gated_join_in_kernel(cfg, m, s));
+        if (masked && s > 1 && most_blocks * strips * groups * s > 2 * num_cus) break;   // (a workspace for full groups)
+        const double t = gated_estimate(cfg, row_blocks, masked ? 0.5 * (double)m : (double)m, strips * groups, k, num_cus, s, kbps,
+                                        gated_join_in_kernel(cfg, m, s));
         if (t < best) {
           best = t;
           pl.cfg = cfg;
