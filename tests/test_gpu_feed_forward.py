@@ -61,7 +61,7 @@ def act_tol(pre, act):
 # ---- the activation -------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])
-@pytest.mark.parametrize("rows,n", [(1, 16), (3, 128), (17, 144), (130, 1040), (33, 4112), (5, 16400)])
+@pytest.mark.parametrize("rows,n", [(1, 16), (3, 128), (17, 144), (130, 1040), (33, 4112), (5, 16400), (9, 1024), (3, 8192), (2, 8208)])
 def test_act(rows, n, act):
     rng = np.random.default_rng(rows * n)
     for dtype in DTYPES:
