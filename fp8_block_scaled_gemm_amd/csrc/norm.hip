@@ -234,7 +234,8 @@ __global__ __launch_bounds__(norm_threads<LT>(), V == 1 ? 3 : 2) void residual_n
   constexpr int kWaves = LT / 64, kRows = norm_rows<LT>();
   __shared__ float red_a[kWaves][3], red_b[kWaves][1];
   __shared__ float cols[kRows > 1 ? kRows : 1][kRows > 1 ? 8 * LT * V : 1];
-  __shared__ v4f s_dv[HASX ? kRows : 1][HASX ? 2 * V : 1][HASX ? LT : 1];
+  constexpr bool kPieces = KIND == kNormWithX;   // dv is gathered piece by piece
+  __shared__ v4f s_dv[kPieces ? kRows : 1][kPieces ? 2 * V : 1][kPieces ? LT : 1];
   // (a row group is whole waves: with its number in a scalar register the loop over its rows has no lane leave it alone)
   const int tid = threadIdx.x % LT, group = __builtin_amdgcn_readfirstlane(threadIdx.x / LT);
   const int64_t first = (int64_t)blockIdx.x * p.rows_per_part;
@@ -253,7 +254,7 @@ __global__ __launch_bounds__(norm_threads<LT>(), V == 1 ? 3 : 2) void residual_n
       dw[i][c] = 0.0f;
       if constexpr (HASX) sum[i][c] = 0.0f;
     }
-    if constexpr (HASX) s_dv[group][2 * i][tid] = s_dv[group][2 * i + 1][tid] = v4f{0.f, 0.f, 0.f, 0.f};
+    if constexpr (kPieces) s_dv[group][2 * i][tid] = s_dv[group][2 * i + 1][tid] = v4f{0.f, 0.f, 0.f, 0.f};
   }
   struct Row {
     Raw8<TR> u[V], ds[V];
@@ -449,7 +450,7 @@ __global__ __launch_bounds__(norm_threads<LT>(), V == 1 ? 3 : 2) void residual_n
         if (row + kRows < piece_end) load_x(row + kRows);
       }
     }
-    if constexpr (KIND == kNormWithX) {
+    if constexpr (kPieces) {
       if (gate_sums) {
         const int64_t seg_first = segment * p.rows_per_gate;
         const bool whole = seg_first >= first && seg_first + p.rows_per_gate <= end;
@@ -497,7 +498,11 @@ __global__ __launch_bounds__(norm_threads<LT>(), V == 1 ? 3 : 2) void residual_n
       flush(
           [&](int i, float* t) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c) t[c] = GATES ? sum[i][c] : s_dv[group][2 * i + (c >> 2)][tid][c & 3];
+            for (int c = 0; c < 8; ++c)
+              if constexpr (kPieces)
+                t[c] = s_dv[group][2 * i + (c >> 2)][tid][c & 3];
+              else
+                t[c] = sum[i][c];
           },
           [&](int c0, const float* t) { store8(mine + plane + c0, narrow8<float>(t)); });
 }
