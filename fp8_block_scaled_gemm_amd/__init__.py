@@ -1253,8 +1253,9 @@ def dg_residual_norm_grad(dy, dsum, x, sum, weight=None, gate=None, post_norm=Fa
     _require(dsum is None or (dsum.dtype == sum.dtype and dsum.shape == sum.shape), "dsum must be like sum")
     device = sum.device
     _require(x is not None or dx is None, "dx without x")
-    dx = _like(dx, sum.shape, dy.dtype, device, "dx") if x is not None else None
-    dresidual = _like(dresidual, sum.shape, sum.dtype, device, "dresidual")
+    if x is not None:
+        dx = torch.empty_like(x) if dx is None else _like(dx, sum.shape, dy.dtype, device, "dx")
+    dresidual = torch.empty_like(sum) if dresidual is None else _like(dresidual, sum.shape, sum.dtype, device, "dresidual")
     dweight = torch.empty(hidden, dtype=torch.float32, device=device) if weight is not None else None
     dgate = torch.empty_like(gate) if gate is not None else None
     dpost = torch.empty(hidden, dtype=torch.float32, device=device) if post_weight is not None else None
