@@ -1436,7 +1436,7 @@ int launch_gemm(int layout, const uint8_t* a, const float* sa, int64_t ld_sa, co
 // streams the weights (csrc/gemm_gated_few.hip), with tiles of 16 or 64 rows.  A wave of a large tile holds gate and up
 // fragments of the same columns, so the epilogue needs no other workgroup.  8192 x 8192 x 7168: 1653 us, 2.33e15 operations/s,
 // the matrix cores busy for half of the cycles and the promotion's FMAs for the other half, as in the plain form.
-const void* gated_few_kernel(int layout, int bm);
+const void* gated_few_kernel(int layout, int bm, bool quantized);
 int gated_few_lds(int bm);
 int launch_gated_join(int layout, GemmParams p, int bm, hipStream_t stream);
 
@@ -1449,10 +1449,10 @@ enum GatedCfgId : int { kGatedRows128 = 0, kGatedSquare, kGatedFew16, kGatedFew6
 constexpr int kMaxStreamSplits = 32;
 
 template <int LAYOUT>
-static LaunchInfo gated_info(int cfg) {
+static LaunchInfo gated_info(int cfg, bool quantized = false) {
   if (cfg >= kGatedFew16 && LAYOUT != kContiguous) {
     const int bm = cfg == kGatedFew16 ? 16 : 64;
-    return LaunchInfo{256, bm, 512, 2, gated_few_kernel(LAYOUT, bm), gated_few_lds(bm)};
+    return LaunchInfo{256, bm, 512, 2, gated_few_kernel(LAYOUT, bm, quantized), gated_few_lds(bm)};
   }
   return cfg == kGatedSquare ? info<CfgSquare, LAYOUT, false, true>() : info<CfgGatedRows128, LAYOUT, false, true>();
 }
@@ -1551,9 +1551,9 @@ static void gated_plan_name(const Plan& pl, char* buf, size_t len) {
 template <int LAYOUT>
 static int launch_gated(GemmParams p, const Plan& pl, hipStream_t stream, int num_cus) {
   if (pl.cfg < kGatedFew16 || pl.splits == 1 || gated_join_in_kernel(pl.cfg, p.m, pl.splits))
-    return launch_info<LAYOUT>(gated_info<LAYOUT>(pl.cfg), p, pl, stream, num_cus);
+    return launch_info<LAYOUT>(gated_info<LAYOUT>(pl.cfg, p.q != nullptr), p, pl, stream, num_cus);
   p.counters = nullptr;   // the second launch ends the tiles
-  const int r = launch_info<LAYOUT>(gated_info<LAYOUT>(pl.cfg), p, pl, stream, num_cus);
+  const int r = launch_info<LAYOUT>(gated_info<LAYOUT>(pl.cfg, p.q != nullptr), p, pl, stream, num_cus);
   return r == kOk ? launch_gated_join(LAYOUT, p, pl.bm, stream) : r;
 }
 

@@ -503,7 +503,8 @@ enum dg_act { DG_ACT_SILU = 0, DG_ACT_GELU = 1 };
  * workspace : as dg_gemm_fp8_nt's (its first 64 KiB zero before the first use, left zero by every call; calls that share it
  *   must be ordered); NULL or smaller than dg_gemm_fp8_gated_workspace_size: no K split.
  * Errors: as the plain forms, an unknown activation, both or neither of d and q, q without s; DG_ERR_UNSUPPORTED where 2 n k or
- * m k reaches 2^31, or KB ld_sa 2^29.  Deterministic; without a K split g and u are the bits of the plain forms.
+ * m k reaches 2^31, or KB ld_sa 2^29.  Deterministic; without a K split the g and u of a bf16 output are the bits of the
+ * plain forms.
  */
 int dg_gemm_fp8_gated_nt(const uint8_t* a, const float* sa, int64_t ld_sa, const uint8_t* b, const float* sb, int act,
                          uint16_t* d, uint8_t* q, float* s, int64_t ld_s, uint16_t* pre, int64_t m, int64_t n, int64_t k,
