@@ -499,7 +499,7 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
       for (int u = 0; u < C::kDmaPerWave; ++u) {
         const int q = iw + C::kIssuers * u;
         const uint32_t voff = base_off + dma_band(u) * band_step;
-        lds_dma16(dma_rsrc(u), sbase + q * (C::kDmaRows * kGroup), chunk_out ? 0xFFFFFFF0u : voff,
+        lds_dma16(dma_rsrc(u), sbase + q * (C::kDmaRows * kGroup), chunk_out ? kOut : voff,
                   kb * kGroup);
       }
       if (sa_active)
@@ -612,7 +612,6 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
       constexpr int kFN = C::kFragN, kFM = C::kFragM;
       constexpr int kBarRow = kFN - 2;   // the rows after the barrier: kBarRow and the last one
       static_assert(kBarRow >= 1, "PIPE: at least three fragment rows");
-      constexpr uint32_t kOut = 0xFFFFFFF0u;   // an offset past every resource: the DMA writes zeros
       using SlotPtr = const uint8_t*;
       // slot 0 (blocks 0, 2, ...) is the buffer the epilogue's strips do not use
       uint8_t* const slot0 = st1;
@@ -641,7 +640,7 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
         constexpr int slot = decltype(slot_c)::value;
         DmaCtx c;
         c.sbase = slot == 0 ? slot0 : slot == 1 ? slot1 : st2;
-        c.kb = kb_begin + tk;
+        c.kb = offset_block(kb_begin + tk, valid);
         c.base_off = dma_off;
         asm volatile("" : "+v"(c.base_off));
         // bitwise, not short-circuit: a branch here would split the block body

@@ -77,6 +77,18 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, in
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, n, kBufferWord3);
 }
 
+// A buffer access of what is not there takes an offset past every resource.  The range check of a raw buffer subtracts the
+// scalar offset from the resource's bytes in 32 bits, so this offset lies outside only while the scalar one is no larger than
+// the resource: an access of a K block behind the last takes the scalar offsets of block 0.  (With its own, the block scale of
+// one column block, bytes 4 kb_total, would be read at scalar offsets to 4 kb_total + 12: at a difference of -4 the check passes.)
+constexpr uint32_t kOut = 0xFFFFFFF0u;
+constexpr bool buffer_in_range(uint32_t voff, uint32_t soff, uint32_t bytes) { return voff < bytes - soff; }
+__host__ __device__ constexpr int offset_block(int kb, bool there) { return there ? kb : 0; }
+// of one K block's scale (gated: two of them) on the rings of two and three slots, and of rows of 16 bytes
+static_assert(!buffer_in_range(kOut, 4 * offset_block(2, false), 4) && !buffer_in_range(kOut, 4 * offset_block(3, false), 8) &&
+              !buffer_in_range(kOut, kGroup * offset_block(3, false), 16) && !buffer_in_range(kOut, 0, 0x7fffffff),
+              "a K block behind the last reads nothing");
+
 struct TileCoord {
   int g, mb, nbt, split;
   int m_lo, m_valid;   // the tile's output rows are those in [m_lo, m_valid)

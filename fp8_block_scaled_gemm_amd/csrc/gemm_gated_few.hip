@@ -75,7 +75,6 @@ __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(
 template <class C, int LAYOUT, bool EXACT>
 __global__ __launch_bounds__(C::kThreads) void gemm_gated_few_kernel(GemmParams p) {
   constexpr int J = C::J, D = C::D, NT = C::kThreads;
-  constexpr uint32_t kOut = 0xFFFFFFF0u;   // an offset past every resource: the load returns zeros
   __shared__ __attribute__((aligned(1024))) uint8_t lds[C::kLds];
   __shared__ int s_prefix[LAYOUT == kMasked ? 1025 : 1];
   __shared__ int s_scan[LAYOUT == kMasked ? 256 : 1];
@@ -138,12 +137,12 @@ __global__ __launch_bounds__(C::kThreads) void gemm_gated_few_kernel(GemmParams 
       return tk < nk && (kb0 + tk) * kGroup + 16 * half + 32 * g4 < p.k ? row_off + 16u * half + 32u * g4 : kOut;
     };
     auto load16 = [&](__amdgpu_buffer_rsrc_t rs, int tk, int half, uint32_t row_off) {
-      return __builtin_amdgcn_raw_buffer_load_b128(rs, offset(tk, half, row_off), (kb0 + tk) * kGroup, 0);
+      return __builtin_amdgcn_raw_buffer_load_b128(rs, offset(tk, half, row_off), offset_block(kb0 + tk, tk < nk) * kGroup, 0);
     };
     auto load_scale = [&](int tk, int row) {   // of row m0 + row (0 past the rows in use)
       return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
                                            rs_sa, tk < nk && row < rows ? (uint32_t)(m0 + row) * 4u : kOut,
-                                           (kb0 + tk) * (int)p.ld_sa * 4, 0));
+                                           offset_block(kb0 + tk, tk < nk) * (int)p.ld_sa * 4, 0));
     };
     const uint32_t w_off = (uint32_t)(16 * wave + l16) * (uint32_t)p.k;
     v8i w[D][2];   // [K block][gate, up]
@@ -225,7 +224,7 @@ __global__ __launch_bounds__(C::kThreads) void gemm_gated_few_kernel(GemmParams 
           const int piece = tid + NT * i, row = piece >> 3, c = piece & 7;
           const bool there = tk < nk && (kb0 + tk) * kGroup + 16 * c < p.k;
           ar[stage][i] = __builtin_amdgcn_raw_buffer_load_b128(rs_a, there ? (uint32_t)row * (uint32_t)p.k + 16u * c : kOut,
-                                                               (kb0 + tk) * kGroup, 0);
+                                                               offset_block(kb0 + tk, tk < nk) * kGroup, 0);
         }
         sr[stage] = load_scale(tk, tid);
       };

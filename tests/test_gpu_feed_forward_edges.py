@@ -14,7 +14,7 @@ import torch
 
 import fp8_block_scaled_gemm_amd as dg
 from gpu_util import device, say
-from test_gpu_gated_gemm import OF, check_bf16, check_fp8, dequantized, operands, reference, same_bits
+from test_gpu_gated_gemm import OF, alone, check_bf16, check_fp8, dequantized, operands, reference, same_bits
 
 pytestmark = pytest.mark.gpu
 
@@ -73,6 +73,30 @@ def test_lengths_of_k_in_groups(k, monkeypatch):
         if c:
             h, eh = reference(am[g, :c], sm[g, :, :c], c, masked[2][g], masked[3][g], "silu")[2::3]
             check_bf16(dm[g, :c], h, eh, f"expert {g}")
+
+
+@pytest.mark.parametrize("n,k", [(16, 16), (128, 128), (112, 128), (128, 256), (64, 384), (128, 400)])
+def test_one_column_block(n, k, monkeypatch):
+    """One column block of one to four K blocks on the rings of two and three slots: the block scales are a few bytes, and
+    the loads issued for K blocks behind the last one lie outside them (they would start 4 to 12 bytes past their end)."""
+    say("gated one column block", n, k)
+    rng = np.random.default_rng(n + k)
+    a, sa, b, sb = operands(rng, (256,), n, k, groups=2)
+    mi = torch.tensor([1, 0], dtype=torch.int32, device=device()).repeat_interleave(128)
+    h = [reference(a[r], sa[:, r], 128, b[e], sb[e], "silu")[2::3] for r, e in ((slice(0, 128), 1), (slice(128, 256), 0))]
+    h, eh = (np.concatenate(x) for x in zip(*h))
+    for tile in ("256x128", "256x256"):
+        monkeypatch.setenv("DG_PLAN", f"tile={tile},splits=1")
+        pre = torch.full((256, 2 * n), 9.0, dtype=BF16, device=device())
+        check_bf16(dg.dg_gemm_fp8_gated_contiguous(a, sa, b, sb, mi, pre=pre), h, eh, "contiguous")
+        q, s = dg.dg_gemm_fp8_gated_contiguous(a, sa, b, sb, mi, out="fp8")
+        check_fp8(q, s[:, :256].t(), h, eh, "contiguous fp8")
+        for e, rows in ((1, slice(0, 128)), (0, slice(128, 256))):
+            d = dg.dg_gemm_fp8_gated_nt(a[rows], sa[:, rows].contiguous(), alone(b[e]), alone(sb[e]))
+            check_bf16(d, h[rows], eh[rows], "normal")
+            for i in (0, 1):
+                plain = dg.dg_gemm_fp8_nt(a[rows], sa[:, rows].contiguous(), alone(b[e, i]), alone(sb[e, i]))
+                same_bits(pre[rows, i * n:(i + 1) * n], plain, f"projection {i}")
 
 
 def wide_reference(a, sa, rows, b, sb):
