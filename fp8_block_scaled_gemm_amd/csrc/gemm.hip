@@ -287,7 +287,8 @@ __device__ __forceinline__ void fused_act_quant_exit(const GemmParams& p) {
 
 // GATED: b holds two matrices, gate and up; a tile's B rows are BN / 2 rows of each, and a wave's fragment rows the gate and
 // the up rows of the same columns, each half with its own block scale.
-template <class C, int LAYOUT, bool FQ = false, bool GATED = false>
+// EXACT (gated, masked layout, quantized outputs): the tiles of groups of few rows have exact products.
+template <class C, int LAYOUT, bool FQ = false, bool GATED = false, bool EXACT = false>
 __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
   constexpr int NT = C::kThreads;
   constexpr int S = C::STAGES;
@@ -303,6 +304,7 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
   static_assert(NT >= 256, "the masked-layout prefix needs 256 threads");
   static_assert(!FQ || LAYOUT == kDense, "activation quantization in the launch: dense layout only");
   static_assert(!GATED || (!FQ && !kRowB), "the gated form has block scales and quantized activations");
+  static_assert(!EXACT || (GATED && C::PIPE && LAYOUT == kMasked), "exact products by the group's rows");
   constexpr int kCols = GATED ? C::BN / 2 : C::BN;   // output columns of a tile
 
   const int tid = threadIdx.x;
@@ -594,6 +596,13 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
       }
     };
 
+    // A tile of a group of few rows, with exact products: kFew fragment columns of 16 rows a wave, the waves' one after the
+    // other (kWavesM kFew of them are kExactRows rows).
+    constexpr int kFew = EXACT ? kExactRows / 16 / C::kWavesM : 1;
+    static_assert(!EXACT || 16 * kFew * C::kWavesM == kExactRows, "few rows: whole fragments a wave");
+    const bool few_rows = EXACT && t.m_valid <= kExactRows;
+    const int wm = few_rows ? 16 * kFew * wave_m : wm0;   // the wave's first row in the tile
+
     // ---- main loop ---------------------------------------------------------------
     if constexpr (C::PIPE) {
       // Two slots; a K block's operands come from slot tk & 1.  A wave's A fragments (weight rows)
@@ -619,9 +628,9 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
       static_assert(S == 2 || GATED, "three slots: the gated form");
       const int sb_copy = S == 3 ? wave & 3 : wave;
       const int lane_off = lds_off(l16, 2 * g4);
-      // this wave's activation-scale rows m0 + wm0 + lane (64 of them, the wave's WM first) and the
+      // this wave's activation-scale rows m0 + wm + lane (64 of them, the wave's WM first) and the
       // scale of its weight block, as byte offsets within a K block's scale row
-      const int sa_row = m0 + wm0 + lane;
+      const int sa_row = m0 + wm + lane;
       const uint32_t sa_lane_off = sa_row < (int)p.ld_sa ? (uint32_t)sa_row * 4u : kOut;
       int sb_blk_w = (n0 + wn0) >> 7;
       sb_blk_w = sb_blk_w < p.nb128 ? sb_blk_w : p.nb128 - 1;
@@ -676,7 +685,7 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
                         *reinterpret_cast<const u32x4*>(sbase + (off ^ 16)));
       };
       auto read_b = [&](SlotPtr sbase, int j) {
-        const int off = (C::BN + wm0 + 16 * j) * kGroup + lane_off;
+        const int off = (C::BN + wm + 16 * j) * kGroup + lane_off;
         return make_v8i(*reinterpret_cast<const u32x4*>(sbase + off),
                         *reinterpret_cast<const u32x4*>(sbase + (off ^ 16)));
       };
@@ -746,6 +755,18 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
           for (int q = R0 * kFM; q < R1 * kFM; ++q) asm volatile("" : "+v"(acc[q / kFM][q % kFM]));
         }
       };
+      // This wave's reads of block tk's slot are done, and its DMAs of block tk+1 have landed; and so every wave's.
+      auto end_of_block = [&] {
+        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+        if constexpr (S == 3) {
+          // those of block tk+2 fly on (__syncthreads would wait for them too)
+          wait_vmcnt<kStageDmas>();
+          asm volatile("s_barrier" ::: "memory");
+        } else {
+          wait_vmcnt<0>();
+          __syncthreads();
+        }
+      };
       // The barrier of block tk (slot CUR; the next block in slot NXT) and its last two rows.  A
       // loop iteration starts here: it waits for every DMA in flight, so what the compiler's wait
       // insertion cannot track across the loop's back edge costs nothing.  On return a[0], a[1]
@@ -755,15 +776,7 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
         constexpr int nxt_slot = decltype(nxt_c)::value;
         const SlotPtr cur = cur_slot == 0 ? slot0 : cur_slot == 1 ? slot1 : st2;
         const SlotPtr nxt = nxt_slot == 0 ? slot0 : nxt_slot == 1 ? slot1 : st2;
-        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): this wave's reads of slot CUR are done
-        if constexpr (S == 3) {
-          // its DMAs of block tk+1 have landed, those of block tk+2 fly on (__syncthreads would wait for them too)
-          wait_vmcnt<kStageDmas>();
-          asm volatile("s_barrier" ::: "memory");
-        } else {
-          wait_vmcnt<0>();                    // its DMAs of block tk+1 have landed
-          __syncthreads();                    // ... and every wave's
-        }
+        end_of_block();
         const DmaCtx dc = dma_ctx(tk + S, cur_c, tk + S < nk);
         read_scales(nxt, rn);
         rows(IC<kBarRow>{}, IC<kFN>{}, cur, nxt, a, bop, sc, rc, &dc);
@@ -781,6 +794,49 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
       if (nk > 0) {
       issue_pipe(1, IC<1>{}, nk > 1);
       if constexpr (S == 3) issue_pipe(2, IC<2>{}, nk > 2);
+      if (few_rows) {
+        // Codes widened to bf16 (the streaming kernel's products, in its order).  The group's rows are spread over all waves: a
+        // wave takes kFew fragment columns of its weight rows.  The ring as below, every wave at a block's end past all that it
+        // reads of the block.
+        if constexpr (EXACT) {
+          // (no branch between a matrix instruction and what reads its result: the compiler leaves out wait states there)
+          auto block = [&](SlotPtr sbase) __attribute__((always_inline)) {
+            float raw[kFM + 2];
+            read_scales(sbase, raw);
+            Wide held[kFew];
+#pragma unroll
+            for (int j = 0; j < kFew; ++j) held[j] = widen_codes(read_b(sbase, j));
+            // (a row's operands are read one row ahead)
+            v8i next = read_a(sbase, 0);
+#pragma unroll
+            for (int i = 0; i < kFN; ++i) {
+              const v8i now = next;
+              if (i + 1 < kFN) next = read_a(sbase, i + 1);
+              __builtin_amdgcn_sched_barrier(0);
+              const Wide w = widen_codes(now);
+#pragma unroll
+              for (int j = 0; j < kFew; ++j) {
+                const v4f part = exact_product(w, held[j]);
+                const float s = raw[j] * raw[i < kFN / 2 ? kFM : kFM + 1];   // fl32(sa * sb)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(part[r], s, acc[i][j][r]);
+              }
+            }
+          };
+          auto step = [&](int tk, auto slot_c) __attribute__((always_inline)) {
+            constexpr int slot = decltype(slot_c)::value;
+            if (m0 + wm < t.m_valid) block(slot == 0 ? slot0 : slot == 1 ? slot1 : st2);
+            end_of_block();
+            issue_pipe(tk + S, slot_c, tk + S < nk);
+          };
+          for (int tk = 0; tk < nk; tk += S) {
+            step(tk, IC<0>{});
+            if (tk + 1 < nk) step(tk + 1, IC<1>{});
+            if constexpr (S == 3)
+              if (tk + 2 < nk) step(tk + 2, IC<2>{});
+          }
+        }
+      } else {
       v8i bop[kFM], a[3];
       float sc[kFM], r0[kFM + 2], r1[kFM + 2];
 #pragma unroll
@@ -822,6 +878,7 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
       if (tk + 1 < nk) {
         rows(IC<0>{}, IC<kBarRow>{}, slot1, slot0, a, bop, sc, r1, nullptr);
         bar_tail(tk + 1, IC<1>{}, IC<0>{}, a, bop, sc, r0, r1);
+      }
       }
       }
       wait_vmcnt<0>();   // the zero-filling DMAs past the last K block
@@ -915,7 +972,7 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
       static_assert(C::kWavesM * 16 * kGatedPitch * 4 <= kStage && C::BN == 2 * kGroup, "a chunk fits in one ring buffer");
       float* chunk = reinterpret_cast<float*>(st0);
       gated_epilogue<NT, LAYOUT, kTwoPass>(
-          p, t, n0, C::kFragM, C::kWavesM * 16, chunk,
+          p, t, n0, few_rows ? kFew : C::kFragM, C::kWavesM * 16, chunk,
           [&](int c) {
             float* dst = chunk + (wave_m * 16 + l16) * kGatedPitch + wave_n * (C::WN / 2) + 4 * g4;
             // constant indices, in blocks that the compiler cannot merge: the accumulators stay in registers
@@ -933,7 +990,7 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
             else if (c == 2) put(IC<2>{});
             else put(IC<3>{});
           },
-          [&](int c, int r) { return m0 + (r >> 4) * C::WM + 16 * c + (r & 15); });
+          [&](int c, int r) { return m0 + (r >> 4) * (few_rows ? 16 * kFew : C::WM) + 16 * c + (r & 15); });
       __syncthreads();   // the next tile's first DMAs may not meet readers of the chunk
       continue;
     }
@@ -1015,9 +1072,9 @@ struct LaunchInfo {
   int lds_bytes;   // the kernel's static LDS: its __shared__ arrays
 };
 
-template <class C, int LAYOUT, bool FQ = false, bool GATED = false>
+template <class C, int LAYOUT, bool FQ = false, bool GATED = false, bool EXACT = false>
 static LaunchInfo info() {
-  void (*fn)(GemmParams) = gemm_fp8_kernel<C, LAYOUT, FQ, GATED>;
+  void (*fn)(GemmParams) = gemm_fp8_kernel<C, LAYOUT, FQ, GATED, EXACT>;
   constexpr int kStage = stage_bytes<C, LAYOUT>();
   constexpr int kLds = 2 * kStage + (C::STAGES > 2 ? kStage : 16) + (C::STAGES > 3 ? kStage : 16) +
                        4 * (LAYOUT == kMasked ? 1025 + 256 + 1 : 3);
@@ -1438,6 +1495,7 @@ int launch_gemm(int layout, const uint8_t* a, const float* sa, int64_t ld_sa, co
 const void* gated_few_kernel(int layout, int bm, bool quantized);
 int gated_few_lds(int bm);
 int launch_gated_join(int layout, GemmParams p, int bm, hipStream_t stream);
+int launch_check_contiguous(const int32_t* m_indices, int64_t m, int64_t groups, hipStream_t stream);
 
 // The 256x128 tile on three slots (157 KB LDS): weights that only a few row blocks read come from memory, whose latency
 // under load passes the time of this tile's K block (32 groups of 256 rows, half in use, 2048 x 7168: 257 us, with two
@@ -1447,12 +1505,32 @@ using CfgGatedRows128 = Cfg<256, 128, 64, 64, 3, false, true>;
 enum GatedCfgId : int { kGatedRows128 = 0, kGatedSquare, kGatedFew16, kGatedFew64 };
 constexpr int kMaxStreamSplits = 32;
 
+// What a quantized output's products are: cut by the FP8 instruction as a bf16 output's are, exact (the streaming kernel,
+// which widens codes to bf16), or in the masked layout exact in the tiles of groups of at most kExactRows rows.
+enum GatedProducts : int { kCut = 0, kExactFew, kExact };
+
+// The FP8 instruction's cut puts one or two codes in 10^4 of a quantized output a step of 6 to 12% away.  Among 10^6 values
+// that is far below the codes' own rounding; among 10^4, or in the one row of a hundred that is far larger than the others,
+// one such step is the error (384 x 176 x 288, contiguous: 0.0069 and 0.0085 of 9 seeds behind the next product, exact 0.0017
+// of each).  So outputs of at most 2^19 values are quantized from exact products, and those of at most 64 rows: the dense
+// form's, the masked buffer's or, in a larger one, each group's.  No plan decides it.
+constexpr int64_t kExactValues = 1 << 19;
+static GatedProducts gated_products(int layout, int64_t groups, int64_t m, int64_t n, bool quantized) {
+  if (!quantized) return kCut;
+  const int64_t values = layout == kMasked ? groups * m * n : m * n;
+  if (values <= kExactValues || (layout != kContiguous && m <= kExactRows)) return kExact;
+  return layout == kMasked ? kExactFew : kCut;
+}
+
 template <int LAYOUT>
 static LaunchInfo gated_info(int cfg, bool quantized = false) {
-  if (cfg >= kGatedFew16 && LAYOUT != kContiguous) {
+  if (cfg >= kGatedFew16) {
     const int bm = cfg == kGatedFew16 ? 16 : 64;
     return LaunchInfo{256, bm, 512, 2, gated_few_kernel(LAYOUT, bm, quantized), gated_few_lds(bm)};
   }
+  if constexpr (LAYOUT == kMasked)
+    if (quantized)
+      return cfg == kGatedSquare ? info<CfgSquare, LAYOUT, false, true, true>() : info<CfgGatedRows128, LAYOUT, false, true, true>();
   return cfg == kGatedSquare ? info<CfgSquare, LAYOUT, false, true>() : info<CfgGatedRows128, LAYOUT, false, true>();
 }
 
@@ -1484,7 +1562,8 @@ static double gated_estimate(int cfg, double row_blocks, double rows, int64_t st
 static bool gated_join_in_kernel(int cfg, int64_t m, int splits) { return cfg == kGatedFew16 && m * splits <= 64; }
 
 // n: the width of h.
-static Plan make_gated_plan(int layout, int64_t m, int64_t n, int64_t k, int64_t call_groups, int num_cus, bool allow_split) {
+static Plan make_gated_plan(int layout, int64_t m, int64_t n, int64_t k, int64_t call_groups, int num_cus, bool allow_split,
+                            GatedProducts products) {
   const int64_t groups = layout == kMasked ? call_groups : 1;
   const int64_t strips = (n + kGroup - 1) / kGroup;
   const int64_t weight_rows = strips * (2 * kGroup);   // rows of b in whole tiles
@@ -1510,6 +1589,7 @@ static Plan make_gated_plan(int layout, int64_t m, int64_t n, int64_t k, int64_t
   const auto most = [&](int cfg) { return cfg >= kGatedFew16 ? kMaxStreamSplits : kMaxSplits; };
   if (layout == kContiguous) {
     pl.cfg = forced >= 0 ? forced
+             : products == kExact ? kGatedFew64
              : choose_contiguous(m, weight_rows, call_groups, num_cus) == kCfgSquare ? kGatedSquare : kGatedRows128;
   } else {
     // The rows that a group of the masked form has are not known here: between none and m, as likely one as the other (32 x 256
@@ -1518,7 +1598,7 @@ static Plan make_gated_plan(int layout, int64_t m, int64_t n, int64_t k, int64_t
     const bool masked = layout == kMasked;
     double best = 1e30;
     for (const int cfg : {kGatedSquare, kGatedRows128, kGatedFew64, kGatedFew16}) {
-      if (forced >= 0 ? cfg != forced : cfg == kGatedFew16 && m > 16) continue;
+      if (forced >= 0 ? cfg != forced : (cfg == kGatedFew16 && m > 16) || (products == kExact && cfg < kGatedFew16)) continue;
       const int64_t bm = gated_info<kDense>(cfg).bm, most_blocks = (m + bm - 1) / bm;
       const double row_blocks =
           masked ? (double)most_blocks - (double)bm * (double)(most_blocks * (most_blocks - 1)) / (2.0 * (double)m) : (double)most_blocks;
@@ -1549,22 +1629,28 @@ static void gated_plan_name(const Plan& pl, char* buf, size_t len) {
 
 template <int LAYOUT>
 static int launch_gated(GemmParams p, const Plan& pl, hipStream_t stream, int num_cus) {
+  const LaunchInfo li = gated_info<LAYOUT>(pl.cfg, p.q != nullptr);
   if (pl.cfg < kGatedFew16 || pl.splits == 1 || gated_join_in_kernel(pl.cfg, p.m, pl.splits))
-    return launch_info<LAYOUT>(gated_info<LAYOUT>(pl.cfg, p.q != nullptr), p, pl, stream, num_cus);
+    return launch_info<LAYOUT>(li, p, pl, stream, num_cus);
   p.counters = nullptr;   // the second launch ends the tiles
-  const int r = launch_info<LAYOUT>(gated_info<LAYOUT>(pl.cfg, p.q != nullptr), p, pl, stream, num_cus);
+  const int r = launch_info<LAYOUT>(li, p, pl, stream, num_cus);
   return r == kOk ? launch_gated_join(LAYOUT, p, pl.bm, stream) : r;
 }
 
 size_t gemm_gated_workspace_size(int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus) {
-  const size_t masked = make_gated_plan(kMasked, m, n, k, groups, num_cus, true).ws_bytes;
-  const size_t dense = groups == 1 ? make_gated_plan(kDense, m, n, k, 1, num_cus, true).ws_bytes : 0;
-  return masked > dense ? masked : dense;   // (one group may be either form's)
+  size_t most = 0;   // (one group may be either form's, and the output of either kind)
+  for (const int layout : {kMasked, kDense})
+    for (const bool quantized : {false, true})
+      if (layout == kMasked || groups == 1) {
+        const Plan pl = make_gated_plan(layout, m, n, k, groups, num_cus, true, gated_products(layout, groups, m, n, quantized));
+        most = pl.ws_bytes > most ? pl.ws_bytes : most;
+      }
+  return most;
 }
 
 void gemm_gated_config_name(int layout, int64_t m, int64_t n, int64_t k, int64_t groups, int num_cus, char* buf,
                             size_t len) {
-  const Plan pl = make_gated_plan(layout, m, n, k, layout == kDense ? 1 : groups, num_cus, layout != kContiguous);
+  const Plan pl = make_gated_plan(layout, m, n, k, layout == kDense ? 1 : groups, num_cus, layout != kContiguous, kCut);
   gated_plan_name(pl, buf, len);
 }
 
@@ -1579,8 +1665,9 @@ int launch_gemm_gated(int layout, const uint8_t* a, const float* sa, int64_t ld_
     return set_error(kUnsupported, "gated gemm: one group's activation scales must be < 2^31 bytes (k=%lld ld_sa=%lld)",
                      (long long)k, (long long)ld_sa);
   const int64_t plan_groups = layout == kDense ? 1 : groups;
-  Plan pl = make_gated_plan(layout, m, n, k, plan_groups, num_cus, layout != kContiguous && ws != nullptr);
-  if (pl.splits > 1 && ws_bytes < pl.ws_bytes) pl = make_gated_plan(layout, m, n, k, plan_groups, num_cus, false);
+  const GatedProducts products = gated_products(layout, groups, m, n, q != nullptr);
+  Plan pl = make_gated_plan(layout, m, n, k, plan_groups, num_cus, layout != kContiguous && ws != nullptr, products);
+  if (pl.splits > 1 && ws_bytes < pl.ws_bytes) pl = make_gated_plan(layout, m, n, k, plan_groups, num_cus, false, products);
   GemmParams p = make_params(layout, pl, a, sa, ld_sa, b, sb, 0, k, d, m_indices, masked_m, groups, m, n, k);
   p.b_gstride = 2 * n * k;
   p.sb_gstride = 2 * (int64_t)p.nb128 * p.kb_total;
@@ -1600,6 +1687,10 @@ int launch_gemm_gated(int layout, const uint8_t* a, const float* sa, int64_t ld_
     std::fprintf(stderr, "[dg] gated gemm %s m=%lld n=%lld k=%lld groups=%lld: %s workspace=%zu/%zu bytes\n",
                  layout == kContiguous ? "contiguous" : layout == kMasked ? "masked" : "normal", (long long)m, (long long)n,
                  (long long)k, (long long)groups, name, pl.ws_bytes, ws_bytes);
+  }
+  if (p.debug && layout == kContiguous && pl.cfg >= kGatedFew16) {   // (the large tiles check their own blocks)
+    const int r = launch_check_contiguous(m_indices, m, groups, stream);
+    if (r != kOk) return r;
   }
   switch (layout) {
     case kContiguous: return launch_gated<kContiguous>(p, pl, stream, num_cus);

@@ -55,6 +55,9 @@ struct GemmParams {
   int act;
 };
 
+// Groups of at most this many rows have exact products in a quantized output of the gated form, whatever the buffer holds.
+constexpr int kExactRows = 64;
+
 // Flag bits of the device diagnostics word (sticky until read with clearing).
 enum DiagFlag : unsigned {
   kDiagMixedBlock = 1u,    // contiguous layout: a 128-row block whose rows name different experts

@@ -9,6 +9,32 @@ namespace dg {
 
 constexpr int kGatedPitch = 2 * kGroup + 4;   // floats of a row of projections in LDS: 128 gate, 128 up, against bank conflicts
 
+// A lane's 32 codes of a K block as bf16, which holds every E4M3 value: four operands of eight.
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+struct Wide { bf16x8 v[4]; };
+__device__ __forceinline__ Wide widen_codes(const v8i& x) {
+  Wide w;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    bf16x2 p[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      p[2 * i] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * t + i], 1.0f, false);
+      p[2 * i + 1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * t + i], 1.0f, true);
+    }
+    w.v[t] = bf16x8{p[0][0], p[0][1], p[1][0], p[1][1], p[2][0], p[2][1], p[3][0], p[3][1]};
+  }
+  return w;
+}
+// The 16 x 16 products of two such operands over a K block, added to 2^-22 of them.
+__device__ __forceinline__ v4f exact_product(const Wide& a, const Wide& b) {
+  v4f sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int t = 0; t < 4; ++t) sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[t], b.v[t], sum, 0, 0, 0);
+  return sum;
+}
+
 // Eight bf16 values (four words) of a row's columns to dst and on, `count` of them there (8, fewer at the row's end,
 // none or negative past it).  A row of odd length begins at any 2-byte address: where dst is not 4-byte aligned, 16
 // neighbouring lanes shift their values by one, each storing its left neighbour's last one with its first seven.  Called by the

@@ -11,8 +11,8 @@
 //   in flight per CU: 8 waves x 4 KB x D of weights, against one stage of 32 KB of the ring of the large tiles.
 // EXACT, for quantized outputs: the codes are widened to bf16, whose products the matrix instruction adds to 2^-22 of them,
 // where the FP8 instruction cuts them at 2^-13 of their largest.  A bf16 output's rounding hides that; a quantized one
-// has a few codes in each 10^4 so near to a border that they come out on its other side, a step of 6 to 12%, and with
-// few rows no others make up for it (1 x 2048 x 7168, SiLU: 13.4 us for 12.2; 64 rows: 22.5 for 20.8).
+// has a few codes in each 10^4 so near to a border that they come out on its other side, a step of 6 to 12%, and
+// among few values no others make up for it (1 x 2048 x 7168, SiLU: 13.2 us for 11.7; 64 rows: 21.5 for 19.4).
 // K is split over workgroups where there are few tiles: fp32 partials of the rows in use go to the workspace.  Their sums,
 // in the order of the splits, end the rows: taken by a second launch, or, of few bytes, by the last workgroup of a tile to
 // arrive (the hand-off of the plain forms).  A CU takes some 30 bytes a nanosecond from memory, so the last workgroup alone
@@ -48,25 +48,6 @@ struct CfgStream {
 // First float of a split tile's partials: tiles numbered by (group, row block, strip of columns), whether they have rows or not.
 __device__ __forceinline__ int64_t partial_at(const GemmParams& p, int bm, int g, int mb, int nbt, int split) {
   return ((((int64_t)g * p.tiles_m + mb) * p.tiles_n + nbt) * p.splits + split) * bm * (2 * kGroup);
-}
-
-// A lane's 32 codes of a K block as bf16, which holds every E4M3 value: four operands of eight.
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-struct Wide { bf16x8 v[4]; };
-__device__ __forceinline__ Wide widen_codes(const v8i& x) {
-  Wide w;
-#pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    bf16x2 p[4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      p[2 * i] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * t + i], 1.0f, false);
-      p[2 * i + 1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * t + i], 1.0f, true);
-    }
-    w.v[t] = bf16x8{p[0][0], p[0][1], p[1][0], p[1][1], p[2][0], p[2][1], p[3][0], p[3][1]};
-  }
-  return w;
 }
 
 // Every wave's LDS operations are done, and every wave is here.
@@ -114,6 +95,11 @@ __global__ __launch_bounds__(C::kThreads) void gemm_gated_few_kernel(GemmParams 
     t.mb = rest % mblocks;
     t.nbt = rest / mblocks;
     const int m0 = t.mb * C::BM, n0 = t.nbt * kGroup;
+    if constexpr (LAYOUT == kContiguous) {   // a tile lies in one block of 128 rows, so in one expert's rows
+      static_assert(kGroup % C::BM == 0, "a block is whole tiles");
+      t.g = p.m_indices[m0];
+      if (t.g < 0 || t.g >= p.num_groups) continue;   // (uniform)
+    }
     const int rows = t.m_valid - m0;   // rows of this tile (more than BM: all)
     const int kb0 = t.split * p.kb_per_split;
     const int kb1 = kb0 + p.kb_per_split < p.kb_total ? kb0 + p.kb_per_split : p.kb_total;
@@ -173,15 +159,13 @@ __global__ __launch_bounds__(C::kThreads) void gemm_gated_few_kernel(GemmParams 
       else return r;
     };
     auto multiply = [&](const Weights* r, const v8i& act_codes, float sa, float sbg, float sbu, int j) {
-      v4f pg = {0.f, 0.f, 0.f, 0.f}, pu = {0.f, 0.f, 0.f, 0.f};
+      v4f pg, pu;
       if constexpr (EXACT) {
         const Wide act = widen_codes(act_codes);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          pg = __builtin_amdgcn_mfma_f32_16x16x32_bf16(r[0].v[t], act.v[t], pg, 0, 0, 0);
-          pu = __builtin_amdgcn_mfma_f32_16x16x32_bf16(r[1].v[t], act.v[t], pu, 0, 0, 0);
-        }
+        pg = exact_product(r[0], act);
+        pu = exact_product(r[1], act);
       } else {
+        pg = pu = v4f{0.f, 0.f, 0.f, 0.f};
         pg = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(r[0], act_codes, pg, 0, 0, 0, 127, 0, 127);
         pu = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(r[1], act_codes, pu, 0, 0, 0, 127, 0, 127);
       }
@@ -412,6 +396,11 @@ int launch_gated_join(int layout, GemmParams p, int bm, hipStream_t stream) {
 
 template <class C, bool EXACT>
 static const void* few_fn(int layout) {
+  if constexpr (EXACT && !C::kDirect)
+    if (layout == kContiguous) {
+      void (*fn)(GemmParams) = gemm_gated_few_kernel<C, kContiguous, EXACT>;
+      return reinterpret_cast<const void*>(fn);
+    }
   void (*fn)(GemmParams) = layout == kMasked ? gemm_gated_few_kernel<C, kMasked, EXACT> : gemm_gated_few_kernel<C, kDense, EXACT>;
   return reinterpret_cast<const void*>(fn);
 }

@@ -505,6 +505,10 @@ enum dg_act { DG_ACT_SILU = 0, DG_ACT_GELU = 1 };
  * Errors: as the plain forms, an unknown activation, both or neither of d and q, q without s; DG_ERR_UNSUPPORTED where 2 n k or
  * m k reaches 2^31, or KB ld_sa 2^29.  Deterministic; without a K split the g and u of a bf16 output are the bits of the
  * plain forms.
+ * Precision of quantized outputs: the matrix instruction adds eight neighbouring FP8 products cut at 2^-13 of the largest's
+ * power of two.  Products are exact and added in fp32 instead where the output has at most 2^19 values (m n; masked:
+ * num_groups m_max n), where m (m_max) is at most 64, and for the groups of at most 64 rows of a larger masked buffer.
+ * Elsewhere one or two codes in 10^4 may be the neighbours of the nearest ones to h.
  */
 int dg_gemm_fp8_gated_nt(const uint8_t* a, const float* sa, int64_t ld_sa, const uint8_t* b, const float* sb, int act,
                          uint16_t* d, uint8_t* q, float* s, int64_t ld_s, uint16_t* pre, int64_t m, int64_t n, int64_t k,
@@ -672,7 +676,9 @@ const char* dg_gemm_int8_config_name(int layout, int64_t m, int64_t n, int64_t k
  * weights; the normal and masked forms of at most 1024 rows, 96 of at most 64), and "splits=S" likewise; their
  * results stay the same bits.
  * The gated FP8 GEMMs take "tile=256x128" or "tile=256x256", or "stream=16" or 64 (rows of the streaming kernel's
- * tile; not the contiguous form), and "splits=S", to 32 for the streaming kernel.
+ * tile; not the contiguous form), and "splits=S", to 32 for the streaming kernel.  A forced 256x128 or 256x256 tile has the
+ * FP8 instruction's products where the plan's own tile would have exact ones (dg_gemm_fp8_gated_nt).  The name
+ * reported is a bf16 output's plan; the workspace is enough for either output.
  * dg_gemm_config_name and dg_gemm_workspace_size (dg_gemm_int8_..., dg_gemm_fp8_gated_...) report the overridden plan; results stay within
  * the GEMM tolerance (a different K split changes the fp32 summation order).  For measuring the
  * alternatives the planner weighs, not for production use.

@@ -307,3 +307,131 @@ def test_block_in_a_graph_and_on_streams():
         for _, out, _ in graphs:
             for x, y in zip(out, want):
                 same_bits(x, y, f"replay {n}")
+
+
+# ---- exact products of quantized outputs -----------------------------------------------------------
+
+def e4m3(x):
+    """The nearest E4M3 values of float64 x."""
+    return host(torch.from_numpy(x).float().clamp(-448, 448).to(torch.float8_e4m3fn))
+
+
+def check_exact(q, s, a, sa, rows, b, sb, what, act="silu"):
+    """Codes and scales of h from exact products: K blocks added to 2^-22, KB promotions of 2^-24 and two rounded scale products
+    (k at most 1024: below 2^-20 of S = sum |a b|), a tenth of what the FP8 instruction loses of such operands.  A code is
+    the nearest one to h / s, or on the other side of a border that lies within these errors."""
+    av, bv = dequantized(a, sa, rows, b, sb)
+    assert av.shape[1] <= 1024
+    g, u = av @ bv[0].T, av @ bv[1].T
+    eg, eu = (2.0 ** -20 * (np.abs(av) @ np.abs(bv[i]).T) for i in (0, 1))
+    f = OF.act_value(g, act)
+    h = f * u
+    tol = 1.13 * eg * np.abs(u) + np.abs(f) * eu + 1.13 * eg * eu + (10 + 6 * np.abs(OF._arg(g, act)[0])) * 2.0 ** -24 * np.abs(h)
+    v, s = host(q.view(torch.float8_e4m3fn)), host(s)
+    for kb in range(-(-h.shape[1] // 128)):
+        c = slice(128 * kb, min(128 * kb + 128, h.shape[1]))
+        want, most = np.abs(h[:, c]).max(1) / 448, tol[:, c].max(1) / 448
+        assert np.all(np.abs(s[:, kb] - want) <= most + 2.0 ** -23 * want), f"{what}: scales"
+        x, e = h[:, c] / want[:, None], (tol[:, c] + np.abs(h[:, c]) * ((most / want)[:, None] + 2.0 ** -22)) / want[:, None]
+        low, high = e4m3(x - e), e4m3(x + e)
+        assert np.all((v[:, c] >= low) & (v[:, c] <= high)), f"{what}: codes"
+
+
+def cut_operands(lead, n, k, groups=None):
+    """Each K block one product of 2^16 beside 127 of 4, of which the FP8 instruction loses seven (4e-4 of the block): gate and
+    up rows alike, so that h = g^2 times the rows' scales."""
+    d = device()
+    a = torch.full((*lead, k), 2.0, device=d)
+    a[..., ::128] = 256.0
+    w = torch.full((*(() if groups is None else (groups,)), 2, n, k), 2.0, device=d)
+    w[..., ::128] = 256.0
+    sa = torch.ones((*lead[:-1], k // 128, -(-lead[-1] // 4) * 4), device=d)
+    sb = torch.ones((*w.shape[:-2], -(-n // 128), k // 128), device=d)
+    fp8 = lambda t: t.to(torch.float8_e4m3fn).view(torch.uint8)   # noqa: E731
+    return fp8(a), sa, fp8(w), sb
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 128, 128), (5, 2048, 1024), (16, 400, 256), (33, 144, 1024), (64, 16384, 128), (65, 272, 640),
+                                   (200, 176, 288), (1000, 512, 256), (512, 1024, 1024), (8192, 64, 128)])
+def test_exact_products(m, n, k):
+    """Quantized outputs of few rows, or of at most 2^19 values."""
+    say("gated exact", m, n, k)
+    rng = np.random.default_rng(m * n)
+    a, sa, b, sb = operands(rng, (m,), n, k)
+    for use in (True, False):
+        q, s = dg.dg_gemm_fp8_gated_nt(a, sa, b, sb, out="fp8", use_workspace=use)
+        check_exact(q, s[:, :m].t(), a, sa, m, b, sb, "normal")
+    if k % 128 == 0:
+        a, sa, b, sb = cut_operands((m,), n, k)
+        q, s = dg.dg_gemm_fp8_gated_nt(a, sa, b, sb, out="fp8")
+        check_exact(q, s[:, :m].t(), a, sa, m, b, sb, "cut")
+
+
+@pytest.mark.parametrize("experts,n,k", [([0], 128, 128), ([2, 0, -1, 1], 176, 288), ([1, 1, 7, 0, 2, -1, 0], 512, 1024),
+                                         ([0] * 20 + [2] * 12, 128, 640)])
+def test_exact_products_contiguous(experts, n, k):
+    say("gated exact contiguous", experts, n, k)
+    rng = np.random.default_rng(n + k)
+    m, groups = 128 * len(experts), 3
+    mi = torch.tensor(np.repeat(experts, 128), dtype=torch.int32, device=device())
+    for made in (operands(rng, (m,), n, k, groups), cut_operands((m,), n, k, groups) if k % 128 == 0 else None):
+        if made is None:
+            continue
+        a, sa, b, sb = made
+        q = torch.full((m, n), 0x11, dtype=torch.uint8, device=device())
+        s = torch.full((-(-n // 128), m + 4), 9.0, device=device())
+        pre = torch.full((m, 2 * n), 9.0, dtype=BF16, device=device())
+        dg.dg_gemm_fp8_gated_contiguous(a, sa, b, sb, mi, act="gelu", out="fp8", q=q, s=s, pre=pre)
+        assert torch.all(s[:, m:] == 9.0)
+        for i, e in enumerate(experts):
+            r = slice(128 * i, 128 * i + 128)
+            if not 0 <= e < groups:
+                assert torch.all(q[r] == 0x11) and torch.all(s[:, r] == 9.0) and torch.all(pre[r] == 9.0)
+                continue
+            check_exact(q[r], s[:, r].t(), a[r], sa[:, r], 128, b[e], sb[e], f"block {i}", "gelu")
+            g, u, _, eg, eu, _ = reference(a[r], sa[:, r], 128, b[e], sb[e], "gelu")
+            check_bf16(pre[r, :n], g, eg, "gate")
+            check_bf16(pre[r, n:], u, eu, "up")
+
+
+@pytest.mark.parametrize("plan", ["", "tile=256x128,splits=1", "tile=256x256,splits=1", "tile=256x128,splits=2",
+                                  "tile=256x256,splits=3"])
+@pytest.mark.parametrize("m,n,k", [(300, 512, 256), (260, 560, 1024), (1100, 144, 400)])
+def test_exact_products_masked(plan, m, n, k, monkeypatch):
+    """A large buffer: groups of at most 64 rows on every tile, beside full ones; their codes are those of a buffer of their
+    own size where no K split changes the order of the sums."""
+    if plan:
+        monkeypatch.setenv("DG_PLAN", plan)
+    say("gated exact masked", plan, m, n, k)
+    rng = np.random.default_rng(m + n)
+    counts = [1, m, 17, 64, 0, 3, 48, 65, 33]
+    groups = len(counts)
+    assert groups * m * n > 1 << 19
+    masked = torch.tensor(counts, dtype=torch.int32, device=device())
+    kinds = [operands(rng, (groups, m), n, k, groups)]
+    if k % 128 == 0:
+        kinds.append(cut_operands((groups, m), n, k, groups))
+    for a, sa, b, sb in kinds:
+        q = torch.full((groups, m, n), 0x11, dtype=torch.uint8, device=device())
+        s = torch.full((groups, -(-n // 128), -(-m // 4) * 4), 9.0, device=device())
+        pre = torch.full((groups, m, 2 * n), 9.0, dtype=BF16, device=device())
+        ws = torch.zeros(256 << 20, dtype=torch.uint8, device=device())
+        dg.dg_gemm_fp8_gated_masked(a, sa, b, sb, masked, out="fp8", q=q, s=s, pre=pre, workspace=ws)
+        assert torch.all(ws[:65536] == 0)
+        for j, c in enumerate(counts):
+            assert torch.all(q[j, c:] == 0x11) and torch.all(s[j, :, c:] == 9.0) and torch.all(pre[j, c:] == 9.0)
+            if 0 < c <= 64:
+                check_exact(q[j, :c], s[j, :, :c].t(), a[j, :c], sa[j], c, b[j], sb[j], f"group of {c}")
+                g, u, _, eg, eu, _ = reference(a[j, :c], sa[j], c, b[j], sb[j], "silu")
+                check_bf16(pre[j, :c, :n], g, eg, "gate")
+                check_bf16(pre[j, :c, n:], u, eu, "up")
+                if plan.endswith("splits=1"):
+                    monkeypatch.setenv("DG_PLAN", "splits=1")
+                    q2, s2 = dg.dg_gemm_fp8_gated_nt(alone(a[j, :c]), alone(sa[j]), alone(b[j]), alone(sb[j]), out="fp8")
+                    monkeypatch.setenv("DG_PLAN", plan)
+                    same_bits(q[j, :c], q2, "codes of the group alone")
+                    same_bits(s[j, :, :c], s2[:, :c], "scales of the group alone")
+            elif c:
+                _, _, h, _, _, eh = reference(a[j, :c], sa[j], c, b[j], sb[j], "silu")
+                if a is kinds[0][0]:
+                    check_fp8(q[j, :c], s[j, :, :c].t(), h, eh, "fp8")
