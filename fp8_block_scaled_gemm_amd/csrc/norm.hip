@@ -683,11 +683,18 @@ static void norm_grad_shape(int64_t hidden, int* lt, int* v) {
 
 // Its workgroups and the rows of each: as many as the CUs hold at once (three of 256 threads, two with twice the columns,
 // one of 512; 8191 x 2048 42.9 us with the sums, 47.9 with 1024 workgroups).
+// A lane adds at most 256 rows of a column one after the other (more only past 2^24 rows of up to 1024, 2^22 of longer
+// ones, where the partials of the second step would be the longer chain): the error of a sum is below 2^-24 times its two
+// chains, rows and partials, of its terms' magnitudes.
 static void norm_grad_parts(int64_t rows, int64_t hidden, int64_t* per_part, int* parts) {
   int lt, v;
   norm_grad_shape(hidden, &lt, &v);
   const int64_t most = v == 1 ? 768 : lt <= 256 ? 512 : 256;
+  const int64_t groups = lt >= kNormThreads ? 1 : kNormThreads / lt;
+  int64_t chain = 256;
+  while (kSumAlong * groups * chain * chain < rows) chain *= 2;
   *per_part = (rows + most - 1) / most;
+  if (*per_part > groups * chain) *per_part = groups * chain;
   *parts = rows == 0 ? 0 : (int)((rows + *per_part - 1) / *per_part);
 }
 

@@ -601,7 +601,8 @@ int dg_residual_norm_int8(const void* x, const void* residual, int dtype, int re
  * for none), x (NULL as there) and sum as the forward pass stored it:
  *   dresidual (residual_dtype; it may be dsum itself) and dx (`dtype`; NULL with x), written;
  *   dweight, dpost_weight fp32 (hidden,), dgate (gate_rows, hidden) in `dtype`: written where not NULL (sums over the rows,
- *   in fp32 in a fixed order, rounded once; NULL where there is no weight, norm or gate).
+ *   in fp32 in a fixed order, at most 256 rows one after the other up to 2^22 of them, rounded once; NULL where there is no
+ *   weight, norm or gate).
  * workspace : dg_residual_norm_grad_workspace_size(rows, hidden) bytes of any content; calls that share it must be ordered.
  *   Not needed (NULL) where dweight, dpost_weight and dgate are NULL.
  * Errors: as dg_residual_norm; DG_ERR_WORKSPACE.  rows = 0 writes zeros to the three sums.

@@ -259,3 +259,52 @@ def test_scales_of_every_size(power):
     want, ws = dg.dg_quantize_per_token_group(h)
     same_bits(q, want)
     same_bits(s[:, :64], ws[:, :64])
+
+
+# ---- the norm gradient's sums over many rows --------------------------------------------------------
+
+MANY_ROWS = [(16384, 1024, 1), (16384, 1024, 4096), (24000, 64, 1), (24000, 64, 3), (24000, 64, 80), (24000, 64, 12000), (24000, 1008, 240),
+             (9000, 2048, 9), (9000, 2048, 1500), (16384, 7168, 1), (16384, 7168, 64), (4100, 16384, 4), ((1 << 20) + 96, 64, 1),
+             ((1 << 20) + 96, 64, 8), ((1 << 20) + 96, 64, 32771), (300000, 1040, 1), (300000, 1040, 750)]
+
+
+@pytest.mark.parametrize("rows,hidden,gates", MANY_ROWS)
+def test_norm_grad_sums_of_many_rows(rows, hidden, gates):
+    """Many rows for every row group of a workgroup, gates shorter and longer than its rows: sums of small integers (rows of +-1
+    have the norm 1), which fp32 holds exactly, so that each row counts once and in its gate only."""
+    say("norm grad many rows", rows, hidden, gates)
+    d = device()
+    gen = torch.Generator(device=d).manual_seed(rows + hidden)
+    ints = lambda n: torch.randint(-n, n + 1, (rows, hidden), generator=gen, device=d)   # noqa: E731
+    s = 1.0 - 2.0 * torch.randint(0, 2, (rows, hidden), generator=gen, device=d)
+    w = torch.ones(hidden, device=d)
+    dy = ints(3).float()
+    dy[-1], dy[0] = 50.0, -40.0
+    got = dg.dg_residual_norm_grad(dy, None, None, s, w, eps=0.0)
+    assert torch.equal(got.dweight.double(), (dy.double() * s).sum(0))
+    del got
+    # dz = dsum without dy; the gate's gradient of dsum x, the first norm's of dsum gate x
+    for dtype in (torch.float32, BF16):
+        dsum, zero = ints(2).float(), torch.zeros((rows, hidden), dtype=dtype, device=d)
+        dsum[-1], dsum[rows // 2] = 30.0, -20.0
+        x = (1.0 - 2.0 * torch.randint(0, 2, (rows, hidden), generator=gen, device=d)).to(dtype)
+        gate = torch.randint(-2, 3, (gates, hidden), generator=gen, device=d).to(dtype)
+        got = dg.dg_residual_norm_grad(zero, dsum, x, s, w, gate=gate, post_norm=True, post_weight=w, eps=0.0)
+        each = (dsum * x).view(gates, rows // gates, hidden).sum(1, dtype=torch.float64)
+        assert torch.equal(got.dgate.double(), each.to(dtype).double())
+        assert torch.equal(got.dpost_weight.double(), (each * gate).sum(0))
+        assert torch.equal(got.dweight, torch.zeros_like(w))
+
+
+@pytest.mark.parametrize("rows,hidden", [(1 << 24, 32), (1 << 20, 1040)])
+def test_norm_grad_chains(rows, hidden):
+    """One term over and over, whose sum fp32 rounds to the same side every time: chains of at most 256 rows (2^24 rows of up to
+    1024, 2^22 of longer ones) and of rows / (64 * 256 * row groups) partials, and 16 more additions."""
+    say("norm grad chains", rows, hidden)
+    d = device()
+    term = 1.0 + 2.0 ** -12 + 2.0 ** -14
+    s, dy = torch.ones((rows, hidden), device=d), torch.full((rows, hidden), term, device=d)
+    got = dg.dg_residual_norm_grad(dy, None, None, s, torch.ones(hidden, device=d), eps=0.0).dweight.double()
+    groups = 4 if hidden <= 1024 else 1
+    chains = 256 + rows / (64 * 256 * groups) + 16
+    assert torch.all((got / (rows * term) - 1).abs() <= chains * 2.0 ** -24)
