@@ -302,7 +302,7 @@ def test_norm_grad_chains(rows, hidden):
     1024, 2^22 of longer ones) and of rows / (64 * 256 * row groups) partials, and 16 more additions."""
     say("norm grad chains", rows, hidden)
     d = device()
-    term = 1.0 + 2.0 ** -12 + 2.0 ** -14
+    term = 1.0 + 7 * 2.0 ** -16
     s, dy = torch.ones((rows, hidden), device=d), torch.full((rows, hidden), term, device=d)
     got = dg.dg_residual_norm_grad(dy, None, None, s, torch.ones(hidden, device=d), eps=0.0).dweight.double()
     groups = 4 if hidden <= 1024 else 1
