@@ -983,7 +983,9 @@ def _gated_operands(a, sa, b, sb, groups):
         _require(shape[-2] % 256 == 0, "b ([G,] 2N, K) needs N a multiple of 128")
         n = shape[-2] // 2
     kb = -(-k // 128)
-    _require(sb.numel() == (groups if lead else 1) * 2 * -(-n // 128) * kb, "sb must be ([G,] 2, ceil(N/128), ceil(K/128))")
+    nb, of = -(-n // 128), (groups,) if lead else ()
+    if sb.shape != (*of, 2, nb, kb) and sb.shape != (*of, 2 * nb, kb):   # (an axis order is not seen in the data)
+        raise ValueError("sb must be ([G,] 2, ceil(N/128), ceil(K/128)) or ([G,] 2 ceil(N/128), ceil(K/128))")
     return n, k, kb
 
 

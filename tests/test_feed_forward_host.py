@@ -115,6 +115,30 @@ def test_gated_binding_refusals():
             bad()
 
 
+def test_gated_scale_shapes():
+    """Weight scales of another axis order have as many elements: refused, not read as if they were in order."""
+    n, k, g = 384, 256, 3
+    a, sa = torch.zeros((128, k), dtype=torch.uint8), torch.zeros((2, 128))
+    mi, mm = torch.zeros(128, dtype=torch.int32), torch.zeros(g, dtype=torch.int32)
+    b, stacked = torch.zeros((g, 2, n, k), dtype=torch.uint8), torch.zeros((g, 2 * n, k), dtype=torch.uint8)
+    right, right_stacked = torch.zeros((g, 2, 3, 2)), torch.zeros((g, 6, 2))
+    for sb in (right.transpose(2, 3), right.transpose(0, 1), right.transpose(2, 3).contiguous(), torch.zeros((2, g, 3, 2)),
+               torch.zeros((g, 2, 6)), torch.zeros((6, g, 2)), torch.zeros((g, 3, 4))):
+        assert sb.numel() == right.numel()
+        for w in (b, stacked):
+            with pytest.raises(ValueError, match="sb must be"):
+                dg.dg_gemm_fp8_gated_contiguous(a, sa, w, sb, mi)
+            with pytest.raises(ValueError, match="sb must be"):
+                dg.dg_gemm_fp8_gated_masked(torch.zeros((g, 8, k), dtype=torch.uint8), torch.zeros((g, 2, 8)), w, sb, mm)
+    for w in (b[0], stacked[0]):
+        for sb in (torch.zeros((2, 2, 3)), torch.zeros((3, 2, 2)), torch.zeros((2, 6)), torch.zeros((1, 6, 2))):
+            with pytest.raises(ValueError, match="sb must be"):
+                dg.dg_gemm_fp8_gated_nt(a, sa, w, sb)
+        for sb in (right[0], right_stacked[0]):   # in order, whichever the weights' shape: refused for the device alone
+            with pytest.raises(ValueError, match="CUDA"):
+                dg.dg_gemm_fp8_gated_nt(a, sa, w, sb)
+
+
 def test_act_refusals(lib):
     def act(pre=P, dt=1, a=0, mi=None, mm=None, per=0, rows=32, n=64, h=P):
         return lib.dg_gated_act(pre, dt, a, mi, mm, per, rows, n, h, None)
