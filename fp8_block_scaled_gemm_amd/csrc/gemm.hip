@@ -303,7 +303,7 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
   __shared__ int s_flag;
   static_assert(NT >= 256, "the masked-layout prefix needs 256 threads");
   static_assert(!FQ || LAYOUT == kDense, "activation quantization in the launch: dense layout only");
-  static_assert(!GATED || (!FQ && !kRowB), "the gated form has block scales and quantized activations");
+  static_assert(!GATED || (!FQ && !kRowB && C::PIPE), "the gated form has block scales and quantized activations");
   static_assert(!EXACT || (GATED && C::PIPE && LAYOUT == kMasked), "exact products by the group's rows");
   constexpr int kCols = GATED ? C::BN / 2 : C::BN;   // output columns of a tile
 
@@ -451,10 +451,9 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
     // chunks of sb[kb][n0 .. n0+BN), clamped to the caller's ld_sb row.
     const int sbr_lane = iw * C::kSbRowLanesPerWave + lane;
     const bool sb_active =
-        issuer && (kRowB ? (lane < C::kSbRowLanesPerWave && sbr_lane < C::BN / 4) : lane < (GATED ? 2 : C::kSbCount));
+        issuer && (kRowB ? (lane < C::kSbRowLanesPerWave && sbr_lane < C::BN / 4) : lane < C::kSbCount);
     int sb_blk = (n0 >> 7) + lane;
     sb_blk = sb_blk < p.nb128 ? sb_blk : p.nb128 - 1;
-    if constexpr (GATED) sb_blk = (n0 >> 7) + (lane & 1) * p.nb128;   // the gate's block and the up matrix's
     int sbr_row = n0 + 4 * sbr_lane;
     sbr_row = sbr_row + 4 <= p.ld_sb ? sbr_row : (int)p.ld_sb - 4;
     const uint32_t sb_src = kRowB ? (uint32_t)sbr_row * 4u : (uint32_t)sb_blk * (uint32_t)p.kb_total * 4u;
@@ -547,7 +546,7 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
       const float* sa_l = reinterpret_cast<const float*>(sbase + C::kSaOffset);
       // block scales: scale[j] = fl32(sa * sb) of the lane's row, the wave's weight block; per-row
       // B scales: scale[j] = sa, and the 4 scales of the lane's 4 B rows of fragment i in sbr[i]
-      float scale[C::kFragM], scale_up[C::kFragM];
+      float scale[C::kFragM];
       v4f sbr[kRowB ? C::kFragN : 1];
       if constexpr (kRowB) {
 #pragma unroll
@@ -556,14 +555,9 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
         for (int i = 0; i < C::kFragN; ++i)
           sbr[i] = *reinterpret_cast<const v4f*>(sbase + C::kSbOffset + 4 * (wn0 + 16 * i + 4 * g4));
       } else {
-        const float sbv = sa_l[C::BM + (wave % C::kIssuers) * (C::kSbWaveBytes / 4) + (GATED ? 0 : sb_idx)];   // an issuer's copy
+        const float sbv = sa_l[C::BM + (wave % C::kIssuers) * (C::kSbWaveBytes / 4) + sb_idx];   // an issuer's copy
 #pragma unroll
         for (int j = 0; j < C::kFragM; ++j) scale[j] = sa_l[wm0 + 16 * j + l16] * sbv;   // fl32(sa * sb)
-        if constexpr (GATED) {
-          const float sbu = sa_l[C::BM + (wave % C::kIssuers) * (C::kSbWaveBytes / 4) + 1];
-#pragma unroll
-          for (int j = 0; j < C::kFragM; ++j) scale_up[j] = sa_l[wm0 + 16 * j + l16] * sbu;
-        }
       }
 
       constexpr int Q = C::kFragN * C::kFragM;
@@ -585,8 +579,7 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
           const int i = (q - 1) / C::kFragM, j = (q - 1) % C::kFragM;
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            acc[i][j][r] = __builtin_fmaf(part[(q - 1) & 1][r], kRowB ? scale[j] * sbr[kRowB ? i : 0][r]
-                                                               : GATED && i >= C::kFragN / 2 ? scale_up[j] : scale[j],
+            acc[i][j][r] = __builtin_fmaf(part[(q - 1) & 1][r], kRowB ? scale[j] * sbr[kRowB ? i : 0][r] : scale[j],
                                           acc[i][j][r]);   // kRowB: fl32(sa * sb) per element
         }
         if (q > 0 && q < Q) {
