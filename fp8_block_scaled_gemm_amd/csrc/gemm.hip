@@ -752,7 +752,8 @@ __global__ __launch_bounds__(C::kThreads) void gemm_fp8_kernel(GemmParams p) {
       auto end_of_block = [&] {
         __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
         if constexpr (S == 3) {
-          // those of block tk+2 fly on (__syncthreads would wait for them too)
+          // Those of block tk+2 fly on.  (__syncthreads and fences of LDS wait for them too: to the compiler they are writes
+          // that the barrier makes visible.  Nothing reads their slot before the barrier after the wait for them.)
           wait_vmcnt<kStageDmas>();
           asm volatile("s_barrier" ::: "memory");
         } else {

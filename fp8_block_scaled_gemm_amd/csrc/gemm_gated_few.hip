@@ -50,8 +50,13 @@ __device__ __forceinline__ int64_t partial_at(const GemmParams& p, int bm, int g
   return ((((int64_t)g * p.tiles_m + mb) * p.tiles_n + nbt) * p.splits + split) * bm * (2 * kGroup);
 }
 
-// Every wave's LDS operations are done, and every wave is here.
-__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+// Every wave's LDS operations are done, and every wave is here: __syncthreads with fences of LDS alone, so that loads from
+// memory into registers fly on over it.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
 
 template <class C, int LAYOUT, bool EXACT>
 __global__ __launch_bounds__(C::kThreads) void gemm_gated_few_kernel(GemmParams p) {
