@@ -277,9 +277,9 @@ __global__ __launch_bounds__(kGradThreads) void gated_act_grad_fp8_kernel(ActGra
     }
     __syncthreads();   // (and the previous matrix's codes are read)
     if (tid < kGroup) {
-      float a = s_max[0][tid];
+      float a = 0.0f;   // (a group of nothing but NaN has the scale 1, as in the quantizer of columns)
 #pragma unroll
-      for (int w = 1; w < kGradThreads / 64; ++w) a = fmaxf(a, s_max[w][tid]);
+      for (int w = 0; w < kGradThreads / 64; ++w) a = fmaxf(a, s_max[w][tid]);
       const GroupScale s = group_scale(a);
       s_scale[tid] = s.d;
       if ((tid & 63) == 0) s_plain[tid >> 6] = s.plain;

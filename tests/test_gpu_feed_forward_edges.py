@@ -308,3 +308,30 @@ def test_norm_grad_chains(rows, hidden):
     groups = 4 if hidden <= 1024 else 1
     chains = 256 + rows / (64 * 256 * groups) + 16
     assert torch.all((got / (rows * term) - 1).abs() <= chains * 2.0 ** -24)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF16])
+def test_act_grad_fp8_of_nan(dtype):
+    """Groups of nothing but NaN, of NaN beside numbers and beside infinities, by rows and by columns: the library's quantizers' bits."""
+    say("act grad fp8 nan", dtype)
+    g = torch.Generator(device=device()).manual_seed(5)
+    rows, n, nan = 272, 256, float("nan")
+    pre = torch.randn((rows, 2 * n), generator=g, device=device()).to(dtype)
+    dh = torch.randn((rows, n), generator=g, device=device()).to(dtype)
+    pre[:, n + 7] = nan           # columns of one projection
+    pre[128:256, 9] = nan
+    dh[3] = nan                   # a row
+    dh[140:150, 40] = nan
+    dh[200, 130] = float("inf")
+    dh[201:205, 130] = nan
+    dh[256:, 200] = nan           # a partial group of rows
+    wide = dg.dg_gated_act_grad(dh.float(), pre.float())
+    h = dg.dg_gated_act(pre.float())
+    got = dg.dg_gated_act_grad_fp8(dh, pre)
+    want = (*dg.dg_quantize_per_token_group(wide), *dg.dg_quantize_per_channel_group(wide), *dg.dg_quantize_per_channel_group(h))
+    for i, (a, b) in enumerate(zip(got, want)):
+        b = b[..., :a.shape[-1]]
+        assert torch.equal(torch.isnan(a.float()), torch.isnan(b.float())), f"output {i}"
+        if a.dtype == torch.float32:   # (any NaN is one)
+            a, b = a.nan_to_num(nan=0.0, posinf=float("inf")), b.nan_to_num(nan=0.0, posinf=float("inf"))
+        same_bits(a, b, f"output {i}")
