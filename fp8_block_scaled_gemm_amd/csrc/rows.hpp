@@ -154,16 +154,17 @@ __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x
 // Quotients by one scale: x r corrected by its exact remainder, r = 1 / s rounded.  They are the IEEE quotients wherever that
 // decides a code: the correction's error is below 2^-24 of a last place, so only a quotient that close to the middle of
 // two fp32 numbers could round otherwise, and a code needs that middle to lie beside a middle of two codes.
-// None of the few pairs of significands that come so near does (enumerated for the middles of E4M3 and of the integers to
-// 127).  Scales outside [2^-60, 2^60], where the remainder may not be exact, take the division itself; above that a
-// quotient whose remainder is not exact is below 2^-40, code 0.  Three instructions a value instead of ten.
+// None of the few pairs of significands that come so near does (the tests compare the codes with those of divisions for every
+// significand of a group's largest value, at the borders of E4M3's codes and their neighbours).  Scales outside [2^-60, 2^60],
+// where the remainder may not be exact, take the division itself; above that a quotient whose remainder is not exact is below
+// 2^-40, code 0.  Three instructions a value instead of ten.
 struct Divisor { float s, r; };
 __device__ __forceinline__ bool scale_in_range(float s) { return __float_as_uint(s) - 0x21800000u <= 0x3c000000u; }
 
 // An E4M3 scale by the rule of the per-token-group quantizer, amax / 448, 1 for an all-zero group, and its reciprocal, both
 // with the bits of IEEE divisions: a product by 1 / 448, and the hardware's reciprocal, each corrected by its exact
-// remainder (compared with the divisions for every number from 2^-60 to 2^70 on the device); the divisions themselves
-// where a scale of the wave lies outside [2^-60, 2^60].  Seven instructions instead of twenty.
+// remainder (every significand of amax in the tests, at four powers of two; the powers change no rounding in the range); the
+// divisions themselves where a scale of the wave lies outside [2^-60, 2^60].  Seven instructions instead of twenty.
 struct GroupScale {
   Divisor d;
   bool plain;   // every active lane's scale lies in the range: quotient<true> serves
@@ -194,7 +195,7 @@ __device__ __forceinline__ float quotient(float x, Divisor d) {
   return __builtin_fmaf(-__builtin_fmaf(q, d.s, -x), d.r, q);   // (in this order -0 stays -0)
 }
 // Four values saturated to E4M3's range (a NaN to -448, as clamp448) -> their codes, packed little-endian.  The conversion
-// keeps the sign of what it rounds to zero, and of -0 (checked on all 2^32 inputs).
+// keeps the sign of what it rounds to zero, and of -0 (the tests quantize every number from -448 to 448 at scale 1).
 __device__ __forceinline__ uint32_t codes4_e4m3(float a, float b, float c, float d) {
   auto sat = [](float v) { return __builtin_amdgcn_fmed3f(v, -kE4M3Max, kE4M3Max); };
   const int w = __builtin_amdgcn_cvt_pk_fp8_f32(sat(a), sat(b), 0, false);

@@ -310,6 +310,55 @@ def test_norm_grad_chains(rows, hidden):
     assert torch.all((got / (rows * term) - 1).abs() <= chains * 2.0 ** -24)
 
 
+# ---- quantization by corrected products, against the library's divisions ---------------------------
+
+def quantized_products(x):
+    """(codes, scales) of dg_gated_act_fp8 for h = x exactly, and of the library's quantizer for x: 2^5 sigmoid(2^5) is 2^5."""
+    pre = torch.cat((torch.full_like(x, 32.0), x * 2.0 ** -5), 1)
+    got = dg.dg_gated_act_fp8(pre)
+    del pre
+    return got, dg.dg_quantize_per_token_group(x)
+
+
+@pytest.mark.parametrize("power", [-52, 0, 8, 66])
+def test_every_significand_of_a_scale(power):
+    """All 2^23 significands of a group's largest value, so every scale and reciprocal of a power of two; with each the
+    values around every border of two codes times that scale (the odd sixteenths above 1 and the odd ones of the subnormal
+    codes, and their two neighbours on each side), where a quotient rounded otherwise would be another code."""
+    say("significands", power)
+    d = device()
+    borders = torch.tensor([(16 + i) / 16.0 for i in range(1, 16, 2)] + [i / 1024.0 for i in range(1, 16, 2)], device=d, dtype=torch.float64)
+    for start in range(0, 1 << 23, 1 << 20):
+        bits = torch.arange(start, start + (1 << 20), device=d, dtype=torch.int32)
+        amax = (bits + ((127 + power) << 23)).view(torch.float32)
+        s = (amax / torch.full_like(amax, 448.0)).double()
+        at = (s[:, None] * borders[None]).float()
+        near = torch.cat([(at.view(torch.int32) + i).view(torch.float32) for i in range(-2, 3)], 1)   # 80 values
+        near[:, ::2] *= -1.0
+        x = torch.cat((amax[:, None], near, torch.zeros((1 << 20, 15), device=d)), 1).contiguous()
+        (q, sq), (want, sw) = quantized_products(x)
+        same_bits(q, want, f"codes from {start}")
+        same_bits(sq, sw[:, :1 << 20], f"scales from {start}")
+
+
+def test_every_value_at_scale_one():
+    """Every fp32 number from 0 to 448, of both signs, in groups whose scale is 1: codes, signs of zeros among them."""
+    say("every value")
+    d = device()
+    top = 0x43e00000   # 448
+    step = 127 << 20
+    for start in range(0, top + 1, step):
+        bits = torch.arange(start, start + step, device=d, dtype=torch.int64).clamp_(max=top).to(torch.int32)
+        for sign in (1.0, -1.0):
+            v = (bits.view(torch.float32) * sign).view(-1, 127)
+            x = torch.cat((torch.full((v.shape[0], 1), 448.0, device=d), v), 1).contiguous()
+            # (numbers that x / 32 does not hold are as good a probe after the product as before it)
+            x = x * 2.0 ** -5 * 2.0 ** 5
+            (q, sq), (want, sw) = quantized_products(x)
+            same_bits(q, want, f"from {start:#x} {sign}")
+            assert torch.all(sq[:, :x.shape[0]] == 1)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, BF16])
 def test_act_grad_fp8_of_nan(dtype):
     """Groups of nothing but NaN, of NaN beside numbers and beside infinities, by rows and by columns: the library's quantizers' bits."""
