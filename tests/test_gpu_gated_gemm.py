@@ -435,3 +435,20 @@ def test_exact_products_masked(plan, m, n, k, monkeypatch):
                 _, _, h, _, _, eh = reference(a[j, :c], sa[j], c, b[j], sb[j], "silu")
                 if a is kinds[0][0]:
                     check_fp8(q[j, :c], s[j, :, :c].t(), h, eh, "fp8")
+
+
+def test_contiguous_checks_of_every_tile(monkeypatch):
+    """DG_DEBUG reports a block that names two experts on the large tiles and on the streaming one, and a good layout as good."""
+    say("gated debug")
+    rng = np.random.default_rng(12)
+    a, sa, b, sb = operands(rng, (512,), 256, 256, 3)
+    good = torch.tensor(np.repeat([0, 2, -1, 1], 128), dtype=torch.int32, device=device())
+    mixed, outside = good.clone(), good.clone()
+    mixed[130] = 1
+    outside[384:] = 5
+    monkeypatch.setenv("DG_DEBUG", "1")
+    dg.dg_get_debug_status(clear=True)
+    for out in ("bf16", "fp8"):
+        for mi, flag, block in ((good, 0, -1), (mixed, 1, 1), (outside, 2, 3)):
+            dg.dg_gemm_fp8_gated_contiguous(a, sa, b, sb, mi, out=out)
+            assert dg.dg_get_debug_status(clear=True) == (flag, block), (out, flag)
