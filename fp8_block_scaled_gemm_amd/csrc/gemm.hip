@@ -1484,7 +1484,7 @@ int launch_gemm(int layout, const uint8_t* a, const float* sa, int64_t ld_sa, co
 // ---- gated form: both projections of a feed-forward block, the activation and the product ------
 // The large tiles of the plain forms, with 128 gate and 128 up rows for 256 rows of weights; for few rows the kernel that
 // streams the weights (csrc/gemm_gated_few.hip), with tiles of 16 or 64 rows.  A wave of a large tile holds gate and up
-// fragments of the same columns, so the epilogue needs no other workgroup.  8192 x 8192 x 7168: 1653 us, 2.33e15 operations/s,
+// fragments of the same columns, so the epilogue needs no other workgroup.  16384 x 8192 x 7168: 1662 us, 2.3e15 operations/s,
 // the matrix cores busy for half of the cycles and the promotion's FMAs for the other half, as in the plain form.
 const void* gated_few_kernel(int layout, int bm, bool quantized);
 int gated_few_lds(int bm);
@@ -1492,8 +1492,8 @@ int launch_gated_join(int layout, GemmParams p, int bm, hipStream_t stream);
 int launch_check_contiguous(const int32_t* m_indices, int64_t m, int64_t groups, hipStream_t stream);
 
 // The 256x128 tile on three slots (157 KB LDS): weights that only a few row blocks read come from memory, whose latency
-// under load passes the time of this tile's K block (32 groups of 256 rows, half in use, 2048 x 7168: 257 us, with two
-// slots 275; contiguous, 8 groups in 8192 rows: 285, with two slots 350).
+// under load passes the time of this tile's K block (32 groups of 256 rows, half in use, 2048 x 7168: 250 us, with two
+// slots 277; contiguous, 8 groups in 8192 rows: 285, with two slots 312).
 using CfgGatedRows128 = Cfg<256, 128, 64, 64, 3, false, true>;
 
 enum GatedCfgId : int { kGatedRows128 = 0, kGatedSquare, kGatedFew16, kGatedFew64 };
@@ -1532,7 +1532,9 @@ static LaunchInfo gated_info(int cfg, bool quantized = false) {
 // `strips` strips of weights.  From timings of every choice on MI355X over 15 dense shapes of 1 to 1024 rows, n 256 to 8192,
 // k 1024 to 7168 (cold weights), and 30 masked ones: a start, the K blocks of a workgroup one after the other, in rounds of
 // the CUs, and the weights' bytes at 5 TB/s (4.4 on 16-row tiles); and for splits the partials: out and back at 4 TB/s with a
-// launch for the streaming kernel, the last workgroup's reading of them for the large tiles and few rows.
+// launch for the streaming kernel, the last workgroup's reading of them for the large tiles and few rows.  Quantized outputs
+// take 8 to 13% more on the streaming tiles; among those, the only ones that exact products have, the same constants chose within
+// 1% of the fastest split on 15 of 19 shapes, 3 to 14% off on the rest.
 static double gated_estimate(int cfg, double row_blocks, double rows, int64_t strips, int64_t k, int num_cus, int splits, int kbps,
                              bool in_kernel) {
   const double bm = cfg == kGatedFew16 ? 16 : cfg == kGatedFew64 ? 64 : cfg == kGatedRows128 ? 128 : 256;
@@ -1552,7 +1554,7 @@ static double gated_estimate(int cfg, double row_blocks, double rows, int64_t st
 }
 
 // Whether the streaming kernel's split tiles are ended by their last workgroup: 16 rows of at most 16 KB of partials each
-// (1 x 2048 x 7168, 14 splits: 12.8 us, with a second launch 15.5).
+// (1 x 2048 x 7168, 14 splits: 12.0 us, with a second launch 13.9).
 static bool gated_join_in_kernel(int cfg, int64_t m, int splits) { return cfg == kGatedFew16 && m * splits <= 64; }
 
 // n: the width of h.

@@ -12,14 +12,15 @@
 // EXACT, for quantized outputs: the codes are widened to bf16, whose products the matrix instruction adds to 2^-22 of them,
 // where the FP8 instruction cuts them at 2^-13 of their largest.  A bf16 output's rounding hides that; a quantized one
 // has a few codes in each 10^4 so near to a border that they come out on its other side, a step of 6 to 12%, and
-// among few values no others make up for it (1 x 2048 x 7168, SiLU: 13.2 us for 11.7; 64 rows: 21.5 for 19.4).
+// among few values no others make up for it (1 x 2048 x 7168, SiLU: 13.2 us for 11.8; 64 rows: 21.5 for 19.5).  In the contiguous
+// layout a tile is half a block of 128 rows (256 x 512 x 7168 67 us, 52 by the FP8 instruction on the 256x128 tile).
 // K is split over workgroups where there are few tiles: fp32 partials of the rows in use go to the workspace.  Their sums,
 // in the order of the splits, end the rows: taken by a second launch, or, of few bytes, by the last workgroup of a tile to
 // arrive (the hand-off of the plain forms).  A CU takes some 30 bytes a nanosecond from memory, so the last workgroup alone
 // is the slower the more there is to add, while a launch costs 3 us whatever it does.
-// Bound by what a CU takes from memory, and for one token by the latencies of one pass: 1 x 2048 x 7168, 14 splits, 11.6 us
+// Bound by what a CU takes from memory, and for one token by the latencies of one pass: 1 x 2048 x 7168, 14 splits, 11.8 us
 // (29 MB; 5.9 us at the rate of a copy); 777 x 1057 x 1552 in 117 tiles of 64 rows on 256 CUs 18 us; 64 x 2048
-// x 7168 in 8 splits 22 us.  Tiles of 128 and 256 rows were no faster than the large tiles.
+// x 7168 in 8 splits 19.5 us.  Tiles of 128 and 256 rows were no faster than the large tiles.
 #include <type_traits>
 
 #include "gemm_common.hpp"
